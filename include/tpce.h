@@ -472,6 +472,123 @@ tpce_status vocab_parallel_ce_loss_static(const void *H, const void *E, const in
                                           int t, int dtype, float *loss, float *lse, void *stream);
 
 /* ---------------------------------------------------------------------------
+ * RMS norm with the residual's addition: what feeds a block.
+ *   S = X + R,  rstd = (sum_c S^2 / h + eps)^-1/2,  Y = S rstd w,
+ * per row of h values; S is rounded to the tensors' type, and the stored value
+ * is what is normalised. Sums and statistics are fp32.
+ * tp_rmsnorm_forward: X, R [T, h] (R NULL: S = X, and S is not written);
+ *   w [h] fp32; outputs S [T, h] (with R; may be X or R itself, in place),
+ *   rstd [T] fp32, and Y [T, h] or Q or both: Y may be NULL when Q is given.
+ *   Q [T, h] (NULL: none) holds Y in 8 bits, rounded from fp32: e4m3 codes with
+ *   Q_scale [T, ceil(h / 128)] fp32, one scale per 128 columns of a row,
+ *   scale = max(amax / 448, 2^-126), amax over the group's finite values;
+ *   Y ~ code * scale. NaN and infinity become the NaN code.
+ * tp_rmsnorm_backward: with g = dY w and xh = S rstd,
+ *   dX = rstd (g - xh sum_c(g xh) / h) + dS   (the gradient of X and of R),
+ *   dw = sum_t dY xh.
+ *   dY, S [T, h], rstd [T] from the forward, dS [T, h] (the gradient that
+ *   reaches S by the residual path; NULL: none); dX [T, h] may be dY or dS
+ *   itself; dw [h] fp32 (NULL: not wanted). dw is deterministic.
+ * Shapes: h a multiple of 8 up to 16384. T == 0: the forward is a no-op, the
+ * backward zeroes dw. Sequence chunks are rows: call once per chunk (dw of the
+ * whole is the chunks' sum).
+ * Workspace: tpce_rmsnorm_workspace_bytes for the backward with dw (partial
+ * sums); 0 for invalid shapes.
+ * ------------------------------------------------------------------------- */
+size_t tpce_rmsnorm_workspace_bytes(int64_t T, int64_t h);
+tpce_status tp_rmsnorm_forward(const void *X, const void *R, const float *w, int64_t T, int64_t h,
+                               float eps, int dtype, void *S, void *Y, void *Q, float *Q_scale,
+                               float *rstd, void *stream);
+tpce_status tp_rmsnorm_backward(const void *dY, const void *S, const float *w, const float *rstd,
+                                const void *dS, int64_t T, int64_t h, int dtype, void *dX, float *dw,
+                                void *ws, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Tokens sorted by expert and back, around a block that serves as an expert
+ * (tp_swiglu_forward / backward or tp_mlp_* on the rows offsets[e] ..
+ * offsets[e + 1] of Xs, once per expert).
+ * tp_expert_plan: ids [T, k] int32, each in [0, E) or -1 (a dropped
+ *   assignment). A stable sort of the assignments i = t k + j by expert:
+ *   row [T, k]       place of the assignment among the sorted ones, -1: dropped
+ *   source [T k]     the assignment at each place, -1 past the last one
+ *   offsets [E + 1]  first place of each expert; offsets[E] = kept assignments
+ *   An id below -1 or from E on counts as dropped and records
+ *   TPCE_ERR_INVALID in the device status word.
+ * tp_expert_dispatch_forward:  Xs[row[t, j]] = X[t];  Xs [T k, h], its rows
+ *   from offsets[E] on are zeros.
+ * tp_expert_dispatch_backward: dX[t] = sum_j dXs[row[t, j]].
+ * tp_expert_combine_forward:   Z[t] = sum_j weights[t, j] Ys[row[t, j]];
+ *   weights [T, k] fp32. A token without kept assignments gets zeros; rows
+ *   that no assignment names are not read.
+ * tp_expert_combine_backward:  dYs[row[t, j]] = weights[t, j] dZ[t] (rows from
+ *   offsets[E] on: zeros), dweights[t, j] = sum_c dZ[t, c] Ys[row[t, j], c]
+ *   (0 for dropped ones).
+ * Sums are fp32 in the order of j, rounded once; results are deterministic.
+ * row and offsets are a plan's; a place outside [-1, T k) is skipped and
+ * recorded in the device status word.
+ * Shapes: 1 <= k <= 32, 1 <= E <= 1024, T k below 2^31 - 1024, h a multiple
+ * of 8 up to 2^20. T == 0: offsets are zeroed, the rest is a no-op. No
+ * workspace.
+ * ------------------------------------------------------------------------- */
+tpce_status tp_expert_plan(const int32_t *ids, int64_t T, int k, int E, int32_t *row,
+                           int32_t *source, int32_t *offsets, void *stream);
+tpce_status tp_expert_dispatch_forward(const void *X, const int32_t *row, const int32_t *offsets,
+                                       int64_t T, int64_t h, int k, int E, int dtype, void *Xs,
+                                       void *stream);
+tpce_status tp_expert_dispatch_backward(const void *dXs, const int32_t *row, int64_t T, int64_t h,
+                                        int k, int dtype, void *dX, void *stream);
+tpce_status tp_expert_combine_forward(const void *Ys, const int32_t *row, const float *weights,
+                                      int64_t T, int64_t h, int k, int dtype, void *Z, void *stream);
+tpce_status tp_expert_combine_backward(const void *dZ, const void *Ys, const int32_t *row,
+                                       const int32_t *offsets, const float *weights, int64_t T,
+                                       int64_t h, int k, int E, int dtype, void *dYs,
+                                       float *dweights, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * tp_adamw_step -- one AdamW step over a list of tensors, in place.
+ * Per value, with g = grad * grad_scale and t = step (from 1):
+ *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2,
+ *   p = p (1 - lr wd) - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * in fp32, each operation rounded on its own. p is fp32, or bf16, or bf16 with
+ * an fp32 master: then the master is what is updated and p its rounding.
+ * state_bits 32: m, v fp32 [n]. state_bits 8: m and r = sqrt(v) as e4m3 codes
+ * [n] with fp32 scales [ceil(n / 128)], one per 128 values of the flat tensor,
+ * as Q of tp_rmsnorm_forward; v then points to r's codes and v_scale to their
+ * scales. Codes and scales of zero bytes are a zero state. The update uses the
+ * moments before they are rounded.
+ * `tensors` is a host array, read during the call; tensors with n == 0 are
+ * skipped (their pointers may be NULL). Every device pointer is 16-byte
+ * aligned, and no two of them overlap.
+ * device_scalars (NULL: none): four fp32 on the device,
+ *   { lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t), lr, grad_scale },
+ * read by the kernel in place of lr, step and grad_scale, which a captured
+ * graph would otherwise repeat: write them anew before each replay.
+ * Lists of up to 400 tensors take one launch.
+ * Errors: TPCE_ERR_INVALID for a beta outside [0, 1), eps < 0, step < 1, an
+ * unknown dtype or state_bits, a master beside fp32 values, a null pointer;
+ * everything is checked before the first launch.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    void *p;             /* [n] p_dtype */
+    void *master;        /* [n] fp32, or NULL; only with a bf16 p */
+    const void *g;       /* [n] g_dtype */
+    void *m;             /* [n] fp32, or e4m3 codes */
+    void *v;             /* [n] fp32, or r's e4m3 codes */
+    float *m_scale;      /* state_bits 8 only */
+    float *v_scale;
+    int64_t n;
+    double weight_decay;
+    int p_dtype;         /* TPCE_BF16 or TPCE_F32 */
+    int g_dtype;
+    int state_bits;      /* 8 or 32 */
+    int reserved;
+} tpce_adamw_tensor;
+
+tpce_status tp_adamw_step(const tpce_adamw_tensor *tensors, int count, double lr, double beta1,
+                          double beta2, double eps, int64_t step, double grad_scale,
+                          const float *device_scalars, void *stream);
+
+/* ---------------------------------------------------------------------------
  * Device status word. Kernels record the first device-side failure (a
  * TPCE_ERR_* code in the low 8 bits, detail above) instead of trapping.
  * tpce_device_status synchronises `stream`, reads the word of the current

@@ -1,0 +1,163 @@
+"""The training-step operators' refusals and sizes, on the CPU: every call here
+is turned down by the library's host checks or the binding's, so none reaches a
+kernel (the pointers are never read)."""
+
+import ctypes
+import math
+
+import pytest
+import torch
+
+P = ctypes.c_void_p
+OK = P(1 << 20)
+ODD = P((1 << 20) + 8)
+INVALID, SHAPE, ALIGN, WORKSPACE = 1, 2, 3, 4
+
+
+@pytest.fixture(scope="module")
+def L():
+    from vocab_ce_gb300 import build
+    build.build()
+    from vocab_ce_gb300._lib import lib
+    return lib()
+
+
+def test_rmsnorm_forward_refusals(L):
+    def call(T=4, h=64, eps=1e-6, dtype=0, X=OK, R=None, w=OK, S=None, Y=OK, Q=None, Qs=None, rstd=OK):
+        return L.tp_rmsnorm_forward(X, R, w, T, h, eps, dtype, S, Y, Q, Qs, rstd, None)
+    assert call(T=0, X=None, Y=None, rstd=None) == 0
+    assert call(T=-1) == SHAPE and call(h=0) == SHAPE and call(h=60) == SHAPE and call(h=16392) == SHAPE
+    assert call(dtype=2) == INVALID and call(eps=-1.0) == INVALID and call(eps=float("nan")) == INVALID
+    assert call(X=None) == INVALID and call(w=None) == INVALID and call(rstd=None) == INVALID
+    assert call(R=OK, S=None) == INVALID          # a sum has to go somewhere
+    assert call(Y=None) == INVALID                # neither output
+    assert call(Q=OK, Qs=None) == INVALID         # codes without scales
+    for name in ("X", "w", "Y", "rstd"):
+        assert call(**{name: ODD}) == ALIGN
+    assert call(R=ODD, S=OK) == ALIGN and call(Q=ODD, Qs=OK) == ALIGN and call(Q=OK, Qs=ODD) == ALIGN
+
+
+def test_rmsnorm_backward_refusals(L):
+    def call(T=4, h=64, dtype=0, dY=OK, S=OK, w=OK, rstd=OK, dS=None, dX=OK, dw=OK, ws=OK, n=1 << 30):
+        return L.tp_rmsnorm_backward(dY, S, w, rstd, dS, T, h, dtype, dX, dw, ws, n, None)
+    assert call(T=-1) == SHAPE and call(h=12) == SHAPE and call(dtype=-1) == INVALID
+    for name in ("dY", "S", "w", "rstd", "dX"):
+        assert call(**{name: None}) == INVALID
+        assert call(**{name: ODD}) == ALIGN
+    assert call(dS=ODD) == ALIGN and call(dw=ODD) == ALIGN and call(ws=ODD) == ALIGN
+    need = L.tpce_rmsnorm_workspace_bytes(4, 64)
+    assert need > 0 and call(ws=None) == WORKSPACE and call(n=need - 1) == WORKSPACE
+    assert str(need) in L.tpce_last_error().decode()
+    assert call(T=0, dY=None, S=None, dX=None, rstd=None, w=None, dw=None, ws=None) == 0
+
+
+def test_rmsnorm_workspace(L):
+    import vocab_ce_gb300 as tp
+    assert tp.rmsnorm_workspace_bytes(0, 64) == 0 and tp.rmsnorm_workspace_bytes(-1, 64) == 0
+    assert tp.rmsnorm_workspace_bytes(4, 60) == 0
+    # one row of fp32 sums for each of a bounded number of blocks
+    for T, h in ((1, 8), (7, 1024), (5, 2048), (1 << 20, 16384)):
+        n = tp.rmsnorm_workspace_bytes(T, h)
+        assert n % (4 * h) == 0 and 1 <= n // (4 * h) <= min(T, 1024)
+
+
+def test_expert_plan_refusals(L):
+    def call(T=4, k=2, E=8, ids=OK, row=OK, source=OK, offsets=OK):
+        return L.tp_expert_plan(ids, T, k, E, row, source, offsets, None)
+    assert call(T=-1) == SHAPE and call(k=0) == SHAPE and call(k=33) == SHAPE
+    assert call(E=0) == SHAPE and call(E=1025) == SHAPE and call(T=1 << 30) == SHAPE
+    for name in ("ids", "row", "source", "offsets"):
+        assert call(**{name: None}) == INVALID
+        assert call(**{name: ODD}) == ALIGN
+    assert call(T=0, offsets=None) == INVALID
+
+
+def test_expert_row_refusals(L):
+    calls = {
+        "dispatch": lambda T=4, h=64, k=2, E=8, dt=0, a=OK, b=OK, c=OK, d=OK:
+            L.tp_expert_dispatch_forward(a, b, c, T, h, k, E, dt, d, None),
+        "dispatch_backward": lambda T=4, h=64, k=2, E=8, dt=0, a=OK, b=OK, c=OK, d=OK:
+            L.tp_expert_dispatch_backward(a, b, T, h, k, dt, d, None),
+        "combine": lambda T=4, h=64, k=2, E=8, dt=0, a=OK, b=OK, c=OK, d=OK:
+            L.tp_expert_combine_forward(a, b, c, T, h, k, dt, d, None),
+        "combine_backward": lambda T=4, h=64, k=2, E=8, dt=0, a=OK, b=OK, c=OK, d=OK, e=OK, f=OK:
+            L.tp_expert_combine_backward(a, f, b, c, OK, T, h, k, E, dt, d, e, None),
+    }
+    for name, call in calls.items():
+        assert call(T=0, a=None, d=None) == 0, name
+        assert call(T=-1) == SHAPE and call(h=4) == SHAPE and call(h=12) == SHAPE and call(h=(1 << 20) + 8) == SHAPE
+        assert call(k=0) == SHAPE and call(k=33) == SHAPE and call(dt=7) == INVALID
+        assert call(T=(1 << 31) // 2) == SHAPE
+        for p in ("a", "b", "d"):
+            assert call(**{p: None}) == INVALID, (name, p)
+            assert call(**{p: ODD}) == ALIGN, (name, p)
+    for name in ("dispatch", "combine", "combine_backward"):
+        assert calls[name](c=None) == INVALID and calls[name](c=ODD) == ALIGN
+    for name in ("dispatch", "combine_backward"):
+        assert calls[name](E=0) == SHAPE and calls[name](E=1025) == SHAPE
+    assert calls["combine_backward"](e=None) == INVALID and calls["combine_backward"](f=ODD) == ALIGN
+
+
+def test_adamw_refusals(L):
+    from vocab_ce_gb300._lib import AdamwTensor
+
+    def call(count=1, lr=1e-3, b1=0.9, b2=0.999, eps=1e-8, step=1, scale=1.0, scalars=None, tensors=True, **kw):
+        f = dict(p=1 << 20, master=None, g=1 << 21, m=1 << 22, v=1 << 23, m_scale=1 << 24, v_scale=1 << 25, n=100,
+                 weight_decay=0.1, p_dtype=0, g_dtype=0, state_bits=8)
+        f.update(kw)
+        arr = (AdamwTensor * 1)(AdamwTensor(**f))
+        return L.tp_adamw_step(arr if tensors else None, count, lr, b1, b2, eps, step, scale, scalars, None)
+    assert call(count=0) == 0 and call(count=0, tensors=False) == 0
+    assert call(count=-1) == INVALID and call(tensors=False) == INVALID
+    nan, inf = float("nan"), float("inf")
+    for bad in (dict(b1=1.0), dict(b1=-0.1), dict(b2=1.0), dict(b2=nan), dict(eps=-1.0), dict(eps=inf), dict(step=0),
+                dict(lr=nan), dict(lr=inf), dict(scale=inf), dict(p_dtype=2), dict(g_dtype=5), dict(state_bits=16),
+                dict(weight_decay=nan), dict(p=None), dict(g=None), dict(m=None), dict(v=None), dict(m_scale=None),
+                dict(v_scale=None), dict(p_dtype=1, master=1 << 26)):
+        assert call(**bad) == INVALID, bad
+    assert call(n=-1) == SHAPE and call(n=1 << 62) == SHAPE
+    for name in ("p", "g", "m", "v", "m_scale", "v_scale", "master"):
+        assert call(**{name: (1 << 20) + 4}) == ALIGN, name
+    assert call(scalars=P((1 << 20) + 2)) == ALIGN
+    # a tensor without values is skipped, whatever its pointers
+    assert call(n=0, p=None, g=None, m=None, v=None) == 0
+
+
+def test_binding_refuses_host_tensors_and_wrong_arguments():
+    import vocab_ce_gb300 as tp
+    x, w = torch.zeros(4, 64, dtype=torch.bfloat16), torch.ones(64)
+    with pytest.raises(ValueError, match="CUDA"):
+        tp.tp_rmsnorm_forward(x, w)
+    with pytest.raises(ValueError, match="float16"):
+        tp.tp_rmsnorm_forward(x.half(), w)
+    with pytest.raises(ValueError, match="matrix"):
+        tp.tp_rmsnorm_forward(x[0], w)
+    with pytest.raises(ValueError, match="CUDA"):
+        tp.tp_rmsnorm_backward(x, x, w, torch.ones(4))
+    with pytest.raises(ValueError, match="CUDA"):
+        tp.tp_expert_plan(torch.zeros(4, 2, dtype=torch.int32), 8)
+    plan = {"row": torch.zeros(4, 2, dtype=torch.int32), "offsets": torch.zeros(9, dtype=torch.int32)}
+    with pytest.raises(ValueError, match="CUDA"):
+        tp.tp_expert_dispatch_forward(x, plan)
+    with pytest.raises(ValueError, match="CUDA"):
+        tp.adamw_step([x], [x], [tp.adamw_state(x)], lr=1e-3, step=1)
+    with pytest.raises(ValueError, match="grads"):
+        tp.adamw_step([x], [], [tp.adamw_state(x)], lr=1e-3, step=1)
+    with pytest.raises(ValueError, match="fp32 already"):
+        tp.adamw_step([w], [w], [tp.adamw_state(w)], lr=1e-3, step=1, masters=[w])
+    with pytest.raises(ValueError, match="bits"):
+        tp.adamw_state(x, bits=4)
+
+
+def test_adamw_state_and_scalars():
+    import vocab_ce_gb300 as tp
+    x = torch.zeros(3, 100, dtype=torch.bfloat16)
+    s = tp.adamw_state(x, bits=8)
+    assert s["m_q"].dtype == torch.float8_e4m3fn and s["r_q"].shape == x.shape
+    assert s["m_scale"].shape == (3,) == s["r_scale"].shape   # 300 values: three groups
+    assert tp.adamw_state(x)["v"].dtype == torch.float32
+    v = tp.adamw_scalars(1e-3, 10, 0.9, 0.99, grad_scale=0.25)
+    want = [1e-3 / (1 - 0.9 ** 10), 1 / math.sqrt(1 - 0.99 ** 10), 1e-3, 0.25]
+    assert v.dtype == torch.float32 and torch.equal(v, torch.tensor(want, dtype=torch.float32))
+    with pytest.raises(ValueError):
+        tp.adamw_scalars(1e-3, 0)

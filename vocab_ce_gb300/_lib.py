@@ -29,6 +29,17 @@ _I64 = ctypes.c_int64
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
 _F = ctypes.c_float
+_D = ctypes.c_double
+
+
+class AdamwTensor(ctypes.Structure):
+    """tpce_adamw_tensor: one tensor of an optimizer step."""
+
+    _fields_ = [("p", _P), ("master", _P), ("g", _P), ("m", _P), ("v", _P), ("m_scale", _P), ("v_scale", _P),
+                ("n", _I64), ("weight_decay", _D), ("p_dtype", _I), ("g_dtype", _I), ("state_bits", _I),
+                ("reserved", _I)]
+
+
 SIGNATURES = {
     "tpce_status_string": (ctypes.c_char_p, [_I]),
     "tpce_version": (_I, []),
@@ -69,6 +80,15 @@ SIGNATURES = {
     "vocab_parallel_ce": (_I, [_P, _P, _P, _I64, _I64, _I64, _I64, _I, _F, _I,
                                _P, _P, _P, _P, _P, _SZ, _P]),
     "vocab_parallel_ce_loss_static": (_I, [_P, _P, _P, _I64, _I64, _I64, _I64, _I, _I, _P, _P, _P]),
+    "tpce_rmsnorm_workspace_bytes": (_SZ, [_I64, _I64]),
+    "tp_rmsnorm_forward": (_I, [_P, _P, _P, _I64, _I64, _F, _I, _P, _P, _P, _P, _P, _P]),
+    "tp_rmsnorm_backward": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I, _P, _P, _P, _SZ, _P]),
+    "tp_expert_plan": (_I, [_P, _I64, _I, _I, _P, _P, _P, _P]),
+    "tp_expert_dispatch_forward": (_I, [_P, _P, _P, _I64, _I64, _I, _I, _I, _P, _P]),
+    "tp_expert_dispatch_backward": (_I, [_P, _P, _I64, _I64, _I, _I, _P, _P]),
+    "tp_expert_combine_forward": (_I, [_P, _P, _P, _I64, _I64, _I, _I, _P, _P]),
+    "tp_expert_combine_backward": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I, _I, _I, _P, _P, _P]),
+    "tp_adamw_step": (_I, [ctypes.POINTER(AdamwTensor), _I, _D, _D, _D, _D, _I64, _D, _P, _P]),
     "tpce_device_status": (_I, [_P, _I, ctypes.POINTER(ctypes.c_uint32)]),
     "tpce_debug_withhold_next_load": (_I, [_I]),
     "tpce_profile_enable": (_I, [_I]),

@@ -1,0 +1,283 @@
+// adamw.cu -- one AdamW step over many tensors in one launch.
+//
+// Per value, with g = grad * grad_scale and t the step's number (from 1):
+//   m = b1 m + (1 - b1) g,   v = b2 v + (1 - b2) g^2,
+//   p = p (1 - lr wd) - lr / (1 - b1^t) * m / (sqrt(v) / sqrt(1 - b2^t) + eps).
+// States in 32 bits hold m and v. States in 8 bits hold m and the root
+// r = sqrt(v), each in e4m3 with one scale per 128 values of the flat tensor
+// (vec.cuh). The root, not v: e4m3 spans a factor of 2^18 between a group's
+// largest and smallest value, which in v would leave only 2^9 in the root that
+// the update divides by. The update uses the new moments before they are rounded.
+//
+// Every product and sum is rounded on its own (no contraction to a fused
+// multiply-add), so that a step gives the same bits wherever a tensor lies in
+// the list and however its tail is handled, and the same as elementary 32-bit
+// operations in the order above: an 8-bit state rounds next to a border the
+// same way everywhere.
+//
+// A parameter is fp32, or bf16, or bf16 with an fp32 master copy (then the
+// master is read and written, and the bf16 weight only written, rounded from
+// it). The tensors' addresses travel in the kernel's parameters: no table is
+// copied to the device, and a captured step keeps them.
+#include <algorithm>
+#include <climits>
+#include <cmath>
+
+#include "host.h"
+#include "step/vec.cuh"
+
+namespace tpce {
+namespace {
+
+using namespace step;
+
+constexpr int kThreads = 256;
+constexpr int kChunk = kThreads * 8;  // values of one block: 16 groups
+
+enum : uint32_t { kParamBf16 = 1u, kMaster = 2u, kGradBf16 = 4u, kState8 = 8u };
+
+struct Entry {
+    void *p, *master;
+    const void *g;
+    void *m, *v;
+    float *m_scale, *v_scale;
+    int64_t n;
+    uint32_t chunk0;  // chunks of the tensors before it
+    uint32_t kind;
+    float decay;      // 1 - lr wd
+    float wd;
+};
+static_assert(sizeof(Entry) == 80, "the table's size is what a launch's parameters hold");
+
+// Parameters of a launch: up to 4 KB for a short list, up to 32,764 bytes for a
+// long one (more take more launches).
+constexpr int kShort = 48, kLong = 400;
+template <int N>
+struct Table {
+    Entry t[N];
+    int count;
+};
+
+struct Scalars {
+    float b1, one_b1, b2, one_b2, eps;
+    float step_size;   // lr / (1 - b1^t)
+    float root_scale;  // 1 / sqrt(1 - b2^t)
+    float grad_scale;
+    const float *device;  // {step_size, root_scale, lr, grad_scale} on the device, or NULL
+};
+
+struct Rates {
+    float step_size, root_scale, grad_scale, decay;
+};
+
+__device__ __forceinline__ void update(const Scalars &k, const Rates &c, float grad, float &p, float &m, float &v,
+                                       float &r) {
+    const float g = __fmul_rn(grad, c.grad_scale);
+    m = __fadd_rn(__fmul_rn(m, k.b1), __fmul_rn(g, k.one_b1));
+    v = __fadd_rn(__fmul_rn(v, k.b2), __fmul_rn(__fmul_rn(g, g), k.one_b2));
+    r = __fsqrt_rn(v);
+    const float u = __fdiv_rn(m, __fadd_rn(__fmul_rn(r, c.root_scale), k.eps));
+    p = __fsub_rn(__fmul_rn(p, c.decay), __fmul_rn(u, c.step_size));
+}
+
+// Eight values from i on; those from n on are zeros, and are not stored.
+template <typename T>
+__device__ __forceinline__ void fetch(const void *base, int64_t i, int64_t n, float (&v)[8]) {
+    const T *p = static_cast<const T *>(base) + i;
+    if (i + 8 <= n) {
+        unpack8(load8(p), v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = i + j < n ? static_cast<float>(p[j]) : 0.0f;
+    }
+}
+template <typename T>
+__device__ __forceinline__ void put(void *base, int64_t i, int64_t n, const float (&v)[8]) {
+    T *p = static_cast<T *>(base) + i;
+    if (i + 8 <= n) {
+        Raw8<T> o;
+        pack8(v, o);
+        store8(p, o);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (i + j < n) p[j] = static_cast<T>(v[j]);
+    }
+}
+__device__ __forceinline__ uint2 fetch_codes(const void *base, int64_t i, int64_t n) {
+    const uint8_t *p = static_cast<const uint8_t *>(base) + i;
+    if (i + 8 <= n) return *reinterpret_cast<const uint2 *>(p);
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (i + j < n) w[j / 4] |= static_cast<uint32_t>(p[j]) << (8 * (j % 4));
+    return make_uint2(w[0], w[1]);
+}
+__device__ __forceinline__ void put_codes(void *base, int64_t i, int64_t n, uint2 q) {
+    uint8_t *p = static_cast<uint8_t *>(base) + i;
+    if (i + 8 <= n) {
+        *reinterpret_cast<uint2 *>(p) = q;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (i + j < n) p[j] = static_cast<uint8_t>((j < 4 ? q.x : q.y) >> (8 * (j % 4)));
+    }
+}
+
+template <int N>
+__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Table<N> table,
+                                                         const __grid_constant__ Scalars k) {
+    // the tensor that holds this block's chunk: the last one that starts at or before it
+    int lo = 0, hi = table.count - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (table.t[mid].chunk0 <= blockIdx.x)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    const Entry &e = table.t[lo];
+    const int64_t n = e.n;
+    const int64_t i = static_cast<int64_t>(blockIdx.x - e.chunk0) * kChunk + threadIdx.x * 8;
+    const uint32_t kind = e.kind;
+    Rates c{k.step_size, k.root_scale, k.grad_scale, e.decay};
+    if (k.device) {
+        c.step_size = __ldg(k.device);
+        c.root_scale = __ldg(k.device + 1);
+        c.decay = __fsub_rn(1.0f, __fmul_rn(__ldg(k.device + 2), e.wd));
+        c.grad_scale = __ldg(k.device + 3);
+    }
+    float p[8], g[8], m[8], v[8], r[8];
+    const int64_t group = i / kGroup;
+    const bool live = i < n;
+    if (kind & kMaster)
+        fetch<float>(e.master, i, n, p);
+    else if (kind & kParamBf16)
+        fetch<__nv_bfloat16>(e.p, i, n, p);
+    else
+        fetch<float>(e.p, i, n, p);
+    if (kind & kGradBf16)
+        fetch<__nv_bfloat16>(e.g, i, n, g);
+    else
+        fetch<float>(e.g, i, n, g);
+    if (kind & kState8) {
+        decode8(fetch_codes(e.m, i, n), live ? e.m_scale[group] : 0.0f, m);
+        decode8(fetch_codes(e.v, i, n), live ? e.v_scale[group] : 0.0f, r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(r[j], r[j]);
+    } else {
+        fetch<float>(e.m, i, n, m);
+        fetch<float>(e.v, i, n, v);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) update(k, c, g[j], p[j], m[j], v[j], r[j]);
+    if (kind & kState8) {
+        // values past the end have no gradient and no moments: they stay zero and leave amax alone
+        const float ms = group_scale(group_amax(m)), rs = group_scale(group_amax(r));
+        if (live) {
+            put_codes(e.m, i, n, encode8(m, __fdiv_rn(1.0f, ms)));
+            put_codes(e.v, i, n, encode8(r, __fdiv_rn(1.0f, rs)));
+            if ((threadIdx.x & 15) == 0) {
+                e.m_scale[group] = ms;
+                e.v_scale[group] = rs;
+            }
+        }
+    } else if (live) {
+        put<float>(e.m, i, n, m);
+        put<float>(e.v, i, n, v);
+    }
+    if (!live) return;
+    if (kind & kMaster) put<float>(e.master, i, n, p);
+    if (kind & kParamBf16)
+        put<__nv_bfloat16>(e.p, i, n, p);
+    else
+        put<float>(e.p, i, n, p);
+}
+
+template <int N>
+tpce_status launch(const Entry *entries, int count, uint32_t chunks, const Scalars &k, cudaStream_t s) {
+    Table<N> table;
+    std::copy(entries, entries + count, table.t);
+    table.count = count;
+    KernelTimer timer("adamw_step", s);
+    adamw_kernel<N><<<chunks, kThreads, 0, s>>>(table, k);
+    return check_launch("adamw_step", s);
+}
+
+}  // namespace
+}  // namespace tpce
+
+// ====================================================================== C ABI
+using namespace tpce;
+
+extern "C" tpce_status tp_adamw_step(const tpce_adamw_tensor *tensors, int count, double lr, double beta1,
+                                     double beta2, double eps, int64_t step, double grad_scale,
+                                     const float *device_scalars, void *stream) {
+    if (count < 0 || (count > 0 && !tensors)) return fail(TPCE_ERR_INVALID, "tp_adamw_step: no tensors");
+    if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !(eps >= 0.0) || !std::isfinite(lr) ||
+        !std::isfinite(eps) || !std::isfinite(grad_scale) || step < 1)
+        return fail(TPCE_ERR_INVALID, "tp_adamw_step: beta1 and beta2 in [0, 1), eps >= 0, step >= 1, finite lr");
+    // everything is checked before anything is launched
+    int64_t total = 0;
+    for (int i = 0; i < count; ++i) {
+        const tpce_adamw_tensor &t = tensors[i];
+        const bool bf = t.p_dtype == TPCE_BF16;
+        if ((!bf && t.p_dtype != TPCE_F32) || (t.g_dtype != TPCE_BF16 && t.g_dtype != TPCE_F32) ||
+            (t.state_bits != 8 && t.state_bits != 32) || !std::isfinite(t.weight_decay))
+            return fail(TPCE_ERR_INVALID, "tp_adamw_step: tensor %d: dtypes, state_bits (8 or 32) or weight_decay", i);
+        if (t.n < 0) return fail(TPCE_ERR_SHAPE, "tp_adamw_step: tensor %d: n = %lld", i, static_cast<long long>(t.n));
+        if (t.n == 0) continue;
+        if (!t.p || !t.g || !t.m || !t.v || (t.state_bits == 8 && (!t.m_scale || !t.v_scale)) || (t.master && !bf))
+            return fail(TPCE_ERR_INVALID, "tp_adamw_step: tensor %d: null pointer, or a master beside fp32 values", i);
+        for (const void *p : {static_cast<const void *>(t.p), static_cast<const void *>(t.master), t.g,
+                              static_cast<const void *>(t.m), static_cast<const void *>(t.v),
+                              static_cast<const void *>(t.m_scale), static_cast<const void *>(t.v_scale)})
+            if (!aligned16(p))
+                return fail(TPCE_ERR_ALIGN, "tp_adamw_step: tensor %d: a pointer is not 16-byte aligned", i);
+        if (t.n > INT64_MAX - kChunk || (t.n + kChunk - 1) / kChunk > INT_MAX - total)
+            return fail(TPCE_ERR_SHAPE, "tp_adamw_step: too many values");
+        total += (t.n + kChunk - 1) / kChunk;
+    }
+    if (reinterpret_cast<uintptr_t>(device_scalars) & 3u)
+        return fail(TPCE_ERR_ALIGN, "tp_adamw_step: device_scalars is not aligned");
+
+    Scalars k{};
+    k.b1 = static_cast<float>(beta1);
+    k.one_b1 = static_cast<float>(1.0 - beta1);
+    k.b2 = static_cast<float>(beta2);
+    k.one_b2 = static_cast<float>(1.0 - beta2);
+    k.eps = static_cast<float>(eps);
+    k.step_size = static_cast<float>(lr / (1.0 - std::pow(beta1, static_cast<double>(step))));
+    k.root_scale = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(beta2, static_cast<double>(step))));
+    k.grad_scale = static_cast<float>(grad_scale);
+    k.device = device_scalars;
+
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    Entry entries[kLong];
+    int held = 0;
+    uint32_t chunks = 0;
+    auto flush = [&]() -> tpce_status {
+        if (!held) return TPCE_OK;
+        tpce_status st = held <= kShort ? launch<kShort>(entries, held, chunks, k, s)
+                                        : launch<kLong>(entries, held, chunks, k, s);
+        held = 0;
+        chunks = 0;
+        return st;
+    };
+    for (int i = 0; i < count; ++i) {
+        const tpce_adamw_tensor &t = tensors[i];
+        if (t.n == 0) continue;
+        Entry &e = entries[held++];
+        e = Entry{t.p, t.master, t.g, t.m, t.v, t.m_scale, t.v_scale, t.n, chunks, 0u, 0.0f, 0.0f};
+        e.kind = (t.p_dtype == TPCE_BF16 ? kParamBf16 : 0u) | (t.master ? kMaster : 0u) |
+                 (t.g_dtype == TPCE_BF16 ? kGradBf16 : 0u) | (t.state_bits == 8 ? kState8 : 0u);
+        e.decay = static_cast<float>(1.0 - lr * t.weight_decay);
+        e.wd = static_cast<float>(t.weight_decay);
+        chunks += static_cast<uint32_t>((t.n + kChunk - 1) / kChunk);
+        if (held == kLong) {
+            tpce_status st = flush();
+            if (st != TPCE_OK) return st;
+        }
+    }
+    return flush();
+}

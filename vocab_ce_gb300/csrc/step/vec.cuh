@@ -1,0 +1,152 @@
+// vec.cuh -- what the row and element kernels of a training step share: eight
+// values of a row in registers, the e4m3 codes with one scale per 128 values,
+// and sums over a warp or a block.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <cfloat>
+#include <cstdint>
+
+namespace tpce {
+namespace step {
+
+// Eight adjacent values as they lie in memory: one 16-byte vector of bf16, two
+// of fp32. Addresses are 16-byte aligned: row widths are multiples of 8.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+    uint4 a;
+};
+template <>
+struct Raw8<float> {
+    float4 a, b;
+};
+
+__device__ __forceinline__ Raw8<__nv_bfloat16> load8(const __nv_bfloat16 *p) {
+    return {*reinterpret_cast<const uint4 *>(p)};
+}
+__device__ __forceinline__ Raw8<float> load8(const float *p) {
+    const float4 *q = reinterpret_cast<const float4 *>(p);
+    return {q[0], q[1]};
+}
+
+__device__ __forceinline__ void zero8(Raw8<__nv_bfloat16> &r) { r.a = make_uint4(0u, 0u, 0u, 0u); }
+__device__ __forceinline__ void zero8(Raw8<float> &r) { r.a = r.b = make_float4(0.f, 0.f, 0.f, 0.f); }
+
+__device__ __forceinline__ void unpack8(const Raw8<__nv_bfloat16> &r, float (&v)[8]) {
+    const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        // a bf16 is the upper half of an fp32
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void unpack8(const Raw8<float> &r, float (&v)[8]) {
+    v[0] = r.a.x; v[1] = r.a.y; v[2] = r.a.z; v[3] = r.a.w;
+    v[4] = r.b.x; v[5] = r.b.y; v[6] = r.b.z; v[7] = r.b.w;
+}
+
+// the one rounding to the stored type (nearest even; none for fp32)
+__device__ __forceinline__ void pack8(const float (&v)[8], Raw8<__nv_bfloat16> &r) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    r.a = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void pack8(const float (&v)[8], Raw8<float> &r) {
+    r.a = make_float4(v[0], v[1], v[2], v[3]);
+    r.b = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const Raw8<__nv_bfloat16> &r) {
+    *reinterpret_cast<uint4 *>(p) = r.a;
+}
+__device__ __forceinline__ void store8(float *p, const Raw8<float> &r) {
+    float4 *q = reinterpret_cast<float4 *>(p);
+    q[0] = r.a;
+    q[1] = r.b;
+}
+
+__device__ __forceinline__ void load8f(const float *p, float (&v)[8]) {
+    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
+// ------------------------------------------------------------------ e4m3 with scales
+// A group of 128 values shares scale = max(amax / 448, 2^-126), amax over its
+// finite values, and holds code = e4m3(x / scale), rounded to nearest even. The
+// lower bound keeps 1 / scale finite (a group of zeros needs no special case).
+// NaN and infinity become the NaN code: a saturated code would hide them.
+constexpr int kGroup = 128;
+constexpr float kE4m3Max = 448.0f;
+
+__device__ __forceinline__ float group_scale(float amax) { return fmaxf(__fmul_rn(amax, 1.0f / kE4m3Max), FLT_MIN); }
+
+__device__ __forceinline__ float finite_abs(float x) {
+    const float a = fabsf(x);
+    return a <= FLT_MAX ? a : 0.0f;
+}
+
+// amax over the 16 lanes that hold a group's 128 values, eight each
+__device__ __forceinline__ float group_amax(const float (&v)[8]) {
+    float a = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a = fmaxf(a, finite_abs(v[i]));
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
+    return a;
+}
+
+__device__ __forceinline__ uint2 encode8(const float (&v)[8], float inv_scale) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float2 t;
+        t.x = fabsf(v[2 * i]) <= FLT_MAX ? __fmul_rn(v[2 * i], inv_scale) : __int_as_float(0x7fffffff);
+        t.y = fabsf(v[2 * i + 1]) <= FLT_MAX ? __fmul_rn(v[2 * i + 1], inv_scale) : __int_as_float(0x7fffffff);
+        w[i] = __nv_cvt_float2_to_fp8x2(t, __NV_SATFINITE, __NV_E4M3);
+    }
+    return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+}
+
+__device__ __forceinline__ void decode8(uint2 q, float scale, float (&v)[8]) {
+    const uint32_t w[4] = {q.x & 0xffffu, q.x >> 16, q.y & 0xffffu, q.y >> 16};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[i]), __NV_E4M3);
+        const float2 f = __half22float2(__half2(h));
+        v[2 * i] = __fmul_rn(f.x, scale);
+        v[2 * i + 1] = __fmul_rn(f.y, scale);
+    }
+}
+
+// ------------------------------------------------------------------ sums
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    return x;
+}
+
+// Sum over the block's warps with one barrier: `buf` is one of two alternating
+// buffers of 32 floats, so that a buffer is written again only after the
+// barrier of the sum between, which every reader of it has passed. The warps'
+// sums are added in the same order in every thread.
+__device__ __forceinline__ float block_sum(float x, float *buf) {
+    x = warp_sum(x);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    if (lane == 0) buf[warp] = x;
+    __syncthreads();
+    return warp_sum(lane < warps ? buf[lane] : 0.0f);
+}
+
+}  // namespace step
+}  // namespace tpce
