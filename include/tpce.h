@@ -563,7 +563,7 @@ tpce_status tp_expert_combine_backward(const void *dZ, const void *Ys, const int
  *   { lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t), lr, grad_scale },
  * read by the kernel in place of lr, step and grad_scale, which a captured
  * graph would otherwise repeat: write them anew before each replay.
- * Lists of up to 400 tensors take one launch.
+ * Lists of up to 368 tensors take one launch.
  * Errors: TPCE_ERR_INVALID for a beta outside [0, 1), eps < 0, step < 1, an
  * unknown dtype or state_bits, a master beside fp32 values, a null pointer;
  * everything is checked before the first launch.

@@ -32,7 +32,13 @@ namespace {
 using namespace step;
 
 constexpr int kThreads = 256;
-constexpr int kChunk = kThreads * 8;  // values of one block: 16 groups
+constexpr int kChunk = kThreads * 8;  // values that a block takes at a time: 16 groups
+
+// Chunks of a tensor with 8-bit states that a block takes one after the other,
+// and the list's number of chunks from which on it does (below it a chunk each
+// keeps more SMs busy). A tensor with 32-bit states has a block for each chunk.
+constexpr int kSpan = 4;
+constexpr int64_t kSpanFrom = 152 * 32;
 
 enum : uint32_t { kParamBf16 = 1u, kMaster = 2u, kGradBf16 = 4u, kState8 = 8u };
 
@@ -42,16 +48,18 @@ struct Entry {
     void *m, *v;
     float *m_scale, *v_scale;
     int64_t n;
-    uint32_t chunk0;  // chunks of the tensors before it
+    uint32_t block0;  // blocks of the tensors before it
     uint32_t kind;
     float decay;      // 1 - lr wd
     float wd;
+    uint32_t span;    // chunks of a block
+    uint32_t unused;
 };
-static_assert(sizeof(Entry) == 80, "the table's size is what a launch's parameters hold");
+static_assert(sizeof(Entry) == 88, "the table's size is what a launch's parameters hold");
 
 // Parameters of a launch: up to 4 KB for a short list, up to 32,764 bytes for a
 // long one (more take more launches).
-constexpr int kShort = 48, kLong = 400;
+constexpr int kShort = 44, kLong = 368;
 template <int N>
 struct Table {
     Entry t[N];
@@ -80,16 +88,18 @@ __device__ __forceinline__ void update(const Scalars &k, const Rates &c, float g
     p = __fsub_rn(__fmul_rn(p, c.decay), __fmul_rn(u, c.step_size));
 }
 
-// Eight values from i on; those from n on are zeros, and are not stored.
+// Eight values from i on as they lie in memory; those from n on are zeros, and
+// are not stored.
 template <typename T>
-__device__ __forceinline__ void fetch(const void *base, int64_t i, int64_t n, float (&v)[8]) {
+__device__ __forceinline__ Raw8<T> fetch(const void *base, int64_t i, int64_t n) {
     const T *p = static_cast<const T *>(base) + i;
-    if (i + 8 <= n) {
-        unpack8(load8(p), v);
-    } else {
+    if (i + 8 <= n) return load8(p);
+    float v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = i + j < n ? static_cast<float>(p[j]) : 0.0f;
-    }
+    for (int j = 0; j < 8; ++j) v[j] = i + j < n ? static_cast<float>(p[j]) : 0.0f;
+    Raw8<T> r;
+    pack8(v, r);  // exact: the values are T's
+    return r;
 }
 template <typename T>
 __device__ __forceinline__ void put(void *base, int64_t i, int64_t n, const float (&v)[8]) {
@@ -124,22 +134,116 @@ __device__ __forceinline__ void put_codes(void *base, int64_t i, int64_t n, uint
     }
 }
 
+// What a thread reads for its eight values: P is the type that is updated (the
+// master's, where there is one), G the gradient's.
+template <typename P, typename G, bool S8>
+struct Inputs;
+template <typename P, typename G>
+struct Inputs<P, G, false> {
+    Raw8<P> p;
+    Raw8<G> g;
+    Raw8<float> m, v;
+    __device__ __forceinline__ void load(const Entry &e, const void *base, int64_t i, int64_t n) {
+        p = fetch<P>(base, i, n);
+        g = fetch<G>(e.g, i, n);
+        m = fetch<float>(e.m, i, n);
+        v = fetch<float>(e.v, i, n);
+    }
+    __device__ __forceinline__ void moments(float (&mm)[8], float (&vv)[8]) const {
+        unpack8(m, mm);
+        unpack8(v, vv);
+    }
+};
+template <typename P, typename G>
+struct Inputs<P, G, true> {
+    Raw8<P> p;
+    Raw8<G> g;
+    uint2 m, r;
+    float ms, rs;
+    __device__ __forceinline__ void load(const Entry &e, const void *base, int64_t i, int64_t n) {
+        p = fetch<P>(base, i, n);
+        g = fetch<G>(e.g, i, n);
+        m = fetch_codes(e.m, i, n);
+        r = fetch_codes(e.v, i, n);
+        ms = rs = 0.0f;
+        if (i < n) {
+            ms = e.m_scale[i / kGroup];
+            rs = e.v_scale[i / kGroup];
+        }
+    }
+    __device__ __forceinline__ void moments(float (&mm)[8], float (&vv)[8]) const {
+        decode8(m, ms, mm);
+        decode8(r, rs, vv);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) vv[j] = __fmul_rn(vv[j], vv[j]);
+    }
+};
+
+// The chunks from value i of this thread on, `left` of them. With 8-bit states
+// the arithmetic takes about as long as the bytes, so the next chunk's values are
+// on their way while one is computed.
+template <typename P, typename G, bool S8>
+__device__ __forceinline__ void run(const Scalars &k, const Rates &c, const Entry &e, int64_t i, int left) {
+    const int64_t n = e.n;
+    const bool master = e.kind & kMaster;
+    void *base = master ? e.master : e.p;
+    Inputs<P, G, S8> next;
+    next.load(e, base, i, n);
+    for (; left > 0; --left, i += kChunk) {
+        const Inputs<P, G, S8> in = next;
+        if (left > 1) next.load(e, base, i + kChunk, n);
+        float p[8], g[8], m[8], v[8], r[8];
+        unpack8(in.p, p);
+        unpack8(in.g, g);
+        in.moments(m, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) update(k, c, g[j], p[j], m[j], v[j], r[j]);
+        if (S8) {
+            // values past the end have no gradient and no moments: they stay zero and leave the scale alone
+            float ms, rs;
+            const uint2 mq = quantize8(m, ms), rq = quantize8(r, rs);
+            if (i < n) {
+                put_codes(e.m, i, n, mq);
+                put_codes(e.v, i, n, rq);
+                if ((threadIdx.x & 15) == 0) {
+                    e.m_scale[i / kGroup] = ms;
+                    e.v_scale[i / kGroup] = rs;
+                }
+            }
+        } else {
+            put<float>(e.m, i, n, m);
+            put<float>(e.v, i, n, v);
+        }
+        put<P>(base, i, n, p);
+        if (master) put<__nv_bfloat16>(e.p, i, n, p);
+    }
+}
+
+template <typename P, typename G>
+__device__ __forceinline__ void run(const Scalars &k, const Rates &c, const Entry &e, int64_t i, int left) {
+    if (e.kind & kState8)
+        run<P, G, true>(k, c, e, i, left);
+    else
+        run<P, G, false>(k, c, e, i, left);
+}
+
 template <int N>
 __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Table<N> table,
                                                          const __grid_constant__ Scalars k) {
-    // the tensor that holds this block's chunk: the last one that starts at or before it
+    // this block's tensor: the last one that starts at or before it
     int lo = 0, hi = table.count - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
-        if (table.t[mid].chunk0 <= blockIdx.x)
+        if (table.t[mid].block0 <= blockIdx.x)
             lo = mid;
         else
             hi = mid - 1;
     }
     const Entry &e = table.t[lo];
-    const int64_t n = e.n;
-    const int64_t i = static_cast<int64_t>(blockIdx.x - e.chunk0) * kChunk + threadIdx.x * 8;
-    const uint32_t kind = e.kind;
+    const int64_t first = static_cast<int64_t>(blockIdx.x - e.block0) * e.span * kChunk;
+    const int64_t chunks = (e.n - first + kChunk - 1) / kChunk;
+    const int left = chunks < e.span ? static_cast<int>(chunks) : static_cast<int>(e.span);
+    const int64_t i = first + threadIdx.x * 8;
     Rates c{k.step_size, k.root_scale, k.grad_scale, e.decay};
     if (k.device) {
         c.step_size = __ldg(k.device);
@@ -147,60 +251,27 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
         c.decay = __fsub_rn(1.0f, __fmul_rn(__ldg(k.device + 2), e.wd));
         c.grad_scale = __ldg(k.device + 3);
     }
-    float p[8], g[8], m[8], v[8], r[8];
-    const int64_t group = i / kGroup;
-    const bool live = i < n;
-    if (kind & kMaster)
-        fetch<float>(e.master, i, n, p);
-    else if (kind & kParamBf16)
-        fetch<__nv_bfloat16>(e.p, i, n, p);
-    else
-        fetch<float>(e.p, i, n, p);
-    if (kind & kGradBf16)
-        fetch<__nv_bfloat16>(e.g, i, n, g);
-    else
-        fetch<float>(e.g, i, n, g);
-    if (kind & kState8) {
-        decode8(fetch_codes(e.m, i, n), live ? e.m_scale[group] : 0.0f, m);
-        decode8(fetch_codes(e.v, i, n), live ? e.v_scale[group] : 0.0f, r);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(r[j], r[j]);
+    const bool narrow = (e.kind & kParamBf16) && !(e.kind & kMaster);
+    if (e.kind & kGradBf16) {
+        if (narrow)
+            run<__nv_bfloat16, __nv_bfloat16>(k, c, e, i, left);
+        else
+            run<float, __nv_bfloat16>(k, c, e, i, left);
     } else {
-        fetch<float>(e.m, i, n, m);
-        fetch<float>(e.v, i, n, v);
+        if (narrow)
+            run<__nv_bfloat16, float>(k, c, e, i, left);
+        else
+            run<float, float>(k, c, e, i, left);
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) update(k, c, g[j], p[j], m[j], v[j], r[j]);
-    if (kind & kState8) {
-        // values past the end have no gradient and no moments: they stay zero and leave amax alone
-        const float ms = group_scale(group_amax(m)), rs = group_scale(group_amax(r));
-        if (live) {
-            put_codes(e.m, i, n, encode8(m, __fdiv_rn(1.0f, ms)));
-            put_codes(e.v, i, n, encode8(r, __fdiv_rn(1.0f, rs)));
-            if ((threadIdx.x & 15) == 0) {
-                e.m_scale[group] = ms;
-                e.v_scale[group] = rs;
-            }
-        }
-    } else if (live) {
-        put<float>(e.m, i, n, m);
-        put<float>(e.v, i, n, v);
-    }
-    if (!live) return;
-    if (kind & kMaster) put<float>(e.master, i, n, p);
-    if (kind & kParamBf16)
-        put<__nv_bfloat16>(e.p, i, n, p);
-    else
-        put<float>(e.p, i, n, p);
 }
 
 template <int N>
-tpce_status launch(const Entry *entries, int count, uint32_t chunks, const Scalars &k, cudaStream_t s) {
+tpce_status launch(const Entry *entries, int count, uint32_t blocks, const Scalars &k, cudaStream_t s) {
     Table<N> table;
     std::copy(entries, entries + count, table.t);
     table.count = count;
     KernelTimer timer("adamw_step", s);
-    adamw_kernel<N><<<chunks, kThreads, 0, s>>>(table, k);
+    adamw_kernel<N><<<blocks, kThreads, 0, s>>>(table, k);
     return check_launch("adamw_step", s);
 }
 
@@ -255,25 +326,27 @@ extern "C" tpce_status tp_adamw_step(const tpce_adamw_tensor *tensors, int count
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     Entry entries[kLong];
     int held = 0;
-    uint32_t chunks = 0;
+    uint32_t blocks = 0;
     auto flush = [&]() -> tpce_status {
         if (!held) return TPCE_OK;
-        tpce_status st = held <= kShort ? launch<kShort>(entries, held, chunks, k, s)
-                                        : launch<kLong>(entries, held, chunks, k, s);
+        tpce_status st = held <= kShort ? launch<kShort>(entries, held, blocks, k, s)
+                                        : launch<kLong>(entries, held, blocks, k, s);
         held = 0;
-        chunks = 0;
+        blocks = 0;
         return st;
     };
     for (int i = 0; i < count; ++i) {
         const tpce_adamw_tensor &t = tensors[i];
         if (t.n == 0) continue;
         Entry &e = entries[held++];
-        e = Entry{t.p, t.master, t.g, t.m, t.v, t.m_scale, t.v_scale, t.n, chunks, 0u, 0.0f, 0.0f};
+        e = Entry{t.p, t.master, t.g, t.m, t.v, t.m_scale, t.v_scale, t.n, blocks, 0u, 0.0f, 0.0f, 1u, 0u};
         e.kind = (t.p_dtype == TPCE_BF16 ? kParamBf16 : 0u) | (t.master ? kMaster : 0u) |
                  (t.g_dtype == TPCE_BF16 ? kGradBf16 : 0u) | (t.state_bits == 8 ? kState8 : 0u);
         e.decay = static_cast<float>(1.0 - lr * t.weight_decay);
         e.wd = static_cast<float>(t.weight_decay);
-        chunks += static_cast<uint32_t>((t.n + kChunk - 1) / kChunk);
+        if (t.state_bits == 8 && total >= kSpanFrom) e.span = kSpan;
+        const int64_t block = static_cast<int64_t>(e.span) * kChunk;
+        blocks += static_cast<uint32_t>((t.n + block - 1) / block);
         if (held == kLong) {
             tpce_status st = flush();
             if (st != TPCE_OK) return st;

@@ -17,6 +17,7 @@
 #include <algorithm>
 #include <climits>
 #include <initializer_list>
+#include <type_traits>
 
 #include "host.h"
 #include "ptx.cuh"
@@ -37,6 +38,7 @@ constexpr int kMaxChoices = 32;
 // summed over the block's warps, over the cluster's blocks (distributed shared
 // memory) and over the experts; pass 2 adds them to the rank.
 constexpr int kPlanWarps = 32;
+constexpr int kBatch = 8;  // vectors of 32 assignments whose loads are under way at once
 
 __device__ __forceinline__ uint32_t read_cluster_u32(const uint32_t *p, uint32_t rank) {
     uint32_t v;
@@ -63,24 +65,29 @@ __global__ void __launch_bounds__(32 * kPlanWarps)
     uint32_t *mine = count + warp * E;
     for (int e = lane; e < E; e += 32) mine[e] = 0u;
     __syncwarp();
-    for (int64_t i0 = first; i0 < last; i0 += 32) {
-        const int64_t i = i0 + lane;
-        int e = -1;
-        if (i < last) {
-            e = __ldg(ids + i);
-            if (e < -1 || e >= E) {
-                ptx::record_error(err, kErrInvalid | (2u << 8));
-                e = -1;
-            }
+    for (int64_t i0 = first; i0 < last; i0 += 32 * kBatch) {
+        int e[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int64_t i = i0 + u * 32 + lane;
+            e[u] = i < last ? __ldg(ids + i) : -1;
         }
-        const uint32_t same = __match_any_sync(0xffffffffu, e);
-        const uint32_t before = __popc(same & ((1u << lane) - 1u));
-        uint32_t seen = 0u;
-        if (e >= 0) seen = mine[e];
-        __syncwarp();
-        if (e >= 0 && before == 0u) mine[e] = seen + __popc(same);
-        __syncwarp();
-        if (i < last) row[i] = e >= 0 ? static_cast<int32_t>(seen + before) : -1;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int64_t i = i0 + u * 32 + lane;
+            if (e[u] < -1 || e[u] >= E) {
+                ptx::record_error(err, kErrInvalid | (2u << 8));
+                e[u] = -1;
+            }
+            const uint32_t same = __match_any_sync(0xffffffffu, e[u]);
+            const uint32_t before = __popc(same & ((1u << lane) - 1u));
+            uint32_t seen = 0u;
+            if (e[u] >= 0) seen = mine[e[u]];
+            __syncwarp();
+            if (e[u] >= 0 && before == 0u) mine[e[u]] = seen + __popc(same);
+            __syncwarp();
+            if (i < last) row[i] = e[u] >= 0 ? static_cast<int32_t>(seen + before) : -1;
+        }
     }
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
@@ -133,13 +140,23 @@ __global__ void __launch_bounds__(32 * kPlanWarps)
         }
     }
     __syncthreads();
-    for (int64_t i = first + lane; i < last; i += 32) {
-        const int32_t r = row[i];
-        if (r < 0) continue;
-        const int x = __ldg(ids + i);
-        const uint32_t p = base[x] + mine[x] + static_cast<uint32_t>(r);
-        row[i] = static_cast<int32_t>(p);
-        source[p] = static_cast<int32_t>(i);
+    for (int64_t i0 = first + lane; i0 < last; i0 += 32 * kBatch) {
+        int32_t r[kBatch];
+        int x[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int64_t i = i0 + u * 32;
+            r[u] = i < last ? row[i] : -1;
+            x[u] = i < last ? __ldg(ids + i) : 0;
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int64_t i = i0 + u * 32;
+            if (r[u] < 0) continue;  // past the run, or dropped: row[i] is -1 already
+            const uint32_t p = base[x[u]] + mine[x[u]] + static_cast<uint32_t>(r[u]);
+            row[i] = static_cast<int32_t>(p);
+            source[p] = static_cast<int32_t>(i);
+        }
     }
     for (int64_t p = kept + static_cast<int64_t>(rank) * blockDim.x + threadIdx.x; p < n;
          p += static_cast<int64_t>(ctas) * blockDim.x)
@@ -153,20 +170,32 @@ struct Split {
     int lanes;   // a power of two, 8 .. 256
     int tokens;  // of a block
 };
-inline Split split_of(int64_t vectors) {
+// Four vectors a thread keep enough loads under way; where that would leave
+// SMs without a block, as many threads as there are vectors.
+inline Split split_of(int64_t vectors, int64_t T) {
     int lanes = 8;
-    while (lanes < 256 && lanes < vectors) lanes *= 2;
+    while (lanes < 256 && lanes * 4 < vectors) lanes *= 2;
+    if (T * lanes < int64_t{256} * num_sms())
+        while (lanes < 256 && lanes < vectors) lanes *= 2;
     return {lanes, 256 / lanes};
 }
 
 // A place read from the plan; one outside the rows is reported and skipped.
-__device__ __forceinline__ int64_t place(const int32_t *row, int64_t i, int64_t n, uint32_t *err) {
-    const int64_t p = __ldg(row + i);
+__device__ __forceinline__ int32_t place(const int32_t *row, int64_t i, int64_t n, uint32_t *err) {
+    const int32_t p = __ldg(row + i);
     if (p < -1 || p >= n) {
         ptx::record_error(err, kErrInvalid | (3u << 8));
         return -1;
     }
     return p;
+}
+
+// The places of K of token t's choices from `row` on, -1 beyond the `left` that it has.
+template <int K>
+__device__ __forceinline__ void places(const int32_t *row, int64_t t, int k, int64_t n, uint32_t *err,
+                                       int32_t (&p)[K], int left) {
+#pragma unroll
+    for (int j = 0; j < K; ++j) p[j] = j < left ? place(row, t * k + j, n, err) : -1;
 }
 
 // Rows offsets[E] .. n of out are zeros: the blocks take them in turn.
@@ -176,6 +205,9 @@ __device__ __forceinline__ void zero_rest(uint4 *out, const int32_t *offsets, in
         for (int c = threadIdx.x; c < vectors; c += blockDim.x) out[p * vectors + c] = make_uint4(0u, 0u, 0u, 0u);
 }
 
+// The kernels hold the places of a token's K choices in registers; for k > K
+// (K is the largest then) they take the choices K at a time.
+template <int K>
 __global__ void __launch_bounds__(256)
     expert_dispatch_kernel(const uint4 *__restrict__ X, const int32_t *__restrict__ row,
                            const int32_t *__restrict__ offsets, int E, int64_t T, int k, int vectors, int lanes,
@@ -184,11 +216,15 @@ __global__ void __launch_bounds__(256)
     const int lane = threadIdx.x & (lanes - 1);
     const int64_t n = T * k;
     if (t < T) {
-        for (int c = lane; c < vectors; c += lanes) {
-            const uint4 v = __ldg(X + t * vectors + c);
-            for (int j = 0; j < k; ++j) {
-                const int64_t p = place(row, t * k + j, n, err);
-                if (p >= 0) out[p * vectors + c] = v;
+        for (int j0 = 0; j0 < k; j0 += K) {
+            int32_t p[K];
+            places(row + j0, t, k, n, err, p, k - j0);
+#pragma unroll 4
+            for (int c = lane; c < vectors; c += lanes) {
+                const uint4 v = __ldg(X + t * vectors + c);
+#pragma unroll
+                for (int j = 0; j < K; ++j)
+                    if (p[j] >= 0) out[static_cast<int64_t>(p[j]) * vectors + c] = v;
             }
         }
     }
@@ -213,7 +249,7 @@ __device__ __forceinline__ uint4 narrow(const float (&v)[4]) {
 }
 
 // NV values a vector: 8 (bf16) or 4 (fp32). weights NULL: all one.
-template <int NV>
+template <int NV, int K>
 __global__ void __launch_bounds__(256)
     expert_combine_kernel(const uint4 *__restrict__ Ys, const int32_t *__restrict__ row,
                           const float *__restrict__ weights, int64_t T, int k, int vectors, int lanes,
@@ -222,59 +258,119 @@ __global__ void __launch_bounds__(256)
     const int lane = threadIdx.x & (lanes - 1);
     if (t >= T) return;
     const int64_t n = T * k;
-    for (int c = lane; c < vectors; c += lanes) {
-        float z[NV] = {};
-#pragma unroll 4
-        for (int j = 0; j < k; ++j) {
-            const int64_t p = place(row, t * k + j, n, err);
-            if (p < 0) continue;
-            const float w = weights ? __ldg(weights + t * k + j) : 1.0f;
-            float y[NV];
-            widen(__ldg(Ys + p * vectors + c), y);
+    constexpr int U = K >= 4 ? 1 : 4 / K;  // vectors at a time: at least four loads under way
+    int32_t p[K];
+    float w[K];
+    auto choices = [&](int j0) {
+        places(row + j0, t, k, n, err, p, k - j0);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) z[i] += w * y[i];
+        for (int j = 0; j < K; ++j) w[j] = weights && j0 + j < k ? __ldg(weights + t * k + j0 + j) : 1.0f;
+    };
+    if (k <= K) choices(0);
+    for (int c0 = lane; c0 < vectors; c0 += U * lanes) {
+        float z[U][NV] = {};
+        for (int j0 = 0; j0 < k; j0 += K) {
+            if (k > K) choices(j0);
+            uint4 y[U][K];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int j = 0; j < K; ++j)
+                    if (p[j] >= 0 && c0 + u * lanes < vectors)
+                        y[u][j] = __ldg(Ys + static_cast<int64_t>(p[j]) * vectors + c0 + u * lanes);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int j = 0; j < K; ++j) {
+                    if (p[j] < 0) continue;
+                    float v[NV];
+                    widen(y[u][j], v);
+#pragma unroll
+                    for (int i = 0; i < NV; ++i) z[u][i] += w[j] * v[i];
+                }
         }
-        Z[t * vectors + c] = narrow(z);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (c0 + u * lanes < vectors) Z[t * vectors + c0 + u * lanes] = narrow(z[u]);
     }
 }
 
-template <int NV>
+template <int NV, int K>
 __global__ void __launch_bounds__(256)
     expert_combine_backward_kernel(const uint4 *__restrict__ dZ, const uint4 *__restrict__ Ys,
                                    const int32_t *__restrict__ row, const int32_t *__restrict__ offsets, int E,
                                    const float *__restrict__ weights, int64_t T, int k, int vectors, int lanes,
                                    uint4 *__restrict__ dYs, float *__restrict__ dweights, uint32_t *err) {
-    __shared__ float red[8];
+    __shared__ float red[8][K];
     const int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x / lanes) + threadIdx.x / lanes;
     const int lane = threadIdx.x & (lanes - 1);
     const int64_t n = T * k;
-    for (int j = 0; j < k; ++j) {
-        const int64_t p = t < T ? place(row, t * k + j, n, err) : -1;
-        float dot = 0.0f;
-        if (p >= 0) {
-            const float w = __ldg(weights + t * k + j);
-            for (int c = lane; c < vectors; c += lanes) {
-                float d[NV], y[NV];
-                widen(__ldg(dZ + t * vectors + c), d);
-                widen(__ldg(Ys + p * vectors + c), y);
+    constexpr int U = K >= 4 ? 1 : 4 / K;
+    for (int j0 = 0; j0 < k; j0 += K) {
+        int32_t p[K];
+        float w[K], dot[K] = {};
 #pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    dot += d[i] * y[i];
-                    d[i] *= w;
+        for (int j = 0; j < K; ++j) p[j] = -1, w[j] = 0.0f;
+        if (t < T) {
+            places(row + j0, t, k, n, err, p, k - j0);
+#pragma unroll
+            for (int j = 0; j < K; ++j)
+                if (p[j] >= 0) w[j] = __ldg(weights + t * k + j0 + j);
+            for (int c0 = lane; c0 < vectors; c0 += U * lanes) {
+                uint4 d[U], y[U][K];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int c = c0 + u * lanes;
+                    if (c >= vectors) continue;
+                    d[u] = __ldg(dZ + t * vectors + c);
+#pragma unroll
+                    for (int j = 0; j < K; ++j)
+                        if (p[j] >= 0) y[u][j] = __ldg(Ys + static_cast<int64_t>(p[j]) * vectors + c);
                 }
-                dYs[p * vectors + c] = narrow(d);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int c = c0 + u * lanes;
+                    if (c >= vectors) continue;
+                    float dv[NV];
+                    widen(d[u], dv);
+#pragma unroll
+                    for (int j = 0; j < K; ++j) {
+                        if (p[j] < 0) continue;
+                        float yv[NV], o[NV];
+                        widen(y[u][j], yv);
+#pragma unroll
+                        for (int i = 0; i < NV; ++i) {
+                            dot[j] += dv[i] * yv[i];
+                            o[i] = dv[i] * w[j];
+                        }
+                        dYs[static_cast<int64_t>(p[j]) * vectors + c] = narrow(o);
+                    }
+                }
             }
         }
         // over the token's lanes: within a warp, then over its warps
-        for (int d = min(lanes, 32) / 2; d > 0; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+            for (int d = min(lanes, 32) / 2; d > 0; d >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], d);
         if (lanes > 32) {
-            if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = dot;
+            const int warp = threadIdx.x >> 5;
+            if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+                for (int j = 0; j < K; ++j) red[warp][j] = dot[j];
+            }
             __syncthreads();
-            if (lane == 0)
-                for (int q = 1; q < lanes / 32; ++q) dot += red[(threadIdx.x >> 5) + q];
+            if (lane == 0) {
+#pragma unroll
+                for (int j = 0; j < K; ++j)
+                    for (int q = 1; q < lanes / 32; ++q) dot[j] += red[warp + q][j];
+            }
             __syncthreads();
         }
-        if (lane == 0 && t < T) dweights[t * k + j] = dot;
+        if (lane == 0 && t < T) {
+#pragma unroll
+            for (int j = 0; j < K; ++j)
+                if (j0 + j < k) dweights[t * k + j0 + j] = dot[j];
+        }
     }
     zero_rest(dYs, offsets, E, n, vectors);
 }
@@ -308,19 +404,30 @@ inline int vectors_of(int64_t h, int dtype) { return static_cast<int>(h * (dtype
 
 inline unsigned blocks_of(int64_t T, const Split &sp) { return static_cast<unsigned>((T + sp.tokens - 1) / sp.tokens); }
 
+// f(integral constant): the fewest of 1, 2, 4, 8 choices held that cover k (8 for more)
+template <typename F>
+void with_choices(int k, F f) {
+    if (k == 1) f(std::integral_constant<int, 1>{});
+    else if (k == 2) f(std::integral_constant<int, 2>{});
+    else if (k <= 4) f(std::integral_constant<int, 4>{});
+    else f(std::integral_constant<int, 8>{});
+}
+
 tpce_status combine(const char *name, const void *Ys, const int32_t *row, const float *weights, int64_t T, int64_t h,
                     int k, int dtype, void *Z, cudaStream_t s) {
     const int v = vectors_of(h, dtype);
-    const Split sp = split_of(v);
+    const Split sp = split_of(v, T);
     KernelTimer timer(name, s);
-    auto go = [&](auto kernel) {
-        kernel<<<blocks_of(T, sp), 256, 0, s>>>(static_cast<const uint4 *>(Ys), row, weights, T, k, v, sp.lanes,
-                                                static_cast<uint4 *>(Z), device_error_word());
-    };
-    if (dtype == TPCE_BF16)
-        go(expert_combine_kernel<8>);
-    else
-        go(expert_combine_kernel<4>);
+    with_choices(k, [&](auto K) {
+        auto go = [&](auto kernel) {
+            kernel<<<blocks_of(T, sp), 256, 0, s>>>(static_cast<const uint4 *>(Ys), row, weights, T, k, v, sp.lanes,
+                                                    static_cast<uint4 *>(Z), device_error_word());
+        };
+        if (dtype == TPCE_BF16)
+            go(expert_combine_kernel<8, decltype(K)::value>);
+        else
+            go(expert_combine_kernel<4, decltype(K)::value>);
+    });
     return check_launch(name, s);
 }
 
@@ -373,10 +480,13 @@ extern "C" tpce_status tp_expert_dispatch_forward(const void *X, const int32_t *
     if ((st = check_pointers("tp_expert_dispatch_forward", {X, row, offsets, Xs})) != TPCE_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int v = vectors_of(h, dtype);
-    const Split sp = split_of(v);
+    const Split sp = split_of(v, T);
     KernelTimer timer("expert_dispatch", s);
-    expert_dispatch_kernel<<<blocks_of(T, sp), 256, 0, s>>>(static_cast<const uint4 *>(X), row, offsets, E, T, k, v,
-                                                            sp.lanes, static_cast<uint4 *>(Xs), device_error_word());
+    with_choices(k, [&](auto K) {
+        expert_dispatch_kernel<decltype(K)::value>
+            <<<blocks_of(T, sp), 256, 0, s>>>(static_cast<const uint4 *>(X), row, offsets, E, T, k, v, sp.lanes,
+                                              static_cast<uint4 *>(Xs), device_error_word());
+    });
     return check_launch("expert_dispatch", s);
 }
 
@@ -405,16 +515,18 @@ extern "C" tpce_status tp_expert_combine_backward(const void *dZ, const void *Ys
         return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int v = vectors_of(h, dtype);
-    const Split sp = split_of(v);
+    const Split sp = split_of(v, T);
     KernelTimer timer("expert_combine_backward", s);
-    auto go = [&](auto kernel) {
-        kernel<<<blocks_of(T, sp), 256, 0, s>>>(static_cast<const uint4 *>(dZ), static_cast<const uint4 *>(Ys), row,
-                                                offsets, E, weights, T, k, v, sp.lanes, static_cast<uint4 *>(dYs),
-                                                dweights, device_error_word());
-    };
-    if (dtype == TPCE_BF16)
-        go(expert_combine_backward_kernel<8>);
-    else
-        go(expert_combine_backward_kernel<4>);
+    with_choices(k, [&](auto K) {
+        auto go = [&](auto kernel) {
+            kernel<<<blocks_of(T, sp), 256, 0, s>>>(static_cast<const uint4 *>(dZ), static_cast<const uint4 *>(Ys),
+                                                    row, offsets, E, weights, T, k, v, sp.lanes,
+                                                    static_cast<uint4 *>(dYs), dweights, device_error_word());
+        };
+        if (dtype == TPCE_BF16)
+            go(expert_combine_backward_kernel<8, decltype(K)::value>);
+        else
+            go(expert_combine_backward_kernel<4, decltype(K)::value>);
+    });
     return check_launch("expert_combine_backward", s);
 }

@@ -10,10 +10,16 @@
 // X and R enter as a sum, so dX is the gradient of both.
 //
 // Both passes read each row once: its values stay in registers between the
-// sum over the row and the output.
+// sum over the row and the output. They are bound by HBM (8 bytes a value in
+// bf16 with the residual), so what matters is the bytes on their way: wide rows
+// come through a ring in shared memory that bulk copies fill some rows ahead,
+// whatever the threads wait for; narrow ones are a warp's, which holds its next
+// row in registers.
 #include <algorithm>
+#include <atomic>
 
 #include "host.h"
+#include "ptx.cuh"
 #include "step/vec.cuh"
 
 namespace tpce {
@@ -21,193 +27,415 @@ namespace {
 
 using namespace step;
 
-constexpr int64_t kMaxWidth = 16384;  // 4 vectors of 8 values for each of 512 threads
+constexpr int64_t kMaxWidth = 16384;  // 2 vectors of 8 values for each of 1024 threads, 4 for each of 512
 constexpr int64_t kMaxRows = int64_t{1} << 40;
 constexpr int kWarps = 8;             // rows of a block where a warp takes a row
-constexpr int64_t kBlocks = 304;      // blocks of the backward: two for each of 152 SMs (fixed, so that the
-                                      // workspace's size is known on the host)
+constexpr int64_t kSms = 152;         // fixed, so that the workspace's size is known on the host
+constexpr int kMaxStages = 4;
+constexpr int kRowsOfBlock = 6;       // of the forward, where there are enough
+constexpr int kSmemPerSm = 228 * 1024;
 
-// A row of up to 1024 values is a warp's (no barrier in its sum), a wider one a block's.
-inline bool warp_rows(int64_t h) { return h <= 1024; }
+// A row of up to 256 values is a warp's (no barrier in its sum), a wider one a block's.
+inline bool warp_rows(int64_t h) { return h <= 256; }
 
-// Where a thread's row is and which of its vectors are the thread's.
-template <bool WARP>
-struct Place {
-    int lane, lanes;       // this thread's place among those that share the row
-    int64_t row, stride;   // first row, rows between
-    __device__ Place() {
-        if (WARP) {
-            lane = threadIdx.x & 31;
-            lanes = 32;
-            row = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-            stride = static_cast<int64_t>(gridDim.x) * kWarps;
-        } else {
-            lane = threadIdx.x;
-            lanes = blockDim.x;
-            row = blockIdx.x;
-            stride = gridDim.x;
-        }
-    }
-};
-
-template <bool WARP>
-__device__ __forceinline__ float row_sum(float x, float *buf) {
-    return WARP ? warp_sum(x) : block_sum(x, buf);
-}
-
-// The vectors of row r of X that are this thread's; zeros past the row's end.
+// The vectors of a row that are this thread's; zeros past the row's end.
 template <typename T, int VPT>
-__device__ __forceinline__ void load_row(const T *X, int64_t r, int h, int lane, int lanes, Raw8<T> (&v)[VPT]) {
+__device__ __forceinline__ void load_row(const T *x, int h, int lane, int lanes, Raw8<T> (&v)[VPT]) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int c = (lane + i * lanes) * 8;
         if (c < h)
-            v[i] = load8(X + r * h + c);
+            v[i] = load8(x + c);
         else
             zero8(v[i]);
     }
 }
-
-template <typename T, int VPT, bool WARP>
-__global__ void __launch_bounds__(WARP ? 32 * kWarps : 512)
-    rmsnorm_forward_kernel(const T *X, const T *R, const float *__restrict__ w, int64_t rows, int h, float eps, T *S,
-                           T *Y, uint8_t *Q, float *Qs, float *__restrict__ rstd_out) {
-    __shared__ float red[2][32];
-    Place<WARP> at;
-    const int groups = (h + kGroup - 1) / kGroup;
-    int turn = 0;
-    Raw8<T> x[VPT], r[VPT];
-    if (at.row < rows) {
-        load_row(X, at.row, h, at.lane, at.lanes, x);
-        if (R) load_row(R, at.row, h, at.lane, at.lanes, r);
+template <int VPT>
+__device__ __forceinline__ void load_weight(const float *w, int h, int lane, int lanes, float (&v)[VPT][8]) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int c = (lane + i * lanes) * 8;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+        if (c < h) load8f(w + c, v[i]);
     }
-    for (int64_t row = at.row; row < rows; row += at.stride) {
-        float s[VPT][8], sq = 0.0f;
+}
+
+// ------------------------------------------------------------------ the ring
+// Stage n % stages holds the n-th row of this block: the rows of up to three
+// tensors, each of `bytes`. Thread 0 fills a stage again after a barrier that
+// every thread passes when it has read the stage. Waits are bounded (ptx.cuh):
+// after one that ran out nothing more is copied, and the block leaves when what
+// was under way has landed.
+struct Ring {
+    uint8_t *data;
+    uint64_t *full;
+    volatile int *abort;
+    uint32_t *err;
+    int stages, bytes, tensors;
+
+    __device__ void init() {
+        if (threadIdx.x == 0) {
+            *abort = 0;
+            for (int i = 0; i < stages; ++i) ptx::mbar_init(full + i, 1);
+            ptx::fence_mbar_init();
+        }
+        __syncthreads();
+    }
+    // thread 0 only: the rows at `offset` bytes of the tensors into a stage
+    __device__ void fill(int stage, const void *a, const void *b, const void *c, int64_t offset) {
+        if (*abort) return;
+        ptx::mbar_arrive_expect_tx(full + stage, static_cast<uint32_t>(bytes) * tensors);
+        uint8_t *to = data + stage * bytes * tensors;
+        copy(to, a, offset, stage);
+        if (tensors > 1) copy(to + bytes, b, offset, stage);
+        if (tensors > 2) copy(to + 2 * bytes, c, offset, stage);
+    }
+    __device__ void copy(void *dst, const void *src, int64_t offset, int stage) {
+        // read once: first to leave L2
+        asm volatile(
+            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], "
+            "%4;" ::"r"(ptx::smem_u32(dst)),
+            "l"(static_cast<const uint8_t *>(src) + offset), "r"(bytes), "r"(ptx::smem_u32(full + stage)),
+            "l"(ptx::l2_policy_evict_first())
+            : "memory");
+    }
+    __device__ void wait(int stage, int phase) { ptx::mbar_wait(full + stage, phase, abort, err, 20u); }
+    // thread 0 only, after the last row: `filled` fills in all
+    __device__ void leave(int filled) {
+        if (!*abort) return;
+        for (int n = filled > stages ? filled - stages : 0; n < filled; ++n)
+            ptx::mbar_wait_drain(full + n % stages, (n / stages) & 1);
+    }
+};
+
+// ------------------------------------------------------------------ forward
+template <typename T, int VPT>
+struct ForwardRow {
+    float s[VPT][8];
+
+    // S of this thread's vectors, to S + off of the row; returns the sum of their squares
+    __device__ __forceinline__ float add(const Raw8<T> (&x)[VPT], const Raw8<T> (&r)[VPT], bool residual, T *S,
+                                         int64_t off, int h, int lane, int lanes) {
+        float sq = 0.0f, sq1 = 0.0f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            unpack8(x[i], s[i]);
-            if (R) {
-                float b[8];
-                unpack8(r[i], b);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) s[i][j] += b[j];
+            if (residual) {
                 Raw8<T> o;
-                pack8(s[i], o);
-                const int c = (at.lane + i * at.lanes) * 8;
-                if (c < h) store8(S + row * h + c, o);
+                add8(x[i], r[i], o);
+                const int c = (lane + i * lanes) * 8;
+                if (c < h) stream8(S + off + c, o);
                 unpack8(o, s[i]);
+            } else {
+                unpack8(x[i], s[i]);
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sq += s[i][j] * s[i][j];
+            for (int j = 0; j < 4; ++j) fma2(sq, sq1, s[i][2 * j], s[i][2 * j + 1], s[i][2 * j], s[i][2 * j + 1]);
         }
-        // the next row is on its way while this one is summed and written
-        if (row + at.stride < rows) {
-            load_row(X, row + at.stride, h, at.lane, at.lanes, x);
-            if (R) load_row(R, row + at.stride, h, at.lane, at.lanes, r);
-        }
-        const float total = row_sum<WARP>(sq, red[turn & 1]);
-        ++turn;
-        const float rstd = 1.0f / sqrtf(total * (1.0f / static_cast<float>(h)) + eps);
-        if (at.lane == 0) rstd_out[row] = rstd;
+        return sq + sq1;
+    }
+
+    __device__ __forceinline__ void finish(float total, float inv_h, float eps, const float (&w)[VPT][8], T *Y,
+                                           uint8_t *Q, float *Qs, float *rstd_out, int64_t row, int64_t off, int h,
+                                           int lane, int lanes) {
+        const float rstd = rsqrtf(total * inv_h + eps);
+        if (lane == 0) rstd_out[row] = rstd;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int c = (at.lane + i * at.lanes) * 8;
-            float wv[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (c < h) load8f(w + c, wv);
+            const int c = (lane + i * lanes) * 8;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s[i][j] = s[i][j] * rstd * wv[j];
+            for (int j = 0; j < 4; ++j) {
+                mul2(s[i][2 * j], s[i][2 * j + 1], rstd, rstd);
+                mul2(s[i][2 * j], s[i][2 * j + 1], w[i][2 * j], w[i][2 * j + 1]);
+            }
             if (Y && c < h) {
                 Raw8<T> o;
                 pack8(s[i], o);
-                store8(Y + row * h + c, o);
+                stream8(Y + off + c, o);
             }
             if (Q) {
-                const float scale = group_scale(group_amax(s[i]));  // lanes past the row's end bring zeros
+                // lanes past the row's end bring zeros
+                if (c >= h) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) s[i][j] = 0.0f;
+                }
+                float scale;
+                const uint2 q = quantize8(s[i], scale);
                 if (c < h) {
-                    *reinterpret_cast<uint2 *>(Q + row * h + c) = encode8(s[i], 1.0f / scale);
-                    if ((at.lane & 15) == 0) Qs[row * groups + c / kGroup] = scale;
+                    __stcs(reinterpret_cast<uint2 *>(Q + off + c), q);
+                    if ((lane & 15) == 0) Qs[row * ((h + kGroup - 1) / kGroup) + c / kGroup] = scale;
                 }
             }
         }
     }
+};
+
+template <typename T>
+__global__ void __launch_bounds__(32 * kWarps)
+    rmsnorm_forward_warp_kernel(const T *X, const T *R, const float *__restrict__ w, int64_t rows, int h, float eps,
+                                T *S, T *Y, uint8_t *Q, float *Qs, float *__restrict__ rstd) {
+    const int lane = threadIdx.x & 31;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kWarps;
+    const float inv_h = 1.0f / static_cast<float>(h);
+    int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    float wv[1][8];
+    load_weight(w, h, lane, 32, wv);
+    Raw8<T> x[1], r[1];
+    if (row < rows) {
+        load_row(X + row * h, h, lane, 32, x);
+        if (R) load_row(R + row * h, h, lane, 32, r);
+    }
+    for (; row < rows; row += stride) {
+        ForwardRow<T, 1> f;
+        const float sq = f.add(x, r, R, S, row * h, h, lane, 32);
+        // the next row is on its way while this one is summed and written
+        if (row + stride < rows) {
+            load_row(X + (row + stride) * h, h, lane, 32, x);
+            if (R) load_row(R + (row + stride) * h, h, lane, 32, r);
+        }
+        f.finish(warp_sum(sq), inv_h, eps, wv, Y, Q, Qs, rstd, row, row * h, h, lane, 32);
+    }
 }
 
-template <typename T, int VPT, bool WARP>
-__global__ void __launch_bounds__(WARP ? 32 * kWarps : 512)
-    rmsnorm_backward_kernel(const T *dY, const T *S, const float *__restrict__ w, const float *__restrict__ rstd_in,
-                            const T *dS, int64_t rows, int h, T *dX, float *__restrict__ part) {
+template <typename T, int VPT, bool RING>
+__global__ void __launch_bounds__(1024)
+    rmsnorm_forward_block_kernel(const T *X, const T *R, const float *__restrict__ w, int64_t rows, int h, float eps,
+                                 T *S, T *Y, uint8_t *Q, float *Qs, float *__restrict__ rstd, int stages,
+                                 uint32_t *err) {
+    extern __shared__ __align__(128) uint8_t data[];
+    __shared__ uint64_t full[kMaxStages];
+    __shared__ int abort;
     __shared__ float red[2][32];
-    __shared__ float fold[WARP ? kWarps * 32 * 8 : 1];
-    Place<WARP> at;
-    int turn = 0;
+    const int lane = threadIdx.x, lanes = blockDim.x;
+    const float inv_h = 1.0f / static_cast<float>(h);
+    const int64_t stride = gridDim.x, row_bytes = static_cast<int64_t>(h) * sizeof(T);
+    Ring ring{data, full, &abort, err, stages, static_cast<int>(row_bytes), R ? 2 : 1};
+    int filled = 0;
+    if (RING) {
+        ring.init();
+        if (lane == 0)
+            for (int64_t r = blockIdx.x; filled < stages && r < rows; ++filled, r += stride)
+                ring.fill(filled, X, R, nullptr, r * row_bytes);
+    }
+    float wv[VPT][8];
+    load_weight(w, h, lane, lanes, wv);
+    int stage = 0, phase = 0, turn = 0;
+    const int64_t step = stride * h;
+    int64_t off = static_cast<int64_t>(blockIdx.x) * h;
+    for (int64_t row = blockIdx.x; row < rows; row += stride, off += step, turn ^= 1) {
+        Raw8<T> x[VPT], r[VPT];
+        if (RING) {
+            ring.wait(stage, phase);
+            const uint8_t *at = data + stage * ring.bytes * ring.tensors;
+            load_row(reinterpret_cast<const T *>(at), h, lane, lanes, x);
+            if (R) load_row(reinterpret_cast<const T *>(at + ring.bytes), h, lane, lanes, r);
+        } else {
+            load_row(X + off, h, lane, lanes, x);
+            if (R) load_row(R + off, h, lane, lanes, r);
+        }
+        ForwardRow<T, VPT> f;
+        const float sq = f.add(x, r, R, S, off, h, lane, lanes);
+        const float total = block_sum(sq, red[turn]);  // its barrier: every thread has read the stage
+        if (RING) {
+            if (lane == 0 && row + stages * stride < rows) {
+                ring.fill(stage, X, R, nullptr, (row + stages * stride) * row_bytes);
+                ++filled;
+            }
+            if (++stage == stages) stage = 0, phase ^= 1;
+        }
+        f.finish(total, inv_h, eps, wv, Y, Q, Qs, rstd, row, off, h, lane, lanes);
+    }
+    if (RING && lane == 0) ring.leave(filled);
+}
+
+// ------------------------------------------------------------------ backward
+// A thread's weights: with one vector they stay in registers, with more they are
+// read again for each vector (the registers hold the sums of dw).
+template <int VPT>
+struct Weights {
+    const float *w;
+    int h, lane, lanes;
+    float held[8];
+    __device__ __forceinline__ Weights(const float *w_, int h_, int lane_, int lanes_)
+        : w(w_), h(h_), lane(lane_), lanes(lanes_) {
+        if (VPT == 1) read(w, 0, held);
+    }
+    __device__ __forceinline__ void read(const float *from, int i, float (&v)[8]) const {
+        const int c = (lane + i * lanes) * 8;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+        if (c < h) load8f(from + c, v);
+    }
+    __device__ __forceinline__ void get(int i, float (&v)[8]) const {
+        if (VPT == 1) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = held[j];
+        } else {
+            // the compiler, which would keep what it has read before, does not know the pointer again
+            const float *again = w;
+            asm volatile("" : "+l"(again));
+            read(again, i, v);
+        }
+    }
+};
+
+// dY xh goes to dw; returns this thread's part of sum g xh.
+template <typename T, int VPT>
+__device__ __forceinline__ float backward_dots(const Raw8<T> (&y)[VPT], const Raw8<T> (&x)[VPT],
+                                               const Weights<VPT> &weights, float rstd, float (&dw)[VPT][8]) {
+    float c = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        float g[8], xh[8], w[8];
+        weights.get(i, w);
+        unpack8(y[i], g);
+        unpack8(x[i], xh);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            xh[j] *= rstd;
+            dw[i][j] += g[j] * xh[j];
+            c += g[j] * w[j] * xh[j];
+        }
+    }
+    return c;
+}
+
+// c = sum g xh / h; to dX, whose row begins there
+template <typename T, int VPT>
+__device__ __forceinline__ void backward_finish(float c, float rstd, const Raw8<T> (&y)[VPT], const Raw8<T> (&x)[VPT],
+                                                const Weights<VPT> &weights, const Raw8<T> (&d)[VPT], bool residual,
+                                                T *dX, int h, int lane, int lanes) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int col = (lane + i * lanes) * 8;
+        float g[8], xh[8], w[8];
+        weights.get(i, w);
+        unpack8(y[i], g);
+        unpack8(x[i], xh);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[j] = (g[j] * w[j] - xh[j] * rstd * c) * rstd;
+        if (residual) {
+            float b[8];
+            unpack8(d[i], b);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) g[j] += b[j];
+        }
+        Raw8<T> out;
+        pack8(g, out);
+        if (col < h) stream8(dX + col, out);
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(32 * kWarps)
+    rmsnorm_backward_warp_kernel(const T *dY, const T *S, const float *__restrict__ w, const float *__restrict__ rstd,
+                                 const T *dS, int64_t rows, int h, T *dX, float *__restrict__ part) {
+    __shared__ float fold[kWarps * 32 * 8];
+    const int lane = threadIdx.x & 31;
+    const float inv_h = 1.0f / static_cast<float>(h);
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kWarps;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    const Weights<1> wv(w, h, lane, 32);
+    float dw[1][8] = {}, r = 0.0f;
+    Raw8<T> y[1], x[1], d[1];
+    if (row < rows) {
+        r = __ldg(rstd + row);
+        load_row(dY + row * h, h, lane, 32, y);
+        load_row(S + row * h, h, lane, 32, x);
+        if (dS) load_row(dS + row * h, h, lane, 32, d);
+    }
+    for (; row < rows; row += stride) {
+        const float now = r;
+        const Raw8<T> y0[1] = {y[0]}, x0[1] = {x[0]}, d0[1] = {d[0]};
+        const int64_t next = row + stride;
+        // the next row is on its way while this one is summed and written
+        if (next < rows) {
+            r = __ldg(rstd + next);
+            load_row(dY + next * h, h, lane, 32, y);
+            load_row(S + next * h, h, lane, 32, x);
+            if (dS) load_row(dS + next * h, h, lane, 32, d);
+        }
+        const float c = warp_sum(backward_dots(y0, x0, wv, now, dw)) * inv_h;
+        backward_finish(c, now, y0, x0, wv, d0, dS, dX + row * h, h, lane, 32);
+    }
+    if (!part) return;
+    // the block's warps hold the same columns: add them in warp order
+#pragma unroll
+    for (int j = 0; j < 8; ++j) fold[(threadIdx.x >> 5) * 256 + lane * 8 + j] = dw[0][j];
+    __syncthreads();
+    const int c = threadIdx.x;  // 256 threads, up to 256 columns
+    if (c < h) {
+        float s = 0.0f;
+#pragma unroll
+        for (int q = 0; q < kWarps; ++q) s += fold[q * 256 + c];
+        part[static_cast<int64_t>(blockIdx.x) * h + c] = s;
+    }
+}
+
+template <typename T, int VPT, bool RING>
+__global__ void __launch_bounds__(VPT == 4 ? 512 : 1024)
+    rmsnorm_backward_block_kernel(const T *dY, const T *S, const float *__restrict__ w, const float *__restrict__ rstd,
+                                  const T *dS, int64_t rows, int h, T *dX, float *__restrict__ part, int stages,
+                                  uint32_t *err) {
+    extern __shared__ __align__(128) uint8_t data[];
+    __shared__ uint64_t full[kMaxStages];
+    __shared__ int abort;
+    __shared__ float red[2][32];
+    const int lane = threadIdx.x, lanes = blockDim.x;
+    const int64_t stride = gridDim.x, row_bytes = static_cast<int64_t>(h) * sizeof(T);
+    Ring ring{data, full, &abort, err, stages, static_cast<int>(row_bytes), dS ? 3 : 2};
+    int filled = 0;
+    if (RING) {
+        ring.init();
+        if (lane == 0)
+            for (int64_t r = blockIdx.x; filled < stages && r < rows; ++filled, r += stride)
+                ring.fill(filled, dY, S, dS, r * row_bytes);
+    }
+    const Weights<VPT> wv(w, h, lane, lanes);
     float dw[VPT][8] = {};
-    Raw8<T> y[VPT], x[VPT], d[VPT];
-    if (at.row < rows) {
-        load_row(dY, at.row, h, at.lane, at.lanes, y);
-        load_row(S, at.row, h, at.lane, at.lanes, x);
-        if (dS) load_row(dS, at.row, h, at.lane, at.lanes, d);
-    }
-    for (int64_t row = at.row; row < rows; row += at.stride) {
-        const float rstd = __ldg(rstd_in + row);
-        float g[VPT][8], xh[VPT][8], c = 0.0f;
+    const float inv_h = 1.0f / static_cast<float>(h);
+    int stage = 0, phase = 0, turn = 0;
+    const int64_t step = stride * h;
+    int64_t off = static_cast<int64_t>(blockIdx.x) * h;
+    for (int64_t row = blockIdx.x; row < rows; row += stride, off += step, turn ^= 1) {
+        const float r = __ldg(rstd + row);
+        Raw8<T> y[VPT], x[VPT], d[VPT];
+        if (RING) {
+            ring.wait(stage, phase);
+            const uint8_t *at = data + stage * ring.bytes * ring.tensors;
+            load_row(reinterpret_cast<const T *>(at), h, lane, lanes, y);
+            load_row(reinterpret_cast<const T *>(at + ring.bytes), h, lane, lanes, x);
+            if (dS) load_row(reinterpret_cast<const T *>(at + 2 * ring.bytes), h, lane, lanes, d);
+        } else {
+            load_row(dY + off, h, lane, lanes, y);
+            load_row(S + off, h, lane, lanes, x);
+            if (dS) load_row(dS + off, h, lane, lanes, d);
+        }
+        const float c = backward_dots(y, x, wv, r, dw);
+        if (VPT > 1) {
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int col = (at.lane + i * at.lanes) * 8;
-            float wv[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (col < h) load8f(w + col, wv);
-            unpack8(y[i], g[i]);
-            unpack8(x[i], xh[i]);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                xh[i][j] *= rstd;
-                dw[i][j] += g[i][j] * xh[i][j];
-                g[i][j] *= wv[j];
-                c += g[i][j] * xh[i][j];
+            for (int i = 0; i < VPT; ++i) {
+                forget(y[i]);
+                forget(x[i]);
             }
         }
-        c = row_sum<WARP>(c, red[turn & 1]) * (1.0f / static_cast<float>(h));
-        ++turn;
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int col = (at.lane + i * at.lanes) * 8;
-            float o[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = (g[i][j] - xh[i][j] * c) * rstd;
-            if (dS) {
-                float b[8];
-                unpack8(d[i], b);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] += b[j];
+        const float total = block_sum(c, red[turn]);  // its barrier: every thread has read the stage
+        if (RING) {
+            if (lane == 0 && row + stages * stride < rows) {
+                ring.fill(stage, dY, S, dS, (row + stages * stride) * row_bytes);
+                ++filled;
             }
-            Raw8<T> out;
-            pack8(o, out);
-            if (col < h) store8(dX + row * h + col, out);
+            if (++stage == stages) stage = 0, phase ^= 1;
         }
-        if (row + at.stride < rows) {
-            load_row(dY, row + at.stride, h, at.lane, at.lanes, y);
-            load_row(S, row + at.stride, h, at.lane, at.lanes, x);
-            if (dS) load_row(dS, row + at.stride, h, at.lane, at.lanes, d);
-        }
+        backward_finish(total * inv_h, r, y, x, wv, d, dS, dX + off, h, lane, lanes);
     }
+    if (RING && lane == 0) ring.leave(filled);
     if (!part) return;
     float *mine = part + static_cast<int64_t>(blockIdx.x) * h;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int col = (at.lane + i * at.lanes) * 8;
-        if (WARP) {
-            // the block's warps hold the same columns: add them in warp order
-            __syncthreads();
-#pragma unroll
-            for (int j = 0; j < 8; ++j) fold[(threadIdx.x >> 5) * 256 + at.lane * 8 + j] = dw[i][j];
-            __syncthreads();
-            const int cc = i * 256 + threadIdx.x;  // 256 threads, the 256 columns of vector i
-            if (cc < h) {
-                float s = 0.0f;
-#pragma unroll
-                for (int q = 0; q < kWarps; ++q) s += fold[q * 256 + threadIdx.x];
-                mine[cc] = s;
-            }
-        } else if (col < h) {
+        const int col = (lane + i * lanes) * 8;
+        if (col < h) {
             float4 *o = reinterpret_cast<float4 *>(mine + col);
             o[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
             o[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
@@ -216,30 +444,73 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarps : 512)
 }
 
 // dw[c] = the blocks' partial sums, always in the same order: 32 columns a block,
-// each of 8 warps adding every eighth row.
-__global__ void __launch_bounds__(256) rmsnorm_dw_kernel(const float *__restrict__ part, int rows, int h,
-                                                         float *__restrict__ dw) {
-    __shared__ float red[8][32];
+// each of 32 warps adding every 32nd row.
+__global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(const float *__restrict__ part, int rows, int h,
+                                                          float *__restrict__ dw) {
+    __shared__ float red[32][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
     float s = 0.0f;
     if (c < h) {
-#pragma unroll 4
-        for (int r = warp; r < rows; r += 8) s += __ldg(part + static_cast<int64_t>(r) * h + c);
+#pragma unroll 8
+        for (int r = warp; r < rows; r += 32) s += __ldg(part + static_cast<int64_t>(r) * h + c);
     }
     red[warp][lane] = s;
     __syncthreads();
     if (warp == 0 && c < h) {
 #pragma unroll
-        for (int i = 1; i < 8; ++i) s += red[i][lane];
+        for (int i = 1; i < 32; ++i) s += red[i][lane];
         dw[c] = s;
     }
 }
 
-// Blocks of the backward and so rows of its partial sums.
-inline int64_t backward_blocks(int64_t T, int64_t h) {
-    return std::min<int64_t>(warp_rows(h) ? (T + kWarps - 1) / kWarps : T, kBlocks);
+// ------------------------------------------------------------------ host
+// Vectors a thread holds, threads of a block, blocks of an SM. The backward
+// has its sums of dw to hold too: one vector a thread as far as that goes.
+struct Layout {
+    int vpt, threads, blocks;
+};
+inline Layout layout_of(int64_t h, bool backward) {
+    const int v = static_cast<int>(h / 8);
+    if (warp_rows(h)) return {1, 32 * kWarps, 4};
+    const int vpt = backward ? (v <= 1024 ? 1 : 4) : (v <= 512 ? 1 : 2);
+    const int threads = ((v + vpt - 1) / vpt + 31) / 32 * 32;
+        return {vpt, threads, std::min(8, (vpt == 4 ? 512 : 1024) / threads)};
 }
+
+// Stages of the ring where `blocks` blocks share an SM; fewer blocks where two
+// stages would not fit, 0 stages where they do not fit even then.
+inline int stages_of(int64_t stage_bytes, int &blocks) {
+    for (; blocks >= 1; --blocks) {
+        const int64_t n = (kSmemPerSm / blocks - 2048) / stage_bytes;
+        if (n >= 2) return static_cast<int>(std::min<int64_t>(n, kMaxStages));
+    }
+    blocks = 1;
+    return 0;
+}
+
+// Blocks of the backward at most, and so rows of its partial sums.
+inline int64_t backward_blocks(int64_t T, int64_t h) {
+    return std::min<int64_t>(warp_rows(h) ? (T + kWarps - 1) / kWarps : T, layout_of(h, true).blocks * kSms);
+}
+
+// More than 48 KB of dynamic shared memory has to be asked for, once for each
+// kernel and device.
+template <auto Kernel>
+struct Fn {
+    static cudaError_t allow(int bytes) {
+        static std::atomic<uint64_t> done{0};
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess || bytes <= 48 * 1024) return e;
+        const uint64_t bit = uint64_t{1} << (dev & 63);
+        if (done.load() & bit) return cudaSuccess;
+        e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerSm - 4096);
+        if (e == cudaSuccess) done.fetch_or(bit);
+        return e;
+    }
+    static constexpr auto fn = Kernel;
+};
 
 tpce_status check_shape(int64_t T, int64_t h, int dtype) {
     if (dtype != TPCE_BF16 && dtype != TPCE_F32) return fail(TPCE_ERR_INVALID, "rmsnorm: dtype %d", dtype);
@@ -249,69 +520,90 @@ tpce_status check_shape(int64_t T, int64_t h, int dtype) {
     return TPCE_OK;
 }
 
-// Vectors a thread holds, and threads of a block.
-struct Launch {
-    int vpt, threads;
-};
-inline Launch launch_of(int64_t h) {
-    const int v = static_cast<int>(h / 8);
-    if (warp_rows(h)) return {v <= 32 ? 1 : v <= 64 ? 2 : 4, 32 * kWarps};
-    const int vpt = v <= 512 ? 1 : v <= 1024 ? 2 : 4;
-    return {vpt, ((v + vpt - 1) / vpt + 31) / 32 * 32};
-}
-
 template <typename T>
 tpce_status forward(const void *X, const void *R, const float *w, int64_t rows, int h, float eps, void *S, void *Y,
                     void *Q, float *Qs, float *rstd, cudaStream_t s) {
-    const Launch L = launch_of(h);
-    const bool warp = warp_rows(h);
-    const int64_t need = warp ? (rows + kWarps - 1) / kWarps : rows;
-    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(need, static_cast<int64_t>(num_sms()) * (2048 / L.threads)));
+    Layout L = layout_of(h, false);
+    const T *x = static_cast<const T *>(X), *r = static_cast<const T *>(R);
+    T *so = static_cast<T *>(S), *yo = static_cast<T *>(Y);
+    uint8_t *q = static_cast<uint8_t *>(Q);
     KernelTimer timer("rmsnorm_forward", s);
-    auto go = [&](auto kernel) {
-        kernel<<<grid, L.threads, 0, s>>>(static_cast<const T *>(X), static_cast<const T *>(R), w, rows, h, eps,
-                                          static_cast<T *>(S), static_cast<T *>(Y), static_cast<uint8_t *>(Q), Qs,
-                                          rstd);
-    };
-    if (warp) {
-        if (L.vpt == 1) go(rmsnorm_forward_kernel<T, 1, true>);
-        else if (L.vpt == 2) go(rmsnorm_forward_kernel<T, 2, true>);
-        else go(rmsnorm_forward_kernel<T, 4, true>);
-    } else {
-        if (L.vpt == 1) go(rmsnorm_forward_kernel<T, 1, false>);
-        else if (L.vpt == 2) go(rmsnorm_forward_kernel<T, 2, false>);
-        else go(rmsnorm_forward_kernel<T, 4, false>);
+    if (warp_rows(h)) {
+        const unsigned grid = static_cast<unsigned>(
+            std::min<int64_t>((rows + kWarps - 1) / kWarps, static_cast<int64_t>(num_sms()) * L.blocks));
+        auto go = [&](auto kernel) {
+            kernel<<<grid, L.threads, 0, s>>>(x, r, w, rows, h, eps, so, yo, q, Qs, rstd);
+        };
+        go(rmsnorm_forward_warp_kernel<T>);
+        return check_launch("rmsnorm_forward", s);
     }
+    const int64_t stage_bytes = static_cast<int64_t>(h) * sizeof(T) * (R ? 2 : 1);
+    const int stages = stages_of(stage_bytes, L.blocks);
+    const int64_t fit = static_cast<int64_t>(num_sms()) * L.blocks;
+    // whole rounds of blocks with six rows each or more: an SM that gets its bytes sooner takes more blocks
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(rows, std::max<int64_t>(1, rows / (kRowsOfBlock * fit)) * fit));
+    // with one row a block there is nothing to fetch ahead
+    const bool ring = stages > 0 && rows > fit;
+    const int smem = ring ? static_cast<int>(stage_bytes * stages) : 0;
+    auto go = [&](auto k) -> cudaError_t {
+        const cudaError_t e = decltype(k)::allow(smem);
+        if (e == cudaSuccess)
+            decltype(k)::fn<<<grid, L.threads, smem, s>>>(x, r, w, rows, h, eps, so, yo, q, Qs, rstd, stages,
+                                                          device_error_word());
+        return e;
+    };
+    cudaError_t e;
+    if (L.vpt == 1)
+        e = ring ? go(Fn<rmsnorm_forward_block_kernel<T, 1, true>>{}) : go(Fn<rmsnorm_forward_block_kernel<T, 1, false>>{});
+    else
+        e = ring ? go(Fn<rmsnorm_forward_block_kernel<T, 2, true>>{}) : go(Fn<rmsnorm_forward_block_kernel<T, 2, false>>{});
+    if (e != cudaSuccess) return fail_cuda(e, "rmsnorm_forward");
     return check_launch("rmsnorm_forward", s);
 }
 
 template <typename T>
 tpce_status backward(const void *dY, const void *S, const float *w, const float *rstd, const void *dS, int64_t rows,
                      int h, void *dX, float *dw, float *part, cudaStream_t s) {
-    const Launch L = launch_of(h);
-    const unsigned grid = static_cast<unsigned>(backward_blocks(rows, h));
+    Layout L = layout_of(h, true);
+    const T *y = static_cast<const T *>(dY), *x = static_cast<const T *>(S), *d = static_cast<const T *>(dS);
+    T *out = static_cast<T *>(dX);
+    if (!dw) part = nullptr;
+    int64_t blocks = backward_blocks(rows, h);
     {
         KernelTimer timer("rmsnorm_backward", s);
-        auto go = [&](auto kernel) {
-            kernel<<<grid, L.threads, 0, s>>>(static_cast<const T *>(dY), static_cast<const T *>(S), w, rstd,
-                                              static_cast<const T *>(dS), rows, h, static_cast<T *>(dX),
-                                              dw ? part : nullptr);
-        };
         if (warp_rows(h)) {
-            if (L.vpt == 1) go(rmsnorm_backward_kernel<T, 1, true>);
-            else if (L.vpt == 2) go(rmsnorm_backward_kernel<T, 2, true>);
-            else go(rmsnorm_backward_kernel<T, 4, true>);
+            auto go = [&](auto kernel) {
+                kernel<<<static_cast<unsigned>(blocks), L.threads, 0, s>>>(y, x, w, rstd, d, rows, h, out, part);
+            };
+            go(rmsnorm_backward_warp_kernel<T>);
         } else {
-            if (L.vpt == 1) go(rmsnorm_backward_kernel<T, 1, false>);
-            else if (L.vpt == 2) go(rmsnorm_backward_kernel<T, 2, false>);
-            else go(rmsnorm_backward_kernel<T, 4, false>);
+            const int64_t stage_bytes = static_cast<int64_t>(h) * sizeof(T) * (dS ? 3 : 2);
+            const int stages = stages_of(stage_bytes, L.blocks);
+            blocks = std::min<int64_t>(blocks, L.blocks * kSms);
+            const bool ring = stages > 0 && rows > blocks;
+            const int smem = ring ? static_cast<int>(stage_bytes * stages) : 0;
+            auto go = [&](auto k) -> cudaError_t {
+                const cudaError_t e = decltype(k)::allow(smem);
+                if (e == cudaSuccess)
+                    decltype(k)::fn<<<static_cast<unsigned>(blocks), L.threads, smem, s>>>(
+                        y, x, w, rstd, d, rows, h, out, part, stages, device_error_word());
+                return e;
+            };
+            cudaError_t e;
+            if (L.vpt == 1)
+                e = ring ? go(Fn<rmsnorm_backward_block_kernel<T, 1, true>>{})
+                         : go(Fn<rmsnorm_backward_block_kernel<T, 1, false>>{});
+            else
+                e = ring ? go(Fn<rmsnorm_backward_block_kernel<T, 4, true>>{})
+                         : go(Fn<rmsnorm_backward_block_kernel<T, 4, false>>{});
+            if (e != cudaSuccess) return fail_cuda(e, "rmsnorm_backward");
         }
         tpce_status st = check_launch("rmsnorm_backward", s);
         if (st != TPCE_OK) return st;
     }
     if (!dw) return TPCE_OK;
     KernelTimer timer("rmsnorm_dw", s);
-    rmsnorm_dw_kernel<<<(h + 31) / 32, 256, 0, s>>>(part, static_cast<int>(grid), h, dw);
+    rmsnorm_dw_kernel<<<(h + 31) / 32, 1024, 0, s>>>(part, static_cast<int>(blocks), h, dw);
     return check_launch("rmsnorm_dw", s);
 }
 

@@ -75,6 +75,62 @@ __device__ __forceinline__ void store8(float *p, const Raw8<float> &r) {
     q[1] = r.b;
 }
 
+// The same for values that nothing reads again soon: first to leave L2.
+__device__ __forceinline__ void stream8(__nv_bfloat16 *p, const Raw8<__nv_bfloat16> &r) {
+    __stcs(reinterpret_cast<uint4 *>(p), r.a);
+}
+__device__ __forceinline__ void stream8(float *p, const Raw8<float> &r) {
+    float4 *q = reinterpret_cast<float4 *>(p);
+    __stcs(q, r.a);
+    __stcs(q + 1, r.b);
+}
+
+// The compiler may not carry values made from r over this point: it makes them
+// again from r, which takes fewer registers.
+__device__ __forceinline__ void forget(Raw8<__nv_bfloat16> &r) {
+    asm volatile("" : "+r"(r.a.x), "+r"(r.a.y), "+r"(r.a.z), "+r"(r.a.w));
+}
+__device__ __forceinline__ void forget(Raw8<float> &r) {
+    asm volatile("" : "+f"(r.a.x), "+f"(r.a.y), "+f"(r.a.z), "+f"(r.a.w), "+f"(r.b.x), "+f"(r.b.y), "+f"(r.b.z),
+                 "+f"(r.b.w));
+}
+
+// (x, y) *= (a, b) and (x, y) += (a, b) * (c, d), two values an instruction; each
+// is rounded as by the single form.
+__device__ __forceinline__ void mul2(float &x, float &y, float a, float b) {
+    asm("{\n\t.reg .b64 p, q;\n\t"
+        "mov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
+        "mul.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(a), "f"(b));
+}
+__device__ __forceinline__ void fma2(float &x, float &y, float a, float b, float c, float d) {
+    asm("{\n\t.reg .b64 p, q, r;\n\t"
+        "mov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tmov.b64 r, {%4, %5};\n\t"
+        "fma.rn.f32x2 p, q, r, p;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+}
+
+// a + b, rounded once to the stored type. A bf16 sum rounded from fp32 would be
+// the same: 24 bits are more than twice 8 and two, so rounding twice never differs.
+__device__ __forceinline__ void add8(const Raw8<__nv_bfloat16> &a, const Raw8<__nv_bfloat16> &b,
+                                     Raw8<__nv_bfloat16> &r) {
+    const uint32_t x[4] = {a.a.x, a.a.y, a.a.z, a.a.w}, y[4] = {b.a.x, b.a.y, b.a.z, b.a.w};
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __hadd2(*reinterpret_cast<const __nv_bfloat162 *>(&x[i]),
+                                         *reinterpret_cast<const __nv_bfloat162 *>(&y[i]));
+        w[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    r.a = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void add8(const Raw8<float> &a, const Raw8<float> &b, Raw8<float> &r) {
+    r.a = make_float4(a.a.x + b.a.x, a.a.y + b.a.y, a.a.z + b.a.z, a.a.w + b.a.w);
+    r.b = make_float4(a.b.x + b.b.x, a.b.y + b.b.y, a.b.z + b.b.z, a.b.w + b.b.w);
+}
+
 __device__ __forceinline__ void load8f(const float *p, float (&v)[8]) {
     const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
@@ -91,30 +147,41 @@ constexpr float kE4m3Max = 448.0f;
 
 __device__ __forceinline__ float group_scale(float amax) { return fmaxf(__fmul_rn(amax, 1.0f / kE4m3Max), FLT_MIN); }
 
-__device__ __forceinline__ float finite_abs(float x) {
-    const float a = fabsf(x);
-    return a <= FLT_MAX ? a : 0.0f;
-}
-
-// amax over the 16 lanes that hold a group's 128 values, eight each
-__device__ __forceinline__ float group_amax(const float (&v)[8]) {
+// Codes and scale of a group whose 128 values lie in 16 adjacent lanes, eight
+// each; every lane of the warp calls it (values past an end: zeros). fmaxf
+// passes over NaN, whose product and code are NaN by themselves; infinities,
+// which would spoil the scale and saturate, are looked for only in a warp
+// whose maximum shows one.
+__device__ __forceinline__ uint2 quantize8(const float (&v)[8], float &scale) {
     float a = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a = fmaxf(a, finite_abs(v[i]));
+    for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(v[i]));
 #pragma unroll
     for (int d = 8; d > 0; d >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
-    return a;
-}
-
-__device__ __forceinline__ uint2 encode8(const float (&v)[8], float inv_scale) {
+    const bool infinite = __any_sync(0xffffffffu, a > FLT_MAX);
+    if (infinite) {
+        a = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(v[i]) <= FLT_MAX ? fabsf(v[i]) : 0.0f);
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
+    }
+    scale = group_scale(a);
+    const float inv = __frcp_rn(scale);
+    float t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = v[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mul2(t[2 * i], t[2 * i + 1], inv, inv);
+    if (infinite) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (!(fabsf(v[i]) <= FLT_MAX)) t[i] = __int_as_float(0x7fffffff);
+    }
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float2 t;
-        t.x = fabsf(v[2 * i]) <= FLT_MAX ? __fmul_rn(v[2 * i], inv_scale) : __int_as_float(0x7fffffff);
-        t.y = fabsf(v[2 * i + 1]) <= FLT_MAX ? __fmul_rn(v[2 * i + 1], inv_scale) : __int_as_float(0x7fffffff);
-        w[i] = __nv_cvt_float2_to_fp8x2(t, __NV_SATFINITE, __NV_E4M3);
-    }
+    for (int i = 0; i < 4; ++i)
+        w[i] = __nv_cvt_float2_to_fp8x2(make_float2(t[2 * i], t[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
     return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 

@@ -18,11 +18,25 @@ from typing import Dict, List, Optional, Sequence, Union
 
 import torch
 
-from ._lib import TPCE_BF16, TPCE_F32, AdamwTensor, check, lib
-from .api import _DT, _need, _ptr, _stream, _workspace, _wsize
+from ._lib import AdamwTensor, check, lib
+from .api import _DT, _need, _workspace, _wsize
 
 GROUP = 128  # values that share one scale in the 8-bit formats
 _E4M3 = torch.float8_e4m3fn
+
+
+# The smallest calls take a few microseconds on the GPU, so the host's part is kept short: the current stream's
+# handle without a Stream object around it, plain integers for pointers, and one test for a fitting tensor.
+def _current() -> int:
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+
+
+def _handle(stream) -> int:
+    return _current() if stream is None else stream.cuda_stream
+
+
+def _ptr(x: Optional[torch.Tensor]):
+    return None if x is None else x.data_ptr()
 
 
 class _On:
@@ -32,7 +46,7 @@ class _On:
 
     def __init__(self, stream, *tensors):
         self.ctx = None
-        if stream is not None and stream.cuda_stream != torch.cuda.current_stream().cuda_stream:
+        if stream is not None and stream.cuda_stream != _current():
             for x in tensors:
                 if x is not None:
                     x.record_stream(stream)
@@ -45,6 +59,12 @@ class _On:
     def __exit__(self, *exc):
         if self.ctx is not None:
             self.ctx.__exit__(*exc)
+
+
+def _fit(x: torch.Tensor, name: str, dtype, shape, dev: torch.device):
+    """x is a contiguous tensor of this type and shape on `dev` (checked to be the current device)."""
+    if x.dtype is not dtype or x.shape != shape or x.device != dev or not x.is_contiguous():
+        _need(x, name, dtype, shape)
 
 
 def _dtype(x: torch.Tensor, name: str) -> int:
@@ -64,7 +84,7 @@ def _out(out, key, shape, dtype, dev) -> torch.Tensor:
     x = out.get(key) if out else None
     if x is None:
         return torch.empty(shape, dtype=dtype, device=dev)
-    _need(x, key, dtype, shape)
+    _fit(x, key, dtype, shape, dev)
     return x
 
 
@@ -87,9 +107,9 @@ def tp_rmsnorm_forward(X: torch.Tensor, w: torch.Tensor, R: Optional[torch.Tenso
     dt, dev = X.dtype, X.device
     code = _dtype(X, "X")
     _need(X, "X")
-    _need(w, "w", torch.float32, (h,))
+    _fit(w, "w", torch.float32, (h,), dev)
     if R is not None:
-        _need(R, "R", dt, (T, h))
+        _fit(R, "R", dt, X.shape, dev)
     if not (want_Y or quantize):
         raise ValueError("tp_rmsnorm_forward: want_Y or quantize")
     res: Dict[str, torch.Tensor] = {}
@@ -103,7 +123,7 @@ def tp_rmsnorm_forward(X: torch.Tensor, w: torch.Tensor, R: Optional[torch.Tenso
             res["Q"] = _out(out, "Q", (T, h), _E4M3, dev)
             res["Q_scale"] = _out(out, "Q_scale", (T, -(-h // GROUP)), torch.float32, dev)
     st = lib().tp_rmsnorm_forward(_ptr(X), _ptr(R), _ptr(w), T, h, eps, code, _ptr(res.get("S")), _ptr(res.get("Y")),
-                                  _ptr(res.get("Q")), _ptr(res.get("Q_scale")), _ptr(res["rstd"]), _stream(stream))
+                                  _ptr(res.get("Q")), _ptr(res.get("Q_scale")), _ptr(res["rstd"]), _handle(stream))
     check(st, "tp_rmsnorm_forward")
     return res
 
@@ -118,11 +138,11 @@ def tp_rmsnorm_backward(dY: torch.Tensor, S: torch.Tensor, w: torch.Tensor, rstd
     dt, dev = S.dtype, S.device
     code = _dtype(S, "S")
     _need(S, "S")
-    _need(dY, "dY", dt, (T, h))
-    _need(w, "w", torch.float32, (h,))
-    _need(rstd, "rstd", torch.float32, (T,))
+    _fit(dY, "dY", dt, S.shape, dev)
+    _fit(w, "w", torch.float32, (h,), dev)
+    _fit(rstd, "rstd", torch.float32, (T,), dev)
     if dS is not None:
-        _need(dS, "dS", dt, (T, h))
+        _fit(dS, "dS", dt, S.shape, dev)
     with _On(stream, dY, S, w, rstd, dS, ws, *_given(out)):
         res = {"dX": _out(out, "dX", (T, h), dt, dev)}
         wk = None
@@ -130,7 +150,7 @@ def tp_rmsnorm_backward(dY: torch.Tensor, S: torch.Tensor, w: torch.Tensor, rstd
             res["dw"] = _out(out, "dw", (h,), torch.float32, dev)
             wk = _workspace(rmsnorm_workspace_bytes(T, h), dev, ws)
     st = lib().tp_rmsnorm_backward(_ptr(dY), _ptr(S), _ptr(w), _ptr(rstd), _ptr(dS), T, h, code, _ptr(res["dX"]),
-                                   _ptr(res.get("dw")), _ptr(wk), _wsize(wk), _stream(stream))
+                                   _ptr(res.get("dw")), _ptr(wk), _wsize(wk), _handle(stream))
     check(st, "tp_rmsnorm_backward")
     return res
 
@@ -150,7 +170,7 @@ def tp_expert_plan(ids: torch.Tensor, experts: int, out: Optional[Dict[str, torc
                "source": _out(out, "source", (T * k,), torch.int32, dev),
                "offsets": _out(out, "offsets", (experts + 1,), torch.int32, dev)}
     check(lib().tp_expert_plan(_ptr(ids), T, k, experts, _ptr(res["row"]), _ptr(res["source"]), _ptr(res["offsets"]),
-                               _stream(stream)), "tp_expert_plan")
+                               _handle(stream)), "tp_expert_plan")
     return res
 
 
@@ -158,9 +178,9 @@ def _plan(plan: Dict[str, torch.Tensor]):
     row, offsets = plan["row"], plan["offsets"]
     T, k = _matrix(row, "plan['row']")
     _need(row, "plan['row']", torch.int32)
-    _need(offsets, "plan['offsets']", torch.int32)
     if offsets.dim() != 1 or offsets.shape[0] < 2:
         raise ValueError("plan['offsets'] must hold experts + 1 values")
+    _fit(offsets, "plan['offsets']", torch.int32, offsets.shape, row.device)
     return row, offsets, T, k, offsets.shape[0] - 1
 
 
@@ -171,11 +191,11 @@ def tp_expert_dispatch_forward(X: torch.Tensor, plan: Dict[str, torch.Tensor], o
     row, offsets, T, k, E = _plan(plan)
     code = _dtype(X, "X")
     h = _matrix(X, "X")[1]
-    _need(X, "X", shape=(T, h))
+    _fit(X, "X", X.dtype, (T, h), row.device)
     with _On(stream, X, row, offsets, out):
         Xs = _out({"Xs": out}, "Xs", (T * k, h), X.dtype, X.device)
     check(lib().tp_expert_dispatch_forward(_ptr(X), _ptr(row), _ptr(offsets), T, h, k, E, code, _ptr(Xs),
-                                           _stream(stream)), "tp_expert_dispatch_forward")
+                                           _handle(stream)), "tp_expert_dispatch_forward")
     return Xs
 
 
@@ -185,10 +205,10 @@ def tp_expert_dispatch_backward(dXs: torch.Tensor, plan: Dict[str, torch.Tensor]
     row, _, T, k, _ = _plan(plan)
     code = _dtype(dXs, "dXs")
     h = _matrix(dXs, "dXs")[1]
-    _need(dXs, "dXs", shape=(T * k, h))
+    _fit(dXs, "dXs", dXs.dtype, (T * k, h), row.device)
     with _On(stream, dXs, row, out):
         dX = _out({"dX": out}, "dX", (T, h), dXs.dtype, dXs.device)
-    check(lib().tp_expert_dispatch_backward(_ptr(dXs), _ptr(row), T, h, k, code, _ptr(dX), _stream(stream)),
+    check(lib().tp_expert_dispatch_backward(_ptr(dXs), _ptr(row), T, h, k, code, _ptr(dX), _handle(stream)),
           "tp_expert_dispatch_backward")
     return dX
 
@@ -199,12 +219,12 @@ def tp_expert_combine_forward(Ys: torch.Tensor, plan: Dict[str, torch.Tensor], w
     row, _, T, k, _ = _plan(plan)
     code = _dtype(Ys, "Ys")
     h = _matrix(Ys, "Ys")[1]
-    _need(Ys, "Ys", shape=(T * k, h))
-    _need(weights, "weights", torch.float32, (T, k))
+    _fit(Ys, "Ys", Ys.dtype, (T * k, h), row.device)
+    _fit(weights, "weights", torch.float32, row.shape, row.device)
     with _On(stream, Ys, row, weights, out):
         Z = _out({"Z": out}, "Z", (T, h), Ys.dtype, Ys.device)
     check(lib().tp_expert_combine_forward(_ptr(Ys), _ptr(row), _ptr(weights), T, h, k, code, _ptr(Z),
-                                          _stream(stream)), "tp_expert_combine_forward")
+                                          _handle(stream)), "tp_expert_combine_forward")
     return Z
 
 
@@ -215,14 +235,14 @@ def tp_expert_combine_backward(dZ: torch.Tensor, Ys: torch.Tensor, plan: Dict[st
     row, offsets, T, k, E = _plan(plan)
     code = _dtype(dZ, "dZ")
     h = _matrix(dZ, "dZ")[1]
-    _need(dZ, "dZ", shape=(T, h))
-    _need(Ys, "Ys", dZ.dtype, (T * k, h))
-    _need(weights, "weights", torch.float32, (T, k))
+    _fit(dZ, "dZ", dZ.dtype, (T, h), row.device)
+    _fit(Ys, "Ys", dZ.dtype, (T * k, h), row.device)
+    _fit(weights, "weights", torch.float32, row.shape, row.device)
     with _On(stream, dZ, Ys, row, offsets, weights, *_given(out)):
         res = {"dYs": _out(out, "dYs", (T * k, h), dZ.dtype, dZ.device),
                "dweights": _out(out, "dweights", (T, k), torch.float32, dZ.device)}
     check(lib().tp_expert_combine_backward(_ptr(dZ), _ptr(Ys), _ptr(row), _ptr(offsets), _ptr(weights), T, h, k, E,
-                                           code, _ptr(res["dYs"]), _ptr(res["dweights"]), _stream(stream)),
+                                           code, _ptr(res["dYs"]), _ptr(res["dweights"]), _handle(stream)),
           "tp_expert_combine_backward")
     return res
 
@@ -257,8 +277,19 @@ def adamw_scalars(lr: float, step: int, beta1: float = 0.9, beta2: float = 0.999
                         dtype=torch.float32)
 
 
-_ENTRY = struct.Struct("=7QqdiiiI")
-assert _ENTRY.size == ctypes.sizeof(AdamwTensor)
+_FIELDS = "7QqdiiiI"  # tpce_adamw_tensor
+assert struct.calcsize("=" + _FIELDS) == ctypes.sizeof(AdamwTensor)
+
+
+def _pointers(name: str, xs: Sequence[torch.Tensor], dtype, shapes, dev) -> List[int]:
+    """The addresses of contiguous tensors of these shapes on device `dev`; dtype None: bf16 or fp32."""
+    for i, x in enumerate(xs):
+        if ((x.dtype is not dtype if dtype is not None else x.dtype not in _DT) or x.shape != shapes[i]
+                or x.get_device() != dev or not x.is_contiguous()):
+            if dtype is None:
+                _dtype(x, f"{name}[{i}]")
+            _need(x, f"{name}[{i}]", dtype, shapes[i])
+    return list(map(torch.Tensor.data_ptr, xs))
 
 
 def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
@@ -281,43 +312,48 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
     if scalars is not None:
         _need(scalars, "scalars", torch.float32, (4,))
     dev = torch.cuda.current_device() if torch.cuda.is_available() else None
-    f32, bf16 = torch.float32, torch.bfloat16
-    buf = bytearray(_ENTRY.size * n)
-    seen = set()
-    used: List[torch.Tensor] = []
-
-    def ptr(what, i, x, dtype, shape):
-        if x.dtype is not dtype or x.shape != shape or not x.is_contiguous() or x.get_device() != dev:
-            _need(x, f"{what}[{i}]", dtype, shape)  # names the reason
-        return x.data_ptr()
-
-    for i in range(n):
-        p, g, st, master = params[i], grads[i], states[i], masters[i]
-        shape = p.shape
-        if p.dtype is not f32 and p.dtype is not bf16 or g.dtype is not f32 and g.dtype is not bf16:
-            raise ValueError(f"params[{i}] and grads[{i}] must be torch.bfloat16 or torch.float32, got {p.dtype} and "
-                             f"{g.dtype}")
-        if master is not None and p.dtype is f32:
+    f32 = torch.float32
+    held = [i for i, x in enumerate(masters) if x is not None]
+    for i in held:
+        if params[i].dtype is f32:
             raise ValueError(f"masters[{i}]: params[{i}] is fp32 already")
-        pp, gp = ptr("params", i, p, p.dtype, shape), ptr("grads", i, g, g.dtype, shape)
-        mp = 0 if master is None else ptr("masters", i, master, f32, shape)
-        if "m" in st:
-            bits, a, b, sa, sb = 32, ptr("m", i, st["m"], f32, shape), ptr("v", i, st["v"], f32, shape), 0, 0
+    shapes = [p.shape for p in params]
+    sizes = [p.numel() for p in params]
+    row = [0] * (13 * n)  # the fields of tensor i from 13 i on
+    row[0::13] = pp = _pointers("params", params, None, shapes, dev)
+    row[2::13] = _pointers("grads", grads, None, shapes, dev)
+    row[7::13], row[8::13] = sizes, decay
+    row[9::13], row[10::13] = [_DT[p.dtype] for p in params], [_DT[g.dtype] for g in grads]
+    if held:
+        for i, a in zip(held, _pointers("masters", [masters[i] for i in held], f32, [shapes[i] for i in held], dev)):
+            row[13 * i + 1] = a
+    # the two kinds of states, each with its places in the list
+    for bits in (32, 8):
+        at = [i for i, st in enumerate(states) if ("m" in st) == (bits == 32)]
+        if not at:
+            continue
+        full = shapes if len(at) == n else [shapes[i] for i in at]
+        few = [(-(-sizes[i] // GROUP),) for i in at]
+        parts = (("m", f32, full, 3), ("v", f32, full, 4)) if bits == 32 else (
+            ("m_q", _E4M3, full, 3), ("r_q", _E4M3, full, 4), ("m_scale", f32, few, 5), ("r_scale", f32, few, 6))
+        for key, dtype, sh, field in parts:
+            got = _pointers(key, [states[i][key] for i in at], dtype, sh, dev)
+            if len(at) == n:
+                row[field::13] = got
+            else:
+                for i, a in zip(at, got):
+                    row[13 * i + field] = a
+        if len(at) == n:
+            row[11::13] = [bits] * n
         else:
-            groups = (-(-p.numel() // GROUP),)
-            bits = 8
-            a, b = ptr("m_q", i, st["m_q"], _E4M3, shape), ptr("r_q", i, st["r_q"], _E4M3, shape)
-            sa, sb = ptr("m_scale", i, st["m_scale"], f32, groups), ptr("r_scale", i, st["r_scale"], f32, groups)
-        if pp:
-            if pp in seen:
-                raise ValueError(f"params[{i}] is in the list twice")
-            seen.add(pp)
-        _ENTRY.pack_into(buf, i * _ENTRY.size, pp, mp, gp, a, b, sa, sb, p.numel(), decay[i],
-                         TPCE_BF16 if p.dtype is bf16 else TPCE_F32, TPCE_BF16 if g.dtype is bf16 else TPCE_F32, bits,
-                         0)
-        if stream is not None:
-            used += [p, g, *st.values()] + ([] if master is None else [master])
-    _On(stream, scalars, *used)
+            for i in at:
+                row[13 * i + 11] = bits
+    if len(set(pp)) != n and len({a for a in pp if a}) != sum(1 for a in pp if a):
+        raise ValueError("params: a tensor is in the list twice")
+    if stream is not None:
+        _On(stream, scalars, *params, *grads, *masters, *(x for st in states for x in st.values()))
+    buf = bytearray(ctypes.sizeof(AdamwTensor) * n)
+    struct.pack_into("=" + _FIELDS * n, buf, 0, *row)
     tensors = (AdamwTensor * n).from_buffer(buf) if n else None
-    check(lib().tp_adamw_step(tensors, n, lr, beta1, beta2, eps, step, grad_scale, _ptr(scalars), _stream(stream)),
+    check(lib().tp_adamw_step(tensors, n, lr, beta1, beta2, eps, step, grad_scale, _ptr(scalars), _handle(stream)),
           "tp_adamw_step")
