@@ -1,7 +1,9 @@
 """Build libtpce.so in-tree with nvcc for sm_103a.
 
 Translation units are compiled in parallel, then linked into
-``vocab_ce_gb300/lib/libtpce.so``. Run ``python -m vocab_ce_gb300.build``.
+``vocab_ce_gb300/lib/libtpce.so``; beside it the host binding of the
+training-step calls, ``_step_binding.so`` (g++ and torch's headers). Run
+``python -m vocab_ce_gb300.build``.
 """
 
 from __future__ import annotations
@@ -10,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -22,6 +25,8 @@ LIB_PATH = os.path.join(LIB_DIR, "libtpce.so")
 
 SOURCES = ["runtime.cu", "mlp.cu", "linear.cu", "ce.cu", "ce_static.cu", "step/norm.cu", "step/experts.cu",
            "step/adamw.cu"]
+BINDING_SOURCE = os.path.join(CSRC, "step", "binding.cpp")
+BINDING_PATH = os.path.join(LIB_DIR, "_step_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                      "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]
@@ -39,13 +44,33 @@ def _deps_mtime() -> float:
     return max(os.path.getmtime(f) for f in files)
 
 
+def _build_binding() -> subprocess.CompletedProcess:
+    import torch
+
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    lib = os.path.join(home, "lib")
+    tmp = BINDING_PATH + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE]
+    for d in (os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+              os.path.join(cuda, "include"), sysconfig.get_paths()["include"]):
+        cmd += ["-isystem", d]
+    cmd += [BINDING_SOURCE, "-o", tmp, "-L", lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+            f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode == 0:
+        os.replace(tmp, BINDING_PATH)
+    return r
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=None, out_path: str = None,
           build_dir: str = None) -> str:
     """Compile and link libtpce.so (default: in-tree). extra_flags are added to
     every nvcc compile (e.g. -DTPCE_EPI_WARPS=8 tuning knobs)."""
     lib_path = out_path or LIB_PATH
     bdir = build_dir or BUILD_DIR
-    if not force and os.path.exists(lib_path) and os.path.getmtime(lib_path) >= _deps_mtime():
+    made = [lib_path] if out_path else [lib_path, BINDING_PATH]
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime() for f in made):
         return lib_path
     os.makedirs(bdir, exist_ok=True)
     os.makedirs(os.path.dirname(lib_path), exist_ok=True)
@@ -58,8 +83,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None, out_path
         r = subprocess.run(cmd, capture_output=True, text=True)
         return src, obj, r
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = None if out_path else ex.submit(_build_binding)
         results = list(ex.map(compile_one, SOURCES))
+    if binding is not None and binding.result().returncode != 0:
+        raise RuntimeError("g++ failed on step/binding.cpp:\n" + binding.result().stderr)
     for src, _, r in results:
         if verbose and (r.stdout or r.stderr):
             sys.stderr.write(r.stdout + r.stderr)
