@@ -58,8 +58,8 @@ struct Entry {
 static_assert(sizeof(Entry) == 88, "the table's size is what a launch's parameters hold");
 
 // Parameters of a launch: up to 4 KB for a short list, up to 32,764 bytes for a
-// long one (more take more launches).
-constexpr int kShort = 44, kLong = 368;
+// long one (more take more launches); what is not used is copied all the same.
+constexpr int kShort = 44, kMiddle = 136, kLong = 368;
 template <int N>
 struct Table {
     Entry t[N];
@@ -329,8 +329,9 @@ extern "C" tpce_status tp_adamw_step(const tpce_adamw_tensor *tensors, int count
     uint32_t blocks = 0;
     auto flush = [&]() -> tpce_status {
         if (!held) return TPCE_OK;
-        tpce_status st = held <= kShort ? launch<kShort>(entries, held, blocks, k, s)
-                                        : launch<kLong>(entries, held, blocks, k, s);
+        tpce_status st = held <= kShort    ? launch<kShort>(entries, held, blocks, k, s)
+                         : held <= kMiddle ? launch<kMiddle>(entries, held, blocks, k, s)
+                                           : launch<kLong>(entries, held, blocks, k, s);
         held = 0;
         blocks = 0;
         return st;

@@ -96,13 +96,16 @@ void need(const at::Tensor &x, const std::string &name, const at::ScalarType *dt
         throw Refused{name + " must have shape " + shape_text(*shape) + ", got " + shape_text(x.sizes())};
 }
 void need(const at::Tensor &x, const char *name, at::ScalarType dtype, at::IntArrayRef shape) {
+    if (x.scalar_type() == dtype && x.is_cuda() && x.sizes() == shape && x.is_contiguous() &&
+        x.device().index() == c10::cuda::current_device())
+        return;
     need(x, std::string(name), &dtype, &shape);
 }
 
-int rows_type(const at::Tensor &x, const std::string &name) {
+int rows_type(const at::Tensor &x, const char *name, Py_ssize_t i = -1) {
     if (x.scalar_type() == at::kBFloat16) return TPCE_BF16;
     if (x.scalar_type() == at::kFloat) return TPCE_F32;
-    throw Refused{name + " must be torch.bfloat16 or torch.float32, got " + dtype_name(x.scalar_type())};
+    throw Refused{name + (i < 0 ? std::string() : "[" + std::to_string(i) + "]") + " must be torch.bfloat16 or torch.float32, got " + dtype_name(x.scalar_type())};
 }
 
 // rows x columns of bf16 or fp32; returns the library's dtype
@@ -131,19 +134,32 @@ at::Tensor output(PyObject *given, const char *name, at::IntArrayRef shape, at::
     need(x, name, dtype, shape);
     return x;
 }
-PyObject *entry(PyObject *out, const char *name) {  // borrowed; NULL where there is none
+// A dict's entry, borrowed; NULL where there is none. Keys are interned once.
+struct Key {
+    const char *name;
+    PyObject *o;
+    explicit Key(const char *n) : name(n), o(PyUnicode_InternFromString(n)) {}
+    PyObject *of(PyObject *dict) const { return PyDict_GetItemWithError(dict, o); }
+};
+PyObject *entry(PyObject *out, const Key &key) {
     if (none(out)) return nullptr;
     if (!PyDict_Check(out)) throw Refused{"out must be a dict of tensors"};
-    return PyDict_GetItemString(out, name);
+    return key.of(out);
 }
+
+// Made at the module's start, with the interpreter there.
+struct Keys {
+    Key S{"S"}, Y{"Y"}, rstd{"rstd"}, Q{"Q"}, Q_scale{"Q_scale"}, dX{"dX"}, dw{"dw"}, row{"row"}, source{"source"}, offsets{"offsets"}, dYs{"dYs"}, dweights{"dweights"}, m{"m"}, v{"v"}, m_q{"m_q"}, r_q{"r_q"}, m_scale{"m_scale"}, r_scale{"r_scale"};
+};
+const Keys *keys;
 
 // A dict of the results, which takes over what it is given.
 struct Results {
     PyObject *d = PyDict_New();
     ~Results() { Py_XDECREF(d); }
-    void add(const char *name, const at::Tensor &x) {
+    void add(const Key &key, const at::Tensor &x) {
         PyObject *o = THPVariable_Wrap(x);
-        const int bad = o ? PyDict_SetItemString(d, name, o) : -1;
+        const int bad = o ? PyDict_SetItem(d, key.o, o) : -1;
         Py_XDECREF(o);
         if (bad) throw Raised{};
     }
@@ -182,13 +198,13 @@ PyObject *rmsnorm_forward(PyObject *const *a) {
     }
     if (!want_Y && !quantize) throw Refused{"tp_rmsnorm_forward: want_Y or quantize"};
     Results res;
-    if (residual) res.add("S", S = output(entry(a[6], "S"), "S", X.sizes(), X.scalar_type(), X));
-    if (want_Y) res.add("Y", Y = output(entry(a[6], "Y"), "Y", X.sizes(), X.scalar_type(), X));
-    const at::Tensor rstd = output(entry(a[6], "rstd"), "rstd", {T}, at::kFloat, X);
-    res.add("rstd", rstd);
+    if (residual) res.add(keys->S, S = output(entry(a[6], keys->S), "S", X.sizes(), X.scalar_type(), X));
+    if (want_Y) res.add(keys->Y, Y = output(entry(a[6], keys->Y), "Y", X.sizes(), X.scalar_type(), X));
+    const at::Tensor rstd = output(entry(a[6], keys->rstd), "rstd", {T}, at::kFloat, X);
+    res.add(keys->rstd, rstd);
     if (quantize) {
-        res.add("Q", Q = output(entry(a[6], "Q"), "Q", X.sizes(), at::kFloat8_e4m3fn, X));
-        res.add("Q_scale", Qs = output(entry(a[6], "Q_scale"), "Q_scale", {T, (h + kGroup - 1) / kGroup}, at::kFloat, X));
+        res.add(keys->Q, Q = output(entry(a[6], keys->Q), "Q", X.sizes(), at::kFloat8_e4m3fn, X));
+        res.add(keys->Q_scale, Qs = output(entry(a[6], keys->Q_scale), "Q_scale", {T, (h + kGroup - 1) / kGroup}, at::kFloat, X));
     }
     raise_on(api.rmsnorm_forward(ptr(X), ptr(R), fptr(w), T, h, static_cast<float>(eps), dt, ptr(S), ptr(Y), ptr(Q),
                                  fptr(Qs), fptr(rstd), stream()),
@@ -211,11 +227,11 @@ PyObject *rmsnorm_backward(PyObject *const *a) {
         need(dS, "dS", S.scalar_type(), S.sizes());
     }
     Results res;
-    const at::Tensor dX = output(entry(a[6], "dX"), "dX", S.sizes(), S.scalar_type(), S);
-    res.add("dX", dX);
+    const at::Tensor dX = output(entry(a[6], keys->dX), "dX", S.sizes(), S.scalar_type(), S);
+    res.add(keys->dX, dX);
     size_t bytes = 0;
     if (truth(a[5])) {
-        res.add("dw", dw = output(entry(a[6], "dw"), "dw", {h}, at::kFloat, S));
+        res.add(keys->dw, dw = output(entry(a[6], keys->dw), "dw", {h}, at::kFloat, S));
         bytes = api.rmsnorm_workspace_bytes(T, h);
         if (!none(a[7])) {
             ws = tensor(a[7], "ws");
@@ -239,12 +255,12 @@ PyObject *expert_plan(PyObject *const *a) {
     const int64_t T = ids.size(0), k = ids.size(1), E = integer(a[1]);
     if (E < 1 || E >= (1 << 30)) throw Refused{"experts must be at least 1"};
     Results res;
-    const at::Tensor row = output(entry(a[2], "row"), "row", ids.sizes(), at::kInt, ids);
-    res.add("row", row);
-    const at::Tensor source = output(entry(a[2], "source"), "source", {T * k}, at::kInt, ids);
-    res.add("source", source);
-    const at::Tensor offsets = output(entry(a[2], "offsets"), "offsets", {E + 1}, at::kInt, ids);
-    res.add("offsets", offsets);
+    const at::Tensor row = output(entry(a[2], keys->row), "row", ids.sizes(), at::kInt, ids);
+    res.add(keys->row, row);
+    const at::Tensor source = output(entry(a[2], keys->source), "source", {T * k}, at::kInt, ids);
+    res.add(keys->source, source);
+    const at::Tensor offsets = output(entry(a[2], keys->offsets), "offsets", {E + 1}, at::kInt, ids);
+    res.add(keys->offsets, offsets);
     raise_on(api.expert_plan(iptr(ids), T, static_cast<int>(std::min<int64_t>(k, 1 << 30)), static_cast<int>(E),
                              iptr(row), iptr(source), iptr(offsets), stream()),
              "tp_expert_plan");
@@ -257,7 +273,7 @@ struct Plan {
     int k, E;
     explicit Plan(PyObject *o) {
         if (!PyDict_Check(o)) throw Refused{"plan must be tp_expert_plan's dict"};
-        PyObject *r = PyDict_GetItemString(o, "row"), *f = PyDict_GetItemString(o, "offsets");
+        PyObject *r = keys->row.of(o), *f = keys->offsets.of(o);
         if (!r || !f) throw Refused{"plan must hold 'row' and 'offsets'"};
         row = tensor(r, "plan['row']");
         offsets = tensor(f, "plan['offsets']");
@@ -321,10 +337,10 @@ PyObject *expert_combine_backward(PyObject *const *a) {
     need(Ys, "Ys", dZ.scalar_type(), {p.row.numel(), h});
     need(weights, "weights", at::kFloat, p.row.sizes());
     Results res;
-    const at::Tensor dYs = output(entry(a[4], "dYs"), "dYs", Ys.sizes(), dZ.scalar_type(), dZ);
-    res.add("dYs", dYs);
-    const at::Tensor dw = output(entry(a[4], "dweights"), "dweights", p.row.sizes(), at::kFloat, dZ);
-    res.add("dweights", dw);
+    const at::Tensor dYs = output(entry(a[4], keys->dYs), "dYs", Ys.sizes(), dZ.scalar_type(), dZ);
+    res.add(keys->dYs, dYs);
+    const at::Tensor dw = output(entry(a[4], keys->dweights), "dweights", p.row.sizes(), at::kFloat, dZ);
+    res.add(keys->dweights, dw);
     raise_on(api.expert_combine_backward(ptr(dZ), ptr(Ys), iptr(p.row), iptr(p.offsets), fptr(weights), p.T, h, p.k,
                                          p.E, dt, ptr(dYs), fptr(dw), stream()),
              "tp_expert_combine_backward");
@@ -365,46 +381,48 @@ PyObject *adamw_step(PyObject *const *a) {
 
     std::vector<tpce_adamw_tensor> t(static_cast<size_t>(n));
     std::unordered_set<void *> seen;
-    // name[i], only put together when it is needed
+    const int dev = n && THPVariable_Check(params[0]) && THPVariable_Unpack(params[0]).is_cuda()
+                        ? c10::cuda::current_device() : -1;
+    // names are put together only for a message
+    auto place = [](const char *name, Py_ssize_t i) { return std::string(name) + "[" + std::to_string(i) + "]"; };
     auto take = [&](PyObject *o, const char *name, Py_ssize_t i, at::ScalarType dtype, at::IntArrayRef shape) {
-        if (!o || !THPVariable_Check(o)) throw Refused{std::string(name) + "[" + std::to_string(i) + "] must be a tensor"};
+        if (!o || !THPVariable_Check(o)) throw Refused{place(name, i) + " must be a tensor"};
         const at::Tensor &x = THPVariable_Unpack(o);
-        if (!x.is_cuda() || x.scalar_type() != dtype || x.sizes() != shape || !x.is_contiguous() ||
-            x.device().index() != c10::cuda::current_device())
-            need(x, std::string(name) + "[" + std::to_string(i) + "]", &dtype, &shape);
+        if (x.scalar_type() != dtype || x.get_device() != dev || x.sizes() != shape || !x.is_contiguous() || dev < 0)
+            need(x, place(name, i), &dtype, &shape);
         return x.data_ptr();
     };
     for (Py_ssize_t i = 0; i < n; ++i) {
         tpce_adamw_tensor &e = t[static_cast<size_t>(i)];
-        const std::string at_i = "[" + std::to_string(i) + "]";
         const at::Tensor &p = tensor(params[i], "params"), &g = tensor(grads[i], "grads");
         const at::IntArrayRef shape = p.sizes();
-        e.p_dtype = rows_type(p, "params" + at_i);
-        e.g_dtype = rows_type(g, "grads" + at_i);
+        e.p_dtype = rows_type(p, "params", i);
+        e.g_dtype = rows_type(g, "grads", i);
         PyObject *master = none(a[3]) ? Py_None : masters[i];
-        if (!none(master) && e.p_dtype == TPCE_F32) throw Refused{"masters" + at_i + ": params" + at_i + " is fp32 already"};
+        if (!none(master) && e.p_dtype == TPCE_F32) 
+            throw Refused{place("masters", i) + ": " + place("params", i) + " is fp32 already"};
         e.p = take(params[i], "params", i, p.scalar_type(), shape);
         e.g = take(grads[i], "grads", i, g.scalar_type(), shape);
         e.master = none(master) ? nullptr : take(master, "masters", i, at::kFloat, shape);
         PyObject *st = states[i];
-        if (!PyDict_Check(st)) throw Refused{"states" + at_i + " must be a dict (adamw_state)"};
+        if (!PyDict_Check(st)) throw Refused{place("states", i) + " must be a dict (adamw_state)"};
         e.n = p.numel();
         e.reserved = 0;
-        if (PyObject *m = PyDict_GetItemString(st, "m")) {
+        if (PyObject *m = keys->m.of(st)) {
             e.state_bits = 32;
             e.m = take(m, "m", i, at::kFloat, shape);
-            e.v = take(PyDict_GetItemString(st, "v"), "v", i, at::kFloat, shape);
+            e.v = take(keys->v.of(st), "v", i, at::kFloat, shape);
             e.m_scale = e.v_scale = nullptr;
         } else {
             const int64_t few[1] = {(e.n + kGroup - 1) / kGroup};
             e.state_bits = 8;
-            e.m = take(PyDict_GetItemString(st, "m_q"), "m_q", i, at::kFloat8_e4m3fn, shape);
-            e.v = take(PyDict_GetItemString(st, "r_q"), "r_q", i, at::kFloat8_e4m3fn, shape);
-            e.m_scale = static_cast<float *>(take(PyDict_GetItemString(st, "m_scale"), "m_scale", i, at::kFloat, few));
-            e.v_scale = static_cast<float *>(take(PyDict_GetItemString(st, "r_scale"), "r_scale", i, at::kFloat, few));
+            e.m = take(keys->m_q.of(st), "m_q", i, at::kFloat8_e4m3fn, shape);
+            e.v = take(keys->r_q.of(st), "r_q", i, at::kFloat8_e4m3fn, shape);
+            e.m_scale = static_cast<float *>(take(keys->m_scale.of(st), "m_scale", i, at::kFloat, few));
+            e.v_scale = static_cast<float *>(take(keys->r_scale.of(st), "r_scale", i, at::kFloat, few));
         }
         e.weight_decay = one ? wd : number(decay[i]);
-        if (e.n && !seen.insert(e.p).second) throw Refused{"params" + at_i + " is in the list twice"};
+        if (e.n && !seen.insert(e.p).second) throw Refused{place("params", i) + " is in the list twice"};
     }
     const float *scalars = nullptr;
     if (!none(a[11])) {
@@ -475,4 +493,7 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_step_binding", nullptr, -1, metho
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__step_binding() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__step_binding() {
+    if (!keys) keys = new Keys;
+    return PyModule_Create(&module);
+}

@@ -46,6 +46,17 @@ __device__ __forceinline__ uint32_t read_cluster_u32(const uint32_t *p, uint32_t
     return v;
 }
 
+// The lanes whose value equals this lane's, from one ballot for each of its bits.
+__device__ __forceinline__ uint32_t same_value(int v, int bits) {
+    uint32_t same = 0xffffffffu;
+    for (int b = 0; b < bits; ++b) {
+        const bool one = (v >> b) & 1;
+        const uint32_t with = __ballot_sync(0xffffffffu, one);
+        same &= one ? with : ~with;
+    }
+    return same;
+}
+
 __global__ void __launch_bounds__(32 * kPlanWarps)
     expert_plan_kernel(const int32_t *__restrict__ ids, int64_t n, int E, int ctas, int32_t *row, int32_t *source,
                        int32_t *offsets, uint32_t *err) {
@@ -65,28 +76,30 @@ __global__ void __launch_bounds__(32 * kPlanWarps)
     uint32_t *mine = count + warp * E;
     for (int e = lane; e < E; e += 32) mine[e] = 0u;
     __syncwarp();
+    const int bits = 32 - __clz(E);  // of the values 0 .. E - 1 and of E, which stands for a dropped one
     for (int64_t i0 = first; i0 < last; i0 += 32 * kBatch) {
         int e[kBatch];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             const int64_t i = i0 + u * 32 + lane;
-            e[u] = i < last ? __ldg(ids + i) : -1;
+            e[u] = i < last ? __ldg(ids + i) : -1;  // dropped, as far as counting goes
         }
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             const int64_t i = i0 + u * 32 + lane;
-            if (e[u] < -1 || e[u] >= E) {
-                ptx::record_error(err, kErrInvalid | (2u << 8));
-                e[u] = -1;
+            if (e[u] < 0 || e[u] >= E) {
+                if (e[u] != -1) ptx::record_error(err, kErrInvalid | (2u << 8));
+                e[u] = E;
             }
-            const uint32_t same = __match_any_sync(0xffffffffu, e[u]);
+            const bool kept = e[u] < E;
+            const uint32_t same = same_value(e[u], bits);
             const uint32_t before = __popc(same & ((1u << lane) - 1u));
             uint32_t seen = 0u;
-            if (e[u] >= 0) seen = mine[e[u]];
+            if (kept) seen = mine[e[u]];
             __syncwarp();
-            if (e[u] >= 0 && before == 0u) mine[e[u]] = seen + __popc(same);
+            if (kept && before == 0u) mine[e[u]] = seen + __popc(same);
             __syncwarp();
-            if (i < last) row[i] = e[u] >= 0 ? static_cast<int32_t>(seen + before) : -1;
+            if (i < last) row[i] = kept ? static_cast<int32_t>(seen + before) : -1;
         }
     }
     __syncthreads();
