@@ -527,11 +527,14 @@ tpce_status tp_rmsnorm_backward(const void *dY, const void *S, const float *w, c
  * row and offsets are a plan's; a place outside [-1, T k) is skipped and
  * recorded in the device status word.
  * Shapes: 1 <= k <= 32, 1 <= E <= 1024, T k below 2^31 - 1024, h a multiple
- * of 8 up to 2^20. T == 0: offsets are zeroed, the rest is a no-op. No
- * workspace.
+ * of 8 up to 2^20. T == 0: offsets are zeroed, the rest is a no-op.
+ * Workspace: tpce_expert_plan_workspace_bytes for the plan (counts of up to 256
+ * blocks of assignments; 0 for up to 2048 assignments and for invalid shapes).
  * ------------------------------------------------------------------------- */
+size_t tpce_expert_plan_workspace_bytes(int64_t T, int k, int E);
 tpce_status tp_expert_plan(const int32_t *ids, int64_t T, int k, int E, int32_t *row,
-                           int32_t *source, int32_t *offsets, void *stream);
+                           int32_t *source, int32_t *offsets, void *ws, size_t ws_bytes,
+                           void *stream);
 tpce_status tp_expert_dispatch_forward(const void *X, const int32_t *row, const int32_t *offsets,
                                        int64_t T, int64_t h, int k, int E, int dtype, void *Xs,
                                        void *stream);

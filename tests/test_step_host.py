@@ -62,14 +62,21 @@ def test_rmsnorm_workspace(L):
 
 
 def test_expert_plan_refusals(L):
-    def call(T=4, k=2, E=8, ids=OK, row=OK, source=OK, offsets=OK):
-        return L.tp_expert_plan(ids, T, k, E, row, source, offsets, None)
+    def call(T=4, k=2, E=8, ids=OK, row=OK, source=OK, offsets=OK, ws=None, n=0):
+        return L.tp_expert_plan(ids, T, k, E, row, source, offsets, ws, n, None)
     assert call(T=-1) == SHAPE and call(k=0) == SHAPE and call(k=33) == SHAPE
     assert call(E=0) == SHAPE and call(E=1025) == SHAPE and call(T=1 << 30) == SHAPE
     for name in ("ids", "row", "source", "offsets"):
         assert call(**{name: None}) == INVALID
         assert call(**{name: ODD}) == ALIGN
     assert call(T=0, offsets=None) == INVALID
+    # few assignments need no workspace; more need E counts for each of at most 256 blocks
+    need = L.tpce_expert_plan_workspace_bytes
+    assert need(1024, 2, 8) == 0 and need(0, 2, 8) == 0 and need(10_000, 0, 8) == 0
+    for T, k, E in ((1025, 2, 8), (16384, 8, 64), (10_000_000, 8, 1024)):
+        assert 0 < need(T, k, E) <= 256 * E * 4 and need(T, k, E) % (4 * E) == 0
+        assert call(T=T, k=k, E=E) == WORKSPACE and call(T=T, k=k, E=E, ws=OK, n=need(T, k, E) - 1) == WORKSPACE
+        assert call(T=T, k=k, E=E, ws=ODD, n=1 << 30) == ALIGN
 
 
 def test_expert_row_refusals(L):

@@ -83,7 +83,8 @@ SIGNATURES = {
     "tpce_rmsnorm_workspace_bytes": (_SZ, [_I64, _I64]),
     "tp_rmsnorm_forward": (_I, [_P, _P, _P, _I64, _I64, _F, _I, _P, _P, _P, _P, _P, _P]),
     "tp_rmsnorm_backward": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I, _P, _P, _P, _SZ, _P]),
-    "tp_expert_plan": (_I, [_P, _I64, _I, _I, _P, _P, _P, _P]),
+    "tpce_expert_plan_workspace_bytes": (_SZ, [_I64, _I, _I]),
+    "tp_expert_plan": (_I, [_P, _I64, _I, _I, _P, _P, _P, _P, _SZ, _P]),
     "tp_expert_dispatch_forward": (_I, [_P, _P, _P, _I64, _I64, _I, _I, _I, _P, _P]),
     "tp_expert_dispatch_backward": (_I, [_P, _P, _I64, _I64, _I, _I, _P, _P]),
     "tp_expert_combine_forward": (_I, [_P, _P, _P, _I64, _I64, _I, _I, _P, _P]),

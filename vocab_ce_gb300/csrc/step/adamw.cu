@@ -24,6 +24,7 @@
 #include <cmath>
 
 #include "host.h"
+#include "step/launch.cuh"
 #include "step/vec.cuh"
 
 namespace tpce {
@@ -244,12 +245,13 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     const int64_t chunks = (e.n - first + kChunk - 1) / kChunk;
     const int left = chunks < e.span ? static_cast<int>(chunks) : static_cast<int>(e.span);
     const int64_t i = first + threadIdx.x * 8;
+    grid_begin();
     Rates c{k.step_size, k.root_scale, k.grad_scale, e.decay};
     if (k.device) {
-        c.step_size = __ldg(k.device);
-        c.root_scale = __ldg(k.device + 1);
-        c.decay = __fsub_rn(1.0f, __fmul_rn(__ldg(k.device + 2), e.wd));
-        c.grad_scale = __ldg(k.device + 3);
+        c.step_size = k.device[0];
+        c.root_scale = k.device[1];
+        c.decay = __fsub_rn(1.0f, __fmul_rn(k.device[2], e.wd));
+        c.grad_scale = k.device[3];
     }
     const bool narrow = (e.kind & kParamBf16) && !(e.kind & kMaster);
     if (e.kind & kGradBf16) {
@@ -266,12 +268,13 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
 }
 
 template <int N>
-tpce_status launch(const Entry *entries, int count, uint32_t blocks, const Scalars &k, cudaStream_t s) {
+tpce_status launch_table(const Entry *entries, int count, uint32_t blocks, const Scalars &k, cudaStream_t s) {
     Table<N> table;
     std::copy(entries, entries + count, table.t);
     table.count = count;
     KernelTimer timer("adamw_step", s);
-    adamw_kernel<N><<<blocks, kThreads, 0, s>>>(table, k);
+    const cudaError_t e = launch(adamw_kernel<N>, blocks, kThreads, 0, s, table, k);
+    if (e != cudaSuccess) return fail_cuda(e, "adamw_step");
     return check_launch("adamw_step", s);
 }
 
@@ -329,9 +332,9 @@ extern "C" tpce_status tp_adamw_step(const tpce_adamw_tensor *tensors, int count
     uint32_t blocks = 0;
     auto flush = [&]() -> tpce_status {
         if (!held) return TPCE_OK;
-        tpce_status st = held <= kShort    ? launch<kShort>(entries, held, blocks, k, s)
-                         : held <= kMiddle ? launch<kMiddle>(entries, held, blocks, k, s)
-                                           : launch<kLong>(entries, held, blocks, k, s);
+        tpce_status st = held <= kShort    ? launch_table<kShort>(entries, held, blocks, k, s)
+                         : held <= kMiddle ? launch_table<kMiddle>(entries, held, blocks, k, s)
+                                           : launch_table<kLong>(entries, held, blocks, k, s);
         held = 0;
         blocks = 0;
         return st;

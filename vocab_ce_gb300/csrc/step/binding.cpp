@@ -33,6 +33,7 @@ struct Api {
     decltype(&tpce_rmsnorm_workspace_bytes) rmsnorm_workspace_bytes;
     decltype(&tp_rmsnorm_forward) rmsnorm_forward;
     decltype(&tp_rmsnorm_backward) rmsnorm_backward;
+    decltype(&tpce_expert_plan_workspace_bytes) expert_plan_workspace_bytes;
     decltype(&tp_expert_plan) expert_plan;
     decltype(&tp_expert_dispatch_forward) expert_dispatch_forward;
     decltype(&tp_expert_dispatch_backward) expert_dispatch_backward;
@@ -170,6 +171,17 @@ struct Results {
     }
 };
 
+// The caller's workspace if it is large enough, or a new one; undefined for 0 bytes.
+at::Tensor workspace(PyObject *given, size_t bytes, const at::Tensor &like) {
+    if (!none(given)) {
+        const at::Tensor &x = tensor(given, "ws");
+        need(x, std::string("ws"), nullptr, nullptr);
+        if (x.nbytes() >= bytes) return x;
+    }
+    return bytes ? empty({static_cast<int64_t>(bytes)}, at::kByte, like) : at::Tensor();
+}
+size_t bytes_of(const at::Tensor &x) { return x.defined() ? x.nbytes() : 0; }
+
 bool truth(PyObject *o) { return PyObject_IsTrue(o) == 1; }
 double number(PyObject *o) {
     const double v = PyFloat_AsDouble(o);
@@ -229,25 +241,18 @@ PyObject *rmsnorm_backward(PyObject *const *a) {
     Results res;
     const at::Tensor dX = output(entry(a[6], keys->dX), "dX", S.sizes(), S.scalar_type(), S);
     res.add(keys->dX, dX);
-    size_t bytes = 0;
     if (truth(a[5])) {
         res.add(keys->dw, dw = output(entry(a[6], keys->dw), "dw", {h}, at::kFloat, S));
-        bytes = api.rmsnorm_workspace_bytes(T, h);
-        if (!none(a[7])) {
-            ws = tensor(a[7], "ws");
-            need(ws, std::string("ws"), nullptr, nullptr);
-        }
-        if (!ws.defined() || ws.nbytes() < bytes) ws = empty({static_cast<int64_t>(bytes)}, at::kByte, S);
-        bytes = ws.nbytes();
+        ws = workspace(a[7], api.rmsnorm_workspace_bytes(T, h), S);
     }
     raise_on(api.rmsnorm_backward(ptr(dY), ptr(S), fptr(w), fptr(rstd), ptr(dS), T, h, dt, ptr(dX), fptr(dw), ptr(ws),
-                                  bytes, stream()),
+                                  bytes_of(ws), stream()),
              "tp_rmsnorm_backward");
     return res.take();
 }
 
 // ------------------------------------------------------------------ experts
-// ids, experts, out
+// ids, experts, out, ws
 PyObject *expert_plan(PyObject *const *a) {
     const at::Tensor &ids = tensor(a[0], "ids");
     if (ids.dim() != 2) throw Refused{"ids must be a matrix of rows, got shape " + shape_text(ids.sizes())};
@@ -261,8 +266,10 @@ PyObject *expert_plan(PyObject *const *a) {
     res.add(keys->source, source);
     const at::Tensor offsets = output(entry(a[2], keys->offsets), "offsets", {E + 1}, at::kInt, ids);
     res.add(keys->offsets, offsets);
-    raise_on(api.expert_plan(iptr(ids), T, static_cast<int>(std::min<int64_t>(k, 1 << 30)), static_cast<int>(E),
-                             iptr(row), iptr(source), iptr(offsets), stream()),
+    const int choices = static_cast<int>(std::min<int64_t>(k, 1 << 30));
+    const at::Tensor ws = workspace(a[3], api.expert_plan_workspace_bytes(T, choices, static_cast<int>(E)), ids);
+    raise_on(api.expert_plan(iptr(ids), T, choices, static_cast<int>(E), iptr(row), iptr(source), iptr(offsets),
+                             ptr(ws), bytes_of(ws), stream()),
              "tp_expert_plan");
     return res.take();
 }
@@ -481,7 +488,7 @@ PyMethodDef methods[] = {
     {"init", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&init)), METH_FASTCALL, nullptr},
     STEP_CALL(rmsnorm_forward, 7),
     STEP_CALL(rmsnorm_backward, 8),
-    STEP_CALL(expert_plan, 3),
+    STEP_CALL(expert_plan, 4),
     STEP_CALL(expert_dispatch_forward, 3),
     STEP_CALL(expert_dispatch_backward, 3),
     STEP_CALL(expert_combine_forward, 4),

@@ -21,6 +21,7 @@
 
 #include "host.h"
 #include "ptx.cuh"
+#include "step/launch.cuh"
 #include "step/vec.cuh"
 
 namespace tpce {
@@ -32,18 +33,49 @@ constexpr int kMaxExperts = 1024;
 constexpr int kMaxChoices = 32;
 
 // ------------------------------------------------------------------ the plan
-// One launch: a cluster of CTAs, one warp of 32 x CTAs for each contiguous run
-// of assignments. Pass 1 counts the run's assignments per expert and gives each
-// its rank among the run's equal ones (kept in row[]); the counts are then
-// summed over the block's warps, over the cluster's blocks (distributed shared
-// memory) and over the experts; pass 2 adds them to the rank.
-constexpr int kPlanWarps = 32;
-constexpr int kBatch = 8;  // vectors of 32 assignments whose loads are under way at once
+// A block takes a chunk of the assignments, each of its warps a contiguous run
+// of the chunk. expert_count_kernel counts the chunks' assignments per expert;
+// expert_place_kernel adds up the counts of the chunks before its own, counts
+// its own per warp and gives each assignment its rank among the equal ones of
+// its run (kept in row[]), and then writes the places. Few assignments are one
+// block's, and need no counting before. Many blocks, because the places of
+// source[] are scattered: one SM stores only about a word of them in a cycle
+// (131,072 assignments over 64 experts took eight SMs 20 us, and take 128 blocks XX).
+constexpr int kPlanThreads = 256;
+constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kBatch = 4;  // vectors of 32 assignments whose loads are under way at once
+constexpr int64_t kPlanChunk = 1024, kPlanBlocks = 256;
 
-__device__ __forceinline__ uint32_t read_cluster_u32(const uint32_t *p, uint32_t rank) {
-    uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(ptx::mapa_shared(ptx::smem_u32(p), rank)) : "memory");
-    return v;
+struct PlanSplit {
+    int64_t chunk;
+    int blocks;
+};
+inline PlanSplit plan_split(int64_t n) {
+    const int64_t chunk = std::max<int64_t>(kPlanChunk, (n + kPlanBlocks - 1) / kPlanBlocks);
+    if (n <= 2 * chunk) return {n, 1};
+    return {chunk, static_cast<int>((n + chunk - 1) / chunk)};
+}
+
+__global__ void __launch_bounds__(kPlanThreads)
+    expert_count_kernel(const int32_t *ids, int64_t n, int64_t chunk, int E, uint32_t *__restrict__ counts) {
+    extern __shared__ uint32_t count[];  // [E]
+    for (int e = threadIdx.x; e < E; e += kPlanThreads) count[e] = 0u;
+    grid_begin();
+    __syncthreads();
+    const int64_t first = blockIdx.x * chunk, last = min(n, first + chunk);
+    for (int64_t i0 = first + threadIdx.x; i0 < last; i0 += kPlanThreads * kBatch) {
+        int e[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int64_t i = i0 + u * kPlanThreads;
+            e[u] = i < last ? ids[i] : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+            if (e[u] >= 0 && e[u] < E) atomicAdd(&count[e[u]], 1u);  // whole numbers: any order gives the same
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += kPlanThreads) counts[static_cast<int64_t>(blockIdx.x) * E + e] = count[e];
 }
 
 // The lanes whose value equals this lane's, from one ballot for each of its bits.
@@ -57,32 +89,49 @@ __device__ __forceinline__ uint32_t same_value(int v, int bits) {
     return same;
 }
 
-__global__ void __launch_bounds__(32 * kPlanWarps)
-    expert_plan_kernel(const int32_t *__restrict__ ids, int64_t n, int E, int ctas, int32_t *row, int32_t *source,
-                       int32_t *offsets, uint32_t *err) {
+// counts NULL: this block is the only one.
+__global__ void __launch_bounds__(kPlanThreads)
+    expert_place_kernel(const int32_t *ids, int64_t n, int64_t chunk, int E,
+                        const uint32_t *counts, int32_t *row, int32_t *source, int32_t *offsets,
+                        uint32_t *err) {
     extern __shared__ uint32_t smem[];
-    uint32_t *count = smem;                      // [kPlanWarps][E], then prefix sums over the warps
-    uint32_t *total = smem + kPlanWarps * E;     // [E] this block's counts
-    uint32_t *base = total + E;                  // [E] first place of this block's share of an expert
+    uint32_t *count = smem;                   // [kPlanWarps][E], then prefix sums over the warps
+    uint32_t *all = smem + kPlanWarps * E;    // [E] assignments of an expert, then the first place of this block's
+    uint32_t *below = all + E;                // [E] those of the blocks before
     __shared__ uint32_t scan[kPlanWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = ctas > 1 ? ptx::cluster_ctarank() : 0u;
+    for (int e = threadIdx.x; e < (kPlanWarps + 2) * E; e += kPlanThreads) smem[e] = 0u;
+    grid_begin();
+    __syncthreads();
+    if (counts) {
+        // E counts a block: a thread adds those of one expert over some of the blocks
+        int width = 1;
+        while (width < E && width < kPlanThreads) width *= 2;
+        const int parts = kPlanThreads / width, part = threadIdx.x / width;
+        for (int e = threadIdx.x & (width - 1); e < E; e += width) {
+            uint32_t sum = 0u, before = 0u;
+#pragma unroll 8
+            for (int q = part; q < static_cast<int>(gridDim.x); q += parts) {
+                const uint32_t c = counts[static_cast<int64_t>(q) * E + e];
+                sum += c;
+                before += q < static_cast<int>(blockIdx.x) ? c : 0u;
+            }
+            atomicAdd(&all[e], sum);
+            atomicAdd(&below[e], before);
+        }
+    }
 
-    const int64_t warps = static_cast<int64_t>(ctas) * kPlanWarps;
-    const int64_t run = ((n + warps - 1) / warps + 31) / 32 * 32;
-    const int64_t first = (static_cast<int64_t>(rank) * kPlanWarps + warp) * run;
-    const int64_t last = min(n, first + run);
-
+    const int64_t begin = blockIdx.x * chunk, end = min(n, begin + chunk);
+    const int64_t run = ((end - begin + kPlanWarps - 1) / kPlanWarps + 31) / 32 * 32;
+    const int64_t first = begin + warp * run, last = min(end, first + run);
     uint32_t *mine = count + warp * E;
-    for (int e = lane; e < E; e += 32) mine[e] = 0u;
-    __syncwarp();
     const int bits = 32 - __clz(E);  // of the values 0 .. E - 1 and of E, which stands for a dropped one
     for (int64_t i0 = first; i0 < last; i0 += 32 * kBatch) {
         int e[kBatch];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             const int64_t i = i0 + u * 32 + lane;
-            e[u] = i < last ? __ldg(ids + i) : -1;  // dropped, as far as counting goes
+            e[u] = i < last ? ids[i] : -1;
         }
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
@@ -103,35 +152,27 @@ __global__ void __launch_bounds__(32 * kPlanWarps)
         }
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+    for (int e = threadIdx.x; e < E; e += kPlanThreads) {
         uint32_t sum = 0u;
-#pragma unroll 8
+#pragma unroll
         for (int q = 0; q < kPlanWarps; ++q) {
             const uint32_t c = count[q * E + e];
             count[q * E + e] = sum;
             sum += c;
         }
-        total[e] = sum;
+        if (!counts) all[e] = sum;
     }
-    if (ctas > 1)
-        ptx::cluster_sync();
-    else
-        __syncthreads();
-    // E <= 1024: one expert a thread
-    uint32_t all = 0u, below = 0u;
-    const int e = threadIdx.x;
-    if (e < E) {
-        if (ctas > 1) {
-            for (int q = 0; q < ctas; ++q) {
-                const uint32_t c = read_cluster_u32(total + e, q);
-                below += q < static_cast<int>(rank) ? c : 0u;
-                all += c;
-            }
-        } else {
-            all = total[e];
-        }
+    __syncthreads();
+    // first places: a scan over the experts, four adjacent ones a thread
+    constexpr int kEach = kMaxExperts / kPlanThreads;
+    uint32_t own[kEach], sum = 0u;
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+        const int e = threadIdx.x * kEach + u;
+        own[u] = e < E ? all[e] : 0u;
+        sum += own[u];
     }
-    uint32_t incl = all;
+    uint32_t incl = sum;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const uint32_t o = __shfl_up_sync(0xffffffffu, incl, d);
@@ -139,17 +180,22 @@ __global__ void __launch_bounds__(32 * kPlanWarps)
     }
     if (lane == 31) scan[warp] = incl;
     __syncthreads();
-    uint32_t prior = 0u, kept = 0u;
+    uint32_t at = incl - sum, kept = 0u;
+#pragma unroll
     for (int q = 0; q < kPlanWarps; ++q) {
-        const uint32_t c = scan[q];
-        prior += q < warp ? c : 0u;
-        kept += c;
+        at += q < warp ? scan[q] : 0u;
+        kept += scan[q];
     }
-    if (e < E) {
-        base[e] = prior + incl - all + below;
-        if (rank == 0) {
-            offsets[e + 1] = static_cast<int32_t>(prior + incl);
-            if (e == 0) offsets[0] = 0;
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+        const int e = threadIdx.x * kEach + u;
+        if (e < E) {
+            all[e] = at + below[e];
+            at += own[u];
+            if (blockIdx.x == 0) {
+                offsets[e + 1] = static_cast<int32_t>(at);
+                if (e == 0) offsets[0] = 0;
+            }
         }
     }
     __syncthreads();
@@ -160,21 +206,20 @@ __global__ void __launch_bounds__(32 * kPlanWarps)
         for (int u = 0; u < kBatch; ++u) {
             const int64_t i = i0 + u * 32;
             r[u] = i < last ? row[i] : -1;
-            x[u] = i < last ? __ldg(ids + i) : 0;
+            x[u] = i < last ? ids[i] : 0;
         }
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             const int64_t i = i0 + u * 32;
             if (r[u] < 0) continue;  // past the run, or dropped: row[i] is -1 already
-            const uint32_t p = base[x[u]] + mine[x[u]] + static_cast<uint32_t>(r[u]);
+            const uint32_t p = all[x[u]] + mine[x[u]] + static_cast<uint32_t>(r[u]);
             row[i] = static_cast<int32_t>(p);
             source[p] = static_cast<int32_t>(i);
         }
     }
-    for (int64_t p = kept + static_cast<int64_t>(rank) * blockDim.x + threadIdx.x; p < n;
-         p += static_cast<int64_t>(ctas) * blockDim.x)
+    for (int64_t p = kept + static_cast<int64_t>(blockIdx.x) * kPlanThreads + threadIdx.x; p < n;
+         p += static_cast<int64_t>(gridDim.x) * kPlanThreads)
         source[p] = -1;
-    if (ctas > 1) ptx::cluster_sync();  // no block leaves while another reads its counts
 }
 
 // ------------------------------------------------------------------ rows by token
@@ -195,7 +240,7 @@ inline Split split_of(int64_t vectors, int64_t T) {
 
 // A place read from the plan; one outside the rows is reported and skipped.
 __device__ __forceinline__ int32_t place(const int32_t *row, int64_t i, int64_t n, uint32_t *err) {
-    const int32_t p = __ldg(row + i);
+    const int32_t p = row[i];
     if (p < -1 || p >= n) {
         ptx::record_error(err, kErrInvalid | (3u << 8));
         return -1;
@@ -213,7 +258,7 @@ __device__ __forceinline__ void places(const int32_t *row, int64_t t, int k, int
 
 // Rows offsets[E] .. n of out are zeros: the blocks take them in turn.
 __device__ __forceinline__ void zero_rest(uint4 *out, const int32_t *offsets, int E, int64_t n, int vectors) {
-    const int64_t kept = max(0, __ldg(offsets + E));
+    const int64_t kept = max(0, offsets[E]);
     for (int64_t p = kept + blockIdx.x; p < n; p += gridDim.x)
         for (int c = threadIdx.x; c < vectors; c += blockDim.x) out[p * vectors + c] = make_uint4(0u, 0u, 0u, 0u);
 }
@@ -222,22 +267,30 @@ __device__ __forceinline__ void zero_rest(uint4 *out, const int32_t *offsets, in
 // (K is the largest then) they take the choices K at a time.
 template <int K>
 __global__ void __launch_bounds__(256)
-    expert_dispatch_kernel(const uint4 *__restrict__ X, const int32_t *__restrict__ row,
-                           const int32_t *__restrict__ offsets, int E, int64_t T, int k, int vectors, int lanes,
+    expert_dispatch_kernel(const uint4 *X, const int32_t *row,
+                           const int32_t *offsets, int E, int64_t T, int k, int vectors, int lanes,
                            uint4 *__restrict__ out, uint32_t *err) {
     const int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x / lanes) + threadIdx.x / lanes;
     const int lane = threadIdx.x & (lanes - 1);
     const int64_t n = T * k;
+    grid_begin();
     if (t < T) {
         for (int j0 = 0; j0 < k; j0 += K) {
             int32_t p[K];
             places(row + j0, t, k, n, err, p, k - j0);
-#pragma unroll 4
-            for (int c = lane; c < vectors; c += lanes) {
-                const uint4 v = __ldg(X + t * vectors + c);
+            for (int c0 = lane; c0 < vectors; c0 += 4 * lanes) {
+                uint4 v[4];
 #pragma unroll
-                for (int j = 0; j < K; ++j)
-                    if (p[j] >= 0) out[static_cast<int64_t>(p[j]) * vectors + c] = v;
+                for (int u = 0; u < 4; ++u)
+                    if (c0 + u * lanes < vectors) v[u] = X[t * vectors + c0 + u * lanes];
+#pragma unroll
+                for (int j = 0; j < K; ++j) {
+                    if (p[j] < 0) continue;
+                    uint4 *to = out + static_cast<int64_t>(p[j]) * vectors + c0;
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (c0 + u * lanes < vectors) to[u * lanes] = v[u];
+                }
             }
         }
     }
@@ -264,61 +317,77 @@ __device__ __forceinline__ uint4 narrow(const float (&v)[4]) {
 // NV values a vector: 8 (bf16) or 4 (fp32). weights NULL: all one.
 template <int NV, int K>
 __global__ void __launch_bounds__(256)
-    expert_combine_kernel(const uint4 *__restrict__ Ys, const int32_t *__restrict__ row,
-                          const float *__restrict__ weights, int64_t T, int k, int vectors, int lanes,
+    expert_combine_kernel(const uint4 *Ys, const int32_t *row,
+                          const float *weights, int64_t T, int k, int vectors, int lanes,
                           uint4 *__restrict__ Z, uint32_t *err) {
     const int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x / lanes) + threadIdx.x / lanes;
     const int lane = threadIdx.x & (lanes - 1);
+    grid_begin();
     if (t >= T) return;
     const int64_t n = T * k;
-    constexpr int U = K >= 4 ? 1 : 4 / K;  // vectors at a time: at least four loads under way
+    constexpr int U = K >= 8 ? 1 : K == 4 ? 2 : 4 / K;  // vectors at a time: four to eight loads under way
     int32_t p[K];
     float w[K];
     auto choices = [&](int j0) {
         places(row + j0, t, k, n, err, p, k - j0);
 #pragma unroll
-        for (int j = 0; j < K; ++j) w[j] = weights && j0 + j < k ? __ldg(weights + t * k + j0 + j) : 1.0f;
+        for (int j = 0; j < K; ++j) w[j] = weights && j0 + j < k ? weights[t * k + j0 + j] : 1.0f;
     };
-    if (k <= K) choices(0);
-    for (int c0 = lane; c0 < vectors; c0 += U * lanes) {
-        float z[U][NV] = {};
-        for (int j0 = 0; j0 < k; j0 += K) {
-            if (k > K) choices(j0);
-            uint4 y[U][K];
+    auto add = [&](const uint4 (&y)[K], float (&z)[NV]) {
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+        for (int j = 0; j < K; ++j) {
+            if (p[j] < 0) continue;
+            float v[NV];
+            widen(y[j], v);
 #pragma unroll
-                for (int j = 0; j < K; ++j)
-                    if (p[j] >= 0 && c0 + u * lanes < vectors)
-                        y[u][j] = __ldg(Ys + static_cast<int64_t>(p[j]) * vectors + c0 + u * lanes);
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int j = 0; j < K; ++j) {
-                    if (p[j] < 0) continue;
-                    float v[NV];
-                    widen(y[u][j], v);
-#pragma unroll
-                    for (int i = 0; i < NV; ++i) z[u][i] += w[j] * v[i];
-                }
+            for (int i = 0; i < NV; ++i) z[i] += w[j] * v[i];
         }
+    };
+    auto load = [&](int c, uint4 (&y)[K]) {
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+            if (p[j] >= 0) y[j] = Ys[static_cast<int64_t>(p[j]) * vectors + c];
+    };
+    if (k > K) {
+        for (int c = lane; c < vectors; c += lanes) {
+            float z[NV] = {};
+            for (int j0 = 0; j0 < k; j0 += K) {
+                uint4 y[K];
+                choices(j0);
+                load(c, y);
+                add(y, z);
+            }
+            Z[t * vectors + c] = narrow(z);
+        }
+        return;
+    }
+    choices(0);
+    for (int c0 = lane; c0 < vectors; c0 += U * lanes) {
+        uint4 y[U][K];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (c0 + u * lanes < vectors) Z[t * vectors + c0 + u * lanes] = narrow(z[u]);
+            if (c0 + u * lanes < vectors) load(c0 + u * lanes, y[u]);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float z[NV] = {};
+            add(y[u], z);
+            if (c0 + u * lanes < vectors) Z[t * vectors + c0 + u * lanes] = narrow(z);
+        }
     }
 }
 
 template <int NV, int K>
 __global__ void __launch_bounds__(256)
-    expert_combine_backward_kernel(const uint4 *__restrict__ dZ, const uint4 *__restrict__ Ys,
-                                   const int32_t *__restrict__ row, const int32_t *__restrict__ offsets, int E,
-                                   const float *__restrict__ weights, int64_t T, int k, int vectors, int lanes,
+    expert_combine_backward_kernel(const uint4 *dZ, const uint4 *Ys,
+                                   const int32_t *row, const int32_t *offsets, int E,
+                                   const float *weights, int64_t T, int k, int vectors, int lanes,
                                    uint4 *__restrict__ dYs, float *__restrict__ dweights, uint32_t *err) {
     __shared__ float red[8][K];
     const int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x / lanes) + threadIdx.x / lanes;
     const int lane = threadIdx.x & (lanes - 1);
     const int64_t n = T * k;
     constexpr int U = K >= 4 ? 1 : 4 / K;
+    grid_begin();
     for (int j0 = 0; j0 < k; j0 += K) {
         int32_t p[K];
         float w[K], dot[K] = {};
@@ -328,17 +397,17 @@ __global__ void __launch_bounds__(256)
             places(row + j0, t, k, n, err, p, k - j0);
 #pragma unroll
             for (int j = 0; j < K; ++j)
-                if (p[j] >= 0) w[j] = __ldg(weights + t * k + j0 + j);
+                if (p[j] >= 0) w[j] = weights[t * k + j0 + j];
             for (int c0 = lane; c0 < vectors; c0 += U * lanes) {
                 uint4 d[U], y[U][K];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const int c = c0 + u * lanes;
                     if (c >= vectors) continue;
-                    d[u] = __ldg(dZ + t * vectors + c);
+                    d[u] = dZ[t * vectors + c];
 #pragma unroll
                     for (int j = 0; j < K; ++j)
-                        if (p[j] >= 0) y[u][j] = __ldg(Ys + static_cast<int64_t>(p[j]) * vectors + c);
+                        if (p[j] >= 0) y[u][j] = Ys[static_cast<int64_t>(p[j]) * vectors + c];
                 }
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
@@ -431,17 +500,18 @@ tpce_status combine(const char *name, const void *Ys, const int32_t *row, const 
     const int v = vectors_of(h, dtype);
     const Split sp = split_of(v, T);
     KernelTimer timer(name, s);
+    cudaError_t e = cudaSuccess;
     with_choices(k, [&](auto K) {
         auto go = [&](auto kernel) {
-            kernel<<<blocks_of(T, sp), 256, 0, s>>>(static_cast<const uint4 *>(Ys), row, weights, T, k, v, sp.lanes,
-                                                    static_cast<uint4 *>(Z), device_error_word());
+            e = launch(kernel, blocks_of(T, sp), 256, 0, s, static_cast<const uint4 *>(Ys), row, weights, T, k, v,
+                       sp.lanes, static_cast<uint4 *>(Z), device_error_word());
         };
         if (dtype == TPCE_BF16)
             go(expert_combine_kernel<8, decltype(K)::value>);
         else
             go(expert_combine_kernel<4, decltype(K)::value>);
     });
-    return check_launch(name, s);
+    return e == cudaSuccess ? check_launch(name, s) : fail_cuda(e, name);
 }
 
 }  // namespace
@@ -450,8 +520,14 @@ tpce_status combine(const char *name, const void *Ys, const int32_t *row, const 
 // ====================================================================== C ABI
 using namespace tpce;
 
+extern "C" size_t tpce_expert_plan_workspace_bytes(int64_t T, int k, int E) {
+    if (check_plan_shape(T, k, E) != TPCE_OK) return 0;
+    const PlanSplit sp = plan_split(T * k);
+    return sp.blocks > 1 ? static_cast<size_t>(sp.blocks) * E * sizeof(uint32_t) : 0;
+}
+
 extern "C" tpce_status tp_expert_plan(const int32_t *ids, int64_t T, int k, int E, int32_t *row, int32_t *source,
-                                      int32_t *offsets, void *stream) {
+                                      int32_t *offsets, void *ws, size_t ws_bytes, void *stream) {
     tpce_status st = check_plan_shape(T, k, E);
     if (st != TPCE_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -461,29 +537,26 @@ extern "C" tpce_status tp_expert_plan(const int32_t *ids, int64_t T, int k, int 
     }
     if ((st = check_pointers("tp_expert_plan", {ids, row, source, offsets})) != TPCE_OK) return st;
     const int64_t n = T * k;
-    const int ctas = n <= 4096 ? 1 : 8;
-    const size_t smem = static_cast<size_t>(kPlanWarps + 2) * E * sizeof(uint32_t);
+    const PlanSplit sp = plan_split(n);
+    uint32_t *counts = nullptr;
     cudaError_t e;
-    if (smem > 48 * 1024) {  // more than a launch has without asking: from 362 experts on
-        e = cudaFuncSetAttribute(expert_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (kPlanWarps + 2) * kMaxExperts * static_cast<int>(sizeof(uint32_t)));
-        if (e != cudaSuccess) return fail_cuda(e, "expert_plan");
+    if (sp.blocks > 1) {
+        const size_t need = tpce_expert_plan_workspace_bytes(T, k, E);
+        if (!ws || ws_bytes < need)
+            return fail(TPCE_ERR_WORKSPACE, "tp_expert_plan: %zu bytes of workspace needed, %zu given", need,
+                        ws ? ws_bytes : size_t{0});
+        if (!aligned16(ws)) return fail(TPCE_ERR_ALIGN, "tp_expert_plan: a pointer is not 16-byte aligned");
+        counts = static_cast<uint32_t *>(ws);
+        KernelTimer timer("expert_count", s);
+        e = launch(expert_count_kernel, sp.blocks, kPlanThreads, E * sizeof(uint32_t), s, ids, n, sp.chunk, E, counts);
+        if (e != cudaSuccess) return fail_cuda(e, "expert_count");
+        if ((st = check_launch("expert_count", s)) != TPCE_OK) return st;
     }
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-    cfg.blockDim = dim3(32 * kPlanWarps);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = static_cast<unsigned>(ctas);
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    KernelTimer timer("expert_plan", s);
-    e = cudaLaunchKernelEx(&cfg, expert_plan_kernel, ids, n, E, ctas, row, source, offsets, device_error_word());
-    if (e != cudaSuccess) return fail_cuda(e, "expert_plan");
-    return check_launch("expert_plan", s);
+    KernelTimer timer("expert_place", s);
+    e = launch(expert_place_kernel, sp.blocks, kPlanThreads, (kPlanWarps + 2) * E * sizeof(uint32_t), s, ids, n,
+               sp.chunk, E, counts, row, source, offsets, device_error_word());
+    if (e != cudaSuccess) return fail_cuda(e, "expert_place");
+    return check_launch("expert_place", s);
 }
 
 extern "C" tpce_status tp_expert_dispatch_forward(const void *X, const int32_t *row, const int32_t *offsets, int64_t T,
@@ -495,12 +568,13 @@ extern "C" tpce_status tp_expert_dispatch_forward(const void *X, const int32_t *
     const int v = vectors_of(h, dtype);
     const Split sp = split_of(v, T);
     KernelTimer timer("expert_dispatch", s);
+    cudaError_t e = cudaSuccess;
     with_choices(k, [&](auto K) {
-        expert_dispatch_kernel<decltype(K)::value>
-            <<<blocks_of(T, sp), 256, 0, s>>>(static_cast<const uint4 *>(X), row, offsets, E, T, k, v, sp.lanes,
-                                              static_cast<uint4 *>(Xs), device_error_word());
+        e = launch(expert_dispatch_kernel<decltype(K)::value>, blocks_of(T, sp), 256, 0, s,
+                   static_cast<const uint4 *>(X), row, offsets, E, T, k, v, sp.lanes, static_cast<uint4 *>(Xs),
+                   device_error_word());
     });
-    return check_launch("expert_dispatch", s);
+    return e == cudaSuccess ? check_launch("expert_dispatch", s) : fail_cuda(e, "expert_dispatch");
 }
 
 extern "C" tpce_status tp_expert_dispatch_backward(const void *dXs, const int32_t *row, int64_t T, int64_t h, int k,
@@ -530,16 +604,17 @@ extern "C" tpce_status tp_expert_combine_backward(const void *dZ, const void *Ys
     const int v = vectors_of(h, dtype);
     const Split sp = split_of(v, T);
     KernelTimer timer("expert_combine_backward", s);
+    cudaError_t e = cudaSuccess;
     with_choices(k, [&](auto K) {
         auto go = [&](auto kernel) {
-            kernel<<<blocks_of(T, sp), 256, 0, s>>>(static_cast<const uint4 *>(dZ), static_cast<const uint4 *>(Ys),
-                                                    row, offsets, E, weights, T, k, v, sp.lanes,
-                                                    static_cast<uint4 *>(dYs), dweights, device_error_word());
+            e = launch(kernel, blocks_of(T, sp), 256, 0, s, static_cast<const uint4 *>(dZ),
+                       static_cast<const uint4 *>(Ys), row, offsets, E, weights, T, k, v, sp.lanes,
+                       static_cast<uint4 *>(dYs), dweights, device_error_word());
         };
         if (dtype == TPCE_BF16)
             go(expert_combine_backward_kernel<8, decltype(K)::value>);
         else
             go(expert_combine_backward_kernel<4, decltype(K)::value>);
     });
-    return check_launch("expert_combine_backward", s);
+    return e == cudaSuccess ? check_launch("expert_combine_backward", s) : fail_cuda(e, "expert_combine_backward");
 }

@@ -20,6 +20,7 @@
 
 #include "host.h"
 #include "ptx.cuh"
+#include "step/launch.cuh"
 #include "step/vec.cuh"
 
 namespace tpce {
@@ -29,14 +30,20 @@ using namespace step;
 
 constexpr int64_t kMaxWidth = 16384;  // 2 vectors of 8 values for each of 1024 threads, 4 for each of 512
 constexpr int64_t kMaxRows = int64_t{1} << 40;
-constexpr int kWarps = 8;             // rows of a block where a warp takes a row
+constexpr int kLanesThreads = 256;    // of a block where a row is some lanes of a warp
 constexpr int64_t kSms = 152;         // fixed, so that the workspace's size is known on the host
 constexpr int kMaxStages = 4;
 constexpr int kRowsOfBlock = 6;       // of the forward, where there are enough
 constexpr int kSmemPerSm = 228 * 1024;
 
-// A row of up to 256 values is a warp's (no barrier in its sum), a wider one a block's.
-inline bool warp_rows(int64_t h) { return h <= 256; }
+// A row of up to 256 values is 8, 16 or 32 lanes of a warp (no barrier in its
+// sum), a wider one a block's.
+inline bool lane_rows(int64_t h) { return h <= 256; }
+inline int lanes_of(int64_t h) { return h <= 64 ? 8 : h <= 128 ? 16 : 32; }
+inline int64_t lane_blocks(int64_t rows, int64_t h) {
+    const int64_t of_block = kLanesThreads / lanes_of(h);
+    return (rows + of_block - 1) / of_block;
+}
 
 // The vectors of a row that are this thread's; zeros past the row's end.
 template <typename T, int VPT>
@@ -110,7 +117,7 @@ struct Ring {
 };
 
 // ------------------------------------------------------------------ forward
-template <typename T, int VPT>
+template <typename T, int VPT, int GROUP_LANES>
 struct ForwardRow {
     float s[VPT][8];
 
@@ -135,11 +142,9 @@ struct ForwardRow {
         return sq + sq1;
     }
 
-    __device__ __forceinline__ void finish(float total, float inv_h, float eps, const float (&w)[VPT][8], T *Y,
-                                           uint8_t *Q, float *Qs, float *rstd_out, int64_t row, int64_t off, int h,
-                                           int lane, int lanes) {
-        const float rstd = rsqrtf(total * inv_h + eps);
-        if (lane == 0) rstd_out[row] = rstd;
+    // the row's columns up to h; its scales begin at Qs
+    __device__ __forceinline__ void finish(float rstd, const float (&w)[VPT][8], T *Y, uint8_t *Q, float *Qs,
+                                           int64_t off, int h, int lane, int lanes) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = (lane + i * lanes) * 8;
@@ -160,46 +165,54 @@ struct ForwardRow {
                     for (int j = 0; j < 8; ++j) s[i][j] = 0.0f;
                 }
                 float scale;
-                const uint2 q = quantize8(s[i], scale);
+                const uint2 q = quantize8<GROUP_LANES>(s[i], scale);
                 if (c < h) {
                     __stcs(reinterpret_cast<uint2 *>(Q + off + c), q);
-                    if ((lane & 15) == 0) Qs[row * ((h + kGroup - 1) / kGroup) + c / kGroup] = scale;
+                    if (lane % GROUP_LANES == 0) Qs[c / kGroup] = scale;
                 }
             }
         }
     }
 };
 
-template <typename T>
-__global__ void __launch_bounds__(32 * kWarps)
-    rmsnorm_forward_warp_kernel(const T *X, const T *R, const float *__restrict__ w, int64_t rows, int h, float eps,
-                                T *S, T *Y, uint8_t *Q, float *Qs, float *__restrict__ rstd) {
-    const int lane = threadIdx.x & 31;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * kWarps;
+__device__ __forceinline__ float rstd_of(float total, float inv_h, float eps) { return rsqrtf(total * inv_h + eps); }
+
+// LANES lanes a row, 256 / LANES rows a block at a time. The lanes of a warp
+// leave together: a row past the last has no columns.
+template <typename T, int LANES>
+__global__ void __launch_bounds__(kLanesThreads)
+    rmsnorm_forward_lanes_kernel(const T *X, const T *R, const float *w, int64_t rows, int h, float eps, T *S, T *Y,
+                                 uint8_t *Q, float *Qs, float *__restrict__ rstd) {
+    grid_begin();
+    const int lane = threadIdx.x % LANES;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * (kLanesThreads / LANES);
     const float inv_h = 1.0f / static_cast<float>(h);
-    int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    const int groups = (h + kGroup - 1) / kGroup;
+    int64_t first = (static_cast<int64_t>(blockIdx.x) * kLanesThreads + (threadIdx.x & ~31u)) / LANES;  // the warp's
+    int64_t row = first + (threadIdx.x & 31) / LANES;
     float wv[1][8];
-    load_weight(w, h, lane, 32, wv);
+    load_weight(w, h, lane, LANES, wv);
     Raw8<T> x[1], r[1];
-    if (row < rows) {
-        load_row(X + row * h, h, lane, 32, x);
-        if (R) load_row(R + row * h, h, lane, 32, r);
-    }
-    for (; row < rows; row += stride) {
-        ForwardRow<T, 1> f;
-        const float sq = f.add(x, r, R, S, row * h, h, lane, 32);
-        // the next row is on its way while this one is summed and written
-        if (row + stride < rows) {
-            load_row(X + (row + stride) * h, h, lane, 32, x);
-            if (R) load_row(R + (row + stride) * h, h, lane, 32, r);
-        }
-        f.finish(warp_sum(sq), inv_h, eps, wv, Y, Q, Qs, rstd, row, row * h, h, lane, 32);
+    auto load = [&](int64_t at) {
+        const int end = at < rows ? h : 0;
+        load_row(X + at * h, end, lane, LANES, x);
+        if (R) load_row(R + at * h, end, lane, LANES, r);
+    };
+    load(row);
+    for (; first < rows; first += stride, row += stride) {
+        const int end = row < rows ? h : 0;
+        ForwardRow<T, 1, LANES < 16 ? LANES : 16> f;
+        const float sq = f.add(x, r, R, S, row * h, end, lane, LANES);
+        load(row + stride);  // the next row is on its way while this one is summed and written
+        const float v = rstd_of(warp_sum<LANES>(sq), inv_h, eps);
+        if (lane == 0 && end) rstd[row] = v;
+        f.finish(v, wv, Y, Q, Qs + row * groups, row * h, end, lane, LANES);
     }
 }
 
 template <typename T, int VPT, bool RING>
 __global__ void __launch_bounds__(1024)
-    rmsnorm_forward_block_kernel(const T *X, const T *R, const float *__restrict__ w, int64_t rows, int h, float eps,
+    rmsnorm_forward_block_kernel(const T *X, const T *R, const float *w, int64_t rows, int h, float eps,
                                  T *S, T *Y, uint8_t *Q, float *Qs, float *__restrict__ rstd, int stages,
                                  uint32_t *err) {
     extern __shared__ __align__(128) uint8_t data[];
@@ -207,12 +220,14 @@ __global__ void __launch_bounds__(1024)
     __shared__ int abort;
     __shared__ float red[2][32];
     const int lane = threadIdx.x, lanes = blockDim.x;
+    const int groups = (h + kGroup - 1) / kGroup;
     const float inv_h = 1.0f / static_cast<float>(h);
     const int64_t stride = gridDim.x, row_bytes = static_cast<int64_t>(h) * sizeof(T);
     Ring ring{data, full, &abort, err, stages, static_cast<int>(row_bytes), R ? 2 : 1};
     int filled = 0;
+    if (RING) ring.init();
+    grid_begin();
     if (RING) {
-        ring.init();
         if (lane == 0)
             for (int64_t r = blockIdx.x; filled < stages && r < rows; ++filled, r += stride)
                 ring.fill(filled, X, R, nullptr, r * row_bytes);
@@ -233,7 +248,7 @@ __global__ void __launch_bounds__(1024)
             load_row(X + off, h, lane, lanes, x);
             if (R) load_row(R + off, h, lane, lanes, r);
         }
-        ForwardRow<T, VPT> f;
+        ForwardRow<T, VPT, 16> f;
         const float sq = f.add(x, r, R, S, off, h, lane, lanes);
         const float total = block_sum(sq, red[turn]);  // its barrier: every thread has read the stage
         if (RING) {
@@ -243,7 +258,9 @@ __global__ void __launch_bounds__(1024)
             }
             if (++stage == stages) stage = 0, phase ^= 1;
         }
-        f.finish(total, inv_h, eps, wv, Y, Q, Qs, rstd, row, off, h, lane, lanes);
+        const float v = rstd_of(total, inv_h, eps);
+        if (lane == 0) rstd[row] = v;
+        f.finish(v, wv, Y, Q, Qs + row * groups, off, h, lane, lanes);
     }
     if (RING && lane == 0) ring.leave(filled);
 }
@@ -326,55 +343,53 @@ __device__ __forceinline__ void backward_finish(float c, float rstd, const Raw8<
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(32 * kWarps)
-    rmsnorm_backward_warp_kernel(const T *dY, const T *S, const float *__restrict__ w, const float *__restrict__ rstd,
-                                 const T *dS, int64_t rows, int h, T *dX, float *__restrict__ part) {
-    __shared__ float fold[kWarps * 32 * 8];
-    const int lane = threadIdx.x & 31;
+template <typename T, int LANES>
+__global__ void __launch_bounds__(kLanesThreads, sizeof(T) == 2 ? 4 : 3)
+    rmsnorm_backward_lanes_kernel(const T *dY, const T *S, const float *w, const float *rstd, const T *dS,
+                                  int64_t rows, int h, T *dX, float *__restrict__ part) {
+    grid_begin();
+    __shared__ float fold[kLanesThreads * 8];
+    const int lane = threadIdx.x % LANES;
     const float inv_h = 1.0f / static_cast<float>(h);
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * kWarps;
-    int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    const Weights<1> wv(w, h, lane, 32);
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * (kLanesThreads / LANES);
+    int64_t first = (static_cast<int64_t>(blockIdx.x) * kLanesThreads + (threadIdx.x & ~31u)) / LANES;  // the warp's
+    int64_t row = first + (threadIdx.x & 31) / LANES;
+    const Weights<1> wv(w, h, lane, LANES);
     float dw[1][8] = {}, r = 0.0f;
     Raw8<T> y[1], x[1], d[1];
-    if (row < rows) {
-        r = __ldg(rstd + row);
-        load_row(dY + row * h, h, lane, 32, y);
-        load_row(S + row * h, h, lane, 32, x);
-        if (dS) load_row(dS + row * h, h, lane, 32, d);
-    }
-    for (; row < rows; row += stride) {
+    auto load = [&](int64_t at) {
+        const int end = at < rows ? h : 0;
+        r = end ? rstd[at] : 0.0f;
+        load_row(dY + at * h, end, lane, LANES, y);
+        load_row(S + at * h, end, lane, LANES, x);
+        if (dS) load_row(dS + at * h, end, lane, LANES, d);
+    };
+    load(row);
+    for (; first < rows; first += stride, row += stride) {
         const float now = r;
         const Raw8<T> y0[1] = {y[0]}, x0[1] = {x[0]}, d0[1] = {d[0]};
-        const int64_t next = row + stride;
-        // the next row is on its way while this one is summed and written
-        if (next < rows) {
-            r = __ldg(rstd + next);
-            load_row(dY + next * h, h, lane, 32, y);
-            load_row(S + next * h, h, lane, 32, x);
-            if (dS) load_row(dS + next * h, h, lane, 32, d);
-        }
-        const float c = warp_sum(backward_dots(y0, x0, wv, now, dw)) * inv_h;
-        backward_finish(c, now, y0, x0, wv, d0, dS, dX + row * h, h, lane, 32);
+        load(row + stride);  // the next row is on its way while this one is summed and written
+        const float c = warp_sum<LANES>(backward_dots(y0, x0, wv, now, dw)) * inv_h;
+        backward_finish(c, now, y0, x0, wv, d0, dS, dX + row * h, row < rows ? h : 0, lane, LANES);
     }
     if (!part) return;
-    // the block's warps hold the same columns: add them in warp order
+    // the block's rows hold the same columns: add them in their order
+    constexpr int kColumns = LANES * 8;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) fold[(threadIdx.x >> 5) * 256 + lane * 8 + j] = dw[0][j];
+    for (int j = 0; j < 8; ++j) fold[threadIdx.x / LANES * kColumns + lane * 8 + j] = dw[0][j];
     __syncthreads();
     const int c = threadIdx.x;  // 256 threads, up to 256 columns
     if (c < h) {
         float s = 0.0f;
 #pragma unroll
-        for (int q = 0; q < kWarps; ++q) s += fold[q * 256 + c];
+        for (int q = 0; q < kLanesThreads / LANES; ++q) s += fold[q * kColumns + c];
         part[static_cast<int64_t>(blockIdx.x) * h + c] = s;
     }
 }
 
 template <typename T, int VPT, bool RING>
 __global__ void __launch_bounds__(VPT == 4 ? 512 : 1024)
-    rmsnorm_backward_block_kernel(const T *dY, const T *S, const float *__restrict__ w, const float *__restrict__ rstd,
+    rmsnorm_backward_block_kernel(const T *dY, const T *S, const float *w, const float *rstd,
                                   const T *dS, int64_t rows, int h, T *dX, float *__restrict__ part, int stages,
                                   uint32_t *err) {
     extern __shared__ __align__(128) uint8_t data[];
@@ -385,8 +400,9 @@ __global__ void __launch_bounds__(VPT == 4 ? 512 : 1024)
     const int64_t stride = gridDim.x, row_bytes = static_cast<int64_t>(h) * sizeof(T);
     Ring ring{data, full, &abort, err, stages, static_cast<int>(row_bytes), dS ? 3 : 2};
     int filled = 0;
+    if (RING) ring.init();
+    grid_begin();
     if (RING) {
-        ring.init();
         if (lane == 0)
             for (int64_t r = blockIdx.x; filled < stages && r < rows; ++filled, r += stride)
                 ring.fill(filled, dY, S, dS, r * row_bytes);
@@ -398,7 +414,7 @@ __global__ void __launch_bounds__(VPT == 4 ? 512 : 1024)
     const int64_t step = stride * h;
     int64_t off = static_cast<int64_t>(blockIdx.x) * h;
     for (int64_t row = blockIdx.x; row < rows; row += stride, off += step, turn ^= 1) {
-        const float r = __ldg(rstd + row);
+        const float r = rstd[row];
         Raw8<T> y[VPT], x[VPT], d[VPT];
         if (RING) {
             ring.wait(stage, phase);
@@ -445,15 +461,16 @@ __global__ void __launch_bounds__(VPT == 4 ? 512 : 1024)
 
 // dw[c] = the blocks' partial sums, always in the same order: 32 columns a block,
 // each of 32 warps adding every 32nd row.
-__global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(const float *__restrict__ part, int rows, int h,
+__global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(const float *part, int rows, int h,
                                                           float *__restrict__ dw) {
     __shared__ float red[32][32];
+    grid_begin();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
     float s = 0.0f;
     if (c < h) {
 #pragma unroll 8
-        for (int r = warp; r < rows; r += 32) s += __ldg(part + static_cast<int64_t>(r) * h + c);
+        for (int r = warp; r < rows; r += 32) s += part[static_cast<int64_t>(r) * h + c];
     }
     red[warp][lane] = s;
     __syncthreads();
@@ -472,17 +489,22 @@ struct Layout {
 };
 inline Layout layout_of(int64_t h, bool backward) {
     const int v = static_cast<int>(h / 8);
-    if (warp_rows(h)) return {1, 32 * kWarps, 4};
+    if (lane_rows(h)) return {1, kLanesThreads, 4};
     const int vpt = backward ? (v <= 1024 ? 1 : 4) : (v <= 512 ? 1 : 2);
     const int threads = ((v + vpt - 1) / vpt + 31) / 32 * 32;
-        return {vpt, threads, std::min(8, (vpt == 4 ? 512 : 1024) / threads)};
+        return {vpt, threads, std::min(backward ? 8 : 16, (vpt == 4 ? 512 : 1024) / threads)};
 }
 
 // Stages of the ring where `blocks` blocks share an SM; fewer blocks where two
-// stages would not fit, 0 stages where they do not fit even then.
+// stages would not fit, 0 stages where they do not fit even then. A block of the
+// backward asks for its whole share, so that no SM takes more than `blocks` of
+// them: its rows are divided evenly, and blocks that begin while the kernel
+// before them ends would pile up on the SMs that were free first (1.6 times the
+// time at h = 512). The forward's blocks are more than have a place.
+inline int share_of(int blocks) { return kSmemPerSm / blocks - 2048; }
 inline int stages_of(int64_t stage_bytes, int &blocks) {
     for (; blocks >= 1; --blocks) {
-        const int64_t n = (kSmemPerSm / blocks - 2048) / stage_bytes;
+        const int64_t n = share_of(blocks) / stage_bytes;
         if (n >= 2) return static_cast<int>(std::min<int64_t>(n, kMaxStages));
     }
     blocks = 1;
@@ -491,7 +513,7 @@ inline int stages_of(int64_t stage_bytes, int &blocks) {
 
 // Blocks of the backward at most, and so rows of its partial sums.
 inline int64_t backward_blocks(int64_t T, int64_t h) {
-    return std::min<int64_t>(warp_rows(h) ? (T + kWarps - 1) / kWarps : T, layout_of(h, true).blocks * kSms);
+    return std::min<int64_t>(lane_rows(h) ? lane_blocks(T, h) : T, layout_of(h, true).blocks * kSms);
 }
 
 // More than 48 KB of dynamic shared memory has to be asked for, once for each
@@ -505,7 +527,7 @@ struct Fn {
         if (e != cudaSuccess || bytes <= 48 * 1024) return e;
         const uint64_t bit = uint64_t{1} << (dev & 63);
         if (done.load() & bit) return cudaSuccess;
-        e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerSm - 4096);
+        e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, share_of(1));
         if (e == cudaSuccess) done.fetch_or(bit);
         return e;
     }
@@ -528,13 +550,17 @@ tpce_status forward(const void *X, const void *R, const float *w, int64_t rows, 
     T *so = static_cast<T *>(S), *yo = static_cast<T *>(Y);
     uint8_t *q = static_cast<uint8_t *>(Q);
     KernelTimer timer("rmsnorm_forward", s);
-    if (warp_rows(h)) {
+    if (lane_rows(h)) {
         const unsigned grid = static_cast<unsigned>(
-            std::min<int64_t>((rows + kWarps - 1) / kWarps, static_cast<int64_t>(num_sms()) * L.blocks));
+            std::min<int64_t>(lane_blocks(rows, h), static_cast<int64_t>(num_sms()) * L.blocks));
         auto go = [&](auto kernel) {
-            kernel<<<grid, L.threads, 0, s>>>(x, r, w, rows, h, eps, so, yo, q, Qs, rstd);
+            return launch(kernel, grid, L.threads, 0, s, x, r, w, rows, h, eps, so, yo, q, Qs, rstd);
         };
-        go(rmsnorm_forward_warp_kernel<T>);
+        const int lanes = lanes_of(h);
+        const cudaError_t e = lanes == 8    ? go(rmsnorm_forward_lanes_kernel<T, 8>)
+                              : lanes == 16 ? go(rmsnorm_forward_lanes_kernel<T, 16>)
+                                            : go(rmsnorm_forward_lanes_kernel<T, 32>);
+        if (e != cudaSuccess) return fail_cuda(e, "rmsnorm_forward");
         return check_launch("rmsnorm_forward", s);
     }
     const int64_t stage_bytes = static_cast<int64_t>(h) * sizeof(T) * (R ? 2 : 1);
@@ -547,10 +573,9 @@ tpce_status forward(const void *X, const void *R, const float *w, int64_t rows, 
     const int smem = ring ? static_cast<int>(stage_bytes * stages) : 0;
     auto go = [&](auto k) -> cudaError_t {
         const cudaError_t e = decltype(k)::allow(smem);
-        if (e == cudaSuccess)
-            decltype(k)::fn<<<grid, L.threads, smem, s>>>(x, r, w, rows, h, eps, so, yo, q, Qs, rstd, stages,
-                                                          device_error_word());
-        return e;
+        if (e != cudaSuccess) return e;
+        return launch(decltype(k)::fn, grid, L.threads, smem, s, x, r, w, rows, h, eps, so, yo, q, Qs, rstd, stages,
+                      device_error_word());
     };
     cudaError_t e;
     if (L.vpt == 1)
@@ -571,23 +596,27 @@ tpce_status backward(const void *dY, const void *S, const float *w, const float 
     int64_t blocks = backward_blocks(rows, h);
     {
         KernelTimer timer("rmsnorm_backward", s);
-        if (warp_rows(h)) {
+        if (lane_rows(h)) {
             auto go = [&](auto kernel) {
-                kernel<<<static_cast<unsigned>(blocks), L.threads, 0, s>>>(y, x, w, rstd, d, rows, h, out, part);
+                return launch(kernel, static_cast<unsigned>(blocks), L.threads, 0, s, y, x, w, rstd, d, rows, h, out,
+                              part);
             };
-            go(rmsnorm_backward_warp_kernel<T>);
+            const int lanes = lanes_of(h);
+            const cudaError_t e = lanes == 8    ? go(rmsnorm_backward_lanes_kernel<T, 8>)
+                                  : lanes == 16 ? go(rmsnorm_backward_lanes_kernel<T, 16>)
+                                                : go(rmsnorm_backward_lanes_kernel<T, 32>);
+            if (e != cudaSuccess) return fail_cuda(e, "rmsnorm_backward");
         } else {
             const int64_t stage_bytes = static_cast<int64_t>(h) * sizeof(T) * (dS ? 3 : 2);
             const int stages = stages_of(stage_bytes, L.blocks);
             blocks = std::min<int64_t>(blocks, L.blocks * kSms);
             const bool ring = stages > 0 && rows > blocks;
-            const int smem = ring ? static_cast<int>(stage_bytes * stages) : 0;
+            const int smem = ring ? share_of(L.blocks) : 0;
             auto go = [&](auto k) -> cudaError_t {
                 const cudaError_t e = decltype(k)::allow(smem);
-                if (e == cudaSuccess)
-                    decltype(k)::fn<<<static_cast<unsigned>(blocks), L.threads, smem, s>>>(
-                        y, x, w, rstd, d, rows, h, out, part, stages, device_error_word());
-                return e;
+                if (e != cudaSuccess) return e;
+                return launch(decltype(k)::fn, static_cast<unsigned>(blocks), L.threads, smem, s, y, x, w, rstd, d,
+                              rows, h, out, part, stages, device_error_word());
             };
             cudaError_t e;
             if (L.vpt == 1)
@@ -603,7 +632,9 @@ tpce_status backward(const void *dY, const void *S, const float *w, const float 
     }
     if (!dw) return TPCE_OK;
     KernelTimer timer("rmsnorm_dw", s);
-    rmsnorm_dw_kernel<<<(h + 31) / 32, 1024, 0, s>>>(part, static_cast<int>(blocks), h, dw);
+    const cudaError_t e = launch(rmsnorm_dw_kernel, static_cast<unsigned>((h + 31) / 32), 1024, 0, s, part,
+                                 static_cast<int>(blocks), h, dw);
+    if (e != cudaSuccess) return fail_cuda(e, "rmsnorm_dw");
     return check_launch("rmsnorm_dw", s);
 }
 

@@ -132,7 +132,7 @@ __device__ __forceinline__ void add8(const Raw8<float> &a, const Raw8<float> &b,
 }
 
 __device__ __forceinline__ void load8f(const float *p, float (&v)[8]) {
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    const float4 a = *(reinterpret_cast<const float4 *>(p)), b = *(reinterpret_cast<const float4 *>(p) + 1);
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
@@ -148,23 +148,25 @@ constexpr float kE4m3Max = 448.0f;
 __device__ __forceinline__ float group_scale(float amax) { return fmaxf(__fmul_rn(amax, 1.0f / kE4m3Max), FLT_MIN); }
 
 // Codes and scale of a group whose 128 values lie in 16 adjacent lanes, eight
-// each; every lane of the warp calls it (values past an end: zeros). fmaxf
+// each (LANES: in fewer, the rest being another group's); every lane of the warp
+// calls it (values past an end: zeros). fmaxf
 // passes over NaN, whose product and code are NaN by themselves; infinities,
 // which would spoil the scale and saturate, are looked for only in a warp
 // whose maximum shows one.
+template <int LANES = 16>
 __device__ __forceinline__ uint2 quantize8(const float (&v)[8], float &scale) {
     float a = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(v[i]));
 #pragma unroll
-    for (int d = 8; d > 0; d >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
+    for (int d = LANES / 2; d > 0; d >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
     const bool infinite = __any_sync(0xffffffffu, a > FLT_MAX);
     if (infinite) {
         a = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(v[i]) <= FLT_MAX ? fabsf(v[i]) : 0.0f);
 #pragma unroll
-        for (int d = 8; d > 0; d >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
+        for (int d = LANES / 2; d > 0; d >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
     }
     scale = group_scale(a);
     const float inv = __frcp_rn(scale);
@@ -197,9 +199,11 @@ __device__ __forceinline__ void decode8(uint2 q, float scale, float (&v)[8]) {
 }
 
 // ------------------------------------------------------------------ sums
+// over groups of LANES adjacent lanes
+template <int LANES = 32>
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    for (int d = LANES / 2; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
     return x;
 }
 

@@ -29,8 +29,8 @@ GROUP = 128  # values that share one scale in the 8-bit formats
 
 BINDING_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "lib", "_step_binding.so")
 # the library's entry points that the binding calls, in its order
-_ENTRIES = ("tpce_rmsnorm_workspace_bytes", "tp_rmsnorm_forward", "tp_rmsnorm_backward", "tp_expert_plan",
-            "tp_expert_dispatch_forward", "tp_expert_dispatch_backward", "tp_expert_combine_forward",
+_ENTRIES = ("tpce_rmsnorm_workspace_bytes", "tp_rmsnorm_forward", "tp_rmsnorm_backward",
+            "tpce_expert_plan_workspace_bytes", "tp_expert_plan", "tp_expert_dispatch_forward", "tp_expert_dispatch_backward", "tp_expert_combine_forward",
             "tp_expert_combine_backward", "tp_adamw_step")
 _lock = threading.Lock()
 _binding = None
@@ -107,14 +107,18 @@ def tp_rmsnorm_backward(dY: torch.Tensor, S: torch.Tensor, w: torch.Tensor, rstd
 
 
 # ---------------------------------------------------------------------- experts
+def expert_plan_workspace_bytes(T: int, k: int, experts: int) -> int:
+    return int(lib().tpce_expert_plan_workspace_bytes(T, k, experts))
+
+
 def tp_expert_plan(ids: torch.Tensor, experts: int, out: Optional[Dict[str, torch.Tensor]] = None,
-                   stream=None) -> Dict[str, torch.Tensor]:
+                   ws: Optional[torch.Tensor] = None, stream=None) -> Dict[str, torch.Tensor]:
     """The stable sort of the assignments ids [T, k] (int32, -1: dropped) by
     expert: row [T, k], source [T k], offsets [experts + 1], all int32."""
     if stream is not None:
-        with _on(stream, ids, out):
-            return _b().expert_plan(ids, experts, out)
-    return _b().expert_plan(ids, experts, out)
+        with _on(stream, ids, out, ws):
+            return _b().expert_plan(ids, experts, out, ws)
+    return _b().expert_plan(ids, experts, out, ws)
 
 
 def tp_expert_dispatch_forward(X: torch.Tensor, plan: Dict[str, torch.Tensor], out: Optional[torch.Tensor] = None,
