@@ -5,9 +5,10 @@ against the formula and against differences. Bounds: _step_ref.
 
 Chains: a thread adds up to 32 squares one after the other, then 5 + 5 steps
 over the warp and the block, so 45 roundings at most; 64 allows for the mean,
-the root and the products as well. dw: a block adds T / 304 rows one after the
-other (T / 304 / 8 a warp), then its warps and the 304 partial rows in chains
-of 38 and 8.
+the root and the products as well. dw: at least 152 blocks share the rows (or
+each has one), so a block adds T / 152 of them one after the other at most;
+then up to 32 of a block's rows and the blocks' partial rows, in chains of 32,
+38 and 32.
 """
 
 import pytest
@@ -21,8 +22,8 @@ pytestmark = pytest.mark.gpu
 EPS = 1e-6
 C = 64 * E32
 TYPES = [torch.bfloat16, torch.float32]
-# one row, rows of less than a group, a group's edge, warp rows of 1, 2 and 4 vectors a lane, the first
-# block rows, 1, 2 and 4 vectors a thread, the widest
+# one row, rows of 8, 16 and 32 lanes and a block's first ones, a group's edge, 1, 2 and 4 vectors a thread, with
+# and without more rows than blocks, the widest
 SHAPES = [(1, 8), (3, 64), (1000, 120), (5, 128), (9, 136), (17, 256), (700, 264), (33, 512), (4, 1000), (65, 1024),
           (1, 1032), (641, 1032), (7, 2048), (3, 4096), (2, 4104), (611, 8192), (5, 8200), (3, 16384), (306, 16376)]
 
