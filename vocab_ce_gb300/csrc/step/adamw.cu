@@ -79,14 +79,30 @@ struct Rates {
     float step_size, root_scale, grad_scale, decay;
 };
 
-__device__ __forceinline__ void update(const Scalars &k, const Rates &c, float grad, float &p, float &m, float &v,
-                                       float &r) {
-    const float g = __fmul_rn(grad, c.grad_scale);
-    m = __fadd_rn(__fmul_rn(m, k.b1), __fmul_rn(g, k.one_b1));
-    v = __fadd_rn(__fmul_rn(v, k.b2), __fmul_rn(__fmul_rn(g, g), k.one_b2));
-    r = __fsqrt_rn(v);
-    const float u = __fdiv_rn(m, __fadd_rn(__fmul_rn(r, c.root_scale), k.eps));
-    p = __fsub_rn(__fmul_rn(p, c.decay), __fmul_rn(u, c.step_size));
+// Two values' step; r becomes the root of the new v.
+__device__ __forceinline__ void update2(const Scalars &k, const Rates &c, const float *grad, float *p, float *m,
+                                        float *v, float *r) {
+    float g0 = grad[0], g1 = grad[1];
+    mul2(g0, g1, c.grad_scale, c.grad_scale);
+    float s0 = g0, s1 = g1;
+    mul2(m[0], m[1], k.b1, k.b1);
+    mul2(s0, s1, k.one_b1, k.one_b1);
+    m[0] = __fadd_rn(m[0], s0);
+    m[1] = __fadd_rn(m[1], s1);
+    mul2(g0, g1, g0, g1);
+    mul2(v[0], v[1], k.b2, k.b2);
+    mul2(g0, g1, k.one_b2, k.one_b2);
+    v[0] = __fadd_rn(v[0], g0);
+    v[1] = __fadd_rn(v[1], g1);
+    r[0] = __fsqrt_rn(v[0]);
+    r[1] = __fsqrt_rn(v[1]);
+    float d0 = r[0], d1 = r[1];
+    mul2(d0, d1, c.root_scale, c.root_scale);
+    float u0 = __fdiv_rn(m[0], __fadd_rn(d0, k.eps)), u1 = __fdiv_rn(m[1], __fadd_rn(d1, k.eps));
+    mul2(u0, u1, c.step_size, c.step_size);
+    mul2(p[0], p[1], c.decay, c.decay);
+    p[0] = __fsub_rn(p[0], u0);
+    p[1] = __fsub_rn(p[1], u1);
 }
 
 // Eight values from i on as they lie in memory; those from n on are zeros, and
@@ -176,7 +192,7 @@ struct Inputs<P, G, true> {
         decode8(m, ms, mm);
         decode8(r, rs, vv);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) vv[j] = __fmul_rn(vv[j], vv[j]);
+        for (int j = 0; j < 8; j += 2) mul2(vv[j], vv[j + 1], vv[j], vv[j + 1]);
     }
 };
 
@@ -198,7 +214,7 @@ __device__ __forceinline__ void run(const Scalars &k, const Rates &c, const Entr
         unpack8(in.g, g);
         in.moments(m, v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) update(k, c, g[j], p[j], m[j], v[j], r[j]);
+        for (int j = 0; j < 8; j += 2) update2(k, c, g + j, p + j, m + j, v + j, r + j);
         if (S8) {
             // values past the end have no gradient and no moments: they stay zero and leave the scale alone
             float ms, rs;

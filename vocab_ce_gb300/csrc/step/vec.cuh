@@ -96,7 +96,9 @@ __device__ __forceinline__ void forget(Raw8<float> &r) {
 }
 
 // (x, y) *= (a, b) and (x, y) += (a, b) * (c, d), two values an instruction; each
-// is rounded as by the single form.
+// is rounded as by the single form. (A paired product and a paired sum after it
+// were fused to one rounding, whatever their rounding modes say: where both
+// roundings count, the sum is a single one.)
 __device__ __forceinline__ void mul2(float &x, float &y, float a, float b) {
     asm("{\n\t.reg .b64 p, q;\n\t"
         "mov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
@@ -193,8 +195,9 @@ __device__ __forceinline__ void decode8(uint2 q, float scale, float (&v)[8]) {
     for (int i = 0; i < 4; ++i) {
         const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[i]), __NV_E4M3);
         const float2 f = __half22float2(__half2(h));
-        v[2 * i] = __fmul_rn(f.x, scale);
-        v[2 * i + 1] = __fmul_rn(f.y, scale);
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+        mul2(v[2 * i], v[2 * i + 1], scale, scale);
     }
 }
 
