@@ -300,7 +300,7 @@ struct Weights {
 template <typename T, int VPT>
 __device__ __forceinline__ float backward_dots(const Raw8<T> (&y)[VPT], const Raw8<T> (&x)[VPT],
                                                const Weights<VPT> &weights, float rstd, float (&dw)[VPT][8]) {
-    float c = 0.0f;
+    float c0 = 0.0f, c1 = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         float g[8], xh[8], w[8];
@@ -308,13 +308,14 @@ __device__ __forceinline__ float backward_dots(const Raw8<T> (&y)[VPT], const Ra
         unpack8(y[i], g);
         unpack8(x[i], xh);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            xh[j] *= rstd;
-            dw[i][j] += g[j] * xh[j];
-            c += g[j] * w[j] * xh[j];
+        for (int j = 0; j < 8; j += 2) {
+            mul2(xh[j], xh[j + 1], rstd, rstd);
+            fma2(dw[i][j], dw[i][j + 1], g[j], g[j + 1], xh[j], xh[j + 1]);
+            mul2(g[j], g[j + 1], w[j], w[j + 1]);
+            fma2(c0, c1, g[j], g[j + 1], xh[j], xh[j + 1]);
         }
     }
-    return c;
+    return c0 + c1;
 }
 
 // c = sum g xh / h; to dX, whose row begins there
@@ -330,7 +331,12 @@ __device__ __forceinline__ void backward_finish(float c, float rstd, const Raw8<
         unpack8(y[i], g);
         unpack8(x[i], xh);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] = (g[j] * w[j] - xh[j] * rstd * c) * rstd;
+        for (int j = 0; j < 8; j += 2) {
+            mul2(xh[j], xh[j + 1], rstd, rstd);
+            mul2(g[j], g[j + 1], w[j], w[j + 1]);
+            mul2(g[j], g[j + 1], rstd, rstd);
+            fma2(g[j], g[j + 1], xh[j], xh[j + 1], -c * rstd, -c * rstd);
+        }
         if (residual) {
             float b[8];
             unpack8(d[i], b);
