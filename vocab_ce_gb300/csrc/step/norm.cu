@@ -385,11 +385,12 @@ __global__ void __launch_bounds__(kLanesThreads, 4)
     int64_t row = first + (threadIdx.x & 31) / LANES;
     Weights<1> wv(w, h, lane, LANES);
     float dw[1][8] = {};
-    // [stage][tensor][16-byte piece][thread], then the statistic: [thread]
+    // [stage][tensor][thread][16-byte piece], then the statistic: [thread]
     constexpr int kPieces = sizeof(T) / 2, kStage = lanes_stage_bytes<T>();
     const int warp = threadIdx.x & ~31, of_warp = threadIdx.x & 31;
     auto slot = [&](int stage, int i, int thread) {
-        return reinterpret_cast<uint4 *>(data + stage * kStage + (i * kLanesThreads + thread) * 16);
+        const int tensor = i / kPieces, piece = i % kPieces;
+        return reinterpret_cast<uint4 *>(data + stage * kStage + ((tensor * kLanesThreads + thread) * kPieces + piece) * 16);
     };
     auto statistic = [&](int stage) {
         return reinterpret_cast<float *>(data + stage * kStage + 3 * kPieces * kLanesThreads * 16) + threadIdx.x;
