@@ -15,6 +15,13 @@
 // operations in the order above: an 8-bit state rounds next to a border the
 // same way everywhere.
 //
+// Bound by HBM: 134 million bf16 weights with fp32 masters and bf16 gradients
+// take 538 us with 32-bit states (28 bytes a value, 7.0 TB/s, a little above the
+// copy rate, as reads and writes meet the same lines) and 335 us with 8-bit ones
+// (16.1 bytes, 6.5 TB/s, 95% of the copy rate). There the arithmetic, some 60
+// instructions a value, takes two thirds of the time that the bytes take, so it
+// is done beside the next chunk's loads (448 us without) and products in pairs.
+//
 // A parameter is fp32, or bf16, or bf16 with an fp32 master copy (then the
 // master is read and written, and the bf16 weight only written, rounded from
 // it). The tensors' addresses travel in the kernel's parameters: no table is

