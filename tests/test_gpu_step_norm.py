@@ -232,3 +232,14 @@ def test_captured_into_a_graph():
         for k, v in {**ref, **refb}.items():
             mine = {**out, **back}[k]
             assert torch.equal(mine.view(torch.uint8), v.view(torch.uint8)), k
+
+
+def test_an_output_that_does_not_fit_is_torchs_own_error():
+    # copies of 512 GiB, more than the device has: torch's error, which a program may catch and go on
+    gpu_or_skip()
+    ids = torch.zeros(1 << 20, 32, dtype=torch.int32, device="cuda")
+    plan = {"row": ids, "offsets": torch.zeros(2, dtype=torch.int32, device="cuda")}
+    big = torch.zeros(1 << 20, 8192, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(torch.OutOfMemoryError):
+        tp.tp_expert_dispatch_forward(big, plan)
+    assert tp.tp_rmsnorm_forward(big[:2], weight(8192))["Y"].shape == (2, 8192)

@@ -13,9 +13,9 @@
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <c10/util/Exception.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include <initializer_list>
 #include <algorithm>
 #include <cstring>
 #include <string>
@@ -42,7 +42,8 @@ struct Api {
     decltype(&tp_adamw_step) adamw_step;
 };
 Api api;
-PyObject *check_status;  // Python's check(status, name): raises for a failure
+PyObject *check_status;   // Python's check(status, name): raises for a failure
+PyObject *out_of_memory;  // torch.OutOfMemoryError
 
 // ------------------------------------------------------------------ errors
 // A refused argument: a ValueError with this text. Raised: Python's error is set.
@@ -444,7 +445,7 @@ PyObject *adamw_step(PyObject *const *a) {
 }
 
 // ------------------------------------------------------------------ the module
-// Nothing is thrown into Python: refusals are ValueErrors, torch's own errors RuntimeErrors.
+// Nothing is thrown into Python: refusals are ValueErrors; torch's own errors are what torch makes of them.
 template <PyObject *(*F)(PyObject *const *), int N>
 PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (n != N) {
@@ -456,22 +457,24 @@ PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t n) {
     } catch (const Refused &e) {
         PyErr_SetString(PyExc_ValueError, e.text.c_str());
     } catch (const Raised &) {
+    } catch (const c10::OutOfMemoryError &e) {
+        PyErr_SetString(out_of_memory, e.what_without_backtrace());
     } catch (const std::exception &e) {
         PyErr_SetString(PyExc_RuntimeError, e.what());
     }
     return nullptr;
 }
 
-// init(check, addresses of Api's members in their order)
+// init(check, torch.OutOfMemoryError, addresses of Api's members in their order)
 PyObject *init(PyObject *, PyObject *const *args, Py_ssize_t n) {
     constexpr Py_ssize_t kMembers = sizeof(Api) / sizeof(void *);
-    if (n != kMembers + 1) {
-        PyErr_SetString(PyExc_TypeError, "init: the status check and every entry point expected");
+    if (n != kMembers + 2) {
+        PyErr_SetString(PyExc_TypeError, "init: the status check, the error and every entry point expected");
         return nullptr;
     }
     void *at[kMembers];
     for (Py_ssize_t i = 0; i < kMembers; ++i) {
-        at[i] = PyLong_AsVoidPtr(args[i + 1]);
+        at[i] = PyLong_AsVoidPtr(args[i + 2]);
         if (!at[i]) {
             if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "init: a null entry point");
             return nullptr;
@@ -480,6 +483,8 @@ PyObject *init(PyObject *, PyObject *const *args, Py_ssize_t n) {
     memcpy(&api, at, sizeof(api));
     Py_INCREF(args[0]);
     Py_XSETREF(check_status, args[0]);
+    Py_INCREF(args[1]);
+    Py_XSETREF(out_of_memory, args[1]);
     Py_RETURN_NONE;
 }
 

@@ -163,7 +163,7 @@ struct ForwardRow {
             if (Y && c < h) {
                 Raw8<T> o;
                 pack8(s[i], o);
-                stream8(Y + off + c, o);
+                store8(Y + off + c, o);
             }
             if (Q) {
                 // lanes past the row's end bring zeros
@@ -174,7 +174,7 @@ struct ForwardRow {
                 float scale;
                 const uint2 q = quantize8<GROUP_LANES>(s[i], scale);
                 if (c < h) {
-                    __stcs(reinterpret_cast<uint2 *>(Q + off + c), q);
+                    *reinterpret_cast<uint2 *>(Q + off + c) = q;
                     if (lane % GROUP_LANES == 0) Qs[c / kGroup] = scale;
                 }
             }
@@ -223,7 +223,8 @@ __global__ void __launch_bounds__(kLanesThreads, 4)
 // of 8192 takes 7 us a call, the host's part; 16,384 x 8192 bf16 with the
 // residual 157 us, 6.8 TB/s, as fast as a copy; 4096 of them with the 8-bit
 // output 50 us, 6.0 TB/s (what is lost is the start and the end of the launch).
-// Loads and stores are marked to leave L2 first (57 us without, for the last).
+// What is read once and S, which waits for the end of the block, are marked to
+// leave L2 first (57 us without, for the last); Y is what the next product reads.
 template <typename T, int VPT, bool RING>
 __global__ void __launch_bounds__(1024)
     rmsnorm_forward_block_kernel(const T *X, const T *R, const float *w, int64_t rows, int h, float eps,

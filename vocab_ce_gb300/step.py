@@ -52,7 +52,8 @@ def _load():
             module = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(module)
             library = lib()
-            module.init(check, *(ctypes.cast(getattr(library, name), ctypes.c_void_p).value for name in _ENTRIES))
+            module.init(check, torch.OutOfMemoryError,
+                        *(ctypes.cast(getattr(library, name), ctypes.c_void_p).value for name in _ENTRIES))
             _binding = module
     return _binding
 
