@@ -10,7 +10,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <c10/util/Exception.h>
@@ -19,7 +19,7 @@
 #include <algorithm>
 #include <cstring>
 #include <string>
-#include <unordered_set>
+#include <utility>
 #include <vector>
 
 #include "tpce.h"
@@ -124,8 +124,9 @@ float *fptr(const at::Tensor &x) { return static_cast<float *>(ptr(x)); }
 int32_t *iptr(const at::Tensor &x) { return static_cast<int32_t *>(ptr(x)); }
 void *stream() { return c10::cuda::getCurrentCUDAStream().stream(); }
 
+// torch's allocation without its dispatch (0.3 us of 1.1 a tensor): `like` is known to be a CUDA tensor
 at::Tensor empty(at::IntArrayRef shape, at::ScalarType dtype, const at::Tensor &like) {
-    return at::empty(shape, like.options().dtype(dtype).requires_grad(false));
+    return at::detail::empty_cuda(shape, dtype, like.device(), std::nullopt);
 }
 
 // The caller's output, checked, or a new one.
@@ -388,7 +389,6 @@ PyObject *adamw_step(PyObject *const *a) {
     const double wd = one ? number(a[4]) : 0.0;
 
     std::vector<tpce_adamw_tensor> t(static_cast<size_t>(n));
-    std::unordered_set<void *> seen;
     const int dev = n && THPVariable_Check(params[0]) && THPVariable_Unpack(params[0]).is_cuda()
                         ? c10::cuda::current_device() : -1;
     // names are put together only for a message
@@ -430,8 +430,15 @@ PyObject *adamw_step(PyObject *const *a) {
             e.v_scale = static_cast<float *>(take(keys->r_scale.of(st), "r_scale", i, at::kFloat, few));
         }
         e.weight_decay = one ? wd : number(decay[i]);
-        if (e.n && !seen.insert(e.p).second) throw Refused{place("params", i) + " is in the list twice"};
     }
+    // no value may be updated twice: the tensors' addresses in order
+    std::vector<std::pair<void *, Py_ssize_t>> order;
+    order.reserve(t.size());
+    for (Py_ssize_t i = 0; i < n; ++i)
+        if (t[static_cast<size_t>(i)].n) order.emplace_back(t[static_cast<size_t>(i)].p, i);
+    std::sort(order.begin(), order.end());
+    for (size_t i = 1; i < order.size(); ++i)
+        if (order[i].first == order[i - 1].first) throw Refused{place("params", order[i].second) + " is in the list twice"};
     const float *scalars = nullptr;
     if (!none(a[11])) {
         const at::Tensor &x = tensor(a[11], "scalars");
