@@ -83,6 +83,38 @@ def test_backward(T, h, dtype, residual):
     assert "dw" not in alone and torch.equal(alone["dX"], got["dX"])
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,h", [(1, 8208), (75, 16384), (77, 8200), (152, 8208), (380, 12288), (1003, 8200), (1003, 16384)])
+@pytest.mark.parametrize("residual", [False, True])
+def test_backward_of_rows_that_two_blocks_share(T, h, dtype, residual):
+    # 76 pairs of blocks: fewer rows than pairs, as many as the ring's stages, many times those; halves of different
+    # lengths. A pair adds T / 76 rows to dw one after the other. In place, on a stream of its own, and a row
+    # that holds an infinity beside rows that do not.
+    gpu_or_skip()
+    S, dY, w = rows(T, h, dtype, 3), rows(T, h, dtype, 4), weight(h)
+    dS = rows(T, h, dtype, 5) if residual else None
+    rstd = norm_forward(S, w, EPS)[1].float()
+    got = tp.tp_rmsnorm_backward(dY, S, w, rstd, dS)
+    dX, dw = norm_backward(dY, S, w, EPS, dS)
+    r, g = rstd.to(D)[:, None], (dY.to(D) * w.to(D)).abs()
+    xh = S.to(D).abs() * r
+    size = r * (g + xh * (g * xh).mean(-1, keepdim=True)) + (0 if dS is None else dS.to(D).abs())
+    near(got["dX"], dX, U[dtype] * dX.abs() + 2 * C * size, "dX")
+    near(got["dw"], dw, (128 + T / 76) * E32 * (dY.to(D).abs() * xh).sum(0), "dw")
+    a = [dY.clone()] + ([dS.clone()] if residual else [])
+    side = torch.cuda.Stream()
+    for into in a:
+        side.wait_stream(torch.cuda.current_stream())
+        again = tp.tp_rmsnorm_backward(a[0], S, w, rstd, a[1] if residual else None, out={"dX": into}, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(into, got["dX"]) and torch.equal(again["dw"], got["dw"])
+        a[0].copy_(dY)
+    last = dY.clone()
+    last[T - 1, h - 1] = float("inf")
+    odd = tp.tp_rmsnorm_backward(last, S, w, rstd, dS, want_dw=False)["dX"]
+    assert torch.equal(odd[:T - 1], got["dX"][:T - 1]) and not bool(odd[T - 1].isfinite().any())
+
+
 def test_gradient_against_differences():
     # f = sum dY Y over the plain 64-bit forward; central differences in 64 bits with step 1e-5 are off by
     # about 1e-10 of f's third derivative, far below the kernel's own fp32 error

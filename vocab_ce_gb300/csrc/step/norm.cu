@@ -28,11 +28,11 @@ namespace {
 
 using namespace step;
 
-constexpr int64_t kMaxWidth = 16384;  // 2 vectors of 8 values for each of 1024 threads, 4 for each of 512
+constexpr int64_t kMaxWidth = 16384;  // 2 vectors of 8 values for each of 1024 threads
 constexpr int64_t kMaxRows = int64_t{1} << 40;
 constexpr int kLanesThreads = 256;    // of a block where a row is some lanes of a warp
 constexpr int64_t kSms = 152;         // fixed, so that the workspace's size is known on the host
-constexpr int kMaxStages = 4;
+constexpr int kMaxStages = 4, kPairStages = 6;
 // Rows of a block of the forward, where there are enough. Blocks that take all
 // their rows from one launch to the end wait for the SM that gets its bytes last:
 // 8192 x 8192 bf16 took 95 us with one round of blocks, 87 with four; with three
@@ -46,33 +46,36 @@ constexpr int kSmemPerSm = 228 * 1024;
 // at h = 64 a whole warp a row took 86 and 87 us for 262,144 fp32 rows, 8 lanes
 // 51 and 46.
 inline bool lane_rows(int64_t h) { return h <= 256; }
+inline bool pair_rows(int64_t h) { return h > 8192; }  // in the backward
 inline int lanes_of(int64_t h) { return h <= 64 ? 8 : h <= 128 ? 16 : 32; }
 inline int64_t lane_blocks(int64_t rows, int64_t h) {
     const int64_t of_block = kLanesThreads / lanes_of(h);
     return (rows + of_block - 1) / of_block;
 }
 
-// The vectors of a row that are this thread's; zeros past the row's end.
+// Eight columns from c on; zeros past the row's end.
+template <typename T>
+__device__ __forceinline__ void load_vector(const T *x, int c, int h, Raw8<T> &v) {
+    if (c < h)
+        v = load8(x + c);
+    else
+        zero8(v);
+}
+__device__ __forceinline__ void load_weights(const float *w, int c, int h, float (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+    if (c < h) load8f(w + c, v);
+}
+// The vectors of a row that are this thread's.
 template <typename T, int VPT>
 __device__ __forceinline__ void load_row(const T *x, int h, int lane, int lanes, Raw8<T> (&v)[VPT]) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int c = (lane + i * lanes) * 8;
-        if (c < h)
-            v[i] = load8(x + c);
-        else
-            zero8(v[i]);
-    }
+    for (int i = 0; i < VPT; ++i) load_vector(x, (lane + i * lanes) * 8, h, v[i]);
 }
 template <int VPT>
-__device__ __forceinline__ void load_weight(const float *w, int h, int lane, int lanes, float (&v)[VPT][8]) {
+__device__ __forceinline__ void load_row_weights(const float *w, int h, int lane, int lanes, float (&v)[VPT][8]) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int c = (lane + i * lanes) * 8;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
-        if (c < h) load8f(w + c, v[i]);
-    }
+    for (int i = 0; i < VPT; ++i) load_weights(w, (lane + i * lanes) * 8, h, v[i]);
 }
 
 // ------------------------------------------------------------------ the ring
@@ -116,9 +119,9 @@ struct Ring {
     }
     __device__ void wait(int stage, int phase) { ptx::mbar_wait(full + stage, phase, abort, err, 20u); }
     // thread 0 only, after the last row: `filled` fills in all
-    __device__ void leave(int filled) {
+    __device__ void leave(int64_t filled) {
         if (!*abort) return;
-        for (int n = filled > stages ? filled - stages : 0; n < filled; ++n)
+        for (int64_t n = filled > stages ? filled - stages : 0; n < filled; ++n)
             ptx::mbar_wait_drain(full + n % stages, (n / stages) & 1);
     }
 };
@@ -199,7 +202,7 @@ __global__ void __launch_bounds__(kLanesThreads, 4)
     int64_t first = (static_cast<int64_t>(blockIdx.x) * kLanesThreads + (threadIdx.x & ~31u)) / LANES;  // the warp's
     int64_t row = first + (threadIdx.x & 31) / LANES;
     float wv[1][8];
-    load_weight(w, h, lane, LANES, wv);
+    load_row_weights(w, h, lane, LANES, wv);
     Raw8<T> x[1], r[1];
     auto load = [&](int64_t at) {
         const int end = at < rows ? h : 0;
@@ -248,7 +251,7 @@ __global__ void __launch_bounds__(1024)
                 ring.fill(filled, X, R, nullptr, r * row_bytes);
     }
     float wv[VPT][8];
-    load_weight(w, h, lane, lanes, wv);
+    load_row_weights(w, h, lane, lanes, wv);
     int stage = 0, phase = 0, turn = 0;
     const int64_t step = stride * h;
     int64_t off = static_cast<int64_t>(blockIdx.x) * h;
@@ -281,87 +284,54 @@ __global__ void __launch_bounds__(1024)
 }
 
 // ------------------------------------------------------------------ backward
-// A thread's weights: with one vector they stay in registers, with more they are
-// read again for each vector (the registers hold the sums of dw).
-template <int VPT>
-struct Weights {
-    const float *w;
-    int h, lane, lanes;
-    float held[8];
-    __device__ __forceinline__ Weights(const float *w_, int h_, int lane_, int lanes_)
-        : w(w_), h(h_), lane(lane_), lanes(lanes_) {
-        if (VPT == 1) read(w, 0, held);
-    }
-    __device__ __forceinline__ void read(const float *from, int i, float (&v)[8]) const {
-        const int c = (lane + i * lanes) * 8;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-        if (c < h) load8f(from + c, v);
-    }
-    __device__ __forceinline__ void get(int i, float (&v)[8]) const {
-        if (VPT == 1) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = held[j];
-        } else {
-            // the compiler, which would keep what it has read before, does not know the pointer again
-            const float *again = w;
-            asm volatile("" : "+l"(again));
-            read(again, i, v);
-        }
-    }
-};
-
 // dY xh goes to dw; returns this thread's part of sum g xh.
-template <typename T, int VPT>
-__device__ __forceinline__ float backward_dots(const Raw8<T> (&y)[VPT], const Raw8<T> (&x)[VPT],
-                                               const Weights<VPT> &weights, float rstd, float (&dw)[VPT][8]) {
+template <typename T>
+__device__ __forceinline__ float backward_dots(const Raw8<T> &y, const Raw8<T> &x, const float (&w)[8], float rstd,
+                                               float (&dw)[8]) {
     float c0 = 0.0f, c1 = 0.0f;
+    float g[8], xh[8];
+    unpack8(y, g);
+    unpack8(x, xh);
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        float g[8], xh[8], w[8];
-        weights.get(i, w);
-        unpack8(y[i], g);
-        unpack8(x[i], xh);
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            mul2(xh[j], xh[j + 1], rstd, rstd);
-            fma2(dw[i][j], dw[i][j + 1], g[j], g[j + 1], xh[j], xh[j + 1]);
-            mul2(g[j], g[j + 1], w[j], w[j + 1]);
-            fma2(c0, c1, g[j], g[j + 1], xh[j], xh[j + 1]);
-        }
+    for (int j = 0; j < 8; j += 2) {
+        mul2(xh[j], xh[j + 1], rstd, rstd);
+        fma2(dw[j], dw[j + 1], g[j], g[j + 1], xh[j], xh[j + 1]);
+        mul2(g[j], g[j + 1], w[j], w[j + 1]);
+        fma2(c0, c1, g[j], g[j + 1], xh[j], xh[j + 1]);
     }
     return c0 + c1;
 }
 
-// c = sum g xh / h; to dX, whose row begins there
-template <typename T, int VPT>
-__device__ __forceinline__ void backward_finish(float c, float rstd, const Raw8<T> (&y)[VPT], const Raw8<T> (&x)[VPT],
-                                                const Weights<VPT> &weights, const Raw8<T> (&d)[VPT], bool residual,
-                                                T *dX, int h, int lane, int lanes) {
+// c = sum g xh / h; to dX where the columns are inside
+template <typename T>
+__device__ __forceinline__ void backward_finish(float c, float rstd, const Raw8<T> &y, const Raw8<T> &x,
+                                                const float (&w)[8], const Raw8<T> &d, bool residual, T *dX,
+                                                bool inside) {
+    float g[8], xh[8];
+    unpack8(y, g);
+    unpack8(x, xh);
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int col = (lane + i * lanes) * 8;
-        float g[8], xh[8], w[8];
-        weights.get(i, w);
-        unpack8(y[i], g);
-        unpack8(x[i], xh);
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            mul2(xh[j], xh[j + 1], rstd, rstd);
-            mul2(g[j], g[j + 1], w[j], w[j + 1]);
-            mul2(g[j], g[j + 1], rstd, rstd);
-            fma2(g[j], g[j + 1], xh[j], xh[j + 1], -c * rstd, -c * rstd);
-        }
-        if (residual) {
-            float b[8];
-            unpack8(d[i], b);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) g[j] += b[j];
-        }
-        Raw8<T> out;
-        pack8(g, out);
-        if (col < h) stream8(dX + col, out);
+    for (int j = 0; j < 8; j += 2) {
+        mul2(xh[j], xh[j + 1], rstd, rstd);
+        mul2(g[j], g[j + 1], w[j], w[j + 1]);
+        mul2(g[j], g[j + 1], rstd, rstd);
+        fma2(g[j], g[j + 1], xh[j], xh[j + 1], -c * rstd, -c * rstd);
     }
+    if (residual) {
+        float b[8];
+        unpack8(d, b);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[j] += b[j];
+    }
+    Raw8<T> out;
+    pack8(g, out);
+    if (inside) stream8(dX, out);
+}
+
+__device__ __forceinline__ void store_partial(float *part, const float (&dw)[8]) {
+    float4 *o = reinterpret_cast<float4 *>(part);
+    o[0] = make_float4(dw[0], dw[1], dw[2], dw[3]);
+    o[1] = make_float4(dw[4], dw[5], dw[6], dw[7]);
 }
 
 // Narrow rows. The values of the rows ahead are a warp's own in shared memory, so
@@ -398,8 +368,8 @@ __global__ void __launch_bounds__(kLanesThreads, 4)
     const int64_t stride = static_cast<int64_t>(gridDim.x) * (kLanesThreads / LANES);
     int64_t first = (static_cast<int64_t>(blockIdx.x) * kLanesThreads + (threadIdx.x & ~31u)) / LANES;  // the warp's
     int64_t row = first + (threadIdx.x & 31) / LANES;
-    Weights<1> wv(w, h, lane, LANES);
-    float dw[1][8] = {};
+    float wv[8], dw[8] = {};
+    load_weights(w, lane * 8, h, wv);
     // [stage][tensor][thread][16-byte piece], then the statistic: [thread]
     constexpr int kPieces = sizeof(T) / 2, kStage = lanes_stage_bytes<T>();
     const int warp = threadIdx.x & ~31, of_warp = threadIdx.x & 31;
@@ -438,13 +408,13 @@ __global__ void __launch_bounds__(kLanesThreads, 4)
     for (; first < rows; first += stride, row += stride) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kAhead<T> - 1) : "memory");
         __syncwarp();
-        Raw8<T> y[1], x[1], d[1];
-        take(stage, 0, y[0]);
-        take(stage, 1, x[0]);
-        if (dS) take(stage, 2, d[0]);
+        Raw8<T> y, x, d;
+        take(stage, 0, y);
+        take(stage, 1, x);
+        if (dS) take(stage, 2, d);
         const float r = *statistic(stage);
         const float c = warp_sum<LANES>(backward_dots(y, x, wv, r, dw)) * inv_h;
-        backward_finish(c, r, y, x, wv, d, dS, dX + row * h, row < rows ? h : 0, lane, LANES);
+        backward_finish(c, r, y, x, wv, d, dS, dX + row * h + lane * 8, row < rows && lane * 8 < h);
         __syncwarp();  // every lane has read the stage
         fill(stage, first + kAhead<T> * stride);
         if (++stage == kAhead<T>) stage = 0;
@@ -456,7 +426,7 @@ __global__ void __launch_bounds__(kLanesThreads, 4)
     float *fold = reinterpret_cast<float *>(data);  // 8 KB: less than a stage, and no copy is under way
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) fold[threadIdx.x / LANES * kColumns + lane * 8 + j] = dw[0][j];
+    for (int j = 0; j < 8; ++j) fold[threadIdx.x / LANES * kColumns + lane * 8 + j] = dw[j];
     __syncthreads();
     const int c = threadIdx.x;  // 256 threads, up to 256 columns
     if (c < h) {
@@ -467,15 +437,14 @@ __global__ void __launch_bounds__(kLanesThreads, 4)
     }
 }
 
-// A row a block, the sums of dw in its registers over all its rows, so the blocks
-// are as many as have a place and their rows are divided evenly. 16,384 x 8192
-// bf16 with the residual path: 158 us with the sum of the blocks' dw, 6.8 TB/s,
-// as fast as a copy; 8192 x 4096 44 us, 6.0 TB/s; 65,536 x 512 50 us, 5.4 TB/s,
-// where every row's sum costs its two warps as much as its values. Rows of more
-// than 8192 values need four vectors a thread, whose sums leave no registers for
-// the weights: 4096 x 16384 121 us, 4.4 TB/s, bound by reading them from L2.
-template <typename T, int VPT, bool RING>
-__global__ void __launch_bounds__(VPT == 4 ? 512 : 1024)
+// A row a block, eight columns a thread and the sums of their dw in its registers
+// over all its rows, so the blocks are as many as have a place and their rows are
+// divided evenly. 16,384 x 8192 bf16 with the residual path: 158 us with the sum
+// of the blocks' dw, 6.8 TB/s, as fast as a copy; 8192 x 4096 44 us, 6.0 TB/s;
+// 65,536 x 512 50 us, 5.4 TB/s, where every row's sum costs its two warps as much
+// as its values.
+template <typename T, bool RING>
+__global__ void __launch_bounds__(1024)
     rmsnorm_backward_block_kernel(const T *dY, const T *S, const float *w, const float *rstd,
                                   const T *dS, int64_t rows, int h, T *dX, float *__restrict__ part, int stages,
                                   uint32_t *err) {
@@ -483,67 +452,178 @@ __global__ void __launch_bounds__(VPT == 4 ? 512 : 1024)
     __shared__ uint64_t full[kMaxStages];
     __shared__ int abort;
     __shared__ float red[2][32];
-    const int lane = threadIdx.x, lanes = blockDim.x;
+    const int col = threadIdx.x * 8;
     const int64_t stride = gridDim.x, row_bytes = static_cast<int64_t>(h) * sizeof(T);
     Ring ring{data, full, &abort, err, stages, static_cast<int>(row_bytes), dS ? 3 : 2};
     int filled = 0;
     if (RING) ring.init();
     grid_begin();
     if (RING) {
-        if (lane == 0)
+        if (threadIdx.x == 0)
             for (int64_t r = blockIdx.x; filled < stages && r < rows; ++filled, r += stride)
                 ring.fill(filled, dY, S, dS, r * row_bytes);
     }
-    const Weights<VPT> wv(w, h, lane, lanes);
-    float dw[VPT][8] = {};
+    float wv[8], dw[8] = {};
+    load_weights(w, col, h, wv);
     const float inv_h = 1.0f / static_cast<float>(h);
     int stage = 0, phase = 0, turn = 0;
     const int64_t step = stride * h;
     int64_t off = static_cast<int64_t>(blockIdx.x) * h;
     for (int64_t row = blockIdx.x; row < rows; row += stride, off += step, turn ^= 1) {
         const float r = rstd[row];
-        Raw8<T> y[VPT], x[VPT], d[VPT];
+        Raw8<T> y, x, d;
         if (RING) {
             ring.wait(stage, phase);
             const uint8_t *at = data + stage * ring.bytes * ring.tensors;
-            load_row(reinterpret_cast<const T *>(at), h, lane, lanes, y);
-            load_row(reinterpret_cast<const T *>(at + ring.bytes), h, lane, lanes, x);
-            if (dS) load_row(reinterpret_cast<const T *>(at + 2 * ring.bytes), h, lane, lanes, d);
+            load_vector(reinterpret_cast<const T *>(at), col, h, y);
+            load_vector(reinterpret_cast<const T *>(at + ring.bytes), col, h, x);
+            if (dS) load_vector(reinterpret_cast<const T *>(at + 2 * ring.bytes), col, h, d);
         } else {
-            load_row(dY + off, h, lane, lanes, y);
-            load_row(S + off, h, lane, lanes, x);
-            if (dS) load_row(dS + off, h, lane, lanes, d);
+            load_vector(dY + off, col, h, y);
+            load_vector(S + off, col, h, x);
+            if (dS) load_vector(dS + off, col, h, d);
         }
-        const float c = backward_dots(y, x, wv, r, dw);
-        if (VPT > 1) {
-#pragma unroll
-            for (int i = 0; i < VPT; ++i) {
-                forget(y[i]);
-                forget(x[i]);
-            }
-        }
-        const float total = block_sum(c, red[turn]);  // its barrier: every thread has read the stage
+        // its barrier: every thread has read the stage
+        const float total = block_sum(backward_dots(y, x, wv, r, dw), red[turn]);
         if (RING) {
-            if (lane == 0 && row + stages * stride < rows) {
+            if (threadIdx.x == 0 && row + stages * stride < rows) {
                 ring.fill(stage, dY, S, dS, (row + stages * stride) * row_bytes);
                 ++filled;
             }
             if (++stage == stages) stage = 0, phase ^= 1;
         }
-        backward_finish(total * inv_h, r, y, x, wv, d, dS, dX + off, h, lane, lanes);
+        backward_finish(total * inv_h, r, y, x, wv, d, dS, dX + off + col, col < h);
     }
-    if (RING && lane == 0) ring.leave(filled);
-    if (!part) return;
-    float *mine = part + static_cast<int64_t>(blockIdx.x) * h;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int col = (lane + i * lanes) * 8;
-        if (col < h) {
-            float4 *o = reinterpret_cast<float4 *>(mine + col);
-            o[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
-            o[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+    if (RING && threadIdx.x == 0) ring.leave(filled);
+    if (part && col < h) store_partial(part + static_cast<int64_t>(blockIdx.x) * h + col, dw);
+}
+
+// Rows of more than 8192 values are shared by the two blocks of a cluster, still
+// eight columns a thread: in one block a thread would hold four vectors, whose
+// sums leave its registers no room for the weights, and reading those from L2 for
+// each row costs as much as the row (121 us for 4096 x 16384, and 122 as four
+// blocks a row).
+//
+// Each warp sends its sum to both blocks, as a store that the receiver's barrier
+// counts: a barrier of the cluster, or a fence, would wait for the rows' stores as
+// well (122 and 162 us). Row n + 1's products are summed before row n is finished,
+// so that its sum is on the way meanwhile, and row n is read from its stage again
+// for that. The last warp fills a stage when every warp has finished its row.
+// A warp sends row n's sum after it has finished row n - 2, and so after every
+// warp of both blocks has sent that of row n - 2, having read that of row n - 4:
+// four buffers.
+//
+// 4096 x 16384 bf16 with the residual path: 104 us, 5.2 TB/s (110 where a row is
+// finished before the next is begun); 16,384 rows 385 us, 5.6 TB/s. Bound by the
+// 0.9 us that a warp takes from a row's wait to its store, whatever the width,
+// and each SM has twice the rows here.
+__host__ __device__ __forceinline__ int half_of_row(int h) { return (h / 8 + 1) / 2 * 8; }
+
+// x to shared memory of a block of the cluster, whose barrier counts the bytes
+__device__ __forceinline__ void send(uint32_t to, uint32_t bar, float x) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(to),
+                 "r"(__float_as_uint(x)), "r"(bar)
+                 : "memory");
+}
+// ptx::mbar_wait for what the other block sends
+__device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, volatile int *abort, uint32_t *err) {
+    auto test = [&] {
+        uint32_t there;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(there)
+            : "r"(ptx::smem_u32(bar)), "r"(parity)
+            : "memory");
+        return there != 0;
+    };
+    return test() || (ptx::mbar_wait(bar, parity, abort, err, 21u) && test());
+}
+
+template <typename T>
+__global__ void __launch_bounds__(1024)
+    rmsnorm_backward_pair_kernel(const T *dY, const T *S, const float *w, const float *rstd, const T *dS, int64_t rows,
+                                 int h, T *dX, float *__restrict__ part, int stages, int tensors, uint32_t *err) {
+    extern __shared__ __align__(128) uint8_t data[];
+    __shared__ uint64_t full[kPairStages], empty[kPairStages], ready[4];
+    __shared__ float sums[4][64];  // [row % 4][block][warp]
+    __shared__ int abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5, col = threadIdx.x * 8;
+    const bool filler = threadIdx.x == blockDim.x - 32;
+    const uint32_t rank = ptx::cluster_ctarank();
+    // this block's columns, from `begin` on
+    const int half = half_of_row(h), begin = rank ? half : 0, columns = rank ? h - half : half;
+    const int64_t pairs = gridDim.x / 2, first = blockIdx.x / 2;
+    const int64_t mine = first < rows ? (rows - first + pairs - 1) / pairs : 0;
+    Ring ring{data, full, &abort, err, stages, columns * static_cast<int>(sizeof(T)), tensors};
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < stages; ++i) ptx::mbar_init(empty + i, warps);
+        for (int i = 0; i < 4; ++i) ptx::mbar_init(ready + i, 1);
+    }
+    ring.init();
+    ptx::cluster_sync();  // the other block's barriers are there before anything is sent to them
+    grid_begin();
+    int64_t filled = 0;
+    auto fill = [&](int stage) {
+        ring.fill(stage, dY, S, dS, ((first + filled * pairs) * h + begin) * sizeof(T));
+        ++filled;
+    };
+    if (filler)
+        while (filled < stages && filled < mine) fill(static_cast<int>(filled));
+    float wv[8], dw[8] = {};
+    load_weights(w + begin, col, columns, wv);
+    const float inv_h = 1.0f / static_cast<float>(h);
+    const float *statistic = rstd + first;
+    float next = mine > 0 ? *statistic : 0.0f, r = 0.0f;
+    const int64_t step = pairs * h;
+    int64_t off = first * h + begin + col;
+    int in = 0, in_phase = 0, out = 0, out_phase = 0;
+    for (int64_t n = 0; n <= mine; ++n) {
+        Raw8<T> y, x, d;
+        const float before = r;
+        if (n < mine) {  // row n: its products
+            r = next;
+            statistic += pairs;
+            if (n + 1 < mine) next = *statistic;
+            ring.wait(in, in_phase);
+            const uint8_t *at = data + in * ring.bytes * ring.tensors;
+            load_vector(reinterpret_cast<const T *>(at), col, columns, y);
+            load_vector(reinterpret_cast<const T *>(at + ring.bytes), col, columns, x);
+            const float sum = warp_sum(backward_dots(y, x, wv, r, dw));
+            const int turn = static_cast<int>(n & 3);
+            if (threadIdx.x == 0) ptx::mbar_arrive_expect_tx(ready + turn, static_cast<uint32_t>(2 * warps) * 4u);
+            if (lane < 2)
+                send(ptx::mapa_shared(ptx::smem_u32(&sums[turn][rank * 32 + warp]), lane),
+                     ptx::mapa_shared(ptx::smem_u32(ready + turn), lane), sum);
+            if (++in == stages) in = 0, in_phase ^= 1;
         }
+        if (n == 0) continue;
+        // row n - 1: its dX
+        if (dS && tensors < 3) {
+            if (col < columns) d = load8(dS + off);
+        }
+        const int turn = static_cast<int>((n - 1) & 3);
+        // (a whole warp leaves, and a block in which a wait ran out sends nothing more)
+        if (!__all_sync(0xffffffffu, wait_cluster(ready + turn, ((n - 1) >> 2) & 1, &abort, err))) break;
+        const float c = warp_sum(lane < warps ? sums[turn][lane] + sums[turn][32 + lane] : 0.0f) * inv_h;
+        const uint8_t *at = data + out * ring.bytes * ring.tensors;
+        load_vector(reinterpret_cast<const T *>(at), col, columns, y);
+        load_vector(reinterpret_cast<const T *>(at + ring.bytes), col, columns, x);
+        if (tensors == 3) load_vector(reinterpret_cast<const T *>(at + 2 * ring.bytes), col, columns, d);
+        backward_finish(c, before, y, x, wv, d, dS, dX + off, col < columns);
+        off += step;
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(empty + out);
+        if (filler && filled < mine) {
+            ptx::mbar_wait(empty + out, out_phase, &abort, err, 22u);
+            fill(out);
+        }
+        if (++out == stages) out = 0, out_phase ^= 1;
     }
+    if (filler) ring.leave(filled);
+    ptx::cluster_sync();  // neither block leaves while the other may send to it
+    if (part && col < columns) store_partial(part + first * h + begin + col, dw);
 }
 
 // dw[c] = the blocks' partial sums, always in the same order: 32 columns a block,
@@ -570,17 +650,16 @@ __global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(const float *part, int
 }
 
 // ------------------------------------------------------------------ host
-// Vectors a thread holds, threads of a block, blocks of an SM. The backward
-// has its sums of dw to hold too: one vector a thread as far as that goes.
+// Vectors a thread holds, threads of a block, blocks of an SM.
 struct Layout {
     int vpt, threads, blocks;
 };
 inline Layout layout_of(int64_t h, bool backward) {
-    const int v = static_cast<int>(h / 8);
     if (lane_rows(h)) return {1, kLanesThreads, 4};
-    const int vpt = backward ? (v <= 1024 ? 1 : 4) : (v <= 512 ? 1 : 2);
+    const int v = static_cast<int>(backward && pair_rows(h) ? half_of_row(static_cast<int>(h)) / 8 : h / 8);
+    const int vpt = backward || v <= 512 ? 1 : 2;
     const int threads = ((v + vpt - 1) / vpt + 31) / 32 * 32;
-        return {vpt, threads, std::min(backward ? 8 : 16, (vpt == 4 ? 512 : 1024) / threads)};
+    return {vpt, threads, std::min(backward ? 8 : 16, 1024 / threads)};
 }
 
 // Stages of the ring where `blocks` blocks share an SM; fewer blocks where two
@@ -599,8 +678,9 @@ inline int stages_of(int64_t stage_bytes, int &blocks) {
     return 0;
 }
 
-// Blocks of the backward at most, and so rows of its partial sums.
+// Blocks of the backward at most (pairs of blocks), and so rows of its partial sums.
 inline int64_t backward_blocks(int64_t T, int64_t h) {
+    if (pair_rows(h)) return std::min<int64_t>(T, kSms / 2);
     return std::min<int64_t>(lane_rows(h) ? lane_blocks(T, h) : T, layout_of(h, true).blocks * kSms);
 }
 
@@ -698,6 +778,19 @@ tpce_status backward(const void *dY, const void *S, const float *w, const float 
                                   : lanes == 16 ? go(Fn<rmsnorm_backward_lanes_kernel<T, 16>>{})
                                                 : go(Fn<rmsnorm_backward_lanes_kernel<T, 32>>{});
             if (e != cudaSuccess) return fail_cuda(e, "rmsnorm_backward");
+        } else if (pair_rows(h)) {
+            // a row in work, one of which the sum is on the way, and one ahead: three stages or more. For that
+            // dS of wide fp32 rows stays out of the ring.
+            const int bytes = half_of_row(h) * static_cast<int>(sizeof(T)), room = share_of(1) - 2048;
+            const int tensors = dS && 3 * 3 * bytes <= room ? 3 : 2;
+            const int stages = std::min(kPairStages, room / (tensors * bytes));
+            const int smem = stages * tensors * bytes;
+            using Pair = Fn<rmsnorm_backward_pair_kernel<T>>;
+            cudaError_t e = Pair::allow(smem, room);
+            if (e == cudaSuccess)
+                e = launch_clusters(2, Pair::fn, static_cast<unsigned>(2 * blocks), L.threads, smem, s, y, x, w, rstd, d,
+                                    rows, h, out, part, stages, tensors, device_error_word());
+            if (e != cudaSuccess) return fail_cuda(e, "rmsnorm_backward");
         } else {
             const int64_t stage_bytes = static_cast<int64_t>(h) * sizeof(T) * (dS ? 3 : 2);
             const int stages = stages_of(stage_bytes, L.blocks);
@@ -710,13 +803,8 @@ tpce_status backward(const void *dY, const void *S, const float *w, const float 
                 return launch(decltype(k)::fn, static_cast<unsigned>(blocks), L.threads, smem, s, y, x, w, rstd, d,
                               rows, h, out, part, stages, device_error_word());
             };
-            cudaError_t e;
-            if (L.vpt == 1)
-                e = ring ? go(Fn<rmsnorm_backward_block_kernel<T, 1, true>>{})
-                         : go(Fn<rmsnorm_backward_block_kernel<T, 1, false>>{});
-            else
-                e = ring ? go(Fn<rmsnorm_backward_block_kernel<T, 4, true>>{})
-                         : go(Fn<rmsnorm_backward_block_kernel<T, 4, false>>{});
+            const cudaError_t e = ring ? go(Fn<rmsnorm_backward_block_kernel<T, true>>{})
+                                       : go(Fn<rmsnorm_backward_block_kernel<T, false>>{});
             if (e != cudaSuccess) return fail_cuda(e, "rmsnorm_backward");
         }
         tpce_status st = check_launch("rmsnorm_backward", s);

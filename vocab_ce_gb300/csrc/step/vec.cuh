@@ -85,16 +85,6 @@ __device__ __forceinline__ void stream8(float *p, const Raw8<float> &r) {
     __stcs(q + 1, r.b);
 }
 
-// The compiler may not carry values made from r over this point: it makes them
-// again from r, which takes fewer registers.
-__device__ __forceinline__ void forget(Raw8<__nv_bfloat16> &r) {
-    asm volatile("" : "+r"(r.a.x), "+r"(r.a.y), "+r"(r.a.z), "+r"(r.a.w));
-}
-__device__ __forceinline__ void forget(Raw8<float> &r) {
-    asm volatile("" : "+f"(r.a.x), "+f"(r.a.y), "+f"(r.a.z), "+f"(r.a.w), "+f"(r.b.x), "+f"(r.b.y), "+f"(r.b.z),
-                 "+f"(r.b.w));
-}
-
 // (x, y) *= (a, b) and (x, y) += (a, b) * (c, d), two values an instruction; each
 // is rounded as by the single form. (A paired product and a paired sum after it
 // were fused to one rounding, whatever their rounding modes say: where both
