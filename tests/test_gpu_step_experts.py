@@ -154,6 +154,14 @@ def test_rows(T, h, k, E, drop, dtype):
     assert tp.device_status() == 0
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("k", range(1, 10))
+def test_every_number_of_choices_over_many_tokens(k, dtype):
+    # several vectors a thread; most choices dropped, so that most rows are only zeroed; a ragged last block
+    test_rows(9001, 168, k, 16, 0.875, dtype)
+    test_rows(4099, 776, k, 11, 0.0, dtype)
+
+
 def test_gradients_against_differences():
     # Z is linear in each argument: a difference of any size is exact up to 64-bit roundings
     gpu_or_skip()

@@ -31,6 +31,7 @@ using namespace step;
 
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxChoices = 32;
+constexpr int kMaxHeld = 8;  // choices of a token in a thread's registers
 
 // ------------------------------------------------------------------ the plan
 // A block takes a chunk of the assignments, each of its warps a contiguous run
@@ -229,13 +230,19 @@ struct Split {
     int lanes;   // a power of two, 8 .. 256
     int tokens;  // of a block
 };
-// Four vectors a thread keep enough loads under way; where that would leave
-// SMs without a block, as many threads as there are vectors.
-inline Split split_of(int64_t vectors, int64_t T) {
+// Four vectors a thread, and eight of rows of less than 8 KB: a thread that reads
+// its token's places for one or two vectors waits for them as long as for the
+// vectors (13,152 tokens of 864 bf16, k = 6, backward: 106, 87, 82 and 79 us with
+// one, two, four and eight; 16,384 of 4096, k = 8: 375 us with four, 381 with
+// eight). As many threads as there are vectors where that would leave an SM with
+// fewer than `blocks`: 512 tokens of 4096, k = 8, take 23 us with four, 28 with
+// one. The combine's backward, which adds over a token's lanes, is faster with two
+// (3551 of 792 fp32, k = 5: 34.6 and 36.8 us).
+inline Split split_of(int64_t vectors, int64_t T, int blocks = 4) {
     int lanes = 8;
-    while (lanes < 256 && lanes * 4 < vectors) lanes *= 2;
-    if (T * lanes < int64_t{256} * num_sms())
-        while (lanes < 256 && lanes < vectors) lanes *= 2;
+    const int each = vectors < 512 ? 8 : 4;
+    const int64_t enough = int64_t{256} * blocks * num_sms();
+    while (lanes < 256 && (lanes * each < vectors || (lanes < vectors && T * lanes < enough))) lanes *= 2;
     return {lanes, 256 / lanes};
 }
 
@@ -257,17 +264,22 @@ __device__ __forceinline__ void places(const int32_t *row, int64_t t, int k, int
     for (int j = 0; j < K; ++j) p[j] = j < left ? place(row, t * k + j, n, err) : -1;
 }
 
-// Rows offsets[E] .. n of out are zeros: the blocks take them in turn.
-__device__ __forceinline__ void zero_rest(uint4 *out, const int32_t *offsets, int E, int64_t n, int vectors) {
-    const int64_t kept = max(0, offsets[E]);
-    for (int64_t p = kept + blockIdx.x; p < n; p += gridDim.x)
-        for (int c = threadIdx.x; c < vectors; c += blockDim.x) out[p * vectors + c] = make_uint4(0u, 0u, 0u, 0u);
+// Rows `kept` .. n of out are zeros: the threads of the grid take their vectors in
+// turn. (With a row a block in turn, 15,938 tokens of 168 bf16 of which half are
+// dropped, k = 7, took 37 us instead of 21 in the combine's backward.)
+__device__ __forceinline__ void zero_rest(uint4 *out, int64_t kept, int64_t n, int vectors) {
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    for (int64_t i = max(int64_t{0}, kept) * vectors + static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+         i < n * vectors; i += stride)
+        out[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// The kernels hold the places of a token's K choices in registers; for k > K
-// (K is the largest then) they take the choices K at a time. All three are bound
-// by HBM: the loads of a thread's vectors are issued together, before anything
-// is done with them.
+// The kernels hold the places of a token's K choices in registers: K is k, or the
+// largest, and then they take the choices K at a time. (With one kernel for 5 to 8
+// choices 7728 tokens of 776 fp32, k = 7, half of them dropped, took 98 us
+// backward instead of 92; with blocks for three of them on an SM instead of two,
+// 82.) All three are bound by HBM: the loads of a thread's vectors are issued
+// together, before anything is done with them.
 //
 // Dispatch: 16,384 tokens of 4096 bf16 to 8 experts each, 1.2 GB, 178 us,
 // 6.8 TB/s, as fast as a copy.
@@ -280,6 +292,7 @@ __global__ void __launch_bounds__(256)
     const int lane = threadIdx.x & (lanes - 1);
     const int64_t n = T * k;
     grid_begin();
+    const int64_t kept = offsets[E];
     if (t < T) {
         for (int j0 = 0; j0 < k; j0 += K) {
             int32_t p[K];
@@ -300,7 +313,7 @@ __global__ void __launch_bounds__(256)
             }
         }
     }
-    zero_rest(out, offsets, E, n, vectors);
+    zero_rest(out, kept, n, vectors);
 }
 
 // The values of one 16-byte vector.
@@ -322,9 +335,11 @@ __device__ __forceinline__ uint4 narrow(const float (&v)[4]) {
 
 // Combine, and the dispatch's backward. NV values a vector: 8 (bf16) or 4 (fp32).
 // weights NULL: all one. The same 1.2 GB as above: 186 us, 6.5 TB/s (206 us where
-// a thread read its places again for each vector).
+// a thread read its places again for each vector). Four blocks an SM for six
+// choices and more, which costs eight of them some spilled registers: 3783 tokens
+// of 768 bf16, half dropped, take 12.5 us instead of 14.5 (the 1.2 GB no more).
 template <int NV, int K>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, K == 5 ? 3 : K > 2 ? 4 : 6)
     expert_combine_kernel(const uint4 *Ys, const int32_t *row,
                           const float *weights, int64_t T, int k, int vectors, int lanes,
                           uint4 *__restrict__ Z, uint32_t *err) {
@@ -333,7 +348,7 @@ __global__ void __launch_bounds__(256)
     grid_begin();
     if (t >= T) return;
     const int64_t n = T * k;
-    constexpr int U = K >= 8 ? 1 : K == 4 ? 2 : 4 / K;  // vectors at a time: four to eight loads under way
+    constexpr int U = K > 5 ? 1 : K > 2 ? 2 : 4 / K;  // vectors at a time: four to ten loads under way
     int32_t p[K];
     float w[K];
     auto choices = [&](int j0) {
@@ -356,7 +371,7 @@ __global__ void __launch_bounds__(256)
         for (int j = 0; j < K; ++j)
             if (p[j] >= 0) y[j] = Ys[static_cast<int64_t>(p[j]) * vectors + c];
     };
-    if (k > K) {
+    if (K == kMaxHeld && k > K) {
         for (int c = lane; c < vectors; c += lanes) {
             float z[NV] = {};
             for (int j0 = 0; j0 < k; j0 += K) {
@@ -387,7 +402,7 @@ __global__ void __launch_bounds__(256)
 // The combine's backward: dZ is read once for all of a token's rows. 4096 tokens
 // of 8192 bf16 and 2 experts, 10% dropped, 0.32 GB: 50 us, 6.4 TB/s.
 template <int NV, int K>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, K > 4 ? 3 : 4)
     expert_combine_backward_kernel(const uint4 *dZ, const uint4 *Ys,
                                    const int32_t *row, const int32_t *offsets, int E,
                                    const float *weights, int64_t T, int k, int vectors, int lanes,
@@ -398,16 +413,16 @@ __global__ void __launch_bounds__(256)
     const int64_t n = T * k;
     constexpr int U = K >= 4 ? 1 : 4 / K;
     grid_begin();
+    const int64_t kept = offsets[E];
     for (int j0 = 0; j0 < k; j0 += K) {
         int32_t p[K];
         float w[K], dot[K] = {};
 #pragma unroll
         for (int j = 0; j < K; ++j) p[j] = -1, w[j] = 0.0f;
         if (t < T) {
-            places(row + j0, t, k, n, err, p, k - j0);
 #pragma unroll
-            for (int j = 0; j < K; ++j)
-                if (p[j] >= 0) w[j] = weights[t * k + j0 + j];
+            for (int j = 0; j < K; ++j) w[j] = j0 + j < k ? weights[t * k + j0 + j] : 0.0f;
+            places(row + j0, t, k, n, err, p, k - j0);
             for (int c0 = lane; c0 < vectors; c0 += U * lanes) {
                 uint4 d[U], y[U][K];
 #pragma unroll
@@ -464,7 +479,7 @@ __global__ void __launch_bounds__(256)
                 if (j0 + j < k) dweights[t * k + j0 + j] = dot[j];
         }
     }
-    zero_rest(dYs, offsets, E, n, vectors);
+    zero_rest(dYs, kept, n, vectors);
 }
 
 // ------------------------------------------------------------------ host
@@ -496,13 +511,13 @@ inline int vectors_of(int64_t h, int dtype) { return static_cast<int>(h * (dtype
 
 inline unsigned blocks_of(int64_t T, const Split &sp) { return static_cast<unsigned>((T + sp.tokens - 1) / sp.tokens); }
 
-// f(integral constant): the fewest of 1, 2, 4, 8 choices held that cover k (8 for more)
-template <typename F>
+// f(integral constant): k choices held, kMaxHeld at a time for more
+template <int K = 1, typename F>
 void with_choices(int k, F f) {
-    if (k == 1) f(std::integral_constant<int, 1>{});
-    else if (k == 2) f(std::integral_constant<int, 2>{});
-    else if (k <= 4) f(std::integral_constant<int, 4>{});
-    else f(std::integral_constant<int, 8>{});
+    if constexpr (K < kMaxHeld) {
+        if (k > K) return with_choices<K + 1>(k, f);
+    }
+    f(std::integral_constant<int, K>{});
 }
 
 tpce_status combine(const char *name, const void *Ys, const int32_t *row, const float *weights, int64_t T, int64_t h,
@@ -612,7 +627,7 @@ extern "C" tpce_status tp_expert_combine_backward(const void *dZ, const void *Ys
         return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int v = vectors_of(h, dtype);
-    const Split sp = split_of(v, T);
+    const Split sp = split_of(v, T, 2);
     KernelTimer timer("expert_combine_backward", s);
     cudaError_t e = cudaSuccess;
     with_choices(k, [&](auto K) {
