@@ -62,6 +62,14 @@ def test_forward(T, h, dtype, residual):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("h", [1024, 2040, 2048, 4080, 4096, 6136, 6144, 12288])
+@pytest.mark.parametrize("residual", [False, True])
+def test_forward_whose_rows_in_flight_are_just_48_kb(h, dtype, residual):
+    # more shared memory than a launch gets without asking begins there, with what the kernel declares counted in
+    test_forward(1500, h, dtype, residual)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("T,h", SHAPES)
 @pytest.mark.parametrize("residual", [False, True])
 def test_backward(T, h, dtype, residual):

@@ -684,15 +684,16 @@ inline int64_t backward_blocks(int64_t T, int64_t h) {
     return std::min<int64_t>(lane_rows(h) ? lane_blocks(T, h) : T, layout_of(h, true).blocks * kSms);
 }
 
-// More than 48 KB of dynamic shared memory has to be asked for (`most`, what any
-// launch of the kernel takes), once for each kernel and device.
+// More than 48 KB of shared memory, what the kernel declares among it, has to be
+// asked for (`most`, what any launch of the kernel takes), once for each kernel
+// and device.
 template <auto Kernel>
 struct Fn {
     static cudaError_t allow(int bytes, int most) {
         static std::atomic<uint64_t> done{0};
         int dev = 0;
         cudaError_t e = cudaGetDevice(&dev);
-        if (e != cudaSuccess || bytes <= 48 * 1024) return e;
+        if (e != cudaSuccess || bytes <= 40 * 1024) return e;
         const uint64_t bit = uint64_t{1} << (dev & 63);
         if (done.load() & bit) return cudaSuccess;
         e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
