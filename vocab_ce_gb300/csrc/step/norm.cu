@@ -33,11 +33,13 @@ constexpr int64_t kMaxRows = int64_t{1} << 40;
 constexpr int kLanesThreads = 256;    // of a block where a row is some lanes of a warp
 constexpr int64_t kSms = 152;         // fixed, so that the workspace's size is known on the host
 constexpr int kMaxStages = 4, kPairStages = 6;
-// Rows of a block of the forward, where there are enough. Blocks that take all
-// their rows from one launch to the end wait for the SM that gets its bytes last:
-// 8192 x 8192 bf16 took 95 us with one round of blocks, 87 with four; with three
-// rows a block the ring is filled too often (4096 x 8192 and 8 bits: 53 and 56 us).
-constexpr int kRowsOfBlock = 6;
+// Rows of a block of the forward, where there are enough, with a residual and
+// without. Blocks that take all their rows from one launch to the end wait for the
+// SM that gets its bytes last: 8192 x 8192 bf16 took 95 us with one round of
+// blocks, 87 with four; with three rows a block the ring is filled too often (4096
+// x 8192 and 8 bits: 53 and 56 us). Without a residual a row is half as long:
+// 4096 x 8192 take 19.7 us with nine, 22.3 with six; 16,384 84.3 and 82.7.
+constexpr int kRowsOfBlock[2] = {6, 9};
 constexpr int kSmemPerSm = 228 * 1024;
 
 // A row of up to 256 values is 8, 16 or 32 lanes of a warp (no barrier in its
@@ -650,14 +652,19 @@ __global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(const float *part, int
 }
 
 // ------------------------------------------------------------------ host
-// Vectors a thread holds, threads of a block, blocks of an SM.
+// Vectors a thread holds, threads of a block, blocks of an SM. `halves`: the
+// forward of bf16 rows without a residual, of which one vector is 16 bytes a thread
+// and row; two a thread, and with them twice as many rows at a time on an SM: 8192
+// x 4096 bf16 and 8 bits 30 us instead of 37, 65,536 x 512 21 instead of 28. Where
+// a vector is 32 bytes already two take longer (10,146 x 3768 with the residual 59
+// and 57 us, 16,384 x 1000 fp32 24.4 and 22.9).
 struct Layout {
     int vpt, threads, blocks;
 };
-inline Layout layout_of(int64_t h, bool backward) {
+inline Layout layout_of(int64_t h, bool backward, bool halves = false) {
     if (lane_rows(h)) return {1, kLanesThreads, 4};
     const int v = static_cast<int>(backward && pair_rows(h) ? half_of_row(static_cast<int>(h)) / 8 : h / 8);
-    const int vpt = backward || v <= 512 ? 1 : 2;
+    const int vpt = backward || (v <= 512 && !halves) ? 1 : 2;
     const int threads = ((v + vpt - 1) / vpt + 31) / 32 * 32;
     return {vpt, threads, std::min(backward ? 8 : 16, 1024 / threads)};
 }
@@ -714,7 +721,7 @@ tpce_status check_shape(int64_t T, int64_t h, int dtype) {
 template <typename T>
 tpce_status forward(const void *X, const void *R, const float *w, int64_t rows, int h, float eps, void *S, void *Y,
                     void *Q, float *Qs, float *rstd, cudaStream_t s) {
-    Layout L = layout_of(h, false);
+    Layout L = layout_of(h, false, sizeof(T) == 2 && !R);
     const T *x = static_cast<const T *>(X), *r = static_cast<const T *>(R);
     T *so = static_cast<T *>(S), *yo = static_cast<T *>(Y);
     uint8_t *q = static_cast<uint8_t *>(Q);
@@ -735,8 +742,10 @@ tpce_status forward(const void *X, const void *R, const float *w, int64_t rows, 
     const int64_t stage_bytes = static_cast<int64_t>(h) * sizeof(T) * (R ? 2 : 1);
     const int stages = stages_of(stage_bytes, L.blocks);
     const int64_t fit = static_cast<int64_t>(num_sms()) * L.blocks;
-    // whole rounds of blocks with six rows each or more: an SM that gets its bytes sooner takes more blocks
-    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(rows, std::max<int64_t>(1, rows / (kRowsOfBlock * fit)) * fit));
+    const int of_block = kRowsOfBlock[R ? 0 : 1];
+    // whole rounds of blocks with that many rows each or more: an SM that gets its bytes sooner takes more blocks
+    const unsigned grid =
+        static_cast<unsigned>(std::min<int64_t>(rows, std::max<int64_t>(1, rows / (of_block * fit)) * fit));
     // with one row a block there is nothing to fetch ahead
     const bool ring = stages > 0 && rows > fit;
     const int smem = ring ? static_cast<int>(stage_bytes * stages) : 0;
