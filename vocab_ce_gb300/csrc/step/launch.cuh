@@ -16,6 +16,11 @@ __device__ __forceinline__ void grid_begin() {
     asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
 }
 
+// The same without letting the next launch begin: for a short kernel of few blocks,
+// whose successor's blocks would find their places while the kernel before it
+// still runs, on some SMs many and on others none.
+__device__ __forceinline__ void grid_begin_alone() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // `ctas` neighbouring blocks form a cluster
 template <typename... P, typename... A>
 cudaError_t launch_clusters(int ctas, void (*kernel)(P...), unsigned grid, int threads, size_t smem, cudaStream_t s,

@@ -628,23 +628,30 @@ __global__ void __launch_bounds__(1024)
     if (part && col < columns) store_partial(part + first * h + begin + col, dw);
 }
 
-// dw[c] = the blocks' partial sums, always in the same order: 32 columns a block,
-// each of 32 warps adding every 32nd row. 2 us, mostly the launch's; a row of
-// partial sums for each block is 0.5% of what 16,384 x 8192 reads.
+// dw[c] = the blocks' partial sums, always in the same order: COLS columns a block,
+// its threads adding every 1024 / COLS-th row, then lanes and warps. 2 us, mostly
+// the launch's; a row of partial sums for each block is 0.5% of what 16,384 x 8192
+// reads. 8 columns a block up to 2048 of them (10,273 x 728 bf16 backward 17.5 us
+// instead of 20.1), 32 beyond (8192 x 4096 44.9 instead of 46.5). A launch after it
+// that began before its end made the next backward 57 us instead of 46 at 32,768 x
+// 1024, and a forward and a backward of 65,536 x 512 131 instead of 99.
+template <int COLS>
 __global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(const float *part, int rows, int h,
                                                           float *__restrict__ dw) {
-    __shared__ float red[32][32];
-    grid_begin();
+    __shared__ float red[32][COLS];
+    grid_begin_alone();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + lane;
+    const int c = blockIdx.x * COLS + lane % COLS;
     float s = 0.0f;
     if (c < h) {
 #pragma unroll 8
-        for (int r = warp; r < rows; r += 32) s += part[static_cast<int64_t>(r) * h + c];
+        for (int r = threadIdx.x / COLS; r < rows; r += 1024 / COLS) s += part[static_cast<int64_t>(r) * h + c];
     }
-    red[warp][lane] = s;
+#pragma unroll
+    for (int d = COLS; d < 32; d <<= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    if (lane < COLS) red[warp][lane] = s;
     __syncthreads();
-    if (warp == 0 && c < h) {
+    if (warp == 0 && lane < COLS && c < h) {
 #pragma unroll
         for (int i = 1; i < 32; ++i) s += red[i][lane];
         dw[c] = s;
@@ -822,7 +829,9 @@ tpce_status backward(const void *dY, const void *S, const float *w, const float 
     }
     if (!dw) return TPCE_OK;
     KernelTimer timer("rmsnorm_dw", s);
-    const cudaError_t e = launch(rmsnorm_dw_kernel, static_cast<unsigned>((h + 31) / 32), 1024, 0, s, part,
+    const int columns = h <= 2048 ? 8 : 32;
+    const cudaError_t e = launch(columns == 8 ? rmsnorm_dw_kernel<8> : rmsnorm_dw_kernel<32>,
+                                 static_cast<unsigned>((h + columns - 1) / columns), 1024, 0, s, part,
                                  static_cast<int>(blocks), h, dw);
     if (e != cudaSuccess) return fail_cuda(e, "rmsnorm_dw");
     return check_launch("rmsnorm_dw", s);
