@@ -123,6 +123,12 @@ def test_backward_of_rows_that_two_blocks_share(T, h, dtype, residual):
     assert torch.equal(odd[:T - 1], got["dX"][:T - 1]) and not bool(odd[T - 1].isfinite().any())
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,h", [(32767, 264), (32768, 264), (40_001, 512), (33_000, 1024)])
+def test_backward_of_many_rows(T, h, dtype):
+    test_backward(T, h, dtype, True)
+
+
 def test_gradient_against_differences():
     # f = sum dY Y over the plain 64-bit forward; central differences in 64 bits with step 1e-5 are off by
     # about 1e-10 of f's third derivative, far below the kernel's own fp32 error

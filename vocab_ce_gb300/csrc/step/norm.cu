@@ -44,7 +44,7 @@ constexpr int kSmemPerSm = 228 * 1024;
 
 // A row of up to 256 values is 8, 16 or 32 lanes of a warp (no barrier in its
 // sum), a wider one a block's. At h = 512 a warp with two vectors a lane took
-// 45 us forward and 55 backward for 65,536 rows, a block of 64 threads 42 and 50;
+// 45 us forward and 55 backward for 65,536 rows, a block of 64 threads 42 and 47;
 // at h = 64 a whole warp a row took 86 and 87 us for 262,144 fp32 rows, 8 lanes
 // 51 and 46.
 inline bool lane_rows(int64_t h) { return h <= 256; }
@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(kLanesThreads, 4)
 // over all its rows, so the blocks are as many as have a place and their rows are
 // divided evenly. 16,384 x 8192 bf16 with the residual path: 158 us with the sum
 // of the blocks' dw, 6.8 TB/s, as fast as a copy; 8192 x 4096 44 us, 6.0 TB/s;
-// 65,536 x 512 50 us, 5.4 TB/s, where every row's sum costs its two warps as much
+// 65,536 x 512 47 us, 5.7 TB/s, where every row's sum costs its two warps as much
 // as its values.
 template <typename T, bool RING>
 __global__ void __launch_bounds__(1024)
@@ -665,15 +665,18 @@ __global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(const float *part, int
 // x 4096 bf16 and 8 bits 30 us instead of 37, 65,536 x 512 21 instead of 28. Where
 // a vector is 32 bytes already two take longer (10,146 x 3768 with the residual 59
 // and 57 us, 16,384 x 1000 fp32 24.4 and 22.9).
+// The backward's blocks each leave a row to the sum of dw: up to 8 on an SM, and 12
+// where that is little beside their own rows (65,536 x 512 47 us with 12, 50 with 8;
+// 4000 x 512 10.4 and 8.2).
 struct Layout {
     int vpt, threads, blocks;
 };
-inline Layout layout_of(int64_t h, bool backward, bool halves = false) {
+inline Layout layout_of(int64_t h, int64_t rows, bool backward, bool halves = false) {
     if (lane_rows(h)) return {1, kLanesThreads, 4};
     const int v = static_cast<int>(backward && pair_rows(h) ? half_of_row(static_cast<int>(h)) / 8 : h / 8);
     const int vpt = backward || (v <= 512 && !halves) ? 1 : 2;
     const int threads = ((v + vpt - 1) / vpt + 31) / 32 * 32;
-    return {vpt, threads, std::min(backward ? 8 : 16, 1024 / threads)};
+    return {vpt, threads, std::min(!backward ? 16 : rows < 32768 ? 8 : 12, 1024 / threads)};
 }
 
 // Stages of the ring where `blocks` blocks share an SM; fewer blocks where two
@@ -695,7 +698,7 @@ inline int stages_of(int64_t stage_bytes, int &blocks) {
 // Blocks of the backward at most (pairs of blocks), and so rows of its partial sums.
 inline int64_t backward_blocks(int64_t T, int64_t h) {
     if (pair_rows(h)) return std::min<int64_t>(T, kSms / 2);
-    return std::min<int64_t>(lane_rows(h) ? lane_blocks(T, h) : T, layout_of(h, true).blocks * kSms);
+    return std::min<int64_t>(lane_rows(h) ? lane_blocks(T, h) : T, layout_of(h, T, true).blocks * kSms);
 }
 
 // More than 48 KB of shared memory, what the kernel declares among it, has to be
@@ -728,7 +731,7 @@ tpce_status check_shape(int64_t T, int64_t h, int dtype) {
 template <typename T>
 tpce_status forward(const void *X, const void *R, const float *w, int64_t rows, int h, float eps, void *S, void *Y,
                     void *Q, float *Qs, float *rstd, cudaStream_t s) {
-    Layout L = layout_of(h, false, sizeof(T) == 2 && !R);
+    Layout L = layout_of(h, rows, false, sizeof(T) == 2 && !R);
     const T *x = static_cast<const T *>(X), *r = static_cast<const T *>(R);
     T *so = static_cast<T *>(S), *yo = static_cast<T *>(Y);
     uint8_t *q = static_cast<uint8_t *>(Q);
@@ -774,7 +777,7 @@ tpce_status forward(const void *X, const void *R, const float *w, int64_t rows, 
 template <typename T>
 tpce_status backward(const void *dY, const void *S, const float *w, const float *rstd, const void *dS, int64_t rows,
                      int h, void *dX, float *dw, float *part, cudaStream_t s) {
-    Layout L = layout_of(h, true);
+    Layout L = layout_of(h, rows, true);
     const T *y = static_cast<const T *>(dY), *x = static_cast<const T *>(S), *d = static_cast<const T *>(dS);
     T *out = static_cast<T *>(dX);
     if (!dw) part = nullptr;
