@@ -280,6 +280,25 @@ def test_captured_into_a_graph():
             assert torch.equal(mine.view(torch.uint8), v.view(torch.uint8)), k
 
 
+def test_rows_that_two_blocks_share_in_a_graph():
+    gpu_or_skip()
+    T, h = 200, 8208
+    S, dY, w = rows(T, h, torch.bfloat16, 16), rows(T, h, torch.bfloat16, 18), weight(h)
+    rstd = norm_forward(S, w, EPS)[1].float()
+    out = tp.tp_rmsnorm_backward(dY, S, w, rstd)
+    ws = torch.empty(tp.rmsnorm_workspace_bytes(T, h), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(3):
+            tp.tp_rmsnorm_backward(dY, S, w, rstd, out=out, ws=ws)
+    for seed in (30, 31):
+        dY.copy_(rows(T, h, torch.bfloat16, seed))
+        graph.replay()
+        ref = tp.tp_rmsnorm_backward(dY, S, w, rstd)
+        assert torch.equal(out["dX"], ref["dX"]) and torch.equal(out["dw"], ref["dw"])
+
+
 def test_an_output_that_does_not_fit_is_torchs_own_error():
     # copies of 512 GiB, more than the device has: torch's error, which a program may catch and go on
     gpu_or_skip()

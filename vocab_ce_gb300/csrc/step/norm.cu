@@ -503,8 +503,7 @@ __global__ void __launch_bounds__(1024)
 // Rows of more than 8192 values are shared by the two blocks of a cluster, still
 // eight columns a thread: in one block a thread would hold four vectors, whose
 // sums leave its registers no room for the weights, and reading those from L2 for
-// each row costs as much as the row (121 us for 4096 x 16384, and 122 as four
-// blocks a row).
+// each row costs as much as the row (121 us for 4096 x 16384).
 //
 // Each warp sends its sum to both blocks, as a store that the receiver's barrier
 // counts: a barrier of the cluster, or a fence, would wait for the rows' stores as
