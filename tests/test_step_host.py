@@ -4,6 +4,9 @@ kernel (the pointers are never read)."""
 
 import ctypes
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -168,3 +171,29 @@ def test_adamw_state_and_scalars():
     assert v.dtype == torch.float32 and torch.equal(v, torch.tensor(want, dtype=torch.float32))
     with pytest.raises(ValueError):
         tp.adamw_scalars(1e-3, 0)
+
+
+_CALL_WITHOUT_A_DEVICE = """
+import ctypes, sys
+from vocab_ce_gb300._lib import lib
+P = ctypes.c_void_p
+p = P(1 << 20)
+L = lib()
+for h in (64, 256, 264, 512, 8192, 16384):
+    for dtype in (0, 1):
+        for T in (1, 4, 100_000):
+            for r in (None, p):
+                assert L.tp_rmsnorm_forward(p, r, p, T, h, 1e-6, dtype, r, p, None, None, p, None) == 5, (h, T)
+                assert L.tpce_last_error()
+            assert L.tp_rmsnorm_backward(p, p, p, p, None, T, h, dtype, p, None, None, 0, None) == 5, (h, T)
+    assert L.tp_expert_combine_forward(p, p, p, 4, h, 2, 0, p, None) == 5
+"""
+
+
+def test_calls_without_a_device_return_a_status(L):
+    # a status code for every layout of the rows: the host arithmetic must not divide by a missing device's SMs
+    if torch.cuda.is_available():
+        pytest.skip("the pointers are not memory: only where no launch can begin")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _CALL_WITHOUT_A_DEVICE], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, (r.returncode, r.stderr[-2000:])

@@ -734,10 +734,13 @@ tpce_status forward(const void *X, const void *R, const float *w, int64_t rows, 
     const T *x = static_cast<const T *>(X), *r = static_cast<const T *>(R);
     T *so = static_cast<T *>(S), *yo = static_cast<T *>(Y);
     uint8_t *q = static_cast<uint8_t *>(Q);
+    // the grids below are multiples of it, and rows are divided by it
+    const int sms = num_sms();
+    if (sms <= 0) return fail(TPCE_ERR_CUDA, "rmsnorm_forward: no usable device");
     KernelTimer timer("rmsnorm_forward", s);
     if (lane_rows(h)) {
         const unsigned grid = static_cast<unsigned>(
-            std::min<int64_t>(lane_blocks(rows, h), static_cast<int64_t>(num_sms()) * L.blocks));
+            std::min<int64_t>(lane_blocks(rows, h), static_cast<int64_t>(sms) * L.blocks));
         auto go = [&](auto kernel) {
             return launch(kernel, grid, L.threads, 0, s, x, r, w, rows, h, eps, so, yo, q, Qs, rstd);
         };
@@ -750,7 +753,7 @@ tpce_status forward(const void *X, const void *R, const float *w, int64_t rows, 
     }
     const int64_t stage_bytes = static_cast<int64_t>(h) * sizeof(T) * (R ? 2 : 1);
     const int stages = stages_of(stage_bytes, L.blocks);
-    const int64_t fit = static_cast<int64_t>(num_sms()) * L.blocks;
+    const int64_t fit = static_cast<int64_t>(sms) * L.blocks;
     const int of_block = kRowsOfBlock[R ? 0 : 1];
     // whole rounds of blocks with that many rows each or more: an SM that gets its bytes sooner takes more blocks
     const unsigned grid =
