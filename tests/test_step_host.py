@@ -195,5 +195,6 @@ def test_calls_without_a_device_return_a_status(L):
     if torch.cuda.is_available():
         pytest.skip("the pointers are not memory: only where no launch can begin")
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
-    r = subprocess.run([sys.executable, "-c", _CALL_WITHOUT_A_DEVICE], cwd=root, capture_output=True, text=True, timeout=300)
+    r = subprocess.run([sys.executable, "-c", _CALL_WITHOUT_A_DEVICE], cwd=root, capture_output=True, text=True,
+                       timeout=300)
     assert r.returncode == 0, (r.returncode, r.stderr[-2000:])

@@ -85,28 +85,34 @@ __device__ __forceinline__ void load_row_weights(const float *w, int h, int lane
 // tensors, each of `bytes`. Thread 0 fills a stage again after a barrier that
 // every thread passes when it has read the stage. Waits are bounded (ptx.cuh):
 // after one that ran out nothing more is copied, and the block leaves when what
-// was under way has landed.
+// was under way has landed, or after the limit of a drain.
 struct Ring {
     uint8_t *data;
     uint64_t *full;
-    volatile int *abort;
+    volatile int *abort;  // a wait ran out; then the number of fills left out since
     uint32_t *err;
     int stages, bytes, tensors;
 
     __device__ void init() {
         if (threadIdx.x == 0) {
-            *abort = 0;
+            abort[0] = abort[1] = 0;
             for (int i = 0; i < stages; ++i) ptx::mbar_init(full + i, 1);
             ptx::fence_mbar_init();
         }
         __syncthreads();
     }
-    // thread 0 only: the rows at `offset` bytes of the tensors into a stage
-    __device__ void fill(int stage, const void *a, const void *b, const void *c, int64_t offset) {
-        if (*abort) return;
+    // thread 0 only: the rows at `offset` bytes of the tensors into a stage. withhold: the
+    // first tensor's row is left out although the barrier counts it, so that the wait for
+    // it runs out (tpce_debug_withhold_next_load).
+    __device__ void fill(int stage, const void *a, const void *b, const void *c, int64_t offset,
+                         bool withhold = false) {
+        if (*abort) {
+            abort[1] = abort[1] + 1;  // leave() waits for those before
+            return;
+        }
         ptx::mbar_arrive_expect_tx(full + stage, static_cast<uint32_t>(bytes) * tensors);
         uint8_t *to = data + stage * bytes * tensors;
-        copy(to, a, offset, stage);
+        if (!withhold) copy(to, a, offset, stage);
         if (tensors > 1) copy(to + bytes, b, offset, stage);
         if (tensors > 2) copy(to + 2 * bytes, c, offset, stage);
     }
@@ -120,9 +126,11 @@ struct Ring {
             : "memory");
     }
     __device__ void wait(int stage, int phase) { ptx::mbar_wait(full + stage, phase, abort, err, 20u); }
-    // thread 0 only, after the last row: `filled` fills in all
+    // thread 0 only, after the last row: `filled` calls of fill, the n-th for stage
+    // n % stages
     __device__ void leave(int64_t filled) {
         if (!*abort) return;
+        filled -= abort[1];
         for (int64_t n = filled > stages ? filled - stages : 0; n < filled; ++n)
             ptx::mbar_wait_drain(full + n % stages, (n / stages) & 1);
     }
@@ -234,23 +242,23 @@ template <typename T, int VPT, bool RING>
 __global__ void __launch_bounds__(1024)
     rmsnorm_forward_block_kernel(const T *X, const T *R, const float *w, int64_t rows, int h, float eps,
                                  T *S, T *Y, uint8_t *Q, float *Qs, float *__restrict__ rstd, int stages,
-                                 uint32_t *err) {
+                                 int withhold, uint32_t *err) {
     extern __shared__ __align__(128) uint8_t data[];
     __shared__ uint64_t full[kMaxStages];
-    __shared__ int abort;
+    __shared__ int abort[2];
     __shared__ float red[2][32];
     const int lane = threadIdx.x, lanes = blockDim.x;
     const int groups = (h + kGroup - 1) / kGroup;
     const float inv_h = 1.0f / static_cast<float>(h);
     const int64_t stride = gridDim.x, row_bytes = static_cast<int64_t>(h) * sizeof(T);
-    Ring ring{data, full, &abort, err, stages, static_cast<int>(row_bytes), R ? 2 : 1};
+    Ring ring{data, full, abort, err, stages, static_cast<int>(row_bytes), R ? 2 : 1};
     int filled = 0;
     if (RING) ring.init();
     grid_begin();
     if (RING) {
         if (lane == 0)
             for (int64_t r = blockIdx.x; filled < stages && r < rows; ++filled, r += stride)
-                ring.fill(filled, X, R, nullptr, r * row_bytes);
+                ring.fill(filled, X, R, nullptr, r * row_bytes, withhold && r == 0);
     }
     float wv[VPT][8];
     load_row_weights(w, h, lane, lanes, wv);
@@ -449,21 +457,21 @@ template <typename T, bool RING>
 __global__ void __launch_bounds__(1024)
     rmsnorm_backward_block_kernel(const T *dY, const T *S, const float *w, const float *rstd,
                                   const T *dS, int64_t rows, int h, T *dX, float *__restrict__ part, int stages,
-                                  uint32_t *err) {
+                                  int withhold, uint32_t *err) {
     extern __shared__ __align__(128) uint8_t data[];
     __shared__ uint64_t full[kMaxStages];
-    __shared__ int abort;
+    __shared__ int abort[2];
     __shared__ float red[2][32];
     const int col = threadIdx.x * 8;
     const int64_t stride = gridDim.x, row_bytes = static_cast<int64_t>(h) * sizeof(T);
-    Ring ring{data, full, &abort, err, stages, static_cast<int>(row_bytes), dS ? 3 : 2};
+    Ring ring{data, full, abort, err, stages, static_cast<int>(row_bytes), dS ? 3 : 2};
     int filled = 0;
     if (RING) ring.init();
     grid_begin();
     if (RING) {
         if (threadIdx.x == 0)
             for (int64_t r = blockIdx.x; filled < stages && r < rows; ++filled, r += stride)
-                ring.fill(filled, dY, S, dS, r * row_bytes);
+                ring.fill(filled, dY, S, dS, r * row_bytes, withhold && r == 0);
     }
     float wv[8], dw[8] = {};
     load_weights(w, col, h, wv);
@@ -545,11 +553,12 @@ __device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, vol
 template <typename T>
 __global__ void __launch_bounds__(1024)
     rmsnorm_backward_pair_kernel(const T *dY, const T *S, const float *w, const float *rstd, const T *dS, int64_t rows,
-                                 int h, T *dX, float *__restrict__ part, int stages, int tensors, uint32_t *err) {
+                                 int h, T *dX, float *__restrict__ part, int stages, int tensors, int withhold,
+                                 uint32_t *err) {
     extern __shared__ __align__(128) uint8_t data[];
     __shared__ uint64_t full[kPairStages], empty[kPairStages], ready[4];
     __shared__ float sums[4][64];  // [row % 4][block][warp]
-    __shared__ int abort;
+    __shared__ int abort[2];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5, col = threadIdx.x * 8;
     const bool filler = threadIdx.x == blockDim.x - 32;
     const uint32_t rank = ptx::cluster_ctarank();
@@ -557,7 +566,7 @@ __global__ void __launch_bounds__(1024)
     const int half = half_of_row(h), begin = rank ? half : 0, columns = rank ? h - half : half;
     const int64_t pairs = gridDim.x / 2, first = blockIdx.x / 2;
     const int64_t mine = first < rows ? (rows - first + pairs - 1) / pairs : 0;
-    Ring ring{data, full, &abort, err, stages, columns * static_cast<int>(sizeof(T)), tensors};
+    Ring ring{data, full, abort, err, stages, columns * static_cast<int>(sizeof(T)), tensors};
     if (threadIdx.x == 0) {
         for (int i = 0; i < stages; ++i) ptx::mbar_init(empty + i, warps);
         for (int i = 0; i < 4; ++i) ptx::mbar_init(ready + i, 1);
@@ -566,12 +575,13 @@ __global__ void __launch_bounds__(1024)
     ptx::cluster_sync();  // the other block's barriers are there before anything is sent to them
     grid_begin();
     int64_t filled = 0;
-    auto fill = [&](int stage) {
-        ring.fill(stage, dY, S, dS, ((first + filled * pairs) * h + begin) * sizeof(T));
+    auto fill = [&](int stage, bool without = false) {
+        ring.fill(stage, dY, S, dS, ((first + filled * pairs) * h + begin) * sizeof(T), without);
         ++filled;
     };
     if (filler)
-        while (filled < stages && filled < mine) fill(static_cast<int>(filled));
+        while (filled < stages && filled < mine)
+            fill(static_cast<int>(filled), withhold && blockIdx.x + filled == 0);
     float wv[8], dw[8] = {};
     load_weights(w + begin, col, columns, wv);
     const float inv_h = 1.0f / static_cast<float>(h);
@@ -606,7 +616,7 @@ __global__ void __launch_bounds__(1024)
         }
         const int turn = static_cast<int>((n - 1) & 3);
         // (a whole warp leaves, and a block in which a wait ran out sends nothing more)
-        if (!__all_sync(0xffffffffu, wait_cluster(ready + turn, ((n - 1) >> 2) & 1, &abort, err))) break;
+        if (!__all_sync(0xffffffffu, wait_cluster(ready + turn, ((n - 1) >> 2) & 1, abort, err))) break;
         const float c = warp_sum(lane < warps ? sums[turn][lane] + sums[turn][32 + lane] : 0.0f) * inv_h;
         const uint8_t *at = data + out * ring.bytes * ring.tensors;
         load_vector(reinterpret_cast<const T *>(at), col, columns, y);
@@ -617,7 +627,7 @@ __global__ void __launch_bounds__(1024)
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(empty + out);
         if (filler && filled < mine) {
-            ptx::mbar_wait(empty + out, out_phase, &abort, err, 22u);
+            ptx::mbar_wait(empty + out, out_phase, abort, err, 22u);
             fill(out);
         }
         if (++out == stages) out = 0, out_phase ^= 1;
@@ -765,7 +775,7 @@ tpce_status forward(const void *X, const void *R, const float *w, int64_t rows, 
         const cudaError_t e = decltype(k)::allow(smem, share_of(1));
         if (e != cudaSuccess) return e;
         return launch(decltype(k)::fn, grid, L.threads, smem, s, x, r, w, rows, h, eps, so, yo, q, Qs, rstd, stages,
-                      device_error_word());
+                      ring ? take_debug_withhold() : 0, device_error_word());
     };
     cudaError_t e;
     if (L.vpt == 1)
@@ -811,7 +821,8 @@ tpce_status backward(const void *dY, const void *S, const float *w, const float 
             cudaError_t e = Pair::allow(smem, room);
             if (e == cudaSuccess)
                 e = launch_clusters(2, Pair::fn, static_cast<unsigned>(2 * blocks), L.threads, smem, s, y, x, w, rstd, d,
-                                    rows, h, out, part, stages, tensors, device_error_word());
+                                    rows, h, out, part, stages, tensors, take_debug_withhold(),
+                                    device_error_word());
             if (e != cudaSuccess) return fail_cuda(e, "rmsnorm_backward");
         } else {
             const int64_t stage_bytes = static_cast<int64_t>(h) * sizeof(T) * (dS ? 3 : 2);
@@ -823,7 +834,8 @@ tpce_status backward(const void *dY, const void *S, const float *w, const float 
                 const cudaError_t e = decltype(k)::allow(smem, share_of(1));
                 if (e != cudaSuccess) return e;
                 return launch(decltype(k)::fn, static_cast<unsigned>(blocks), L.threads, smem, s, y, x, w, rstd, d,
-                              rows, h, out, part, stages, device_error_word());
+                              rows, h, out, part, stages, ring ? take_debug_withhold() : 0,
+                              device_error_word());
             };
             const cudaError_t e = ring ? go(Fn<rmsnorm_backward_block_kernel<T, true>>{})
                                        : go(Fn<rmsnorm_backward_block_kernel<T, false>>{});
