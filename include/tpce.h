@@ -617,7 +617,7 @@ tpce_status tpce_device_status(void *stream, int clear, uint32_t *detail);
  * context usable. That launch's outputs are undefined. An RMS norm whose rows
  * come through a ring in shared memory (wider than 256 values, more rows than
  * blocks have a place, and every backward wider than 8192) takes it the same
- * way: block 0 leaves one copy of its first row out. The arming is used up
+ * way: block 0 counts bytes on its first row that nothing copies. The arming is used up
  * by that one launch; tpce_debug_withhold_next_load(0) disarms it unused.
  * Process-wide; returns TPCE_OK.
  * ------------------------------------------------------------------------- */

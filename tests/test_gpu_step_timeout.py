@@ -1,13 +1,12 @@
-"""The RMS norm's bounded waits when a copy never comes.
+"""The RMS norm's bounded waits when what they wait for never comes.
 
 tpce_debug_withhold_next_load(1) makes block 0 of the next norm launch whose
-rows come through a ring leave one copy of its first row out, although the
-stage's barrier counts its bytes: the wait for that row cannot complete. No
-fault is involved. For each kernel with a ring the test checks that
+rows come through a ring count bytes on its first row that nothing copies: the
+wait for that row cannot complete. No fault is involved. For each kernel with a ring the test checks that
 
-* the call returns, after the wait's bound (2 s) and the drain's (50 ms, which
-  the withheld stage uses up: the block may not leave before it has waited for
-  what is under way), and well before any outer limit;
+* the call returns, after the wait's bound (2 s) and a drain's (50 ms: the block
+  may not leave while something is under way to its shared memory), and well
+  before any outer limit;
 * the device status word names a wait of the norm;
 * the context is usable: the same call again gives the bits from before.
 """
@@ -45,8 +44,8 @@ def backward(T, h, dtype, residual):
     return lambda: tp.tp_rmsnorm_backward(y, s, w, rstd, dS=d)
 
 
-# every kernel with a ring; a row of one tensor (nothing of it comes) and of two or three (the rest comes); more rows
-# than fill the ring once, so that block 0 has fills to skip after its wait ran out
+# every kernel with a ring, one to three tensors a row; more rows than fill the ring once, so that block 0 has fills
+# to skip after its wait ran out
 CASES = {
     "forward": (forward, 30_000, 1024, torch.bfloat16, False),
     "forward residual": (forward, 3000, 8192, torch.bfloat16, True),

@@ -84,35 +84,36 @@ __device__ __forceinline__ void load_row_weights(const float *w, int h, int lane
 // Stage n % stages holds the n-th row of this block: the rows of up to three
 // tensors, each of `bytes`. Thread 0 fills a stage again after a barrier that
 // every thread passes when it has read the stage. Waits are bounded (ptx.cuh):
-// after one that ran out nothing more is copied, and the block leaves when what
-// was under way has landed, or after the limit of a drain.
+// after one that ran out nothing more is copied, and the block stays for the time
+// that a drain may take, in which what is under way to its shared memory lands.
+// (Which stages are still being filled is not counted: the counter cost wide rows
+// in fp32 2% of their time in every launch.)
 struct Ring {
     uint8_t *data;
     uint64_t *full;
-    volatile int *abort;  // a wait ran out; then the number of fills left out since
+    volatile int *abort;
     uint32_t *err;
     int stages, bytes, tensors;
 
-    __device__ void init() {
+    // withhold: block 0 counts bytes on its first row that nothing copies, so that the wait
+    // for it runs out (tpce_debug_withhold_next_load)
+    __device__ void init(int withhold) {
         if (threadIdx.x == 0) {
-            abort[0] = abort[1] = 0;
+            *abort = 0;
             for (int i = 0; i < stages; ++i) ptx::mbar_init(full + i, 1);
+            if (withhold && blockIdx.x == 0)
+                asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], 16;" ::"r"(ptx::smem_u32(full))
+                             : "memory");
             ptx::fence_mbar_init();
         }
         __syncthreads();
     }
-    // thread 0 only: the rows at `offset` bytes of the tensors into a stage. withhold: the
-    // first tensor's row is left out although the barrier counts it, so that the wait for
-    // it runs out (tpce_debug_withhold_next_load).
-    __device__ void fill(int stage, const void *a, const void *b, const void *c, int64_t offset,
-                         bool withhold = false) {
-        if (*abort) {
-            abort[1] = abort[1] + 1;  // leave() waits for those before
-            return;
-        }
+    // thread 0 only: the rows at `offset` bytes of the tensors into a stage
+    __device__ void fill(int stage, const void *a, const void *b, const void *c, int64_t offset) {
+        if (*abort) return;
         ptx::mbar_arrive_expect_tx(full + stage, static_cast<uint32_t>(bytes) * tensors);
         uint8_t *to = data + stage * bytes * tensors;
-        if (!withhold) copy(to, a, offset, stage);
+        copy(to, a, offset, stage);
         if (tensors > 1) copy(to + bytes, b, offset, stage);
         if (tensors > 2) copy(to + 2 * bytes, c, offset, stage);
     }
@@ -126,13 +127,11 @@ struct Ring {
             : "memory");
     }
     __device__ void wait(int stage, int phase) { ptx::mbar_wait(full + stage, phase, abort, err, 20u); }
-    // thread 0 only, after the last row: `filled` calls of fill, the n-th for stage
-    // n % stages
-    __device__ void leave(int64_t filled) {
+    // one thread, after the last row
+    __device__ void leave() {
         if (!*abort) return;
-        filled -= abort[1];
-        for (int64_t n = filled > stages ? filled - stages : 0; n < filled; ++n)
-            ptx::mbar_wait_drain(full + n % stages, (n / stages) & 1);
+        for (const uint64_t t0 = ptx::globaltimer(); ptx::globaltimer() - t0 < kDrainLimitNs;) {
+        }
     }
 };
 
@@ -245,20 +244,19 @@ __global__ void __launch_bounds__(1024)
                                  int withhold, uint32_t *err) {
     extern __shared__ __align__(128) uint8_t data[];
     __shared__ uint64_t full[kMaxStages];
-    __shared__ int abort[2];
+    __shared__ int abort;
     __shared__ float red[2][32];
     const int lane = threadIdx.x, lanes = blockDim.x;
     const int groups = (h + kGroup - 1) / kGroup;
     const float inv_h = 1.0f / static_cast<float>(h);
     const int64_t stride = gridDim.x, row_bytes = static_cast<int64_t>(h) * sizeof(T);
-    Ring ring{data, full, abort, err, stages, static_cast<int>(row_bytes), R ? 2 : 1};
-    int filled = 0;
-    if (RING) ring.init();
+    Ring ring{data, full, &abort, err, stages, static_cast<int>(row_bytes), R ? 2 : 1};
+    if (RING) ring.init(withhold);
     grid_begin();
     if (RING) {
+        int64_t r = blockIdx.x;
         if (lane == 0)
-            for (int64_t r = blockIdx.x; filled < stages && r < rows; ++filled, r += stride)
-                ring.fill(filled, X, R, nullptr, r * row_bytes, withhold && r == 0);
+            for (int i = 0; i < stages && r < rows; ++i, r += stride) ring.fill(i, X, R, nullptr, r * row_bytes);
     }
     float wv[VPT][8];
     load_row_weights(w, h, lane, lanes, wv);
@@ -280,17 +278,15 @@ __global__ void __launch_bounds__(1024)
         const float sq = f.add(x, r, R, S, off, h, lane, lanes);
         const float total = block_sum(sq, red[turn]);  // its barrier: every thread has read the stage
         if (RING) {
-            if (lane == 0 && row + stages * stride < rows) {
+            if (lane == 0 && row + stages * stride < rows)
                 ring.fill(stage, X, R, nullptr, (row + stages * stride) * row_bytes);
-                ++filled;
-            }
             if (++stage == stages) stage = 0, phase ^= 1;
         }
         const float v = rstd_of(total, inv_h, eps);
         if (lane == 0) rstd[row] = v;
         f.finish(v, wv, Y, Q, Qs + row * groups, off, h, lane, lanes);
     }
-    if (RING && lane == 0) ring.leave(filled);
+    if (RING && lane == 0) ring.leave();
 }
 
 // ------------------------------------------------------------------ backward
@@ -460,18 +456,17 @@ __global__ void __launch_bounds__(1024)
                                   int withhold, uint32_t *err) {
     extern __shared__ __align__(128) uint8_t data[];
     __shared__ uint64_t full[kMaxStages];
-    __shared__ int abort[2];
+    __shared__ int abort;
     __shared__ float red[2][32];
     const int col = threadIdx.x * 8;
     const int64_t stride = gridDim.x, row_bytes = static_cast<int64_t>(h) * sizeof(T);
-    Ring ring{data, full, abort, err, stages, static_cast<int>(row_bytes), dS ? 3 : 2};
-    int filled = 0;
-    if (RING) ring.init();
+    Ring ring{data, full, &abort, err, stages, static_cast<int>(row_bytes), dS ? 3 : 2};
+    if (RING) ring.init(withhold);
     grid_begin();
     if (RING) {
+        int64_t r = blockIdx.x;
         if (threadIdx.x == 0)
-            for (int64_t r = blockIdx.x; filled < stages && r < rows; ++filled, r += stride)
-                ring.fill(filled, dY, S, dS, r * row_bytes, withhold && r == 0);
+            for (int i = 0; i < stages && r < rows; ++i, r += stride) ring.fill(i, dY, S, dS, r * row_bytes);
     }
     float wv[8], dw[8] = {};
     load_weights(w, col, h, wv);
@@ -496,15 +491,13 @@ __global__ void __launch_bounds__(1024)
         // its barrier: every thread has read the stage
         const float total = block_sum(backward_dots(y, x, wv, r, dw), red[turn]);
         if (RING) {
-            if (threadIdx.x == 0 && row + stages * stride < rows) {
+            if (threadIdx.x == 0 && row + stages * stride < rows)
                 ring.fill(stage, dY, S, dS, (row + stages * stride) * row_bytes);
-                ++filled;
-            }
             if (++stage == stages) stage = 0, phase ^= 1;
         }
         backward_finish(total * inv_h, r, y, x, wv, d, dS, dX + off + col, col < h);
     }
-    if (RING && threadIdx.x == 0) ring.leave(filled);
+    if (RING && threadIdx.x == 0) ring.leave();
     if (part && col < h) store_partial(part + static_cast<int64_t>(blockIdx.x) * h + col, dw);
 }
 
@@ -558,7 +551,7 @@ __global__ void __launch_bounds__(1024)
     extern __shared__ __align__(128) uint8_t data[];
     __shared__ uint64_t full[kPairStages], empty[kPairStages], ready[4];
     __shared__ float sums[4][64];  // [row % 4][block][warp]
-    __shared__ int abort[2];
+    __shared__ int abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5, col = threadIdx.x * 8;
     const bool filler = threadIdx.x == blockDim.x - 32;
     const uint32_t rank = ptx::cluster_ctarank();
@@ -566,22 +559,21 @@ __global__ void __launch_bounds__(1024)
     const int half = half_of_row(h), begin = rank ? half : 0, columns = rank ? h - half : half;
     const int64_t pairs = gridDim.x / 2, first = blockIdx.x / 2;
     const int64_t mine = first < rows ? (rows - first + pairs - 1) / pairs : 0;
-    Ring ring{data, full, abort, err, stages, columns * static_cast<int>(sizeof(T)), tensors};
+    Ring ring{data, full, &abort, err, stages, columns * static_cast<int>(sizeof(T)), tensors};
     if (threadIdx.x == 0) {
         for (int i = 0; i < stages; ++i) ptx::mbar_init(empty + i, warps);
         for (int i = 0; i < 4; ++i) ptx::mbar_init(ready + i, 1);
     }
-    ring.init();
+    ring.init(withhold);
     ptx::cluster_sync();  // the other block's barriers are there before anything is sent to them
     grid_begin();
     int64_t filled = 0;
-    auto fill = [&](int stage, bool without = false) {
-        ring.fill(stage, dY, S, dS, ((first + filled * pairs) * h + begin) * sizeof(T), without);
+    auto fill = [&](int stage) {
+        ring.fill(stage, dY, S, dS, ((first + filled * pairs) * h + begin) * sizeof(T));
         ++filled;
     };
     if (filler)
-        while (filled < stages && filled < mine)
-            fill(static_cast<int>(filled), withhold && blockIdx.x + filled == 0);
+        while (filled < stages && filled < mine) fill(static_cast<int>(filled));
     float wv[8], dw[8] = {};
     load_weights(w + begin, col, columns, wv);
     const float inv_h = 1.0f / static_cast<float>(h);
@@ -616,7 +608,7 @@ __global__ void __launch_bounds__(1024)
         }
         const int turn = static_cast<int>((n - 1) & 3);
         // (a whole warp leaves, and a block in which a wait ran out sends nothing more)
-        if (!__all_sync(0xffffffffu, wait_cluster(ready + turn, ((n - 1) >> 2) & 1, abort, err))) break;
+        if (!__all_sync(0xffffffffu, wait_cluster(ready + turn, ((n - 1) >> 2) & 1, &abort, err))) break;
         const float c = warp_sum(lane < warps ? sums[turn][lane] + sums[turn][32 + lane] : 0.0f) * inv_h;
         const uint8_t *at = data + out * ring.bytes * ring.tensors;
         load_vector(reinterpret_cast<const T *>(at), col, columns, y);
@@ -627,13 +619,15 @@ __global__ void __launch_bounds__(1024)
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(empty + out);
         if (filler && filled < mine) {
-            ptx::mbar_wait(empty + out, out_phase, abort, err, 22u);
+            ptx::mbar_wait(empty + out, out_phase, &abort, err, 22u);
             fill(out);
         }
         if (++out == stages) out = 0, out_phase ^= 1;
     }
-    if (filler) ring.leave(filled);
     ptx::cluster_sync();  // neither block leaves while the other may send to it
+    // A block that has waited for every row's sums has received all that was sent to it;
+    // to one that gave up, what was sent before the barrier may still be on its way.
+    if (threadIdx.x == 0) ring.leave();
     if (part && col < columns) store_partial(part + first * h + begin + col, dw);
 }
 
