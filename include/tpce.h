@@ -561,15 +561,18 @@ tpce_status tp_expert_combine_backward(const void *dZ, const void *Ys, const int
  * moments before they are rounded.
  * `tensors` is a host array, read during the call; tensors with n == 0 are
  * skipped (their pointers may be NULL). Every device pointer is 16-byte
- * aligned, and no two of them overlap.
+ * aligned, and what is written overlaps nothing else of the list: a state, a
+ * master or a part of a parameter given twice is refused (gradients are only
+ * read, and may be shared).
  * device_scalars (NULL: none): four fp32 on the device,
  *   { lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t), lr, grad_scale },
  * read by the kernel in place of lr, step and grad_scale, which a captured
  * graph would otherwise repeat: write them anew before each replay.
  * Lists of up to 368 tensors take one launch.
  * Errors: TPCE_ERR_INVALID for a beta outside [0, 1), eps < 0, step < 1, an
- * unknown dtype or state_bits, a master beside fp32 values, a null pointer;
- * everything is checked before the first launch.
+ * unknown dtype or state_bits, a master beside fp32 values, a null pointer, an
+ * overlap; TPCE_ERR_WORKSPACE if the host has no memory for the list's check.
+ * Everything is checked before the first launch.
  * ------------------------------------------------------------------------- */
 typedef struct {
     void *p;             /* [n] p_dtype */

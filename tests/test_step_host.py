@@ -5,6 +5,7 @@ kernel (the pointers are never read)."""
 import ctypes
 import math
 import os
+import random
 import subprocess
 import sys
 
@@ -198,3 +199,96 @@ def test_calls_without_a_device_return_a_status(L):
     r = subprocess.run([sys.executable, "-c", _CALL_WITHOUT_A_DEVICE], cwd=root, capture_output=True, text=True,
                        timeout=300)
     assert r.returncode == 0, (r.returncode, r.stderr[-2000:])
+
+
+def _adamw_list(L, *tensors):
+    """The status of a step over tensors given as dicts of addresses, as a list or one of many others."""
+    from vocab_ce_gb300._lib import AdamwTensor
+    return L.tp_adamw_step((AdamwTensor * len(tensors))(*(AdamwTensor(**t) for t in tensors)), len(tensors), 1e-3, 0.9,
+                           0.999, 1e-8, 1, 1.0, None, None)
+
+
+def _adamw_tensor(at, n=300, bits=8, p_dtype=0, g_dtype=0):
+    """Every part in a place of its own, 1 MB apart from `at` MB on."""
+    names = ["p", "g", "m", "v"] + (["m_scale", "v_scale"] if bits == 8 else []) + (["master"] if p_dtype == 0 else [])
+    return dict({k: (at + i) << 20 for i, k in enumerate(names)}, n=n, weight_decay=0.0, p_dtype=p_dtype,
+                g_dtype=g_dtype, state_bits=bits)
+
+
+@pytest.mark.parametrize("others", [0, 3, 30])
+def test_adamw_refuses_what_would_be_written_twice(L, others):
+    # the others make the list long enough for every way of the check, and stand in no order
+    rest = [_adamw_tensor(1000 + 10 * ((7 * i) % others), 1 + 37 * i, (8, 32)[i % 2], i // 2 % 2) for i in range(others)]
+
+    def refused(*tensors, says):
+        for order in (tensors, tensors[::-1]):
+            for at in {0, len(rest) // 2, len(rest)}:
+                assert _adamw_list(L, *rest[:at], *order, *rest[at:]) == INVALID, says
+                text = L.tpce_last_error().decode()
+                assert "overlaps" in text and all(w in text for w in says), (text, says)
+
+    for bits in (8, 32):
+        for p_dtype in (0, 1):
+            a, b = _adamw_tensor(1, 300, bits, p_dtype), _adamw_tensor(100, 300, bits, p_dtype)
+            written = [k for k in a if k in ("p", "m", "v", "m_scale", "v_scale", "master")]
+            state, value, grad = (1, 2, 2) if bits == 8 else (4, 2, 2)
+            size = {"p": 300 * (2 if p_dtype == 0 else 4), "m": 300 * state, "v": 300 * state, "m_scale": 12,
+                    "v_scale": 12, "master": 1200, "g": 600}
+            for k in written:
+                refused(a, dict(b, **{k: a[k]}), says=[k])                              # the same place
+                refused(a, dict(b, p=a[k] + size[k] // 2 // 16 * 16), says=[k, "p"])    # inside it
+                refused(a, dict(b, g=a[k]), says=[k, "g"])                              # read while it is written
+                refused(dict(a, **{k: a["g"] + 592}), says=[k, "g"])                    # the last values of its own
+            refused(dict(a, v=a["m"]), says=["m", "v"])
+            refused(a, dict(b, p=a["m"] - 304), says=["p", "m"])                        # from before it into it
+            # a large one around small ones
+            refused(_adamw_tensor(1, (8 << 20), bits, p_dtype), b, says=["overlaps"])
+
+
+def test_adamw_accepts_neighbours_and_shared_gradients(L):
+    # side by side without a gap, in either order; one gradient for several parameters: what comes next is the launch,
+    # which fails where there is no device
+    if torch.cuda.is_available():
+        pytest.skip("the pointers are not memory: only where no launch can begin")
+    for count in (1, 2, 20, 100):
+        at, list_ = 1 << 20, []
+        for i in range(count):
+            n, t = 16 * (1 + i % 9), dict(weight_decay=0.0, p_dtype=0, g_dtype=0, state_bits=8, n=16 * (1 + i % 9))
+            for k, size in (("p", 2 * n), ("master", 4 * n), ("m", n), ("v", n), ("m_scale", 16), ("v_scale", 16)):
+                t[k] = at
+                at += size
+            list_.append(t)
+        for t in list_:
+            t["g"] = at
+        for order in (list_, list_[::-1], list_[::2] + list_[1::2]):
+            assert _adamw_list(L, *order) == 5, L.tpce_last_error()
+
+
+def test_adamw_overlaps_of_random_lists(L):
+    # against every pair compared
+    if torch.cuda.is_available():
+        pytest.skip("the pointers are not memory: only where no launch can begin")
+    rng = random.Random(0)
+    seen = [0, 0]
+    for _ in range(400):
+        count, room = rng.choice([1, 2, 5, 12, 40]), rng.choice([20, 2000, 40_000])
+        list_, ranges = [], []
+        for i in range(count):
+            n, bits = rng.randint(0, 400), rng.choice([8, 32])
+            t = dict(n=n, weight_decay=0.0, p_dtype=rng.randint(0, 1), g_dtype=rng.randint(0, 1), state_bits=bits)
+            state, scales = (1, 4 * -(-n // 128)) if bits == 8 else (4, 0)
+            sizes = {"p": n * (2, 4)[t["p_dtype"]], "m": n * state, "v": n * state, "g": n * (2, 4)[t["g_dtype"]],
+                     "m_scale": scales, "v_scale": scales}
+            if t["p_dtype"] == 0 and rng.random() < 0.5:
+                sizes["master"] = 4 * n
+            for k, size in sizes.items():
+                t[k] = (1 << 24) + 16 * rng.randrange(room) + 16 * room * i * (rng.random() < 0.7)
+                if size:
+                    ranges.append((t[k], t[k] + size, k == "g"))
+            list_.append(t)
+        bad = any(a[0] < b[1] and b[0] < a[1] and not (a[2] and b[2])
+                  for i, a in enumerate(ranges) for b in ranges[:i])
+        want = INVALID if bad else 5 if ranges else 0
+        assert _adamw_list(L, *list_) == want, L.tpce_last_error()
+        seen[bad] += 1
+    assert min(seen) > 40, seen

@@ -431,23 +431,26 @@ PyObject *adamw_step(PyObject *const *a) {
         }
         e.weight_decay = one ? wd : number(decay[i]);
     }
-    // no value may be updated twice: the tensors' addresses in order
-    std::vector<std::pair<void *, Py_ssize_t>> order;
-    order.reserve(t.size());
-    for (Py_ssize_t i = 0; i < n; ++i)
-        if (t[static_cast<size_t>(i)].n) order.emplace_back(t[static_cast<size_t>(i)].p, i);
-    std::sort(order.begin(), order.end());
-    for (size_t i = 1; i < order.size(); ++i)
-        if (order[i].first == order[i - 1].first) throw Refused{place("params", order[i].second) + " is in the list twice"};
     const float *scalars = nullptr;
     if (!none(a[11])) {
         const at::Tensor &x = tensor(a[11], "scalars");
         need(x, "scalars", at::kFloat, {4});
         scalars = static_cast<const float *>(x.data_ptr());
     }
-    raise_on(api.adamw_step(t.data(), static_cast<int>(n), number(a[5]), number(a[7]), number(a[8]), number(a[9]),
-                            integer(a[6]), number(a[10]), scalars, n ? stream() : nullptr),
-             "tp_adamw_step");
+    const tpce_status st =
+        api.adamw_step(t.data(), static_cast<int>(n), number(a[5]), number(a[7]), number(a[8]), number(a[9]),
+                       integer(a[6]), number(a[10]), scalars, n ? stream() : nullptr);
+    if (st == TPCE_ERR_INVALID) {
+        // the commonest overlap by its name: the parameters' addresses in order
+        std::vector<std::pair<void *, Py_ssize_t>> order;
+        for (Py_ssize_t i = 0; i < n; ++i)
+            if (t[static_cast<size_t>(i)].n) order.emplace_back(t[static_cast<size_t>(i)].p, i);
+        std::sort(order.begin(), order.end());
+        for (size_t i = 1; i < order.size(); ++i)
+            if (order[i].first == order[i - 1].first)
+                throw Refused{place("params", order[i].second) + " is in the list twice"};
+    }
+    raise_on(st, "tp_adamw_step");
     Py_RETURN_NONE;
 }
 
