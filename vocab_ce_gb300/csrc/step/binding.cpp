@@ -129,13 +129,31 @@ at::Tensor empty(at::IntArrayRef shape, at::ScalarType dtype, const at::Tensor &
     return at::detail::empty_cuda(shape, dtype, like.device(), std::nullopt);
 }
 
+// A call has written to x in place: what autograd has saved of it is no longer that.
+// (Tensors of inference mode have no version.)
+void changed(c10::TensorImpl *x) {
+    if (!x->is_inference()) x->bump_version();
+}
+
 // The caller's output, checked, or a new one.
-at::Tensor output(PyObject *given, const char *name, at::IntArrayRef shape, at::ScalarType dtype,
-                  const at::Tensor &like) {
-    if (none(given)) return empty(shape, dtype, like);
+struct Output {
+    at::Tensor x;
+    bool given = false;
+    operator const at::Tensor &() const { return x; }
+    void written() const {
+        if (given) changed(x.unsafeGetTensorImpl());
+    }
+};
+Output output(PyObject *given, const char *name, at::IntArrayRef shape, at::ScalarType dtype, const at::Tensor &like) {
+    if (none(given)) return {empty(shape, dtype, like)};
     const at::Tensor &x = tensor(given, name);
     need(x, name, dtype, shape);
-    return x;
+    return {x, true};
+}
+// after a call that did not fail
+template <typename... O>
+void written(const O &...outputs) {
+    (outputs.written(), ...);
 }
 // A dict's entry, borrowed; NULL where there is none. Keys are interned once.
 struct Key {
@@ -205,7 +223,8 @@ PyObject *rmsnorm_forward(PyObject *const *a) {
     need(w, "w", at::kFloat, {h});
     const bool residual = !none(a[2]), quantize = truth(a[4]), want_Y = truth(a[5]);
     const double eps = number(a[3]);
-    at::Tensor R, S, Y, Q, Qs;
+    at::Tensor R;
+    Output S, Y, Q, Qs;
     if (residual) {
         R = tensor(a[2], "R");
         need(R, "R", X.scalar_type(), X.sizes());
@@ -214,7 +233,7 @@ PyObject *rmsnorm_forward(PyObject *const *a) {
     Results res;
     if (residual) res.add(keys->S, S = output(entry(a[6], keys->S), "S", X.sizes(), X.scalar_type(), X));
     if (want_Y) res.add(keys->Y, Y = output(entry(a[6], keys->Y), "Y", X.sizes(), X.scalar_type(), X));
-    const at::Tensor rstd = output(entry(a[6], keys->rstd), "rstd", {T}, at::kFloat, X);
+    const Output rstd = output(entry(a[6], keys->rstd), "rstd", {T}, at::kFloat, X);
     res.add(keys->rstd, rstd);
     if (quantize) {
         res.add(keys->Q, Q = output(entry(a[6], keys->Q), "Q", X.sizes(), at::kFloat8_e4m3fn, X));
@@ -223,6 +242,7 @@ PyObject *rmsnorm_forward(PyObject *const *a) {
     raise_on(api.rmsnorm_forward(ptr(X), ptr(R), fptr(w), T, h, static_cast<float>(eps), dt, ptr(S), ptr(Y), ptr(Q),
                                  fptr(Qs), fptr(rstd), stream()),
              "tp_rmsnorm_forward");
+    written(S, Y, Q, Qs, rstd);
     return res.take();
 }
 
@@ -235,13 +255,14 @@ PyObject *rmsnorm_backward(PyObject *const *a) {
     need(dY, "dY", S.scalar_type(), S.sizes());
     need(w, "w", at::kFloat, {h});
     need(rstd, "rstd", at::kFloat, {T});
-    at::Tensor dS, dw, ws;
+    at::Tensor dS, ws;
+    Output dw;
     if (!none(a[4])) {
         dS = tensor(a[4], "dS");
         need(dS, "dS", S.scalar_type(), S.sizes());
     }
     Results res;
-    const at::Tensor dX = output(entry(a[6], keys->dX), "dX", S.sizes(), S.scalar_type(), S);
+    const Output dX = output(entry(a[6], keys->dX), "dX", S.sizes(), S.scalar_type(), S);
     res.add(keys->dX, dX);
     if (truth(a[5])) {
         res.add(keys->dw, dw = output(entry(a[6], keys->dw), "dw", {h}, at::kFloat, S));
@@ -250,6 +271,7 @@ PyObject *rmsnorm_backward(PyObject *const *a) {
     raise_on(api.rmsnorm_backward(ptr(dY), ptr(S), fptr(w), fptr(rstd), ptr(dS), T, h, dt, ptr(dX), fptr(dw), ptr(ws),
                                   bytes_of(ws), stream()),
              "tp_rmsnorm_backward");
+    written(dX, dw);
     return res.take();
 }
 
@@ -262,17 +284,18 @@ PyObject *expert_plan(PyObject *const *a) {
     const int64_t T = ids.size(0), k = ids.size(1), E = integer(a[1]);
     if (E < 1 || E >= (1 << 30)) throw Refused{"experts must be at least 1"};
     Results res;
-    const at::Tensor row = output(entry(a[2], keys->row), "row", ids.sizes(), at::kInt, ids);
+    const Output row = output(entry(a[2], keys->row), "row", ids.sizes(), at::kInt, ids);
     res.add(keys->row, row);
-    const at::Tensor source = output(entry(a[2], keys->source), "source", {T * k}, at::kInt, ids);
+    const Output source = output(entry(a[2], keys->source), "source", {T * k}, at::kInt, ids);
     res.add(keys->source, source);
-    const at::Tensor offsets = output(entry(a[2], keys->offsets), "offsets", {E + 1}, at::kInt, ids);
+    const Output offsets = output(entry(a[2], keys->offsets), "offsets", {E + 1}, at::kInt, ids);
     res.add(keys->offsets, offsets);
     const int choices = static_cast<int>(std::min<int64_t>(k, 1 << 30));
     const at::Tensor ws = workspace(a[3], api.expert_plan_workspace_bytes(T, choices, static_cast<int>(E)), ids);
     raise_on(api.expert_plan(iptr(ids), T, choices, static_cast<int>(E), iptr(row), iptr(source), iptr(offsets),
                              ptr(ws), bytes_of(ws), stream()),
              "tp_expert_plan");
+    written(row, source, offsets);
     return res.take();
 }
 
@@ -303,10 +326,11 @@ PyObject *expert_dispatch_forward(PyObject *const *a) {
     const int dt = matrix(X, "X");
     const int64_t h = X.size(1);
     need(X, "X", X.scalar_type(), {p.T, h});
-    const at::Tensor Xs = output(a[2], "Xs", {p.row.numel(), h}, X.scalar_type(), X);
+    const Output Xs = output(a[2], "Xs", {p.row.numel(), h}, X.scalar_type(), X);
     raise_on(api.expert_dispatch_forward(ptr(X), iptr(p.row), iptr(p.offsets), p.T, h, p.k, p.E, dt, ptr(Xs), stream()),
              "tp_expert_dispatch_forward");
-    return THPVariable_Wrap(Xs);
+    written(Xs);
+    return THPVariable_Wrap(Xs.x);
 }
 
 // dXs, plan, out
@@ -316,10 +340,11 @@ PyObject *expert_dispatch_backward(PyObject *const *a) {
     const int dt = matrix(dXs, "dXs");
     const int64_t h = dXs.size(1);
     need(dXs, "dXs", dXs.scalar_type(), {p.row.numel(), h});
-    const at::Tensor dX = output(a[2], "dX", {p.T, h}, dXs.scalar_type(), dXs);
+    const Output dX = output(a[2], "dX", {p.T, h}, dXs.scalar_type(), dXs);
     raise_on(api.expert_dispatch_backward(ptr(dXs), iptr(p.row), p.T, h, p.k, dt, ptr(dX), stream()),
              "tp_expert_dispatch_backward");
-    return THPVariable_Wrap(dX);
+    written(dX);
+    return THPVariable_Wrap(dX.x);
 }
 
 // Ys, plan, weights, out
@@ -330,10 +355,11 @@ PyObject *expert_combine_forward(PyObject *const *a) {
     const int64_t h = Ys.size(1);
     need(Ys, "Ys", Ys.scalar_type(), {p.row.numel(), h});
     need(weights, "weights", at::kFloat, p.row.sizes());
-    const at::Tensor Z = output(a[3], "Z", {p.T, h}, Ys.scalar_type(), Ys);
+    const Output Z = output(a[3], "Z", {p.T, h}, Ys.scalar_type(), Ys);
     raise_on(api.expert_combine_forward(ptr(Ys), iptr(p.row), fptr(weights), p.T, h, p.k, dt, ptr(Z), stream()),
              "tp_expert_combine_forward");
-    return THPVariable_Wrap(Z);
+    written(Z);
+    return THPVariable_Wrap(Z.x);
 }
 
 // dZ, Ys, plan, weights, out
@@ -346,13 +372,14 @@ PyObject *expert_combine_backward(PyObject *const *a) {
     need(Ys, "Ys", dZ.scalar_type(), {p.row.numel(), h});
     need(weights, "weights", at::kFloat, p.row.sizes());
     Results res;
-    const at::Tensor dYs = output(entry(a[4], keys->dYs), "dYs", Ys.sizes(), dZ.scalar_type(), dZ);
+    const Output dYs = output(entry(a[4], keys->dYs), "dYs", Ys.sizes(), dZ.scalar_type(), dZ);
     res.add(keys->dYs, dYs);
-    const at::Tensor dw = output(entry(a[4], keys->dweights), "dweights", p.row.sizes(), at::kFloat, dZ);
+    const Output dw = output(entry(a[4], keys->dweights), "dweights", p.row.sizes(), at::kFloat, dZ);
     res.add(keys->dweights, dw);
     raise_on(api.expert_combine_backward(ptr(dZ), ptr(Ys), iptr(p.row), iptr(p.offsets), fptr(weights), p.T, h, p.k,
                                          p.E, dt, ptr(dYs), fptr(dw), stream()),
              "tp_expert_combine_backward");
+    written(dYs, dw);
     return res.take();
 }
 
@@ -389,6 +416,10 @@ PyObject *adamw_step(PyObject *const *a) {
     const double wd = one ? number(a[4]) : 0.0;
 
     std::vector<tpce_adamw_tensor> t(static_cast<size_t>(n));
+    // What a backward pass may have saved: parameters and masters, kept by the list's own references. The states are
+    // the step's alone (with them it is 500 counters for 100 tensors, and 4 us more).
+    std::vector<c10::TensorImpl *> updated;
+    updated.reserve(static_cast<size_t>(n) * 2);
     const int dev = n && THPVariable_Check(params[0]) && THPVariable_Unpack(params[0]).is_cuda()
                         ? c10::cuda::current_device() : -1;
     // names are put together only for a message
@@ -400,6 +431,12 @@ PyObject *adamw_step(PyObject *const *a) {
             need(x, place(name, i), &dtype, &shape);
         return x.data_ptr();
     };
+    // the same of a value that autograd may know
+    auto update = [&](PyObject *o, const char *name, Py_ssize_t i, at::ScalarType dtype, at::IntArrayRef shape) {
+        void *at = take(o, name, i, dtype, shape);
+        updated.push_back(THPVariable_Unpack(o).unsafeGetTensorImpl());
+        return at;
+    };
     for (Py_ssize_t i = 0; i < n; ++i) {
         tpce_adamw_tensor &e = t[static_cast<size_t>(i)];
         const at::Tensor &p = tensor(params[i], "params"), &g = tensor(grads[i], "grads");
@@ -409,9 +446,9 @@ PyObject *adamw_step(PyObject *const *a) {
         PyObject *master = none(a[3]) ? Py_None : masters[i];
         if (!none(master) && e.p_dtype == TPCE_F32) 
             throw Refused{place("masters", i) + ": " + place("params", i) + " is fp32 already"};
-        e.p = take(params[i], "params", i, p.scalar_type(), shape);
+        e.p = update(params[i], "params", i, p.scalar_type(), shape);
         e.g = take(grads[i], "grads", i, g.scalar_type(), shape);
-        e.master = none(master) ? nullptr : take(master, "masters", i, at::kFloat, shape);
+        e.master = none(master) ? nullptr : update(master, "masters", i, at::kFloat, shape);
         PyObject *st = states[i];
         if (!PyDict_Check(st)) throw Refused{place("states", i) + " must be a dict (adamw_state)"};
         e.n = p.numel();
@@ -451,6 +488,7 @@ PyObject *adamw_step(PyObject *const *a) {
                 throw Refused{place("params", order[i].second) + " is in the list twice"};
     }
     raise_on(st, "tp_adamw_step");
+    for (c10::TensorImpl *x : updated) changed(x);
     Py_RETURN_NONE;
 }
 
