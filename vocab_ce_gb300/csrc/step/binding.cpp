@@ -202,7 +202,11 @@ at::Tensor workspace(PyObject *given, size_t bytes, const at::Tensor &like) {
 }
 size_t bytes_of(const at::Tensor &x) { return x.defined() ? x.nbytes() : 0; }
 
-bool truth(PyObject *o) { return PyObject_IsTrue(o) == 1; }
+bool truth(PyObject *o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw Raised{};
+    return v == 1;
+}
 double number(PyObject *o) {
     const double v = PyFloat_AsDouble(o);
     if (v == -1.0 && PyErr_Occurred()) throw Raised{};
