@@ -24,14 +24,14 @@ from typing import Dict, Optional, Sequence, Union
 import torch
 
 from ._lib import check, lib
+from .build import binding_path
 
 GROUP = 128  # values that share one scale in the 8-bit formats
 
-BINDING_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "lib", "_step_binding.so")
 # the library's entry points that the binding calls, in its order
 _ENTRIES = ("tpce_rmsnorm_workspace_bytes", "tp_rmsnorm_forward", "tp_rmsnorm_backward",
-            "tpce_expert_plan_workspace_bytes", "tp_expert_plan", "tp_expert_dispatch_forward", "tp_expert_dispatch_backward", "tp_expert_combine_forward",
-            "tp_expert_combine_backward", "tp_adamw_step")
+            "tpce_expert_plan_workspace_bytes", "tp_expert_plan", "tp_expert_dispatch_forward",
+            "tp_expert_dispatch_backward", "tp_expert_combine_forward", "tp_expert_combine_backward", "tp_adamw_step")
 _lock = threading.Lock()
 _binding = None
 
@@ -45,10 +45,11 @@ def _load():
     global _binding
     with _lock:
         if _binding is None:
-            if not os.path.exists(BINDING_PATH):
-                raise RuntimeError(f"the step binding is not built ({BINDING_PATH}); run "
+            path = binding_path()
+            if not os.path.exists(path):
+                raise RuntimeError(f"the step binding is not built for this torch and Python ({path}); run "
                                    "`python -m vocab_ce_gb300.build`")
-            spec = importlib.util.spec_from_file_location("_step_binding", BINDING_PATH)
+            spec = importlib.util.spec_from_file_location("_step_binding", path)
             module = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(module)
             library = lib()
