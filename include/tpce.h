@@ -556,7 +556,8 @@ tpce_status tp_expert_combine_backward(const void *dZ, const void *Ys, const int
  * an fp32 master: then the master is what is updated and p its rounding.
  * state_bits 32: m, v fp32 [n]. state_bits 8: m and r = sqrt(v) as e4m3 codes
  * [n] with fp32 scales [ceil(n / 128)], one per 128 values of the flat tensor,
- * as Q of tp_rmsnorm_forward; v then points to r's codes and v_scale to their
+ * as Q of tp_rmsnorm_forward, but that a root which is not zero gets at least
+ * the smallest code, 2^-9; v then points to r's codes and v_scale to their
  * scales. Codes and scales of zero bytes are a zero state. The update uses the
  * moments before they are rounded.
  * `tensors` is a host array, read during the call; tensors with n == 0 are

@@ -8,6 +8,10 @@
 // (vec.cuh). The root, not v: e4m3 spans a factor of 2^18 between a group's
 // largest and smallest value, which in v would leave only 2^9 in the root that
 // the update divides by. The update uses the new moments before they are rounded.
+// A root that is not zero gets no code of zero: its m has a scale of its own and may
+// survive, and the next step would divide it by that step's gradient alone, or by eps
+// (gradients present one step in twenty, spread over three decades: steps of 2.1 lr in
+// 32 bits, and of 8.5, 85 and 850 lr at gradients of 0.1, 1 and 10 without this).
 //
 // Every product and sum is rounded on its own (no contraction to a fused
 // multiply-add), so that a step gives the same bits wherever a tensor lies in
@@ -227,7 +231,7 @@ __device__ __forceinline__ void run(const Scalars &k, const Rates &c, const Entr
         if (S8) {
             // values past the end have no gradient and no moments: they stay zero and leave the scale alone
             float ms, rs;
-            const uint2 mq = quantize8(m, ms), rq = quantize8(r, rs);
+            const uint2 mq = quantize8(m, ms), rq = quantize8<16, true>(r, rs);
             if (i < n) {
                 put_codes(e.m, i, n, mq);
                 put_codes(e.v, i, n, rq);

@@ -135,7 +135,7 @@ __device__ __forceinline__ void load8f(const float *p, float (&v)[8]) {
 // lower bound keeps 1 / scale finite (a group of zeros needs no special case).
 // NaN and infinity become the NaN code: a saturated code would hide them.
 constexpr int kGroup = 128;
-constexpr float kE4m3Max = 448.0f;
+constexpr float kE4m3Max = 448.0f, kE4m3Least = 1.0f / 512.0f;
 
 __device__ __forceinline__ float group_scale(float amax) { return fmaxf(__fmul_rn(amax, 1.0f / kE4m3Max), FLT_MIN); }
 
@@ -144,8 +144,9 @@ __device__ __forceinline__ float group_scale(float amax) { return fmaxf(__fmul_r
 // calls it (values past an end: zeros). fmaxf
 // passes over NaN, whose product and code are NaN by themselves; infinities,
 // which would spoil the scale and saturate, are looked for only in a warp
-// whose maximum shows one.
-template <int LANES = 16>
+// whose maximum shows one. DIVISOR: none of the values is negative, and one that is
+// not zero gets no code below the smallest, 2^-9: what divides by it stays bounded.
+template <int LANES = 16, bool DIVISOR = false>
 __device__ __forceinline__ uint2 quantize8(const float (&v)[8], float &scale) {
     float a = 0.0f;
 #pragma unroll
@@ -171,6 +172,16 @@ __device__ __forceinline__ uint2 quantize8(const float (&v)[8], float &scale) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (!(fabsf(v[i]) <= FLT_MAX)) t[i] = __int_as_float(0x7fffffff);
+    }
+    if (DIVISOR) {
+        float least = t[0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) least = fminf(least, t[i]);
+        if (least < kE4m3Least) {  // few threads: a value below 4e-6 of the group's largest, or none
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (v[i] > 0.0f && t[i] < kE4m3Least) t[i] = kE4m3Least;
+        }
     }
     uint32_t w[4];
 #pragma unroll
