@@ -560,6 +560,15 @@ tpce_status tp_expert_combine_backward(const void *dZ, const void *Ys, const int
  * the smallest code, 2^-9; v then points to r's codes and v_scale to their
  * scales. Codes and scales of zero bytes are a zero state. The update uses the
  * moments before they are rounded.
+ * r is rounded to the nearest code; with state_bits 8 | TPCE_ADAMW_RANDOM to
+ * one of the two codes around it, so that its expectation is r (the choice is a
+ * hash of the value, its place in the tensor and the step: equal calls give
+ * equal bits). To nearest, while a group's largest root stays, another of its
+ * roots does not grow before its gradients are
+ *   sqrt(((17/16)^2 - beta2) / (1 - beta2))
+ * times it: 11.4 at beta2 = 0.999, 3.7 at 0.99, 1.9 at 0.95. Updates are too
+ * large by up to that factor where gradients have grown. Round at random for a
+ * beta2 near 1.
  * `tensors` is a host array, read during the call; tensors with n == 0 are
  * skipped (their pointers may be NULL). Every device pointer is 16-byte
  * aligned, and what is written overlaps nothing else of the list: a state, a
@@ -575,6 +584,8 @@ tpce_status tp_expert_combine_backward(const void *dZ, const void *Ys, const int
  * overlap; TPCE_ERR_WORKSPACE if the host has no memory for the list's check.
  * Everything is checked before the first launch.
  * ------------------------------------------------------------------------- */
+#define TPCE_ADAMW_RANDOM 256
+
 typedef struct {
     void *p;             /* [n] p_dtype */
     void *master;        /* [n] fp32, or NULL; only with a bf16 p */
@@ -587,7 +598,7 @@ typedef struct {
     double weight_decay;
     int p_dtype;         /* TPCE_BF16 or TPCE_F32 */
     int g_dtype;
-    int state_bits;      /* 8 or 32 */
+    int state_bits;      /* 8, 32, or 8 | TPCE_ADAMW_RANDOM */
     int reserved;
 } tpce_adamw_tensor;
 

@@ -67,3 +67,190 @@ def test_a_root_that_is_not_zero_keeps_a_code(n, p_dtype, master):
     tp.adamw_step([p], [zero + 1e-15], [st], lr=1e-3, step=2)
     assert bool((st["r_q"].float() == 448.0).all()) and math.isclose(float(st["r_scale"][0]) * 448.0,
                                                                      1e-15 * math.sqrt(1 - 0.999), rel_tol=1e-5)
+
+
+# ------------------------------------------------------------------ how far a root may lag
+def roots(st):
+    """A state's roots, and their scales spread over the values."""
+    if "v" in st:
+        return st["v"].sqrt(), None
+    n = st["r_q"].numel()
+    s = st["r_scale"].repeat_interleave(128)[:n]
+    return st["r_q"].float() * s, s
+
+
+def lag(beta2):
+    """Rounded to nearest, a root that stays has (17/16 r)^2 >= beta2 r^2 + (1 - beta2) g^2: half a step of a code is
+    at most 1/16 of it. So r >= g times this."""
+    return math.sqrt((1.0 - beta2) / ((17.0 / 16.0) ** 2 - beta2))
+
+
+@pytest.mark.parametrize("beta2", [0.95, 0.99, 0.999])
+@pytest.mark.parametrize("p_dtype,master", [(F32, False), (BF, True)])
+def test_rounded_to_nearest_a_root_lags_no_further_than_stated(beta2, p_dtype, master):
+    gpu_or_skip()
+    n, steps = 100 * 128, 3000
+    size = 10.0 ** (-2.0 - torch.rand(n, generator=generator(1), device="cuda"))
+    size[0::128] = 1.0
+    sign = torch.where(torch.rand(n, generator=generator(2), device="cuda") < 0.5, 1.0, -1.0)
+    p32 = torch.zeros(n, device="cuda")
+    p, held = (p32.to(p_dtype), p32) if master else (p32, None)
+    st = tp.adamw_state(p, 8)
+    for t in range(1, 2 * steps + 1):
+        if t == steps + 1:
+            size[size < 0.5] *= 20.0    # still below the largest
+        p.zero_()
+        p32.zero_()
+        tp.adamw_step([p], [sign * size], [st], lr=1.0, step=t, beta2=beta2, masters=[held])
+    r, _ = roots(st)
+    assert bool((r >= 0.99 * lag(beta2) * size).all()), float((r / size).min())
+    # the steps: of 1 lr with roots that are right; the moment is off by at most 1/16 of nine tenths of itself
+    assert float(p32.abs().max()) <= 1.07 / lag(beta2)
+
+
+def run_noise(bits, rounding, beta2, steps=3000, groups=100):
+    """Normal gradients whose size grows by 5 halfway, but for each group's largest; the state and the last step."""
+    g, n = generator(3), groups * 128
+    size = 10.0 ** (-1.0 - torch.rand(n, generator=g, device="cuda"))
+    size[0::128] = 1.0
+    p = torch.zeros(n, device="cuda")
+    st = tp.adamw_state(p, bits)
+    for t in range(1, 2 * steps + 1):
+        if t == steps + 1:
+            size = torch.where(size < 0.5, 5.0 * size, size)
+        p.zero_()
+        tp.adamw_step([p], [size * torch.randn(n, generator=g, device="cuda")], [st], lr=1.0, step=t, beta2=beta2,
+                      rounding=rounding)
+    return roots(st)[0], p
+
+
+@pytest.mark.parametrize("beta2", [0.95, 0.99, 0.999])
+def test_rounded_at_random_roots_and_steps_follow_the_gradients(beta2):
+    """The expectation of a root is the exact one's, so its median stays near it (simulated on the CPU beforehand: 0.98
+    to 1.00, and 0.38 rounded to nearest with beta2 = 0.999); an update divides by it."""
+    gpu_or_skip()
+    want, step = run_noise(32, "nearest", beta2)
+    r, moved = run_noise(8, "random", beta2)
+    assert 0.9 <= float((r / want).median()) <= 1.1
+    ratio = (moved / step)[step.abs() > 1e-2]
+    assert 0.85 <= float(ratio.median()) <= 1.2
+
+
+# ------------------------------------------------------------------ random rounding, one step
+def state8(n, seed, spread=3.0):
+    """Codes and scales as steps leave them: the largest of a group at code 448."""
+    from test_gpu_step_adamw import quantize
+    size = 10.0 ** (-spread * torch.rand(n, generator=generator(seed), device="cuda"))
+    m = 1e-3 * size * torch.randn(n, generator=generator(seed + 1), device="cuda")
+    r = 1e-3 * size * (0.5 + torch.rand(n, generator=generator(seed + 2), device="cuda"))
+    (mq, ms), (rq, rs) = quantize(m), quantize(r)
+    g = 1e-3 * size * torch.randn(n, generator=generator(seed + 3), device="cuda")
+    return {"m_q": mq, "m_scale": ms, "r_q": rq, "r_scale": rs}, g
+
+
+def copy(st):
+    return {k: v.clone() for k, v in st.items()}
+
+
+def same(a, b):
+    return all(torch.equal(a[k].view(torch.uint8), b[k].view(torch.uint8)) for k in a)
+
+
+@pytest.mark.parametrize("spread", [0.0, 3.0, 5.0])
+def test_a_random_code_is_a_neighbour_and_right_on_average(spread):
+    gpu_or_skip()
+    n = 1 << 20
+    st, g = state8(n, 10, spread)
+    m = st["m_q"].float() * st["m_scale"].repeat_interleave(128)
+    r = st["r_q"].float() * st["r_scale"].repeat_interleave(128)
+    exact = {"m": m, "v": r * r}                       # the same step with its roots left in 32 bits
+    near, rand = copy(st), copy(st)
+    p = [torch.zeros(n, device="cuda") for _ in range(3)]
+    for x, s, how in zip(p, (exact, near, rand), ("nearest", "nearest", "random")):
+        tp.adamw_step([x], [g], [s], lr=1e-3, step=5, rounding=how)
+    # nothing but the roots' codes differs
+    assert torch.equal(p[0], p[1]) and torch.equal(p[0], p[2])
+    assert same({k: near[k] for k in ("m_q", "m_scale", "r_scale")}, {k: rand[k] for k in ("m_q", "m_scale", "r_scale")})
+    t = exact["v"].double().sqrt() / rand["r_scale"].double().repeat_interleave(128)
+    q = rand["r_q"].double()
+    step = torch.exp2(t.log2().floor().clamp_min(-6.0) - 3.0)
+    off = (q - t) / step
+    inside = (t > LEAST) & (t < 447.0)                 # below: the smallest code; above: the largest
+    assert bool((off[inside].abs() < 1.0 + 1e-5).all())
+    assert bool((q[t <= LEAST] == LEAST).all()) and bool((q[t >= 447.0] >= 416.0).all())
+    # each is off by less than a step with mean 0: the mean of N is within 5 / sqrt(12 N) or so of 0
+    count = int(inside.sum())
+    assert abs(float(off[inside].mean())) <= 5.0 * 0.5 / math.sqrt(count)
+    for lo in (0.0, 0.25, 0.5, 0.75):                  # wherever between the codes the value lies
+        part = inside & ((t / step).frac() >= lo) & ((t / step).frac() < lo + 0.25)
+        count = int(part.sum())                        # (a step of beta2 = 0.999 moves few roots far)
+        assert count == 0 or abs(float(off[part].mean())) <= 5.0 * 0.5 / math.sqrt(count)
+
+
+def test_random_rounding_repeats_itself_and_varies_with_the_step():
+    gpu_or_skip()
+    sizes = [5, 128, 700, 2053, 300, 4096]
+    made = [state8(n, 20 + i) for i, n in enumerate(sizes)]
+
+    def run(which, step=9, rounding="random"):
+        sts = [copy(made[i][0]) for i in which]
+        ps = [torch.zeros(sizes[i], device="cuda") for i in which]
+        tp.adamw_step(ps, [made[i][1] for i in which], sts, lr=1e-3, step=step, rounding=rounding)
+        return sts
+
+    whole = run(range(6))
+    assert all(same(a, b) for a, b in zip(whole, run(range(6))))
+    for i in range(6):
+        assert same(whole[i], run([i])[0])             # alone, and wherever it is in the list
+    assert same(whole[5], run([5, 2])[0])
+    other = run(range(6), step=10)
+    # where a value lies at f between two codes, two independent choices differ with 2 f (1 - f)
+    differ, chance = 0, 0.0
+    for (st, g), a, b in zip(made, whole, other):
+        n = g.numel()
+        r = st["r_q"].float() * st["r_scale"].repeat_interleave(128)[:n]
+        exact = {"m": torch.zeros(n, device="cuda"), "v": r * r}
+        tp.adamw_step([torch.zeros(n, device="cuda")], [g], [exact], lr=1e-3, step=9)
+        t = exact["v"].double().sqrt() / a["r_scale"].double().repeat_interleave(128)[:n]
+        f = (t / torch.exp2(t.log2().floor().clamp_min(-6.0) - 3.0)).frac()
+        chance += float((2.0 * f * (1.0 - f)).sum())
+        differ += int((a["r_q"].float() != b["r_q"].float()).sum())
+    assert chance > 50 and abs(differ - chance) <= 5.0 * math.sqrt(chance), (differ, chance)
+    assert any(not same(a, b) for a, b in zip(whole, run(range(6), rounding="nearest")))
+
+
+def test_random_rounding_leaves_zeros_nans_and_32_bits_alone():
+    gpu_or_skip()
+    n = 700
+    g = torch.randn(n, generator=generator(5), device="cuda")
+    g[3], g[200], g[500], g[128:136] = float("nan"), float("inf"), 1e-15, 0.0
+    states = [tp.adamw_state(g, 8), tp.adamw_state(g, 32)]
+    alone = tp.adamw_state(g, 32)
+    p = [torch.zeros(n, device="cuda") for _ in range(3)]
+    tp.adamw_step(p[:2], [g, g], states, lr=1e-3, step=1, rounding="random")
+    tp.adamw_step(p[2:], [g], [alone], lr=1e-3, step=1)
+    r, odd = states[0]["r_q"].float(), ~g.isfinite()
+    assert torch.equal(r.isnan(), odd) and bool((r[g == 0] == 0).all()) and float(r[500]) == LEAST
+    assert bool((r[~odd & (g != 0)] >= LEAST).all()) and bool(states[0]["r_scale"].isfinite().all())
+    assert same(states[1], alone) and torch.equal(p[1][~odd], p[2][~odd])
+
+
+def test_random_rounding_in_a_captured_step():
+    gpu_or_skip()
+    st, g = state8(3000, 30)
+    eager, captured = copy(st), copy(st)
+    p = [torch.zeros(3000, device="cuda") for _ in range(3)]
+    scalars = tp.adamw_scalars(1e-3, 6).cuda()
+    tp.adamw_step([p[0]], [g], [copy(st)], lr=1e-3, step=6, scalars=scalars, rounding="random")   # loads the kernel
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        tp.adamw_step([p[1]], [g], [captured], lr=1e-3, step=6, scalars=scalars, rounding="random")
+    graph.replay()
+    tp.adamw_step([p[2]], [g], [eager], lr=1e-3, step=6, rounding="random")
+    assert same(eager, captured)
+    for k, v in st.items():
+        captured[k].copy_(v)
+    scalars.copy_(tp.adamw_scalars(1e-3, 7))
+    graph.replay()                                     # another step's numbers: other codes
+    assert not same({"r_q": eager["r_q"]}, {"r_q": captured["r_q"]})

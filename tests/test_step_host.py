@@ -292,3 +292,14 @@ def test_adamw_overlaps_of_random_lists(L):
         assert _adamw_list(L, *list_) == want, L.tpce_last_error()
         seen[bad] += 1
     assert min(seen) > 40, seen
+
+
+def test_adamw_rounding_is_nearest_or_random(L):
+    import vocab_ce_gb300 as tp
+    for bits in (32 | 256, 16 | 256, 256, 8 | 512):
+        assert _adamw_list(L, dict(_adamw_tensor(1), state_bits=bits)) == INVALID, bits
+    t = dict(_adamw_tensor(1), state_bits=8 | 256)
+    assert _adamw_list(L, t, dict(_adamw_tensor(20), v=t["v"])) == INVALID and b"overlaps" in L.tpce_last_error()
+    assert _adamw_list(L, dict(t, m_scale=None)) == INVALID
+    with pytest.raises(ValueError, match="rounding"):
+        tp.adamw_step([], [], [], lr=1e-3, step=1, rounding="up")

@@ -13,6 +13,17 @@
 // (gradients present one step in twenty, spread over three decades: steps of 2.1 lr in
 // 32 bits, and of 8.5, 85 and 850 lr at gradients of 0.1, 1 and 10 without this).
 //
+// Roots are rounded to nearest, or at random where asked. To nearest, a root that a
+// step moves by less than half a code stays: with beta2 near 1 it does not grow with
+// its gradients until they are sqrt(((17/16)^2 - b2) / (1 - b2)) times it (11.4 at
+// 0.999, 3.7 at 0.99, 1.9 at 0.95) while its group's largest root stays, and its
+// updates are too large by up to that. (Gradients that grow by 5 beside a larger one,
+// b2 = 0.999: 3000 steps later the roots are 0.38 of what they should be, rounded at
+// random 0.98.) It shrinks no sooner, which makes steps small. At random it is the
+// hash of the value, its place and the step that decides, so a step repeats its bits:
+// 16 instructions a value (134 million with masters 368 us instead of 338, 42 million
+// without 114 instead of 98).
+//
 // Every product and sum is rounded on its own (no contraction to a fused
 // multiply-add), so that a step gives the same bits wherever a tensor lies in
 // the list and however its tail is handled, and the same as elementary 32-bit
@@ -54,7 +65,7 @@ constexpr int kChunk = kThreads * 8;  // values that a block takes at a time: 16
 constexpr int kSpan = 4;
 constexpr int64_t kSpanFrom = 152 * 32;
 
-enum : uint32_t { kParamBf16 = 1u, kMaster = 2u, kGradBf16 = 4u, kState8 = 8u };
+enum : uint32_t { kParamBf16 = 1u, kMaster = 2u, kGradBf16 = 4u, kState8 = 8u, kRandom = 16u };
 
 struct Entry {
     void *p, *master;
@@ -85,11 +96,13 @@ struct Scalars {
     float step_size;   // lr / (1 - b1^t)
     float root_scale;  // 1 / sqrt(1 - b2^t)
     float grad_scale;
+    uint32_t step;        // of the seed of random rounding
     const float *device;  // {step_size, root_scale, lr, grad_scale} on the device, or NULL
 };
 
 struct Rates {
     float step_size, root_scale, grad_scale, decay;
+    uint32_t seed;
 };
 
 // Two values' step; r becomes the root of the new v.
@@ -212,8 +225,8 @@ struct Inputs<P, G, true> {
 // The chunks from value i of this thread on, `left` of them. With 8-bit states
 // the arithmetic takes about as long as the bytes, so the next chunk's values are
 // on their way while one is computed.
-template <typename P, typename G, bool S8>
-__device__ __forceinline__ void run(const Scalars &k, const Rates &c, const Entry &e, int64_t i, int left) {
+template <typename P, typename G, bool S8, bool RANDOM>
+__device__ __forceinline__ void run_state(const Scalars &k, const Rates &c, const Entry &e, int64_t i, int left) {
     const int64_t n = e.n;
     const bool master = e.kind & kMaster;
     void *base = master ? e.master : e.p;
@@ -231,7 +244,8 @@ __device__ __forceinline__ void run(const Scalars &k, const Rates &c, const Entr
         if (S8) {
             // values past the end have no gradient and no moments: they stay zero and leave the scale alone
             float ms, rs;
-            const uint2 mq = quantize8(m, ms), rq = quantize8<16, true>(r, rs);
+            const uint2 mq = quantize8(m, ms),
+                        rq = quantize8<16, true, RANDOM>(r, rs, c.seed + static_cast<uint32_t>(i));
             if (i < n) {
                 put_codes(e.m, i, n, mq);
                 put_codes(e.v, i, n, rq);
@@ -249,15 +263,19 @@ __device__ __forceinline__ void run(const Scalars &k, const Rates &c, const Entr
     }
 }
 
-template <typename P, typename G>
+template <typename P, typename G, bool RANDOM>
 __device__ __forceinline__ void run(const Scalars &k, const Rates &c, const Entry &e, int64_t i, int left) {
-    if (e.kind & kState8)
-        run<P, G, true>(k, c, e, i, left);
+    if (RANDOM && (e.kind & kRandom))
+        run_state<P, G, true, true>(k, c, e, i, left);
+    else if (e.kind & kState8)
+        run_state<P, G, true, false>(k, c, e, i, left);
     else
-        run<P, G, false>(k, c, e, i, left);
+        run_state<P, G, false, false>(k, c, e, i, left);
 }
 
-template <int N>
+// RANDOM: some tensor of the list rounds at random; a kernel of its own, so that the
+// others' have no registers for it.
+template <int N, bool RANDOM>
 __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Table<N> table,
                                                          const __grid_constant__ Scalars k) {
     // this block's tensor: the last one that starts at or before it
@@ -275,37 +293,42 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     const int left = chunks < e.span ? static_cast<int>(chunks) : static_cast<int>(e.span);
     const int64_t i = first + threadIdx.x * 8;
     grid_begin();
-    Rates c{k.step_size, k.root_scale, k.grad_scale, e.decay};
+    Rates c{k.step_size, k.root_scale, k.grad_scale, e.decay, 0u};
     if (k.device) {
         c.step_size = k.device[0];
         c.root_scale = k.device[1];
         c.decay = __fsub_rn(1.0f, __fmul_rn(k.device[2], e.wd));
         c.grad_scale = k.device[3];
     }
+    // a captured step repeats k.step; its rates differ from step to step
+    if (RANDOM) c.seed = (k.step + __float_as_uint(c.step_size) * 3u + __float_as_uint(c.root_scale) * 5u) * 0xBB67AE85u;
     const bool narrow = (e.kind & kParamBf16) && !(e.kind & kMaster);
     if (e.kind & kGradBf16) {
         if (narrow)
-            run<__nv_bfloat16, __nv_bfloat16>(k, c, e, i, left);
+            run<__nv_bfloat16, __nv_bfloat16, RANDOM>(k, c, e, i, left);
         else
-            run<float, __nv_bfloat16>(k, c, e, i, left);
+            run<float, __nv_bfloat16, RANDOM>(k, c, e, i, left);
     } else {
         if (narrow)
-            run<__nv_bfloat16, float>(k, c, e, i, left);
+            run<__nv_bfloat16, float, RANDOM>(k, c, e, i, left);
         else
-            run<float, float>(k, c, e, i, left);
+            run<float, float, RANDOM>(k, c, e, i, left);
     }
 }
 
 template <int N>
-tpce_status launch_table(const Entry *entries, int count, uint32_t blocks, const Scalars &k, cudaStream_t s) {
+tpce_status launch_table(const Entry *entries, int count, uint32_t blocks, bool random, const Scalars &k,
+                         cudaStream_t s) {
     Table<N> table;
     std::copy(entries, entries + count, table.t);
     table.count = count;
     KernelTimer timer("adamw_step", s);
-    const cudaError_t e = launch(adamw_kernel<N>, blocks, kThreads, 0, s, table, k);
+    const cudaError_t e = launch(random ? adamw_kernel<N, true> : adamw_kernel<N, false>, blocks, kThreads, 0, s, table, k);
     if (e != cudaSuccess) return fail_cuda(e, "adamw_step");
     return check_launch("adamw_step", s);
 }
+
+inline bool state8(const tpce_adamw_tensor &t) { return (t.state_bits & ~TPCE_ADAMW_RANDOM) == 8; }
 
 // ------------------------------------------------------------------ overlaps
 // Blocks of a launch run in any order, so nothing that a step writes may be written
@@ -329,10 +352,10 @@ inline void ranges_of(const tpce_adamw_tensor &t, F take) {
     };
     part(0, t.p, n * (t.p_dtype == TPCE_BF16 ? 2 : 4), 0);
     if (t.master) part(1, t.master, n * 4, 0);
-    const uint64_t state = t.state_bits == 8 ? 1 : 4;
+    const uint64_t state = state8(t) ? 1 : 4;
     part(2, t.m, n * state, 0);
     part(3, t.v, n * state, 0);
-    if (t.state_bits == 8) {
+    if (state8(t)) {
         part(4, t.m_scale, (n + kGroup - 1) / kGroup * 4, 0);
         part(5, t.v_scale, (n + kGroup - 1) / kGroup * 4, 0);
     }
@@ -443,11 +466,13 @@ extern "C" tpce_status tp_adamw_step(const tpce_adamw_tensor *tensors, int count
         const tpce_adamw_tensor &t = tensors[i];
         const bool bf = t.p_dtype == TPCE_BF16;
         if ((!bf && t.p_dtype != TPCE_F32) || (t.g_dtype != TPCE_BF16 && t.g_dtype != TPCE_F32) ||
-            (t.state_bits != 8 && t.state_bits != 32) || !std::isfinite(t.weight_decay))
-            return fail(TPCE_ERR_INVALID, "tp_adamw_step: tensor %d: dtypes, state_bits (8 or 32) or weight_decay", i);
+            (!state8(t) && t.state_bits != 32) || !std::isfinite(t.weight_decay))
+            return fail(TPCE_ERR_INVALID,
+                        "tp_adamw_step: tensor %d: dtypes, state_bits (8, 32 or 8 | TPCE_ADAMW_RANDOM) or weight_decay",
+                        i);
         if (t.n < 0) return fail(TPCE_ERR_SHAPE, "tp_adamw_step: tensor %d: n = %lld", i, static_cast<long long>(t.n));
         if (t.n == 0) continue;
-        if (!t.p || !t.g || !t.m || !t.v || (t.state_bits == 8 && (!t.m_scale || !t.v_scale)) || (t.master && !bf))
+        if (!t.p || !t.g || !t.m || !t.v || (state8(t) && (!t.m_scale || !t.v_scale)) || (t.master && !bf))
             return fail(TPCE_ERR_INVALID, "tp_adamw_step: tensor %d: null pointer, or a master beside fp32 values", i);
         for (const void *p : {static_cast<const void *>(t.p), static_cast<const void *>(t.master), t.g,
                               static_cast<const void *>(t.m), static_cast<const void *>(t.v),
@@ -474,18 +499,21 @@ extern "C" tpce_status tp_adamw_step(const tpce_adamw_tensor *tensors, int count
     k.step_size = static_cast<float>(lr / (1.0 - std::pow(beta1, static_cast<double>(step))));
     k.root_scale = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(beta2, static_cast<double>(step))));
     k.grad_scale = static_cast<float>(grad_scale);
+    k.step = static_cast<uint32_t>(step);
     k.device = device_scalars;
 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     Entry entries[kLong];
     int held = 0;
     uint32_t blocks = 0;
+    bool random = false;
     auto flush = [&]() -> tpce_status {
         if (!held) return TPCE_OK;
-        tpce_status st = held <= kShort    ? launch_table<kShort>(entries, held, blocks, k, s)
-                         : held <= kMiddle ? launch_table<kMiddle>(entries, held, blocks, k, s)
-                                           : launch_table<kLong>(entries, held, blocks, k, s);
+        tpce_status st = held <= kShort    ? launch_table<kShort>(entries, held, blocks, random, k, s)
+                         : held <= kMiddle ? launch_table<kMiddle>(entries, held, blocks, random, k, s)
+                                           : launch_table<kLong>(entries, held, blocks, random, k, s);
         held = 0;
+        random = false;
         blocks = 0;
         return st;
     };
@@ -495,10 +523,12 @@ extern "C" tpce_status tp_adamw_step(const tpce_adamw_tensor *tensors, int count
         Entry &e = entries[held++];
         e = Entry{t.p, t.master, t.g, t.m, t.v, t.m_scale, t.v_scale, t.n, blocks, 0u, 0.0f, 0.0f, 1u, 0u};
         e.kind = (t.p_dtype == TPCE_BF16 ? kParamBf16 : 0u) | (t.master ? kMaster : 0u) |
-                 (t.g_dtype == TPCE_BF16 ? kGradBf16 : 0u) | (t.state_bits == 8 ? kState8 : 0u);
+                 (t.g_dtype == TPCE_BF16 ? kGradBf16 : 0u) | (state8(t) ? kState8 : 0u) |
+                 (t.state_bits & TPCE_ADAMW_RANDOM ? kRandom : 0u);
+        random |= (e.kind & kRandom) != 0u;
         e.decay = static_cast<float>(1.0 - lr * t.weight_decay);
         e.wd = static_cast<float>(t.weight_decay);
-        if (t.state_bits == 8 && total >= kSpanFrom) e.span = kSpan;
+        if (state8(t) && total >= kSpanFrom) e.span = kSpan;
         const int64_t block = static_cast<int64_t>(e.span) * kChunk;
         blocks += static_cast<uint32_t>((t.n + block - 1) / block);
         if (held == kLong) {

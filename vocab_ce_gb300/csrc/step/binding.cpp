@@ -400,7 +400,7 @@ struct Items {
 };
 
 // params, grads, states, masters (or None), weight_decay (a number or a list), lr, step, beta1, beta2, eps,
-// grad_scale, scalars
+// grad_scale, scalars, whether 8-bit roots are rounded at random
 PyObject *adamw_step(PyObject *const *a) {
     const Items params(a[0], "params must be a sequence"), grads(a[1], "grads must be a sequence"),
         states(a[2], "states must be a sequence");
@@ -418,6 +418,7 @@ PyObject *adamw_step(PyObject *const *a) {
     if (!none(a[3])) count("masters", masters.size());
     if (!one) count("weight_decay", decay.size());
     const double wd = one ? number(a[4]) : 0.0;
+    const bool random = truth(a[12]);
 
     std::vector<tpce_adamw_tensor> t(static_cast<size_t>(n));
     // What a backward pass may have saved: parameters and masters, kept by the list's own references. The states are
@@ -464,7 +465,7 @@ PyObject *adamw_step(PyObject *const *a) {
             e.m_scale = e.v_scale = nullptr;
         } else {
             const int64_t few[1] = {(e.n + kGroup - 1) / kGroup};
-            e.state_bits = 8;
+            e.state_bits = random ? 8 | TPCE_ADAMW_RANDOM : 8;
             e.m = take(keys->m_q.of(st), "m_q", i, at::kFloat8_e4m3fn, shape);
             e.v = take(keys->r_q.of(st), "r_q", i, at::kFloat8_e4m3fn, shape);
             e.m_scale = static_cast<float *>(take(keys->m_scale.of(st), "m_scale", i, at::kFloat, few));
@@ -550,7 +551,7 @@ PyMethodDef methods[] = {
     STEP_CALL(expert_dispatch_backward, 3),
     STEP_CALL(expert_combine_forward, 4),
     STEP_CALL(expert_combine_backward, 5),
-    STEP_CALL(adamw_step, 12),
+    STEP_CALL(adamw_step, 13),
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_step_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -139,6 +139,27 @@ constexpr float kE4m3Max = 448.0f, kE4m3Least = 1.0f / 512.0f;
 
 __device__ __forceinline__ float group_scale(float amax) { return fmaxf(__fmul_rn(amax, 1.0f / kE4m3Max), FLT_MIN); }
 
+// 20 bits that depend on all bits of a value and of its place: products and shifted
+// exclusive ors, twice. The multipliers are 2^32 times the golden ratio's fraction and
+// that of the root of 3, odd. The same value in the same place and step always gives
+// the same bits.
+__device__ __forceinline__ uint32_t noise20(uint32_t value, uint32_t place) {
+    uint32_t x = value ^ (place * 0x9E3779B9u);
+    x = (x ^ (x >> 16)) * 0xBB67AE85u;
+    x = (x ^ (x >> 15)) * 0x9E3779B9u;
+    return x >> 12;
+}
+
+// x (0 .. 448) to one of the two e4m3 values around it, the upper one where the 20 bits
+// of x that e4m3 does not hold and `noise` carry: with the probability of x's place
+// between them. Below 2^-6 the codes are 2^-9 apart, as fp32's are after 2^-6 is added
+// and 20 bits are cleared. Other values (NaN) stay.
+__device__ __forceinline__ float round_randomly(float x, uint32_t noise) {
+    const float below = x < 0.015625f ? 0.015625f : 0.0f;
+    const float r = __uint_as_float((__float_as_uint(x + below) + noise) & 0xfff00000u) - below;
+    return x <= 512.0f ? r : x;
+}
+
 // Codes and scale of a group whose 128 values lie in 16 adjacent lanes, eight
 // each (LANES: in fewer, the rest being another group's); every lane of the warp
 // calls it (values past an end: zeros). fmaxf
@@ -146,8 +167,11 @@ __device__ __forceinline__ float group_scale(float amax) { return fmaxf(__fmul_r
 // which would spoil the scale and saturate, are looked for only in a warp
 // whose maximum shows one. DIVISOR: none of the values is negative, and one that is
 // not zero gets no code below the smallest, 2^-9: what divides by it stays bounded.
-template <int LANES = 16, bool DIVISOR = false>
-__device__ __forceinline__ uint2 quantize8(const float (&v)[8], float &scale) {
+// RANDOM (of values that are not negative): a value between two codes becomes either,
+// the nearer one more often, so that its expectation is the value; `seed` differs from
+// eight values to the next.
+template <int LANES = 16, bool DIVISOR = false, bool RANDOM = false>
+__device__ __forceinline__ uint2 quantize8(const float (&v)[8], float &scale, uint32_t seed = 0u) {
     float a = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(v[i]));
@@ -168,6 +192,10 @@ __device__ __forceinline__ uint2 quantize8(const float (&v)[8], float &scale) {
     for (int i = 0; i < 8; ++i) t[i] = v[i];
 #pragma unroll
     for (int i = 0; i < 4; ++i) mul2(t[2 * i], t[2 * i + 1], inv, inv);
+    if (RANDOM) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] = round_randomly(t[i], noise20(__float_as_uint(v[i]), seed + i));
+    }
     if (infinite) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
