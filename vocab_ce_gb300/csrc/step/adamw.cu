@@ -21,7 +21,7 @@
 // b2 = 0.999: 3000 steps later the roots are 0.38 of what they should be, rounded at
 // random 0.98.) It shrinks no sooner, which makes steps small. At random it is the
 // hash of the value, its place and the step that decides, so a step repeats its bits:
-// 16 instructions a value (134 million with masters 368 us instead of 338, 42 million
+// some 15 instructions a value (134 million with masters 368 us instead of 338, 42 million
 // without 114 instead of 98).
 //
 // Every product and sum is rounded on its own (no contraction to a fused
