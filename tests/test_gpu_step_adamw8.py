@@ -254,3 +254,30 @@ def test_random_rounding_in_a_captured_step():
     scalars.copy_(tp.adamw_scalars(1e-3, 7))
     graph.replay()                                     # another step's numbers: other codes
     assert not same({"r_q": eager["r_q"]}, {"r_q": captured["r_q"]})
+
+
+def test_one_list_may_round_either_way():
+    # by the C ABI, where it is each tensor's: in the same launch, tensors rounded to nearest and with 32-bit states
+    # keep their bits
+    gpu_or_skip()
+    from vocab_ce_gb300._lib import AdamwTensor, lib
+    sizes = [(700, "nearest"), (5000, "random"), (300, None), (129, "random"), (2049, "nearest")]
+    made = [state8(n, 40 + i) for i, (n, _) in enumerate(sizes)]
+
+    def fresh():
+        return [(torch.zeros(n, device="cuda"), g, copy(st) if how else tp.adamw_state(g, 32))
+                for (n, how), (st, g) in zip(sizes, made)]
+
+    one, alone = fresh(), fresh()
+    table = (AdamwTensor * len(sizes))()
+    for e, (p, g, st), (n, how) in zip(table, one, sizes):
+        e.p, e.g, e.n, e.p_dtype, e.g_dtype = p.data_ptr(), g.data_ptr(), n, 1, 1
+        e.state_bits = 32 if how is None else 8 | (256 if how == "random" else 0)
+        names = ("m", "v") if how is None else ("m_q", "r_q", "m_scale", "r_scale")
+        for field, name in zip(("m", "v", "m_scale", "v_scale"), names):
+            setattr(e, field, st[name].data_ptr())
+    stream = torch.cuda.current_stream().cuda_stream
+    assert lib().tp_adamw_step(table, len(sizes), 1e-3, 0.9, 0.999, 1e-8, 5, 1.0, None, stream) == 0
+    for (p, g, st), (q, h, su), (_, how) in zip(one, alone, sizes):
+        tp.adamw_step([q], [h], [su], lr=1e-3, step=5, rounding=how or "nearest")
+        assert torch.equal(p, q) and same(st, su), how
