@@ -188,6 +188,12 @@ for h in (64, 256, 264, 512, 8192, 16384):
                 assert L.tpce_last_error()
             assert L.tp_rmsnorm_backward(p, p, p, p, None, T, h, dtype, p, None, None, 0, None) == 5, (h, T)
     assert L.tp_expert_combine_forward(p, p, p, 4, h, 2, 0, p, None) == 5
+# without tokens an output is set to zero: the text is that failure's, not an earlier one's
+assert L.tp_rmsnorm_forward(p, None, p, 4, 60, 1e-6, 0, None, p, None, None, p, None) == 2
+assert L.tp_rmsnorm_backward(None, None, None, None, None, 0, 64, 0, None, p, None, 0, None) == 5
+assert b"tp_rmsnorm_backward: cuda" in L.tpce_last_error(), L.tpce_last_error()
+assert L.tp_expert_plan(None, 0, 2, 8, None, None, p, None, 0, None) == 5
+assert b"tp_expert_plan: cuda" in L.tpce_last_error(), L.tpce_last_error()
 """
 
 

@@ -558,7 +558,8 @@ extern "C" tpce_status tp_expert_plan(const int32_t *ids, int64_t T, int k, int 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (T == 0) {
         if ((st = check_pointers("tp_expert_plan", {offsets})) != TPCE_OK) return st;
-        return cudaMemsetAsync(offsets, 0, sizeof(int32_t) * (E + 1), s) == cudaSuccess ? TPCE_OK : TPCE_ERR_CUDA;
+        const cudaError_t e = cudaMemsetAsync(offsets, 0, sizeof(int32_t) * (E + 1), s);
+        return e == cudaSuccess ? TPCE_OK : fail_cuda(e, "tp_expert_plan");
     }
     if ((st = check_pointers("tp_expert_plan", {ids, row, source, offsets})) != TPCE_OK) return st;
     const int64_t n = T * k;

@@ -891,8 +891,8 @@ extern "C" tpce_status tp_rmsnorm_backward(const void *dY, const void *S, const 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (T == 0) {
         // no tokens: an empty sum
-        if (dw && cudaMemsetAsync(dw, 0, sizeof(float) * h, s) != cudaSuccess) return TPCE_ERR_CUDA;
-        return TPCE_OK;
+        const cudaError_t e = dw ? cudaMemsetAsync(dw, 0, sizeof(float) * h, s) : cudaSuccess;
+        return e == cudaSuccess ? TPCE_OK : fail_cuda(e, "tp_rmsnorm_backward");
     }
     if (dw && (!ws || ws_bytes < tpce_rmsnorm_workspace_bytes(T, h)))
         return fail(TPCE_ERR_WORKSPACE, "tp_rmsnorm_backward: %zu bytes of workspace needed, %zu given",
