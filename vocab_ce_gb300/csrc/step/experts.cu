@@ -558,7 +558,7 @@ extern "C" tpce_status tp_expert_plan(const int32_t *ids, int64_t T, int k, int 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (T == 0) {
         if ((st = check_pointers("tp_expert_plan", {offsets})) != TPCE_OK) return st;
-        const cudaError_t e = cudaMemsetAsync(offsets, 0, sizeof(int32_t) * (E + 1), s);
+        const cudaError_t e = taken(cudaMemsetAsync(offsets, 0, sizeof(int32_t) * (E + 1), s));
         return e == cudaSuccess ? TPCE_OK : fail_cuda(e, "tp_expert_plan");
     }
     if ((st = check_pointers("tp_expert_plan", {ids, row, source, offsets})) != TPCE_OK) return st;

@@ -21,6 +21,13 @@ __device__ __forceinline__ void grid_begin() {
 // still runs, on some SMs many and on others none.
 __device__ __forceinline__ void grid_begin_alone() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// A failed call's error, taken off the runtime's record as well: there the check after
+// the next launch would find it, and report a kernel as failed that has run.
+inline cudaError_t taken(cudaError_t e) {
+    if (e != cudaSuccess) cudaGetLastError();
+    return e;
+}
+
 // `ctas` neighbouring blocks form a cluster
 template <typename... P, typename... A>
 cudaError_t launch_clusters(int ctas, void (*kernel)(P...), unsigned grid, int threads, size_t smem, cudaStream_t s,
@@ -38,7 +45,8 @@ cudaError_t launch_clusters(int ctas, void (*kernel)(P...), unsigned grid, int t
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = ctas > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+    cudaGetLastError();  // what an earlier call has left there, and returned to its caller
+    return taken(cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...));
 }
 template <typename... P, typename... A>
 cudaError_t launch(void (*kernel)(P...), unsigned grid, int threads, size_t smem, cudaStream_t s, const A &...args) {

@@ -712,11 +712,11 @@ struct Fn {
     static cudaError_t allow(int bytes, int most) {
         static std::atomic<uint64_t> done{0};
         int dev = 0;
-        cudaError_t e = cudaGetDevice(&dev);
+        cudaError_t e = taken(cudaGetDevice(&dev));
         if (e != cudaSuccess || bytes <= 40 * 1024) return e;
         const uint64_t bit = uint64_t{1} << (dev & 63);
         if (done.load() & bit) return cudaSuccess;
-        e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        e = taken(cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
         if (e == cudaSuccess) done.fetch_or(bit);
         return e;
     }
@@ -891,7 +891,7 @@ extern "C" tpce_status tp_rmsnorm_backward(const void *dY, const void *S, const 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (T == 0) {
         // no tokens: an empty sum
-        const cudaError_t e = dw ? cudaMemsetAsync(dw, 0, sizeof(float) * h, s) : cudaSuccess;
+        const cudaError_t e = dw ? taken(cudaMemsetAsync(dw, 0, sizeof(float) * h, s)) : cudaSuccess;
         return e == cudaSuccess ? TPCE_OK : fail_cuda(e, "tp_rmsnorm_backward");
     }
     if (dw && (!ws || ws_bytes < tpce_rmsnorm_workspace_bytes(T, h)))
