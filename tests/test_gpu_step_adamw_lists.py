@@ -7,7 +7,7 @@ import torch
 
 import vocab_ce_gb300 as tp
 from _parity import gpu_or_skip
-from test_gpu_step_adamw import KINDS, copy, elementary, same, step, tensors
+from test_gpu_step_adamw import HYPER, KINDS, copy, elementary, same, step, tensors
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
@@ -83,3 +83,22 @@ def test_a_list_long_enough_for_blocks_of_several_chunks():
         t = copy(old[i])
         step([t])
         same(t, many[i])
+
+
+@pytest.mark.parametrize("own_stream", [False, True])
+def test_lists_that_can_be_read_once(own_stream):
+    # model.parameters() and the like; with a stream the tensors are recorded on it first
+    gpu_or_skip()
+    old = [tensors(n, BF, F32, True, 8, n) for n in (300, 77, 4000)]
+    one, two = [copy(t) for t in old], [copy(t) for t in old]
+    stream = torch.cuda.Stream() if own_stream else None
+    if stream is not None:
+        stream.wait_stream(torch.cuda.current_stream())
+    tp.adamw_step((t["p"] for t in one), (t["g"] for t in one), (t["st"] for t in one),
+                  masters=(t["master"] for t in one), weight_decay=(0.1 for t in one), stream=stream, **HYPER)
+    if stream is not None:
+        torch.cuda.current_stream().wait_stream(stream)
+    step(two)
+    for t, q, o in zip(one, two, old):
+        same(t, q)
+        assert not torch.equal(t["master"], o["master"])

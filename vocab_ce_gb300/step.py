@@ -211,7 +211,10 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
         raise ValueError('adamw_step: rounding must be "nearest" or "random"')
     random = rounding == "random"
     if stream is not None:
-        with _on(stream, list(params), list(grads), list(states), list(masters or ()), scalars):
+        # read twice below, which an iterator does not allow
+        params, grads, states = list(params), list(grads), list(states)
+        masters = None if masters is None else list(masters)
+        with _on(stream, params, grads, states, masters, scalars):
             return _b().adamw_step(params, grads, states, masters, weight_decay, lr, step, beta1, beta2, eps,
                                    grad_scale, scalars, random)
     return _b().adamw_step(params, grads, states, masters, weight_decay, lr, step, beta1, beta2, eps, grad_scale,
