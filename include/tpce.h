@@ -491,7 +491,8 @@ tpce_status vocab_parallel_ce_loss_static(const void *H, const void *E, const in
  *   itself; dw [h] fp32 (NULL: not wanted). dw is deterministic.
  * Shapes: h a multiple of 8 up to 16384. T == 0: the forward is a no-op, the
  * backward zeroes dw. Sequence chunks are rows: call once per chunk (dw of the
- * whole is the chunks' sum).
+ * whole is the chunks' sum). Every pointer is 16-byte aligned: inside one rstd
+ * or Q_scale a chunk begins at a multiple of four values, inside Q at one of 16.
  * Workspace: tpce_rmsnorm_workspace_bytes for the backward with dw (partial
  * sums); 0 for invalid shapes.
  * ------------------------------------------------------------------------- */

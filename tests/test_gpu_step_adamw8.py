@@ -170,7 +170,8 @@ def test_a_random_code_is_a_neighbour_and_right_on_average(spread):
         tp.adamw_step([x], [g], [s], lr=1e-3, step=5, rounding=how)
     # nothing but the roots' codes differs
     assert torch.equal(p[0], p[1]) and torch.equal(p[0], p[2])
-    assert same({k: near[k] for k in ("m_q", "m_scale", "r_scale")}, {k: rand[k] for k in ("m_q", "m_scale", "r_scale")})
+    others = ("m_q", "m_scale", "r_scale")
+    assert same({k: near[k] for k in others}, {k: rand[k] for k in others})
     t = exact["v"].double().sqrt() / rand["r_scale"].double().repeat_interleave(128)
     q = rand["r_q"].double()
     step = torch.exp2(t.log2().floor().clamp_min(-6.0) - 3.0)

@@ -30,7 +30,8 @@ def test_what_would_be_written_twice_is_refused(bits):
            ([p, q], [g, h], [st, dict(su, **{k: st[k] for k in list(st)[:1]})], None),  # a part of it
            ([b, c], [g, h], [st, su], [p, p]),                                      # one master for two
            ([b, p], [g, h], [st, su], [p, None]),                                   # a master that is a parameter too
-           ([flat[:600], flat[320:920]], [normal(600, 7), normal(600, 8)], [one, tp.adamw_state(flat[:600], bits)], None),
+           ([flat[:600], flat[320:920]], [normal(600, 7), normal(600, 8)],          # neighbours that overlap
+            [one, tp.adamw_state(flat[:600], bits)], None),
            ([p, q], [g, p], [st, su], None)]                                        # a gradient that is a parameter
     if bits == 32:
         bad.append(([p, q], [g, st["m"]], [st, su], None))                          # a gradient that is a moment

@@ -224,7 +224,8 @@ def _adamw_tensor(at, n=300, bits=8, p_dtype=0, g_dtype=0):
 @pytest.mark.parametrize("others", [0, 3, 30])
 def test_adamw_refuses_what_would_be_written_twice(L, others):
     # the others make the list long enough for every way of the check, and stand in no order
-    rest = [_adamw_tensor(1000 + 10 * ((7 * i) % others), 1 + 37 * i, (8, 32)[i % 2], i // 2 % 2) for i in range(others)]
+    rest = [_adamw_tensor(1000 + 10 * ((7 * i) % others), 1 + 37 * i, (8, 32)[i % 2], i // 2 % 2)
+            for i in range(others)]
 
     def refused(*tensors, says):
         for order in (tensors, tensors[::-1]):

@@ -14,8 +14,8 @@ from .api import (TpceError, attn_workspace_bytes, tp_attn_out_backward_sp, tp_a
                   tp_mlp_forward, tp_mlp_forward_sp, tp_swiglu_backward, tp_swiglu_backward_sp, tp_swiglu_forward,
                   tp_swiglu_forward_sp, vocab_parallel_ce, vocab_parallel_ce_loss_static)
 from .step import (adamw_scalars, adamw_state, adamw_step, expert_plan_workspace_bytes, rmsnorm_workspace_bytes,
-                   tp_expert_combine_backward, tp_expert_combine_forward, tp_expert_dispatch_backward, tp_expert_dispatch_forward, tp_expert_plan,
-                   tp_rmsnorm_backward, tp_rmsnorm_forward)
+                   tp_expert_combine_backward, tp_expert_combine_forward, tp_expert_dispatch_backward,
+                   tp_expert_dispatch_forward, tp_expert_plan, tp_rmsnorm_backward, tp_rmsnorm_forward)
 
 __all__ = ["TpceError", "attn_workspace_bytes", "tp_attn_out_backward_sp", "tp_attn_out_forward_sp",
            "tp_attn_qkv_backward_sp", "tp_attn_qkv_forward_sp", "tp_column_linear_backward_sp",

@@ -21,7 +21,7 @@
 // b2 = 0.999: 3000 steps later the roots are 0.38 of what they should be, rounded at
 // random 0.98.) It shrinks no sooner, which makes steps small. At random it is the
 // hash of the value, its place and the step that decides, so a step repeats its bits:
-// some 15 instructions a value (134 million with masters 368 us instead of 338, 42 million
+// 16 instructions a value more (134 million with masters 368 us instead of 338, 42 million
 // without 114 instead of 98).
 //
 // Every product and sum is rounded on its own (no contraction to a fused
@@ -32,8 +32,8 @@
 //
 // Bound by HBM: 134 million bf16 weights with fp32 masters and bf16 gradients
 // take 538 us with 32-bit states (28 bytes a value, 7.0 TB/s, a little above the
-// copy rate, as reads and writes meet the same lines) and 335 us with 8-bit ones
-// (16.1 bytes, 6.5 TB/s, 95% of the copy rate). There the arithmetic, some 60
+// copy rate, as reads and writes meet the same lines) and 338 us with 8-bit ones
+// (16.1 bytes, 6.4 TB/s, 94% of the copy rate). There the arithmetic, 66
 // instructions a value, takes two thirds of the time that the bytes take, so it
 // is done beside the next chunk's loads (448 us without) and products in pairs.
 //
@@ -301,7 +301,8 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
         c.grad_scale = k.device[3];
     }
     // a captured step repeats k.step; its rates differ from step to step
-    if (RANDOM) c.seed = (k.step + __float_as_uint(c.step_size) * 3u + __float_as_uint(c.root_scale) * 5u) * 0xBB67AE85u;
+    if (RANDOM)
+        c.seed = (k.step + __float_as_uint(c.step_size) * 3u + __float_as_uint(c.root_scale) * 5u) * 0xBB67AE85u;
     const bool narrow = (e.kind & kParamBf16) && !(e.kind & kMaster);
     if (e.kind & kGradBf16) {
         if (narrow)
@@ -323,7 +324,8 @@ tpce_status launch_table(const Entry *entries, int count, uint32_t blocks, bool 
     std::copy(entries, entries + count, table.t);
     table.count = count;
     KernelTimer timer("adamw_step", s);
-    const cudaError_t e = launch(random ? adamw_kernel<N, true> : adamw_kernel<N, false>, blocks, kThreads, 0, s, table, k);
+    const cudaError_t e =
+        launch(random ? adamw_kernel<N, true> : adamw_kernel<N, false>, blocks, kThreads, 0, s, table, k);
     if (e != cudaSuccess) return fail_cuda(e, "adamw_step");
     return check_launch("adamw_step", s);
 }

@@ -107,7 +107,8 @@ void need(const at::Tensor &x, const char *name, at::ScalarType dtype, at::IntAr
 int rows_type(const at::Tensor &x, const char *name, Py_ssize_t i = -1) {
     if (x.scalar_type() == at::kBFloat16) return TPCE_BF16;
     if (x.scalar_type() == at::kFloat) return TPCE_F32;
-    throw Refused{name + (i < 0 ? std::string() : "[" + std::to_string(i) + "]") + " must be torch.bfloat16 or torch.float32, got " + dtype_name(x.scalar_type())};
+    throw Refused{name + (i < 0 ? std::string() : "[" + std::to_string(i) + "]") +
+                  " must be torch.bfloat16 or torch.float32, got " + dtype_name(x.scalar_type())};
 }
 
 // rows x columns of bf16 or fp32; returns the library's dtype
@@ -170,7 +171,9 @@ PyObject *entry(PyObject *out, const Key &key) {
 
 // Made at the module's start, with the interpreter there.
 struct Keys {
-    Key S{"S"}, Y{"Y"}, rstd{"rstd"}, Q{"Q"}, Q_scale{"Q_scale"}, dX{"dX"}, dw{"dw"}, row{"row"}, source{"source"}, offsets{"offsets"}, dYs{"dYs"}, dweights{"dweights"}, m{"m"}, v{"v"}, m_q{"m_q"}, r_q{"r_q"}, m_scale{"m_scale"}, r_scale{"r_scale"};
+    Key S{"S"}, Y{"Y"}, rstd{"rstd"}, Q{"Q"}, Q_scale{"Q_scale"}, dX{"dX"}, dw{"dw"};
+    Key row{"row"}, source{"source"}, offsets{"offsets"}, dYs{"dYs"}, dweights{"dweights"};
+    Key m{"m"}, v{"v"}, m_q{"m_q"}, r_q{"r_q"}, m_scale{"m_scale"}, r_scale{"r_scale"};
 };
 const Keys *keys;
 
@@ -241,7 +244,8 @@ PyObject *rmsnorm_forward(PyObject *const *a) {
     res.add(keys->rstd, rstd);
     if (quantize) {
         res.add(keys->Q, Q = output(entry(a[6], keys->Q), "Q", X.sizes(), at::kFloat8_e4m3fn, X));
-        res.add(keys->Q_scale, Qs = output(entry(a[6], keys->Q_scale), "Q_scale", {T, (h + kGroup - 1) / kGroup}, at::kFloat, X));
+        res.add(keys->Q_scale, Qs = output(entry(a[6], keys->Q_scale), "Q_scale", {T, (h + kGroup - 1) / kGroup},
+                                           at::kFloat, X));
     }
     raise_on(api.rmsnorm_forward(ptr(X), ptr(R), fptr(w), T, h, static_cast<float>(eps), dt, ptr(S), ptr(Y), ptr(Q),
                                  fptr(Qs), fptr(rstd), stream()),
@@ -411,7 +415,8 @@ PyObject *adamw_step(PyObject *const *a) {
     Py_DECREF(nothing);
     const Py_ssize_t n = params.size();
     auto count = [&](const char *name, Py_ssize_t m) {
-        if (m != n) throw Refused{std::string(name) + ": " + std::to_string(n) + " entries expected, got " + std::to_string(m)};
+        if (m != n)
+            throw Refused{std::string(name) + ": " + std::to_string(n) + " entries expected, got " + std::to_string(m)};
     };
     count("grads", grads.size());
     count("states", states.size());
@@ -541,7 +546,8 @@ PyObject *init(PyObject *, PyObject *const *args, Py_ssize_t n) {
     Py_RETURN_NONE;
 }
 
-#define STEP_CALL(name, n) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&call<name, n>)), METH_FASTCALL, nullptr}
+#define STEP_CALL(name, n) \
+    {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&call<name, n>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {
     {"init", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&init)), METH_FASTCALL, nullptr},
     STEP_CALL(rmsnorm_forward, 7),

@@ -335,9 +335,16 @@ __device__ __forceinline__ uint4 narrow(const float (&v)[4]) {
 
 // Combine, and the dispatch's backward. NV values a vector: 8 (bf16) or 4 (fp32).
 // weights NULL: all one. The same 1.2 GB as above: 186 us, 6.5 TB/s (206 us where
-// a thread read its places again for each vector). Four blocks an SM for six
-// choices and more, which costs eight of them some spilled registers: 3783 tokens
-// of 768 bf16, half dropped, take 12.5 us instead of 14.5 (the 1.2 GB no more).
+// a thread read its places again for each vector).
+// Blocks that an SM must have room for, and with them the registers (8192 tokens of
+// 4096 bf16, us): six for one and two choices (22.2 and 31.7; with four 23.1 and
+// 34.7), four for three and four (42.4, 50.7; with three 42.6, 53.5), three for five
+// (61.7; with four 70.3, though 4000 of 1000 fp32 take 16.8 instead of 17.6), four
+// for six to eight, which costs eight some spilled registers (71.1, 80.3, 92.8; with
+// three 71.1, 84.6, 92.9, and 3783 of 768, half dropped, k = 7, 8.6 instead of 7.1).
+// Vectors at a time: one for six and more (two: 88.3, 110, 143), two for three to
+// five (one: 42.4, 52.4, 62.9; fp32 k = 3 14.2 instead of 12.1), four and two for one
+// and two (two and one: 23.7, 34.4).
 template <int NV, int K>
 __global__ void __launch_bounds__(256, K == 5 ? 3 : K > 2 ? 4 : 6)
     expert_combine_kernel(const uint4 *Ys, const int32_t *row,
@@ -400,7 +407,11 @@ __global__ void __launch_bounds__(256, K == 5 ? 3 : K > 2 ? 4 : 6)
 }
 
 // The combine's backward: dZ is read once for all of a token's rows. 4096 tokens
-// of 8192 bf16 and 2 experts, 10% dropped, 0.32 GB: 50 us, 6.4 TB/s.
+// of 8192 bf16 and 2 experts, 10% dropped, 0.32 GB: 50 us, 6.4 TB/s. Three blocks an
+// SM from five choices on (8192 of 4096 bf16, k = 7 and 8: 155 and 176 us, with four
+// 173 and 206; five take 114 and with four 112, six 132 and 141), four below (k = 4:
+// 92, with three 96). One vector at a time from four choices on (92; two: 96), four
+// and two for one and two (33 and 52; one: 41 and 57).
 template <int NV, int K>
 __global__ void __launch_bounds__(256, K > 4 ? 3 : 4)
     expert_combine_backward_kernel(const uint4 *dZ, const uint4 *Ys,
@@ -608,7 +619,8 @@ extern "C" tpce_status tp_expert_dispatch_backward(const void *dXs, const int32_
     tpce_status st = check_rows_shape(T, h, k, 1, dtype);
     if (st != TPCE_OK || T == 0) return st;
     if ((st = check_pointers("tp_expert_dispatch_backward", {dXs, row, dX})) != TPCE_OK) return st;
-    return combine("expert_dispatch_backward", dXs, row, nullptr, T, h, k, dtype, dX, static_cast<cudaStream_t>(stream));
+    return combine("expert_dispatch_backward", dXs, row, nullptr, T, h, k, dtype, dX,
+                   static_cast<cudaStream_t>(stream));
 }
 
 extern "C" tpce_status tp_expert_combine_forward(const void *Ys, const int32_t *row, const float *weights, int64_t T,

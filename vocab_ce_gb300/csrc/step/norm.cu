@@ -381,7 +381,8 @@ __global__ void __launch_bounds__(kLanesThreads, 4)
     const int warp = threadIdx.x & ~31, of_warp = threadIdx.x & 31;
     auto slot = [&](int stage, int i, int thread) {
         const int tensor = i / kPieces, piece = i % kPieces;
-        return reinterpret_cast<uint4 *>(data + stage * kStage + ((tensor * kLanesThreads + thread) * kPieces + piece) * 16);
+        return reinterpret_cast<uint4 *>(data + stage * kStage +
+                                         ((tensor * kLanesThreads + thread) * kPieces + piece) * 16);
     };
     auto statistic = [&](int stage) {
         return reinterpret_cast<float *>(data + stage * kStage + 3 * kPieces * kLanesThreads * 16) + threadIdx.x;
@@ -669,8 +670,10 @@ __global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(const float *part, int
 // a vector is 32 bytes already two take longer (10,146 x 3768 with the residual 59
 // and 57 us, 16,384 x 1000 fp32 24.4 and 22.9).
 // The backward's blocks each leave a row to the sum of dw: up to 8 on an SM, and 12
-// where that is little beside their own rows (65,536 x 512 47 us with 12, 50 with 8;
-// 4000 x 512 10.4 and 8.2).
+// where that is little beside their own rows, from 32,768 of them on, where both take
+// the same (512 values: 28.5 us either way; 4000 rows 8.8 with 8 and 9.2 with 12,
+// 16,384 17.6 and 18.5, 131,072 91.0 and 87.7; 264 values: 27.5 and 26.5, 16.9 and
+// 17.1 for 16,384 rows, 88.5 and 80.1 for 131,072).
 struct Layout {
     int vpt, threads, blocks;
 };
@@ -773,9 +776,11 @@ tpce_status forward(const void *X, const void *R, const float *w, int64_t rows, 
     };
     cudaError_t e;
     if (L.vpt == 1)
-        e = ring ? go(Fn<rmsnorm_forward_block_kernel<T, 1, true>>{}) : go(Fn<rmsnorm_forward_block_kernel<T, 1, false>>{});
+        e = ring ? go(Fn<rmsnorm_forward_block_kernel<T, 1, true>>{})
+                 : go(Fn<rmsnorm_forward_block_kernel<T, 1, false>>{});
     else
-        e = ring ? go(Fn<rmsnorm_forward_block_kernel<T, 2, true>>{}) : go(Fn<rmsnorm_forward_block_kernel<T, 2, false>>{});
+        e = ring ? go(Fn<rmsnorm_forward_block_kernel<T, 2, true>>{})
+                 : go(Fn<rmsnorm_forward_block_kernel<T, 2, false>>{});
     if (e != cudaSuccess) return fail_cuda(e, "rmsnorm_forward");
     return check_launch("rmsnorm_forward", s);
 }
@@ -814,8 +819,8 @@ tpce_status backward(const void *dY, const void *S, const float *w, const float 
             using Pair = Fn<rmsnorm_backward_pair_kernel<T>>;
             cudaError_t e = Pair::allow(smem, room);
             if (e == cudaSuccess)
-                e = launch_clusters(2, Pair::fn, static_cast<unsigned>(2 * blocks), L.threads, smem, s, y, x, w, rstd, d,
-                                    rows, h, out, part, stages, tensors, take_debug_withhold(),
+                e = launch_clusters(2, Pair::fn, static_cast<unsigned>(2 * blocks), L.threads, smem, s, y, x, w, rstd,
+                                    d, rows, h, out, part, stages, tensors, take_debug_withhold(),
                                     device_error_word());
             if (e != cudaSuccess) return fail_cuda(e, "rmsnorm_backward");
         } else {
