@@ -529,6 +529,9 @@ tpce_status tp_rmsnorm_backward(const void *dY, const void *S, const float *w, c
  * recorded in the device status word.
  * Shapes: 1 <= k <= 32, 1 <= E <= 1024, T k below 2^31 - 1024, h a multiple
  * of 8 up to 2^20. T == 0: offsets are zeroed, the rest is a no-op.
+ * The plan's pointers do not overlap (TPCE_ERR_INVALID); ids stay as they are
+ * until it has run: one that changes meanwhile is dropped and recorded, where it
+ * would lead outside.
  * Workspace: tpce_expert_plan_workspace_bytes for the plan (counts of up to 256
  * blocks of assignments; 0 for up to 2048 assignments and for invalid shapes).
  * ------------------------------------------------------------------------- */

@@ -83,6 +83,27 @@ def test_expert_plan_refusals(L):
         assert call(T=T, k=k, E=E, ws=ODD, n=1 << 30) == ALIGN
 
 
+def test_expert_plan_refuses_overlaps(L):
+    # row in the place of ids would make the second pass take ranks for experts
+    def call(T, k=2, E=8, ws=None, n=0, **at):
+        p = dict(ids=1 << 20, row=2 << 20, source=3 << 20, offsets=4 << 20)
+        p.update(at)
+        return L.tp_expert_plan(P(p["ids"]), T, k, E, P(p["row"]), P(p["source"]), P(p["offsets"]), ws, n, None)
+    for T in (4, 5000):
+        bytes_ = 4 * 2 * T
+        ws, n = P(5 << 20), L.tpce_expert_plan_workspace_bytes(T, 2, 8)
+        for a, b in (("row", "ids"), ("source", "ids"), ("offsets", "ids"), ("source", "row"), ("offsets", "source")):
+            base = dict(ids=1 << 20, row=2 << 20, source=3 << 20, offsets=4 << 20)[b]
+            for shift in (0, 16, bytes_ - 16):
+                assert call(T, ws=ws, n=n, **{a: base + shift}) == INVALID, (a, b, shift)
+                assert b"overlap" in L.tpce_last_error()
+    for at in (1 << 20, (2 << 20) + 4 * 2 * 5000 - 16, (3 << 20) - 16, 4 << 20):
+        assert call(5000, ws=P(at), n=1 << 20) == INVALID and b"overlap" in L.tpce_last_error()
+    if not torch.cuda.is_available():      # side by side: what comes next is the launch, which fails without a device
+        assert call(4, row=(1 << 20) + 32, source=(1 << 20) + 64, offsets=(1 << 20) + 96) == 5
+        assert call(5000, ws=P((4 << 20) + 48), n=1 << 20) == 5
+
+
 def test_expert_row_refusals(L):
     calls = {
         "dispatch": lambda T=4, h=64, k=2, E=8, dt=0, a=OK, b=OK, c=OK, d=OK:

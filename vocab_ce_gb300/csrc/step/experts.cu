@@ -18,6 +18,7 @@
 #include <climits>
 #include <initializer_list>
 #include <type_traits>
+#include <utility>
 
 #include "host.h"
 #include "ptx.cuh"
@@ -214,7 +215,14 @@ __global__ void __launch_bounds__(kPlanThreads)
         for (int u = 0; u < kBatch; ++u) {
             const int64_t i = i0 + u * 32;
             if (r[u] < 0) continue;  // past the run, or dropped: row[i] is -1 already
-            const uint32_t p = all[x[u]] + mine[x[u]] + static_cast<uint32_t>(r[u]);
+            // ids read a second time: one that has changed meanwhile must lead nowhere
+            const bool known = static_cast<uint32_t>(x[u]) < static_cast<uint32_t>(E);
+            const uint32_t p = known ? all[x[u]] + mine[x[u]] + static_cast<uint32_t>(r[u]) : UINT_MAX;
+            if (p >= n) {
+                ptx::record_error(err, kErrInvalid | (4u << 8));
+                row[i] = -1;
+                continue;
+            }
             row[i] = static_cast<int32_t>(p);
             source[p] = static_cast<int32_t>(i);
         }
@@ -518,6 +526,11 @@ tpce_status check_pointers(const char *name, std::initializer_list<const void *>
     return TPCE_OK;
 }
 
+inline bool overlap(const void *a, size_t a_bytes, const void *b, size_t b_bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a_bytes && b_bytes && x < y + b_bytes && y < x + a_bytes;
+}
+
 inline int vectors_of(int64_t h, int dtype) { return static_cast<int>(h * (dtype == TPCE_BF16 ? 2 : 4) / 16); }
 
 inline unsigned blocks_of(int64_t T, const Split &sp) { return static_cast<unsigned>((T + sp.tokens - 1) / sp.tokens); }
@@ -577,13 +590,23 @@ extern "C" tpce_status tp_expert_plan(const int32_t *ids, int64_t T, int k, int 
     const PlanSplit sp = plan_split(n);
     uint32_t *counts = nullptr;
     cudaError_t e;
+    const size_t need = tpce_expert_plan_workspace_bytes(T, k, E);
     if (sp.blocks > 1) {
-        const size_t need = tpce_expert_plan_workspace_bytes(T, k, E);
         if (!ws || ws_bytes < need)
             return fail(TPCE_ERR_WORKSPACE, "tp_expert_plan: %zu bytes of workspace needed, %zu given", need,
                         ws ? ws_bytes : size_t{0});
         if (!aligned16(ws)) return fail(TPCE_ERR_ALIGN, "tp_expert_plan: a pointer is not 16-byte aligned");
         counts = static_cast<uint32_t *>(ws);
+    }
+    // ids are read again after places and counts have been written
+    const size_t each = static_cast<size_t>(n) * sizeof(int32_t);
+    const std::pair<const void *, size_t> parts[] = {
+        {ids, each}, {row, each}, {source, each}, {offsets, sizeof(int32_t) * (E + 1)}, {counts, need}};
+    for (const auto &a : parts)
+        for (const auto &b : parts)
+            if (&a < &b && overlap(a.first, a.second, b.first, b.second))
+                return fail(TPCE_ERR_INVALID, "tp_expert_plan: ids, row, source, offsets or ws overlap");
+    if (counts) {
         KernelTimer timer("expert_count", s);
         e = launch(expert_count_kernel, sp.blocks, kPlanThreads, E * sizeof(uint32_t), s, ids, n, sp.chunk, E, counts);
         if (e != cudaSuccess) return fail_cuda(e, "expert_count");
