@@ -93,7 +93,7 @@ class ExpertLayer:
         tp.adamw_step([self.params[n] for n in names], [grads[n] for n in names], [self.states[n] for n in names],
                       lr=lr, step=step, weight_decay=[weight_decay if self.params[n].dim() == 2 else 0.0 for n in names],
                       masters=[self.masters.get(n) for n in names],
-                      rounding="random")  # of the 8-bit roots: beta2 is 0.999
+                      rounding="random")  # of the 8-bit states: beta2 is 0.999
 
 
 def train(steps: int = 40, T: int = 1024, h: int = 256, f: int = 512, experts: int = 8, k: int = 2, vocab: int = 1000,

@@ -564,15 +564,16 @@ tpce_status tp_expert_combine_backward(const void *dZ, const void *Ys, const int
  * the smallest code, 2^-9; v then points to r's codes and v_scale to their
  * scales. Codes and scales of zero bytes are a zero state. The update uses the
  * moments before they are rounded.
- * r is rounded to the nearest code; with state_bits 8 | TPCE_ADAMW_RANDOM to
- * one of the two codes around it, so that its expectation is r (the choice is a
- * hash of the value, its place in the tensor and the step: equal calls give
- * equal bits). To nearest, while a group's largest root stays, another of its
- * roots does not grow before its gradients are
- *   sqrt(((17/16)^2 - beta2) / (1 - beta2))
- * times it: 11.4 at beta2 = 0.999, 3.7 at 0.99, 1.9 at 0.95. Updates are too
- * large by up to that factor where gradients have grown. Round at random for a
- * beta2 near 1.
+ * Codes are rounded to nearest; with state_bits 8 | TPCE_ADAMW_RANDOM to one of
+ * the two codes around the value, so that its expectation is the value (the
+ * choice is a hash of the value, its place in the tensor and the step: equal
+ * calls give equal bits). To nearest, while a group's largest value stays,
+ *   another root does not grow before its gradients are
+ *   sqrt(((17/16)^2 - beta2) / (1 - beta2)) times it (11.4 at beta2 = 0.999, 3.7
+ *   at 0.99, 1.9 at 0.95), and updates may be too large by that factor;
+ *   another moment whose gradients have ended stops shrinking, for beta1 above
+ *   15/16 at any size, and its parameter goes on moving.
+ * Round at random for beta2 near 1 or beta1 above 15/16.
  * `tensors` is a host array, read during the call; tensors with n == 0 are
  * skipped (their pointers may be NULL). Every device pointer is 16-byte
  * aligned, and what is written overlaps nothing else of the list: a state, a

@@ -13,16 +13,20 @@
 // (gradients present one step in twenty, spread over three decades: steps of 2.1 lr in
 // 32 bits, and of 8.5, 85 and 850 lr at gradients of 0.1, 1 and 10 without this).
 //
-// Roots are rounded to nearest, or at random where asked. To nearest, a root that a
-// step moves by less than half a code stays: with beta2 near 1 it does not grow with
-// its gradients until they are sqrt(((17/16)^2 - b2) / (1 - b2)) times it (11.4 at
-// 0.999, 3.7 at 0.99, 1.9 at 0.95) while its group's largest root stays, and its
-// updates are too large by up to that. (Gradients that grow by 5 beside a larger one,
-// b2 = 0.999: 3000 steps later the roots are 0.38 of what they should be, rounded at
-// random 0.98.) It shrinks no sooner, which makes steps small. At random it is the
-// hash of the value, its place and the step that decides, so a step repeats its bits:
-// 16 instructions a value more (134 million with masters 368 us instead of 338, 42 million
-// without 114 instead of 98).
+// Codes are rounded to nearest, or at random where asked. To nearest, what a step
+// moves by less than half a code stays, while its group's scale does:
+// - a root does not grow with its gradients until they are
+//   sqrt(((17/16)^2 - b2) / (1 - b2)) times it (11.4 at b2 = 0.999, 3.7 at 0.99, 1.9 at
+//   0.95), and its updates are too large by up to that. (Gradients that grow by 5
+//   beside a larger one, b2 = 0.999: 3000 steps later the roots are 0.38 of what they
+//   should be, rounded at random 0.98.) It shrinks no sooner, which makes steps small.
+// - a moment without gradients does not shrink below 1 / (2 - 2 b1) steps of its codes:
+//   at b1 = 0.9 four of the smallest, which are nothing beside the others; from 15/16
+//   on any, and its parameter goes on moving (b1 = 0.95 beside a steady moment: 74 lr in
+//   1000 steps, 2.1 in 32 bits and at random).
+// At random it is a hash of the value, its place and the step that decides, so a step
+// repeats its bits. Two hashes a value, 34 instructions of 100, bind it to those: 134
+// million with masters 427 us instead of 338, 42 million without 134 instead of 98.
 //
 // Every product and sum is rounded on its own (no contraction to a fused
 // multiply-add), so that a step gives the same bits wherever a tensor lies in
@@ -244,8 +248,9 @@ __device__ __forceinline__ void run_state(const Scalars &k, const Rates &c, cons
         if (S8) {
             // values past the end have no gradient and no moments: they stay zero and leave the scale alone
             float ms, rs;
-            const uint2 mq = quantize8(m, ms),
-                        rq = quantize8<16, true, RANDOM>(r, rs, c.seed + static_cast<uint32_t>(i));
+            const uint32_t place = c.seed + static_cast<uint32_t>(i);
+            const uint2 mq = quantize8<16, false, RANDOM>(m, ms, place + 0x40000000u),
+                        rq = quantize8<16, true, RANDOM>(r, rs, place);
             if (i < n) {
                 put_codes(e.m, i, n, mq);
                 put_codes(e.v, i, n, rq);

@@ -404,7 +404,7 @@ struct Items {
 };
 
 // params, grads, states, masters (or None), weight_decay (a number or a list), lr, step, beta1, beta2, eps,
-// grad_scale, scalars, whether 8-bit roots are rounded at random
+// grad_scale, scalars, whether 8-bit states are rounded at random
 PyObject *adamw_step(PyObject *const *a) {
     const Items params(a[0], "params must be a sequence"), grads(a[1], "grads must be a sequence"),
         states(a[2], "states must be a sequence");

@@ -167,9 +167,8 @@ __device__ __forceinline__ float round_randomly(float x, uint32_t noise) {
 // which would spoil the scale and saturate, are looked for only in a warp
 // whose maximum shows one. DIVISOR: none of the values is negative, and one that is
 // not zero gets no code below the smallest, 2^-9: what divides by it stays bounded.
-// RANDOM (of values that are not negative): a value between two codes becomes either,
-// the nearer one more often, so that its expectation is the value; `seed` differs from
-// eight values to the next.
+// RANDOM: a value between two codes becomes either, the nearer one more often, so that
+// its expectation is the value; `seed` differs by 8 from eight values to the next.
 template <int LANES = 16, bool DIVISOR = false, bool RANDOM = false>
 __device__ __forceinline__ uint2 quantize8(const float (&v)[8], float &scale, uint32_t seed = 0u) {
     float a = 0.0f;
@@ -194,7 +193,10 @@ __device__ __forceinline__ uint2 quantize8(const float (&v)[8], float &scale, ui
     for (int i = 0; i < 4; ++i) mul2(t[2 * i], t[2 * i + 1], inv, inv);
     if (RANDOM) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t[i] = round_randomly(t[i], noise20(__float_as_uint(v[i]), seed + i));
+        for (int i = 0; i < 8; ++i) {
+            const float r = round_randomly(fabsf(t[i]), noise20(__float_as_uint(v[i]), seed + i));
+            t[i] = DIVISOR ? r : copysignf(r, t[i]);
+        }
     }
     if (infinite) {
 #pragma unroll

@@ -201,12 +201,13 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
     and states (``adamw_state``; the two kinds may mix). step counts from 1.
     weight_decay: a number, or one for each tensor. scalars: an fp32 tensor of
     four on the device (``adamw_scalars``) that replaces lr, step and
-    grad_scale, for steps captured into a graph. rounding: of the roots in
-    8-bit states, "nearest", or "random" where beta2 is near 1: rounded to the
-    nearest code, a root does not grow with its gradients until they are
-    sqrt(((17/16)^2 - beta2) / (1 - beta2)) times it (11.4 at 0.999, 1.9 at
-    0.95) while its group's largest stays. Random rounding keeps its
-    expectation, and gives the same bits for the same arguments."""
+    grad_scale, for steps captured into a graph. rounding: of 8-bit states,
+    "nearest", or "random" where beta2 is near 1 or beta1 above 15/16. To
+    nearest, while its group's largest value stays, a root does not grow with
+    its gradients until they are sqrt(((17/16)^2 - beta2) / (1 - beta2)) times
+    it (11.4 at 0.999, 1.9 at 0.95), and a moment without gradients stops
+    shrinking. Random rounding keeps the values' expectations, and gives the
+    same bits for the same arguments."""
     if rounding not in ("nearest", "random"):
         raise ValueError('adamw_step: rounding must be "nearest" or "random"')
     random = rounding == "random"
