@@ -505,6 +505,36 @@ tpce_status tp_rmsnorm_backward(const void *dY, const void *S, const float *w, c
                                 void *ws, size_t ws_bytes, void *stream);
 
 /* ---------------------------------------------------------------------------
+ * The embedding: rows of the token table E [v_pad, h] by id, and the table's
+ * gradient. The table may be the one that vocab_parallel_ce multiplies by (tied).
+ * tp_embedding_forward:  X[t] = scale E[ids[t]];  ids [T] int32, each in
+ *   [0, v_valid) or -1 (padding: a row of zeros); X [T, h].
+ * tp_embedding_backward: dE[v] = scale sum over the t with ids[t] = v of dX[t],
+ *   all v_pad rows written (accumulate 0), or added to what dE holds
+ *   (accumulate not 0: rows that no token names are neither read nor written;
+ *   dE is then vocab_parallel_ce's, or the sum of the batches before).
+ * The product and the sums, in the order of the tokens, are fp32 and rounded
+ * once; results are deterministic.
+ * An id below -1 or from v_valid on counts as padding and records
+ * TPCE_ERR_INVALID in the device status word. ids stay as they are until the
+ * backward has run (one that changes meanwhile leads to no access outside).
+ * Shapes: h a multiple of 8 up to 2^20, T up to 2^28, 1 <= v_valid <= v_pad up
+ * to 2^30, T h and v_pad h up to 2^40; scale finite. What is written overlaps
+ * nothing else (TPCE_ERR_INVALID). T == 0: dE is zeroed unless accumulate; the
+ * rest is a no-op.
+ * Workspace: tpce_embedding_workspace_bytes for the backward (the sorted tokens,
+ * and two fp32 rows for each of up to 1024 chunks of them); 0 for T == 0 and
+ * invalid shapes.
+ * ------------------------------------------------------------------------- */
+size_t tpce_embedding_workspace_bytes(int64_t T, int64_t h, int64_t v_pad);
+tpce_status tp_embedding_forward(const int32_t *ids, const void *E, int64_t T, int64_t h,
+                                 int64_t v_pad, int64_t v_valid, float scale, int dtype, void *X,
+                                 void *stream);
+tpce_status tp_embedding_backward(const void *dX, const int32_t *ids, int64_t T, int64_t h,
+                                  int64_t v_pad, int64_t v_valid, float scale, int dtype,
+                                  int accumulate, void *dE, void *ws, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
  * Tokens sorted by expert and back, around a block that serves as an expert
  * (tp_swiglu_forward / backward or tp_mlp_* on the rows offsets[e] ..
  * offsets[e + 1] of Xs, once per expert).

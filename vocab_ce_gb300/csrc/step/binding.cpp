@@ -40,6 +40,9 @@ struct Api {
     decltype(&tp_expert_combine_forward) expert_combine_forward;
     decltype(&tp_expert_combine_backward) expert_combine_backward;
     decltype(&tp_adamw_step) adamw_step;
+    decltype(&tpce_embedding_workspace_bytes) embedding_workspace_bytes;
+    decltype(&tp_embedding_forward) embedding_forward;
+    decltype(&tp_embedding_backward) embedding_backward;
 };
 Api api;
 PyObject *check_status;   // Python's check(status, name): raises for a failure
@@ -391,6 +394,47 @@ PyObject *expert_combine_backward(PyObject *const *a) {
     return res.take();
 }
 
+// ------------------------------------------------------------------ embedding
+void need_ids(const at::Tensor &ids) {
+    if (ids.dim() != 1) throw Refused{"ids must be a vector of tokens, got shape " + shape_text(ids.sizes())};
+    need(ids, "ids", at::kInt, ids.sizes());
+}
+
+// ids, E, v_valid (or None), scale, out
+PyObject *embedding_forward(PyObject *const *a) {
+    const at::Tensor &ids = tensor(a[0], "ids"), &E = tensor(a[1], "E");
+    const int dt = matrix(E, "E");
+    need_ids(ids);
+    const int64_t T = ids.size(0), h = E.size(1), v_pad = E.size(0), v_valid = none(a[2]) ? v_pad : integer(a[2]);
+    const double scale = number(a[3]);
+    const Output X = output(a[4], "X", {T, h}, E.scalar_type(), E);
+    raise_on(api.embedding_forward(iptr(ids), ptr(E), T, h, v_pad, v_valid, static_cast<float>(scale), dt, ptr(X),
+                                   stream()),
+             "tp_embedding_forward");
+    written(X);
+    return THPVariable_Wrap(X.x);
+}
+
+// dX, ids, v_pad, v_valid (or None), scale, out, accumulate, ws
+PyObject *embedding_backward(PyObject *const *a) {
+    const at::Tensor &dX = tensor(a[0], "dX"), &ids = tensor(a[1], "ids");
+    const int dt = matrix(dX, "dX");
+    need_ids(ids);
+    const int64_t T = ids.size(0), h = dX.size(1), v_pad = integer(a[2]), v_valid = none(a[3]) ? v_pad : integer(a[3]);
+    need(dX, "dX", dX.scalar_type(), {T, h});
+    const double scale = number(a[4]);
+    const bool add = truth(a[6]);
+    if (add && none(a[5])) throw Refused{"tp_embedding_backward: accumulate needs out, the gradient that is added to"};
+    if (v_pad < 1 || v_pad > (int64_t{1} << 30)) throw Refused{"v_pad must be 1 .. 2^30"};
+    const Output dE = output(a[5], "dE", {v_pad, h}, dX.scalar_type(), dX);
+    const at::Tensor ws = workspace(a[7], api.embedding_workspace_bytes(T, h, v_pad), dX);
+    raise_on(api.embedding_backward(ptr(dX), iptr(ids), T, h, v_pad, v_valid, static_cast<float>(scale), dt, add,
+                                    ptr(dE), ptr(ws), bytes_of(ws), stream()),
+             "tp_embedding_backward");
+    written(dE);
+    return THPVariable_Wrap(dE.x);
+}
+
 // ------------------------------------------------------------------ AdamW
 // A list's entries, held while they are used.
 struct Items {
@@ -558,6 +602,8 @@ PyMethodDef methods[] = {
     STEP_CALL(expert_combine_forward, 4),
     STEP_CALL(expert_combine_backward, 5),
     STEP_CALL(adamw_step, 13),
+    STEP_CALL(embedding_forward, 5),
+    STEP_CALL(embedding_backward, 8),
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_step_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

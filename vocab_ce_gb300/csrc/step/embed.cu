@@ -1,0 +1,590 @@
+// embed.cu -- rows of the token table by id, and the table's gradient.
+//
+//   forward   X[t] = scale E[ids[t]]                       (ids[t] = -1: zeros)
+//   backward  dE[v] = scale sum over the t with ids[t] = v of dX[t],
+// the second written whole (rows that no token names are zeros) or added to what
+// dE holds, as a table has it that the loss is tied to; then only the rows that
+// tokens name are touched. The product and the sums are taken in 32 bits and
+// rounded once.
+//
+// The backward sorts the tokens by id, stably (a radix sort: whole numbers, no
+// order of atomics in it), and adds up runs of equal ids in the order of the
+// tokens, so the result is the same every time. A frequent id's run is long: the
+// sorted tokens are cut into chunks of equal length, and a run that crosses a
+// cut leaves fp32 sums in the workspace that a last kernel adds in order.
+// All of it is bound by HBM.
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <initializer_list>
+#include <utility>
+
+#include "host.h"
+#include "ptx.cuh"
+#include "step/launch.cuh"
+#include "step/vec.cuh"
+
+namespace tpce {
+namespace {
+
+using namespace step;
+
+constexpr int64_t kMaxTokens = int64_t{1} << 28, kMaxTable = int64_t{1} << 30;
+constexpr int kThreads = 256;
+
+// ------------------------------------------------------------------ forward
+// `lanes` threads of a block share a piece of lanes * U vectors of a token's row.
+template <typename T, int U>
+__global__ void __launch_bounds__(kThreads)
+    embed_forward_kernel(const T *E, const int32_t *ids, int64_t tokens, int64_t v_valid, int vectors, int lanes,
+                         int parts, float scale, T *__restrict__ X, uint32_t *err) {
+    const int64_t piece = static_cast<int64_t>(blockIdx.x) * (kThreads / lanes) + threadIdx.x / lanes;
+    const int64_t t = piece / parts;
+    const int c0 = static_cast<int>(piece - t * parts) * lanes * U + (threadIdx.x & (lanes - 1));
+    grid_begin();
+    if (t >= tokens) return;
+    const int32_t id = ids[t];
+    const bool known = id >= 0 && id < v_valid;
+    if (!known && id != -1) ptx::record_error(err, kErrInvalid | (5u << 8));
+    Raw8<T> r[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        zero8(r[u]);
+        if (known && c0 + u * lanes < vectors)
+            r[u] = load8(E + (static_cast<int64_t>(id) * vectors + c0 + u * lanes) * 8);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (c0 + u * lanes >= vectors) continue;
+        if (known) {
+            float v[8];
+            unpack8(r[u], v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mul2(v[2 * i], v[2 * i + 1], scale, scale);
+            pack8(v, r[u]);
+        }
+        store8(X + (t * vectors + c0 + u * lanes) * 8, r[u]);
+    }
+}
+
+// ------------------------------------------------------------------ the sort
+// Passes over kDigit bits, the lowest first. A block takes a chunk of the tokens,
+// each of its warps a contiguous run of the chunk. One block does all passes in
+// one launch; several count their digits in one launch and place in the next.
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxBins = 1024;
+constexpr int64_t kSortChunk = 1024, kSortBlocks = 256;
+
+struct SortSplit {
+    int64_t chunk;
+    int blocks, passes, bits;  // bits of a pass
+};
+inline SortSplit sort_split(int64_t tokens, int64_t v_pad) {
+    SortSplit sp{};
+    int all = 1;  // of the keys 0 .. v_pad; v_pad is that of a token without a row
+    while ((int64_t{1} << all) <= v_pad) ++all;
+    sp.passes = (all + 9) / 10;
+    sp.bits = (all + sp.passes - 1) / sp.passes;
+    sp.chunk = std::max<int64_t>(kSortChunk, (tokens + kSortBlocks - 1) / kSortBlocks);
+    sp.blocks = tokens <= 2 * sp.chunk ? 1 : static_cast<int>((tokens + sp.chunk - 1) / sp.chunk);
+    if (sp.blocks == 1) sp.chunk = tokens;
+    return sp;
+}
+
+// The key of a token in the first pass, where ids are the keys.
+__device__ __forceinline__ int32_t key_of(int32_t id, int32_t v_valid, int32_t v_pad, uint32_t *err) {
+    if (id >= 0 && id < v_valid) return id;
+    if (id != -1) ptx::record_error(err, kErrInvalid | (5u << 8));
+    return v_pad;
+}
+
+__global__ void __launch_bounds__(kThreads)
+    embed_count_kernel(const int32_t *keys, int64_t n, int64_t chunk, int shift, int bins, bool ids, int32_t v_valid,
+                       int32_t v_pad, uint32_t *__restrict__ counts) {
+    extern __shared__ uint32_t count[];  // [bins]
+    for (int b = threadIdx.x; b < bins; b += kThreads) count[b] = 0u;
+    grid_begin();
+    __syncthreads();
+    const int64_t first = blockIdx.x * chunk, last = min(n, first + chunk);
+#pragma unroll 4
+    for (int64_t i = first + threadIdx.x; i < last; i += kThreads) {
+        const int32_t k = ids ? key_of(keys[i], v_valid, v_pad, nullptr) : keys[i];
+        atomicAdd(&count[(k >> shift) & (bins - 1)], 1u);  // whole numbers: any order gives the same
+    }
+    __syncthreads();
+    for (int b = threadIdx.x; b < bins; b += kThreads)
+        counts[static_cast<int64_t>(blockIdx.x) * bins + b] = count[b];
+}
+
+// One pass of a block: from keys (of the tokens from[i], or of i itself) to key_out and token_out.
+// counts NULL: this block is the only one.
+__device__ void sort_pass(const int32_t *keys, const int32_t *from, int64_t n, int64_t chunk, int shift, int bits,
+                          const uint32_t *counts, int32_t v_valid, int32_t v_pad, int32_t *key_out,
+                          int32_t *token_out, uint32_t *smem, uint32_t *scan, uint32_t *err) {
+    const int bins = 1 << bits;
+    uint32_t *count = smem;                    // [kWarps][bins], then the next place of each warp's digits
+    uint32_t *all = smem + kWarps * bins;      // [bins] of all blocks
+    uint32_t *below = all + bins;              // [bins] of the blocks before
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool ids = from == nullptr;
+    for (int b = threadIdx.x; b < (kWarps + 2) * bins; b += kThreads) smem[b] = 0u;
+    __syncthreads();
+    if (counts) {
+        int width = 1;
+        while (width < bins && width < kThreads) width *= 2;
+        const int parts = kThreads / width, part = threadIdx.x / width;
+        for (int b = threadIdx.x & (width - 1); b < bins; b += width) {
+            uint32_t sum = 0u, before = 0u;
+#pragma unroll 8
+            for (int q = part; q < static_cast<int>(gridDim.x); q += parts) {
+                const uint32_t c = counts[static_cast<int64_t>(q) * bins + b];
+                sum += c;
+                before += q < static_cast<int>(blockIdx.x) ? c : 0u;
+            }
+            atomicAdd(&all[b], sum);
+            atomicAdd(&below[b], before);
+        }
+    }
+    const int64_t begin = blockIdx.x * chunk, end = min(n, begin + chunk);
+    const int64_t run = ((end - begin + kWarps - 1) / kWarps + 31) / 32 * 32;
+    const int64_t first = begin + warp * run, last = min(end, first + run);
+    uint32_t *mine = count + warp * bins;
+    auto digit = [&](int32_t k) { return (k >> shift) & (bins - 1); };
+#pragma unroll 4
+    for (int64_t i = first + lane; i < last; i += 32)
+        atomicAdd(&mine[digit(ids ? key_of(keys[i], v_valid, v_pad, err) : keys[i])], 1u);
+    __syncthreads();
+    for (int b = threadIdx.x; b < bins; b += kThreads) {
+        uint32_t sum = 0u;
+#pragma unroll
+        for (int q = 0; q < kWarps; ++q) {
+            const uint32_t c = count[q * bins + b];
+            count[q * bins + b] = sum;
+            sum += c;
+        }
+        if (!counts) all[b] = sum;
+    }
+    __syncthreads();
+    // first places: a scan over the digits, adjacent ones a thread
+    constexpr int kEach = kMaxBins / kThreads;
+    uint32_t own[kEach], sum = 0u;
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+        const int b = threadIdx.x * kEach + u;
+        own[u] = b < bins ? all[b] : 0u;
+        sum += own[u];
+    }
+    uint32_t incl = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t o = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += o;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    uint32_t at = incl - sum;
+    for (int q = 0; q < warp; ++q) at += scan[q];
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+        const int b = threadIdx.x * kEach + u;
+        if (b < bins) {
+            const uint32_t place = at + below[b];
+            at += own[u];
+            for (int q = 0; q < kWarps; ++q) count[q * bins + b] += place;
+        }
+    }
+    __syncthreads();
+    constexpr int kBatch = 4;
+    for (int64_t i0 = first; i0 < last; i0 += 32 * kBatch) {
+        int32_t k[kBatch], t[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int64_t i = i0 + u * 32 + lane;
+            k[u] = i < last ? (ids ? key_of(keys[i], v_valid, v_pad, nullptr) : keys[i]) : 0;
+            t[u] = i >= last ? 0 : ids ? static_cast<int32_t>(i) : from[i];
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const bool there = i0 + u * 32 + lane < last;
+            const int d = there ? digit(k[u]) : bins;
+            const uint32_t same = same_value(d, bits + 1);
+            const uint32_t before = __popc(same & ((1u << lane) - 1u));
+            uint32_t p = UINT_MAX;
+            if (there) p = mine[d] + before;
+            __syncwarp();
+            if (there && before == 0u) mine[d] += __popc(same);
+            __syncwarp();
+            // an id that changes while it is sorted must lead nowhere
+            if (there && p < n) {
+                key_out[p] = k[u];
+                token_out[p] = t[u];
+            }
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kThreads)
+    embed_place_kernel(const int32_t *keys, const int32_t *from, int64_t n, int64_t chunk, int shift, int bits,
+                       const uint32_t *counts, int32_t v_valid, int32_t v_pad, int32_t *key_out, int32_t *token_out,
+                       uint32_t *err) {
+    extern __shared__ uint32_t smem[];
+    __shared__ uint32_t scan[kWarps];
+    grid_begin();
+    sort_pass(keys, from, n, chunk, shift, bits, counts, v_valid, v_pad, key_out, token_out, smem, scan, err);
+}
+
+// All passes of few tokens; the last one ends in key[1], token[1] (odd passes) or key[0], token[0].
+struct SortBuffers {
+    int32_t *key[2], *token[2];
+};
+__global__ void __launch_bounds__(kThreads)
+    embed_sort_kernel(const int32_t *ids, int64_t n, int passes, int bits, int32_t v_valid, int32_t v_pad,
+                      SortBuffers buf, uint32_t *err) {
+    extern __shared__ uint32_t smem[];
+    __shared__ uint32_t scan[kWarps];
+    grid_begin();
+    for (int p = 0; p < passes; ++p) {
+        const int to = (p + 1) & 1;
+        sort_pass(p ? buf.key[to ^ 1] : ids, p ? buf.token[to ^ 1] : nullptr, n, n, p * bits, bits, nullptr, v_valid,
+                  v_pad, buf.key[to], buf.token[to], smem, scan, err);
+        __syncthreads();  // the block's stores to global memory, too, are seen by its threads after this
+    }
+}
+
+// ------------------------------------------------------------------ the sums
+// Chunks of sorted tokens. A chunk's first run may have begun before it, and its
+// last may go on after it: their sums go to the workspace, the first's to row 2 c,
+// the last's to row 2 c + 1 (a run that does both is the chunk's only one: row 2 c).
+struct SumSplit {
+    int64_t chunk;
+    int chunks, lanes;  // threads of a row's piece of lanes vectors of eight columns
+    int parts;          // pieces of a row
+};
+inline SumSplit sum_split(int64_t tokens, int64_t h) {
+    SumSplit sp{};
+    sp.chunk = std::max<int64_t>(16, (tokens + 1023) / 1024);
+    sp.chunks = static_cast<int>((tokens + sp.chunk - 1) / sp.chunk);
+    const int64_t vectors = h / 8;
+    sp.lanes = 8;
+    while (sp.lanes < kThreads && sp.lanes < vectors) sp.lanes *= 2;
+    sp.parts = static_cast<int>((vectors + sp.lanes - 1) / sp.lanes);
+    return sp;
+}
+
+template <typename T>
+__device__ __forceinline__ void finish_row(const float (&sum)[8], const Raw8<T> &old, bool add, float scale,
+                                           T *__restrict__ to) {
+    float v[8] = {};
+    if (add) unpack8(old, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = add ? fmaf(sum[i], scale, v[i]) : sum[i] * scale;
+    Raw8<T> r;
+    pack8(v, r);
+    store8(to, r);
+}
+
+// Whether a row is among the sorted keys.
+__device__ __forceinline__ bool among(const int32_t *key, int64_t n, int32_t v) {
+    int64_t lo = 0, hi = n;
+    while (lo < hi) {
+        const int64_t mid = (lo + hi) >> 1;
+        if (key[mid] < v)
+            lo = mid + 1;
+        else
+            hi = mid;
+    }
+    return lo < n && key[lo] == v;
+}
+
+constexpr int kFillRows = 32;
+
+// The first `fill` blocks write zeros to the rows that no token names, kFillRows of
+// them each; the others add up chunks. Loads are issued four tokens at a time, with
+// the old row where a run ends.
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 4)
+    embed_sum_kernel(const T *dX, const int32_t *key, const int32_t *token, int64_t n, int64_t v_pad, int vectors,
+                     SumSplit sp, unsigned fill, bool add, float scale, float *__restrict__ partial, T *dE) {
+    grid_begin();
+    if (blockIdx.x < fill) {
+        __shared__ bool named[kFillRows];
+        const int64_t v0 = static_cast<int64_t>(blockIdx.x) * kFillRows;
+        if (threadIdx.x < kFillRows) {
+            const int64_t v = v0 + threadIdx.x;
+            named[threadIdx.x] = v >= v_pad || among(key, n, static_cast<int32_t>(v));
+        }
+        __syncthreads();
+        Raw8<T> zero;
+        zero8(zero);
+        for (int r = 0; r < kFillRows; ++r) {
+            if (named[r]) continue;
+            for (int c = threadIdx.x; c < vectors; c += kThreads)
+                store8(dE + ((v0 + r) * vectors + c) * 8, zero);
+        }
+        return;
+    }
+    const int64_t piece = static_cast<int64_t>(blockIdx.x - fill) * (kThreads / sp.lanes) + threadIdx.x / sp.lanes;
+    const int64_t c = piece / sp.parts;
+    const int at = static_cast<int>(piece - c * sp.parts) * sp.lanes + (threadIdx.x & (sp.lanes - 1));
+    if (c >= sp.chunks || at >= vectors) return;
+    const int64_t p0 = c * sp.chunk, p1 = min(n, p0 + sp.chunk);
+    int32_t now = key[p0];
+    bool open = p0 > 0 && key[p0 - 1] == now;  // the run at hand began in a chunk before
+    float sum[8] = {};
+    constexpr int kBatch = 4;
+    for (int64_t p = p0; p < p1 && static_cast<uint32_t>(now) < v_pad; p += kBatch) {
+        int32_t k[kBatch + 1];
+        Raw8<T> x[kBatch], old[kBatch];
+        bool there[kBatch];
+#pragma unroll
+        for (int u = 0; u <= kBatch; ++u) k[u] = p + u < n ? key[p + u] : -1;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            // places that the sort has not written (ids that changed under it) lead nowhere
+            const int32_t t = p + u < p1 ? token[p + u] : -1;
+            there[u] = static_cast<uint32_t>(k[u]) < v_pad && static_cast<uint32_t>(t) < n;
+            if (there[u]) x[u] = load8(dX + (static_cast<int64_t>(t) * vectors + at) * 8);
+            if (add && there[u] && k[u + 1] != k[u])
+                old[u] = load8(dE + (static_cast<int64_t>(k[u]) * vectors + at) * 8);
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            if (!there[u]) {
+                now = static_cast<int32_t>(v_pad);
+                break;
+            }
+            float v[8];
+            unpack8(x[u], v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[i] += v[i];
+            const bool ends = k[u + 1] != k[u], cut = p + u + 1 == p1;
+            if (!ends && !cut) continue;
+            if (ends && !open) {
+                finish_row(sum, old[u], add, scale, dE + (static_cast<int64_t>(k[u]) * vectors + at) * 8);
+            } else {
+                float4 *to = reinterpret_cast<float4 *>(partial + ((2 * c + (open ? 0 : 1)) * vectors + at) * 8);
+                to[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+                to[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
+            }
+            open = false;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
+        }
+    }
+}
+
+// The runs that cross a cut, by the chunk that they begin in.
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+    embed_join_kernel(const int32_t *key, int64_t n, int64_t v_pad, int vectors, SumSplit sp, bool add, float scale,
+                      const float *partial, T *dE) {
+    const int64_t piece = static_cast<int64_t>(blockIdx.x) * (kThreads / sp.lanes) + threadIdx.x / sp.lanes;
+    const int64_t c = piece / sp.parts;
+    const int at = static_cast<int>(piece - c * sp.parts) * sp.lanes + (threadIdx.x & (sp.lanes - 1));
+    grid_begin();
+    if (c >= sp.chunks - 1 || at >= vectors) return;
+    const int64_t p0 = c * sp.chunk, p1 = p0 + sp.chunk;  // not the last chunk: p1 < n
+    const int32_t k = key[p1];
+    if (static_cast<uint32_t>(k) >= v_pad || key[p1 - 1] != k) return;
+    if (key[p0] == k && p0 > 0 && key[p0 - 1] == k) return;  // begun before this chunk
+    T *row = dE + (static_cast<int64_t>(k) * vectors + at) * 8;
+    Raw8<T> old;
+    zero8(old);
+    if (add) old = load8(row);
+    float sum[8];
+    load8f(partial + ((2 * c + 1) * vectors + at) * 8, sum);
+    for (int64_t m = c + 1; m < sp.chunks && key[m * sp.chunk] == k; ++m) {
+        float v[8];
+        load8f(partial + (2 * m * vectors + at) * 8, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] += v[i];
+    }
+    finish_row(sum, old, add, scale, row);
+}
+
+// ------------------------------------------------------------------ host
+tpce_status check_shape(const char *name, int64_t T, int64_t h, int64_t v_pad, int64_t v_valid, float scale,
+                        int dtype) {
+    if (dtype != TPCE_BF16 && dtype != TPCE_F32) return fail(TPCE_ERR_INVALID, "%s: dtype %d", name, dtype);
+    if (!std::isfinite(scale)) return fail(TPCE_ERR_INVALID, "%s: scale is not finite", name);
+    if (T < 0 || T > kMaxTokens || h < 8 || h % 8 != 0 || h > (1 << 20) || v_pad < 1 || v_pad > kMaxTable ||
+        v_valid < 1 || v_valid > v_pad || T > (int64_t{1} << 40) / h || v_pad > (int64_t{1} << 40) / h)
+        return fail(TPCE_ERR_SHAPE,
+                    "%s: T = %lld (up to 2^28), h = %lld (a multiple of 8 up to 2^20), v_pad = %lld (up to 2^30), "
+                    "v_valid = %lld (1 .. v_pad), T h and v_pad h up to 2^40",
+                    name, static_cast<long long>(T), static_cast<long long>(h), static_cast<long long>(v_pad),
+                    static_cast<long long>(v_valid));
+    return TPCE_OK;
+}
+
+tpce_status check_pointers(const char *name, std::initializer_list<const void *> need) {
+    for (const void *p : need)
+        if (!p) return fail(TPCE_ERR_INVALID, "%s: null pointer", name);
+    for (const void *p : need)
+        if (!aligned16(p)) return fail(TPCE_ERR_ALIGN, "%s: a pointer is not 16-byte aligned", name);
+    return TPCE_OK;
+}
+
+inline bool overlap(const void *a, size_t a_bytes, const void *b, size_t b_bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a_bytes && b_bytes && x < y + b_bytes && y < x + a_bytes;
+}
+
+inline size_t bytes_of(int64_t rows, int64_t h, int dtype) {
+    return static_cast<size_t>(rows) * static_cast<size_t>(h) * (dtype == TPCE_BF16 ? 2 : 4);
+}
+
+// The workspace: keys and tokens twice, the blocks' counts, the cut runs' sums.
+struct Layout {
+    size_t each, counts, partial, total;
+};
+inline Layout layout_of(int64_t T, int64_t h, int64_t v_pad) {
+    const SortSplit so = sort_split(T, v_pad);
+    const SumSplit su = sum_split(T, h);
+    Layout l{};
+    l.each = round_up(static_cast<size_t>(T) * sizeof(int32_t), 256);
+    l.counts = 4 * l.each;
+    l.partial = l.counts +
+                round_up(so.blocks > 1 ? static_cast<size_t>(so.blocks) * (size_t{4} << so.bits) : 0, 256);
+    l.total = l.partial + (su.chunks > 1 ? 2 * static_cast<size_t>(su.chunks) * static_cast<size_t>(h) * 4 : 0);
+    return l;
+}
+
+template <typename T>
+tpce_status embed_forward(const int32_t *ids, const void *E, int64_t tokens, int64_t h, int64_t v_valid, float scale,
+                          void *X, cudaStream_t s) {
+    const int vectors = static_cast<int>(h / 8);
+    int lanes = 8;
+    while (lanes < kThreads && lanes * 2 < vectors) lanes *= 2;
+    // two vectors a thread, one where that would leave SMs without a block
+    const bool few = tokens * vectors < int64_t{2} * kThreads * 2 * num_sms();
+    const int each = lanes * (few ? 1 : 2);
+    const int parts = (vectors + each - 1) / each;
+    const unsigned blocks = static_cast<unsigned>((tokens * parts + kThreads / lanes - 1) / (kThreads / lanes));
+    KernelTimer timer("embed_forward", s);
+    auto go = [&](auto kernel) {
+        return launch(kernel, blocks, kThreads, 0, s, static_cast<const T *>(E), ids, tokens, v_valid, vectors, lanes,
+                      parts, scale, static_cast<T *>(X), device_error_word());
+    };
+    const cudaError_t e = few ? go(embed_forward_kernel<T, 1>) : go(embed_forward_kernel<T, 2>);
+    return e == cudaSuccess ? check_launch("embed_forward", s) : fail_cuda(e, "embed_forward");
+}
+
+tpce_status embed_sort(const int32_t *ids, int64_t T, int64_t v_pad, int64_t v_valid, const SortSplit &sp,
+                       const SortBuffers &buf, uint32_t *counts, cudaStream_t s) {
+    const size_t smem = (kWarps + 2) * (size_t{4} << sp.bits);
+    const int32_t valid = static_cast<int32_t>(v_valid), pad = static_cast<int32_t>(v_pad);
+    KernelTimer timer("embed_sort", s);
+    if (sp.blocks == 1) {
+        const cudaError_t e = launch(embed_sort_kernel, 1, kThreads, smem, s, ids, T, sp.passes, sp.bits, valid, pad,
+                                     buf, device_error_word());
+        return e == cudaSuccess ? check_launch("embed_sort", s) : fail_cuda(e, "embed_sort");
+    }
+    for (int p = 0; p < sp.passes; ++p) {
+        const int to = (p + 1) & 1;
+        const int32_t *keys = p ? buf.key[to ^ 1] : ids, *from = p ? buf.token[to ^ 1] : nullptr;
+        cudaError_t e = launch(embed_count_kernel, sp.blocks, kThreads, size_t{4} << sp.bits, s, keys, T, sp.chunk,
+                               p * sp.bits, 1 << sp.bits, p == 0, valid, pad, counts);
+        if (e != cudaSuccess) return fail_cuda(e, "embed_count");
+        tpce_status st = check_launch("embed_count", s);
+        if (st != TPCE_OK) return st;
+        e = launch(embed_place_kernel, sp.blocks, kThreads, smem, s, keys, from, T, sp.chunk, p * sp.bits, sp.bits,
+                   counts, valid, pad, buf.key[to], buf.token[to], device_error_word());
+        if (e != cudaSuccess) return fail_cuda(e, "embed_place");
+        if ((st = check_launch("embed_place", s)) != TPCE_OK) return st;
+    }
+    return TPCE_OK;
+}
+
+template <typename T>
+tpce_status embed_sums(const void *dX, int64_t tokens, int64_t h, int64_t v_pad, const int32_t *key,
+                       const int32_t *token, float scale, bool add, float *partial, void *dE, cudaStream_t s) {
+    const SumSplit sp = sum_split(tokens, h);
+    const int vectors = static_cast<int>(h / 8);
+    const int64_t of_block = kThreads / sp.lanes;
+    const int64_t blocks = (static_cast<int64_t>(sp.chunks) * sp.parts + of_block - 1) / of_block;
+    const unsigned fill = add ? 0u : static_cast<unsigned>((v_pad + kFillRows - 1) / kFillRows);
+    {
+        KernelTimer timer("embed_sum", s);
+        const cudaError_t e =
+            launch(embed_sum_kernel<T>, fill + static_cast<unsigned>(blocks), kThreads, 0, s,
+                   static_cast<const T *>(dX), key, token, tokens, v_pad, vectors, sp, fill, add, scale, partial,
+                   static_cast<T *>(dE));
+        if (e != cudaSuccess) return fail_cuda(e, "embed_sum");
+        const tpce_status st = check_launch("embed_sum", s);
+        if (st != TPCE_OK || sp.chunks == 1) return st;
+    }
+    KernelTimer timer("embed_join", s);
+    const cudaError_t e = launch(embed_join_kernel<T>, static_cast<unsigned>(blocks), kThreads, 0, s, key, tokens,
+                                 v_pad, vectors, sp, add, scale, partial, static_cast<T *>(dE));
+    return e == cudaSuccess ? check_launch("embed_join", s) : fail_cuda(e, "embed_join");
+}
+
+}  // namespace
+}  // namespace tpce
+
+// ====================================================================== C ABI
+using namespace tpce;
+
+extern "C" tpce_status tp_embedding_forward(const int32_t *ids, const void *E, int64_t T, int64_t h, int64_t v_pad,
+                                            int64_t v_valid, float scale, int dtype, void *X, void *stream) {
+    tpce_status st = check_shape("tp_embedding_forward", T, h, v_pad, v_valid, scale, dtype);
+    if (st != TPCE_OK || T == 0) return st;
+    if ((st = check_pointers("tp_embedding_forward", {ids, E, X})) != TPCE_OK) return st;
+    const size_t rows = bytes_of(T, h, dtype);
+    if (overlap(X, rows, E, bytes_of(v_valid, h, dtype)) || overlap(X, rows, ids, static_cast<size_t>(T) * 4))
+        return fail(TPCE_ERR_INVALID, "tp_embedding_forward: X overlaps E or ids");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return dtype == TPCE_BF16 ? embed_forward<__nv_bfloat16>(ids, E, T, h, v_valid, scale, X, s)
+                              : embed_forward<float>(ids, E, T, h, v_valid, scale, X, s);
+}
+
+extern "C" size_t tpce_embedding_workspace_bytes(int64_t T, int64_t h, int64_t v_pad) {
+    if (check_shape("embedding", T, h, v_pad, 1, 1.0f, TPCE_BF16) != TPCE_OK || T == 0) return 0;
+    return layout_of(T, h, v_pad).total;
+}
+
+extern "C" tpce_status tp_embedding_backward(const void *dX, const int32_t *ids, int64_t T, int64_t h, int64_t v_pad,
+                                             int64_t v_valid, float scale, int dtype, int accumulate, void *dE,
+                                             void *ws, size_t ws_bytes, void *stream) {
+    const char *name = "tp_embedding_backward";
+    tpce_status st = check_shape(name, T, h, v_pad, v_valid, scale, dtype);
+    if (st != TPCE_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const size_t table = bytes_of(v_pad, h, dtype);
+    if (T == 0) {
+        if (accumulate) return TPCE_OK;
+        if ((st = check_pointers(name, {dE})) != TPCE_OK) return st;
+        const cudaError_t e = taken(cudaMemsetAsync(dE, 0, table, s));
+        return e == cudaSuccess ? TPCE_OK : fail_cuda(e, name);
+    }
+    if ((st = check_pointers(name, {dX, ids, dE})) != TPCE_OK) return st;
+    const Layout l = layout_of(T, h, v_pad);
+    if (!ws || ws_bytes < l.total)
+        return fail(TPCE_ERR_WORKSPACE, "%s: %zu bytes of workspace needed, %zu given", name, l.total,
+                    ws ? ws_bytes : size_t{0});
+    if (!aligned16(ws)) return fail(TPCE_ERR_ALIGN, "%s: a pointer is not 16-byte aligned", name);
+    const std::pair<const void *, size_t> parts[] = {
+        {dX, bytes_of(T, h, dtype)}, {ids, static_cast<size_t>(T) * 4}, {dE, table}, {ws, l.total}};
+    for (const auto &a : parts)
+        for (const auto &b : parts)
+            // dX and ids are only read
+            if (&a < &b && &b > &parts[1] && overlap(a.first, a.second, b.first, b.second))
+                return fail(TPCE_ERR_INVALID, "%s: dE or ws overlaps another argument", name);
+    char *base = static_cast<char *>(ws);
+    SortBuffers buf;
+    for (int i = 0; i < 2; ++i) {
+        buf.key[i] = reinterpret_cast<int32_t *>(base + 2 * i * l.each);
+        buf.token[i] = reinterpret_cast<int32_t *>(base + (2 * i + 1) * l.each);
+    }
+    uint32_t *counts = reinterpret_cast<uint32_t *>(base + l.counts);
+    float *partial = reinterpret_cast<float *>(base + l.partial);
+    const SortSplit sp = sort_split(T, v_pad);
+    if ((st = embed_sort(ids, T, v_pad, v_valid, sp, buf, counts, s)) != TPCE_OK) return st;
+    const int last = sp.passes & 1;
+    return dtype == TPCE_BF16
+               ? embed_sums<__nv_bfloat16>(dX, T, h, v_pad, buf.key[last], buf.token[last], scale, accumulate != 0,
+                                           partial, dE, s)
+               : embed_sums<float>(dX, T, h, v_pad, buf.key[last], buf.token[last], scale, accumulate != 0, partial,
+                                   dE, s);
+}

@@ -81,17 +81,6 @@ __global__ void __launch_bounds__(kPlanThreads)
     for (int e = threadIdx.x; e < E; e += kPlanThreads) counts[static_cast<int64_t>(blockIdx.x) * E + e] = count[e];
 }
 
-// The lanes whose value equals this lane's, from one ballot for each of its bits.
-__device__ __forceinline__ uint32_t same_value(int v, int bits) {
-    uint32_t same = 0xffffffffu;
-    for (int b = 0; b < bits; ++b) {
-        const bool one = (v >> b) & 1;
-        const uint32_t with = __ballot_sync(0xffffffffu, one);
-        same &= one ? with : ~with;
-    }
-    return same;
-}
-
 // counts NULL: this block is the only one.
 __global__ void __launch_bounds__(kPlanThreads)
     expert_place_kernel(const int32_t *ids, int64_t n, int64_t chunk, int E,

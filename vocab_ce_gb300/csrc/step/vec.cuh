@@ -1,6 +1,6 @@
 // vec.cuh -- what the row and element kernels of a training step share: eight
 // values of a row in registers, the e4m3 codes with one scale per 128 values,
-// and sums over a warp or a block.
+// equal values of a warp, and sums over a warp or a block.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -230,6 +230,18 @@ __device__ __forceinline__ void decode8(uint2 q, float scale, float (&v)[8]) {
         v[2 * i + 1] = f.y;
         mul2(v[2 * i], v[2 * i + 1], scale, scale);
     }
+}
+
+// ------------------------------------------------------------------ sorting
+// The lanes whose value equals this lane's, from one ballot for each of its bits.
+__device__ __forceinline__ uint32_t same_value(int v, int bits) {
+    uint32_t same = 0xffffffffu;
+    for (int b = 0; b < bits; ++b) {
+        const bool one = (v >> b) & 1;
+        const uint32_t with = __ballot_sync(0xffffffffu, one);
+        same &= one ? with : ~with;
+    }
+    return same;
 }
 
 // ------------------------------------------------------------------ sums

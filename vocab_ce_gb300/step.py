@@ -31,7 +31,8 @@ GROUP = 128  # values that share one scale in the 8-bit formats
 # the library's entry points that the binding calls, in its order
 _ENTRIES = ("tpce_rmsnorm_workspace_bytes", "tp_rmsnorm_forward", "tp_rmsnorm_backward",
             "tpce_expert_plan_workspace_bytes", "tp_expert_plan", "tp_expert_dispatch_forward",
-            "tp_expert_dispatch_backward", "tp_expert_combine_forward", "tp_expert_combine_backward", "tp_adamw_step")
+            "tp_expert_dispatch_backward", "tp_expert_combine_forward", "tp_expert_combine_backward", "tp_adamw_step",
+            "tpce_embedding_workspace_bytes", "tp_embedding_forward", "tp_embedding_backward")
 _lock = threading.Lock()
 _binding = None
 
@@ -159,6 +160,34 @@ def tp_expert_combine_backward(dZ: torch.Tensor, Ys: torch.Tensor, plan: Dict[st
         with _on(stream, dZ, Ys, plan, weights, out):
             return _b().expert_combine_backward(dZ, Ys, plan, weights, out)
     return _b().expert_combine_backward(dZ, Ys, plan, weights, out)
+
+
+# ---------------------------------------------------------------------- embedding
+def embedding_workspace_bytes(T: int, h: int, v_pad: int) -> int:
+    return int(lib().tpce_embedding_workspace_bytes(T, h, v_pad))
+
+
+def tp_embedding_forward(ids: torch.Tensor, E: torch.Tensor, v_valid: Optional[int] = None, scale: float = 1.0,
+                         out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """X [T, h]: scale times the row of E [v_pad, h] that each of ids [T] (int32)
+    names. An id is in [0, v_valid) (default: all rows) or -1, padding, whose row
+    is zeros; others count as padding and are reported by ``device_status``."""
+    if stream is not None:
+        with _on(stream, ids, E, out):
+            return _b().embedding_forward(ids, E, v_valid, scale, out)
+    return _b().embedding_forward(ids, E, v_valid, scale, out)
+
+
+def tp_embedding_backward(dX: torch.Tensor, ids: torch.Tensor, v_pad: int, v_valid: Optional[int] = None,
+                          scale: float = 1.0, out: Optional[torch.Tensor] = None, accumulate: bool = False,
+                          ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """dE [v_pad, h]: scale times the sum of dX [T, h] over each id's tokens,
+    rows without tokens zero. accumulate: added to ``out`` instead, the dE of
+    ``vocab_parallel_ce`` where the table is tied, or of the batches before."""
+    if stream is not None:
+        with _on(stream, dX, ids, out, ws):
+            return _b().embedding_backward(dX, ids, v_pad, v_valid, scale, out, accumulate, ws)
+    return _b().embedding_backward(dX, ids, v_pad, v_valid, scale, out, accumulate, ws)
 
 
 # ---------------------------------------------------------------------- AdamW
