@@ -337,7 +337,7 @@ tpce_status tp_row_linear_backward_sp(const void *const *dY_chunks, const void *
  * Attention projections ("Distributed tensor parallelism ...", section "The
  * Multi-Head Attention Block"; "Mathematical Foundations ...", section
  * "Self-Attention Layer Decomposition"). The attention core between them is
- * not part of this library.
+ * tp_attn_core_*, below.
  *
  * tp_attn_qkv_*: the fused Q, K, V projection, column-parallel by heads:
  *   QKV = X Wqkv + bqkv,  X [T, h], Wqkv [h, (n_heads + 2 n_kv_heads) d],
@@ -375,6 +375,50 @@ tpce_status tp_attn_out_backward(const void *dZ, const void *O, const void *Wo,
                                  int64_t T, int64_t h, int64_t n_heads, int64_t head_dim, int t,
                                  int dtype, void *dO, void *dWo, float *dbo,
                                  void *ws, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * The attention core between the projections: causal softmax attention on the
+ * fused rows of tp_attn_qkv_forward ("Mathematical Foundations ...", section
+ * "Self-Attention Layer Decomposition"). Each head is computed on its own, so the
+ * split of heads over t shards changes nothing here and t is no argument.
+ *   QKV [T, (n_heads + 2 n_kv_heads) d], columns as tp_attn_qkv_* has them.
+ *   offsets [sequences + 1] int32 on the device, ascending within [0, T]: sequence
+ *   b is rows offsets[b] .. offsets[b + 1]; NULL: one sequence of all T rows.
+ *   Queries and keys of a sequence count from 0; query i sees key j of its own
+ *   sequence when  j <= i and (window == 0 or i - j < window or j < sinks):
+ *   with a window, the last `window` keys up to its own and the first `sinks`
+ *   ones, which stay visible. A query always sees its own key.
+ * tp_attn_core_forward: for each query head, with the K and V of its group,
+ *   S = scale Q K^T, O = softmax(S) V over the visible keys, lse = log sum exp S.
+ *   O [T, n_heads d], lse [n_heads, T] fp32 (for the backward).
+ * tp_attn_core_backward: dQKV [T, (n_heads + 2 n_kv_heads) d] from dO [T, n_heads d],
+ *   the forward's QKV, O and lse; K's and V's gradients are sums over the heads
+ *   of their group. dQKV is what tp_attn_qkv_backward takes.
+ * Rows that belong to no sequence (before the first, behind the last) are not
+ * read as keys; their O, lse and dQKV are zeros.
+ * bf16: products on the tensor cores with fp32 sums; P and dS are rounded to bf16
+ * as their operands. fp32: products and sums in fp32 (no tf32). Softmax
+ * statistics are fp32. What a query does not see does not reach it, infinities
+ * and NaN included. Results are deterministic.
+ * Offsets that fall or lie outside [0, T] are read as the nearest that do not,
+ * and record TPCE_ERR_INVALID in the device status word.
+ * Shapes: n_heads a multiple of n_kv_heads, up to 4096; d a multiple of 8 up to
+ * 128; T up to 2^30, T n_heads up to 2^33, (T / 64 + sequences + 2) n_heads below
+ * 2^31; scale finite;
+ * window and sinks not negative. What is written overlaps nothing else
+ * (TPCE_ERR_INVALID). T == 0 is a no-op.
+ * Workspace: tpce_attn_core_workspace_bytes for the backward.
+ * ------------------------------------------------------------------------- */
+size_t tpce_attn_core_workspace_bytes(int64_t T, int64_t n_heads);
+tpce_status tp_attn_core_forward(const void *QKV, const int32_t *offsets, int sequences, int64_t T,
+                                 int64_t n_heads, int64_t n_kv_heads, int64_t head_dim,
+                                 int64_t window, int64_t sinks, float scale, int dtype, void *O,
+                                 float *lse, void *stream);
+tpce_status tp_attn_core_backward(const void *dO, const void *QKV, const void *O, const float *lse,
+                                  const int32_t *offsets, int sequences, int64_t T, int64_t n_heads,
+                                  int64_t n_kv_heads, int64_t head_dim, int64_t window,
+                                  int64_t sinks, float scale, int dtype, void *dQKV, void *ws,
+                                  size_t ws_bytes, void *stream);
 
 /* Sequence-parallel forms of the attention projections: the QKV projection
  * is the column-parallel entry (X and dX as chunks), the output projection

@@ -92,6 +92,10 @@ SIGNATURES = {
     "tpce_embedding_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
     "tp_embedding_forward": (_I, [_P, _P, _I64, _I64, _I64, _I64, _F, _I, _P, _P]),
     "tp_embedding_backward": (_I, [_P, _P, _I64, _I64, _I64, _I64, _F, _I, _I, _P, _P, _SZ, _P]),
+    "tpce_attn_core_workspace_bytes": (_SZ, [_I64, _I64]),
+    "tp_attn_core_forward": (_I, [_P, _P, _I, _I64, _I64, _I64, _I64, _I64, _I64, _F, _I, _P, _P, _P]),
+    "tp_attn_core_backward": (_I, [_P, _P, _P, _P, _P, _I, _I64, _I64, _I64, _I64, _I64, _I64, _F, _I, _P, _P, _SZ,
+                                   _P]),
     "tp_adamw_step": (_I, [ctypes.POINTER(AdamwTensor), _I, _D, _D, _D, _D, _I64, _D, _P, _P]),
     "tpce_device_status": (_I, [_P, _I, ctypes.POINTER(ctypes.c_uint32)]),
     "tpce_debug_withhold_next_load": (_I, [_I]),

@@ -24,7 +24,7 @@ LIB_DIR = os.path.join(PKG, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libtpce.so")
 
 SOURCES = ["runtime.cu", "mlp.cu", "linear.cu", "ce.cu", "ce_static.cu", "step/norm.cu", "step/experts.cu",
-           "step/adamw.cu", "step/embed.cu"]
+           "step/adamw.cu", "step/embed.cu", "attn/forward.cu", "attn/backward.cu"]
 BINDING_SOURCE = os.path.join(CSRC, "step", "binding.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",

@@ -1,0 +1,296 @@
+// attn.cuh -- what the attention core's kernels share: the call's shape, which
+// sequence and tile a block has, which keys a query sees, and the tiles that are
+// computed without tensor cores.
+//
+// Queries and keys of one sequence are numbered from 0. Query i sees key j when
+//   j <= i  and  (window == 0  or  i - j < window  or  j < sinks).
+// With S = scale Q K^T over the visible keys, P = softmax(S), O = P V and
+// lse = log sum exp S (natural logarithm). Backward, from dO:
+//   delta_i = sum_c dO_ic O_ic,  dP = dO V^T,  dS = P (dP - delta),
+//   dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO,
+// the last two summed over the query heads that share the key/value head.
+// P is formed as 2^(S log2(e) - m), one product and one exponential of base two.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "host.h"
+#include "ptx.cuh"
+#include "step/launch.cuh"
+#include "step/vec.cuh"
+
+namespace tpce {
+namespace attn {
+
+using step::grid_begin;
+using step::load8;
+using step::pack8;
+using step::Raw8;
+using step::store8;
+using step::unpack8;
+using step::zero8;
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kMaxDim = 128;
+
+// The fused rows: for each key/value head its group's query heads, then K, then V.
+struct Shape {
+    int64_t T;
+    int n_q, n_kv, group, d;
+    int64_t ld;              // (n_q + 2 n_kv) d
+    const int32_t *offsets;  // [sequences + 1] or NULL: one sequence of T tokens
+    int sequences;
+    int window, sinks;
+    float scale;
+    uint32_t *err;
+
+    __device__ __forceinline__ int q_head(int h) const { return h / group * (group + 2) + h % group; }
+    __device__ __forceinline__ int k_head(int kv) const { return kv * (group + 2) + group; }
+    __device__ __forceinline__ int v_head(int kv) const { return kv * (group + 2) + group + 1; }
+};
+
+__device__ __forceinline__ bool sees(const Shape &s, int i, int j) {
+    return j <= i && (s.window == 0 || i - j < s.window || j < s.sinks);
+}
+
+// ------------------------------------------------------------------ which tile
+// Of a sequence: its first row among the T, its length, the tile of it. n == 0: the
+// block has no tile; it may zero the rows that belong to no sequence.
+struct Tile {
+    int64_t row0;
+    int n, tile, tiles;
+    int64_t head_rows, tail_row;  // rows before the first sequence, and the first one after the last
+    int part, parts;              // of the blocks without a tile
+};
+
+// Every lane of a warp calls it. `x` counts tiles of `rows` rows over all sequences;
+// the grid has grid_tiles of them for each head, more than there are tiles. Offsets
+// that fall, or lie outside, are read as the nearest that do not.
+__device__ __forceinline__ Tile find_tile(const Shape &s, int x, int rows, int grid_tiles) {
+    Tile t{};
+    if (!s.offsets) {
+        const int tiles = static_cast<int>((s.T + rows - 1) / rows);
+        if (x < tiles) {
+            t.n = static_cast<int>(s.T);
+            t.tile = x;
+            t.tiles = tiles;
+            return t;
+        }
+        t.tail_row = s.T;
+        t.part = x - tiles;
+        t.parts = grid_tiles - tiles;
+        return t;
+    }
+    const int lane = threadIdx.x & 31;
+    const int T = static_cast<int>(s.T);
+    int first = s.offsets[0];
+    if (first < 0 || first > T) {
+        if (lane == 0) ptx::record_error(s.err, kErrInvalid | (6u << 8));
+        first = first < 0 ? 0 : T;
+    }
+    int end = first, before = 0;  // of the sequences so far: the last row, the tiles
+    for (int b0 = 0; b0 < s.sequences; b0 += 32) {
+        const int given = b0 + lane < s.sequences ? s.offsets[b0 + lane + 1] : end;
+        int e = max(end, min(given, T));
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, e, d);
+            if (lane >= d) e = max(e, o);
+        }
+        const int up = __shfl_up_sync(0xffffffffu, e, 1);
+        const int begin = lane == 0 ? end : up;
+        if (b0 + lane < s.sequences && given != e) ptx::record_error(s.err, kErrInvalid | (6u << 8));
+        const int tiles = (e - begin + rows - 1) / rows;
+        int sum = tiles;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, sum, d);
+            if (lane >= d) sum += o;
+        }
+        const int at = x - before - (sum - tiles);
+        const uint32_t found = __ballot_sync(0xffffffffu, at >= 0 && at < tiles);
+        if (found) {
+            const int who = __ffs(found) - 1;
+            t.row0 = __shfl_sync(0xffffffffu, begin, who);
+            t.n = __shfl_sync(0xffffffffu, e - begin, who);
+            t.tile = __shfl_sync(0xffffffffu, at, who);
+            t.tiles = __shfl_sync(0xffffffffu, tiles, who);
+            return t;
+        }
+        end = __shfl_sync(0xffffffffu, e, 31);
+        before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    t.head_rows = first;
+    t.tail_row = end;
+    t.part = x - before;
+    t.parts = grid_tiles - before;
+    return t;
+}
+
+// Tiles in a grid for each head: all sequences' tiles and one more at least.
+inline int64_t grid_tiles(const Shape &s, int rows) { return s.T / rows + (s.offsets ? s.sequences : 1) + 1; }
+
+// The columns c0 .. c0 + d of the rows that belong to no sequence become zeros.
+template <typename T>
+__device__ __forceinline__ void zero_rest(const Shape &s, const Tile &t, T *out, int64_t ld, int64_t c0) {
+    Raw8<T> zero;
+    zero8(zero);
+    const int vectors = s.d / 8;
+    const int64_t rows = t.head_rows + (s.T - t.tail_row);
+    for (int64_t i = static_cast<int64_t>(t.part) * blockDim.x + threadIdx.x; i < rows * vectors;
+         i += static_cast<int64_t>(t.parts) * blockDim.x) {
+        const int64_t r = i / vectors;
+        store8(out + (r < t.head_rows ? r : t.tail_row + r - t.head_rows) * ld + c0 + (i - r * vectors) * 8, zero);
+    }
+}
+
+// ------------------------------------------------------------------ key tiles of queries, query tiles of keys
+// The tiles of `rows` keys that queries q0 .. q1 - 1 see: 0 .. first - 1 (sinks), then from .. last.
+struct KeyTiles {
+    int first, from, last;
+    __device__ __forceinline__ int count() const { return first + last - from + 1; }
+    __device__ __forceinline__ int at(int u) const { return u < first ? u : from + u - first; }
+};
+__device__ __forceinline__ KeyTiles key_tiles(const Shape &s, int q0, int q1, int rows) {
+    KeyTiles k{};
+    const int lo = s.window && q0 >= s.window ? q0 - s.window + 1 : 0;
+    k.from = lo / rows;
+    k.last = (q1 - 1) / rows;
+    k.first = min((min(s.sinks, lo) + rows - 1) / rows, k.from);
+    return k;
+}
+
+// The end (one past the last) of the queries that see any of the keys k0 .. k1 - 1 of n.
+__device__ __forceinline__ int query_end(const Shape &s, int k0, int k1, int n) {
+    if (s.window == 0 || k0 < s.sinks) return n;
+    return static_cast<int>(min(static_cast<int64_t>(n), static_cast<int64_t>(k1) - 1 + s.window));
+}
+
+// Whether every query q0 .. q1 - 1 sees every key k0 .. k1 - 1.
+__device__ __forceinline__ bool all_seen(const Shape &s, int q0, int q1, int k0, int k1) {
+    return k1 - 1 <= q0 && (s.window == 0 || q1 - 1 - k0 < s.window || k1 <= s.sinks);
+}
+
+// ------------------------------------------------------------------ tiles without tensor cores
+// 64 queries by 64 keys on 256 threads, all in fp32: the path of fp32 tensors, whose
+// products would lose 13 bits as tf32, and of tiles in which something was infinite
+// or NaN (a tensor core multiplies what is masked by zero, and 0 inf is NaN: here a
+// masked factor is passed over). Thread (ty, tx) of 16 x 16 has the rows 4 ty .. and
+// the columns tx + 16 j of a 64 x 64 product, and the columns 4 tx + 64 m of a row of d.
+constexpr int kRows = 64, kPlainThreads = 256;
+constexpr int kPitchP = kRows + 4;
+
+struct PlainSmem {
+    int pitch;  // of a row of d values: 16-byte aligned, a row's start four banks after the one before
+    __host__ __device__ explicit PlainSmem(int d) : pitch(d + 4 + (d % 32 == 0 ? 0 : (32 - d % 32) % 32)) {}
+    __host__ __device__ size_t rows() const { return static_cast<size_t>(kRows) * pitch; }
+    __host__ __device__ size_t forward() const { return 4 * (3 * rows() + kRows * kPitchP); }
+    __host__ __device__ size_t backward() const { return 4 * (4 * rows() + 2 * kRows * kPitchP); }
+};
+
+// the threads that compute a tile, which may be some of a larger block's
+__device__ __forceinline__ void plain_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// Rows r0 .. of a tile (zeros from row n on) into shared memory.
+template <typename T>
+__device__ __forceinline__ void plain_load(float *to, int pitch, const T *from, int64_t ld, int r0, int n, int d) {
+    const int vectors = d / 8;
+    for (int i = threadIdx.x; i < kRows * vectors; i += kPlainThreads) {
+        const int r = i / vectors, c = i - r * vectors;
+        float v[8] = {};
+        if (r0 + r < n) unpack8(load8(from + (r0 + r) * ld + c * 8), v);
+        float4 *p = reinterpret_cast<float4 *>(to + r * pitch + c * 8);
+        p[0] = make_float4(v[0], v[1], v[2], v[3]);
+        p[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+}
+
+// s[i][j] = sum_c A[4 ty + i][c] B[tx + 16 j][c]
+__device__ __forceinline__ void plain_dots(const float *A, const float *B, int pitch, int d, float (&s)[4][4]) {
+    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[i][j] = 0.0f;
+#pragma unroll 2
+    for (int c = 0; c < d; c += 4) {
+        float4 a[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4 *>(A + (4 * ty + i) * pitch + c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4 *>(B + (tx + 16 * j) * pitch + c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
+                s[i][j] = fmaf(a[i].y, b[j].y, s[i][j]);
+                s[i][j] = fmaf(a[i].z, b[j].z, s[i][j]);
+                s[i][j] = fmaf(a[i].w, b[j].w, s[i][j]);
+            }
+    }
+}
+
+// o[i][m] += sum_k P[4 ty + i][k] X[k][4 tx + 64 m ..]  (ROWS: P[k][4 ty + i]); a zero factor
+// of a masked tile is passed over, whatever it would multiply.
+template <bool MASKED, bool ROWS>
+__device__ __forceinline__ void plain_add(const float *P, const float *X, int pitch, int d, float (&o)[4][2][4]) {
+    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+#pragma unroll 2
+    for (int k = 0; k < kRows; k += 4) {
+        float4 p[4];  // four rows (or columns) of P, four k each
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            p[i] = *reinterpret_cast<const float4 *>(ROWS ? P + (k + i) * kPitchP + 4 * ty : P + (4 * ty + i) * kPitchP + k);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            const int c = 4 * tx + 64 * m;
+            if (c >= d) continue;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float4 x = *reinterpret_cast<const float4 *>(X + (k + q) * pitch + c);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 f4 = ROWS ? p[q] : p[i];
+                    const int at = ROWS ? i : q;
+                    const float f = at == 0 ? f4.x : at == 1 ? f4.y : at == 2 ? f4.z : f4.w;
+                    if (MASKED && f == 0.0f) continue;
+                    o[i][m][0] = fmaf(f, x.x, o[i][m][0]);
+                    o[i][m][1] = fmaf(f, x.y, o[i][m][1]);
+                    o[i][m][2] = fmaf(f, x.z, o[i][m][2]);
+                    o[i][m][3] = fmaf(f, x.w, o[i][m][3]);
+                }
+            }
+        }
+    }
+}
+
+// Four adjacent values in the tensors' type.
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, const float (&v)[4]) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+    *reinterpret_cast<uint2 *>(p) =
+        make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+}
+__device__ __forceinline__ void store4(float *p, const float (&v)[4]) {
+    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+
+__device__ __forceinline__ float max16(float x) {
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+    return x;
+}
+__device__ __forceinline__ float sum16(float x) {
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    return x;
+}
+
+}  // namespace attn
+}  // namespace tpce

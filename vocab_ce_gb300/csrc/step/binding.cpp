@@ -17,6 +17,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 #include <string>
 #include <utility>
@@ -43,6 +44,9 @@ struct Api {
     decltype(&tpce_embedding_workspace_bytes) embedding_workspace_bytes;
     decltype(&tp_embedding_forward) embedding_forward;
     decltype(&tp_embedding_backward) embedding_backward;
+    decltype(&tpce_attn_core_workspace_bytes) attn_core_workspace_bytes;
+    decltype(&tp_attn_core_forward) attn_core_forward;
+    decltype(&tp_attn_core_backward) attn_core_backward;
 };
 Api api;
 PyObject *check_status;   // Python's check(status, name): raises for a failure
@@ -176,6 +180,7 @@ PyObject *entry(PyObject *out, const Key &key) {
 struct Keys {
     Key S{"S"}, Y{"Y"}, rstd{"rstd"}, Q{"Q"}, Q_scale{"Q_scale"}, dX{"dX"}, dw{"dw"};
     Key row{"row"}, source{"source"}, offsets{"offsets"}, dYs{"dYs"}, dweights{"dweights"};
+    Key O{"O"}, lse{"lse"};
     Key m{"m"}, v{"v"}, m_q{"m_q"}, r_q{"r_q"}, m_scale{"m_scale"}, r_scale{"r_scale"};
 };
 const Keys *keys;
@@ -435,6 +440,67 @@ PyObject *embedding_backward(PyObject *const *a) {
     return THPVariable_Wrap(dE.x);
 }
 
+// ------------------------------------------------------------------ attention core
+// QKV, n_heads, n_kv_heads, offsets, window, sinks, scale: what both directions take first
+struct Heads {
+    const at::Tensor &QKV;
+    int dt;
+    int64_t T, n, n_kv, d, window, sinks;
+    at::Tensor offsets;
+    int sequences = 0;
+    float scale;
+    Heads(const at::Tensor &x, PyObject *const *a)
+        : QKV(x), dt(matrix(x, "QKV")), T(x.size(0)), n(integer(a[0])), n_kv(integer(a[1])), window(integer(a[3])),
+          sinks(integer(a[4])) {
+        if (n < 1 || n_kv < 1 || n > (1 << 20) || n_kv > (1 << 20) || n % n_kv != 0)
+            throw Refused{"n_heads must be a multiple of n_kv_heads"};
+        if (x.size(1) % (n + 2 * n_kv) != 0)
+            throw Refused{"QKV must have (n_heads + 2 n_kv_heads) columns of equal width, got shape " +
+                          shape_text(x.sizes())};
+        d = x.size(1) / (n + 2 * n_kv);
+        if (!none(a[2])) {
+            offsets = tensor(a[2], "offsets");
+            if (offsets.dim() != 1 || offsets.size(0) < 2 || offsets.size(0) > (1 << 30))
+                throw Refused{"offsets must hold sequences + 1 values"};
+            need(offsets, "offsets", at::kInt, offsets.sizes());
+            sequences = static_cast<int>(offsets.size(0) - 1);
+        }
+        scale = none(a[5]) ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(d))) : static_cast<float>(number(a[5]));
+    }
+};
+
+// QKV, n_heads, n_kv_heads, offsets, window, sinks, scale, out
+PyObject *attn_core_forward(PyObject *const *a) {
+    const Heads s(tensor(a[0], "QKV"), a + 1);
+    Results res;
+    const Output O = output(entry(a[7], keys->O), "O", {s.T, s.n * s.d}, s.QKV.scalar_type(), s.QKV);
+    res.add(keys->O, O);
+    const Output lse = output(entry(a[7], keys->lse), "lse", {s.n, s.T}, at::kFloat, s.QKV);
+    res.add(keys->lse, lse);
+    raise_on(api.attn_core_forward(ptr(s.QKV), iptr(s.offsets), s.sequences, s.T, s.n, s.n_kv, s.d, s.window, s.sinks,
+                                   s.scale, s.dt, ptr(O), fptr(lse), stream()),
+             "tp_attn_core_forward");
+    written(O, lse);
+    return res.take();
+}
+
+// dO, QKV, O, lse, n_heads, n_kv_heads, offsets, window, sinks, scale, out, ws
+PyObject *attn_core_backward(PyObject *const *a) {
+    const at::Tensor &dO = tensor(a[0], "dO"), &O = tensor(a[2], "O"), &lse = tensor(a[3], "lse");
+    const Heads s(tensor(a[1], "QKV"), a + 4);
+    need(dO, "dO", s.QKV.scalar_type(), {s.T, s.n * s.d});
+    need(O, "O", s.QKV.scalar_type(), {s.T, s.n * s.d});
+    need(lse, "lse", at::kFloat, {s.n, s.T});
+    const Output dQKV = output(a[10], "dQKV", s.QKV.sizes(), s.QKV.scalar_type(), s.QKV);
+    const at::Tensor ws = workspace(a[11], api.attn_core_workspace_bytes(s.T, s.n), s.QKV);
+    raise_on(api.attn_core_backward(ptr(dO), ptr(s.QKV), ptr(O), fptr(lse), iptr(s.offsets), s.sequences, s.T, s.n,
+                                    s.n_kv, s.d, s.window, s.sinks, s.scale, s.dt, ptr(dQKV), ptr(ws), bytes_of(ws),
+                                    stream()),
+             "tp_attn_core_backward");
+    written(dQKV);
+    return THPVariable_Wrap(dQKV.x);
+}
+
 // ------------------------------------------------------------------ AdamW
 // A list's entries, held while they are used.
 struct Items {
@@ -604,6 +670,8 @@ PyMethodDef methods[] = {
     STEP_CALL(adamw_step, 13),
     STEP_CALL(embedding_forward, 5),
     STEP_CALL(embedding_backward, 8),
+    STEP_CALL(attn_core_forward, 8),
+    STEP_CALL(attn_core_backward, 12),
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_step_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

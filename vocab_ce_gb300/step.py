@@ -32,7 +32,8 @@ GROUP = 128  # values that share one scale in the 8-bit formats
 _ENTRIES = ("tpce_rmsnorm_workspace_bytes", "tp_rmsnorm_forward", "tp_rmsnorm_backward",
             "tpce_expert_plan_workspace_bytes", "tp_expert_plan", "tp_expert_dispatch_forward",
             "tp_expert_dispatch_backward", "tp_expert_combine_forward", "tp_expert_combine_backward", "tp_adamw_step",
-            "tpce_embedding_workspace_bytes", "tp_embedding_forward", "tp_embedding_backward")
+            "tpce_embedding_workspace_bytes", "tp_embedding_forward", "tp_embedding_backward",
+            "tpce_attn_core_workspace_bytes", "tp_attn_core_forward", "tp_attn_core_backward")
 _lock = threading.Lock()
 _binding = None
 
@@ -188,6 +189,38 @@ def tp_embedding_backward(dX: torch.Tensor, ids: torch.Tensor, v_pad: int, v_val
         with _on(stream, dX, ids, out, ws):
             return _b().embedding_backward(dX, ids, v_pad, v_valid, scale, out, accumulate, ws)
     return _b().embedding_backward(dX, ids, v_pad, v_valid, scale, out, accumulate, ws)
+
+
+# ---------------------------------------------------------------------- attention core
+def attn_core_workspace_bytes(T: int, n_heads: int) -> int:
+    return int(lib().tpce_attn_core_workspace_bytes(T, n_heads))
+
+
+def tp_attn_core_forward(QKV: torch.Tensor, n_heads: int, n_kv_heads: int, offsets: Optional[torch.Tensor] = None,
+                         window: int = 0, sinks: int = 0, scale: Optional[float] = None,
+                         out: Optional[Dict[str, torch.Tensor]] = None, stream=None) -> Dict[str, torch.Tensor]:
+    """Causal attention on the fused rows of ``tp_attn_qkv_forward``: O [T, n_heads d]
+    and lse [n_heads, T]. offsets [sequences + 1] (int32): sequence b is the rows
+    offsets[b] .. offsets[b + 1] (default: one of all rows); rows of none give
+    zeros. With a window, a query sees the last ``window`` keys up to its own and
+    the first ``sinks`` of its sequence; window 0: all up to its own. scale
+    (default 1 / sqrt(d)) multiplies the scores."""
+    if stream is not None:
+        with _on(stream, QKV, offsets, out):
+            return _b().attn_core_forward(QKV, n_heads, n_kv_heads, offsets, window, sinks, scale, out)
+    return _b().attn_core_forward(QKV, n_heads, n_kv_heads, offsets, window, sinks, scale, out)
+
+
+def tp_attn_core_backward(dO: torch.Tensor, QKV: torch.Tensor, O: torch.Tensor, lse: torch.Tensor, n_heads: int,
+                          n_kv_heads: int, offsets: Optional[torch.Tensor] = None, window: int = 0, sinks: int = 0,
+                          scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                          ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """dQKV, in QKV's columns: what ``tp_attn_qkv_backward`` takes. QKV, O and lse
+    are the forward's, the other arguments the same as there."""
+    if stream is not None:
+        with _on(stream, dO, QKV, O, lse, offsets, out, ws):
+            return _b().attn_core_backward(dO, QKV, O, lse, n_heads, n_kv_heads, offsets, window, sinks, scale, out, ws)
+    return _b().attn_core_backward(dO, QKV, O, lse, n_heads, n_kv_heads, offsets, window, sinks, scale, out, ws)
 
 
 # ---------------------------------------------------------------------- AdamW
