@@ -1,0 +1,88 @@
+// tc.cuh -- what the attention kernels on the tensor cores share: 128 x 128 tiles in
+// shared memory as TMA leaves them, their descriptors, and the products.
+//
+// A tile of 128 rows of one head is one or two blocks of 64 columns, a block 128 rows
+// of 128 bytes with the 128-byte swizzle. The same tile serves as an operand by rows
+// (K-major: a sum over the head's d columns) and by columns (MN-major: a sum over the
+// tile's rows). Columns past d are zeros.
+#pragma once
+
+#include "attn/attn.cuh"
+#include "attn/host.cuh"
+
+namespace tpce {
+namespace attn {
+
+constexpr int kTile = 128;
+constexpr uint32_t kBlockBytes = kTile * 128, kTileBytes = 2 * kBlockBytes;
+constexpr uint32_t kTmemCols = 512;
+
+__device__ __forceinline__ uint64_t desc_rows(uint32_t tile) { return ptx::sdesc_sw128(tile, 16, 1024); }
+__device__ __forceinline__ uint64_t desc_cols(uint32_t tile) { return ptx::sdesc_sw128(tile, kBlockBytes, 1024); }
+// sixteen of the summed index further
+__device__ __forceinline__ uint64_t step_rows(uint64_t desc, int k) {
+    return desc + static_cast<uint32_t>(((k >> 2) * kBlockBytes + (k & 3) * 32) >> 4);
+}
+__device__ __forceinline__ uint64_t step_cols(uint64_t desc, int k) {
+    return desc + static_cast<uint32_t>((k * 16 * 128) >> 4);
+}
+
+// D = A B^T over d: 128 x 128 scores of two tiles' rows.
+__device__ __forceinline__ void mma_scores(uint32_t d_tmem, uint32_t a_tile, uint32_t b_tile, int d) {
+    constexpr uint32_t kIdesc = ptx::idesc_f32acc(kTile, kTile, 1, false, false);
+    const uint64_t a = desc_rows(a_tile), b = desc_rows(b_tile);
+    const int steps = (d + 15) / 16;
+    for (int k = 0; k < steps; ++k) ptx::mma_bf16(d_tmem, step_rows(a, k), step_rows(b, k), kIdesc, k != 0);
+}
+
+// D (+)= A X: A (bf16 in tensor memory, from a_tmem on, its second 64 columns of K
+// second_half further) times a tile's 128 rows of d columns.
+__device__ __forceinline__ void mma_weighted(uint32_t d_tmem, uint32_t a_tmem, uint32_t second_half, uint32_t x_tile,
+                                             uint32_t idesc, bool accumulate) {
+    const uint64_t x = desc_cols(x_tile);
+#pragma unroll
+    for (int k = 0; k < kTile / 16; ++k)
+        ptx::mma_bf16_ts(d_tmem, a_tmem + (k & 3) * 8 + (k >> 2) * second_half, step_cols(x, k), idesc,
+                         (accumulate || k) ? 1u : 0u);
+}
+// the width of such a product: d, rounded up to what the instruction takes
+__host__ __device__ inline int width16(int d) { return (d + 15) / 16 * 16; }
+__device__ __forceinline__ uint32_t idesc_weighted(int d) {
+    return ptx::idesc_f32acc(kTile, 16, 1, false, true) +
+           (static_cast<uint32_t>((width16(d) - 16) >> 3) << 17);
+}
+
+// (x, y) = (x, y) * f + (a, a); 2^x to 2 units in the last place, results below 2^-126 zero
+__device__ __forceinline__ void scale2(float &x, float &y, float f, float a) {
+    asm("{\n\t.reg .b64 p, q, r;\n\t"
+        "mov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %2};\n\tmov.b64 r, {%3, %3};\n\t"
+        "fma.rn.f32x2 p, p, q, r;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(f), "f"(a));
+}
+__device__ __forceinline__ void add2(float &x, float &y, float a, float b) {
+    asm("{\n\t.reg .b64 p, q;\n\t"
+        "mov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
+        "add.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(a), "f"(b));
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// The blocks of one head's tile of rows, into one stage.
+__device__ __forceinline__ void load_tile(uint8_t *to, const CUtensorMap *m, uint64_t *bar, int head, int64_t row,
+                                          int blocks) {
+    for (int b = 0; b < blocks; ++b)
+        ptx::tma_load_3d(to + b * kBlockBytes, m, bar, b * 64, head, static_cast<int>(row));
+}
+
+}  // namespace attn
+}  // namespace tpce

@@ -44,6 +44,12 @@ class KernelTimer {
 bool make_tmap(CUtensorMap *m, int dt, const void *base, uint64_t inner, uint64_t outer, uint64_t ld,
                uint32_t box_inner, uint32_t box_outer, int swizzle = 128);
 
+// Map of `heads` heads of `d` bf16 each in a row of pitch `ld`, `rows` rows: boxes of
+// 64 columns of one head and box_rows rows, zeros past the head's and the tensor's end,
+// 128-byte swizzle.
+bool make_tmap_heads(CUtensorMap *m, const void *base, uint64_t d, uint64_t heads, uint64_t rows, uint64_t ld,
+                     uint32_t box_rows);
+
 // fp32 -> bf16, n elements (n % 8 == 0, 16-byte aligned)
 tpce_status f32_to_bf16(const float *in, void *out, int64_t n, cudaStream_t s);
 

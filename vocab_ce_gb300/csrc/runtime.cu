@@ -127,6 +127,20 @@ bool make_tmap(CUtensorMap *m, int dt, const void *base, uint64_t inner, uint64_
     return r == CUDA_SUCCESS;
 }
 
+bool make_tmap_heads(CUtensorMap *m, const void *base, uint64_t d, uint64_t heads, uint64_t rows, uint64_t ld,
+                     uint32_t box_rows) {
+    auto fn = encode_fn();
+    if (!fn || d == 0 || d % 8 != 0 || ld % 8 != 0 || rows == 0 || !aligned16(base)) return false;
+    cuuint64_t dims[3] = {d, heads, rows};
+    cuuint64_t strides[2] = {d * 2, ld * 2};
+    cuuint32_t box[3] = {64, 1, box_rows};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 // ------------------------------------------------------------------ profiling
 namespace {
 struct Rec {
