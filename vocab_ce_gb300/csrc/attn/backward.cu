@@ -7,6 +7,7 @@
 // or tensor memory: nothing is added by atomics and results are the same every time.
 #include "attn/attn.cuh"
 #include "attn/host.cuh"
+#include "attn/tc.cuh"
 
 namespace tpce {
 namespace {
@@ -92,7 +93,7 @@ __device__ __forceinline__ void plain_store(const Shape &s, const float (&o)[4][
 
 // dQ of queries q0 .. q0 + 63 of one head.
 template <typename T>
-__device__ __noinline__ void plain_dq_tile(const Shape &s, const T *QKV, const T *dO, const float2 *stats,
+__device__ __forceinline__ void plain_dq_tile(const Shape &s, const T *QKV, const T *dO, const float2 *stats,
                                            int64_t row0, int n, int q0, int h, T *dQKV, float *smem) {
     const PlainSmem lay(s.d);
     float *Q = smem, *K = Q + lay.rows(), *V = K + lay.rows(), *G = V + lay.rows(), *dS = G + lay.rows();
@@ -124,7 +125,7 @@ __device__ __noinline__ void plain_dq_tile(const Shape &s, const T *QKV, const T
 
 // dK and dV of keys k0 .. k0 + 63 of one key/value head.
 template <typename T>
-__device__ __noinline__ void plain_dkv_tile(const Shape &s, const T *QKV, const T *dO, const float2 *stats,
+__device__ __forceinline__ void plain_dkv_tile(const Shape &s, const T *QKV, const T *dO, const float2 *stats,
                                             int64_t row0, int n, int k0, int kv, T *dQKV, float *smem) {
     const PlainSmem lay(s.d);
     float *Q = smem, *K = Q + lay.rows(), *V = K + lay.rows(), *G = V + lay.rows(), *P = G + lay.rows(),
@@ -193,7 +194,575 @@ __global__ void __launch_bounds__(kPlainThreads)
     plain_dkv_tile(s, QKV, dO, stats, t.row0, t.n, t.tile * kRows, kv, dQKV, reinterpret_cast<float *>(smem4));
 }
 
+// ------------------------------------------------------------------ tiles on the tensor cores
+// Twelve warps: 0 - 7 compute, a thread one row of a 128 x 128 tile and half of its
+// columns (warps 4 - 7 the second half); warp 8 loads; warp 9 issues the products;
+// warp 10 fetches the queries' statistics where they go by columns; the last one only
+// lends its registers. Products run in the order in which they are issued, which is
+// what keeps a buffer of tensor memory from being written while one before reads it.
+constexpr int kBwdThreads = 384, kBwdRing = 5;
+// the two tiles that stay, the ring, statistics of two tiles, barriers
+constexpr uint32_t kBwdSmem = 2 * kTileBytes + kBwdRing * kTileBytes + 2 * kTile * 8 + 256;
+static_assert(kBwdSmem <= static_cast<uint32_t>(kMaxSmem), "the ring fits");
+
+// A ring of tiles as one warp fills and another uses it: positions count on, each is a
+// slot and the parity of its round.
+struct Ring {
+    uint8_t *at;
+    uint64_t *full, *empty;
+    __device__ __forceinline__ static int slot(int pos) { return pos % kBwdRing; }
+    __device__ __forceinline__ static uint32_t parity(int pos) { return static_cast<uint32_t>(pos / kBwdRing) & 1u; }
+};
+
+struct BwdSmem {
+    uint8_t *tiles;  // the two that stay
+    Ring ring;
+    float *stats;  // [2][2][kTile]
+    uint64_t *stay, *scores, *dots, *p_ready, *ds_ready, *stats_full, *stats_empty, *done, *drain;
+    uint32_t *tmem_slot;
+    volatile int *abort_flag, *odd;
+    __device__ __forceinline__ explicit BwdSmem(uint8_t *raw) {
+        tiles = raw;  // 1024-byte aligned, as the swizzle needs it
+        ring.at = tiles + 2 * kTileBytes;
+        stats = reinterpret_cast<float *>(ring.at + kBwdRing * kTileBytes);
+        uint64_t *b = reinterpret_cast<uint64_t *>(stats + 4 * kTile);
+        ring.full = b;
+        ring.empty = b + kBwdRing;
+        b += 2 * kBwdRing;
+        stay = b;
+        scores = b + 1;      // [2]
+        dots = b + 3;
+        p_ready = b + 4;
+        ds_ready = b + 5;
+        stats_full = b + 6;  // [2]
+        stats_empty = b + 8;  // [2]
+        done = b + 10;
+        drain = b + 11;
+        tmem_slot = reinterpret_cast<uint32_t *>(b + 12);
+        abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+        odd = abort_flag + 1;
+    }
+    __device__ __forceinline__ void init() const {
+        for (int i = 0; i < kBwdRing; ++i) {
+            ptx::mbar_init(&ring.full[i], 1);
+            ptx::mbar_init(&ring.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&scores[i], 1);
+            ptx::mbar_init(&stats_full[i], 32);
+            ptx::mbar_init(&stats_empty[i], 8);
+        }
+        ptx::mbar_init(stay, 1);
+        ptx::mbar_init(dots, 1);
+        ptx::mbar_init(p_ready, 8);
+        ptx::mbar_init(ds_ready, 8);
+        ptx::mbar_init(done, 1);
+        ptx::mbar_init(drain, 1);
+        *abort_flag = 0;
+        *odd = 0;
+        ptx::fence_mbar_init();
+    }
+};
+
+// Loads one tile into the next place of the ring; false when a wait gave up.
+__device__ __forceinline__ bool ring_load(const BwdSmem &m, int pos, const CUtensorMap *map, int head, int64_t row,
+                                          int blocks, uint32_t *err) {
+    const int slot = Ring::slot(pos);
+    if (!ptx::mbar_wait(&m.ring.empty[slot], Ring::parity(pos) ^ 1, m.abort_flag, err, 30)) return false;
+    ptx::mbar_arrive_expect_tx(&m.ring.full[slot], blocks * kBlockBytes);
+    load_tile(m.ring.at + slot * kTileBytes, map, &m.ring.full[slot], head, row, blocks);
+    return true;
+}
+// After a wait gave up: the loads of the positions before `pos` land.
+__device__ __forceinline__ void ring_drain(const BwdSmem &m, int pos) {
+    ptx::mbar_wait_drain(m.stay, 0);
+    for (int p = max(0, pos - kBwdRing); p < pos; ++p)
+        ptx::mbar_wait_drain(&m.ring.full[Ring::slot(p)], Ring::parity(p));
+}
+
+// 64 columns of this thread's row.
+__device__ __forceinline__ void read_half(uint32_t taddr, float (&x)[2][32]) {
+    ptx::tmem_ld32_async(taddr, x[0]);
+    ptx::tmem_ld32_async(taddr + 32, x[1]);
+    ptx::tmem_wait_ld();
+    ptx::tmem_ready(x[0]);
+    ptx::tmem_ready(x[1]);
+}
+
+// This thread's row of an accumulator, times f, from column c0 on (up to 64), to `to`; false if
+// something is not finite.
+__device__ __forceinline__ bool write_half(uint32_t taddr, float f, int c0, int d, __nv_bfloat16 *to, bool mine) {
+    float check = 0.0f;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        if (c0 + b * 32 >= d) break;
+        float o[32];
+        ptx::tmem_ld32_async(taddr + b * 32, o);
+        ptx::tmem_wait_ld();
+        ptx::tmem_ready(o);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const int c = c0 + b * 32 + v * 8;
+            if (c >= d) continue;
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                y[e] = o[v * 8 + e] * f;
+                check = fmaf(y[e], 0.0f, check);
+            }
+            Raw8<__nv_bfloat16> r;
+            pack8(y, r);
+            if (mine) store8(to + c, r);
+        }
+    }
+    return !mine || check == 0.0f;  // NaN is not 0
+}
+
+// dK and dV of 128 keys. Per tile of 128 queries of a head, with the keys as rows:
+//   S^T = K Q^T  ->  P^T = 2^(S^T c - lse)   ->  dV += P^T dO
+//   dP^T = V dO^T  ->  dS^T = P^T (dP^T - delta)  ->  dK += dS^T Q
+// Tensor memory: S^T, dP^T, dV, dK, 128 columns each; P^T and dS^T overwrite what they
+// are made of, in bf16, each half of the columns its own place. In the order
+//   S(0) dP(0) | dV(0) S(1) dK(0) dP(1) | dV(1) S(2) ..
+// two products are under way while the threads form P or dS.
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    tc_dkv_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap map_do, const Shape s,
+                  const __nv_bfloat16 *QKV, const __nv_bfloat16 *dO, const float2 *stats, int tiles,
+                  __nv_bfloat16 *dQKV) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const BwdSmem m(smem_raw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        m.init();
+        ptx::prefetch_tmap(&map);
+        ptx::prefetch_tmap(&map_do);
+    }
+    grid_begin();
+    const int kv = blockIdx.x % s.n_kv;
+    const Tile t = find_tile(s, blockIdx.x / s.n_kv, kTile, tiles);
+    if (t.n == 0) {
+        zero_rest(s, t, dQKV, s.ld, static_cast<int64_t>(s.k_head(kv)) * s.d);
+        zero_rest(s, t, dQKV, s.ld, static_cast<int64_t>(s.v_head(kv)) * s.d);
+        return;
+    }
+    // the first keys are seen by the most queries: they come first
+    const int k0 = t.tile * kTile;
+    const int end = query_end(s, k0, min(t.n, k0 + kTile), t.n);
+    const int of_head = (end - k0 + kTile - 1) / kTile, count = of_head * s.group;
+    if (warp == 9) {
+        ptx::tmem_alloc(m.tmem_slot, kTmemCols);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *m.tmem_slot, t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 384;
+    const int blocks = s.d > 64 ? 2 : 1;
+
+    if (warp == 8) {
+        if (lane == 0) {
+            ptx::mbar_arrive_expect_tx(m.stay, 2 * blocks * kBlockBytes);
+            load_tile(m.tiles, &map, m.stay, s.k_head(kv), t.row0 + k0, blocks);
+            load_tile(m.tiles + kTileBytes, &map, m.stay, s.v_head(kv), t.row0 + k0, blocks);
+            int pos = 0;
+            bool ok = true;
+            for (int g = 0; g < s.group && ok; ++g)
+                for (int q = 0; q < of_head && ok; ++q) {
+                    const int64_t row = t.row0 + k0 + q * kTile;
+                    const int h = kv * s.group + g;
+                    ok = ring_load(m, pos, &map, s.q_head(h), row, blocks, s.err);
+                    pos += ok;
+                    ok = ok && ring_load(m, pos, &map_do, h, row, blocks, s.err);
+                    pos += ok;
+                }
+            if (*m.abort_flag) ring_drain(m, pos);
+        }
+    } else if (warp == 9) {
+        if (lane == 0) {
+            const uint32_t idesc = idesc_weighted(s.d), base = ptx::smem_u32(m.ring.at), k_tile = ptx::smem_u32(m.tiles);
+            auto tile = [&](int pos) { return base + Ring::slot(pos) * kTileBytes; };
+            auto arrived = [&](int pos) {
+                return ptx::mbar_wait(&m.ring.full[Ring::slot(pos)], Ring::parity(pos), m.abort_flag, s.err, 31);
+            };
+            bool ok = ptx::mbar_wait(m.stay, 0, m.abort_flag, s.err, 32) && arrived(0);
+            if (ok) {
+                ptx::tc_fence_after();
+                mma_scores(t_s, k_tile, tile(0), s.d);
+                ptx::mma_commit(m.scores);
+                ok = arrived(1);
+            }
+            if (ok) {
+                mma_scores(t_dp, k_tile + kTileBytes, tile(1), s.d);
+                ptx::mma_commit(m.dots);
+            }
+            for (int it = 0; it < count && ok; ++it) {
+                const int q = 2 * it, o = q + 1;
+                const bool more = it + 1 < count;
+                ok = ptx::mbar_wait(m.p_ready, it & 1, m.abort_flag, s.err, 33);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                mma_weighted(t_dv, t_s, 64, tile(o), idesc, it > 0);
+                ptx::mma_commit(&m.ring.empty[Ring::slot(o)]);
+                if (more) {
+                    ok = arrived(q + 2);
+                    if (!ok) break;
+                    mma_scores(t_s, k_tile, tile(q + 2), s.d);
+                    ptx::mma_commit(m.scores);
+                }
+                ok = ptx::mbar_wait(m.ds_ready, it & 1, m.abort_flag, s.err, 34);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                mma_weighted(t_dk, t_dp, 64, tile(q), idesc, it > 0);
+                ptx::mma_commit(&m.ring.empty[Ring::slot(q)]);
+                if (more) {
+                    ok = arrived(o + 2);
+                    if (!ok) break;
+                    mma_scores(t_dp, k_tile + kTileBytes, tile(o + 2), s.d);
+                    ptx::mma_commit(m.dots);
+                }
+            }
+            if (ok) ptx::mma_commit(m.done);
+            ptx::mma_commit(m.drain);
+            ptx::mbar_wait_drain(m.drain, 0);
+        }
+    } else if (warp == 10) {
+        // the statistics of a tile, when the one two before has been used; queries past the end: P = 2^-inf
+        int it = 0;
+        bool ok = true;
+        for (int g = 0; g < s.group && ok; ++g) {
+            const float2 *from = stats + (kv * s.group + g) * s.T + t.row0;
+            for (int q = 0; q < of_head && ok; ++q, ++it) {
+                float2 v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int row = k0 + q * kTile + e * 32 + lane;
+                    v[e] = row < t.n ? from[row] : make_float2(INFINITY, 0.0f);
+                }
+                ok = ptx::mbar_wait(&m.stats_empty[it & 1], ((it >> 1) & 1) ^ 1, m.abort_flag, s.err, 35);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                float *to = m.stats + (it & 1) * 2 * kTile;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    to[e * 32 + lane] = v[e].x;
+                    to[kTile + e * 32 + lane] = v[e].y;
+                }
+                ptx::mbar_arrive(&m.stats_full[it & 1]);
+            }
+        }
+    } else if (warp < 8) {
+        const int half = warp >> 2, r = (warp & 3) * 32 + lane, key = k0 + r;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const float c = s.scale * kLog2e;
+        const int limit = s.window && key >= s.sinks ? min(t.n, key + s.window) : t.n;  // queries below it see the key
+        bool alive = true;
+        int q = 0;
+        for (int it = 0; it < count && alive; ++it) {
+            const int q0 = k0 + q * kTile;
+            q = q + 1 == of_head ? 0 : q + 1;
+            const bool masked = !all_seen(s, q0, q0 + kTile, k0, k0 + kTile) || q0 + kTile > t.n;
+            const int lo = key - q0 - half * 64, hi = limit - q0 - half * 64;
+            const float *lse = m.stats + (it & 1) * 2 * kTile + half * 64, *delta = lse + kTile;
+            bool ok = ptx::mbar_wait(&m.stats_full[it & 1], (it >> 1) & 1, m.abort_flag, s.err, 36) &&
+                      ptx::mbar_wait(m.scores, it & 1, m.abort_flag, s.err, 37);
+            if (!__all_sync(0xffffffffu, ok)) {
+                alive = false;
+                break;
+            }
+            ptx::tc_fence_after();
+            float x[2][32];
+            read_half(t_s + lanes + half * 64, x);
+            uint32_t p[32];
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    const float4 l4 = *reinterpret_cast<const float4 *>(lse + b * 32 + e);
+                    const float l[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+                    for (int f = 0; f < 4; ++f) {
+                        float &v = x[b][e + f];
+                        v = exp2_fast(fmaf(v, c, -l[f]));
+                        if (masked && (b * 32 + e + f < lo || b * 32 + e + f >= hi)) v = 0.0f;
+                    }
+                    p[(b * 32 + e) / 2] = pack2(x[b][e], x[b][e + 1]);
+                    p[(b * 32 + e) / 2 + 1] = pack2(x[b][e + 2], x[b][e + 3]);
+                }
+            ptx::tmem_st32_async(t_s + lanes + half * 64, p);
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(m.p_ready);
+            ok = ptx::mbar_wait(m.dots, it & 1, m.abort_flag, s.err, 38);
+            if (!__all_sync(0xffffffffu, ok)) {
+                alive = false;
+                break;
+            }
+            ptx::tc_fence_after();
+            float y[2][32];
+            read_half(t_dp + lanes + half * 64, y);
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    const float4 d4 = *reinterpret_cast<const float4 *>(delta + b * 32 + e);
+                    const float dl[4] = {d4.x, d4.y, d4.z, d4.w};
+#pragma unroll
+                    for (int f = 0; f < 4; ++f) {
+                        float &v = y[b][e + f];
+                        v = x[b][e + f] * (v - dl[f]);
+                        // what is masked may be infinite here
+                        if (masked && (b * 32 + e + f < lo || b * 32 + e + f >= hi)) v = 0.0f;
+                    }
+                    p[(b * 32 + e) / 2] = pack2(y[b][e], y[b][e + 1]);
+                    p[(b * 32 + e) / 2 + 1] = pack2(y[b][e + 2], y[b][e + 3]);
+                }
+            ptx::tmem_st32_async(t_dp + lanes + half * 64, p);
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                ptx::mbar_arrive(m.ds_ready);
+                ptx::mbar_arrive(&m.stats_empty[it & 1]);
+            }
+        }
+        if (alive) {
+            const bool ok = ptx::mbar_wait(m.done, 0, m.abort_flag, s.err, 39);
+            alive = __all_sync(0xffffffffu, ok);
+        }
+        if (alive) {
+            ptx::tc_fence_after();
+            // warps 0 - 3 write dK, 4 - 7 dV
+            const bool mine = key < t.n;
+            const uint32_t from = (half ? t_dv : t_dk) + lanes;
+            __nv_bfloat16 *to = dQKV + (t.row0 + key) * s.ld +
+                                static_cast<int64_t>(half ? s.v_head(kv) : s.k_head(kv)) * s.d;
+            const float f = half ? 1.0f : s.scale;
+            bool fine = write_half(from, f, 0, s.d, to, mine);
+            fine = write_half(from + 64, f, 64, s.d, to, mine) && fine;
+            if (!fine) *m.odd = 1;
+        }
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, kTmemCols);
+    }
+    // something masked may have been infinite (0 inf is NaN): once more, passing it over
+    if (*m.odd && !*m.abort_flag && threadIdx.x < kPlainThreads) {
+#pragma unroll 1
+        for (int k = k0; k < min(t.n, k0 + kTile); k += kRows) {
+            plain_sync();
+            plain_dkv_tile(s, QKV, dO, stats, t.row0, t.n, k, kv, dQKV, reinterpret_cast<float *>(m.tiles));
+        }
+    }
+}
+
+// dQ of 128 queries of a head. Per tile of 128 keys, with the queries as rows:
+//   S = Q K^T, dP = dO V^T  ->  dS = 2^(S c - lse) (dP - delta)  ->  dQ += dS K
+// Tensor memory: two S (dS overwrites the one that it is made of), dP, dQ. In the order
+//   S(0) dP(0) | S(1) dQ(0) dP(1) | S(2) dQ(1) ..
+// the next S is under way while the threads form dS, and P is formed during dQ and dP.
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    tc_dq_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap map_do, const Shape s,
+                 const __nv_bfloat16 *QKV, const __nv_bfloat16 *dO, const float2 *stats, int tiles,
+                 __nv_bfloat16 *dQKV) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const BwdSmem m(smem_raw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        m.init();
+        ptx::prefetch_tmap(&map);
+        ptx::prefetch_tmap(&map_do);
+    }
+    grid_begin();
+    const int h = blockIdx.x % s.n_q, kv = h / s.group;
+    const Tile t = find_tile(s, blockIdx.x / s.n_q, kTile, tiles);
+    if (t.n == 0) {
+        zero_rest(s, t, dQKV, s.ld, static_cast<int64_t>(s.q_head(h)) * s.d);
+        return;
+    }
+    const int q0 = (t.tiles - 1 - t.tile) * kTile;
+    const KeyTiles kt = key_tiles(s, q0, min(t.n, q0 + kTile), kTile);
+    const int count = kt.count();
+    if (warp == 9) {
+        ptx::tmem_alloc(m.tmem_slot, kTmemCols);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *m.tmem_slot, t_dp = tmem + 256, t_dq = tmem + 384;
+    const int blocks = s.d > 64 ? 2 : 1;
+
+    if (warp == 8) {
+        if (lane == 0) {
+            ptx::mbar_arrive_expect_tx(m.stay, 2 * blocks * kBlockBytes);
+            load_tile(m.tiles, &map, m.stay, s.q_head(h), t.row0 + q0, blocks);
+            load_tile(m.tiles + kTileBytes, &map_do, m.stay, h, t.row0 + q0, blocks);
+            int pos = 0;
+            bool ok = true;
+            for (int u = 0; u < count && ok; ++u) {
+                const int64_t row = t.row0 + static_cast<int64_t>(kt.at(u)) * kTile;
+                ok = ring_load(m, pos, &map, s.k_head(kv), row, blocks, s.err);
+                pos += ok;
+                ok = ok && ring_load(m, pos, &map, s.v_head(kv), row, blocks, s.err);
+                pos += ok;
+            }
+            if (*m.abort_flag) ring_drain(m, pos);
+        }
+    } else if (warp == 9) {
+        if (lane == 0) {
+            const uint32_t idesc = idesc_weighted(s.d), base = ptx::smem_u32(m.ring.at), q_tile = ptx::smem_u32(m.tiles);
+            auto tile = [&](int pos) { return base + Ring::slot(pos) * kTileBytes; };
+            auto arrived = [&](int pos) {
+                return ptx::mbar_wait(&m.ring.full[Ring::slot(pos)], Ring::parity(pos), m.abort_flag, s.err, 41);
+            };
+            bool ok = ptx::mbar_wait(m.stay, 0, m.abort_flag, s.err, 42) && arrived(0);
+            if (ok) {
+                ptx::tc_fence_after();
+                mma_scores(tmem, q_tile, tile(0), s.d);
+                ptx::mma_commit(&m.scores[0]);
+                ok = arrived(1);
+            }
+            if (ok) {
+                mma_scores(t_dp, q_tile + kTileBytes, tile(1), s.d);
+                ptx::mma_commit(m.dots);
+                ptx::mma_commit(&m.ring.empty[Ring::slot(1)]);
+            }
+            for (int it = 0; it < count && ok; ++it) {
+                const int k = 2 * it;
+                const bool more = it + 1 < count;
+                if (more) {
+                    ok = arrived(k + 2);
+                    if (!ok) break;
+                    mma_scores(tmem + ((it + 1) & 1) * 128, q_tile, tile(k + 2), s.d);
+                    ptx::mma_commit(&m.scores[(it + 1) & 1]);
+                }
+                ok = ptx::mbar_wait(m.ds_ready, it & 1, m.abort_flag, s.err, 43);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                mma_weighted(t_dq, tmem + (it & 1) * 128, 64, tile(k), idesc, it > 0);
+                ptx::mma_commit(&m.ring.empty[Ring::slot(k)]);
+                if (more) {
+                    ok = arrived(k + 3);
+                    if (!ok) break;
+                    mma_scores(t_dp, q_tile + kTileBytes, tile(k + 3), s.d);
+                    ptx::mma_commit(m.dots);
+                    ptx::mma_commit(&m.ring.empty[Ring::slot(k + 3)]);
+                }
+            }
+            if (ok) ptx::mma_commit(m.done);
+            ptx::mma_commit(m.drain);
+            ptx::mbar_wait_drain(m.drain, 0);
+        }
+    } else if (warp < 8) {
+        const int half = warp >> 2, row = q0 + (warp & 3) * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const float c = s.scale * kLog2e;
+        const bool mine = row < t.n;
+        const float2 st = mine ? stats[h * s.T + t.row0 + row] : make_float2(INFINITY, 0.0f);
+        bool alive = true;
+        for (int it = 0; it < count && alive; ++it) {
+            const int k0 = kt.at(it) * kTile;
+            const bool masked = !all_seen(s, q0, q0 + kTile, k0, k0 + kTile);
+            const int hi = row - k0 - half * 64, lo = s.window ? hi - s.window + 1 : INT_MIN,
+                      sink = s.sinks - k0 - half * 64;
+            const uint32_t t_s = tmem + (it & 1) * 128 + lanes + half * 64;
+            bool ok = ptx::mbar_wait(&m.scores[it & 1], (it >> 1) & 1, m.abort_flag, s.err, 44);
+            if (!__all_sync(0xffffffffu, ok)) {
+                alive = false;
+                break;
+            }
+            ptx::tc_fence_after();
+            float x[2][32], y[2][32];
+            read_half(t_s, x);
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    scale2(x[b][e], x[b][e + 1], c, -st.x);
+                    x[b][e] = exp2_fast(x[b][e]);
+                    x[b][e + 1] = exp2_fast(x[b][e + 1]);
+                }
+            ok = ptx::mbar_wait(m.dots, it & 1, m.abort_flag, s.err, 45);
+            if (!__all_sync(0xffffffffu, ok)) {
+                alive = false;
+                break;
+            }
+            ptx::tc_fence_after();
+            read_half(t_dp + lanes + half * 64, y);
+            uint32_t p[32];
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) {
+                        const int at = b * 32 + e + f;
+                        float &v = y[b][e + f];
+                        v = x[b][e + f] * (v - st.y);
+                        if (masked && (at > hi || (at < lo && at >= sink))) v = 0.0f;
+                    }
+                    p[(b * 32 + e) / 2] = pack2(y[b][e], y[b][e + 1]);
+                }
+            ptx::tmem_st32_async(t_s, p);
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(m.ds_ready);
+        }
+        if (alive) {
+            const bool ok = ptx::mbar_wait(m.done, 0, m.abort_flag, s.err, 46);
+            alive = __all_sync(0xffffffffu, ok);
+        }
+        if (alive && half * 64 < s.d) {
+            ptx::tc_fence_after();
+            __nv_bfloat16 *to = dQKV + (t.row0 + row) * s.ld + static_cast<int64_t>(s.q_head(h)) * s.d;
+            if (!write_half(t_dq + lanes + half * 64, s.scale, half * 64, s.d, to, mine)) *m.odd = 1;
+        }
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, kTmemCols);
+    }
+    if (*m.odd && !*m.abort_flag && threadIdx.x < kPlainThreads) {
+#pragma unroll 1
+        for (int q = q0; q < min(t.n, q0 + kTile); q += kRows) {
+            plain_sync();
+            plain_dq_tile(s, QKV, dO, stats, t.row0, t.n, q, h, dQKV, reinterpret_cast<float *>(m.tiles));
+        }
+    }
+}
+
 // ------------------------------------------------------------------ host
+tpce_status tc_backward(const Shape &s, const void *QKV, const void *dO, const float2 *stats, void *dQKV,
+                        cudaStream_t stream) {
+    CUtensorMap map, map_do;
+    if (!make_tmap_heads(&map, QKV, s.d, s.n_q + 2 * s.n_kv, s.T, s.ld, kTile) ||
+        !make_tmap_heads(&map_do, dO, s.d, s.n_q, s.T, static_cast<uint64_t>(s.n_q) * s.d, kTile))
+        return fail(TPCE_ERR_CUDA, "attn_backward: tensor map");
+    const int tiles = static_cast<int>(grid_tiles(s, kTile));
+    auto go = [&](auto kernel, const char *name, int heads) {
+        KernelTimer timer(name, stream);
+        const cudaError_t e = step::launch(kernel, static_cast<unsigned>(tiles) * heads, kBwdThreads, kBwdSmem,
+                                           stream, map, map_do, s, static_cast<const __nv_bfloat16 *>(QKV),
+                                           static_cast<const __nv_bfloat16 *>(dO), stats, tiles,
+                                           static_cast<__nv_bfloat16 *>(dQKV));
+        return e == cudaSuccess ? check_launch(name, stream) : fail_cuda(e, name);
+    };
+    cudaError_t e = allow_smem<tc_dkv_kernel>();
+    if (e == cudaSuccess) e = allow_smem<tc_dq_kernel>();
+    if (e != cudaSuccess) return fail_cuda(e, "attn_backward");
+    const tpce_status st = go(tc_dkv_kernel, "attn_dkv", s.n_kv);
+    return st != TPCE_OK ? st : go(tc_dq_kernel, "attn_dq", s.n_q);
+}
+
 template <typename T>
 tpce_status plain_backward(const Shape &s, const void *QKV, const void *dO, const float2 *stats, void *dQKV,
                            cudaStream_t stream) {
@@ -261,7 +830,7 @@ extern "C" tpce_status tp_attn_core_backward(const void *dO, const void *QKV, co
     float2 *stats = static_cast<float2 *>(ws);
     if (dtype == TPCE_BF16) {
         if ((st = delta<__nv_bfloat16>(s, dO, O, lse, stats, stream_)) != TPCE_OK) return st;
-        return plain_backward<__nv_bfloat16>(s, QKV, dO, stats, dQKV, stream_);
+        return tc_backward(s, QKV, dO, stats, dQKV, stream_);
     }
     if ((st = delta<float>(s, dO, O, lse, stats, stream_)) != TPCE_OK) return st;
     return plain_backward<float>(s, QKV, dO, stats, dQKV, stream_);
