@@ -89,15 +89,15 @@ __device__ __forceinline__ Tile find_tile(const Shape &s, int x, int rows, int g
     }
     const int lane = threadIdx.x & 31;
     const int T = static_cast<int>(s.T);
-    int first = s.offsets[0];
+    int first = s.offsets[0], given = lane < s.sequences ? s.offsets[lane + 1] : 0;
     if (first < 0 || first > T) {
         if (lane == 0) ptx::record_error(s.err, kErrInvalid | (6u << 8));
         first = first < 0 ? 0 : T;
     }
     int end = first, before = 0;  // of the sequences so far: the last row, the tiles
     for (int b0 = 0; b0 < s.sequences; b0 += 32) {
-        const int given = b0 + lane < s.sequences ? s.offsets[b0 + lane + 1] : end;
-        int e = max(end, min(given, T));
+        if (b0) given = b0 + lane < s.sequences ? s.offsets[b0 + lane + 1] : 0;
+        int e = b0 + lane < s.sequences ? max(end, min(given, T)) : end;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int o = __shfl_up_sync(0xffffffffu, e, d);

@@ -356,7 +356,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    const uint32_t tmem = *m.tmem_slot, t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 384;
+    constexpr uint32_t tmem = 0,  // all columns there are: they begin at 0
+                       t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 384;
     const int blocks = s.d > 64 ? 2 : 1;
 
     if (warp == 8) {
@@ -378,51 +379,52 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             if (*m.abort_flag) ring_drain(m, pos);
         }
     } else if (warp == 9) {
-        if (lane == 0) {
+        {
+            const bool leader = ptx::elect_one();
             const uint32_t idesc = idesc_weighted(s.d), base = ptx::smem_u32(m.ring.at), k_tile = ptx::smem_u32(m.tiles);
             auto tile = [&](int pos) { return base + Ring::slot(pos) * kTileBytes; };
             auto arrived = [&](int pos) {
-                return ptx::mbar_wait(&m.ring.full[Ring::slot(pos)], Ring::parity(pos), m.abort_flag, s.err, 31);
+                return wait_all(&m.ring.full[Ring::slot(pos)], Ring::parity(pos), m.abort_flag, s.err, 31);
             };
-            bool ok = ptx::mbar_wait(m.stay, 0, m.abort_flag, s.err, 32) && arrived(0);
+            bool ok = wait_all(m.stay, 0, m.abort_flag, s.err, 32) && arrived(0);
             if (ok) {
                 ptx::tc_fence_after();
-                mma_scores(t_s, k_tile, tile(0), s.d);
-                ptx::mma_commit(m.scores);
+                mma_scores(leader, t_s, k_tile, tile(0), s.d);
+                commit(leader, m.scores);
                 ok = arrived(1);
             }
             if (ok) {
-                mma_scores(t_dp, k_tile + kTileBytes, tile(1), s.d);
-                ptx::mma_commit(m.dots);
+                mma_scores(leader, t_dp, k_tile + kTileBytes, tile(1), s.d);
+                commit(leader, m.dots);
             }
             for (int it = 0; it < count && ok; ++it) {
                 const int q = 2 * it, o = q + 1;
                 const bool more = it + 1 < count;
-                ok = ptx::mbar_wait(m.p_ready, it & 1, m.abort_flag, s.err, 33);
+                ok = wait_all(m.p_ready, it & 1, m.abort_flag, s.err, 33);
                 if (!ok) break;
                 ptx::tc_fence_after();
-                mma_weighted(t_dv, t_s, 64, tile(o), idesc, it > 0);
-                ptx::mma_commit(&m.ring.empty[Ring::slot(o)]);
+                mma_weighted(leader, t_dv, t_s, 64, tile(o), idesc, it > 0);
+                commit(leader, &m.ring.empty[Ring::slot(o)]);
                 if (more) {
                     ok = arrived(q + 2);
                     if (!ok) break;
-                    mma_scores(t_s, k_tile, tile(q + 2), s.d);
-                    ptx::mma_commit(m.scores);
+                    mma_scores(leader, t_s, k_tile, tile(q + 2), s.d);
+                    commit(leader, m.scores);
                 }
-                ok = ptx::mbar_wait(m.ds_ready, it & 1, m.abort_flag, s.err, 34);
+                ok = wait_all(m.ds_ready, it & 1, m.abort_flag, s.err, 34);
                 if (!ok) break;
                 ptx::tc_fence_after();
-                mma_weighted(t_dk, t_dp, 64, tile(q), idesc, it > 0);
-                ptx::mma_commit(&m.ring.empty[Ring::slot(q)]);
+                mma_weighted(leader, t_dk, t_dp, 64, tile(q), idesc, it > 0);
+                commit(leader, &m.ring.empty[Ring::slot(q)]);
                 if (more) {
                     ok = arrived(o + 2);
                     if (!ok) break;
-                    mma_scores(t_dp, k_tile + kTileBytes, tile(o + 2), s.d);
-                    ptx::mma_commit(m.dots);
+                    mma_scores(leader, t_dp, k_tile + kTileBytes, tile(o + 2), s.d);
+                    commit(leader, m.dots);
                 }
             }
-            if (ok) ptx::mma_commit(m.done);
-            ptx::mma_commit(m.drain);
+            if (ok) commit(leader, m.done);
+            commit(leader, m.drain);
             ptx::mbar_wait_drain(m.drain, 0);
         }
     } else if (warp == 10) {
@@ -438,8 +440,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     const int row = k0 + q * kTile + e * 32 + lane;
                     v[e] = row < t.n ? from[row] : make_float2(INFINITY, 0.0f);
                 }
-                ok = ptx::mbar_wait(&m.stats_empty[it & 1], ((it >> 1) & 1) ^ 1, m.abort_flag, s.err, 35);
-                ok = __all_sync(0xffffffffu, ok);
+                ok = wait_all(&m.stats_empty[it & 1], ((it >> 1) & 1) ^ 1, m.abort_flag, s.err, 35);
                 if (!ok) break;
                 float *to = m.stats + (it & 1) * 2 * kTile;
 #pragma unroll
@@ -461,14 +462,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const int q0 = k0 + q * kTile;
             q = q + 1 == of_head ? 0 : q + 1;
             const bool masked = !all_seen(s, q0, q0 + kTile, k0, k0 + kTile) || q0 + kTile > t.n;
-            const int lo = key - q0 - half * 64, hi = limit - q0 - half * 64;
-            const float *lse = m.stats + (it & 1) * 2 * kTile + half * 64, *delta = lse + kTile;
-            bool ok = ptx::mbar_wait(&m.stats_full[it & 1], (it >> 1) & 1, m.abort_flag, s.err, 36) &&
-                      ptx::mbar_wait(m.scores, it & 1, m.abort_flag, s.err, 37);
-            if (!__all_sync(0xffffffffu, ok)) {
-                alive = false;
-                break;
+            uint32_t seen[2];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                // queries from the key's own on, below its limit
+                const int at = q0 + half * 64 + b * 32;
+                seen[b] = masked ? below(limit - at) & ~below(key - at) : 0xffffffffu;
             }
+            const float *lse = m.stats + (it & 1) * 2 * kTile + half * 64, *delta = lse + kTile;
+            alive = wait_all(&m.stats_full[it & 1], (it >> 1) & 1, m.abort_flag, s.err, 36) &&
+                    wait_all(m.scores, it & 1, m.abort_flag, s.err, 37);
+            if (!alive) break;
             ptx::tc_fence_after();
             float x[2][32];
             read_half(t_s + lanes + half * 64, x);
@@ -483,7 +487,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     for (int f = 0; f < 4; ++f) {
                         float &v = x[b][e + f];
                         v = exp2_fast(fmaf(v, c, -l[f]));
-                        if (masked && (b * 32 + e + f < lo || b * 32 + e + f >= hi)) v = 0.0f;
+                        if (masked) v = seen[b] & (1u << (e + f)) ? v : 0.0f;
                     }
                     p[(b * 32 + e) / 2] = pack2(x[b][e], x[b][e + 1]);
                     p[(b * 32 + e) / 2 + 1] = pack2(x[b][e + 2], x[b][e + 3]);
@@ -493,11 +497,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(m.p_ready);
-            ok = ptx::mbar_wait(m.dots, it & 1, m.abort_flag, s.err, 38);
-            if (!__all_sync(0xffffffffu, ok)) {
-                alive = false;
-                break;
-            }
+            alive = wait_all(m.dots, it & 1, m.abort_flag, s.err, 38);
+            if (!alive) break;
             ptx::tc_fence_after();
             float y[2][32];
             read_half(t_dp + lanes + half * 64, y);
@@ -512,7 +513,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                         float &v = y[b][e + f];
                         v = x[b][e + f] * (v - dl[f]);
                         // what is masked may be infinite here
-                        if (masked && (b * 32 + e + f < lo || b * 32 + e + f >= hi)) v = 0.0f;
+                        if (masked) v = seen[b] & (1u << (e + f)) ? v : 0.0f;
                     }
                     p[(b * 32 + e) / 2] = pack2(y[b][e], y[b][e + 1]);
                     p[(b * 32 + e) / 2 + 1] = pack2(y[b][e + 2], y[b][e + 3]);
@@ -526,10 +527,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 ptx::mbar_arrive(&m.stats_empty[it & 1]);
             }
         }
-        if (alive) {
-            const bool ok = ptx::mbar_wait(m.done, 0, m.abort_flag, s.err, 39);
-            alive = __all_sync(0xffffffffu, ok);
-        }
+        if (alive) alive = wait_all(m.done, 0, m.abort_flag, s.err, 39);
         if (alive) {
             ptx::tc_fence_after();
             // warps 0 - 3 write dK, 4 - 7 dV
@@ -594,7 +592,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    const uint32_t tmem = *m.tmem_slot, t_dp = tmem + 256, t_dq = tmem + 384;
+    constexpr uint32_t tmem = 0, t_dp = tmem + 256, t_dq = tmem + 384;
     const int blocks = s.d > 64 ? 2 : 1;
 
     if (warp == 8) {
@@ -614,23 +612,24 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             if (*m.abort_flag) ring_drain(m, pos);
         }
     } else if (warp == 9) {
-        if (lane == 0) {
+        {
+            const bool leader = ptx::elect_one();
             const uint32_t idesc = idesc_weighted(s.d), base = ptx::smem_u32(m.ring.at), q_tile = ptx::smem_u32(m.tiles);
             auto tile = [&](int pos) { return base + Ring::slot(pos) * kTileBytes; };
             auto arrived = [&](int pos) {
-                return ptx::mbar_wait(&m.ring.full[Ring::slot(pos)], Ring::parity(pos), m.abort_flag, s.err, 41);
+                return wait_all(&m.ring.full[Ring::slot(pos)], Ring::parity(pos), m.abort_flag, s.err, 41);
             };
-            bool ok = ptx::mbar_wait(m.stay, 0, m.abort_flag, s.err, 42) && arrived(0);
+            bool ok = wait_all(m.stay, 0, m.abort_flag, s.err, 42) && arrived(0);
             if (ok) {
                 ptx::tc_fence_after();
-                mma_scores(tmem, q_tile, tile(0), s.d);
-                ptx::mma_commit(&m.scores[0]);
+                mma_scores(leader, tmem, q_tile, tile(0), s.d);
+                commit(leader, &m.scores[0]);
                 ok = arrived(1);
             }
             if (ok) {
-                mma_scores(t_dp, q_tile + kTileBytes, tile(1), s.d);
-                ptx::mma_commit(m.dots);
-                ptx::mma_commit(&m.ring.empty[Ring::slot(1)]);
+                mma_scores(leader, t_dp, q_tile + kTileBytes, tile(1), s.d);
+                commit(leader, m.dots);
+                commit(leader, &m.ring.empty[Ring::slot(1)]);
             }
             for (int it = 0; it < count && ok; ++it) {
                 const int k = 2 * it;
@@ -638,24 +637,24 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 if (more) {
                     ok = arrived(k + 2);
                     if (!ok) break;
-                    mma_scores(tmem + ((it + 1) & 1) * 128, q_tile, tile(k + 2), s.d);
-                    ptx::mma_commit(&m.scores[(it + 1) & 1]);
+                    mma_scores(leader, tmem + ((it + 1) & 1) * 128, q_tile, tile(k + 2), s.d);
+                    commit(leader, &m.scores[(it + 1) & 1]);
                 }
-                ok = ptx::mbar_wait(m.ds_ready, it & 1, m.abort_flag, s.err, 43);
+                ok = wait_all(m.ds_ready, it & 1, m.abort_flag, s.err, 43);
                 if (!ok) break;
                 ptx::tc_fence_after();
-                mma_weighted(t_dq, tmem + (it & 1) * 128, 64, tile(k), idesc, it > 0);
-                ptx::mma_commit(&m.ring.empty[Ring::slot(k)]);
+                mma_weighted(leader, t_dq, tmem + (it & 1) * 128, 64, tile(k), idesc, it > 0);
+                commit(leader, &m.ring.empty[Ring::slot(k)]);
                 if (more) {
                     ok = arrived(k + 3);
                     if (!ok) break;
-                    mma_scores(t_dp, q_tile + kTileBytes, tile(k + 3), s.d);
-                    ptx::mma_commit(m.dots);
-                    ptx::mma_commit(&m.ring.empty[Ring::slot(k + 3)]);
+                    mma_scores(leader, t_dp, q_tile + kTileBytes, tile(k + 3), s.d);
+                    commit(leader, m.dots);
+                    commit(leader, &m.ring.empty[Ring::slot(k + 3)]);
                 }
             }
-            if (ok) ptx::mma_commit(m.done);
-            ptx::mma_commit(m.drain);
+            if (ok) commit(leader, m.done);
+            commit(leader, m.drain);
             ptx::mbar_wait_drain(m.drain, 0);
         }
     } else if (warp < 8) {
@@ -668,14 +667,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         for (int it = 0; it < count && alive; ++it) {
             const int k0 = kt.at(it) * kTile;
             const bool masked = !all_seen(s, q0, q0 + kTile, k0, k0 + kTile);
-            const int hi = row - k0 - half * 64, lo = s.window ? hi - s.window + 1 : INT_MIN,
-                      sink = s.sinks - k0 - half * 64;
-            const uint32_t t_s = tmem + (it & 1) * 128 + lanes + half * 64;
-            bool ok = ptx::mbar_wait(&m.scores[it & 1], (it >> 1) & 1, m.abort_flag, s.err, 44);
-            if (!__all_sync(0xffffffffu, ok)) {
-                alive = false;
-                break;
+            uint32_t seen[2];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int at = k0 + half * 64 + b * 32, hi = row - at;
+                seen[b] = visible(hi, s.window ? hi - s.window + 1 : -kTile, s.sinks - at);
             }
+            const uint32_t t_s = tmem + (it & 1) * 128 + lanes + half * 64;
+            alive = wait_all(&m.scores[it & 1], (it >> 1) & 1, m.abort_flag, s.err, 44);
+            if (!alive) break;
             ptx::tc_fence_after();
             float x[2][32], y[2][32];
             read_half(t_s, x);
@@ -687,11 +687,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     x[b][e] = exp2_fast(x[b][e]);
                     x[b][e + 1] = exp2_fast(x[b][e + 1]);
                 }
-            ok = ptx::mbar_wait(m.dots, it & 1, m.abort_flag, s.err, 45);
-            if (!__all_sync(0xffffffffu, ok)) {
-                alive = false;
-                break;
-            }
+            alive = wait_all(m.dots, it & 1, m.abort_flag, s.err, 45);
+            if (!alive) break;
             ptx::tc_fence_after();
             read_half(t_dp + lanes + half * 64, y);
             uint32_t p[32];
@@ -701,10 +698,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 for (int e = 0; e < 32; e += 2) {
 #pragma unroll
                     for (int f = 0; f < 2; ++f) {
-                        const int at = b * 32 + e + f;
                         float &v = y[b][e + f];
                         v = x[b][e + f] * (v - st.y);
-                        if (masked && (at > hi || (at < lo && at >= sink))) v = 0.0f;
+                        if (masked) v = seen[b] & (1u << (e + f)) ? v : 0.0f;
                     }
                     p[(b * 32 + e) / 2] = pack2(y[b][e], y[b][e + 1]);
                 }
@@ -714,10 +710,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(m.ds_ready);
         }
-        if (alive) {
-            const bool ok = ptx::mbar_wait(m.done, 0, m.abort_flag, s.err, 46);
-            alive = __all_sync(0xffffffffu, ok);
-        }
+        if (alive) alive = wait_all(m.done, 0, m.abort_flag, s.err, 46);
         if (alive && half * 64 < s.d) {
             ptx::tc_fence_after();
             __nv_bfloat16 *to = dQKV + (t.row0 + row) * s.ld + static_cast<int64_t>(s.q_head(h)) * s.d;

@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    constexpr uint32_t tmem = 0;  // all columns there are: they begin at 0
     const int blocks = s.d > 64 ? 2 : 1;
 
     if (warp < 8) {
@@ -251,12 +251,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         for (int u = 0; u < count && alive; ++u) {
             const int k = kt.both.at(u);
             if (!kt.needs(i, k)) continue;
-            const bool ok = ptx::mbar_wait(&s_full[i], phase, abort_flag, s.err, 24);
+            alive = wait_all(&s_full[i], phase, abort_flag, s.err, 24);
             phase ^= 1;
-            if (!__all_sync(0xffffffffu, ok)) {
-                alive = false;
-                break;
-            }
+            if (!alive) break;
             ptx::tc_fence_after();
             float x[4][32];
 #pragma unroll
@@ -266,11 +263,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             for (int b = 0; b < 4; ++b) ptx::tmem_ready(x[b]);
             const int k0 = k * kTile;
             if (!all_seen(s, my_q0, my_q0 + kTile, k0, k0 + kTile)) {
-                // columns up to `hi`, from `lo` on or below `sink`
-                const int hi = row - k0, lo = s.window ? row - s.window + 1 - k0 : INT_MIN, sink = s.sinks - k0;
+                const int hi = row - k0, lo = s.window ? hi - s.window + 1 : -kTile, sink = s.sinks - k0;
 #pragma unroll
-                for (int e = 0; e < kTile; ++e)
-                    if (e > hi || (e < lo && e >= sink)) x[e / 32][e % 32] = -INFINITY;
+                for (int b = 0; b < 4; ++b) {
+                    const uint32_t seen = visible(hi - b * 32, lo - b * 32, sink - b * 32);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[b][e] = seen & (1u << e) ? x[b][e] : -INFINITY;
+                }
             }
             float top[4];
 #pragma unroll
@@ -313,11 +312,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&p_full[i]);
         }
-        if (alive) {
-            const bool ok = ptx::mbar_wait(&o_full[i], 0, abort_flag, s.err, 25);
-            alive = __all_sync(0xffffffffu, ok);
-        }
-        if (alive) {
+        if (alive && wait_all(&o_full[i], 0, abort_flag, s.err, 25)) {
             ptx::tc_fence_after();
             const float inv = 1.0f / l;
             const bool mine = row < t.n;
@@ -383,15 +378,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             }
         } else if (warp == 9) {
             // ------------------------------------------------ products
-            if (lane == 0) {
+            {
+                const bool leader = ptx::elect_one();
                 const uint32_t idesc = idesc_weighted(s.d);
                 const uint32_t q_tile = ptx::smem_u32(smem), base = ptx::smem_u32(ring);
                 int stage = 0;
                 uint32_t phase = 0, p_phase[2] = {0, 0};
                 bool begun[2] = {false, false};
-                bool ok = ptx::mbar_wait(q_full, 0, abort_flag, s.err, 21);
+                bool ok = wait_all(q_full, 0, abort_flag, s.err, 21);
                 auto next = [&](int &at) {
-                    ok = ok && ptx::mbar_wait(&full[stage], phase, abort_flag, s.err, 22);
+                    ok = ok && wait_all(&full[stage], phase, abort_flag, s.err, 22);
                     at = stage;
                     if (++stage == kFwdStages) {
                         stage = 0;
@@ -407,26 +403,26 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     for (int i = 0; i < 2; ++i) {
                         if (!ok) break;
                         if (u > 0 && kt.needs(i, kt.both.at(u - 1))) {
-                            if (!ptx::mbar_wait(&p_full[i], p_phase[i], abort_flag, s.err, 23)) {
+                            if (!wait_all(&p_full[i], p_phase[i], abort_flag, s.err, 23)) {
                                 ok = false;
                                 break;
                             }
                             p_phase[i] ^= 1;
                             ptx::tc_fence_after();
-                            mma_weighted(tmem + 256 + i * 128, tmem + i * 128, 32, base + v_stage * kTileBytes, idesc,
+                            mma_weighted(leader, tmem + 256 + i * 128, tmem + i * 128, 32, base + v_stage * kTileBytes, idesc,
                                          begun[i]);
                             begun[i] = true;
-                            if (kt.both.at(u - 1) == kt.one[i].last) ptx::mma_commit(&o_full[i]);
+                            if (kt.both.at(u - 1) == kt.one[i].last) commit(leader, &o_full[i]);
                         }
                         if (u < count && kt.needs(i, kt.both.at(u))) {
-                            mma_scores(tmem + i * 128, q_tile + i * kTileBytes, base + k_stage * kTileBytes, s.d);
-                            ptx::mma_commit(&s_full[i]);
+                            mma_scores(leader, tmem + i * 128, q_tile + i * kTileBytes, base + k_stage * kTileBytes, s.d);
+                            commit(leader, &s_full[i]);
                         }
                     }
-                    if (u < count) ptx::mma_commit(&empty[k_stage]);
-                    if (u > 0) ptx::mma_commit(&empty[v_stage]);
+                    if (u < count) commit(leader, &empty[k_stage]);
+                    if (u > 0) commit(leader, &empty[v_stage]);
                 }
-                ptx::mma_commit(drain);
+                commit(leader, drain);
                 ptx::mbar_wait_drain(drain, 0);
             }
         }

@@ -27,23 +27,41 @@ __device__ __forceinline__ uint64_t step_cols(uint64_t desc, int k) {
     return desc + static_cast<uint32_t>((k * 16 * 128) >> 4);
 }
 
+// The columns of one row that are visible, as bits of 32 columns each: those up to hi,
+// from lo on or below sink (all relative to the tile's first column).
+__device__ __forceinline__ uint32_t below(int n) {  // bits 0 .. n - 1
+    return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+__device__ __forceinline__ uint32_t visible(int hi, int lo, int sink) {
+    return below(hi + 1) & (~below(lo) | below(sink));
+}
+
+// All lanes of the warp that issues products call these; `leader` is the one that does.
 // D = A B^T over d: 128 x 128 scores of two tiles' rows.
-__device__ __forceinline__ void mma_scores(uint32_t d_tmem, uint32_t a_tile, uint32_t b_tile, int d) {
+__device__ __forceinline__ void mma_scores(bool leader, uint32_t d_tmem, uint32_t a_tile, uint32_t b_tile, int d) {
     constexpr uint32_t kIdesc = ptx::idesc_f32acc(kTile, kTile, 1, false, false);
     const uint64_t a = desc_rows(a_tile), b = desc_rows(b_tile);
     const int steps = (d + 15) / 16;
-    for (int k = 0; k < steps; ++k) ptx::mma_bf16(d_tmem, step_rows(a, k), step_rows(b, k), kIdesc, k != 0);
+    if (leader) {
+#pragma unroll
+        for (int k = 0; k < kMaxDim / 16; ++k)
+            if (k < steps) ptx::mma_bf16(d_tmem, step_rows(a, k), step_rows(b, k), kIdesc, k != 0);
+    }
+    __syncwarp();
 }
 
 // D (+)= A X: A (bf16 in tensor memory, from a_tmem on, its second 64 columns of K
 // second_half further) times a tile's 128 rows of d columns.
-__device__ __forceinline__ void mma_weighted(uint32_t d_tmem, uint32_t a_tmem, uint32_t second_half, uint32_t x_tile,
+__device__ __forceinline__ void mma_weighted(bool leader, uint32_t d_tmem, uint32_t a_tmem, uint32_t second_half, uint32_t x_tile,
                                              uint32_t idesc, bool accumulate) {
     const uint64_t x = desc_cols(x_tile);
+    if (leader) {
 #pragma unroll
-    for (int k = 0; k < kTile / 16; ++k)
-        ptx::mma_bf16_ts(d_tmem, a_tmem + (k & 3) * 8 + (k >> 2) * second_half, step_cols(x, k), idesc,
-                         (accumulate || k) ? 1u : 0u);
+        for (int k = 0; k < kTile / 16; ++k)
+            ptx::mma_bf16_ts(d_tmem, a_tmem + (k & 3) * 8 + (k >> 2) * second_half, step_cols(x, k), idesc,
+                             (accumulate || k) ? 1u : 0u);
+    }
+    __syncwarp();
 }
 // the width of such a product: d, rounded up to what the instruction takes
 __host__ __device__ inline int width16(int d) { return (d + 15) / 16 * 16; }
@@ -75,6 +93,18 @@ __device__ __forceinline__ float exp2_fast(float x) {
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// A wait of all lanes, which all get the same answer.
+__device__ __forceinline__ bool wait_all(uint64_t *bar, uint32_t parity, volatile int *abort_flag, uint32_t *err,
+                                         uint32_t where) {
+    const bool ok = ptx::mbar_wait(bar, parity, abort_flag, err, where);
+    return __all_sync(0xffffffffu, ok);
+}
+
+__device__ __forceinline__ void commit(bool leader, uint64_t *bar) {
+    if (leader) ptx::mma_commit(bar);
+    __syncwarp();
 }
 
 // The blocks of one head's tile of rows, into one stage.
