@@ -18,6 +18,7 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <cstddef>
 #include <cstdint>
 
 #include "host.h"
@@ -136,20 +137,6 @@ __device__ __forceinline__ Tile find_tile(const Shape &s, int x, int rows, int g
 // Tiles in a grid for each head: all sequences' tiles and one more at least.
 inline int64_t grid_tiles(const Shape &s, int rows) { return s.T / rows + (s.offsets ? s.sequences : 1) + 1; }
 
-// The columns c0 .. c0 + d of the rows that belong to no sequence become zeros.
-template <typename T>
-__device__ __forceinline__ void zero_rest(const Shape &s, const Tile &t, T *out, int64_t ld, int64_t c0) {
-    Raw8<T> zero;
-    zero8(zero);
-    const int vectors = s.d / 8;
-    const int64_t rows = t.head_rows + (s.T - t.tail_row);
-    for (int64_t i = static_cast<int64_t>(t.part) * blockDim.x + threadIdx.x; i < rows * vectors;
-         i += static_cast<int64_t>(t.parts) * blockDim.x) {
-        const int64_t r = i / vectors;
-        store8(out + (r < t.head_rows ? r : t.tail_row + r - t.head_rows) * ld + c0 + (i - r * vectors) * 8, zero);
-    }
-}
-
 // ------------------------------------------------------------------ key tiles of queries, query tiles of keys
 // The tiles of `rows` keys that queries q0 .. q1 - 1 see: 0 .. first - 1 (sinks), then from .. last.
 struct KeyTiles {
@@ -196,6 +183,22 @@ struct PlainSmem {
 
 // the threads that compute a tile, which may be some of a larger block's
 __device__ __forceinline__ void plain_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// The columns c0 .. c0 + d of the rows that belong to no sequence become zeros, by the
+// block's first 256 threads.
+template <typename T>
+__device__ __forceinline__ void zero_rest(const Shape &s, const Tile &t, T *out, int64_t ld, int64_t c0) {
+    if (threadIdx.x >= kPlainThreads) return;
+    Raw8<T> zero;
+    zero8(zero);
+    const int vectors = s.d / 8;
+    const int64_t rows = t.head_rows + (s.T - t.tail_row);
+    for (int64_t i = static_cast<int64_t>(t.part) * kPlainThreads + threadIdx.x; i < rows * vectors;
+         i += static_cast<int64_t>(t.parts) * kPlainThreads) {
+        const int64_t r = i / vectors;
+        store8(out + (r < t.head_rows ? r : t.tail_row + r - t.head_rows) * ld + c0 + (i - r * vectors) * 8, zero);
+    }
+}
 
 // Rows r0 .. of a tile (zeros from row n on) into shared memory.
 template <typename T>

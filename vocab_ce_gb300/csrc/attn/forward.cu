@@ -101,8 +101,8 @@ template <typename T>
 __device__ __forceinline__ void forward_rest(const Shape &s, const Tile &t, int h, T *O, float *lse) {
     zero_rest(s, t, O, static_cast<int64_t>(s.n_q) * s.d, static_cast<int64_t>(h) * s.d);
     const int64_t rows = t.head_rows + (s.T - t.tail_row);
-    for (int64_t r = static_cast<int64_t>(t.part) * blockDim.x + threadIdx.x; r < rows;
-         r += static_cast<int64_t>(t.parts) * blockDim.x)
+    for (int64_t r = static_cast<int64_t>(t.part) * kPlainThreads + threadIdx.x; r < rows;
+         r += static_cast<int64_t>(t.parts) * kPlainThreads)
         lse[h * s.T + (r < t.head_rows ? r : t.tail_row + r - t.head_rows)] = 0.0f;
 }
 
@@ -135,12 +135,14 @@ tpce_status plain_forward(const Shape &s, const void *QKV, void *O, float *lse, 
 }
 
 // ------------------------------------------------------------------ tiles on the tensor cores
-// A block has two tiles of 128 queries that read the same keys: two heads of a group
-// where it is even, else two neighbouring tiles of one head. Twelve warps,
-// of which the last two only lend their registers:
+// One block an SM stays for all its work: pairs of 128-query tiles that read the same
+// keys, two heads of a group where it is even, else two neighbouring tiles of one head.
+// Twelve warps, of which the last only lends its registers:
 //   warps 0 - 3, 4 - 7   the softmax of tile 0 and of tile 1, a thread a query
-//   warp 8               loads: Q once, then K and V tiles through a ring
+//   warp 8               loads: Q of a pair, K and V tiles through a ring
 //   warp 9               issues the products
+//   warp 10              finds the next pair, two ahead
+// so that the next pair's loads and first scores run while results are written.
 // Tensor memory: the scores S of both tiles (128 columns each; P overwrites the first
 // half of S in bf16) and both O. For each key tile
 //   S = Q K^T  ->  softmax threads: running maximum, P = 2^(S c - m), row sums  ->  O += P V
@@ -152,177 +154,229 @@ tpce_status plain_forward(const Shape &s, const void *QKV, void *O, float *lse, 
 // and O, l and lse are as exact.
 constexpr int kFwdThreads = 384, kFwdStages = 5;
 constexpr float kRaise = 8.0f;  // in powers of two
-constexpr uint32_t kFwdSmem = 1024 + 2 * kTileBytes + kFwdStages * kTileBytes + 256;
-static_assert(kFwdSmem <= static_cast<uint32_t>(kMaxSmem), "the ring fits");
+constexpr int kOddBits = 1024;
+
+// A pair of tiles, or rows without a sequence (n == 0), or the end (unit < 0).
+struct Work {
+    Tile t;
+    int unit, first;
+};
+struct FwdSmem {
+    uint8_t q[2][kTileBytes];
+    uint8_t ring[kFwdStages][kTileBytes];
+    uint64_t full[kFwdStages], empty[kFwdStages];
+    uint64_t q_full, q_empty;
+    uint64_t s_full[2], p_full[2][2], o_full[2], o_empty[2];
+    uint64_t work_full[2], work_empty[2];
+    uint64_t drain;
+    Work work[2];
+    uint32_t odd[2][kOddBits / 32];  // of the block's pairs: a tile has results that are not finite
+    uint32_t tmem_slot;
+    int abort_flag;
+};
+static_assert(sizeof(FwdSmem) <= static_cast<size_t>(kMaxSmem), "the ring fits");
+constexpr int kWorkReaders = 10;  // warps
 
 // The key tiles of both tiles together, and which of the two needs one.
-struct PairTiles {
+struct Pair {
+    int head[2], q0[2], count;
     KeyTiles one[2], both;
+    __device__ __forceinline__ bool there(int i) const { return one[i].last >= 0; }
     __device__ __forceinline__ bool needs(int i, int k) const {
-        const KeyTiles &t = i ? one[1] : one[0];
-        return k < t.first || (k >= t.from && k <= t.last);
+        return k < one[i].first || (k >= one[i].from && k <= one[i].last);
+    }
+    __device__ __forceinline__ Pair(const Shape &s, const Work &w, bool by_heads) {
+        head[0] = by_heads ? 2 * w.unit : w.unit;
+        head[1] = head[0] + (by_heads ? 1 : 0);
+        q0[0] = w.first;
+        q0[1] = w.first + (by_heads ? 0 : kTile);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            one[i] = q0[i] < w.t.n ? key_tiles(s, q0[i], min(w.t.n, q0[i] + kTile), kTile) : KeyTiles{0, 0, -1};
+        both = one[0];
+        if (there(1)) {
+            both.last = one[1].last;
+            // the second tile's window begins later: what only its sinks need is needed by the first anyway
+            both.first = max(one[0].first, min(one[1].first, one[0].from));
+        }
+        count = both.count();
     }
 };
+
+// The block's r-th pair: neighbouring blocks take neighbouring pairs, in turn from both
+// ends, and the pairs with the most keys come first.
+__device__ __forceinline__ Work find_work(const Shape &s, int r, int units, int tiles, bool by_heads) {
+    Work w{};
+    w.unit = -1;
+    const int64_t item = static_cast<int64_t>(r) * gridDim.x + (r & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    if (item >= static_cast<int64_t>(units) * tiles) return w;
+    const int rows = by_heads ? kTile : 2 * kTile;
+    w.t = find_tile(s, static_cast<int>(item / units), rows, tiles);
+    if (w.t.n == 0 && w.t.head_rows + (s.T - w.t.tail_row) == 0) return w;  // no rows left to be zeroed
+    w.unit = static_cast<int>(item % units);
+    w.first = (w.t.tiles - 1 - w.t.tile) * rows;
+    return w;
+}
 
 __global__ void __launch_bounds__(kFwdThreads, 1)
     tc_forward_kernel(const __grid_constant__ CUtensorMap map, const Shape s, const __nv_bfloat16 *QKV, bool by_heads,
                       int tiles, __nv_bfloat16 *O, float *lse) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *ring = smem + 2 * kTileBytes;
-    uint64_t *full = reinterpret_cast<uint64_t *>(ring + kFwdStages * kTileBytes);
-    uint64_t *empty = full + kFwdStages, *q_full = empty + kFwdStages, *s_full = q_full + 1, *p_full = s_full + 2,
-             *o_full = p_full + 2, *drain = o_full + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    volatile int *odd = abort_flag + 1;  // [2] a tile has results that are not finite
-
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    FwdSmem &m = *reinterpret_cast<FwdSmem *>(smem_raw);
+    volatile int *abort_flag = &m.abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int units = by_heads ? s.n_q / 2 : s.n_q;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kFwdStages; ++i) {
-            ptx::mbar_init(&full[i], 1);
-            ptx::mbar_init(&empty[i], 1);
+            ptx::mbar_init(&m.full[i], 1);
+            ptx::mbar_init(&m.empty[i], 1);
         }
-        ptx::mbar_init(q_full, 1);
+        ptx::mbar_init(&m.q_full, 1);
+        ptx::mbar_init(&m.q_empty, 1);
         for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(&s_full[i], 1);
-            ptx::mbar_init(&p_full[i], 4);
-            ptx::mbar_init(&o_full[i], 1);
-            odd[i] = 0;
+            ptx::mbar_init(&m.s_full[i], 1);
+            ptx::mbar_init(&m.p_full[i][0], 4);
+            ptx::mbar_init(&m.p_full[i][1], 4);
+            ptx::mbar_init(&m.o_full[i], 1);
+            ptx::mbar_init(&m.o_empty[i], 4);
+            ptx::mbar_init(&m.work_full[i], 1);
+            ptx::mbar_init(&m.work_empty[i], kWorkReaders);
         }
-        ptx::mbar_init(drain, 1);
-        *abort_flag = 0;
+        ptx::mbar_init(&m.drain, 1);
+        m.abort_flag = 0;
         ptx::fence_mbar_init();
         ptx::prefetch_tmap(&map);
     }
-    grid_begin();
-    const int units = by_heads ? s.n_q / 2 : s.n_q;
-    const int unit = blockIdx.x % units;
-    const Tile t = find_tile(s, blockIdx.x / units, by_heads ? kTile : 2 * kTile, tiles);
-    const int head0 = by_heads ? 2 * unit : unit;
-    if (t.n == 0) {
-        forward_rest(s, t, head0, O, lse);
-        if (by_heads) forward_rest(s, t, head0 + 1, O, lse);
-        return;
-    }
-    // the last queries see the most keys: they come first
-    const int first = (t.tiles - 1 - t.tile) * (by_heads ? kTile : 2 * kTile);
-    const int head[2] = {head0, by_heads ? head0 + 1 : head0};
-    const int q0[2] = {first, by_heads ? first : first + kTile};
-    PairTiles kt;
-    bool there[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        there[i] = q0[i] < t.n;
-        kt.one[i] = there[i] ? key_tiles(s, q0[i], min(t.n, q0[i] + kTile), kTile) : KeyTiles{0, 0, -1};
-    }
-    kt.both = kt.one[0];
-    if (there[1]) {
-        kt.both.last = kt.one[1].last;
-        // the second tile's window begins later: what only its sinks need is needed by the first anyway
-        kt.both.first = max(kt.one[0].first, min(kt.one[1].first, kt.one[0].from));
-    }
-    const int count = kt.both.count();
-    const int kv = head0 / s.group;
-
+    if (threadIdx.x < 2 * kOddBits / 32) m.odd[threadIdx.x / (kOddBits / 32)][threadIdx.x % (kOddBits / 32)] = 0u;
     if (warp == 9) {
-        ptx::tmem_alloc(tmem_slot, kTmemCols);
+        ptx::tmem_alloc(&m.tmem_slot, kTmemCols);
         ptx::tmem_relinquish();
     }
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
+    grid_begin();
     constexpr uint32_t tmem = 0;  // all columns there are: they begin at 0
-    const int blocks = s.d > 64 ? 2 : 1;
+    // the next work of the warp that calls it, read by all its lanes; false at the end
+    int round = 0;
+    auto next_work = [&](Work &w) {
+        const int at = round & 1;
+        const uint32_t parity = (round >> 1) & 1;
+        ++round;
+        if (!wait_all(&m.work_full[at], parity, abort_flag, s.err, 28)) return false;
+        w = m.work[at];
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&m.work_empty[at]);
+        return w.unit >= 0;
+    };
 
     if (warp < 8) {
-        ptx::registers_up<208>();  // 2 x 208 + 88 = 3 x 168, the launch's
         // ------------------------------------------------ softmax
+        ptx::registers_up<208>();  // 2 x 208 + 88 = 3 x 168, the launch's
         const int i = warp >> 2;
-        const int my_q0 = i ? q0[1] : q0[0], my_head = i ? head[1] : head[0];
-        const int row = my_q0 + (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t s_tmem = tmem + i * 128 + lanes, o_tmem = tmem + 256 + i * 128 + lanes;
         const float c = s.scale * kLog2e;
-        const int wide = (width16(s.d) + 31) / 32;  // pieces of 32 columns of O
-        float m = -INFINITY, l = 0.0f;
-        uint32_t phase = 0;
-        bool alive = i ? there[1] : there[0], begun = false;
-        for (int u = 0; u < count && alive; ++u) {
-            const int k = kt.both.at(u);
-            if (!kt.needs(i, k)) continue;
-            alive = wait_all(&s_full[i], phase, abort_flag, s.err, 24);
-            phase ^= 1;
-            if (!alive) break;
-            ptx::tc_fence_after();
-            float x[4][32];
+        uint32_t phase = 0, o_phase = 0;
+        Work w;
+        while (next_work(w)) {
+            if (w.t.n == 0) {
+                const int head0 = by_heads ? 2 * w.unit : w.unit;
+                forward_rest(s, w.t, head0, O, lse);
+                if (by_heads) forward_rest(s, w.t, head0 + 1, O, lse);
+                continue;
+            }
+            const Pair pr(s, w, by_heads);
+            if (!(i ? pr.there(1) : pr.there(0))) continue;
+            const KeyTiles my = i ? pr.one[1] : pr.one[0];
+            const int my_q0 = i ? pr.q0[1] : pr.q0[0], my_head = i ? pr.head[1] : pr.head[0];
+            const int row = my_q0 + (warp & 3) * 32 + lane;
+            float top = -INFINITY, l = 0.0f;  // the maximum that P is relative to, times c; the sum of P
+            bool alive = true;
+            const int count = my.count();
+            for (int u = 0; u < count; ++u) {
+                const int k0 = my.at(u) * kTile;
+                alive = wait_all(&m.s_full[i], phase, abort_flag, s.err, 24);
+                if (!alive) break;
+                ptx::tc_fence_after();
+                float x[4][32];
 #pragma unroll
-            for (int b = 0; b < 4; ++b) ptx::tmem_ld32_async(s_tmem + b * 32, x[b]);
-            ptx::tmem_wait_ld();
+                for (int b = 0; b < 4; ++b) ptx::tmem_ld32_async(s_tmem + b * 32, x[b]);
+                ptx::tmem_wait_ld();
 #pragma unroll
-            for (int b = 0; b < 4; ++b) ptx::tmem_ready(x[b]);
-            const int k0 = k * kTile;
-            if (!all_seen(s, my_q0, my_q0 + kTile, k0, k0 + kTile)) {
-                const int hi = row - k0, lo = s.window ? hi - s.window + 1 : -kTile, sink = s.sinks - k0;
+                for (int b = 0; b < 4; ++b) ptx::tmem_ready(x[b]);
+                if (!all_seen(s, my_q0, my_q0 + kTile, k0, k0 + kTile)) {
+                    const int hi = row - k0, lo = s.window ? hi - s.window + 1 : -kTile, sink = s.sinks - k0;
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const uint32_t seen = visible(hi - b * 32, lo - b * 32, sink - b * 32);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) x[b][e] = seen & (1u << e) ? x[b][e] : -INFINITY;
+                    }
+                }
+                float high[4];
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
-                    const uint32_t seen = visible(hi - b * 32, lo - b * 32, sink - b * 32);
+                    high[b] = fmaxf(x[b][0], x[b][1]);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) x[b][e] = seen & (1u << e) ? x[b][e] : -INFINITY;
+                    for (int e = 2; e < 32; e += 2) high[b] = max3(high[b], x[b][e], x[b][e + 1]);
                 }
-            }
-            float top[4];
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                top[b] = x[b][0];
-#pragma unroll
-                for (int e = 1; e < 32; ++e) top[b] = fmaxf(top[b], x[b][e]);
-            }
-            const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
-            const bool raise = most > m + kRaise;  // the first one, too: m is -inf
-            if (__any_sync(0xffffffffu, raise)) {
-                const float to = fmaxf(m, most);
-                const float shrink = m == -INFINITY ? 0.0f : exp2_fast(m - to);
-                if (begun) {
-                    for (int b = 0; b < width16(s.d) / 16; ++b) ptx::tmem_scale16(o_tmem + b * 16, shrink);
+                const float most = fmaxf(max3(high[0], high[1], high[2]), high[3]) * c;
+                if (__any_sync(0xffffffffu, most > top + kRaise)) {  // the first one, too: top is -inf
+                    const float to = fmaxf(top, most);
+                    const float shrink = top == -INFINITY ? 0.0f : exp2_fast(top - to);
+                    if (u > 0) {
+                        for (int b = 0; b < width16(s.d) / 16; ++b) ptx::tmem_scale16(o_tmem + b * 16, shrink);
+                    }
+                    l *= shrink;
+                    top = to;
                 }
-                l *= shrink;
-                m = to;
-            }
-            begun = true;
-            const float at = m == -INFINITY ? 0.0f : m;  // no key seen yet: 2^-inf
-            float sum[4] = {};
+                const float at = top == -INFINITY ? 0.0f : top;  // no key seen yet: 2^-inf
+                float sum[4] = {};
+                // P by halves: the first is multiplied while the second is formed
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                uint32_t p[32];
+                for (int b = 0; b < 4; ++b) {
+                    uint32_t p[16];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    float v = x[2 * b + e / 16][2 * e % 32], w = x[2 * b + e / 16][2 * e % 32 + 1];
-                    scale2(v, w, c, -at);
-                    v = exp2_fast(v);
-                    w = exp2_fast(w);
-                    add2(sum[(e & 1) * 2], sum[(e & 1) * 2 + 1], v, w);
-                    p[e] = pack2(v, w);
+                    for (int e = 0; e < 16; ++e) {
+                        float v = x[b][2 * e], y = x[b][2 * e + 1];
+                        scale2(v, y, c, -at);
+                        v = exp2_fast(v);
+                        y = exp2_fast(y);
+                        add2(sum[(e & 1) * 2], sum[(e & 1) * 2 + 1], v, y);
+                        p[e] = pack2(v, y);
+                    }
+                    ptx::tmem_st16_async(s_tmem + b * 16, p);
+                    if (b & 1) {
+                        ptx::tmem_wait_st();
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(&m.p_full[i][b >> 1]);
+                    }
                 }
-                ptx::tmem_st32_async(s_tmem + b * 32, p);
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                phase ^= 1;
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            ptx::tmem_wait_st();
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&p_full[i]);
-        }
-        if (alive && wait_all(&o_full[i], 0, abort_flag, s.err, 25)) {
+            if (!alive || !wait_all(&m.o_full[i], o_phase, abort_flag, s.err, 25)) break;
+            o_phase ^= 1;
             ptx::tc_fence_after();
             const float inv = 1.0f / l;
-            const bool mine = row < t.n;
+            const bool mine = row < w.t.n;
             float check = l * 0.0f;  // stays 0 while everything is finite
-            __nv_bfloat16 *to = O + (t.row0 + row) * s.n_q * s.d + static_cast<int64_t>(my_head) * s.d;
-            for (int b = 0; b < wide; ++b) {
+            __nv_bfloat16 *to = O + (w.t.row0 + row) * s.n_q * s.d + static_cast<int64_t>(my_head) * s.d;
+            const int wide = (width16(s.d) + 31) / 32;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                if (b >= wide) break;
                 float o[32];
                 ptx::tmem_ld32_async(o_tmem + b * 32, o);
                 ptx::tmem_wait_ld();
                 ptx::tmem_ready(o);
+                if (b == wide - 1) {
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&m.o_empty[i]);
+                }
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
                     if (b * 32 + v * 8 >= s.d) continue;
@@ -337,93 +391,142 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     if (mine) store8(to + b * 32 + v * 8, r);
                 }
             }
-            if (mine) lse[my_head * s.T + t.row0 + row] = (m + log2f(l)) * kLn2;
-            if (mine && check != 0.0f) odd[i] = 1;  // NaN is not 0
+            if (mine) lse[my_head * s.T + w.t.row0 + row] = (top + log2f(l)) * kLn2;
+            if (mine && check != 0.0f)  // NaN is not 0
+                atomicOr(&m.odd[i][(round - 1) % kOddBits / 32], 1u << ((round - 1) & 31));
         }
     } else {
         ptx::registers_down<88>();
         if (warp == 8) {
             // ------------------------------------------------ loads
-            if (lane == 0) {
-                const uint32_t bytes = blocks * kBlockBytes;
-                ptx::mbar_arrive_expect_tx(q_full, (there[1] ? 2 : 1) * bytes);
+            const int blocks = s.d > 64 ? 2 : 1;
+            const uint32_t bytes = blocks * kBlockBytes;
+            int stage = 0;
+            uint32_t phase = 0, issued = 0, parity = 0, q_phase = 0;
+            bool ok = true, any = false;
+            auto load = [&](int at_head, int64_t row) {
+                ok = ok && wait_all(&m.empty[stage], phase ^ 1, abort_flag, s.err, 20);
+                if (!ok) return;
+                if (lane == 0) {
+                    ptx::mbar_arrive_expect_tx(&m.full[stage], bytes);
+                    load_tile(m.ring[stage], &map, &m.full[stage], at_head, row, blocks);
+                }
+                __syncwarp();
+                issued |= 1u << stage;
+                parity = (parity & ~(1u << stage)) | (phase << stage);
+                if (++stage == kFwdStages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            };
+            Work w;
+            while (ok && next_work(w)) {
+                if (w.t.n == 0) continue;
+                const Pair pr(s, w, by_heads);
+                const int kv = pr.head[0] / s.group;
+                ok = wait_all(&m.q_empty, q_phase ^ 1, abort_flag, s.err, 27);
+                if (!ok) break;
+                q_phase ^= 1;
+                any = true;
+                if (lane == 0) {
+                    ptx::mbar_arrive_expect_tx(&m.q_full, (pr.there(1) ? 2 : 1) * bytes);
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if (there[i]) load_tile(smem + i * kTileBytes, &map, q_full, s.q_head(head[i]), t.row0 + q0[i], blocks);
-                int stage = 0;
-                uint32_t phase = 0, issued = 0, parity = 0;
-                auto load = [&](int at_head, int k) {
-                    if (!ptx::mbar_wait(&empty[stage], phase ^ 1, abort_flag, s.err, 20)) return false;
-                    ptx::mbar_arrive_expect_tx(&full[stage], bytes);
-                    issued |= 1u << stage;
-                    parity = (parity & ~(1u << stage)) | (phase << stage);
-                    load_tile(ring + stage * kTileBytes, &map, &full[stage], at_head,
-                              t.row0 + static_cast<int64_t>(k) * kTile, blocks);
-                    if (++stage == kFwdStages) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
-                    return true;
-                };
+                    for (int i = 0; i < 2; ++i)
+                        if (pr.there(i))
+                            load_tile(m.q[i], &map, &m.q_full, s.q_head(pr.head[i]), w.t.row0 + pr.q0[i], blocks);
+                }
+                __syncwarp();
                 // in the order of their use: K of a tile, then V of the one before
-                for (int u = 0; u <= count; ++u) {
-                    if (u < count && !load(s.k_head(kv), kt.both.at(u))) break;
-                    if (u > 0 && !load(s.v_head(kv), kt.both.at(u - 1))) break;
+                for (int u = 0; u <= pr.count && ok; ++u) {
+                    if (u < pr.count)
+                        load(s.k_head(kv), w.t.row0 + static_cast<int64_t>(pr.both.at(u)) * kTile);
+                    if (u > 0) load(s.v_head(kv), w.t.row0 + static_cast<int64_t>(pr.both.at(u - 1)) * kTile);
                 }
-                if (*abort_flag) {
-                    ptx::mbar_wait_drain(q_full, 0);
-                    for (int i = 0; i < kFwdStages; ++i)
-                        if (issued & (1u << i)) ptx::mbar_wait_drain(&full[i], (parity >> i) & 1u);
-                }
+            }
+            if (*abort_flag && lane == 0) {
+                if (any) ptx::mbar_wait_drain(&m.q_full, q_phase ^ 1);
+                for (int i = 0; i < kFwdStages; ++i)
+                    if (issued & (1u << i)) ptx::mbar_wait_drain(&m.full[i], (parity >> i) & 1u);
             }
         } else if (warp == 9) {
             // ------------------------------------------------ products
-            {
-                const bool leader = ptx::elect_one();
-                const uint32_t idesc = idesc_weighted(s.d);
-                const uint32_t q_tile = ptx::smem_u32(smem), base = ptx::smem_u32(ring);
-                int stage = 0;
-                uint32_t phase = 0, p_phase[2] = {0, 0};
+            const bool leader = ptx::elect_one();
+            const uint32_t idesc = idesc_weighted(s.d);
+            const uint32_t q_tile = ptx::smem_u32(m.q[0]), base = ptx::smem_u32(m.ring[0]);
+            int stage = 0;
+            uint32_t phase = 0, p_phase[2] = {0, 0}, o_phase[2] = {0, 0}, q_phase = 0;
+            bool ok = true;
+            auto wait = [&](uint64_t *bar, uint32_t parity, uint32_t where) {
+                ok = ok && wait_all(bar, parity, abort_flag, s.err, where);
+            };
+            auto next = [&](int &at) {
+                wait(&m.full[stage], phase, 22);
+                at = stage;
+                if (++stage == kFwdStages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            };
+            Work w;
+            while (ok && next_work(w)) {
+                if (w.t.n == 0) continue;
+                const Pair pr(s, w, by_heads);
+                wait(&m.q_full, q_phase, 21);
+                q_phase ^= 1;
                 bool begun[2] = {false, false};
-                bool ok = wait_all(q_full, 0, abort_flag, s.err, 21);
-                auto next = [&](int &at) {
-                    ok = ok && wait_all(&full[stage], phase, abort_flag, s.err, 22);
-                    at = stage;
-                    if (++stage == kFwdStages) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
-                };
-                for (int u = 0; u <= count && ok; ++u) {
+                for (int u = 0; u <= pr.count && ok; ++u) {
                     int k_stage = 0, v_stage = 0;
-                    if (u < count) next(k_stage);
-                    if (u > 0 && ok) next(v_stage);
-                    ptx::tc_fence_after();
+                    if (u < pr.count) next(k_stage);
+                    if (u > 0) next(v_stage);
+                    if (!ok) break;
+                    const int k_now = u < pr.count ? pr.both.at(u) : -1, k_before = u > 0 ? pr.both.at(u - 1) : -1;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        if (!ok) break;
-                        if (u > 0 && kt.needs(i, kt.both.at(u - 1))) {
-                            if (!wait_all(&p_full[i], p_phase[i], abort_flag, s.err, 23)) {
-                                ok = false;
-                                break;
+                        if (u > 0 && pr.needs(i, k_before)) {
+                            if (!begun[i]) {
+                                wait(&m.o_empty[i], o_phase[i] ^ 1, 26);
+                                o_phase[i] ^= 1;
                             }
-                            p_phase[i] ^= 1;
+                            wait(&m.p_full[i][0], p_phase[i], 23);
+                            if (!ok) break;
                             ptx::tc_fence_after();
-                            mma_weighted(leader, tmem + 256 + i * 128, tmem + i * 128, 32, base + v_stage * kTileBytes, idesc,
-                                         begun[i]);
+                            mma_weighted<0, 4>(leader, tmem + 256 + i * 128, tmem + i * 128, 32,
+                                               base + v_stage * kTileBytes, idesc, begun[i]);
+                            wait(&m.p_full[i][1], p_phase[i], 23);
+                            if (!ok) break;
+                            ptx::tc_fence_after();
+                            mma_weighted<4, 8>(leader, tmem + 256 + i * 128, tmem + i * 128, 32,
+                                               base + v_stage * kTileBytes, idesc, true);
+                            p_phase[i] ^= 1;
                             begun[i] = true;
-                            if (kt.both.at(u - 1) == kt.one[i].last) commit(leader, &o_full[i]);
+                            if (k_before == pr.one[i].last) commit(leader, &m.o_full[i]);
                         }
-                        if (u < count && kt.needs(i, kt.both.at(u))) {
-                            mma_scores(leader, tmem + i * 128, q_tile + i * kTileBytes, base + k_stage * kTileBytes, s.d);
-                            commit(leader, &s_full[i]);
+                        if (u < pr.count && pr.needs(i, k_now)) {
+                            mma_scores(leader, tmem + i * 128, q_tile + i * kTileBytes, base + k_stage * kTileBytes,
+                                       s.d);
+                            commit(leader, &m.s_full[i]);
                         }
                     }
-                    if (u < count) commit(leader, &empty[k_stage]);
-                    if (u > 0) commit(leader, &empty[v_stage]);
+                    if (!ok) break;
+                    if (u < pr.count) commit(leader, &m.empty[k_stage]);
+                    if (u > 0) commit(leader, &m.empty[v_stage]);
+                    if (u == pr.count - 1) commit(leader, &m.q_empty);
                 }
-                commit(leader, drain);
-                ptx::mbar_wait_drain(drain, 0);
+            }
+            commit(leader, &m.drain);
+            if (lane == 0) ptx::mbar_wait_drain(&m.drain, 0);
+            __syncwarp();
+        } else if (warp == 10) {
+            // ------------------------------------------------ what comes next
+            for (int r = 0;; ++r) {
+                const Work w = find_work(s, r, units, tiles, by_heads);
+                if (!wait_all(&m.work_empty[r & 1], ((r >> 1) & 1) ^ 1, abort_flag, s.err, 29)) break;
+                if (lane == 0) {
+                    m.work[r & 1] = w;
+                    ptx::mbar_arrive(&m.work_full[r & 1]);
+                }
+                __syncwarp();
+                if (w.unit < 0) break;
             }
         }
     }
@@ -436,13 +539,27 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     }
     // What is masked has met 0 times its value: a tile with results that are not finite
     // is computed again where masked values are passed over.
+    uint32_t any = 0;
+    for (int i = 0; i < 2 * kOddBits / 32; ++i) any |= m.odd[i / (kOddBits / 32)][i % (kOddBits / 32)];
+    if (any == 0 || *abort_flag || threadIdx.x >= kPlainThreads) return;
+    // the bits lie where the tiles below do not reach
+    static_assert(offsetof(FwdSmem, odd) >= 4 * (3 * kRows * (kMaxDim + 4) + kRows * kPitchP), "room for plain tiles");
 #pragma unroll 1
-    for (int i = 0; i < 2; ++i) {
-        if (!odd[i] || *abort_flag || threadIdx.x >= kPlainThreads) continue;
-        const int begin = i ? q0[1] : q0[0];
-        for (int q = begin; q < min(t.n, begin + kTile); q += kRows) {
-            plain_sync();
-            plain_forward_tile(s, QKV, t.row0, t.n, q, i ? head[1] : head[0], O, lse, reinterpret_cast<float *>(smem));
+    for (int r = 0;; ++r) {
+        const Work w = find_work(s, r, units, tiles, by_heads);
+        if (w.unit < 0 || w.t.n == 0) break;
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+            if (!(m.odd[i][r % kOddBits / 32] & (1u << (r & 31)))) continue;
+            const Pair pr(s, w, by_heads);
+            if (!(i ? pr.there(1) : pr.there(0))) continue;
+            const int begin = i ? pr.q0[1] : pr.q0[0];
+#pragma unroll 1
+            for (int q = begin; q < min(w.t.n, begin + kTile); q += kRows) {
+                plain_sync();
+                plain_forward_tile(s, QKV, w.t.row0, w.t.n, q, i ? pr.head[1] : pr.head[0], O, lse,
+                                   reinterpret_cast<float *>(smem_raw));
+            }
         }
     }
 }
@@ -454,11 +571,12 @@ tpce_status tc_forward(const Shape &s, const void *QKV, void *O, float *lse, cud
         return fail(TPCE_ERR_CUDA, "%s: tensor map", name);
     const bool by_heads = s.group % 2 == 0;
     const int tiles = static_cast<int>(grid_tiles(s, by_heads ? kTile : 2 * kTile));
-    const unsigned blocks = static_cast<unsigned>(tiles) * (by_heads ? s.n_q / 2 : s.n_q);
+    const int64_t pairs = static_cast<int64_t>(tiles) * (by_heads ? s.n_q / 2 : s.n_q);
+    const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(pairs, num_sms()));
     cudaError_t e = allow_smem<tc_forward_kernel>();
     if (e != cudaSuccess) return fail_cuda(e, name);
     KernelTimer timer(name, stream);
-    e = step::launch(tc_forward_kernel, blocks, kFwdThreads, kFwdSmem, stream, map, s,
+    e = step::launch(tc_forward_kernel, blocks, kFwdThreads, sizeof(FwdSmem), stream, map, s,
                      static_cast<const __nv_bfloat16 *>(QKV), by_heads, tiles, static_cast<__nv_bfloat16 *>(O), lse);
     return e == cudaSuccess ? check_launch(name, stream) : fail_cuda(e, name);
 }

@@ -50,16 +50,17 @@ __device__ __forceinline__ void mma_scores(bool leader, uint32_t d_tmem, uint32_
     __syncwarp();
 }
 
-// D (+)= A X: A (bf16 in tensor memory, from a_tmem on, its second 64 columns of K
+// Steps FIRST .. LAST - 1 of sixteen rows of D (+)= A X: A (bf16 in tensor memory, from a_tmem on, its second 64 columns of K
 // second_half further) times a tile's 128 rows of d columns.
+template <int FIRST = 0, int LAST = kTile / 16>
 __device__ __forceinline__ void mma_weighted(bool leader, uint32_t d_tmem, uint32_t a_tmem, uint32_t second_half, uint32_t x_tile,
                                              uint32_t idesc, bool accumulate) {
     const uint64_t x = desc_cols(x_tile);
     if (leader) {
 #pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
+        for (int k = FIRST; k < LAST; ++k)
             ptx::mma_bf16_ts(d_tmem, a_tmem + (k & 3) * 8 + (k >> 2) * second_half, step_cols(x, k), idesc,
-                             (accumulate || k) ? 1u : 0u);
+                             (accumulate || k > FIRST) ? 1u : 0u);
     }
     __syncwarp();
 }
@@ -84,6 +85,11 @@ __device__ __forceinline__ void add2(float &x, float &y, float a, float b) {
         "add.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
         : "+f"(x), "+f"(y)
         : "f"(a), "f"(b));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
 }
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
