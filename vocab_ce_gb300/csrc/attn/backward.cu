@@ -280,15 +280,6 @@ __device__ __forceinline__ void ring_drain(const BwdSmem &m, int pos) {
         ptx::mbar_wait_drain(&m.ring.full[Ring::slot(p)], Ring::parity(p));
 }
 
-// 64 columns of this thread's row.
-__device__ __forceinline__ void read_half(uint32_t taddr, float (&x)[2][32]) {
-    ptx::tmem_ld32_async(taddr, x[0]);
-    ptx::tmem_ld32_async(taddr + 32, x[1]);
-    ptx::tmem_wait_ld();
-    ptx::tmem_ready(x[0]);
-    ptx::tmem_ready(x[1]);
-}
-
 // This thread's row of an accumulator, times f, from column c0 on (up to 64), to `to`; false if
 // something is not finite.
 __device__ __forceinline__ bool write_half(uint32_t taddr, float f, int c0, int d, __nv_bfloat16 *to, bool mine) {
@@ -389,13 +380,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             bool ok = wait_all(m.stay, 0, m.abort_flag, s.err, 32) && arrived(0);
             if (ok) {
                 ptx::tc_fence_after();
-                mma_scores(leader, t_s, k_tile, tile(0), s.d);
-                commit(leader, m.scores);
+                mma_scores(leader, t_s, k_tile, tile(0), s.d, m.scores);
                 ok = arrived(1);
             }
             if (ok) {
-                mma_scores(leader, t_dp, k_tile + kTileBytes, tile(1), s.d);
-                commit(leader, m.dots);
+                mma_scores(leader, t_dp, k_tile + kTileBytes, tile(1), s.d, m.dots);
             }
             for (int it = 0; it < count && ok; ++it) {
                 const int q = 2 * it, o = q + 1;
@@ -408,8 +397,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 if (more) {
                     ok = arrived(q + 2);
                     if (!ok) break;
-                    mma_scores(leader, t_s, k_tile, tile(q + 2), s.d);
-                    commit(leader, m.scores);
+                    mma_scores(leader, t_s, k_tile, tile(q + 2), s.d, m.scores);
                 }
                 ok = wait_all(m.ds_ready, it & 1, m.abort_flag, s.err, 34);
                 if (!ok) break;
@@ -419,8 +407,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 if (more) {
                     ok = arrived(o + 2);
                     if (!ok) break;
-                    mma_scores(leader, t_dp, k_tile + kTileBytes, tile(o + 2), s.d);
-                    commit(leader, m.dots);
+                    mma_scores(leader, t_dp, k_tile + kTileBytes, tile(o + 2), s.d, m.dots);
                 }
             }
             if (ok) commit(leader, m.done);
@@ -622,13 +609,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             bool ok = wait_all(m.stay, 0, m.abort_flag, s.err, 42) && arrived(0);
             if (ok) {
                 ptx::tc_fence_after();
-                mma_scores(leader, tmem, q_tile, tile(0), s.d);
-                commit(leader, &m.scores[0]);
+                mma_scores(leader, tmem, q_tile, tile(0), s.d, &m.scores[0]);
                 ok = arrived(1);
             }
             if (ok) {
-                mma_scores(leader, t_dp, q_tile + kTileBytes, tile(1), s.d);
-                commit(leader, m.dots);
+                mma_scores(leader, t_dp, q_tile + kTileBytes, tile(1), s.d, m.dots);
                 commit(leader, &m.ring.empty[Ring::slot(1)]);
             }
             for (int it = 0; it < count && ok; ++it) {
@@ -637,8 +622,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 if (more) {
                     ok = arrived(k + 2);
                     if (!ok) break;
-                    mma_scores(leader, tmem + ((it + 1) & 1) * 128, q_tile, tile(k + 2), s.d);
-                    commit(leader, &m.scores[(it + 1) & 1]);
+                    mma_scores(leader, tmem + ((it + 1) & 1) * 128, q_tile, tile(k + 2), s.d, &m.scores[(it + 1) & 1]);
                 }
                 ok = wait_all(m.ds_ready, it & 1, m.abort_flag, s.err, 43);
                 if (!ok) break;
@@ -648,8 +632,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 if (more) {
                     ok = arrived(k + 3);
                     if (!ok) break;
-                    mma_scores(leader, t_dp, q_tile + kTileBytes, tile(k + 3), s.d);
-                    commit(leader, m.dots);
+                    mma_scores(leader, t_dp, q_tile + kTileBytes, tile(k + 3), s.d, m.dots);
                     commit(leader, &m.ring.empty[Ring::slot(k + 3)]);
                 }
             }

@@ -137,11 +137,17 @@ tpce_status plain_forward(const Shape &s, const void *QKV, void *O, float *lse, 
 // ------------------------------------------------------------------ tiles on the tensor cores
 // One block an SM stays for all its work: pairs of 128-query tiles that read the same
 // keys, two heads of a group where it is even, else two neighbouring tiles of one head.
-// Twelve warps, of which the last only lends its registers:
-//   warps 0 - 3, 4 - 7   the softmax of tile 0 and of tile 1, a thread a query
-//   warp 8               loads: Q of a pair, K and V tiles through a ring
-//   warp 9               issues the products
-//   warp 10              finds the next pair, two ahead
+// Twenty warps:
+//   warps 0 - 7, 8 - 15  the softmax of tile 0 and of tile 1, two threads a query: the
+//                        first four warps have the first 64 keys of a tile, the next four
+//                        the others (with one thread a query the tensor cores waited for it)
+//   warp 16              loads: Q of a pair, K and V tiles through a ring
+//   warps 17, 18         issue the products of tile 0 and of tile 1, in turn: while one has
+//                        its products under way the other waits for what it needs next
+//                        (one warp for both left the tensor cores idle in its waits, a sixth
+//                        of the time; two that do not take turns split them when both have
+//                        something, so that neither tile's threads have theirs early)
+//   warp 19              finds the next pair, two ahead
 // so that the next pair's loads and first scores run while results are written.
 // Tensor memory: the scores S of both tiles (128 columns each; P overwrites the first
 // half of S in bf16) and both O. For each key tile
@@ -152,9 +158,10 @@ tpce_status plain_forward(const Shape &s, const void *QKV, void *O, float *lse, 
 // complete up to the keys before. A thread raises its maximum (and scales its O in
 // tensor memory) only when a score is more than 2^8 above it: P then stays below 2^8,
 // and O, l and lse are as exact.
-constexpr int kFwdThreads = 384, kFwdStages = 5;
+constexpr int kFwdThreads = 640, kFwdStages = 4;
+constexpr int kSoftWarps = 16, kLoadWarp = 16, kMmaWarp = 17, kWorkWarp = 19;
 constexpr float kRaise = 8.0f;  // in powers of two
-constexpr int kOddBits = 1024;
+constexpr int kOddBits = 512;
 
 // A pair of tiles, or rows without a sequence (n == 0), or the end (unit < 0).
 struct Work {
@@ -164,9 +171,11 @@ struct Work {
 struct FwdSmem {
     uint8_t q[2][kTileBytes];
     uint8_t ring[kFwdStages][kTileBytes];
+    uint8_t out[kSoftWarps][32 * 64];  // a warp's rows on their way to O, 32 columns at a time; its rows' maxima
+    float row_sum[kSoftWarps][32];
     uint64_t full[kFwdStages], empty[kFwdStages];
     uint64_t q_full, q_empty;
-    uint64_t s_full[2], p_full[2][2], o_full[2], o_empty[2];
+    uint64_t turn[2], s_full[2], p_full[2], o_full[2], o_empty[2];
     uint64_t work_full[2], work_empty[2];
     uint64_t drain;
     Work work[2];
@@ -175,7 +184,7 @@ struct FwdSmem {
     int abort_flag;
 };
 static_assert(sizeof(FwdSmem) <= static_cast<size_t>(kMaxSmem), "the ring fits");
-constexpr int kWorkReaders = 10;  // warps
+constexpr int kWorkReaders = kSoftWarps + 3;  // warps
 
 // The key tiles of both tiles together, and which of the two needs one.
 struct Pair {
@@ -229,26 +238,26 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kFwdStages; ++i) {
             ptx::mbar_init(&m.full[i], 1);
-            ptx::mbar_init(&m.empty[i], 1);
+            ptx::mbar_init(&m.empty[i], 2);
         }
         ptx::mbar_init(&m.q_full, 1);
-        ptx::mbar_init(&m.q_empty, 1);
+        ptx::mbar_init(&m.q_empty, 2);
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&m.s_full[i], 1);
-            ptx::mbar_init(&m.p_full[i][0], 4);
-            ptx::mbar_init(&m.p_full[i][1], 4);
+            ptx::mbar_init(&m.turn[i], 1);
+            ptx::mbar_init(&m.p_full[i], 8);
             ptx::mbar_init(&m.o_full[i], 1);
-            ptx::mbar_init(&m.o_empty[i], 4);
+            ptx::mbar_init(&m.o_empty[i], 8);
             ptx::mbar_init(&m.work_full[i], 1);
             ptx::mbar_init(&m.work_empty[i], kWorkReaders);
         }
-        ptx::mbar_init(&m.drain, 1);
+        ptx::mbar_init(&m.drain, 2);
         m.abort_flag = 0;
         ptx::fence_mbar_init();
         ptx::prefetch_tmap(&map);
     }
     if (threadIdx.x < 2 * kOddBits / 32) m.odd[threadIdx.x / (kOddBits / 32)][threadIdx.x % (kOddBits / 32)] = 0u;
-    if (warp == 9) {
+    if (warp == kMmaWarp) {
         ptx::tmem_alloc(&m.tmem_slot, kTmemCols);
         ptx::tmem_relinquish();
     }
@@ -270,13 +279,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         return w.unit >= 0;
     };
 
-    if (warp < 8) {
+    if (warp < kSoftWarps) {
         // ------------------------------------------------ softmax
-        ptx::registers_up<208>();  // 2 x 208 + 88 = 3 x 168, the launch's
-        const int i = warp >> 2;
+        ptx::registers_up<104>();  // 4 x 104 + 64 = 5 x 96, the launch's
+        const int i = warp >> 3, half = (warp >> 2) & 1, r = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t s_tmem = tmem + i * 128 + lanes, o_tmem = tmem + 256 + i * 128 + lanes;
+        const uint32_t s_tmem = tmem + i * 128 + lanes, o_tmem = tmem + 256 + i * 128 + half * 64 + lanes;
         const float c = s.scale * kLog2e;
+        // the two warps that share queries meet
+        auto meet = [&] { asm volatile("bar.sync %0, 64;" ::"r"(2 + i * 4 + (warp & 3)) : "memory"); };
         uint32_t phase = 0, o_phase = 0;
         Work w;
         while (next_work(w)) {
@@ -290,7 +301,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             if (!(i ? pr.there(1) : pr.there(0))) continue;
             const KeyTiles my = i ? pr.one[1] : pr.one[0];
             const int my_q0 = i ? pr.q0[1] : pr.q0[0], my_head = i ? pr.head[1] : pr.head[0];
-            const int row = my_q0 + (warp & 3) * 32 + lane;
+            const int row = my_q0 + r;
             float top = -INFINITY, l = 0.0f;  // the maximum that P is relative to, times c; the sum of P
             bool alive = true;
             const int count = my.count();
@@ -298,17 +309,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 const int k0 = my.at(u) * kTile;
                 alive = wait_all(&m.s_full[i], phase, abort_flag, s.err, 24);
                 if (!alive) break;
+                phase ^= 1;
                 ptx::tc_fence_after();
-                float x[4][32];
-#pragma unroll
-                for (int b = 0; b < 4; ++b) ptx::tmem_ld32_async(s_tmem + b * 32, x[b]);
-                ptx::tmem_wait_ld();
-#pragma unroll
-                for (int b = 0; b < 4; ++b) ptx::tmem_ready(x[b]);
+                float x[2][32];
+                read_half(s_tmem + half * 64, x);
                 if (!all_seen(s, my_q0, my_q0 + kTile, k0, k0 + kTile)) {
-                    const int hi = row - k0, lo = s.window ? hi - s.window + 1 : -kTile, sink = s.sinks - k0;
+                    const int hi = row - k0 - half * 64, lo = s.window ? hi - s.window + 1 : -kTile,
+                              sink = s.sinks - k0 - half * 64;
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) {
+                    for (int b = 0; b < 2; ++b) {
                         const uint32_t seen = visible(hi - b * 32, lo - b * 32, sink - b * 32);
 #pragma unroll
                         for (int e = 0; e < 32; ++e) x[b][e] = seen & (1u << e) ? x[b][e] : -INFINITY;
@@ -317,25 +326,30 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 float high[4];
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
-                    high[b] = fmaxf(x[b][0], x[b][1]);
+                    const float(&y)[32] = x[b >> 1];
+                    high[b] = fmaxf(y[(b & 1) * 16], y[(b & 1) * 16 + 1]);
 #pragma unroll
-                    for (int e = 2; e < 32; e += 2) high[b] = max3(high[b], x[b][e], x[b][e + 1]);
+                    for (int e = 2; e < 16; e += 2)
+                        high[b] = max3(high[b], y[(b & 1) * 16 + e], y[(b & 1) * 16 + e + 1]);
                 }
-                const float most = fmaxf(max3(high[0], high[1], high[2]), high[3]) * c;
+                float most = fmaxf(max3(high[0], high[1], high[2]), high[3]);
+                reinterpret_cast<float *>(m.out[warp])[lane] = most;
+                meet();  // and both have read S: P may overwrite it
+                most = fmaxf(most, reinterpret_cast<const float *>(m.out[warp ^ 4])[lane]) * c;
                 if (__any_sync(0xffffffffu, most > top + kRaise)) {  // the first one, too: top is -inf
                     const float to = fmaxf(top, most);
                     const float shrink = top == -INFINITY ? 0.0f : exp2_fast(top - to);
                     if (u > 0) {
-                        for (int b = 0; b < width16(s.d) / 16; ++b) ptx::tmem_scale16(o_tmem + b * 16, shrink);
+                        for (int b = half * 64; b < min(width16(s.d), half * 64 + 64); b += 16)
+                            ptx::tmem_scale16(o_tmem + b - half * 64, shrink);
                     }
                     l *= shrink;
                     top = to;
                 }
                 const float at = top == -INFINITY ? 0.0f : top;  // no key seen yet: 2^-inf
                 float sum[4] = {};
-                // P by halves: the first is multiplied while the second is formed
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
+                for (int b = 0; b < 2; ++b) {
                     uint32_t p[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
@@ -346,16 +360,19 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                         add2(sum[(e & 1) * 2], sum[(e & 1) * 2 + 1], v, y);
                         p[e] = pack2(v, y);
                     }
-                    ptx::tmem_st16_async(s_tmem + b * 16, p);
-                    if (b & 1) {
-                        ptx::tmem_wait_st();
-                        ptx::tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(&m.p_full[i][b >> 1]);
-                    }
+                    ptx::tmem_st16_async(s_tmem + half * 32 + b * 16, p);
                 }
+                ptx::tmem_wait_st();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&m.p_full[i]);
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                phase ^= 1;
+            }
+            if (alive) {
+                // of both halves (the next pair's sums come after its maxima, when these have been read)
+                m.row_sum[warp][lane] = l;
+                meet();
+                l = m.row_sum[warp & ~4][lane] + m.row_sum[warp | 4][lane];
             }
             if (!alive || !wait_all(&m.o_full[i], o_phase, abort_flag, s.err, 25)) break;
             o_phase ^= 1;
@@ -363,41 +380,50 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             const float inv = 1.0f / l;
             const bool mine = row < w.t.n;
             float check = l * 0.0f;  // stays 0 while everything is finite
-            __nv_bfloat16 *to = O + (w.t.row0 + row) * s.n_q * s.d + static_cast<int64_t>(my_head) * s.d;
-            const int wide = (width16(s.d) + 31) / 32;
+            // through shared memory, so that four lanes write 64 adjacent bytes of a row
+            uint8_t *out = m.out[warp];
+            const int rows = min(32, w.t.n - (row - lane));
+            __nv_bfloat16 *to = O + (w.t.row0 + row - lane) * s.n_q * s.d + static_cast<int64_t>(my_head) * s.d;
+            float o[2][32];
+            read_half(o_tmem, o);
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&m.o_empty[i]);
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                if (b >= wide) break;
-                float o[32];
-                ptx::tmem_ld32_async(o_tmem + b * 32, o);
-                ptx::tmem_wait_ld();
-                ptx::tmem_ready(o);
-                if (b == wide - 1) {
-                    ptx::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(&m.o_empty[i]);
-                }
+            for (int b = 0; b < 2; ++b) {
+                const int c0 = half * 64 + b * 32;
+                if (c0 >= s.d) break;
+                __syncwarp();  // the columns before have been read
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
-                    if (b * 32 + v * 8 >= s.d) continue;
                     float y[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        y[e] = o[v * 8 + e] * inv;
-                        check = fmaf(y[e], 0.0f, check);
+                    for (int e = 0; e < 8; ++e) y[e] = o[b][v * 8 + e] * inv;
+                    if (c0 + v * 8 < s.d) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) check = fmaf(y[e], 0.0f, check);
                     }
-                    Raw8<__nv_bfloat16> r;
-                    pack8(y, r);
-                    if (mine) store8(to + b * 32 + v * 8, r);
+                    Raw8<__nv_bfloat16> p;
+                    pack8(y, p);
+                    *reinterpret_cast<uint4 *>(out + lane * 64 + ((v ^ ((lane >> 1) & 3)) << 4)) = p.a;
+                }
+                __syncwarp();
+                const int v = lane & 3, col = c0 + v * 8;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int at = 8 * k + (lane >> 2);
+                    const uint4 y = *reinterpret_cast<const uint4 *>(out + at * 64 + ((v ^ ((at >> 1) & 3)) << 4));
+                    if (at < rows && col < s.d)
+                        *reinterpret_cast<uint4 *>(to + static_cast<int64_t>(at) * s.n_q * s.d + col) = y;
                 }
             }
-            if (mine) lse[my_head * s.T + w.t.row0 + row] = (top + log2f(l)) * kLn2;
+            if (mine && !half) lse[my_head * s.T + w.t.row0 + row] = (top + log2f(l)) * kLn2;
             if (mine && check != 0.0f)  // NaN is not 0
                 atomicOr(&m.odd[i][(round - 1) % kOddBits / 32], 1u << ((round - 1) & 31));
         }
     } else {
-        ptx::registers_down<88>();
-        if (warp == 8) {
+        ptx::registers_down<64>();
+        if (warp == kLoadWarp) {
             // ------------------------------------------------ loads
             const int blocks = s.d > 64 ? 2 : 1;
             const uint32_t bytes = blocks * kBlockBytes;
@@ -436,11 +462,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                             load_tile(m.q[i], &map, &m.q_full, s.q_head(pr.head[i]), w.t.row0 + pr.q0[i], blocks);
                 }
                 __syncwarp();
-                // in the order of their use: K of a tile, then V of the one before
+                // in the order of their use: K of a tile after V of the one before
                 for (int u = 0; u <= pr.count && ok; ++u) {
-                    if (u < pr.count)
-                        load(s.k_head(kv), w.t.row0 + static_cast<int64_t>(pr.both.at(u)) * kTile);
                     if (u > 0) load(s.v_head(kv), w.t.row0 + static_cast<int64_t>(pr.both.at(u - 1)) * kTile);
+                    if (u < pr.count) load(s.k_head(kv), w.t.row0 + static_cast<int64_t>(pr.both.at(u)) * kTile);
                 }
             }
             if (*abort_flag && lane == 0) {
@@ -448,75 +473,71 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 for (int i = 0; i < kFwdStages; ++i)
                     if (issued & (1u << i)) ptx::mbar_wait_drain(&m.full[i], (parity >> i) & 1u);
             }
-        } else if (warp == 9) {
+        } else if (warp < kWorkWarp) {
             // ------------------------------------------------ products
+            const int i = warp - kMmaWarp;
             const bool leader = ptx::elect_one();
             const uint32_t idesc = idesc_weighted(s.d);
-            const uint32_t q_tile = ptx::smem_u32(m.q[0]), base = ptx::smem_u32(m.ring[0]);
-            int stage = 0;
-            uint32_t phase = 0, p_phase[2] = {0, 0}, o_phase[2] = {0, 0}, q_phase = 0;
+            const uint32_t q_tile = ptx::smem_u32(m.q[0]) + i * kTileBytes, base = ptx::smem_u32(m.ring[0]);
+            const uint32_t t_s = tmem + i * 128, t_o = tmem + 256 + i * 128;
+            int pos = 0;  // tiles of the ring used so far
+            uint32_t p_phase = 0, o_phase = 0, q_phase = 0, turns = 0;
             bool ok = true;
             auto wait = [&](uint64_t *bar, uint32_t parity, uint32_t where) {
-                ok = ok && wait_all(bar, parity, abort_flag, s.err, where);
+                ok = ok && wait_all<true>(bar, parity, abort_flag, s.err, where);
             };
-            auto next = [&](int &at) {
-                wait(&m.full[stage], phase, 22);
-                at = stage;
-                if (++stage == kFwdStages) {
-                    stage = 0;
-                    phase ^= 1;
-                }
+            auto arrived = [&](int at) { wait(&m.full[at % kFwdStages], (at / kFwdStages) & 1, 22); };
+            auto tile = [&](int at) { return base + (at % kFwdStages) * kTileBytes; };
+            // each turn of tile 0 is followed by one of tile 1, with something to issue or without
+            auto my_turn = [&] {
+                if (i == 1 || turns > 0) wait(&m.turn[i], (i == 1 ? turns : turns - 1) & 1, 32);
+                ++turns;
             };
             Work w;
             while (ok && next_work(w)) {
                 if (w.t.n == 0) continue;
                 const Pair pr(s, w, by_heads);
+                const KeyTiles my = i ? pr.one[1] : pr.one[0];
                 wait(&m.q_full, q_phase, 21);
                 q_phase ^= 1;
-                bool begun[2] = {false, false};
+                bool begun = false;
                 for (int u = 0; u <= pr.count && ok; ++u) {
-                    int k_stage = 0, v_stage = 0;
-                    if (u < pr.count) next(k_stage);
-                    if (u > 0) next(v_stage);
-                    if (!ok) break;
+                    // V of the tile before at pos, then K of this one
+                    const int v_at = pos, k_at = u > 0 ? pos + 1 : pos;
                     const int k_now = u < pr.count ? pr.both.at(u) : -1, k_before = u > 0 ? pr.both.at(u - 1) : -1;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (u > 0 && pr.needs(i, k_before)) {
-                            if (!begun[i]) {
-                                wait(&m.o_empty[i], o_phase[i] ^ 1, 26);
-                                o_phase[i] ^= 1;
-                            }
-                            wait(&m.p_full[i][0], p_phase[i], 23);
-                            if (!ok) break;
-                            ptx::tc_fence_after();
-                            mma_weighted<0, 4>(leader, tmem + 256 + i * 128, tmem + i * 128, 32,
-                                               base + v_stage * kTileBytes, idesc, begun[i]);
-                            wait(&m.p_full[i][1], p_phase[i], 23);
-                            if (!ok) break;
-                            ptx::tc_fence_after();
-                            mma_weighted<4, 8>(leader, tmem + 256 + i * 128, tmem + i * 128, 32,
-                                               base + v_stage * kTileBytes, idesc, true);
-                            p_phase[i] ^= 1;
-                            begun[i] = true;
-                            if (k_before == pr.one[i].last) commit(leader, &m.o_full[i]);
-                        }
-                        if (u < pr.count && pr.needs(i, k_now)) {
-                            mma_scores(leader, tmem + i * 128, q_tile + i * kTileBytes, base + k_stage * kTileBytes,
-                                       s.d);
-                            commit(leader, &m.s_full[i]);
-                        }
+                    const bool sums = u > 0 && pr.needs(i, k_before), scores = u < pr.count && pr.needs(i, k_now);
+                    if (u < pr.count) arrived(k_at);
+                    if (u > 0) arrived(v_at);
+                    if (sums && !begun) {
+                        wait(&m.o_empty[i], o_phase ^ 1, 26);
+                        o_phase ^= 1;
+                    }
+                    my_turn();
+                    if (sums) {
+                        wait(&m.p_full[i], p_phase, 23);
+                        p_phase ^= 1;
                     }
                     if (!ok) break;
-                    if (u < pr.count) commit(leader, &m.empty[k_stage]);
-                    if (u > 0) commit(leader, &m.empty[v_stage]);
+                    ptx::tc_fence_after();
+                    if (sums) {
+                        mma_weighted(leader, t_o, t_s, 32, tile(v_at), idesc, begun);
+                        begun = true;
+                    }
+                    if (scores)
+                        mma_scores(leader, t_s, q_tile, tile(k_at), s.d, &m.s_full[i], &m.turn[i ^ 1]);
+                    else if (leader)
+                        ptx::mbar_arrive(&m.turn[i ^ 1]);
+                    if (u > 0 && k_before == my.last) commit(leader, &m.o_full[i]);
+                    if (u > 0) commit(leader, &m.empty[v_at % kFwdStages]);
+                    if (u < pr.count) commit(leader, &m.empty[k_at % kFwdStages]);
                     if (u == pr.count - 1) commit(leader, &m.q_empty);
+                    pos = u < pr.count ? k_at + 1 : v_at + 1;
                 }
             }
             commit(leader, &m.drain);
             if (lane == 0) ptx::mbar_wait_drain(&m.drain, 0);
             __syncwarp();
-        } else if (warp == 10) {
+        } else {
             // ------------------------------------------------ what comes next
             for (int r = 0;; ++r) {
                 const Work w = find_work(s, r, units, tiles, by_heads);
@@ -533,7 +554,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 
     ptx::tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == kMmaWarp) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, kTmemCols);
     }

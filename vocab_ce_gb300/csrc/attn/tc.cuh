@@ -37,17 +37,22 @@ __device__ __forceinline__ uint32_t visible(int hi, int lo, int sink) {
 }
 
 // All lanes of the warp that issues products call these; `leader` is the one that does.
-// D = A B^T over d: 128 x 128 scores of two tiles' rows.
-__device__ __forceinline__ void mma_scores(bool leader, uint32_t d_tmem, uint32_t a_tile, uint32_t b_tile, int d) {
+// D = A B^T over d: 128 x 128 scores of two tiles' rows, and the barrier that they arrive
+// on; `turn` is told when most of them are issued.
+__device__ __forceinline__ void mma_scores(bool leader, uint32_t d_tmem, uint32_t a_tile, uint32_t b_tile, int d,
+                                           uint64_t *done, uint64_t *turn = nullptr) {
     constexpr uint32_t kIdesc = ptx::idesc_f32acc(kTile, kTile, 1, false, false);
     const uint64_t a = desc_rows(a_tile), b = desc_rows(b_tile);
     const int steps = (d + 15) / 16;
     if (leader) {
 #pragma unroll
         for (int k = 0; k < kMaxDim / 16; ++k)
-            if (k < steps) ptx::mma_bf16(d_tmem, step_rows(a, k), step_rows(b, k), kIdesc, k != 0);
+            if (k < steps) {
+                if (turn && k == max(0, steps - 3)) ptx::mbar_arrive(turn);
+                ptx::mma_bf16(d_tmem, step_rows(a, k), step_rows(b, k), kIdesc, k != 0);
+            }
+        ptx::mma_commit(done);
     }
-    __syncwarp();
 }
 
 // Steps FIRST .. LAST - 1 of sixteen rows of D (+)= A X: A (bf16 in tensor memory, from a_tmem on, its second 64 columns of K
@@ -62,7 +67,6 @@ __device__ __forceinline__ void mma_weighted(bool leader, uint32_t d_tmem, uint3
             ptx::mma_bf16_ts(d_tmem, a_tmem + (k & 3) * 8 + (k >> 2) * second_half, step_cols(x, k), idesc,
                              (accumulate || k > FIRST) ? 1u : 0u);
     }
-    __syncwarp();
 }
 // the width of such a product: d, rounded up to what the instruction takes
 __host__ __device__ inline int width16(int d) { return (d + 15) / 16 * 16; }
@@ -101,16 +105,42 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// A wait of all lanes, which all get the same answer.
+// 64 columns of this thread's row.
+__device__ __forceinline__ void read_half(uint32_t taddr, float (&x)[2][32]) {
+    ptx::tmem_ld32_async(taddr, x[0]);
+    ptx::tmem_ld32_async(taddr + 32, x[1]);
+    ptx::tmem_wait_ld();
+    ptx::tmem_ready(x[0]);
+    ptx::tmem_ready(x[1]);
+}
+
+// A wait of all lanes, which all get the same answer; bounded as mbar_wait() is. Reading
+// the timer takes a while: with it in each round the many warps that wait do not crowd
+// out those that work, and the few that issue products look at it now and then only
+// (EAGER). (Sleeping in the try, trying from one lane, or trying without a pause cost the
+// forward 7, 20 and 13%.)
+template <bool EAGER = false>
 __device__ __forceinline__ bool wait_all(uint64_t *bar, uint32_t parity, volatile int *abort_flag, uint32_t *err,
                                          uint32_t where) {
-    const bool ok = ptx::mbar_wait(bar, parity, abort_flag, err, where);
-    return __all_sync(0xffffffffu, ok);
+    const uint32_t a = ptx::smem_u32(bar);
+    uint64_t since = 0;
+#pragma unroll 1
+    for (uint32_t i = 1; !__all_sync(0xffffffffu, ptx::mbar_try_wait(a, parity)); ++i) {
+        if (EAGER && i % 64 != 0) continue;
+        const uint64_t now = ptx::globaltimer();
+        if (since == 0) since = now;
+        if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
+        if (__any_sync(0xffffffffu, now - since > kWaitLimitNs)) {
+            ptx::record_error(err, kErrTimeout | (where << 8));
+            *abort_flag = 1;
+            return false;
+        }
+    }
+    return true;
 }
 
 __device__ __forceinline__ void commit(bool leader, uint64_t *bar) {
     if (leader) ptx::mma_commit(bar);
-    __syncwarp();
 }
 
 // The blocks of one head's tile of rows, into one stage.
