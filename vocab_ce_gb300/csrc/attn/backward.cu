@@ -196,10 +196,10 @@ __global__ void __launch_bounds__(kPlainThreads)
 
 // ------------------------------------------------------------------ tiles on the tensor cores
 // Twelve warps: 0 - 7 compute, a thread one row of a 128 x 128 tile and half of its
-// columns (warps 4 - 7 the second half); warp 8 loads; warp 9 issues the products;
-// warp 10 fetches the queries' statistics where they go by columns; the last one only
-// lends its registers. Products run in the order in which they are issued, which is
-// what keeps a buffer of tensor memory from being written while one before reads it.
+// columns (warps 4 - 7 the second half); warp 8 loads; warps 9 and 10 issue the
+// products (dQ: warp 9 alone); warp 11 fetches the queries' statistics where they go by
+// columns. A warp's products run in the order in which they are issued, which is what
+// keeps a buffer of tensor memory from being written while one before reads it.
 constexpr int kBwdThreads = 384, kBwdRing = 5;
 // the two tiles that stay, the ring, statistics of two tiles, barriers
 constexpr uint32_t kBwdSmem = 2 * kTileBytes + kBwdRing * kTileBytes + 2 * kTile * 8 + 256;
@@ -218,7 +218,7 @@ struct BwdSmem {
     uint8_t *tiles;  // the two that stay
     Ring ring;
     float *stats;  // [2][2][kTile]
-    uint64_t *stay, *scores, *dots, *p_ready, *ds_ready, *stats_full, *stats_empty, *done, *drain;
+    uint64_t *stay, *scores, *dots, *p_ready, *ds_ready, *stats_full, *stats_empty, *done, *drain, *turn;
     uint32_t *tmem_slot;
     volatile int *abort_flag, *odd;
     __device__ __forceinline__ explicit BwdSmem(uint8_t *raw) {
@@ -238,16 +238,19 @@ struct BwdSmem {
         stats_empty = b + 8;  // [2]
         done = b + 10;
         drain = b + 11;
-        tmem_slot = reinterpret_cast<uint32_t *>(b + 12);
+        turn = b + 12;  // [2]
+        tmem_slot = reinterpret_cast<uint32_t *>(b + 14);
         abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
         odd = abort_flag + 1;
     }
-    __device__ __forceinline__ void init() const {
+    // issuers: warps that issue products
+    __device__ __forceinline__ void init(int issuers) const {
         for (int i = 0; i < kBwdRing; ++i) {
             ptx::mbar_init(&ring.full[i], 1);
-            ptx::mbar_init(&ring.empty[i], 1);
+            ptx::mbar_init(&ring.empty[i], issuers);
         }
         for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&turn[i], 1);
             ptx::mbar_init(&scores[i], 1);
             ptx::mbar_init(&stats_full[i], 32);
             ptx::mbar_init(&stats_empty[i], 8);
@@ -256,8 +259,8 @@ struct BwdSmem {
         ptx::mbar_init(dots, 1);
         ptx::mbar_init(p_ready, 8);
         ptx::mbar_init(ds_ready, 8);
-        ptx::mbar_init(done, 1);
-        ptx::mbar_init(drain, 1);
+        ptx::mbar_init(done, issuers);
+        ptx::mbar_init(drain, issuers);
         *abort_flag = 0;
         *odd = 0;
         ptx::fence_mbar_init();
@@ -313,9 +316,11 @@ __device__ __forceinline__ bool write_half(uint32_t taddr, float f, int c0, int 
 //   S^T = K Q^T  ->  P^T = 2^(S^T c - lse)   ->  dV += P^T dO
 //   dP^T = V dO^T  ->  dS^T = P^T (dP^T - delta)  ->  dK += dS^T Q
 // Tensor memory: S^T, dP^T, dV, dK, 128 columns each; P^T and dS^T overwrite what they
-// are made of, in bf16, each half of the columns its own place. In the order
-//   S(0) dP(0) | dV(0) S(1) dK(0) dP(1) | dV(1) S(2) ..
-// two products are under way while the threads form P or dS.
+// are made of, in bf16, each half of the columns its own place. One warp issues S and
+// dV, the other dP and dK, in turn:
+//   S(0), dP(0), dV(0) S(1), dK(0) dP(1), dV(1) S(2), ..
+// so that two products are under way while the threads form P or dS, and each warp
+// waits for what it needs during the other's.
 __global__ void __launch_bounds__(kBwdThreads, 1)
     tc_dkv_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap map_do, const Shape s,
                   const __nv_bfloat16 *QKV, const __nv_bfloat16 *dO, const float2 *stats, int tiles,
@@ -324,7 +329,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const BwdSmem m(smem_raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        m.init();
+        m.init(2);
         ptx::prefetch_tmap(&map);
         ptx::prefetch_tmap(&map_do);
     }
@@ -369,52 +374,44 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 }
             if (*m.abort_flag) ring_drain(m, pos);
         }
-    } else if (warp == 9) {
-        {
-            const bool leader = ptx::elect_one();
-            const uint32_t idesc = idesc_weighted(s.d), base = ptx::smem_u32(m.ring.at), k_tile = ptx::smem_u32(m.tiles);
-            auto tile = [&](int pos) { return base + Ring::slot(pos) * kTileBytes; };
-            auto arrived = [&](int pos) {
-                return wait_all(&m.ring.full[Ring::slot(pos)], Ring::parity(pos), m.abort_flag, s.err, 31);
-            };
-            bool ok = wait_all(m.stay, 0, m.abort_flag, s.err, 32) && arrived(0);
-            if (ok) {
-                ptx::tc_fence_after();
-                mma_scores(leader, t_s, k_tile, tile(0), s.d, m.scores);
-                ok = arrived(1);
-            }
-            if (ok) {
-                mma_scores(leader, t_dp, k_tile + kTileBytes, tile(1), s.d, m.dots);
-            }
-            for (int it = 0; it < count && ok; ++it) {
-                const int q = 2 * it, o = q + 1;
-                const bool more = it + 1 < count;
-                ok = wait_all(m.p_ready, it & 1, m.abort_flag, s.err, 33);
-                if (!ok) break;
-                ptx::tc_fence_after();
-                mma_weighted(leader, t_dv, t_s, 64, tile(o), idesc, it > 0);
-                commit(leader, &m.ring.empty[Ring::slot(o)]);
-                if (more) {
-                    ok = arrived(q + 2);
-                    if (!ok) break;
-                    mma_scores(leader, t_s, k_tile, tile(q + 2), s.d, m.scores);
-                }
-                ok = wait_all(m.ds_ready, it & 1, m.abort_flag, s.err, 34);
-                if (!ok) break;
-                ptx::tc_fence_after();
-                mma_weighted(leader, t_dk, t_dp, 64, tile(q), idesc, it > 0);
-                commit(leader, &m.ring.empty[Ring::slot(q)]);
-                if (more) {
-                    ok = arrived(o + 2);
-                    if (!ok) break;
-                    mma_scores(leader, t_dp, k_tile + kTileBytes, tile(o + 2), s.d, m.dots);
-                }
-            }
-            if (ok) commit(leader, m.done);
-            commit(leader, m.drain);
-            ptx::mbar_wait_drain(m.drain, 0);
+    } else if (warp == 9 || warp == 10) {
+        // step `it`: the sum with tile it - 1, then the scores (or dots) of tile it
+        const int i = warp - 9;
+        const bool leader = ptx::elect_one();
+        const uint32_t idesc = idesc_weighted(s.d), base = ptx::smem_u32(m.ring.at);
+        const uint32_t stays = ptx::smem_u32(m.tiles) + i * kTileBytes;  // K, V
+        const uint32_t t_in = i ? t_dp : t_s, t_sum = i ? t_dk : t_dv;
+        uint64_t *const ready = i ? m.ds_ready : m.p_ready, *const out = i ? m.dots : m.scores;
+        bool ok = true;
+        auto wait = [&](uint64_t *bar, uint32_t parity, uint32_t where) {
+            ok = ok && wait_all<true>(bar, parity, m.abort_flag, s.err, where);
+        };
+        auto arrived = [&](int pos) { wait(&m.ring.full[Ring::slot(pos)], Ring::parity(pos), 31); };
+        auto tile = [&](int pos) { return base + Ring::slot(pos) * kTileBytes; };
+        wait(m.stay, 0, 32);
+        for (int it = 0; it <= count && ok; ++it) {
+            // Q of a tile is at 2 it, dO at 2 it + 1; the sums take dO for dV and Q for dK
+            const int in = 2 * it + i, of = 2 * (it - 1) + (i ^ 1);
+            const bool scores = it < count, sums = it > 0;
+            if (scores) arrived(in);
+            if (sums) arrived(of);
+            if (i == 1 || it > 0) wait(&m.turn[i], (i == 1 ? it : it - 1) & 1, 33);
+            if (sums) wait(ready, (it - 1) & 1, 34);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            if (sums) mma_weighted(leader, t_sum, t_in, 64, tile(of), idesc, it > 1);
+            if (scores)
+                mma_scores(leader, t_in, stays, tile(in), s.d, out, &m.turn[i ^ 1]);
+            else if (leader)
+                ptx::mbar_arrive(&m.turn[i ^ 1]);
+            if (sums) commit(leader, &m.ring.empty[Ring::slot(of)]);
+            if (scores) commit(leader, &m.ring.empty[Ring::slot(in)]);
         }
-    } else if (warp == 10) {
+        if (ok) commit(leader, m.done);
+        commit(leader, m.drain);
+        if (lane == 0) ptx::mbar_wait_drain(m.drain, 0);
+        __syncwarp();
+    } else if (warp == 11) {
         // the statistics of a tile, when the one two before has been used; queries past the end: P = 2^-inf
         int it = 0;
         bool ok = true;
@@ -548,8 +545,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 // dQ of 128 queries of a head. Per tile of 128 keys, with the queries as rows:
 //   S = Q K^T, dP = dO V^T  ->  dS = 2^(S c - lse) (dP - delta)  ->  dQ += dS K
 // Tensor memory: two S (dS overwrites the one that it is made of), dP, dQ. In the order
-//   S(0) dP(0) | S(1) dQ(0) dP(1) | S(2) dQ(1) ..
-// the next S is under way while the threads form dS, and P is formed during dQ and dP.
+//   S(0) dP(0) | S(1) dP(1) dQ(0) | S(2) dP(2) dQ(1) | ..
+// dP of the next keys is begun as soon as the threads have read the one before, and P
+// is formed of the next S before dP has come.
 __global__ void __launch_bounds__(kBwdThreads, 1)
     tc_dq_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap map_do, const Shape s,
                  const __nv_bfloat16 *QKV, const __nv_bfloat16 *dO, const float2 *stats, int tiles,
@@ -558,7 +556,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const BwdSmem m(smem_raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        m.init();
+        m.init(1);
         ptx::prefetch_tmap(&map);
         ptx::prefetch_tmap(&map_do);
     }
@@ -604,7 +602,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const uint32_t idesc = idesc_weighted(s.d), base = ptx::smem_u32(m.ring.at), q_tile = ptx::smem_u32(m.tiles);
             auto tile = [&](int pos) { return base + Ring::slot(pos) * kTileBytes; };
             auto arrived = [&](int pos) {
-                return wait_all(&m.ring.full[Ring::slot(pos)], Ring::parity(pos), m.abort_flag, s.err, 41);
+                return wait_all<true>(&m.ring.full[Ring::slot(pos)], Ring::parity(pos), m.abort_flag, s.err, 41);
             };
             bool ok = wait_all(m.stay, 0, m.abort_flag, s.err, 42) && arrived(0);
             if (ok) {
@@ -618,23 +616,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
             for (int it = 0; it < count && ok; ++it) {
                 const int k = 2 * it;
-                const bool more = it + 1 < count;
-                if (more) {
+                if (it + 1 < count) {
                     ok = arrived(k + 2);
                     if (!ok) break;
                     mma_scores(leader, tmem + ((it + 1) & 1) * 128, q_tile, tile(k + 2), s.d, &m.scores[(it + 1) & 1]);
+                    ok = arrived(k + 3) && wait_all<true>(m.p_ready, it & 1, m.abort_flag, s.err, 43);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    mma_scores(leader, t_dp, q_tile + kTileBytes, tile(k + 3), s.d, m.dots);
+                    commit(leader, &m.ring.empty[Ring::slot(k + 3)]);
                 }
-                ok = wait_all(m.ds_ready, it & 1, m.abort_flag, s.err, 43);
+                ok = wait_all<true>(m.ds_ready, it & 1, m.abort_flag, s.err, 47);
                 if (!ok) break;
                 ptx::tc_fence_after();
                 mma_weighted(leader, t_dq, tmem + (it & 1) * 128, 64, tile(k), idesc, it > 0);
                 commit(leader, &m.ring.empty[Ring::slot(k)]);
-                if (more) {
-                    ok = arrived(k + 3);
-                    if (!ok) break;
-                    mma_scores(leader, t_dp, q_tile + kTileBytes, tile(k + 3), s.d, m.dots);
-                    commit(leader, &m.ring.empty[Ring::slot(k + 3)]);
-                }
             }
             if (ok) commit(leader, m.done);
             commit(leader, m.drain);
@@ -674,6 +670,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             if (!alive) break;
             ptx::tc_fence_after();
             read_half(t_dp + lanes + half * 64, y);
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(m.p_ready);  // dP has been read
             uint32_t p[32];
 #pragma unroll
             for (int b = 0; b < 2; ++b)
