@@ -429,8 +429,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 float *to = m.stats + (it & 1) * 2 * kTile;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    to[e * 32 + lane] = v[e].x;
-                    to[kTile + e * 32 + lane] = v[e].y;
+                    to[e * 32 + lane] = -v[e].x;  // both are subtracted
+                    to[kTile + e * 32 + lane] = -v[e].y;
                 }
                 ptx::mbar_arrive(&m.stats_full[it & 1]);
             }
@@ -462,20 +462,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             read_half(t_s + lanes + half * 64, x);
             uint32_t p[32];
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+            for (int b = 0; b < 2; ++b) {
 #pragma unroll
                 for (int e = 0; e < 32; e += 4) {
-                    const float4 l4 = *reinterpret_cast<const float4 *>(lse + b * 32 + e);
-                    const float l[4] = {l4.x, l4.y, l4.z, l4.w};
-#pragma unroll
-                    for (int f = 0; f < 4; ++f) {
-                        float &v = x[b][e + f];
-                        v = exp2_fast(fmaf(v, c, -l[f]));
-                        if (masked) v = seen[b] & (1u << (e + f)) ? v : 0.0f;
-                    }
-                    p[(b * 32 + e) / 2] = pack2(x[b][e], x[b][e + 1]);
-                    p[(b * 32 + e) / 2 + 1] = pack2(x[b][e + 2], x[b][e + 3]);
+                    const float4 l = *reinterpret_cast<const float4 *>(lse + b * 32 + e);
+                    float(&y)[32] = x[b];
+                    scale2(y[e], y[e + 1], c, l.x, l.y);
+                    scale2(y[e + 2], y[e + 3], c, l.z, l.w);
                 }
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[b][e] = exp2_fast(x[b][e]);
+                if (masked) keep(x[b], seen[b], 0.0f);
+                pack32(x[b], p + b * 16);
+            }
             ptx::tmem_st32_async(t_s + lanes + half * 64, p);
             ptx::tmem_wait_st();
             ptx::tc_fence_before();
@@ -487,21 +486,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             float y[2][32];
             read_half(t_dp + lanes + half * 64, y);
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+            for (int b = 0; b < 2; ++b) {
 #pragma unroll
                 for (int e = 0; e < 32; e += 4) {
-                    const float4 d4 = *reinterpret_cast<const float4 *>(delta + b * 32 + e);
-                    const float dl[4] = {d4.x, d4.y, d4.z, d4.w};
-#pragma unroll
-                    for (int f = 0; f < 4; ++f) {
-                        float &v = y[b][e + f];
-                        v = x[b][e + f] * (v - dl[f]);
-                        // what is masked may be infinite here
-                        if (masked) v = seen[b] & (1u << (e + f)) ? v : 0.0f;
-                    }
-                    p[(b * 32 + e) / 2] = pack2(y[b][e], y[b][e + 1]);
-                    p[(b * 32 + e) / 2 + 1] = pack2(y[b][e + 2], y[b][e + 3]);
+                    const float4 d = *reinterpret_cast<const float4 *>(delta + b * 32 + e);
+                    float(&v)[32] = y[b];
+                    add2(v[e], v[e + 1], d.x, d.y);
+                    add2(v[e + 2], v[e + 3], d.z, d.w);
+                    step::mul2(v[e], v[e + 1], x[b][e], x[b][e + 1]);
+                    step::mul2(v[e + 2], v[e + 3], x[b][e + 2], x[b][e + 3]);
                 }
+                if (masked) keep(y[b], seen[b], 0.0f);  // what is masked may be infinite here
+                pack32(y[b], p + b * 16);
+            }
             ptx::tmem_st32_async(t_dp + lanes + half * 64, p);
             ptx::tmem_wait_st();
             ptx::tc_fence_before();
@@ -662,7 +659,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
-                    scale2(x[b][e], x[b][e + 1], c, -st.x);
+                    scale2(x[b][e], x[b][e + 1], c, -st.x, -st.x);
                     x[b][e] = exp2_fast(x[b][e]);
                     x[b][e + 1] = exp2_fast(x[b][e + 1]);
                 }
@@ -675,17 +672,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             if (lane == 0) ptx::mbar_arrive(m.p_ready);  // dP has been read
             uint32_t p[32];
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+            for (int b = 0; b < 2; ++b) {
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
-#pragma unroll
-                    for (int f = 0; f < 2; ++f) {
-                        float &v = y[b][e + f];
-                        v = x[b][e + f] * (v - st.y);
-                        if (masked) v = seen[b] & (1u << (e + f)) ? v : 0.0f;
-                    }
-                    p[(b * 32 + e) / 2] = pack2(y[b][e], y[b][e + 1]);
+                    add2(y[b][e], y[b][e + 1], -st.y, -st.y);
+                    step::mul2(y[b][e], y[b][e + 1], x[b][e], x[b][e + 1]);
                 }
+                if (masked) keep(y[b], seen[b], 0.0f);
+                pack32(y[b], p + b * 16);
+            }
             ptx::tmem_st32_async(t_s, p);
             ptx::tmem_wait_st();
             ptx::tc_fence_before();

@@ -317,11 +317,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     const int hi = row - k0 - half * 64, lo = s.window ? hi - s.window + 1 : -kTile,
                               sink = s.sinks - k0 - half * 64;
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        const uint32_t seen = visible(hi - b * 32, lo - b * 32, sink - b * 32);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) x[b][e] = seen & (1u << e) ? x[b][e] : -INFINITY;
-                    }
+                    for (int b = 0; b < 2; ++b)
+                        keep(x[b], visible(hi - b * 32, lo - b * 32, sink - b * 32), -INFINITY);
                 }
                 float high[4];
 #pragma unroll
@@ -354,7 +351,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         float v = x[b][2 * e], y = x[b][2 * e + 1];
-                        scale2(v, y, c, -at);
+                        scale2(v, y, c, -at, -at);
                         v = exp2_fast(v);
                         y = exp2_fast(y);
                         add2(sum[(e & 1) * 2], sum[(e & 1) * 2 + 1], v, y);

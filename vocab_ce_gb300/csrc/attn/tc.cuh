@@ -75,13 +75,13 @@ __device__ __forceinline__ uint32_t idesc_weighted(int d) {
            (static_cast<uint32_t>((width16(d) - 16) >> 3) << 17);
 }
 
-// (x, y) = (x, y) * f + (a, a); 2^x to 2 units in the last place, results below 2^-126 zero
-__device__ __forceinline__ void scale2(float &x, float &y, float f, float a) {
+// (x, y) = (x, y) * f + (a, b); 2^x to 2 units in the last place, results below 2^-126 zero
+__device__ __forceinline__ void scale2(float &x, float &y, float f, float a, float b) {
     asm("{\n\t.reg .b64 p, q, r;\n\t"
-        "mov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %2};\n\tmov.b64 r, {%3, %3};\n\t"
+        "mov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %2};\n\tmov.b64 r, {%3, %4};\n\t"
         "fma.rn.f32x2 p, p, q, r;\n\tmov.b64 {%0, %1}, p;\n\t}"
         : "+f"(x), "+f"(y)
-        : "f"(f), "f"(a));
+        : "f"(f), "f"(a), "f"(b));
 }
 __device__ __forceinline__ void add2(float &x, float &y, float a, float b) {
     asm("{\n\t.reg .b64 p, q;\n\t"
@@ -112,6 +112,17 @@ __device__ __forceinline__ void read_half(uint32_t taddr, float (&x)[2][32]) {
     ptx::tmem_wait_ld();
     ptx::tmem_ready(x[0]);
     ptx::tmem_ready(x[1]);
+}
+
+// The columns of 32 that are not in `seen` become `other`. One branch around all of it
+// where a tile may be visible as a whole: one a value makes a phase three times as long.
+__device__ __forceinline__ void keep(float (&x)[32], uint32_t seen, float other) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) x[e] = seen & (1u << e) ? x[e] : other;
+}
+__device__ __forceinline__ void pack32(const float (&x)[32], uint32_t *p) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) p[e] = pack2(x[2 * e], x[2 * e + 1]);
 }
 
 // A wait of all lanes, which all get the same answer; bounded as mbar_wait() is. Reading
