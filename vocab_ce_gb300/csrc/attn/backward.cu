@@ -267,13 +267,15 @@ struct BwdSmem {
     }
 };
 
-// Loads one tile into the next place of the ring; false when a wait gave up.
-__device__ __forceinline__ bool ring_load(const BwdSmem &m, int pos, const CUtensorMap *map, int head, int64_t row,
-                                          int blocks, uint32_t *err) {
+// Loads one tile into the next place of the ring (all lanes call it); false when a wait gave up.
+__device__ __forceinline__ bool ring_load(const BwdSmem &m, bool leader, int pos, const CUtensorMap *map, int head,
+                                          int64_t row, int blocks, uint32_t *err) {
     const int slot = Ring::slot(pos);
-    if (!ptx::mbar_wait(&m.ring.empty[slot], Ring::parity(pos) ^ 1, m.abort_flag, err, 30)) return false;
-    ptx::mbar_arrive_expect_tx(&m.ring.full[slot], blocks * kBlockBytes);
-    load_tile(m.ring.at + slot * kTileBytes, map, &m.ring.full[slot], head, row, blocks);
+    if (!wait_all<true>(&m.ring.empty[slot], Ring::parity(pos) ^ 1, m.abort_flag, err, 30)) return false;
+    if (leader) {
+        ptx::mbar_arrive_expect_tx(&m.ring.full[slot], blocks * kBlockBytes);
+        load_tile(m.ring.at + slot * kTileBytes, map, &m.ring.full[slot], head, row, blocks);
+    }
     return true;
 }
 // After a wait gave up: the loads of the positions before `pos` land.
@@ -357,19 +359,22 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const int blocks = s.d > 64 ? 2 : 1;
 
     if (warp == 8) {
-        if (lane == 0) {
-            ptx::mbar_arrive_expect_tx(m.stay, 2 * blocks * kBlockBytes);
-            load_tile(m.tiles, &map, m.stay, s.k_head(kv), t.row0 + k0, blocks);
-            load_tile(m.tiles + kTileBytes, &map, m.stay, s.v_head(kv), t.row0 + k0, blocks);
+        {
+            const bool leader = ptx::elect_one();
+            if (leader) {
+                ptx::mbar_arrive_expect_tx(m.stay, 2 * blocks * kBlockBytes);
+                load_tile(m.tiles, &map, m.stay, s.k_head(kv), t.row0 + k0, blocks);
+                load_tile(m.tiles + kTileBytes, &map, m.stay, s.v_head(kv), t.row0 + k0, blocks);
+            }
             int pos = 0;
             bool ok = true;
             for (int g = 0; g < s.group && ok; ++g)
                 for (int q = 0; q < of_head && ok; ++q) {
                     const int64_t row = t.row0 + k0 + q * kTile;
                     const int h = kv * s.group + g;
-                    ok = ring_load(m, pos, &map, s.q_head(h), row, blocks, s.err);
+                    ok = ring_load(m, leader, pos, &map, s.q_head(h), row, blocks, s.err);
                     pos += ok;
-                    ok = ok && ring_load(m, pos, &map_do, h, row, blocks, s.err);
+                    ok = ok && ring_load(m, leader, pos, &map_do, h, row, blocks, s.err);
                     pos += ok;
                 }
             if (*m.abort_flag) ring_drain(m, pos);
@@ -446,13 +451,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const int q0 = k0 + q * kTile;
             q = q + 1 == of_head ? 0 : q + 1;
             const bool masked = !all_seen(s, q0, q0 + kTile, k0, k0 + kTile) || q0 + kTile > t.n;
-            uint32_t seen[2];
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                // queries from the key's own on, below its limit
+            // queries from the key's own on, below its limit
+            auto seen = [&](int b) {
                 const int at = q0 + half * 64 + b * 32;
-                seen[b] = masked ? below(limit - at) & ~below(key - at) : 0xffffffffu;
-            }
+                return below(limit - at) & ~below(key - at);
+            };
             const float *lse = m.stats + (it & 1) * 2 * kTile + half * 64, *delta = lse + kTile;
             alive = wait_all(&m.stats_full[it & 1], (it >> 1) & 1, m.abort_flag, s.err, 36) &&
                     wait_all(m.scores, it & 1, m.abort_flag, s.err, 37);
@@ -472,7 +475,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 }
 #pragma unroll
                 for (int e = 0; e < 32; ++e) x[b][e] = exp2_fast(x[b][e]);
-                if (masked) keep(x[b], seen[b], 0.0f);
+                if (masked) keep(x[b], seen(b), 0.0f);
                 pack32(x[b], p + b * 16);
             }
             ptx::tmem_st32_async(t_s + lanes + half * 64, p);
@@ -496,7 +499,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     step::mul2(v[e], v[e + 1], x[b][e], x[b][e + 1]);
                     step::mul2(v[e + 2], v[e + 3], x[b][e + 2], x[b][e + 3]);
                 }
-                if (masked) keep(y[b], seen[b], 0.0f);  // what is masked may be infinite here
+                if (masked) keep(y[b], seen(b), 0.0f);  // what is masked may be infinite here
                 pack32(y[b], p + b * 16);
             }
             ptx::tmem_st32_async(t_dp + lanes + half * 64, p);
@@ -578,17 +581,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const int blocks = s.d > 64 ? 2 : 1;
 
     if (warp == 8) {
-        if (lane == 0) {
-            ptx::mbar_arrive_expect_tx(m.stay, 2 * blocks * kBlockBytes);
-            load_tile(m.tiles, &map, m.stay, s.q_head(h), t.row0 + q0, blocks);
-            load_tile(m.tiles + kTileBytes, &map_do, m.stay, h, t.row0 + q0, blocks);
+        {
+            const bool leader = ptx::elect_one();
+            if (leader) {
+                ptx::mbar_arrive_expect_tx(m.stay, 2 * blocks * kBlockBytes);
+                load_tile(m.tiles, &map, m.stay, s.q_head(h), t.row0 + q0, blocks);
+                load_tile(m.tiles + kTileBytes, &map_do, m.stay, h, t.row0 + q0, blocks);
+            }
             int pos = 0;
             bool ok = true;
             for (int u = 0; u < count && ok; ++u) {
                 const int64_t row = t.row0 + static_cast<int64_t>(kt.at(u)) * kTile;
-                ok = ring_load(m, pos, &map, s.k_head(kv), row, blocks, s.err);
+                ok = ring_load(m, leader, pos, &map, s.k_head(kv), row, blocks, s.err);
                 pos += ok;
-                ok = ok && ring_load(m, pos, &map, s.v_head(kv), row, blocks, s.err);
+                ok = ok && ring_load(m, leader, pos, &map, s.v_head(kv), row, blocks, s.err);
                 pos += ok;
             }
             if (*m.abort_flag) ring_drain(m, pos);
@@ -643,12 +649,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         for (int it = 0; it < count && alive; ++it) {
             const int k0 = kt.at(it) * kTile;
             const bool masked = !all_seen(s, q0, q0 + kTile, k0, k0 + kTile);
-            uint32_t seen[2];
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
+            auto seen = [&](int b) {
                 const int at = k0 + half * 64 + b * 32, hi = row - at;
-                seen[b] = visible(hi, s.window ? hi - s.window + 1 : -kTile, s.sinks - at);
-            }
+                return visible(hi, s.window ? hi - s.window + 1 : -kTile, s.sinks - at);
+            };
             const uint32_t t_s = tmem + (it & 1) * 128 + lanes + half * 64;
             alive = wait_all(&m.scores[it & 1], (it >> 1) & 1, m.abort_flag, s.err, 44);
             if (!alive) break;
@@ -678,7 +682,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     add2(y[b][e], y[b][e + 1], -st.y, -st.y);
                     step::mul2(y[b][e], y[b][e + 1], x[b][e], x[b][e + 1]);
                 }
-                if (masked) keep(y[b], seen[b], 0.0f);
+                if (masked) keep(y[b], seen(b), 0.0f);
                 pack32(y[b], p + b * 16);
             }
             ptx::tmem_st32_async(t_s, p);
