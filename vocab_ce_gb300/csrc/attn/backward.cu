@@ -205,13 +205,18 @@ constexpr int kBwdThreads = 384, kBwdRing = 5;
 constexpr uint32_t kBwdSmem = 2 * kTileBytes + kBwdRing * kTileBytes + 2 * kTile * 8 + 256;
 static_assert(kBwdSmem <= static_cast<uint32_t>(kMaxSmem), "the ring fits");
 
-// A ring of tiles as one warp fills and another uses it: positions count on, each is a
-// slot and the parity of its round.
+// The tiles that come and go, two of each step: those that are used from a step's first
+// product to its last (Q for dK and dV, K for dQ) have three places, the others (dO, V)
+// two. (One ring of five for both in turn made a tile wait for the other kind's last use:
+// dQ stood still for 500 of 2400 cycles a step.)
+constexpr int kLong = 0, kShort = 1;
 struct Ring {
     uint8_t *at;
     uint64_t *full, *empty;
-    __device__ __forceinline__ static int slot(int pos) { return pos % kBwdRing; }
-    __device__ __forceinline__ static uint32_t parity(int pos) { return static_cast<uint32_t>(pos / kBwdRing) & 1u; }
+    __device__ __forceinline__ static int slot(int kind, int pos) { return kind == kLong ? pos % 3 : 3 + (pos & 1); }
+    __device__ __forceinline__ static uint32_t parity(int kind, int pos) {
+        return static_cast<uint32_t>(kind == kLong ? pos / 3 : pos >> 1) & 1u;
+    }
 };
 
 struct BwdSmem {
@@ -267,22 +272,24 @@ struct BwdSmem {
     }
 };
 
-// Loads one tile into the next place of the ring (all lanes call it); false when a wait gave up.
-__device__ __forceinline__ bool ring_load(const BwdSmem &m, bool leader, int pos, const CUtensorMap *map, int head,
-                                          int64_t row, int blocks, uint32_t *err) {
-    const int slot = Ring::slot(pos);
-    if (!wait_all<true>(&m.ring.empty[slot], Ring::parity(pos) ^ 1, m.abort_flag, err, 30)) return false;
+// Loads the tile of step `pos` of its kind (all lanes call it); false when a wait gave up.
+__device__ __forceinline__ bool ring_load(const BwdSmem &m, bool leader, int kind, int pos, const CUtensorMap *map,
+                                          int head, int64_t row, int blocks, uint32_t *err) {
+    const int slot = Ring::slot(kind, pos);
+    if (!wait_all<true>(&m.ring.empty[slot], Ring::parity(kind, pos) ^ 1, m.abort_flag, err, 30)) return false;
     if (leader) {
         ptx::mbar_arrive_expect_tx(&m.ring.full[slot], blocks * kBlockBytes);
         load_tile(m.ring.at + slot * kTileBytes, map, &m.ring.full[slot], head, row, blocks);
     }
     return true;
 }
-// After a wait gave up: the loads of the positions before `pos` land.
-__device__ __forceinline__ void ring_drain(const BwdSmem &m, int pos) {
+// After a wait gave up: the loads of the steps before `pos` land.
+__device__ __forceinline__ void ring_drain(const BwdSmem &m, int longs, int shorts) {
     ptx::mbar_wait_drain(m.stay, 0);
-    for (int p = max(0, pos - kBwdRing); p < pos; ++p)
-        ptx::mbar_wait_drain(&m.ring.full[Ring::slot(p)], Ring::parity(p));
+    for (int p = max(0, longs - 3); p < longs; ++p)
+        ptx::mbar_wait_drain(&m.ring.full[Ring::slot(kLong, p)], Ring::parity(kLong, p));
+    for (int p = max(0, shorts - 2); p < shorts; ++p)
+        ptx::mbar_wait_drain(&m.ring.full[Ring::slot(kShort, p)], Ring::parity(kShort, p));
 }
 
 // This thread's row of an accumulator, times f, from column c0 on (up to 64), to `to`; false if
@@ -366,18 +373,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 load_tile(m.tiles, &map, m.stay, s.k_head(kv), t.row0 + k0, blocks);
                 load_tile(m.tiles + kTileBytes, &map, m.stay, s.v_head(kv), t.row0 + k0, blocks);
             }
-            int pos = 0;
+            int longs = 0, shorts = 0;
             bool ok = true;
             for (int g = 0; g < s.group && ok; ++g)
                 for (int q = 0; q < of_head && ok; ++q) {
                     const int64_t row = t.row0 + k0 + q * kTile;
                     const int h = kv * s.group + g;
-                    ok = ring_load(m, leader, pos, &map, s.q_head(h), row, blocks, s.err);
-                    pos += ok;
-                    ok = ok && ring_load(m, leader, pos, &map_do, h, row, blocks, s.err);
-                    pos += ok;
+                    ok = ring_load(m, leader, kLong, longs, &map, s.q_head(h), row, blocks, s.err);
+                    longs += ok;
+                    ok = ok && ring_load(m, leader, kShort, shorts, &map_do, h, row, blocks, s.err);
+                    shorts += ok;
                 }
-            if (*m.abort_flag) ring_drain(m, pos);
+            if (*m.abort_flag && leader) ring_drain(m, longs, shorts);
         }
     } else if (warp == 9 || warp == 10) {
         // step `it`: the sum with tile it - 1, then the scores (or dots) of tile it
@@ -391,26 +398,28 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         auto wait = [&](uint64_t *bar, uint32_t parity, uint32_t where) {
             ok = ok && wait_all<true>(bar, parity, m.abort_flag, s.err, where);
         };
-        auto arrived = [&](int pos) { wait(&m.ring.full[Ring::slot(pos)], Ring::parity(pos), 31); };
-        auto tile = [&](int pos) { return base + Ring::slot(pos) * kTileBytes; };
+        // Q (long) serves S and dK, dO (short) dP and dV
+        const int kind_in = i ? kShort : kLong, kind_of = i ? kLong : kShort;
+        auto arrived = [&](int kind, int pos) {
+            wait(&m.ring.full[Ring::slot(kind, pos)], Ring::parity(kind, pos), 31);
+        };
+        auto tile = [&](int kind, int pos) { return base + Ring::slot(kind, pos) * kTileBytes; };
         wait(m.stay, 0, 32);
         for (int it = 0; it <= count && ok; ++it) {
-            // Q of a tile is at 2 it, dO at 2 it + 1; the sums take dO for dV and Q for dK
-            const int in = 2 * it + i, of = 2 * (it - 1) + (i ^ 1);
             const bool scores = it < count, sums = it > 0;
-            if (scores) arrived(in);
-            if (sums) arrived(of);
+            if (scores) arrived(kind_in, it);
+            if (sums) arrived(kind_of, it - 1);
             if (i == 1 || it > 0) wait(&m.turn[i], (i == 1 ? it : it - 1) & 1, 33);
             if (sums) wait(ready, (it - 1) & 1, 34);
             if (!ok) break;
             ptx::tc_fence_after();
-            if (sums) mma_weighted(leader, t_sum, t_in, 64, tile(of), idesc, it > 1);
+            if (sums) mma_weighted(leader, t_sum, t_in, 64, tile(kind_of, it - 1), idesc, it > 1);
             if (scores)
-                mma_scores(leader, t_in, stays, tile(in), s.d, out, &m.turn[i ^ 1]);
+                mma_scores(leader, t_in, stays, tile(kind_in, it), s.d, out, &m.turn[i ^ 1]);
             else if (leader)
                 ptx::mbar_arrive(&m.turn[i ^ 1]);
-            if (sums) commit(leader, &m.ring.empty[Ring::slot(of)]);
-            if (scores) commit(leader, &m.ring.empty[Ring::slot(in)]);
+            if (sums) commit(leader, &m.ring.empty[Ring::slot(kind_of, it - 1)]);
+            if (scores) commit(leader, &m.ring.empty[Ring::slot(kind_in, it)]);
         }
         if (ok) commit(leader, m.done);
         commit(leader, m.drain);
@@ -457,8 +466,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 return below(limit - at) & ~below(key - at);
             };
             const float *lse = m.stats + (it & 1) * 2 * kTile + half * 64, *delta = lse + kTile;
-            alive = wait_all(&m.stats_full[it & 1], (it >> 1) & 1, m.abort_flag, s.err, 36) &&
-                    wait_all(m.scores, it & 1, m.abort_flag, s.err, 37);
+            alive = wait_all<true>(&m.stats_full[it & 1], (it >> 1) & 1, m.abort_flag, s.err, 36) &&
+                    wait_all<true>(m.scores, it & 1, m.abort_flag, s.err, 37);
             if (!alive) break;
             ptx::tc_fence_after();
             float x[2][32];
@@ -483,7 +492,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(m.p_ready);
-            alive = wait_all(m.dots, it & 1, m.abort_flag, s.err, 38);
+            alive = wait_all<true>(m.dots, it & 1, m.abort_flag, s.err, 38);
             if (!alive) break;
             ptx::tc_fence_after();
             float y[2][32];
@@ -511,7 +520,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 ptx::mbar_arrive(&m.stats_empty[it & 1]);
             }
         }
-        if (alive) alive = wait_all(m.done, 0, m.abort_flag, s.err, 39);
+        if (alive) alive = wait_all<true>(m.done, 0, m.abort_flag, s.err, 39);
         if (alive) {
             ptx::tc_fence_after();
             // warps 0 - 3 write dK, 4 - 7 dV
@@ -588,52 +597,48 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 load_tile(m.tiles, &map, m.stay, s.q_head(h), t.row0 + q0, blocks);
                 load_tile(m.tiles + kTileBytes, &map_do, m.stay, h, t.row0 + q0, blocks);
             }
-            int pos = 0;
+            int longs = 0, shorts = 0;
             bool ok = true;
             for (int u = 0; u < count && ok; ++u) {
                 const int64_t row = t.row0 + static_cast<int64_t>(kt.at(u)) * kTile;
-                ok = ring_load(m, leader, pos, &map, s.k_head(kv), row, blocks, s.err);
-                pos += ok;
-                ok = ok && ring_load(m, leader, pos, &map, s.v_head(kv), row, blocks, s.err);
-                pos += ok;
+                ok = ring_load(m, leader, kLong, longs, &map, s.k_head(kv), row, blocks, s.err);
+                longs += ok;
+                ok = ok && ring_load(m, leader, kShort, shorts, &map, s.v_head(kv), row, blocks, s.err);
+                shorts += ok;
             }
-            if (*m.abort_flag) ring_drain(m, pos);
+            if (*m.abort_flag && leader) ring_drain(m, longs, shorts);
         }
     } else if (warp == 9) {
         {
             const bool leader = ptx::elect_one();
             const uint32_t idesc = idesc_weighted(s.d), base = ptx::smem_u32(m.ring.at), q_tile = ptx::smem_u32(m.tiles);
-            auto tile = [&](int pos) { return base + Ring::slot(pos) * kTileBytes; };
-            auto arrived = [&](int pos) {
-                return wait_all<true>(&m.ring.full[Ring::slot(pos)], Ring::parity(pos), m.abort_flag, s.err, 41);
+            auto tile = [&](int kind, int pos) { return base + Ring::slot(kind, pos) * kTileBytes; };
+            auto arrived = [&](int kind, int pos) {
+                return wait_all<true>(&m.ring.full[Ring::slot(kind, pos)], Ring::parity(kind, pos), m.abort_flag, s.err,
+                                      41);
             };
-            bool ok = wait_all(m.stay, 0, m.abort_flag, s.err, 42) && arrived(0);
-            if (ok) {
+            auto scores = [&](int it) {
+                if (!arrived(kLong, it)) return false;
                 ptx::tc_fence_after();
-                mma_scores(leader, tmem, q_tile, tile(0), s.d, &m.scores[0]);
-                ok = arrived(1);
-            }
-            if (ok) {
-                mma_scores(leader, t_dp, q_tile + kTileBytes, tile(1), s.d, m.dots);
-                commit(leader, &m.ring.empty[Ring::slot(1)]);
-            }
+                mma_scores(leader, tmem + (it & 1) * 128, q_tile, tile(kLong, it), s.d, &m.scores[it & 1]);
+                return true;
+            };
+            auto dots = [&](int it) {
+                if (!arrived(kShort, it)) return false;
+                if (it > 0 && !wait_all<true>(m.p_ready, (it - 1) & 1, m.abort_flag, s.err, 43)) return false;
+                ptx::tc_fence_after();
+                mma_scores(leader, t_dp, q_tile + kTileBytes, tile(kShort, it), s.d, m.dots);
+                commit(leader, &m.ring.empty[Ring::slot(kShort, it)]);
+                return true;
+            };
+            bool ok = wait_all(m.stay, 0, m.abort_flag, s.err, 42) && scores(0) && dots(0);
             for (int it = 0; it < count && ok; ++it) {
-                const int k = 2 * it;
-                if (it + 1 < count) {
-                    ok = arrived(k + 2);
-                    if (!ok) break;
-                    mma_scores(leader, tmem + ((it + 1) & 1) * 128, q_tile, tile(k + 2), s.d, &m.scores[(it + 1) & 1]);
-                    ok = arrived(k + 3) && wait_all<true>(m.p_ready, it & 1, m.abort_flag, s.err, 43);
-                    if (!ok) break;
-                    ptx::tc_fence_after();
-                    mma_scores(leader, t_dp, q_tile + kTileBytes, tile(k + 3), s.d, m.dots);
-                    commit(leader, &m.ring.empty[Ring::slot(k + 3)]);
-                }
-                ok = wait_all<true>(m.ds_ready, it & 1, m.abort_flag, s.err, 47);
+                if (it + 1 < count) ok = scores(it + 1) && dots(it + 1);
+                ok = ok && wait_all<true>(m.ds_ready, it & 1, m.abort_flag, s.err, 47);
                 if (!ok) break;
                 ptx::tc_fence_after();
-                mma_weighted(leader, t_dq, tmem + (it & 1) * 128, 64, tile(k), idesc, it > 0);
-                commit(leader, &m.ring.empty[Ring::slot(k)]);
+                mma_weighted(leader, t_dq, tmem + (it & 1) * 128, 64, tile(kLong, it), idesc, it > 0);
+                commit(leader, &m.ring.empty[Ring::slot(kLong, it)]);
             }
             if (ok) commit(leader, m.done);
             commit(leader, m.drain);
@@ -654,7 +659,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 return visible(hi, s.window ? hi - s.window + 1 : -kTile, s.sinks - at);
             };
             const uint32_t t_s = tmem + (it & 1) * 128 + lanes + half * 64;
-            alive = wait_all(&m.scores[it & 1], (it >> 1) & 1, m.abort_flag, s.err, 44);
+            alive = wait_all<true>(&m.scores[it & 1], (it >> 1) & 1, m.abort_flag, s.err, 44);
             if (!alive) break;
             ptx::tc_fence_after();
             float x[2][32], y[2][32];
@@ -667,7 +672,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     x[b][e] = exp2_fast(x[b][e]);
                     x[b][e + 1] = exp2_fast(x[b][e + 1]);
                 }
-            alive = wait_all(m.dots, it & 1, m.abort_flag, s.err, 45);
+            alive = wait_all<true>(m.dots, it & 1, m.abort_flag, s.err, 45);
             if (!alive) break;
             ptx::tc_fence_after();
             read_half(t_dp + lanes + half * 64, y);
@@ -691,7 +696,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(m.ds_ready);
         }
-        if (alive) alive = wait_all(m.done, 0, m.abort_flag, s.err, 46);
+        if (alive) alive = wait_all<true>(m.done, 0, m.abort_flag, s.err, 46);
         if (alive && half * 64 < s.d) {
             ptx::tc_fence_after();
             __nv_bfloat16 *to = dQKV + (t.row0 + row) * s.ld + static_cast<int64_t>(s.q_head(h)) * s.d;
