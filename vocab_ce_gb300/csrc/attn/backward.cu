@@ -16,11 +16,12 @@ using namespace attn;
 
 // ------------------------------------------------------------------ delta
 // stats[h, t] = (lse log2(e), delta): what the tiles need of a query. 16 lanes a row of
-// one head; bound by reading O and dO.
+// one head; bound by reading O and dO. The counter of the units that follow begins at 0.
 template <typename T>
 __global__ void __launch_bounds__(256) delta_kernel(const Shape s, const T *dO, const T *O, const float *lse,
-                                                    float2 *__restrict__ stats) {
+                                                    float2 *__restrict__ stats, int *counter) {
     grid_begin();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *counter = 0;
     const int64_t i = static_cast<int64_t>(blockIdx.x) * 16 + threadIdx.x / 16;
     const int lane = threadIdx.x & 15;
     const int64_t t = i / s.n_q;
@@ -195,133 +196,111 @@ __global__ void __launch_bounds__(kPlainThreads)
 }
 
 // ------------------------------------------------------------------ tiles on the tensor cores
-// Twelve warps: 0 - 7 compute, a thread one row of a 128 x 128 tile and half of its
-// columns (warps 4 - 7 the second half); warp 8 loads; warps 9 and 10 issue the
-// products (dQ: warp 9 alone); warp 11 fetches the queries' statistics where they go by
-// columns. A warp's products run in the order in which they are issued, which is what
-// keeps a buffer of tensor memory from being written while one before reads it.
-constexpr int kBwdThreads = 384, kBwdRing = 5;
-// the two tiles that stay, the ring, statistics of two tiles, barriers
-constexpr uint32_t kBwdSmem = 2 * kTileBytes + kBwdRing * kTileBytes + 2 * kTile * 8 + 256;
-static_assert(kBwdSmem <= static_cast<uint32_t>(kMaxSmem), "the ring fits");
-
+// The work is cut into units: dK and dV of 128 keys of a key/value head, and dQ of 128
+// queries of a head. One block an SM takes units from a counter until there are none,
+// those of dK and dV first and among each kind the ones with the most steps first, so
+// that the small ones fill what the large ones leave. Sixteen warps, a warpgroup each of
+//   warps 0 - 3, 4 - 7   compute: a thread one row of a 128 x 128 tile and half of its
+//                        columns (warps 4 - 7 the second half)
+//   warps 8, 11, 12      load tiles; fetch the queries' statistics where they go by
+//                        columns; take the next unit, two ahead
+//   warps 9, 10          issue the products
+// While a unit's results are written the next one's tiles are loaded and its first
+// scores formed.
+constexpr int kBwdThreads = 512;
 // The tiles that come and go, two of each step: those that are used from a step's first
 // product to its last (Q for dK and dV, K for dQ) have three places, the others (dO, V)
 // two. (One ring of five for both in turn made a tile wait for the other kind's last use:
 // dQ stood still for 500 of 2400 cycles a step.)
-constexpr int kLong = 0, kShort = 1;
-struct Ring {
-    uint8_t *at;
-    uint64_t *full, *empty;
-    __device__ __forceinline__ static int slot(int kind, int pos) { return kind == kLong ? pos % 3 : 3 + (pos & 1); }
-    __device__ __forceinline__ static uint32_t parity(int kind, int pos) {
-        return static_cast<uint32_t>(kind == kLong ? pos / 3 : pos >> 1) & 1u;
-    }
+constexpr int kLong = 0, kShort = 1, kPlaces = 5;
+__device__ __forceinline__ int place_of(int kind, int n) { return kind == kLong ? n % 3 : 3 + (n & 1); }
+__device__ __forceinline__ uint32_t round_of(int kind, int n) {
+    return static_cast<uint32_t>(kind == kLong ? n / 3 : n >> 1) & 1u;
+}
+
+enum Kind : int { kKeys, kQueries, kRest, kEnd };  // of a unit; kRest: rows without a sequence
+struct Unit {
+    Tile t;
+    int kind, head, first, steps, id;
 };
 
 struct BwdSmem {
-    uint8_t *tiles;  // the two that stay
-    Ring ring;
-    float *stats;  // [2][2][kTile]
-    uint64_t *stay, *scores, *dots, *p_ready, *ds_ready, *stats_full, *stats_empty, *done, *drain, *turn;
-    uint32_t *tmem_slot;
-    volatile int *abort_flag, *odd;
-    __device__ __forceinline__ explicit BwdSmem(uint8_t *raw) {
-        tiles = raw;  // 1024-byte aligned, as the swizzle needs it
-        ring.at = tiles + 2 * kTileBytes;
-        stats = reinterpret_cast<float *>(ring.at + kBwdRing * kTileBytes);
-        uint64_t *b = reinterpret_cast<uint64_t *>(stats + 4 * kTile);
-        ring.full = b;
-        ring.empty = b + kBwdRing;
-        b += 2 * kBwdRing;
-        stay = b;
-        scores = b + 1;      // [2]
-        dots = b + 3;
-        p_ready = b + 4;
-        ds_ready = b + 5;
-        stats_full = b + 6;  // [2]
-        stats_empty = b + 8;  // [2]
-        done = b + 10;
-        drain = b + 11;
-        turn = b + 12;  // [2]
-        tmem_slot = reinterpret_cast<uint32_t *>(b + 14);
-        abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-        odd = abort_flag + 1;
-    }
-    // issuers: warps that issue products
-    __device__ __forceinline__ void init(int issuers) const {
-        for (int i = 0; i < kBwdRing; ++i) {
-            ptx::mbar_init(&ring.full[i], 1);
-            ptx::mbar_init(&ring.empty[i], issuers);
-        }
-        for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(&turn[i], 1);
-            ptx::mbar_init(&scores[i], 1);
-            ptx::mbar_init(&stats_full[i], 32);
-            ptx::mbar_init(&stats_empty[i], 8);
-        }
-        ptx::mbar_init(stay, 1);
-        ptx::mbar_init(dots, 1);
-        ptx::mbar_init(p_ready, 8);
-        ptx::mbar_init(ds_ready, 8);
-        ptx::mbar_init(done, issuers);
-        ptx::mbar_init(drain, issuers);
-        *abort_flag = 0;
-        *odd = 0;
-        ptx::fence_mbar_init();
-    }
+    uint8_t stay[2][kTileBytes];  // K and V, or Q and dO
+    uint8_t ring[kPlaces][kTileBytes];
+    float stats[2][2][kTile];     // -lse log2(e) and -delta of a step's queries
+    uint64_t full[kPlaces], empty[kPlaces], stay_full, stay_empty;
+    uint64_t scores[2], dots, p_ready, ds_ready, stats_full[2], stats_empty[2], turn[2];
+    uint64_t done, read;          // a unit's products are complete; its results have been read
+    uint64_t unit_full[2], unit_empty[2], drain;
+    Unit unit[2];
+    uint32_t tmem_slot;
+    int abort_flag, odd;          // odd: the last of the block's units that has results which are not finite
+};
+static_assert(sizeof(BwdSmem) <= static_cast<size_t>(kMaxSmem), "the ring fits");
+static_assert(offsetof(BwdSmem, full) >= 4 * (4 * kRows * (kMaxDim + 4) + 2 * kRows * kPitchP), "room for plain tiles");
+constexpr int kUnitReaders = 12;  // warps
+
+// What the backward keeps in its workspace beside the statistics.
+struct Shared {
+    int *counter;  // of units taken; zeroed by the kernel before
+    int *next;     // [units] the block's odd unit before this one
 };
 
-// Loads the tile of step `pos` of its kind (all lanes call it); false when a wait gave up.
-__device__ __forceinline__ bool ring_load(const BwdSmem &m, bool leader, int kind, int pos, const CUtensorMap *map,
-                                          int head, int64_t row, int blocks, uint32_t *err) {
-    const int slot = Ring::slot(kind, pos);
-    if (!wait_all<true>(&m.ring.empty[slot], Ring::parity(kind, pos) ^ 1, m.abort_flag, err, 30)) return false;
-    if (leader) {
-        ptx::mbar_arrive_expect_tx(&m.ring.full[slot], blocks * kBlockBytes);
-        load_tile(m.ring.at + slot * kTileBytes, map, &m.ring.full[slot], head, row, blocks);
-    }
-    return true;
-}
-// After a wait gave up: the loads of the steps before `pos` land.
-__device__ __forceinline__ void ring_drain(const BwdSmem &m, int longs, int shorts) {
-    ptx::mbar_wait_drain(m.stay, 0);
-    for (int p = max(0, longs - 3); p < longs; ++p)
-        ptx::mbar_wait_drain(&m.ring.full[Ring::slot(kLong, p)], Ring::parity(kLong, p));
-    for (int p = max(0, shorts - 2); p < shorts; ++p)
-        ptx::mbar_wait_drain(&m.ring.full[Ring::slot(kShort, p)], Ring::parity(kShort, p));
+// Tiles of all sequences, and the rows of none.
+__device__ __forceinline__ Tile count_tiles(const Shape &s, int &tiles) {
+    Tile t = find_tile(s, INT_MAX, kTile, 0);
+    tiles = INT_MAX - t.part;
+    t.part = blockIdx.x;
+    t.parts = gridDim.x;
+    return t;
 }
 
-// This thread's row of an accumulator, times f, from column c0 on (up to 64), to `to`; false if
+// Unit `id` of so many tiles; every lane of a warp calls it.
+__device__ __forceinline__ Unit find_unit(const Shape &s, int id, int tiles) {
+    Unit u{};
+    u.id = id;
+    u.kind = kEnd;
+    const int64_t of_keys = static_cast<int64_t>(tiles) * s.n_kv, all = of_keys + static_cast<int64_t>(tiles) * s.n_q;
+    if (id >= all) return u;
+    u.kind = id < of_keys ? kKeys : kQueries;
+    const int heads = u.kind == kKeys ? s.n_kv : s.n_q, at = u.kind == kKeys ? id : static_cast<int>(id - of_keys);
+    u.head = at % heads;
+    u.t = find_tile(s, at / heads, kTile, 0);
+    if (u.kind == kKeys) {
+        // the first keys are seen by the most queries, the last queries see the most keys
+        u.first = u.t.tile * kTile;
+        const int end = query_end(s, u.first, min(u.t.n, u.first + kTile), u.t.n);
+        u.steps = (end - u.first + kTile - 1) / kTile * s.group;
+    } else {
+        u.first = (u.t.tiles - 1 - u.t.tile) * kTile;
+        u.steps = key_tiles(s, u.first, min(u.t.n, u.first + kTile), kTile).count();
+    }
+    return u;
+}
+
+// Half a row of an accumulator (up to 64 columns from c0 on), times f, to `to`; false if
 // something is not finite.
-__device__ __forceinline__ bool write_half(uint32_t taddr, float f, int c0, int d, __nv_bfloat16 *to, bool mine) {
+__device__ __forceinline__ bool write_half(const float (&o)[2][32], float f, int c0, int d, __nv_bfloat16 *to,
+                                           bool mine) {
     float check = 0.0f;
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-        if (c0 + b * 32 >= d) break;
-        float o[32];
-        ptx::tmem_ld32_async(taddr + b * 32, o);
-        ptx::tmem_wait_ld();
-        ptx::tmem_ready(o);
+    for (int v = 0; v < 8; ++v) {
+        const int c = c0 + v * 8;
+        if (c >= d) continue;
+        float y[8];
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            const int c = c0 + b * 32 + v * 8;
-            if (c >= d) continue;
-            float y[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                y[e] = o[v * 8 + e] * f;
-                check = fmaf(y[e], 0.0f, check);
-            }
-            Raw8<__nv_bfloat16> r;
-            pack8(y, r);
-            if (mine) store8(to + c, r);
+        for (int e = 0; e < 8; ++e) {
+            y[e] = o[v >> 2][(v & 3) * 8 + e] * f;
+            check = fmaf(y[e], 0.0f, check);
         }
+        Raw8<__nv_bfloat16> r;
+        pack8(y, r);
+        if (mine) store8(to + c, r);
     }
     return !mine || check == 0.0f;  // NaN is not 0
 }
 
-// dK and dV of 128 keys. Per tile of 128 queries of a head, with the keys as rows:
+// Keys as rows, per tile of 128 queries of a head:
 //   S^T = K Q^T  ->  P^T = 2^(S^T c - lse)   ->  dV += P^T dO
 //   dP^T = V dO^T  ->  dS^T = P^T (dP^T - delta)  ->  dK += dS^T Q
 // Tensor memory: S^T, dP^T, dV, dK, 128 columns each; P^T and dS^T overwrite what they
@@ -330,377 +309,431 @@ __device__ __forceinline__ bool write_half(uint32_t taddr, float f, int c0, int 
 //   S(0), dP(0), dV(0) S(1), dK(0) dP(1), dV(1) S(2), ..
 // so that two products are under way while the threads form P or dS, and each warp
 // waits for what it needs during the other's.
-__global__ void __launch_bounds__(kBwdThreads, 1)
-    tc_dkv_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap map_do, const Shape s,
-                  const __nv_bfloat16 *QKV, const __nv_bfloat16 *dO, const float2 *stats, int tiles,
-                  __nv_bfloat16 *dQKV) {
-    extern __shared__ __align__(1024) uint8_t smem_raw[];
-    const BwdSmem m(smem_raw);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) {
-        m.init(2);
-        ptx::prefetch_tmap(&map);
-        ptx::prefetch_tmap(&map_do);
-    }
-    grid_begin();
-    const int kv = blockIdx.x % s.n_kv;
-    const Tile t = find_tile(s, blockIdx.x / s.n_kv, kTile, tiles);
-    if (t.n == 0) {
-        zero_rest(s, t, dQKV, s.ld, static_cast<int64_t>(s.k_head(kv)) * s.d);
-        zero_rest(s, t, dQKV, s.ld, static_cast<int64_t>(s.v_head(kv)) * s.d);
-        return;
-    }
-    // the first keys are seen by the most queries: they come first
-    const int k0 = t.tile * kTile;
-    const int end = query_end(s, k0, min(t.n, k0 + kTile), t.n);
-    const int of_head = (end - k0 + kTile - 1) / kTile, count = of_head * s.group;
-    if (warp == 9) {
-        ptx::tmem_alloc(m.tmem_slot, kTmemCols);
-        ptx::tmem_relinquish();
-    }
-    ptx::tc_fence_before();
-    __syncthreads();
-    ptx::tc_fence_after();
-    constexpr uint32_t tmem = 0,  // all columns there are: they begin at 0
-                       t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 384;
-    const int blocks = s.d > 64 ? 2 : 1;
-
-    if (warp == 8) {
-        {
-            const bool leader = ptx::elect_one();
-            if (leader) {
-                ptx::mbar_arrive_expect_tx(m.stay, 2 * blocks * kBlockBytes);
-                load_tile(m.tiles, &map, m.stay, s.k_head(kv), t.row0 + k0, blocks);
-                load_tile(m.tiles + kTileBytes, &map, m.stay, s.v_head(kv), t.row0 + k0, blocks);
-            }
-            int longs = 0, shorts = 0;
-            bool ok = true;
-            for (int g = 0; g < s.group && ok; ++g)
-                for (int q = 0; q < of_head && ok; ++q) {
-                    const int64_t row = t.row0 + k0 + q * kTile;
-                    const int h = kv * s.group + g;
-                    ok = ring_load(m, leader, kLong, longs, &map, s.q_head(h), row, blocks, s.err);
-                    longs += ok;
-                    ok = ok && ring_load(m, leader, kShort, shorts, &map_do, h, row, blocks, s.err);
-                    shorts += ok;
-                }
-            if (*m.abort_flag && leader) ring_drain(m, longs, shorts);
-        }
-    } else if (warp == 9 || warp == 10) {
-        // step `it`: the sum with tile it - 1, then the scores (or dots) of tile it
-        const int i = warp - 9;
-        const bool leader = ptx::elect_one();
-        const uint32_t idesc = idesc_weighted(s.d), base = ptx::smem_u32(m.ring.at);
-        const uint32_t stays = ptx::smem_u32(m.tiles) + i * kTileBytes;  // K, V
-        const uint32_t t_in = i ? t_dp : t_s, t_sum = i ? t_dk : t_dv;
-        uint64_t *const ready = i ? m.ds_ready : m.p_ready, *const out = i ? m.dots : m.scores;
-        bool ok = true;
-        auto wait = [&](uint64_t *bar, uint32_t parity, uint32_t where) {
-            ok = ok && wait_all<true>(bar, parity, m.abort_flag, s.err, where);
-        };
-        // Q (long) serves S and dK, dO (short) dP and dV
-        const int kind_in = i ? kShort : kLong, kind_of = i ? kLong : kShort;
-        auto arrived = [&](int kind, int pos) {
-            wait(&m.ring.full[Ring::slot(kind, pos)], Ring::parity(kind, pos), 31);
-        };
-        auto tile = [&](int kind, int pos) { return base + Ring::slot(kind, pos) * kTileBytes; };
-        wait(m.stay, 0, 32);
-        for (int it = 0; it <= count && ok; ++it) {
-            const bool scores = it < count, sums = it > 0;
-            if (scores) arrived(kind_in, it);
-            if (sums) arrived(kind_of, it - 1);
-            if (i == 1 || it > 0) wait(&m.turn[i], (i == 1 ? it : it - 1) & 1, 33);
-            if (sums) wait(ready, (it - 1) & 1, 34);
-            if (!ok) break;
-            ptx::tc_fence_after();
-            if (sums) mma_weighted(leader, t_sum, t_in, 64, tile(kind_of, it - 1), idesc, it > 1);
-            if (scores)
-                mma_scores(leader, t_in, stays, tile(kind_in, it), s.d, out, &m.turn[i ^ 1]);
-            else if (leader)
-                ptx::mbar_arrive(&m.turn[i ^ 1]);
-            if (sums) commit(leader, &m.ring.empty[Ring::slot(kind_of, it - 1)]);
-            if (scores) commit(leader, &m.ring.empty[Ring::slot(kind_in, it)]);
-        }
-        if (ok) commit(leader, m.done);
-        commit(leader, m.drain);
-        if (lane == 0) ptx::mbar_wait_drain(m.drain, 0);
-        __syncwarp();
-    } else if (warp == 11) {
-        // the statistics of a tile, when the one two before has been used; queries past the end: P = 2^-inf
-        int it = 0;
-        bool ok = true;
-        for (int g = 0; g < s.group && ok; ++g) {
-            const float2 *from = stats + (kv * s.group + g) * s.T + t.row0;
-            for (int q = 0; q < of_head && ok; ++q, ++it) {
-                float2 v[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int row = k0 + q * kTile + e * 32 + lane;
-                    v[e] = row < t.n ? from[row] : make_float2(INFINITY, 0.0f);
-                }
-                ok = wait_all(&m.stats_empty[it & 1], ((it >> 1) & 1) ^ 1, m.abort_flag, s.err, 35);
-                if (!ok) break;
-                float *to = m.stats + (it & 1) * 2 * kTile;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    to[e * 32 + lane] = -v[e].x;  // both are subtracted
-                    to[kTile + e * 32 + lane] = -v[e].y;
-                }
-                ptx::mbar_arrive(&m.stats_full[it & 1]);
-            }
-        }
-    } else if (warp < 8) {
-        const int half = warp >> 2, r = (warp & 3) * 32 + lane, key = k0 + r;
-        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const float c = s.scale * kLog2e;
-        const int limit = s.window && key >= s.sinks ? min(t.n, key + s.window) : t.n;  // queries below it see the key
-        bool alive = true;
-        int q = 0;
-        for (int it = 0; it < count && alive; ++it) {
-            const int q0 = k0 + q * kTile;
-            q = q + 1 == of_head ? 0 : q + 1;
-            const bool masked = !all_seen(s, q0, q0 + kTile, k0, k0 + kTile) || q0 + kTile > t.n;
-            // queries from the key's own on, below its limit
-            auto seen = [&](int b) {
-                const int at = q0 + half * 64 + b * 32;
-                return below(limit - at) & ~below(key - at);
-            };
-            const float *lse = m.stats + (it & 1) * 2 * kTile + half * 64, *delta = lse + kTile;
-            alive = wait_all<true>(&m.stats_full[it & 1], (it >> 1) & 1, m.abort_flag, s.err, 36) &&
-                    wait_all<true>(m.scores, it & 1, m.abort_flag, s.err, 37);
-            if (!alive) break;
-            ptx::tc_fence_after();
-            float x[2][32];
-            read_half(t_s + lanes + half * 64, x);
-            uint32_t p[32];
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-#pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    const float4 l = *reinterpret_cast<const float4 *>(lse + b * 32 + e);
-                    float(&y)[32] = x[b];
-                    scale2(y[e], y[e + 1], c, l.x, l.y);
-                    scale2(y[e + 2], y[e + 3], c, l.z, l.w);
-                }
-#pragma unroll
-                for (int e = 0; e < 32; ++e) x[b][e] = exp2_fast(x[b][e]);
-                if (masked) keep(x[b], seen(b), 0.0f);
-                pack32(x[b], p + b * 16);
-            }
-            ptx::tmem_st32_async(t_s + lanes + half * 64, p);
-            ptx::tmem_wait_st();
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(m.p_ready);
-            alive = wait_all<true>(m.dots, it & 1, m.abort_flag, s.err, 38);
-            if (!alive) break;
-            ptx::tc_fence_after();
-            float y[2][32];
-            read_half(t_dp + lanes + half * 64, y);
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-#pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    const float4 d = *reinterpret_cast<const float4 *>(delta + b * 32 + e);
-                    float(&v)[32] = y[b];
-                    add2(v[e], v[e + 1], d.x, d.y);
-                    add2(v[e + 2], v[e + 3], d.z, d.w);
-                    step::mul2(v[e], v[e + 1], x[b][e], x[b][e + 1]);
-                    step::mul2(v[e + 2], v[e + 3], x[b][e + 2], x[b][e + 3]);
-                }
-                if (masked) keep(y[b], seen(b), 0.0f);  // what is masked may be infinite here
-                pack32(y[b], p + b * 16);
-            }
-            ptx::tmem_st32_async(t_dp + lanes + half * 64, p);
-            ptx::tmem_wait_st();
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                ptx::mbar_arrive(m.ds_ready);
-                ptx::mbar_arrive(&m.stats_empty[it & 1]);
-            }
-        }
-        if (alive) alive = wait_all<true>(m.done, 0, m.abort_flag, s.err, 39);
-        if (alive) {
-            ptx::tc_fence_after();
-            // warps 0 - 3 write dK, 4 - 7 dV
-            const bool mine = key < t.n;
-            const uint32_t from = (half ? t_dv : t_dk) + lanes;
-            __nv_bfloat16 *to = dQKV + (t.row0 + key) * s.ld +
-                                static_cast<int64_t>(half ? s.v_head(kv) : s.k_head(kv)) * s.d;
-            const float f = half ? 1.0f : s.scale;
-            bool fine = write_half(from, f, 0, s.d, to, mine);
-            fine = write_half(from + 64, f, 64, s.d, to, mine) && fine;
-            if (!fine) *m.odd = 1;
-        }
-    }
-
-    ptx::tc_fence_before();
-    __syncthreads();
-    if (warp == 9) {
-        ptx::tc_fence_after();
-        ptx::tmem_dealloc(tmem, kTmemCols);
-    }
-    // something masked may have been infinite (0 inf is NaN): once more, passing it over
-    if (*m.odd && !*m.abort_flag && threadIdx.x < kPlainThreads) {
-#pragma unroll 1
-        for (int k = k0; k < min(t.n, k0 + kTile); k += kRows) {
-            plain_sync();
-            plain_dkv_tile(s, QKV, dO, stats, t.row0, t.n, k, kv, dQKV, reinterpret_cast<float *>(m.tiles));
-        }
-    }
-}
-
-// dQ of 128 queries of a head. Per tile of 128 keys, with the queries as rows:
+//
+// Queries as rows, per tile of 128 keys:
 //   S = Q K^T, dP = dO V^T  ->  dS = 2^(S c - lse) (dP - delta)  ->  dQ += dS K
-// Tensor memory: two S (dS overwrites the one that it is made of), dP, dQ. In the order
-//   S(0) dP(0) | S(1) dP(1) dQ(0) | S(2) dP(2) dQ(1) | ..
+// Tensor memory: two S (dS overwrites the one that it is made of), dP, dQ. One warp, in
+// the order  S(0) dP(0) | S(1) dP(1) dQ(0) | S(2) dP(2) dQ(1) | ..
 // dP of the next keys is begun as soon as the threads have read the one before, and P
 // is formed of the next S before dP has come.
+//
+// Steps are counted through all of a block's units: barriers go by their number.
+constexpr uint32_t kSumV = 256, kSumK = 384, kDots = 256, kSumQ = 384;  // and at 0 and 128 S^T and dP^T, or the two S
+
 __global__ void __launch_bounds__(kBwdThreads, 1)
-    tc_dq_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap map_do, const Shape s,
-                 const __nv_bfloat16 *QKV, const __nv_bfloat16 *dO, const float2 *stats, int tiles,
-                 __nv_bfloat16 *dQKV) {
+    tc_backward_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap map_do,
+                       const Shape s, const __nv_bfloat16 *QKV, const __nv_bfloat16 *dO, const float2 *stats,
+                       Shared shared, __nv_bfloat16 *dQKV) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    const BwdSmem m(smem_raw);
+    BwdSmem &m = *reinterpret_cast<BwdSmem *>(smem_raw);
+    volatile int *abort_flag = &m.abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        m.init(1);
+        for (int i = 0; i < kPlaces; ++i) {
+            ptx::mbar_init(&m.full[i], 1);
+            ptx::mbar_init(&m.empty[i], 2);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&m.scores[i], 1);
+            ptx::mbar_init(&m.turn[i], 1);
+            ptx::mbar_init(&m.stats_full[i], 32);
+            ptx::mbar_init(&m.stats_empty[i], 8);
+            ptx::mbar_init(&m.unit_full[i], 1);
+            ptx::mbar_init(&m.unit_empty[i], kUnitReaders);
+        }
+        ptx::mbar_init(&m.stay_full, 1);
+        ptx::mbar_init(&m.stay_empty, 2);
+        ptx::mbar_init(&m.dots, 1);
+        ptx::mbar_init(&m.p_ready, 8);
+        ptx::mbar_init(&m.ds_ready, 8);
+        ptx::mbar_init(&m.done, 2);
+        ptx::mbar_init(&m.read, 8);
+        ptx::mbar_init(&m.drain, 2);
+        m.abort_flag = 0;
+        m.odd = -1;
+        ptx::fence_mbar_init();
         ptx::prefetch_tmap(&map);
         ptx::prefetch_tmap(&map_do);
     }
-    grid_begin();
-    const int h = blockIdx.x % s.n_q, kv = h / s.group;
-    const Tile t = find_tile(s, blockIdx.x / s.n_q, kTile, tiles);
-    if (t.n == 0) {
-        zero_rest(s, t, dQKV, s.ld, static_cast<int64_t>(s.q_head(h)) * s.d);
-        return;
-    }
-    const int q0 = (t.tiles - 1 - t.tile) * kTile;
-    const KeyTiles kt = key_tiles(s, q0, min(t.n, q0 + kTile), kTile);
-    const int count = kt.count();
     if (warp == 9) {
-        ptx::tmem_alloc(m.tmem_slot, kTmemCols);
+        ptx::tmem_alloc(&m.tmem_slot, kTmemCols);
         ptx::tmem_relinquish();
     }
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    constexpr uint32_t tmem = 0, t_dp = tmem + 256, t_dq = tmem + 384;
+    grid_begin();
+    // the next unit of the warp that calls it, read by all its lanes; false at the end
+    int round = 0;
+    auto next_unit = [&](Unit &u) {
+        const int at = round & 1;
+        const uint32_t parity = (round >> 1) & 1;
+        ++round;
+        if (!wait_all(&m.unit_full[at], parity, abort_flag, s.err, 48)) return false;
+        u = m.unit[at];
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&m.unit_empty[at]);
+        return u.kind != kEnd;
+    };
     const int blocks = s.d > 64 ? 2 : 1;
+    int n = 0, units = 0;  // steps and units (with steps) so far
+    Unit u;
 
-    if (warp == 8) {
-        {
-            const bool leader = ptx::elect_one();
-            if (leader) {
-                ptx::mbar_arrive_expect_tx(m.stay, 2 * blocks * kBlockBytes);
-                load_tile(m.tiles, &map, m.stay, s.q_head(h), t.row0 + q0, blocks);
-                load_tile(m.tiles + kTileBytes, &map_do, m.stay, h, t.row0 + q0, blocks);
-            }
-            int longs = 0, shorts = 0;
-            bool ok = true;
-            for (int u = 0; u < count && ok; ++u) {
-                const int64_t row = t.row0 + static_cast<int64_t>(kt.at(u)) * kTile;
-                ok = ring_load(m, leader, kLong, longs, &map, s.k_head(kv), row, blocks, s.err);
-                longs += ok;
-                ok = ok && ring_load(m, leader, kShort, shorts, &map, s.v_head(kv), row, blocks, s.err);
-                shorts += ok;
-            }
-            if (*m.abort_flag && leader) ring_drain(m, longs, shorts);
-        }
-    } else if (warp == 9) {
-        {
-            const bool leader = ptx::elect_one();
-            const uint32_t idesc = idesc_weighted(s.d), base = ptx::smem_u32(m.ring.at), q_tile = ptx::smem_u32(m.tiles);
-            auto tile = [&](int kind, int pos) { return base + Ring::slot(kind, pos) * kTileBytes; };
-            auto arrived = [&](int kind, int pos) {
-                return wait_all<true>(&m.ring.full[Ring::slot(kind, pos)], Ring::parity(kind, pos), m.abort_flag, s.err,
-                                      41);
-            };
-            auto scores = [&](int it) {
-                if (!arrived(kLong, it)) return false;
-                ptx::tc_fence_after();
-                mma_scores(leader, tmem + (it & 1) * 128, q_tile, tile(kLong, it), s.d, &m.scores[it & 1]);
-                return true;
-            };
-            auto dots = [&](int it) {
-                if (!arrived(kShort, it)) return false;
-                if (it > 0 && !wait_all<true>(m.p_ready, (it - 1) & 1, m.abort_flag, s.err, 43)) return false;
-                ptx::tc_fence_after();
-                mma_scores(leader, t_dp, q_tile + kTileBytes, tile(kShort, it), s.d, m.dots);
-                commit(leader, &m.ring.empty[Ring::slot(kShort, it)]);
-                return true;
-            };
-            bool ok = wait_all(m.stay, 0, m.abort_flag, s.err, 42) && scores(0) && dots(0);
-            for (int it = 0; it < count && ok; ++it) {
-                if (it + 1 < count) ok = scores(it + 1) && dots(it + 1);
-                ok = ok && wait_all<true>(m.ds_ready, it & 1, m.abort_flag, s.err, 47);
-                if (!ok) break;
-                ptx::tc_fence_after();
-                mma_weighted(leader, t_dq, tmem + (it & 1) * 128, 64, tile(kLong, it), idesc, it > 0);
-                commit(leader, &m.ring.empty[Ring::slot(kLong, it)]);
-            }
-            if (ok) commit(leader, m.done);
-            commit(leader, m.drain);
-            ptx::mbar_wait_drain(m.drain, 0);
-        }
-    } else if (warp < 8) {
-        const int half = warp >> 2, row = q0 + (warp & 3) * 32 + lane;
+    if (warp < 8) {
+        // ------------------------------------------------ compute
+        ptx::registers_up<184>();  // 2 x 184 + 2 x 72 = 4 x 128, the launch's
+        const int half = warp >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const float c = s.scale * kLog2e;
-        const bool mine = row < t.n;
-        const float2 st = mine ? stats[h * s.T + t.row0 + row] : make_float2(INFINITY, 0.0f);
+        int steps_of_keys = 0;
         bool alive = true;
-        for (int it = 0; it < count && alive; ++it) {
-            const int k0 = kt.at(it) * kTile;
-            const bool masked = !all_seen(s, q0, q0 + kTile, k0, k0 + kTile);
-            auto seen = [&](int b) {
-                const int at = k0 + half * 64 + b * 32, hi = row - at;
-                return visible(hi, s.window ? hi - s.window + 1 : -kTile, s.sinks - at);
-            };
-            const uint32_t t_s = tmem + (it & 1) * 128 + lanes + half * 64;
-            alive = wait_all<true>(&m.scores[it & 1], (it >> 1) & 1, m.abort_flag, s.err, 44);
-            if (!alive) break;
-            ptx::tc_fence_after();
-            float x[2][32], y[2][32];
-            read_half(t_s, x);
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    scale2(x[b][e], x[b][e + 1], c, -st.x, -st.x);
-                    x[b][e] = exp2_fast(x[b][e]);
-                    x[b][e + 1] = exp2_fast(x[b][e + 1]);
-                }
-            alive = wait_all<true>(m.dots, it & 1, m.abort_flag, s.err, 45);
-            if (!alive) break;
-            ptx::tc_fence_after();
-            read_half(t_dp + lanes + half * 64, y);
+        auto wait = [&](uint64_t *bar, uint32_t parity, uint32_t where) {
+            alive = alive && wait_all<true>(bar, parity, abort_flag, s.err, where);
+            return alive;
+        };
+        auto tell = [&](uint64_t *bar) {
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(m.p_ready);  // dP has been read
-            uint32_t p[32];
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    add2(y[b][e], y[b][e + 1], -st.y, -st.y);
-                    step::mul2(y[b][e], y[b][e + 1], x[b][e], x[b][e + 1]);
-                }
-                if (masked) keep(y[b], seen(b), 0.0f);
-                pack32(y[b], p + b * 16);
+            if (lane == 0) ptx::mbar_arrive(bar);
+        };
+        while (alive && next_unit(u)) {
+            if (u.kind == kRest) {
+                for (int h = 0; h < s.n_q + 2 * s.n_kv; ++h)
+                    zero_rest(s, u.t, dQKV, s.ld, static_cast<int64_t>(h) * s.d);
+                continue;
             }
-            ptx::tmem_st32_async(t_s, p);
-            ptx::tmem_wait_st();
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(m.ds_ready);
-        }
-        if (alive) alive = wait_all<true>(m.done, 0, m.abort_flag, s.err, 46);
-        if (alive && half * 64 < s.d) {
+            const int row = u.first + r;
+            const bool mine = row < u.t.n;
+            bool fine = true;
+            if (u.kind == kKeys) {
+                const int limit = s.window && row >= s.sinks ? min(u.t.n, row + s.window) : u.t.n;  // of queries
+                const int of_head = u.steps / s.group;
+                int q = 0;
+                for (int it = 0; it < u.steps; ++it, ++n, ++steps_of_keys) {
+                    const int q0 = u.first + q * kTile, k0 = u.first;
+                    q = q + 1 == of_head ? 0 : q + 1;
+                    const bool masked = !all_seen(s, q0, q0 + kTile, k0, k0 + kTile) || q0 + kTile > u.t.n;
+                    // queries from the key's own on, below its limit
+                    auto seen = [&](int b) {
+                        const int at = q0 + half * 64 + b * 32;
+                        return below(limit - at) & ~below(row - at);
+                    };
+                    const int buf = steps_of_keys & 1;
+                    const float *lse = m.stats[buf][0] + half * 64, *delta = m.stats[buf][1] + half * 64;
+                    wait(&m.stats_full[buf], (steps_of_keys >> 1) & 1, 36);
+                    if (!wait(&m.scores[n & 1], (n >> 1) & 1, 37)) break;
+                    ptx::tc_fence_after();
+                    float x[2][32], y[2][32];
+                    uint32_t p[32];
+                    read_half(lanes + half * 64, x);
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 l = *reinterpret_cast<const float4 *>(lse + b * 32 + e);
+                            float(&v)[32] = x[b];
+                            scale2(v[e], v[e + 1], c, l.x, l.y);
+                            scale2(v[e + 2], v[e + 3], c, l.z, l.w);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) x[b][e] = exp2_fast(x[b][e]);
+                        if (masked) keep(x[b], seen(b), 0.0f);
+                        pack32(x[b], p + b * 16);
+                    }
+                    ptx::tmem_st32_async(lanes + half * 64, p);
+                    ptx::tmem_wait_st();
+                    tell(&m.p_ready);
+                    if (!wait(&m.dots, n & 1, 38)) break;
+                    ptx::tc_fence_after();
+                    read_half(128 + lanes + half * 64, y);
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 d = *reinterpret_cast<const float4 *>(delta + b * 32 + e);
+                            float(&v)[32] = y[b];
+                            add2(v[e], v[e + 1], d.x, d.y);
+                            add2(v[e + 2], v[e + 3], d.z, d.w);
+                            step::mul2(v[e], v[e + 1], x[b][e], x[b][e + 1]);
+                            step::mul2(v[e + 2], v[e + 3], x[b][e + 2], x[b][e + 3]);
+                        }
+                        if (masked) keep(y[b], seen(b), 0.0f);  // what is masked may be infinite here
+                        pack32(y[b], p + b * 16);
+                    }
+                    ptx::tmem_st32_async(128 + lanes + half * 64, p);
+                    ptx::tmem_wait_st();
+                    tell(&m.ds_ready);
+                    if (lane == 0) ptx::mbar_arrive(&m.stats_empty[buf]);
+                }
+            } else {
+                const KeyTiles kt = key_tiles(s, u.first, min(u.t.n, u.first + kTile), kTile);
+                const float2 st = mine ? stats[u.head * s.T + u.t.row0 + row] : make_float2(INFINITY, 0.0f);
+                for (int it = 0; it < u.steps; ++it, ++n) {
+                    const int q0 = u.first, k0 = kt.at(it) * kTile;
+                    const bool masked = !all_seen(s, q0, q0 + kTile, k0, k0 + kTile);
+                    auto seen = [&](int b) {
+                        const int at = k0 + half * 64 + b * 32, hi = row - at;
+                        return visible(hi, s.window ? hi - s.window + 1 : -kTile, s.sinks - at);
+                    };
+                    const uint32_t t_s = (n & 1) * 128 + lanes + half * 64;
+                    if (!wait(&m.scores[n & 1], (n >> 1) & 1, 44)) break;
+                    ptx::tc_fence_after();
+                    float x[2][32], y[2][32];
+                    read_half(t_s, x);
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            scale2(x[b][e], x[b][e + 1], c, -st.x, -st.x);
+                            x[b][e] = exp2_fast(x[b][e]);
+                            x[b][e + 1] = exp2_fast(x[b][e + 1]);
+                        }
+                    if (!wait(&m.dots, n & 1, 45)) break;
+                    ptx::tc_fence_after();
+                    read_half(kDots + lanes + half * 64, y);
+                    tell(&m.p_ready);  // dP has been read
+                    uint32_t p[32];
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            add2(y[b][e], y[b][e + 1], -st.y, -st.y);
+                            step::mul2(y[b][e], y[b][e + 1], x[b][e], x[b][e + 1]);
+                        }
+                        if (masked) keep(y[b], seen(b), 0.0f);
+                        pack32(y[b], p + b * 16);
+                    }
+                    ptx::tmem_st32_async(t_s, p);
+                    ptx::tmem_wait_st();
+                    tell(&m.ds_ready);
+                }
+            }
+            if (!wait(&m.done, units & 1, 46)) break;
+            ++units;
             ptx::tc_fence_after();
-            __nv_bfloat16 *to = dQKV + (t.row0 + row) * s.ld + static_cast<int64_t>(s.q_head(h)) * s.d;
-            if (!write_half(t_dq + lanes + half * 64, s.scale, half * 64, s.d, to, mine)) *m.odd = 1;
+            float o[2][32];
+            if (u.kind == kKeys) {
+                // both halves of dK by warps 0 - 3, of dV by warps 4 - 7
+                __nv_bfloat16 *to = dQKV + (u.t.row0 + row) * s.ld +
+                                    static_cast<int64_t>(half ? s.v_head(u.head) : s.k_head(u.head)) * s.d;
+                const uint32_t from = (half ? kSumV : kSumK) + lanes;
+                const float f = half ? 1.0f : s.scale;
+                read_half(from, o);
+                fine = write_half(o, f, 0, s.d, to, mine);
+                read_half(from + 64, o);
+                tell(&m.read);
+                fine = write_half(o, f, 64, s.d, to, mine) && fine;
+            } else {
+                __nv_bfloat16 *to =
+                    dQKV + (u.t.row0 + row) * s.ld + static_cast<int64_t>(s.q_head(u.head)) * s.d;
+                read_half(kSumQ + lanes + half * 64, o);
+                tell(&m.read);
+                fine = write_half(o, s.scale, half * 64, s.d, to, mine);
+            }
+            // the block's odd units are a list that begins at m.odd
+            if (!__all_sync(0xffffffffu, fine) && lane == 0) {
+                const int before = atomicExch(&m.odd, u.id);
+                if (before != u.id) shared.next[u.id] = before;  // not put there by another warp
+            }
+        }
+    } else {
+        ptx::registers_down<72>();
+        bool ok = true;
+        auto wait = [&](uint64_t *bar, uint32_t parity, uint32_t where) {
+            ok = ok && wait_all<true>(bar, parity, abort_flag, s.err, where);
+            return ok;
+        };
+        if (warp == 8) {
+            // ------------------------------------------------ loads
+            const bool leader = ptx::elect_one();
+            const uint32_t bytes = blocks * kBlockBytes;
+            auto load = [&](int kind, int at, const CUtensorMap *from, int head, int64_t row) {
+                const int place = place_of(kind, at);
+                if (!wait(&m.empty[place], round_of(kind, at) ^ 1, 30)) return;
+                if (leader) {
+                    ptx::mbar_arrive_expect_tx(&m.full[place], bytes);
+                    load_tile(m.ring[place], from, &m.full[place], head, row, blocks);
+                }
+            };
+            int longs = 0, shorts = 0;
+            while (ok && next_unit(u)) {
+                if (u.kind == kRest) continue;
+                const bool keys = u.kind == kKeys;
+                const int kv = keys ? u.head : u.head / s.group;
+                if (!wait(&m.stay_empty, (units & 1) ^ 1, 27)) break;
+                ++units;
+                const int64_t row = u.t.row0 + u.first;
+                if (leader) {
+                    ptx::mbar_arrive_expect_tx(&m.stay_full, 2 * bytes);
+                    load_tile(m.stay[0], &map, &m.stay_full, keys ? s.k_head(kv) : s.q_head(u.head), row, blocks);
+                    load_tile(m.stay[1], keys ? &map : &map_do, &m.stay_full, keys ? s.v_head(kv) : u.head, row, blocks);
+                }
+                const KeyTiles kt = key_tiles(s, u.first, min(u.t.n, u.first + kTile), kTile);
+                const int of_head = u.steps / s.group;
+                int g = 0, q = 0;
+                for (int it = 0; it < u.steps && ok; ++it, ++n) {
+                    if (keys) {
+                        const int h = kv * s.group + g;
+                        const int64_t at = row + q * kTile;
+                        load(kLong, n, &map, s.q_head(h), at);
+                        longs = ok ? n + 1 : longs;
+                        if (ok) load(kShort, n, &map_do, h, at);
+                        if (++q == of_head) {
+                            q = 0;
+                            ++g;
+                        }
+                    } else {
+                        const int64_t at = u.t.row0 + static_cast<int64_t>(kt.at(it)) * kTile;
+                        load(kLong, n, &map, s.k_head(kv), at);
+                        longs = ok ? n + 1 : longs;
+                        if (ok) load(kShort, n, &map, s.v_head(kv), at);
+                    }
+                    shorts = ok ? n + 1 : shorts;
+                }
+            }
+            if (*abort_flag && leader) {
+                if (units) ptx::mbar_wait_drain(&m.stay_full, (units - 1) & 1);
+                for (int i = max(0, longs - 3); i < longs; ++i)
+                    ptx::mbar_wait_drain(&m.full[place_of(kLong, i)], round_of(kLong, i));
+                for (int i = max(0, shorts - 2); i < shorts; ++i)
+                    ptx::mbar_wait_drain(&m.full[place_of(kShort, i)], round_of(kShort, i));
+            }
+            __syncwarp();
+        } else if (warp == 9 || warp == 10) {
+            // ------------------------------------------------ products
+            const int i = warp - 9;
+            const bool leader = ptx::elect_one();
+            const uint32_t idesc = idesc_weighted(s.d), base = ptx::smem_u32(m.ring[0]),
+                           stays = ptx::smem_u32(m.stay[0]);
+            auto arrived = [&](int kind, int at) { wait(&m.full[place_of(kind, at)], round_of(kind, at), 31); };
+            auto tile = [&](int kind, int at) { return base + place_of(kind, at) * kTileBytes; };
+            auto free_place = [&](int kind, int at) { commit(leader, &m.empty[place_of(kind, at)]); };
+            int turns = 0;
+            while (ok && next_unit(u)) {
+                if (u.kind == kRest) continue;
+                // the unit before has left tensor memory, but for its results
+                if (units > 0) wait(&m.done, (units - 1) & 1, 35);
+                wait(&m.stay_full, units & 1, 32);
+                if (u.kind == kKeys) {
+                    // step `it`: the sum with the tile of step it - 1, then the scores (or dots) of this one
+                    const uint32_t t_in = i * 128, t_sum = i ? kSumK : kSumV;
+                    const int kind_in = i ? kShort : kLong, kind_of = i ? kLong : kShort;
+                    uint64_t *const ready = i ? &m.ds_ready : &m.p_ready;
+                    for (int it = 0; it <= u.steps && ok; ++it, ++n) {
+                        const bool scores = it < u.steps, sums = it > 0;
+                        if (scores) arrived(kind_in, n);
+                        if (sums) arrived(kind_of, n - 1);
+                        // a turn of the first warp, then one of the second
+                        if (i == 1 || turns > 0) wait(&m.turn[i], (i == 1 ? turns : turns - 1) & 1, 33);
+                        ++turns;
+                        if (sums) wait(ready, (n - 1) & 1, 34);
+                        if (!ok) break;
+                        ptx::tc_fence_after();
+                        if (sums) mma_weighted(leader, t_sum, t_in, 64, tile(kind_of, n - 1), idesc, it > 1);
+                        if (scores)
+                            mma_scores(leader, t_in, stays + i * kTileBytes, tile(kind_in, n), s.d,
+                                       i ? &m.dots : &m.scores[n & 1], &m.turn[i ^ 1]);
+                        else if (leader)
+                            ptx::mbar_arrive(&m.turn[i ^ 1]);
+                        if (it == u.steps - 1) commit(leader, &m.stay_empty);
+                        if (sums) free_place(kind_of, n - 1);
+                        if (scores) free_place(kind_in, n);
+                    }
+                    --n;  // the last turn was one more than there are steps
+                } else if (i == 0) {
+                    auto scores = [&](int at) {
+                        arrived(kLong, at);
+                        if (!ok) return;
+                        ptx::tc_fence_after();
+                        mma_scores(leader, (at & 1) * 128, stays, tile(kLong, at), s.d, &m.scores[at & 1]);
+                    };
+                    auto dots = [&](int at, bool first) {
+                        arrived(kShort, at);
+                        // dP before has been read; of a unit's first: and what is in its place
+                        if (first && units > 0) wait(&m.read, (units - 1) & 1, 26);
+                        if (!first) wait(&m.p_ready, (at - 1) & 1, 43);
+                        if (!ok) return;
+                        ptx::tc_fence_after();
+                        mma_scores(leader, kDots, stays + kTileBytes, tile(kShort, at), s.d, &m.dots);
+                        // the places are given back by two warps elsewhere
+                        free_place(kShort, at);
+                        free_place(kShort, at);
+                    };
+                    scores(n);
+                    dots(n, true);
+                    for (int it = 0; it < u.steps && ok; ++it, ++n) {
+                        if (it + 1 < u.steps) {
+                            scores(n + 1);
+                            dots(n + 1, false);
+                        }
+                        if (it == max(0, u.steps - 2) && ok) {
+                            commit(leader, &m.stay_empty);
+                            commit(leader, &m.stay_empty);
+                        }
+                        if (!wait(&m.ds_ready, n & 1, 47)) break;
+                        ptx::tc_fence_after();
+                        mma_weighted(leader, kSumQ, (n & 1) * 128, 64, tile(kLong, n), idesc, it > 0);
+                        free_place(kLong, n);
+                        free_place(kLong, n);
+                    }
+                } else {
+                    n += u.steps;
+                }
+                if (!ok) break;
+                ++units;
+                commit(leader, &m.done);
+            }
+            commit(leader, &m.drain);
+            if (lane == 0) ptx::mbar_wait_drain(&m.drain, 0);
+            __syncwarp();
+        } else if (warp == 11) {
+            // ------------------------------------------------ the queries' statistics; past the end P is 2^-inf
+            while (ok && next_unit(u)) {
+                if (u.kind != kKeys) continue;
+                const int of_head = u.steps / s.group;
+                for (int g = 0; g < s.group && ok; ++g) {
+                    const float2 *from = stats + (u.head * s.group + g) * s.T + u.t.row0;
+                    for (int q = 0; q < of_head; ++q, ++n) {
+                        float2 v[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int row = u.first + q * kTile + e * 32 + lane;
+                            v[e] = row < u.t.n ? from[row] : make_float2(INFINITY, 0.0f);
+                        }
+                        if (!wait(&m.stats_empty[n & 1], ((n >> 1) & 1) ^ 1, 29)) break;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            m.stats[n & 1][0][e * 32 + lane] = -v[e].x;  // both are subtracted
+                            m.stats[n & 1][1][e * 32 + lane] = -v[e].y;
+                        }
+                        ptx::mbar_arrive(&m.stats_full[n & 1]);
+                    }
+                }
+            }
+        } else if (warp == 12) {
+            // ------------------------------------------------ what comes next
+            int tiles;
+            const Tile rest = count_tiles(s, tiles);
+            bool zero = rest.head_rows + (s.T - rest.tail_row) != 0;
+            for (int r = 0;; ++r) {
+                Unit next{};
+                if (zero) {
+                    next.t = rest;
+                    next.kind = kRest;
+                    zero = false;
+                } else {
+                    int id = lane == 0 ? atomicAdd(shared.counter, 1) : 0;
+                    id = __shfl_sync(0xffffffffu, id, 0);
+                    next = find_unit(s, id, tiles);
+                }
+                if (!wait(&m.unit_empty[r & 1], ((r >> 1) & 1) ^ 1, 28)) break;
+                if (lane == 0) {
+                    m.unit[r & 1] = next;
+                    ptx::mbar_arrive(&m.unit_full[r & 1]);
+                }
+                __syncwarp();
+                if (next.kind == kEnd) break;
+            }
         }
     }
 
@@ -708,38 +741,54 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     __syncthreads();
     if (warp == 9) {
         ptx::tc_fence_after();
-        ptx::tmem_dealloc(tmem, kTmemCols);
+        ptx::tmem_dealloc(0, kTmemCols);
     }
-    if (*m.odd && !*m.abort_flag && threadIdx.x < kPlainThreads) {
+    // What is masked has met 0 times its value: a unit with results that are not finite is
+    // computed again where masked values are passed over.
+    int odd = m.odd;
+    if (odd < 0 || *abort_flag || threadIdx.x >= kPlainThreads) return;
+    int tiles;
+    count_tiles(s, tiles);
+    plain_sync();  // all have read m.odd
+    for (; odd >= 0; odd = shared.next[odd]) {
+        const Unit w = find_unit(s, odd, tiles);
 #pragma unroll 1
-        for (int q = q0; q < min(t.n, q0 + kTile); q += kRows) {
+        for (int at = w.first; at < min(w.t.n, w.first + kTile); at += kRows) {
             plain_sync();
-            plain_dq_tile(s, QKV, dO, stats, t.row0, t.n, q, h, dQKV, reinterpret_cast<float *>(m.tiles));
+            if (w.kind == kKeys)
+                plain_dkv_tile(s, QKV, dO, stats, w.t.row0, w.t.n, at, w.head, dQKV, reinterpret_cast<float *>(smem_raw));
+            else
+                plain_dq_tile(s, QKV, dO, stats, w.t.row0, w.t.n, at, w.head, dQKV, reinterpret_cast<float *>(smem_raw));
         }
     }
 }
 
 // ------------------------------------------------------------------ host
+// The workspace: statistics, the counter, the lists of odd units.
+inline int64_t units_of(int64_t T, int64_t n_heads, int64_t n_kv_heads, int64_t sequences) {
+    return (T / kTile + sequences) * (n_heads + n_kv_heads);
+}
+inline size_t stats_bytes(int64_t T, int64_t n_heads) {
+    return round_up(static_cast<size_t>(T * n_heads) * sizeof(float2), 256);
+}
+
 tpce_status tc_backward(const Shape &s, const void *QKV, const void *dO, const float2 *stats, void *dQKV,
                         cudaStream_t stream) {
+    const char *name = "attn_backward";
     CUtensorMap map, map_do;
     if (!make_tmap_heads(&map, QKV, s.d, s.n_q + 2 * s.n_kv, s.T, s.ld, kTile) ||
         !make_tmap_heads(&map_do, dO, s.d, s.n_q, s.T, static_cast<uint64_t>(s.n_q) * s.d, kTile))
-        return fail(TPCE_ERR_CUDA, "attn_backward: tensor map");
-    const int tiles = static_cast<int>(grid_tiles(s, kTile));
-    auto go = [&](auto kernel, const char *name, int heads) {
-        KernelTimer timer(name, stream);
-        const cudaError_t e = step::launch(kernel, static_cast<unsigned>(tiles) * heads, kBwdThreads, kBwdSmem,
-                                           stream, map, map_do, s, static_cast<const __nv_bfloat16 *>(QKV),
-                                           static_cast<const __nv_bfloat16 *>(dO), stats, tiles,
-                                           static_cast<__nv_bfloat16 *>(dQKV));
-        return e == cudaSuccess ? check_launch(name, stream) : fail_cuda(e, name);
-    };
-    cudaError_t e = allow_smem<tc_dkv_kernel>();
-    if (e == cudaSuccess) e = allow_smem<tc_dq_kernel>();
-    if (e != cudaSuccess) return fail_cuda(e, "attn_backward");
-    const tpce_status st = go(tc_dkv_kernel, "attn_dkv", s.n_kv);
-    return st != TPCE_OK ? st : go(tc_dq_kernel, "attn_dq", s.n_q);
+        return fail(TPCE_ERR_CUDA, "%s: tensor map", name);
+    cudaError_t e = allow_smem<tc_backward_kernel>();
+    if (e != cudaSuccess) return fail_cuda(e, name);
+    const int64_t units = units_of(s.T, s.n_q, s.n_kv, s.offsets ? s.sequences : 1);
+    char *after = reinterpret_cast<char *>(const_cast<float2 *>(stats)) + stats_bytes(s.T, s.n_q);
+    const Shared shared{reinterpret_cast<int *>(after), reinterpret_cast<int *>(after + 256)};
+    KernelTimer timer(name, stream);
+    e = step::launch(tc_backward_kernel, static_cast<unsigned>(std::min<int64_t>(units, num_sms())), kBwdThreads,
+                     sizeof(BwdSmem), stream, map, map_do, s, static_cast<const __nv_bfloat16 *>(QKV),
+                     static_cast<const __nv_bfloat16 *>(dO), stats, shared, static_cast<__nv_bfloat16 *>(dQKV));
+    return e == cudaSuccess ? check_launch(name, stream) : fail_cuda(e, name);
 }
 
 template <typename T>
@@ -767,7 +816,8 @@ tpce_status delta(const Shape &s, const void *dO, const void *O, const float *ls
     KernelTimer timer("attn_delta", stream);
     const cudaError_t e =
         step::launch(delta_kernel<T>, static_cast<unsigned>((s.T * s.n_q + 15) / 16), 256, 0, stream, s,
-                     static_cast<const T *>(dO), static_cast<const T *>(O), lse, stats);
+                     static_cast<const T *>(dO), static_cast<const T *>(O), lse, stats,
+                     reinterpret_cast<int *>(reinterpret_cast<char *>(stats) + stats_bytes(s.T, s.n_q)));
     return e == cudaSuccess ? check_launch("attn_delta", stream) : fail_cuda(e, "attn_delta");
 }
 
@@ -779,7 +829,8 @@ using namespace tpce;
 
 extern "C" size_t tpce_attn_core_workspace_bytes(int64_t T, int64_t n_heads) {
     if (T <= 0 || T > (int64_t{1} << 30) || n_heads < 1 || n_heads > 4096) return 0;
-    return static_cast<size_t>(T * n_heads) * sizeof(float2);
+    // no more tiles than rows, for query and key/value heads
+    return stats_bytes(T, n_heads) + 256 + static_cast<size_t>(T * 2 * n_heads) * sizeof(int);
 }
 
 extern "C" tpce_status tp_attn_core_backward(const void *dO, const void *QKV, const void *O, const float *lse,
