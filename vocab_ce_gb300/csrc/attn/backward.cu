@@ -230,6 +230,7 @@ struct BwdSmem {
     float stats[2][2][kTile];     // -lse log2(e) and -delta of a step's queries
     uint64_t full[kPlaces], empty[kPlaces], stay_full, stay_empty;
     uint64_t scores[2], dots, p_ready, ds_ready, stats_full[2], stats_empty[2], turn[2];
+    uint64_t sum_done;            // a step's sum of dQ is complete
     uint64_t done, read;          // a unit's products are complete; its results have been read
     uint64_t unit_full[2], unit_empty[2], drain;
     Unit unit[2];
@@ -312,8 +313,8 @@ __device__ __forceinline__ bool write_half(const float (&o)[2][32], float f, int
 //
 // Queries as rows, per tile of 128 keys:
 //   S = Q K^T, dP = dO V^T  ->  dS = 2^(S c - lse) (dP - delta)  ->  dQ += dS K
-// Tensor memory: two S (dS overwrites the one that it is made of), dP, dQ. One warp, in
-// the order  S(0) dP(0) | S(1) dP(1) dQ(0) | S(2) dP(2) dQ(1) | ..
+// Tensor memory: two S (dS overwrites the one that it is made of), dP, dQ. One warp issues
+// S, the other dP and dQ, in the order  S(0), dP(0), S(1), dP(1) dQ(0), S(2), dP(2) dQ(1), ..
 // dP of the next keys is begun as soon as the threads have read the one before, and P
 // is formed of the next S before dP has come.
 //
@@ -346,6 +347,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         ptx::mbar_init(&m.dots, 1);
         ptx::mbar_init(&m.p_ready, 8);
         ptx::mbar_init(&m.ds_ready, 8);
+        ptx::mbar_init(&m.sum_done, 1);
         ptx::mbar_init(&m.done, 2);
         ptx::mbar_init(&m.read, 8);
         ptx::mbar_init(&m.drain, 2);
@@ -605,15 +607,27 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const bool leader = ptx::elect_one();
             const uint32_t idesc = idesc_weighted(s.d), base = ptx::smem_u32(m.ring[0]),
                            stays = ptx::smem_u32(m.stay[0]);
-            auto arrived = [&](int kind, int at) { wait(&m.full[place_of(kind, at)], round_of(kind, at), 31); };
+            auto wait_for = [&](const auto &phases, uint32_t where) {
+                ok = ok && wait_each(phases, abort_flag, s.err, where);
+                return ok;
+            };
+            auto arrived = [&](bool needed, int kind, int at) {
+                return Phase{needed ? &m.full[place_of(kind, at)] : nullptr, round_of(kind, at)};
+            };
+            // a turn of the first warp, then one of the second
+            int turns = 0, sums_of_queries = 0;
+            auto my_turn = [&] {
+                const int before = i == 1 ? turns : turns - 1;
+                ++turns;
+                return Phase{before >= 0 ? &m.turn[i] : nullptr, before & 1u};
+            };
             auto tile = [&](int kind, int at) { return base + place_of(kind, at) * kTileBytes; };
             auto free_place = [&](int kind, int at) { commit(leader, &m.empty[place_of(kind, at)]); };
-            int turns = 0;
             while (ok && next_unit(u)) {
                 if (u.kind == kRest) continue;
                 // the unit before has left tensor memory, but for its results
-                if (units > 0) wait(&m.done, (units - 1) & 1, 35);
-                wait(&m.stay_full, units & 1, 32);
+                const Phase begin[2] = {{units > 0 ? &m.done : nullptr, (units - 1) & 1u}, {&m.stay_full, units & 1u}};
+                wait_for(begin, 32);
                 if (u.kind == kKeys) {
                     // step `it`: the sum with the tile of step it - 1, then the scores (or dots) of this one
                     const uint32_t t_in = i * 128, t_sum = i ? kSumK : kSumV;
@@ -621,13 +635,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     uint64_t *const ready = i ? &m.ds_ready : &m.p_ready;
                     for (int it = 0; it <= u.steps && ok; ++it, ++n) {
                         const bool scores = it < u.steps, sums = it > 0;
-                        if (scores) arrived(kind_in, n);
-                        if (sums) arrived(kind_of, n - 1);
-                        // a turn of the first warp, then one of the second
-                        if (i == 1 || turns > 0) wait(&m.turn[i], (i == 1 ? turns : turns - 1) & 1, 33);
-                        ++turns;
-                        if (sums) wait(ready, (n - 1) & 1, 34);
-                        if (!ok) break;
+                        const Phase phases[4] = {arrived(scores, kind_in, n), arrived(sums, kind_of, n - 1), my_turn(),
+                                                 {sums ? ready : nullptr, (n - 1) & 1u}};
+                        if (!wait_for(phases, 33)) break;
                         ptx::tc_fence_after();
                         if (sums) mma_weighted(leader, t_sum, t_in, 64, tile(kind_of, n - 1), idesc, it > 1);
                         if (scores)
@@ -641,43 +651,41 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     }
                     --n;  // the last turn was one more than there are steps
                 } else if (i == 0) {
-                    auto scores = [&](int at) {
-                        arrived(kLong, at);
-                        if (!ok) return;
-                        ptx::tc_fence_after();
-                        mma_scores(leader, (at & 1) * 128, stays, tile(kLong, at), s.d, &m.scores[at & 1]);
-                    };
-                    auto dots = [&](int at, bool first) {
-                        arrived(kShort, at);
-                        // dP before has been read; of a unit's first: and what is in its place
-                        if (first && units > 0) wait(&m.read, (units - 1) & 1, 26);
-                        if (!first) wait(&m.p_ready, (at - 1) & 1, 43);
-                        if (!ok) return;
-                        ptx::tc_fence_after();
-                        mma_scores(leader, kDots, stays + kTileBytes, tile(kShort, at), s.d, &m.dots);
-                        // the places are given back by two warps elsewhere
-                        free_place(kShort, at);
-                        free_place(kShort, at);
-                    };
-                    scores(n);
-                    dots(n, true);
                     for (int it = 0; it < u.steps && ok; ++it, ++n) {
-                        if (it + 1 < u.steps) {
-                            scores(n + 1);
-                            dots(n + 1, false);
-                        }
-                        if (it == max(0, u.steps - 2) && ok) {
-                            commit(leader, &m.stay_empty);
-                            commit(leader, &m.stay_empty);
-                        }
-                        if (!wait(&m.ds_ready, n & 1, 47)) break;
+                        // dS in this S's place has been used
+                        const Phase phases[3] = {arrived(true, kLong, n), my_turn(),
+                                                 {it > 1 ? &m.sum_done : nullptr, (sums_of_queries - 2) & 1u}};
+                        ++sums_of_queries;
+                        if (!wait_for(phases, 43)) break;
                         ptx::tc_fence_after();
-                        mma_weighted(leader, kSumQ, (n & 1) * 128, 64, tile(kLong, n), idesc, it > 0);
+                        mma_scores(leader, (n & 1) * 128, stays, tile(kLong, n), s.d, &m.scores[n & 1], &m.turn[1]);
                         free_place(kLong, n);
-                        free_place(kLong, n);
+                        if (it == u.steps - 1) commit(leader, &m.stay_empty);
                     }
                 } else {
-                    n += u.steps;
+                    auto sum = [&](int at, bool first) {
+                        if (!wait(&m.ds_ready, at & 1, 47)) return;
+                        ptx::tc_fence_after();
+                        mma_weighted(leader, kSumQ, (at & 1) * 128, 64, tile(kLong, at), idesc, !first);
+                        free_place(kLong, at);
+                        commit(leader, &m.sum_done);
+                    };
+                    for (int it = 0; it < u.steps && ok; ++it, ++n) {
+                        // dP before has been read; of a unit's first: what was in its place before
+                        const Phase phases[4] = {arrived(true, kShort, n), arrived(true, kLong, n), my_turn(),
+                                                 it > 0          ? Phase{&m.p_ready, (n - 1) & 1u}
+                                                 : units > 0     ? Phase{&m.read, (units - 1) & 1u}
+                                                                 : Phase{nullptr, 0}};
+                        if (!wait_for(phases, 26)) break;
+                        ptx::tc_fence_after();
+                        mma_scores(leader, kDots, stays + kTileBytes, tile(kShort, n), s.d, &m.dots, &m.turn[0]);
+                        // a place is given back by two warps elsewhere
+                        free_place(kShort, n);
+                        free_place(kShort, n);
+                        if (it == u.steps - 1) commit(leader, &m.stay_empty);
+                        if (it > 0) sum(n - 1, it == 1);
+                    }
+                    if (ok) sum(n - 1, u.steps == 1);
                 }
                 if (!ok) break;
                 ++units;

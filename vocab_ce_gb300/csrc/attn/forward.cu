@@ -478,17 +478,21 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             const uint32_t q_tile = ptx::smem_u32(m.q[0]) + i * kTileBytes, base = ptx::smem_u32(m.ring[0]);
             const uint32_t t_s = tmem + i * 128, t_o = tmem + 256 + i * 128;
             int pos = 0;  // tiles of the ring used so far
-            uint32_t p_phase = 0, o_phase = 0, q_phase = 0, turns = 0;
+            int turns = 0;
+            uint32_t p_phase = 0, o_phase = 0, q_phase = 0;
             bool ok = true;
             auto wait = [&](uint64_t *bar, uint32_t parity, uint32_t where) {
                 ok = ok && wait_all<true>(bar, parity, abort_flag, s.err, where);
             };
-            auto arrived = [&](int at) { wait(&m.full[at % kFwdStages], (at / kFwdStages) & 1, 22); };
+            auto arrived = [&](bool needed, int at) {
+                return Phase{needed ? &m.full[at % kFwdStages] : nullptr, (at / kFwdStages) & 1u};
+            };
             auto tile = [&](int at) { return base + (at % kFwdStages) * kTileBytes; };
             // each turn of tile 0 is followed by one of tile 1, with something to issue or without
             auto my_turn = [&] {
-                if (i == 1 || turns > 0) wait(&m.turn[i], (i == 1 ? turns : turns - 1) & 1, 32);
+                const int before = i == 1 ? turns : turns - 1;
                 ++turns;
+                return Phase{before >= 0 ? &m.turn[i] : nullptr, before & 1u};
             };
             Work w;
             while (ok && next_work(w)) {
@@ -503,17 +507,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     const int v_at = pos, k_at = u > 0 ? pos + 1 : pos;
                     const int k_now = u < pr.count ? pr.both.at(u) : -1, k_before = u > 0 ? pr.both.at(u - 1) : -1;
                     const bool sums = u > 0 && pr.needs(i, k_before), scores = u < pr.count && pr.needs(i, k_now);
-                    if (u < pr.count) arrived(k_at);
-                    if (u > 0) arrived(v_at);
-                    if (sums && !begun) {
-                        wait(&m.o_empty[i], o_phase ^ 1, 26);
-                        o_phase ^= 1;
-                    }
-                    my_turn();
-                    if (sums) {
-                        wait(&m.p_full[i], p_phase, 23);
-                        p_phase ^= 1;
-                    }
+                    const Phase phases[5] = {arrived(u < pr.count, k_at), arrived(u > 0, v_at), my_turn(),
+                                             {sums && !begun ? &m.o_empty[i] : nullptr, o_phase ^ 1},
+                                             {sums ? &m.p_full[i] : nullptr, p_phase}};
+                    if (sums && !begun) o_phase ^= 1;
+                    if (sums) p_phase ^= 1;
+                    ok = ok && wait_each(phases, abort_flag, s.err, 23);
                     if (!ok) break;
                     ptx::tc_fence_after();
                     if (sums) {
