@@ -15,27 +15,42 @@ namespace {
 using namespace attn;
 
 // ------------------------------------------------------------------ delta
-// stats[h, t] = (lse log2(e), delta): what the tiles need of a query. 16 lanes a row of
-// one head; bound by reading O and dO. The counter of the units that follow begins at 0.
+// stats[h, t] = (lse log2(e), delta): what the tiles need of a query. 16 lanes take
+// kDeltaRows rows of one head each, all loads of which are under way together; bound by
+// reading O and dO. The counter of the units that follow begins at 0.
+constexpr int kDeltaRows = 4;
 template <typename T>
 __global__ void __launch_bounds__(256) delta_kernel(const Shape s, const T *dO, const T *O, const float *lse,
                                                     float2 *__restrict__ stats, int *counter) {
     grid_begin();
     if (blockIdx.x == 0 && threadIdx.x == 0) *counter = 0;
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 16 + threadIdx.x / 16;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * 16 * kDeltaRows + threadIdx.x / 16, rows = s.T * s.n_q;
     const int lane = threadIdx.x & 15;
-    const int64_t t = i / s.n_q;
-    const int h = static_cast<int>(i - t * s.n_q);
-    float sum = 0.0f;
-    if (t < s.T && lane * 8 < s.d) {
-        float a[8], b[8];
-        unpack8(load8(dO + i * s.d + lane * 8), a);
-        unpack8(load8(O + i * s.d + lane * 8), b);
+    Raw8<T> a[kDeltaRows], b[kDeltaRows];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) sum = fmaf(a[c], b[c], sum);
+    for (int k = 0; k < kDeltaRows; ++k) {
+        const int64_t i = first + 16 * k;
+        zero8(a[k]);
+        zero8(b[k]);
+        if (i < rows && lane * 8 < s.d) {
+            a[k] = load8(dO + i * s.d + lane * 8);
+            b[k] = load8(O + i * s.d + lane * 8);
+        }
     }
-    sum = sum16(sum);
-    if (t < s.T && lane == 0) stats[h * s.T + t] = make_float2(lse[h * s.T + t] * kLog2e, sum);
+#pragma unroll
+    for (int k = 0; k < kDeltaRows; ++k) {
+        const int64_t i = first + 16 * k;
+        float x[8], y[8], sum = 0.0f;
+        unpack8(a[k], x);
+        unpack8(b[k], y);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) sum = fmaf(x[c], y[c], sum);
+        sum = sum16(sum);
+        if (i < rows && lane == 0) {
+            const int64_t at = i % s.n_q * s.T + i / s.n_q;
+            stats[at] = make_float2(lse[at] * kLog2e, sum);
+        }
+    }
 }
 
 // ------------------------------------------------------------------ plain tiles
@@ -823,7 +838,7 @@ tpce_status delta(const Shape &s, const void *dO, const void *O, const float *ls
                   cudaStream_t stream) {
     KernelTimer timer("attn_delta", stream);
     const cudaError_t e =
-        step::launch(delta_kernel<T>, static_cast<unsigned>((s.T * s.n_q + 15) / 16), 256, 0, stream, s,
+        step::launch(delta_kernel<T>, static_cast<unsigned>((s.T * s.n_q + 16 * kDeltaRows - 1) / (16 * kDeltaRows)), 256, 0, stream, s,
                      static_cast<const T *>(dO), static_cast<const T *>(O), lse, stats,
                      reinterpret_cast<int *>(reinterpret_cast<char *>(stats) + stats_bytes(s.T, s.n_q)));
     return e == cudaSuccess ? check_launch("attn_delta", stream) : fail_cuda(e, "attn_delta");

@@ -14,6 +14,7 @@
 // cut leaves fp32 sums in the workspace that a last kernel adds in order.
 // All of it is bound by HBM.
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <initializer_list>
@@ -68,16 +69,19 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // ------------------------------------------------------------------ the sort
-// Passes over kDigit bits, the lowest first. A block takes a chunk of the tokens,
-// each of its warps a contiguous run of the chunk. One block does all passes in
-// one launch; several count their digits in one launch and place in the next.
-constexpr int kWarps = kThreads / 32;
-constexpr int kMaxBins = 1024;
-constexpr int64_t kSortChunk = 1024, kSortBlocks = 256;
+// Passes over up to ten bits, the lowest first. A block takes a chunk of the tokens,
+// each of its warps a contiguous run of the chunk. Up to kClusterTokens tokens are
+// sorted by the blocks of one cluster in one launch, which read each other's counts of
+// digits (16,384 tokens over 129,024 ids: two launches a pass took 22 us, this one
+// takes SORT us); for more the blocks' counts are one launch and their places the next.
+constexpr int kClusterThreads = 1024;
+constexpr int kMaxBins = 1024, kCluster = 8;
+constexpr int64_t kSortChunk = 1024, kSortBlocks = 256, kClusterTokens = 65536;
 
 struct SortSplit {
     int64_t chunk;
     int blocks, passes, bits;  // bits of a pass
+    bool cluster;              // one of `blocks` blocks
 };
 inline SortSplit sort_split(int64_t tokens, int64_t v_pad) {
     SortSplit sp{};
@@ -85,9 +89,15 @@ inline SortSplit sort_split(int64_t tokens, int64_t v_pad) {
     while ((int64_t{1} << all) <= v_pad) ++all;
     sp.passes = (all + 9) / 10;
     sp.bits = (all + sp.passes - 1) / sp.passes;
+    sp.cluster = tokens <= kClusterTokens;
     sp.chunk = std::max<int64_t>(kSortChunk, (tokens + kSortBlocks - 1) / kSortBlocks);
-    sp.blocks = tokens <= 2 * sp.chunk ? 1 : static_cast<int>((tokens + sp.chunk - 1) / sp.chunk);
-    if (sp.blocks == 1) sp.chunk = tokens;
+    if (sp.cluster) {
+        sp.blocks = 1;
+        while (sp.blocks < kCluster && sp.blocks * kSortChunk < tokens) sp.blocks *= 2;
+        sp.chunk = (tokens + sp.blocks - 1) / sp.blocks;
+    } else {
+        sp.blocks = static_cast<int>((tokens + sp.chunk - 1) / sp.chunk);
+    }
     return sp;
 }
 
@@ -116,57 +126,94 @@ __global__ void __launch_bounds__(kThreads)
         counts[static_cast<int64_t>(blockIdx.x) * bins + b] = count[b];
 }
 
-// One pass of a block: from keys (of the tokens from[i], or of i itself) to key_out and token_out.
-// counts NULL: this block is the only one.
-__device__ void sort_pass(const int32_t *keys, const int32_t *from, int64_t n, int64_t chunk, int shift, int bits,
-                          const uint32_t *counts, int32_t v_valid, int32_t v_pad, int32_t *key_out,
-                          int32_t *token_out, uint32_t *smem, uint32_t *scan, uint32_t *err) {
+__device__ __forceinline__ uint32_t load_cluster(uint32_t addr) {
+    uint32_t x;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(addr) : "memory");
+    return x;
+}
+
+// One pass of block `block` of `blocks`: from keys (of the tokens from[i], or of i itself) to key_out and
+// token_out. counts: of all blocks' digits, from the launch before; NULL: the blocks are a cluster (or one).
+// C holds a warp's counts and places; a cluster's tokens fit 16 bits.
+template <int THREADS, typename C>
+__host__ __device__ constexpr size_t sort_smem(int bits) {
+    return (size_t{THREADS / 32} * sizeof(C) + 3 * sizeof(uint32_t)) << bits;
+}
+template <int THREADS, typename C>
+__device__ void sort_pass(const int32_t *keys, const int32_t *from, int64_t n, int64_t chunk, int block, int blocks,
+                          int shift, int bits, const uint32_t *counts, int32_t v_valid, int32_t v_pad,
+                          int32_t *key_out, int32_t *token_out, uint32_t *smem, uint32_t *scan, uint32_t *err) {
+    constexpr int kWarps = THREADS / 32, kInWord = 4 / sizeof(C);
     const int bins = 1 << bits;
-    uint32_t *count = smem;                    // [kWarps][bins], then the next place of each warp's digits
-    uint32_t *all = smem + kWarps * bins;      // [bins] of all blocks
-    uint32_t *below = all + bins;              // [bins] of the blocks before
+    uint32_t *all = smem;                        // [bins] of all blocks
+    uint32_t *below = all + bins;                // [bins] of the blocks before
+    uint32_t *total = below + bins;              // [bins] of this block
+    uint32_t *words = total + bins;              // [kWarps][bins], then the next place of each warp's digits
+    C *count = reinterpret_cast<C *>(words);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const bool ids = from == nullptr;
-    for (int b = threadIdx.x; b < (kWarps + 2) * bins; b += kThreads) smem[b] = 0u;
+    for (int b = threadIdx.x; b < 2 * bins; b += THREADS) smem[b] = 0u;
+    for (int b = threadIdx.x; b < kWarps * bins / kInWord; b += THREADS) words[b] = 0u;
     __syncthreads();
     if (counts) {
         int width = 1;
-        while (width < bins && width < kThreads) width *= 2;
-        const int parts = kThreads / width, part = threadIdx.x / width;
+        while (width < bins && width < THREADS) width *= 2;
+        const int parts = THREADS / width, part = threadIdx.x / width;
         for (int b = threadIdx.x & (width - 1); b < bins; b += width) {
             uint32_t sum = 0u, before = 0u;
 #pragma unroll 8
-            for (int q = part; q < static_cast<int>(gridDim.x); q += parts) {
+            for (int q = part; q < blocks; q += parts) {
                 const uint32_t c = counts[static_cast<int64_t>(q) * bins + b];
                 sum += c;
-                before += q < static_cast<int>(blockIdx.x) ? c : 0u;
+                before += q < block ? c : 0u;
             }
             atomicAdd(&all[b], sum);
             atomicAdd(&below[b], before);
         }
     }
-    const int64_t begin = blockIdx.x * chunk, end = min(n, begin + chunk);
+    const int64_t begin = min(n, block * chunk), end = min(n, begin + chunk);
     const int64_t run = ((end - begin + kWarps - 1) / kWarps + 31) / 32 * 32;
-    const int64_t first = begin + warp * run, last = min(end, first + run);
-    uint32_t *mine = count + warp * bins;
+    const int64_t first = min(end, begin + warp * run), last = min(end, first + run);
+    C *mine = count + warp * bins;
     auto digit = [&](int32_t k) { return (k >> shift) & (bins - 1); };
 #pragma unroll 4
-    for (int64_t i = first + lane; i < last; i += 32)
-        atomicAdd(&mine[digit(ids ? key_of(keys[i], v_valid, v_pad, err) : keys[i])], 1u);
+    for (int64_t i = first + lane; i < last; i += 32) {
+        const int at = warp * bins + digit(ids ? key_of(keys[i], v_valid, v_pad, err) : keys[i]);
+        atomicAdd(&words[at / kInWord], 1u << (at % kInWord * (8 * sizeof(C) % 32)));
+    }
     __syncthreads();
-    for (int b = threadIdx.x; b < bins; b += kThreads) {
+    for (int b = threadIdx.x; b < bins; b += THREADS) {
         uint32_t sum = 0u;
 #pragma unroll
         for (int q = 0; q < kWarps; ++q) {
             const uint32_t c = count[q * bins + b];
-            count[q * bins + b] = sum;
+            count[q * bins + b] = static_cast<C>(sum);
             sum += c;
         }
-        if (!counts) all[b] = sum;
+        total[b] = sum;
+        if (!counts && blocks == 1) all[b] = sum;
     }
     __syncthreads();
+    if (!counts && blocks > 1) {
+        ptx::cluster_sync();
+        for (int b = threadIdx.x; b < bins; b += THREADS) {
+            uint32_t sum = 0u, before = 0u;
+            const uint32_t at = ptx::smem_u32(&total[b]);
+            uint32_t c[kCluster];
+#pragma unroll
+            for (int q = 0; q < kCluster; ++q) c[q] = q < blocks ? load_cluster(ptx::mapa_shared(at, q)) : 0u;
+#pragma unroll
+            for (int q = 0; q < kCluster; ++q) {
+                sum += c[q];
+                before += q < block ? c[q] : 0u;
+            }
+            all[b] = sum;
+            below[b] = before;
+        }
+        __syncthreads();
+    }
     // first places: a scan over the digits, adjacent ones a thread
-    constexpr int kEach = kMaxBins / kThreads;
+    constexpr int kEach = kMaxBins / THREADS;
     uint32_t own[kEach], sum = 0u;
 #pragma unroll
     for (int u = 0; u < kEach; ++u) {
@@ -190,7 +237,8 @@ __device__ void sort_pass(const int32_t *keys, const int32_t *from, int64_t n, i
         if (b < bins) {
             const uint32_t place = at + below[b];
             at += own[u];
-            for (int q = 0; q < kWarps; ++q) count[q * bins + b] += place;
+#pragma unroll 8
+            for (int q = 0; q < kWarps; ++q) count[q * bins + b] = static_cast<C>(count[q * bins + b] + place);
         }
     }
     __syncthreads();
@@ -205,6 +253,7 @@ __device__ void sort_pass(const int32_t *keys, const int32_t *from, int64_t n, i
         }
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
+            if (i0 + u * 32 >= last) break;
             const bool there = i0 + u * 32 + lane < last;
             const int d = there ? digit(k[u]) : bins;
             const uint32_t same = same_value(d, bits + 1);
@@ -212,7 +261,7 @@ __device__ void sort_pass(const int32_t *keys, const int32_t *from, int64_t n, i
             uint32_t p = UINT_MAX;
             if (there) p = mine[d] + before;
             __syncwarp();
-            if (there && before == 0u) mine[d] += __popc(same);
+            if (there && before == 0u) mine[d] = static_cast<C>(mine[d] + __popc(same));
             __syncwarp();
             // an id that changes while it is sorted must lead nowhere
             if (there && p < n) {
@@ -228,26 +277,39 @@ __global__ void __launch_bounds__(kThreads)
                        const uint32_t *counts, int32_t v_valid, int32_t v_pad, int32_t *key_out, int32_t *token_out,
                        uint32_t *err) {
     extern __shared__ uint32_t smem[];
-    __shared__ uint32_t scan[kWarps];
+    __shared__ uint32_t scan[kThreads / 32];
     grid_begin();
-    sort_pass(keys, from, n, chunk, shift, bits, counts, v_valid, v_pad, key_out, token_out, smem, scan, err);
+    sort_pass<kThreads, uint32_t>(keys, from, n, chunk, blockIdx.x, gridDim.x, shift, bits, counts, v_valid, v_pad, key_out, token_out,
+              smem, scan, err);
 }
 
-// All passes of few tokens; the last one ends in key[1], token[1] (odd passes) or key[0], token[0].
+// All passes of a cluster's tokens; the last one ends in key[1], token[1] (odd passes) or key[0], token[0].
+// The blocks after the first `blocks`, if there are any, write zeros to the table meanwhile: all of it, since
+// which rows will be written again is not known yet.
 struct SortBuffers {
     int32_t *key[2], *token[2];
 };
-__global__ void __launch_bounds__(kThreads)
-    embed_sort_kernel(const int32_t *ids, int64_t n, int passes, int bits, int32_t v_valid, int32_t v_pad,
-                      SortBuffers buf, uint32_t *err) {
+__global__ void __launch_bounds__(kClusterThreads)
+    embed_sort_kernel(const int32_t *ids, int64_t n, int64_t chunk, int blocks, int passes, int bits, int32_t v_valid,
+                      int32_t v_pad, SortBuffers buf, uint4 *table, int64_t vectors, uint32_t *err) {
     extern __shared__ uint32_t smem[];
-    __shared__ uint32_t scan[kWarps];
+    __shared__ uint32_t scan[kClusterThreads / 32];
     grid_begin();
+    if (static_cast<int>(blockIdx.x) >= blocks) {
+        const int64_t stride = static_cast<int64_t>(gridDim.x - blocks) * kClusterThreads;
+        for (int64_t i = static_cast<int64_t>(blockIdx.x - blocks) * kClusterThreads + threadIdx.x; i < vectors; i += stride)
+            table[i] = make_uint4(0u, 0u, 0u, 0u);
+        return;
+    }
     for (int p = 0; p < passes; ++p) {
         const int to = (p + 1) & 1;
-        sort_pass(p ? buf.key[to ^ 1] : ids, p ? buf.token[to ^ 1] : nullptr, n, n, p * bits, bits, nullptr, v_valid,
-                  v_pad, buf.key[to], buf.token[to], smem, scan, err);
-        __syncthreads();  // the block's stores to global memory, too, are seen by its threads after this
+        sort_pass<kClusterThreads, uint16_t>(p ? buf.key[to ^ 1] : ids, p ? buf.token[to ^ 1] : nullptr, n, chunk, blockIdx.x, blocks, p * bits,
+                  bits, nullptr, v_valid, v_pad, buf.key[to], buf.token[to], smem, scan, err);
+        // the next pass reads what all blocks have written, and writes counts that they have read
+        if (blocks > 1)
+            ptx::cluster_sync();
+        else
+            __syncthreads();
     }
 }
 
@@ -302,7 +364,7 @@ constexpr int kFillRows = 32;
 // them each; the others add up chunks. Loads are issued four tokens at a time, with
 // the old row where a run ends.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
     embed_sum_kernel(const T *dX, const int32_t *key, const int32_t *token, int64_t n, int64_t v_pad, int vectors,
                      SumSplit sp, unsigned fill, bool add, float scale, float *__restrict__ partial, T *dE) {
     grid_begin();
@@ -373,33 +435,60 @@ __global__ void __launch_bounds__(kThreads, 4)
     }
 }
 
-// The runs that cross a cut, by the chunk that they begin in.
+// The runs that cross a cut, by the chunk that they begin in: a block looks at
+// kJoinChunks chunks, a lane at one, and adds up the runs that it finds for its columns.
+// (A warp for each chunk and 256 columns took 52 us for 1024 chunks of 8192 columns,
+// nearly all of it warps that found nothing; JOIN.)
+constexpr int kJoinChunks = 8;
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
-    embed_join_kernel(const int32_t *key, int64_t n, int64_t v_pad, int vectors, SumSplit sp, bool add, float scale,
-                      const float *partial, T *dE) {
-    const int64_t piece = static_cast<int64_t>(blockIdx.x) * (kThreads / sp.lanes) + threadIdx.x / sp.lanes;
-    const int64_t c = piece / sp.parts;
-    const int at = static_cast<int>(piece - c * sp.parts) * sp.lanes + (threadIdx.x & (sp.lanes - 1));
+__global__ void __launch_bounds__(kThreads, 2)
+    embed_join_kernel(const int32_t *key, int64_t n, int64_t v_pad, int vectors, SumSplit sp, unsigned groups,
+                      bool add, float scale, const float *partial, T *dE) {
+    const int lane = threadIdx.x & 31;
+    const int at = static_cast<int>(blockIdx.x / groups) * kThreads + threadIdx.x;
     grid_begin();
-    if (c >= sp.chunks - 1 || at >= vectors) return;
-    const int64_t p0 = c * sp.chunk, p1 = p0 + sp.chunk;  // not the last chunk: p1 < n
-    const int32_t k = key[p1];
-    if (static_cast<uint32_t>(k) >= v_pad || key[p1 - 1] != k) return;
-    if (key[p0] == k && p0 > 0 && key[p0 - 1] == k) return;  // begun before this chunk
-    T *row = dE + (static_cast<int64_t>(k) * vectors + at) * 8;
-    Raw8<T> old;
-    zero8(old);
-    if (add) old = load8(row);
-    float sum[8];
-    load8f(partial + ((2 * c + 1) * vectors + at) * 8, sum);
-    for (int64_t m = c + 1; m < sp.chunks && key[m * sp.chunk] == k; ++m) {
-        float v[8];
-        load8f(partial + (2 * m * vectors + at) * 8, v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum[i] += v[i];
+    const int64_t c0 = static_cast<int64_t>(blockIdx.x % groups) * kJoinChunks, mine = c0 + lane;
+    int32_t k = -1;
+    if (lane < kJoinChunks && mine < sp.chunks - 1) {  // not the last chunk: p1 < n
+        const int64_t p0 = mine * sp.chunk, p1 = p0 + sp.chunk;
+        const int32_t next = key[p1], last = key[p1 - 1], first = key[p0], before = p0 > 0 ? key[p0 - 1] : -1;
+        if (static_cast<uint32_t>(next) < v_pad && last == next && !(first == next && before == next)) k = next;
     }
-    finish_row(sum, old, add, scale, row);
+    for (uint32_t left = __ballot_sync(0xffffffffu, k >= 0); left != 0; left &= left - 1) {
+        const int who = __ffs(left) - 1;
+        const int32_t id = __shfl_sync(0xffffffffu, k, who);
+        const int64_t c = c0 + who;
+        const bool there = at < vectors;
+        T *row = dE + (static_cast<int64_t>(id) * vectors + at) * 8;
+        Raw8<T> old;
+        zero8(old);
+        float sum[8] = {};
+        if (there) {
+            if (add) old = load8(row);
+            load8f(partial + ((2 * c + 1) * vectors + at) * 8, sum);
+        }
+        // the chunks after it that begin with the run, kBatch at a time
+        constexpr int kBatch = 8;
+        for (int64_t m = c + 1; m < sp.chunks; m += 32) {
+            const bool on = m + lane < sp.chunks && key[(m + lane) * sp.chunk] == id;
+            const uint32_t which = __ballot_sync(0xffffffffu, on);
+            const int count = which == 0xffffffffu ? 32 : __ffs(~which) - 1;
+            for (int j0 = 0; j0 < count && there; j0 += kBatch) {
+                float v[kBatch][8];
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j)
+                    if (j0 + j < count) load8f(partial + (2 * (m + j0 + j) * vectors + at) * 8, v[j]);
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    if (j0 + j >= count) break;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) sum[i] += v[j][i];
+                }
+            }
+            if (count < 32) break;
+        }
+        if (there) finish_row(sum, old, add, scale, row);
+    }
 }
 
 // ------------------------------------------------------------------ host
@@ -445,7 +534,7 @@ inline Layout layout_of(int64_t T, int64_t h, int64_t v_pad) {
     l.each = round_up(static_cast<size_t>(T) * sizeof(int32_t), 256);
     l.counts = 4 * l.each;
     l.partial = l.counts +
-                round_up(so.blocks > 1 ? static_cast<size_t>(so.blocks) * (size_t{4} << so.bits) : 0, 256);
+                round_up(!so.cluster ? static_cast<size_t>(so.blocks) * (size_t{4} << so.bits) : 0, 256);
     l.total = l.partial + (su.chunks > 1 ? 2 * static_cast<size_t>(su.chunks) * static_cast<size_t>(h) * 4 : 0);
     return l;
 }
@@ -456,9 +545,9 @@ tpce_status embed_forward(const int32_t *ids, const void *E, int64_t tokens, int
     const int vectors = static_cast<int>(h / 8);
     int lanes = 8;
     while (lanes < kThreads && lanes * 2 < vectors) lanes *= 2;
-    // two vectors a thread, one where that would leave SMs without a block
-    const bool few = tokens * vectors < int64_t{2} * kThreads * 2 * num_sms();
-    const int each = lanes * (few ? 1 : 2);
+    // four vectors a thread (16,384 rows of 8192 bf16: 66 us, with two 70), one where that would leave SMs idle
+    const bool few = tokens * vectors < int64_t{4} * kThreads * 2 * num_sms();
+    const int each = lanes * (few ? 1 : 4);
     const int parts = (vectors + each - 1) / each;
     const unsigned blocks = static_cast<unsigned>((tokens * parts + kThreads / lanes - 1) / (kThreads / lanes));
     KernelTimer timer("embed_forward", s);
@@ -466,18 +555,35 @@ tpce_status embed_forward(const int32_t *ids, const void *E, int64_t tokens, int
         return launch(kernel, blocks, kThreads, 0, s, static_cast<const T *>(E), ids, tokens, v_valid, vectors, lanes,
                       parts, scale, static_cast<T *>(X), device_error_word());
     };
-    const cudaError_t e = few ? go(embed_forward_kernel<T, 1>) : go(embed_forward_kernel<T, 2>);
+    const cudaError_t e = few ? go(embed_forward_kernel<T, 1>) : go(embed_forward_kernel<T, 4>);
     return e == cudaSuccess ? check_launch("embed_forward", s) : fail_cuda(e, "embed_forward");
 }
 
+// table: what is to be zeroed meanwhile (a cluster's sort only), or NULL
 tpce_status embed_sort(const int32_t *ids, int64_t T, int64_t v_pad, int64_t v_valid, const SortSplit &sp,
-                       const SortBuffers &buf, uint32_t *counts, cudaStream_t s) {
-    const size_t smem = (kWarps + 2) * (size_t{4} << sp.bits);
+                       const SortBuffers &buf, uint32_t *counts, void *table, size_t table_bytes, cudaStream_t s) {
     const int32_t valid = static_cast<int32_t>(v_valid), pad = static_cast<int32_t>(v_pad);
     KernelTimer timer("embed_sort", s);
-    if (sp.blocks == 1) {
-        const cudaError_t e = launch(embed_sort_kernel, 1, kThreads, smem, s, ids, T, sp.passes, sp.bits, valid, pad,
-                                     buf, device_error_word());
+    if (sp.cluster) {
+        static std::atomic<uint64_t> allowed{0};  // devices on which the kernel may have more than 48 KB
+        const size_t smem = sort_smem<kClusterThreads, uint16_t>(sp.bits);
+        int dev = 0;
+        cudaError_t e = taken(cudaGetDevice(&dev));
+        const uint64_t bit = uint64_t{1} << (dev & 63);
+        if (e == cudaSuccess && !(allowed.load() & bit)) {
+            e = taken(cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           static_cast<int>(sort_smem<kClusterThreads, uint16_t>(10))));
+            if (e == cudaSuccess) allowed.fetch_or(bit);
+        }
+        if (e != cudaSuccess) return fail_cuda(e, "embed_sort");
+        // a block an SM zeroes the table, or fewer
+        const int64_t vectors = table ? static_cast<int64_t>(table_bytes / 16) : 0;
+        const int64_t fill = std::min<int64_t>((vectors + 4 * kClusterThreads - 1) / (4 * kClusterThreads),
+                                               int64_t{2} * num_sms());
+        const unsigned blocks = static_cast<unsigned>((sp.blocks + fill + sp.blocks - 1) / sp.blocks * sp.blocks);
+        e = launch_clusters(sp.blocks, embed_sort_kernel, blocks, kClusterThreads, smem, s, ids, T, sp.chunk, sp.blocks,
+                            sp.passes, sp.bits, valid, pad, buf, static_cast<uint4 *>(table), vectors,
+                            device_error_word());
         return e == cudaSuccess ? check_launch("embed_sort", s) : fail_cuda(e, "embed_sort");
     }
     for (int p = 0; p < sp.passes; ++p) {
@@ -488,7 +594,7 @@ tpce_status embed_sort(const int32_t *ids, int64_t T, int64_t v_pad, int64_t v_v
         if (e != cudaSuccess) return fail_cuda(e, "embed_count");
         tpce_status st = check_launch("embed_count", s);
         if (st != TPCE_OK) return st;
-        e = launch(embed_place_kernel, sp.blocks, kThreads, smem, s, keys, from, T, sp.chunk, p * sp.bits, sp.bits,
+        e = launch(embed_place_kernel, sp.blocks, kThreads, sort_smem<kThreads, uint32_t>(sp.bits), s, keys, from, T, sp.chunk, p * sp.bits, sp.bits,
                    counts, valid, pad, buf.key[to], buf.token[to], device_error_word());
         if (e != cudaSuccess) return fail_cuda(e, "embed_place");
         if ((st = check_launch("embed_place", s)) != TPCE_OK) return st;
@@ -498,12 +604,13 @@ tpce_status embed_sort(const int32_t *ids, int64_t T, int64_t v_pad, int64_t v_v
 
 template <typename T>
 tpce_status embed_sums(const void *dX, int64_t tokens, int64_t h, int64_t v_pad, const int32_t *key,
-                       const int32_t *token, float scale, bool add, float *partial, void *dE, cudaStream_t s) {
+                       const int32_t *token, float scale, bool add, bool zeroed, float *partial, void *dE,
+                       cudaStream_t s) {
     const SumSplit sp = sum_split(tokens, h);
     const int vectors = static_cast<int>(h / 8);
     const int64_t of_block = kThreads / sp.lanes;
     const int64_t blocks = (static_cast<int64_t>(sp.chunks) * sp.parts + of_block - 1) / of_block;
-    const unsigned fill = add ? 0u : static_cast<unsigned>((v_pad + kFillRows - 1) / kFillRows);
+    const unsigned fill = add || zeroed ? 0u : static_cast<unsigned>((v_pad + kFillRows - 1) / kFillRows);
     {
         KernelTimer timer("embed_sum", s);
         const cudaError_t e =
@@ -515,8 +622,10 @@ tpce_status embed_sums(const void *dX, int64_t tokens, int64_t h, int64_t v_pad,
         if (st != TPCE_OK || sp.chunks == 1) return st;
     }
     KernelTimer timer("embed_join", s);
-    const cudaError_t e = launch(embed_join_kernel<T>, static_cast<unsigned>(blocks), kThreads, 0, s, key, tokens,
-                                 v_pad, vectors, sp, add, scale, partial, static_cast<T *>(dE));
+    const unsigned groups = static_cast<unsigned>((sp.chunks + kJoinChunks - 1) / kJoinChunks);
+    const cudaError_t e = launch(embed_join_kernel<T>, groups * static_cast<unsigned>((vectors + kThreads - 1) / kThreads),
+                                 kThreads, 0, s, key, tokens, v_pad, vectors, sp, groups, add, scale, partial,
+                                 static_cast<T *>(dE));
     return e == cudaSuccess ? check_launch("embed_join", s) : fail_cuda(e, "embed_join");
 }
 
@@ -580,11 +689,12 @@ extern "C" tpce_status tp_embedding_backward(const void *dX, const int32_t *ids,
     uint32_t *counts = reinterpret_cast<uint32_t *>(base + l.counts);
     float *partial = reinterpret_cast<float *>(base + l.partial);
     const SortSplit sp = sort_split(T, v_pad);
-    if ((st = embed_sort(ids, T, v_pad, v_valid, sp, buf, counts, s)) != TPCE_OK) return st;
+    const bool zeroed = sp.cluster && !accumulate;
+    if ((st = embed_sort(ids, T, v_pad, v_valid, sp, buf, counts, zeroed ? dE : nullptr, table, s)) != TPCE_OK) return st;
     const int last = sp.passes & 1;
     return dtype == TPCE_BF16
                ? embed_sums<__nv_bfloat16>(dX, T, h, v_pad, buf.key[last], buf.token[last], scale, accumulate != 0,
-                                           partial, dE, s)
-               : embed_sums<float>(dX, T, h, v_pad, buf.key[last], buf.token[last], scale, accumulate != 0, partial,
-                                   dE, s);
+                                           zeroed, partial, dE, s)
+               : embed_sums<float>(dX, T, h, v_pad, buf.key[last], buf.token[last], scale, accumulate != 0, zeroed,
+                                   partial, dE, s);
 }
