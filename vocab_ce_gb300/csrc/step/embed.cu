@@ -75,6 +75,7 @@ __global__ void __launch_bounds__(kThreads)
 // digits (16,384 tokens over 129,024 ids: two launches a pass took 22 us, this one
 // takes SORT us); for more the blocks' counts are one launch and their places the next.
 constexpr int kClusterThreads = 1024;
+constexpr int64_t kZeroed = 96 << 20;
 constexpr int kMaxBins = 1024, kCluster = 8;
 constexpr int64_t kSortChunk = 1024, kSortBlocks = 256, kClusterTokens = 65536;
 
@@ -284,8 +285,8 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // All passes of a cluster's tokens; the last one ends in key[1], token[1] (odd passes) or key[0], token[0].
-// The blocks after the first `blocks`, if there are any, write zeros to the table meanwhile: all of it, since
-// which rows will be written again is not known yet.
+// The blocks after the first `blocks`, if there are any, write zeros to the table's first rows meanwhile, as many
+// as the sort leaves time for (kZeroed bytes), whether tokens name them or not: that is not known yet.
 struct SortBuffers {
     int32_t *key[2], *token[2];
 };
@@ -360,17 +361,18 @@ __device__ __forceinline__ bool among(const int32_t *key, int64_t n, int32_t v) 
 
 constexpr int kFillRows = 32;
 
-// The first `fill` blocks write zeros to the rows that no token names, kFillRows of
-// them each; the others add up chunks. Loads are issued four tokens at a time, with
+// The first `fill` blocks write zeros to the rows from `zeroed` on that no token names,
+// kFillRows of them each; the others add up chunks. Loads are issued four tokens at a time, with
 // the old row where a run ends.
 template <typename T>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
     embed_sum_kernel(const T *dX, const int32_t *key, const int32_t *token, int64_t n, int64_t v_pad, int vectors,
-                     SumSplit sp, unsigned fill, bool add, float scale, float *__restrict__ partial, T *dE) {
+                     SumSplit sp, unsigned fill, int64_t zeroed, bool add, float scale, float *__restrict__ partial,
+                     T *dE) {
     grid_begin();
     if (blockIdx.x < fill) {
         __shared__ bool named[kFillRows];
-        const int64_t v0 = static_cast<int64_t>(blockIdx.x) * kFillRows;
+        const int64_t v0 = zeroed + static_cast<int64_t>(blockIdx.x) * kFillRows;
         if (threadIdx.x < kFillRows) {
             const int64_t v = v0 + threadIdx.x;
             named[threadIdx.x] = v >= v_pad || among(key, n, static_cast<int32_t>(v));
@@ -559,7 +561,7 @@ tpce_status embed_forward(const int32_t *ids, const void *E, int64_t tokens, int
     return e == cudaSuccess ? check_launch("embed_forward", s) : fail_cuda(e, "embed_forward");
 }
 
-// table: what is to be zeroed meanwhile (a cluster's sort only), or NULL
+// table_bytes of the table are zeroed meanwhile (by a cluster's sort only)
 tpce_status embed_sort(const int32_t *ids, int64_t T, int64_t v_pad, int64_t v_valid, const SortSplit &sp,
                        const SortBuffers &buf, uint32_t *counts, void *table, size_t table_bytes, cudaStream_t s) {
     const int32_t valid = static_cast<int32_t>(v_valid), pad = static_cast<int32_t>(v_pad);
@@ -577,7 +579,7 @@ tpce_status embed_sort(const int32_t *ids, int64_t T, int64_t v_pad, int64_t v_v
         }
         if (e != cudaSuccess) return fail_cuda(e, "embed_sort");
         // a block an SM zeroes the table, or fewer
-        const int64_t vectors = table ? static_cast<int64_t>(table_bytes / 16) : 0;
+        const int64_t vectors = static_cast<int64_t>(table_bytes / 16);
         const int64_t fill = std::min<int64_t>((vectors + 4 * kClusterThreads - 1) / (4 * kClusterThreads),
                                                int64_t{2} * num_sms());
         const unsigned blocks = static_cast<unsigned>((sp.blocks + fill + sp.blocks - 1) / sp.blocks * sp.blocks);
@@ -604,18 +606,18 @@ tpce_status embed_sort(const int32_t *ids, int64_t T, int64_t v_pad, int64_t v_v
 
 template <typename T>
 tpce_status embed_sums(const void *dX, int64_t tokens, int64_t h, int64_t v_pad, const int32_t *key,
-                       const int32_t *token, float scale, bool add, bool zeroed, float *partial, void *dE,
+                       const int32_t *token, float scale, bool add, int64_t zeroed, float *partial, void *dE,
                        cudaStream_t s) {
     const SumSplit sp = sum_split(tokens, h);
     const int vectors = static_cast<int>(h / 8);
     const int64_t of_block = kThreads / sp.lanes;
     const int64_t blocks = (static_cast<int64_t>(sp.chunks) * sp.parts + of_block - 1) / of_block;
-    const unsigned fill = add || zeroed ? 0u : static_cast<unsigned>((v_pad + kFillRows - 1) / kFillRows);
+    const unsigned fill = add ? 0u : static_cast<unsigned>((v_pad - zeroed + kFillRows - 1) / kFillRows);
     {
         KernelTimer timer("embed_sum", s);
         const cudaError_t e =
             launch(embed_sum_kernel<T>, fill + static_cast<unsigned>(blocks), kThreads, 0, s,
-                   static_cast<const T *>(dX), key, token, tokens, v_pad, vectors, sp, fill, add, scale, partial,
+                   static_cast<const T *>(dX), key, token, tokens, v_pad, vectors, sp, fill, zeroed, add, scale, partial,
                    static_cast<T *>(dE));
         if (e != cudaSuccess) return fail_cuda(e, "embed_sum");
         const tpce_status st = check_launch("embed_sum", s);
@@ -689,8 +691,10 @@ extern "C" tpce_status tp_embedding_backward(const void *dX, const int32_t *ids,
     uint32_t *counts = reinterpret_cast<uint32_t *>(base + l.counts);
     float *partial = reinterpret_cast<float *>(base + l.partial);
     const SortSplit sp = sort_split(T, v_pad);
-    const bool zeroed = sp.cluster && !accumulate;
-    if ((st = embed_sort(ids, T, v_pad, v_valid, sp, buf, counts, zeroed ? dE : nullptr, table, s)) != TPCE_OK) return st;
+    const size_t row = table / static_cast<size_t>(v_pad);
+    const int64_t zeroed = sp.cluster && !accumulate ? std::min(v_pad, static_cast<int64_t>(kZeroed / row)) : 0;
+    if ((st = embed_sort(ids, T, v_pad, v_valid, sp, buf, counts, dE, static_cast<size_t>(zeroed) * row, s)) != TPCE_OK)
+        return st;
     const int last = sp.passes & 1;
     return dtype == TPCE_BF16
                ? embed_sums<__nv_bfloat16>(dX, T, h, v_pad, buf.key[last], buf.token[last], scale, accumulate != 0,
