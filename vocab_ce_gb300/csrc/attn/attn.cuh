@@ -200,27 +200,45 @@ __device__ __forceinline__ void zero_rest(const Shape &s, const Tile &t, T *out,
     }
 }
 
-// Rows r0 .. of a tile (zeros from row n on) into shared memory.
+// Rows r0 .. of a tile (zeros from row n on), fetched into registers, all loads of which
+// are under way together and during whatever comes before put() writes them to shared
+// memory. (With each load waited for a step of 64 x 64 took 12 us, mostly that.)
 template <typename T>
-__device__ __forceinline__ void plain_load(float *to, int pitch, const T *from, int64_t ld, int r0, int n, int d) {
-    const int vectors = d / 8;
-    for (int i = threadIdx.x; i < kRows * vectors; i += kPlainThreads) {
-        const int r = i / vectors, c = i - r * vectors;
-        float v[8] = {};
-        if (r0 + r < n) unpack8(load8(from + (r0 + r) * ld + c * 8), v);
-        float4 *p = reinterpret_cast<float4 *>(to + r * pitch + c * 8);
-        p[0] = make_float4(v[0], v[1], v[2], v[3]);
-        p[1] = make_float4(v[4], v[5], v[6], v[7]);
+struct PlainRows {
+    static constexpr int kEach = kRows * kMaxDim / 8 / kPlainThreads;
+    Raw8<T> v[kEach];
+    __device__ __forceinline__ void fetch(const T *from, int64_t ld, int r0, int n, int d) {
+        const int vectors = d / 8;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int i = threadIdx.x + k * kPlainThreads, r = i / vectors, c = i - r * vectors;
+            zero8(v[k]);
+            if (r < kRows && r0 + r < n) v[k] = load8(from + (r0 + r) * ld + c * 8);
+        }
     }
-}
+    __device__ __forceinline__ void put(float *to, int pitch, int d) const {
+        const int vectors = d / 8;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int i = threadIdx.x + k * kPlainThreads, r = i / vectors, c = i - r * vectors;
+            if (r >= kRows) break;
+            float x[8];
+            unpack8(v[k], x);
+            float4 *p = reinterpret_cast<float4 *>(to + r * pitch + c * 8);
+            p[0] = make_float4(x[0], x[1], x[2], x[3]);
+            p[1] = make_float4(x[4], x[5], x[6], x[7]);
+        }
+    }
+};
 
-// s[i][j] = sum_c A[4 ty + i][c] B[tx + 16 j][c]
+// s[i][j] = sum_c A[4 ty + i][c] B[tx + 16 j][c], even and odd c two sums of one instruction
 __device__ __forceinline__ void plain_dots(const float *A, const float *B, int pitch, int d, float (&s)[4][4]) {
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    float odd[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[i][j] = 0.0f;
+        for (int j = 0; j < 4; ++j) s[i][j] = odd[i][j] = 0.0f;
 #pragma unroll 2
     for (int c = 0; c < d; c += 4) {
         float4 a[4], b[4];
@@ -232,12 +250,14 @@ __device__ __forceinline__ void plain_dots(const float *A, const float *B, int p
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
-                s[i][j] = fmaf(a[i].y, b[j].y, s[i][j]);
-                s[i][j] = fmaf(a[i].z, b[j].z, s[i][j]);
-                s[i][j] = fmaf(a[i].w, b[j].w, s[i][j]);
+                step::fma2(s[i][j], odd[i][j], a[i].x, a[i].y, b[j].x, b[j].y);
+                step::fma2(s[i][j], odd[i][j], a[i].z, a[i].w, b[j].z, b[j].w);
             }
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[i][j] += odd[i][j];
 }
 
 // o[i][m] += sum_k P[4 ty + i][k] X[k][4 tx + 64 m ..]  (ROWS: P[k][4 ty + i]); a zero factor
@@ -264,10 +284,8 @@ __device__ __forceinline__ void plain_add(const float *P, const float *X, int pi
                     const int at = ROWS ? i : q;
                     const float f = at == 0 ? f4.x : at == 1 ? f4.y : at == 2 ? f4.z : f4.w;
                     if (MASKED && f == 0.0f) continue;
-                    o[i][m][0] = fmaf(f, x.x, o[i][m][0]);
-                    o[i][m][1] = fmaf(f, x.y, o[i][m][1]);
-                    o[i][m][2] = fmaf(f, x.z, o[i][m][2]);
-                    o[i][m][3] = fmaf(f, x.w, o[i][m][3]);
+                    step::fma2(o[i][m][0], o[i][m][1], f, f, x.x, x.y);
+                    step::fma2(o[i][m][2], o[i][m][3], f, f, x.z, x.w);
                 }
             }
         }

@@ -26,6 +26,11 @@ __global__ void __launch_bounds__(256) delta_kernel(const Shape s, const T *dO, 
     if (blockIdx.x == 0 && threadIdx.x == 0) *counter = 0;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * 16 * kDeltaRows + threadIdx.x / 16, rows = s.T * s.n_q;
     const int lane = threadIdx.x & 15;
+    // lane k keeps row k's statistics: its lse is under way with everything else
+    const int64_t mine = first + 16 * (lane < kDeltaRows ? lane : 0), t = mine / s.n_q, at = (mine - t * s.n_q) * s.T + t;
+    const bool keeps = lane < kDeltaRows && mine < rows;
+    const float own_lse = keeps ? lse[at] : 0.0f;
+    float own = 0.0f;
     Raw8<T> a[kDeltaRows], b[kDeltaRows];
 #pragma unroll
     for (int k = 0; k < kDeltaRows; ++k) {
@@ -39,18 +44,15 @@ __global__ void __launch_bounds__(256) delta_kernel(const Shape s, const T *dO, 
     }
 #pragma unroll
     for (int k = 0; k < kDeltaRows; ++k) {
-        const int64_t i = first + 16 * k;
         float x[8], y[8], sum = 0.0f;
         unpack8(a[k], x);
         unpack8(b[k], y);
 #pragma unroll
         for (int c = 0; c < 8; ++c) sum = fmaf(x[c], y[c], sum);
         sum = sum16(sum);
-        if (i < rows && lane == 0) {
-            const int64_t at = i % s.n_q * s.T + i / s.n_q;
-            stats[at] = make_float2(lse[at] * kLog2e, sum);
-        }
+        if (lane == k) own = sum;
     }
+    if (keeps) stats[at] = make_float2(own_lse * kLog2e, own);
 }
 
 // ------------------------------------------------------------------ plain tiles
@@ -120,13 +122,22 @@ __device__ __forceinline__ void plain_dq_tile(const Shape &s, const T *QKV, cons
     const KeyTiles tiles = key_tiles(s, q0, min(n, q0 + kRows), kRows);
     float o[4][2][4];
     clear(o);
-    plain_load(Q, lay.pitch, base + qc, s.ld, q0, n, d);
-    plain_load(G, lay.pitch, dO + row0 * ldo + static_cast<int64_t>(h) * d, ldo, q0, n, d);
+    PlainRows<T> one, two;
+    one.fetch(base + qc, s.ld, q0, n, d);
+    two.fetch(dO + row0 * ldo + static_cast<int64_t>(h) * d, ldo, q0, n, d);
+    one.put(Q, lay.pitch, d);
+    two.put(G, lay.pitch, d);
+    one.fetch(base + kc, s.ld, tiles.at(0) * kRows, n, d);
+    two.fetch(base + vc, s.ld, tiles.at(0) * kRows, n, d);
     for (int u = 0; u < tiles.count(); ++u) {
         const int k0 = tiles.at(u) * kRows;
         plain_sync();
-        plain_load(K, lay.pitch, base + kc, s.ld, k0, n, d);
-        plain_load(V, lay.pitch, base + vc, s.ld, k0, n, d);
+        one.put(K, lay.pitch, d);
+        two.put(V, lay.pitch, d);
+        if (u + 1 < tiles.count()) {
+            one.fetch(base + kc, s.ld, tiles.at(u + 1) * kRows, n, d);
+            two.fetch(base + vc, s.ld, tiles.at(u + 1) * kRows, n, d);
+        }
         plain_sync();
         const bool masked = !all_seen(s, q0, q0 + kRows, k0, k0 + kRows) || q0 + kRows > n;
         plain_scores(s, Q, K, G, V, lay.pitch, stats + h * s.T + row0, q0, k0, n, masked, nullptr, dS);
@@ -153,15 +164,27 @@ __device__ __forceinline__ void plain_dkv_tile(const Shape &s, const T *QKV, con
     float ok[4][2][4], ov[4][2][4];
     clear(ok);
     clear(ov);
-    plain_load(K, lay.pitch, base + kc, s.ld, k0, n, d);
-    plain_load(V, lay.pitch, base + vc, s.ld, k0, n, d);
+    PlainRows<T> one, two;
+    one.fetch(base + kc, s.ld, k0, n, d);
+    two.fetch(base + vc, s.ld, k0, n, d);
+    one.put(K, lay.pitch, d);
+    two.put(V, lay.pitch, d);
     const int end = query_end(s, k0, min(n, k0 + kRows), n);
+    auto fetch = [&](int h, int q0) {
+        one.fetch(base + static_cast<int64_t>(s.q_head(h)) * d, s.ld, q0, n, d);
+        two.fetch(dO + row0 * ldo + static_cast<int64_t>(h) * d, ldo, q0, n, d);
+    };
+    fetch(kv * s.group, k0);
     for (int g = 0; g < s.group; ++g) {
         const int h = kv * s.group + g;
         for (int q0 = k0; q0 < end; q0 += kRows) {
             plain_sync();
-            plain_load(Q, lay.pitch, base + static_cast<int64_t>(s.q_head(h)) * d, s.ld, q0, n, d);
-            plain_load(G, lay.pitch, dO + row0 * ldo + static_cast<int64_t>(h) * d, ldo, q0, n, d);
+            one.put(Q, lay.pitch, d);
+            two.put(G, lay.pitch, d);
+            if (q0 + kRows < end)
+                fetch(h, q0 + kRows);
+            else if (g + 1 < s.group)
+                fetch(h + 1, k0);
             plain_sync();
             const bool masked = !all_seen(s, q0, q0 + kRows, k0, k0 + kRows) || q0 + kRows > n;
             plain_scores(s, Q, K, G, V, lay.pitch, stats + h * s.T + row0, q0, k0, n, masked, P, dS);
@@ -292,28 +315,6 @@ __device__ __forceinline__ Unit find_unit(const Shape &s, int id, int tiles) {
         u.steps = key_tiles(s, u.first, min(u.t.n, u.first + kTile), kTile).count();
     }
     return u;
-}
-
-// Half a row of an accumulator (up to 64 columns from c0 on), times f, to `to`; false if
-// something is not finite.
-__device__ __forceinline__ bool write_half(const float (&o)[2][32], float f, int c0, int d, __nv_bfloat16 *to,
-                                           bool mine) {
-    float check = 0.0f;
-#pragma unroll
-    for (int v = 0; v < 8; ++v) {
-        const int c = c0 + v * 8;
-        if (c >= d) continue;
-        float y[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            y[e] = o[v >> 2][(v & 3) * 8 + e] * f;
-            check = fmaf(y[e], 0.0f, check);
-        }
-        Raw8<__nv_bfloat16> r;
-        pack8(y, r);
-        if (mine) store8(to + c, r);
-    }
-    return !mine || check == 0.0f;  // NaN is not 0
 }
 
 // Keys as rows, per tile of 128 queries of a head:
@@ -529,23 +530,22 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             ++units;
             ptx::tc_fence_after();
             float o[2][32];
+            const int head = u.kind == kQueries ? s.q_head(u.head) : half ? s.v_head(u.head) : s.k_head(u.head);
+            const int rows = u.t.n - (row - lane);
+            __nv_bfloat16 *to = dQKV + (u.t.row0 + row - lane) * s.ld + static_cast<int64_t>(head) * s.d;
             if (u.kind == kKeys) {
                 // both halves of dK by warps 0 - 3, of dV by warps 4 - 7
-                __nv_bfloat16 *to = dQKV + (u.t.row0 + row) * s.ld +
-                                    static_cast<int64_t>(half ? s.v_head(u.head) : s.k_head(u.head)) * s.d;
                 const uint32_t from = (half ? kSumV : kSumK) + lanes;
                 const float f = half ? 1.0f : s.scale;
                 read_half(from, o);
-                fine = write_half(o, f, 0, s.d, to, mine);
+                fine = write_rows(o, f, 0, s.d, to, s.ld, rows);
                 read_half(from + 64, o);
                 tell(&m.read);
-                fine = write_half(o, f, 64, s.d, to, mine) && fine;
+                if (s.d > 64) fine = write_rows(o, f, 64, s.d, to, s.ld, rows) && fine;
             } else {
-                __nv_bfloat16 *to =
-                    dQKV + (u.t.row0 + row) * s.ld + static_cast<int64_t>(s.q_head(u.head)) * s.d;
                 read_half(kSumQ + lanes + half * 64, o);
                 tell(&m.read);
-                fine = write_half(o, s.scale, half * 64, s.d, to, mine);
+                if (half * 64 < s.d) fine = write_rows(o, s.scale, half * 64, s.d, to, s.ld, rows);
             }
             // the block's odd units are a list that begins at m.odd
             if (!__all_sync(0xffffffffu, fine) && lane == 0) {

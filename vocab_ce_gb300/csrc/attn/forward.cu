@@ -35,12 +35,20 @@ __device__ __forceinline__ void plain_forward_tile(const Shape &s, const T *QKV,
             for (int b = 0; b < 4; ++b) o[i][a][b] = 0.0f;
     }
     const float c = s.scale * kLog2e;
-    plain_load(Q, lay.pitch, q, s.ld, q0, n, d);
+    PlainRows<T> rows_q, rows_k, rows_v;
+    rows_q.fetch(q, s.ld, q0, n, d);
+    rows_k.fetch(k, s.ld, tiles.at(0) * kRows, n, d);
+    rows_v.fetch(v, s.ld, tiles.at(0) * kRows, n, d);
+    rows_q.put(Q, lay.pitch, d);
     for (int u = 0; u < tiles.count(); ++u) {
         const int k0 = tiles.at(u) * kRows;
         plain_sync();
-        plain_load(K, lay.pitch, k, s.ld, k0, n, d);
-        plain_load(V, lay.pitch, v, s.ld, k0, n, d);
+        rows_k.put(K, lay.pitch, d);
+        rows_v.put(V, lay.pitch, d);
+        if (u + 1 < tiles.count()) {
+            rows_k.fetch(k, s.ld, tiles.at(u + 1) * kRows, n, d);
+            rows_v.fetch(v, s.ld, tiles.at(u + 1) * kRows, n, d);
+        }
         plain_sync();
         float x[4][4];
         plain_dots(Q, K, lay.pitch, d, x);
@@ -377,7 +385,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             const float inv = 1.0f / l;
             const bool mine = row < w.t.n;
             float check = l * 0.0f;  // stays 0 while everything is finite
-            // through shared memory, so that four lanes write 64 adjacent bytes of a row
+            // through shared memory, so that four lanes write 64 adjacent bytes of a row (with exchanges between
+            // lanes, as the backward has it, and a fifth place in the ring instead: 1.5% slower)
             uint8_t *out = m.out[warp];
             const int rows = min(32, w.t.n - (row - lane));
             __nv_bfloat16 *to = O + (w.t.row0 + row - lane) * s.n_q * s.d + static_cast<int64_t>(my_head) * s.d;
