@@ -270,7 +270,7 @@ struct BwdSmem {
     uint64_t scores[2], dots, p_ready, ds_ready, stats_full[2], stats_empty[2], turn[2];
     uint64_t sum_done;            // a step's sum of dQ is complete
     uint64_t done, read;          // a unit's products are complete; its results have been read
-    uint64_t unit_full[2], unit_empty[2], drain;
+    uint64_t unit_full[2], unit_empty[2], drain, aux;
     Unit unit[2];
     uint32_t tmem_slot;
     int abort_flag, odd;          // odd: the last of the block's units that has results which are not finite
@@ -367,6 +367,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         ptx::mbar_init(&m.done, 2);
         ptx::mbar_init(&m.read, 8);
         ptx::mbar_init(&m.drain, 2);
+        ptx::mbar_init(&m.aux, 1);
         m.abort_flag = 0;
         m.odd = -1;
         ptx::fence_mbar_init();
@@ -564,13 +565,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             // ------------------------------------------------ loads
             const bool leader = ptx::elect_one();
             const uint32_t bytes = blocks * kBlockBytes;
-            auto load = [&](int kind, int at, const CUtensorMap *from, int head, int64_t row) {
+            uint32_t aux_phase = 0;
+            auto load = [&](int kind, int at, const CUtensorMap *from, int head, int64_t row, int rows) {
                 const int place = place_of(kind, at);
                 if (!wait(&m.empty[place], round_of(kind, at) ^ 1, 30)) return;
-                if (leader) {
-                    ptx::mbar_arrive_expect_tx(&m.full[place], bytes);
-                    load_tile(m.ring[place], from, &m.full[place], head, row, blocks);
-                }
+                ok = load_rows(leader, m.ring[place], from, &m.full[place], &m.aux, aux_phase, head, row, blocks, rows,
+                               abort_flag, s.err);
             };
             int longs = 0, shorts = 0;
             while (ok && next_unit(u)) {
@@ -592,18 +592,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     if (keys) {
                         const int h = kv * s.group + g;
                         const int64_t at = row + q * kTile;
-                        load(kLong, n, &map, s.q_head(h), at);
+                        const int left = u.t.n - (u.first + q * kTile), rows = left < kTile ? left : 0;
+                        load(kLong, n, &map, s.q_head(h), at, rows);
                         longs = ok ? n + 1 : longs;
-                        if (ok) load(kShort, n, &map_do, h, at);
+                        if (ok) load(kShort, n, &map_do, h, at, rows);
                         if (++q == of_head) {
                             q = 0;
                             ++g;
                         }
                     } else {
                         const int64_t at = u.t.row0 + static_cast<int64_t>(kt.at(it)) * kTile;
-                        load(kLong, n, &map, s.k_head(kv), at);
+                        const int left = u.t.n - kt.at(it) * kTile;
+                        load(kLong, n, &map, s.k_head(kv), at, left < kTile ? left : 0);
                         longs = ok ? n + 1 : longs;
-                        if (ok) load(kShort, n, &map, s.v_head(kv), at);
+                        if (ok) load(kShort, n, &map, s.v_head(kv), at, 0);
                     }
                     shorts = ok ? n + 1 : shorts;
                 }
@@ -766,7 +768,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         ptx::tc_fence_after();
         ptx::tmem_dealloc(0, kTmemCols);
     }
-    // What is masked has met 0 times its value: a unit with results that are not finite is
+    // What is masked within a sequence has met 0 times its value: a unit with results that are not finite is
     // computed again where masked values are passed over.
     int odd = m.odd;
     if (odd < 0 || *abort_flag || threadIdx.x >= kPlainThreads) return;

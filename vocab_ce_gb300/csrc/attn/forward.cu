@@ -185,7 +185,7 @@ struct FwdSmem {
     uint64_t q_full, q_empty;
     uint64_t turn[2], s_full[2], p_full[2], o_full[2], o_empty[2];
     uint64_t work_full[2], work_empty[2];
-    uint64_t drain;
+    uint64_t drain, aux;
     Work work[2];
     uint32_t odd[2][kOddBits / 32];  // of the block's pairs: a tile has results that are not finite
     uint32_t tmem_slot;
@@ -260,6 +260,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             ptx::mbar_init(&m.work_empty[i], kWorkReaders);
         }
         ptx::mbar_init(&m.drain, 2);
+        ptx::mbar_init(&m.aux, 1);
         m.abort_flag = 0;
         ptx::fence_mbar_init();
         ptx::prefetch_tmap(&map);
@@ -435,15 +436,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             const uint32_t bytes = blocks * kBlockBytes;
             int stage = 0;
             uint32_t phase = 0, issued = 0, parity = 0, q_phase = 0;
+            const bool leader = ptx::elect_one();
             bool ok = true, any = false;
-            auto load = [&](int at_head, int64_t row) {
+            uint32_t aux_phase = 0;
+            auto load = [&](int at_head, int64_t row, int rows) {
                 ok = ok && wait_all(&m.empty[stage], phase ^ 1, abort_flag, s.err, 20);
                 if (!ok) return;
-                if (lane == 0) {
-                    ptx::mbar_arrive_expect_tx(&m.full[stage], bytes);
-                    load_tile(m.ring[stage], &map, &m.full[stage], at_head, row, blocks);
-                }
-                __syncwarp();
+                ok = load_rows(leader, m.ring[stage], &map, &m.full[stage], &m.aux, aux_phase, at_head, row, blocks,
+                               rows, abort_flag, s.err);
                 issued |= 1u << stage;
                 parity = (parity & ~(1u << stage)) | (phase << stage);
                 if (++stage == kFwdStages) {
@@ -470,8 +470,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 __syncwarp();
                 // in the order of their use: K of a tile after V of the one before
                 for (int u = 0; u <= pr.count && ok; ++u) {
-                    if (u > 0) load(s.v_head(kv), w.t.row0 + static_cast<int64_t>(pr.both.at(u - 1)) * kTile);
-                    if (u < pr.count) load(s.k_head(kv), w.t.row0 + static_cast<int64_t>(pr.both.at(u)) * kTile);
+                    const int v0 = u > 0 ? pr.both.at(u - 1) * kTile : 0;
+                    if (u > 0) load(s.v_head(kv), w.t.row0 + v0, v0 + kTile > w.t.n ? w.t.n - v0 : 0);
+                    if (u < pr.count) load(s.k_head(kv), w.t.row0 + static_cast<int64_t>(pr.both.at(u)) * kTile, 0);
                 }
             }
             if (*abort_flag && lane == 0) {
@@ -563,8 +564,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, kTmemCols);
     }
-    // What is masked has met 0 times its value: a tile with results that are not finite
-    // is computed again where masked values are passed over.
+    // What is masked within a sequence has met 0 times its value: a tile with results that
+    // are not finite is computed again where masked values are passed over.
     uint32_t any = 0;
     for (int i = 0; i < 2 * kOddBits / 32; ++i) any |= m.odd[i / (kOddBits / 32)][i % (kOddBits / 32)];
     if (any == 0 || *abort_flag || threadIdx.x >= kPlainThreads) return;

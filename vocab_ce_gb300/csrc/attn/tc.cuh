@@ -234,11 +234,43 @@ __device__ __forceinline__ void commit(bool leader, uint64_t *bar) {
     if (leader) ptx::mma_commit(bar);
 }
 
+// Rows `from` .. 127 of a tile in shared memory become zeros, by a warp.
+__device__ __forceinline__ void zero_tail(uint8_t *tile, int from, int blocks) {
+    const int lane = threadIdx.x & 31;
+    for (int b = 0; b < blocks; ++b)
+        for (int i = from * 8 + lane; i < kTile * 8; i += 32)
+            *reinterpret_cast<uint4 *>(tile + b * kBlockBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+}
+
 // The blocks of one head's tile of rows, into one stage.
 __device__ __forceinline__ void load_tile(uint8_t *to, const CUtensorMap *m, uint64_t *bar, int head, int64_t row,
                                           int blocks) {
     for (int b = 0; b < blocks; ++b)
         ptx::tma_load_3d(to + b * kBlockBytes, m, bar, b * 64, head, static_cast<int>(row));
+}
+
+// The same by the warp that loads, counted on `full`; of a tile that a sequence ends in,
+// `rows` of it (0: all 128), the others are zeros: what is there belongs to the next
+// sequence or to none, its factors in a sum over rows are zeros, and it may be infinite or
+// NaN. Such a tile lands on `aux` first. (Zeroed by the warps that issue products it cost
+// the forward 4 to 7%, for the instructions between a wait and its products.)
+__device__ __forceinline__ bool load_rows(bool leader, uint8_t *to, const CUtensorMap *m, uint64_t *full, uint64_t *aux,
+                                          uint32_t &aux_phase, int head, int64_t row, int blocks, int rows,
+                                          volatile int *abort_flag, uint32_t *err) {
+    uint64_t *const bar = rows ? aux : full;
+    if (leader) {
+        ptx::mbar_arrive_expect_tx(bar, blocks * kBlockBytes);
+        load_tile(to, m, bar, head, row, blocks);
+    }
+    __syncwarp();
+    if (!rows) return true;
+    const bool ok = wait_all<true>(aux, aux_phase, abort_flag, err, 49);
+    aux_phase ^= 1;
+    if (ok) zero_tail(to, rows, blocks);
+    if (leader) ptx::mbar_arrive(full);
+    return ok;
 }
 
 }  // namespace attn
