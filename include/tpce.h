@@ -710,7 +710,9 @@ tpce_status tpce_device_status(void *stream, int clear, uint32_t *detail);
  * context usable. That launch's outputs are undefined. An RMS norm whose rows
  * come through a ring in shared memory (wider than 256 values, more rows than
  * blocks have a place, and every backward wider than 8192) takes it the same
- * way: block 0 counts bytes on its first row that nothing copies. The arming is used up
+ * way: block 0 counts bytes on its first row that nothing copies. So does a bf16 attention
+ * core (tp_attn_core_*, scale above 0): block 0 loads none of its first tile of keys (or, in the
+ * backward, of its first step's tiles). The arming is used up
  * by that one launch; tpce_debug_withhold_next_load(0) disarms it unused.
  * Process-wide; returns TPCE_OK.
  * ------------------------------------------------------------------------- */

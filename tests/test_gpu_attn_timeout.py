@@ -1,0 +1,49 @@
+"""The attention core's bounded waits when what they wait for never comes.
+
+tpce_debug_withhold_next_load(1) makes block 0 of the next bf16 attention launch
+load nothing of its first tile of keys (of its first step's tiles in the
+backward): the waits for it cannot complete. No fault is involved. The call
+returns after the waits' bound (2 s) and a drain's, the status word names a
+timeout, and the same call again gives the bits from before.
+"""
+
+import time
+
+import pytest
+import torch
+
+import vocab_ce_gb300 as tp
+from _parity import gpu_or_skip
+from vocab_ce_gb300._lib import lib
+
+pytestmark = pytest.mark.gpu
+TIMEOUT = 6
+WAIT_S = 2.0
+
+
+@pytest.mark.parametrize("T,G,window", [(3000, 2, 0), (700, 1, 200), (50, 4, 0)])
+@pytest.mark.parametrize("direction", ["forward", "backward"])
+def test_a_tile_that_never_comes(direction, T, G, window):
+    gpu_or_skip()
+    g = torch.Generator(device="cuda").manual_seed(T)
+    QKV = torch.randn(T, (G + 2) * 2 * 64, generator=g, device="cuda").bfloat16()
+    dO = torch.randn(T, G * 2 * 64, generator=g, device="cuda").bfloat16()
+    f = tp.tp_attn_core_forward(QKV, 2 * G, 2, window=window)
+
+    def call():
+        if direction == "forward":
+            return tp.tp_attn_core_forward(QKV, 2 * G, 2, window=window)["O"]
+        return tp.tp_attn_core_backward(dO, QKV, f["O"], f["lse"], 2 * G, 2, window=window)
+
+    good = call()
+    torch.cuda.synchronize()
+    assert tp.device_status() == 0
+    assert lib().tpce_debug_withhold_next_load(1) == 0
+    t0 = time.monotonic()
+    call()
+    torch.cuda.synchronize()
+    took = time.monotonic() - t0
+    assert WAIT_S - 0.1 <= took < WAIT_S + 1.0, took
+    assert tp.device_status() == TIMEOUT and tp.device_status() == 0
+    again = call()
+    assert torch.equal(good, again) and tp.device_status() == 0

@@ -340,7 +340,7 @@ constexpr uint32_t kSumV = 256, kSumK = 384, kDots = 256, kSumQ = 384;  // and a
 __global__ void __launch_bounds__(kBwdThreads, 1)
     tc_backward_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap map_do,
                        const Shape s, const __nv_bfloat16 *QKV, const __nv_bfloat16 *dO, const float2 *stats,
-                       Shared shared, __nv_bfloat16 *dQKV) {
+                       Shared shared, int debug_withhold, __nv_bfloat16 *dQKV) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     BwdSmem &m = *reinterpret_cast<BwdSmem *>(smem_raw);
     volatile int *abort_flag = &m.abort_flag;
@@ -570,7 +570,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 const int place = place_of(kind, at);
                 if (!wait(&m.empty[place], round_of(kind, at) ^ 1, 30)) return;
                 ok = load_rows(leader, m.ring[place], from, &m.full[place], &m.aux, aux_phase, head, row, blocks, rows,
-                               abort_flag, s.err);
+                               abort_flag, s.err, debug_withhold != 0 && blockIdx.x == 0 && n == 0);
             };
             int longs = 0, shorts = 0;
             while (ok && next_unit(u)) {
@@ -812,7 +812,8 @@ tpce_status tc_backward(const Shape &s, const void *QKV, const void *dO, const f
     KernelTimer timer(name, stream);
     e = step::launch(tc_backward_kernel, static_cast<unsigned>(std::min<int64_t>(units, num_sms())), kBwdThreads,
                      sizeof(BwdSmem), stream, map, map_do, s, static_cast<const __nv_bfloat16 *>(QKV),
-                     static_cast<const __nv_bfloat16 *>(dO), stats, shared, static_cast<__nv_bfloat16 *>(dQKV));
+                     static_cast<const __nv_bfloat16 *>(dO), stats, shared, take_debug_withhold(),
+                     static_cast<__nv_bfloat16 *>(dQKV));
     return e == cudaSuccess ? check_launch(name, stream) : fail_cuda(e, name);
 }
 

@@ -237,7 +237,7 @@ __device__ __forceinline__ Work find_work(const Shape &s, int r, int units, int 
 
 __global__ void __launch_bounds__(kFwdThreads, 1)
     tc_forward_kernel(const __grid_constant__ CUtensorMap map, const Shape s, const __nv_bfloat16 *QKV, bool by_heads,
-                      int tiles, __nv_bfloat16 *O, float *lse) {
+                      int tiles, int debug_withhold, __nv_bfloat16 *O, float *lse) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     FwdSmem &m = *reinterpret_cast<FwdSmem *>(smem_raw);
     volatile int *abort_flag = &m.abort_flag;
@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 ok = ok && wait_all(&m.empty[stage], phase ^ 1, abort_flag, s.err, 20);
                 if (!ok) return;
                 ok = load_rows(leader, m.ring[stage], &map, &m.full[stage], &m.aux, aux_phase, at_head, row, blocks,
-                               rows, abort_flag, s.err);
+                               rows, abort_flag, s.err, debug_withhold != 0 && blockIdx.x == 0 && issued == 0);
                 issued |= 1u << stage;
                 parity = (parity & ~(1u << stage)) | (phase << stage);
                 if (++stage == kFwdStages) {
@@ -604,7 +604,8 @@ tpce_status tc_forward(const Shape &s, const void *QKV, void *O, float *lse, cud
     if (e != cudaSuccess) return fail_cuda(e, name);
     KernelTimer timer(name, stream);
     e = step::launch(tc_forward_kernel, blocks, kFwdThreads, sizeof(FwdSmem), stream, map, s,
-                     static_cast<const __nv_bfloat16 *>(QKV), by_heads, tiles, static_cast<__nv_bfloat16 *>(O), lse);
+                     static_cast<const __nv_bfloat16 *>(QKV), by_heads, tiles, take_debug_withhold(),
+                     static_cast<__nv_bfloat16 *>(O), lse);
     return e == cudaSuccess ? check_launch(name, stream) : fail_cuda(e, name);
 }
 

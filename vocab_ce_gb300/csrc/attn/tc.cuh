@@ -254,15 +254,15 @@ __device__ __forceinline__ void load_tile(uint8_t *to, const CUtensorMap *m, uin
 // The same by the warp that loads, counted on `full`; of a tile that a sequence ends in,
 // `rows` of it (0: all 128), the others are zeros: what is there belongs to the next
 // sequence or to none, its factors in a sum over rows are zeros, and it may be infinite or
-// NaN. Such a tile lands on `aux` first. (Zeroed by the warps that issue products it cost
+// NaN. Such a tile lands on `aux` first. withhold: the failure path's test, nothing is loaded. (Zeroed by the warps that issue products it cost
 // the forward 4 to 7%, for the instructions between a wait and its products.)
 __device__ __forceinline__ bool load_rows(bool leader, uint8_t *to, const CUtensorMap *m, uint64_t *full, uint64_t *aux,
                                           uint32_t &aux_phase, int head, int64_t row, int blocks, int rows,
-                                          volatile int *abort_flag, uint32_t *err) {
+                                          volatile int *abort_flag, uint32_t *err, bool withhold = false) {
     uint64_t *const bar = rows ? aux : full;
     if (leader) {
         ptx::mbar_arrive_expect_tx(bar, blocks * kBlockBytes);
-        load_tile(to, m, bar, head, row, blocks);
+        if (!withhold) load_tile(to, m, bar, head, row, blocks);
     }
     __syncwarp();
     if (!rows) return true;
