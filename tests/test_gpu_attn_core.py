@@ -319,3 +319,20 @@ def test_tensors_that_are_refused():
         tp.tp_attn_core_backward(dO, QKV, f["O"], f["lse"], 2, 1, out=dO)
     with pytest.raises(tp.TpceError, match="overlap"):
         tp.tp_attn_core_backward(dO, QKV, f["O"], f["lse"], 2, 1, out=QKV)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("lengths,n_kv,G,d,window,sinks", [
+    ((70,), 1, 1, 64, 0, 0),        # two steps on two blocks
+    ((130,), 1, 1, 8, 0, 0),        # three on four: one has none
+    ((500,), 1, 1, 128, 0, 0),      # eight on eight
+    ((600, 3), 1, 2, 40, 0, 0),
+    ((1, 64, 65, 300), 1, 1, 96, 0, 0),
+    ((1000,), 2, 2, 64, 0, 0),      # four, of more blocks than run at once
+    ((700,), 1, 3, 64, 100, 5),
+])
+def test_tiles_that_blocks_share(lengths, n_kv, G, d, window, sinks, dtype):
+    # fp32, and bf16 with a scale that is not positive: calls with few tiles for the SMs
+    gpu_or_skip()
+    QKV, dO, edges, offsets = make(lengths, 0, 2, n_kv, G, d, dtype, 11)
+    check(QKV, dO, edges, offsets, n_kv * G, n_kv, window, sinks, dtype, 0.2 if dtype == F32 else -0.2)

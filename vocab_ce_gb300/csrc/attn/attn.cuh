@@ -302,6 +302,65 @@ __device__ __forceinline__ void store4(float *p, const float (&v)[4]) {
     *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
 }
 
+// Where there are fewer tiles than the SMs have room for, the blocks of a cluster share
+// one: rank r of `ranks` takes its steps r, r + ranks, .., and the sums of all are added in
+// the order of the ranks, by each rank those of 64 / ranks rows. (rank, ranks) = (0, 1): alone.
+struct Share {
+    int rank, ranks;
+};
+constexpr int kMaxRanks = 8;
+__device__ __forceinline__ Share this_share(int ranks) {
+    return Share{static_cast<int>(blockIdx.x % static_cast<unsigned>(ranks)), ranks};
+}
+// For `units` tiles, `longest` of which have about `steps` steps each; an SM has the
+// registers for one block. As long as all blocks run at once more ranks cost nothing (a
+// sequence of 200 tokens, one head: forward 39 -> 14 us, backward 69 -> 24). Beyond that,
+// where the last queries see many more keys than the first ones, up to four that keep
+// `least` / 2 steps pay while the longest tiles hold up the rest (1024 tokens, 4 heads on 2,
+// width 64: forward 92 -> 36 us, backward 312 -> 88; 2048 tokens, 8 heads on 4, width 128,
+// backward 1018 -> 828). Eight did not (60 and 131 us in the first of these: a cluster waits
+// for as many SMs of one group), nor do any where a window makes all tiles alike (window
+// 128: 28 -> 44 and 92 -> 103 us).
+inline int ranks_of(const Shape &s, int64_t units, int64_t longest, int64_t steps, int64_t least) {
+    const int64_t room = num_sms();
+    const bool uneven = s.window == 0 || 2 * int64_t{s.window} >= s.T;
+    int ranks = 1;
+    while (ranks < kMaxRanks && ranks < steps) {
+        const bool fits = 2 * ranks * units <= room;
+        const bool pays = uneven && ranks < 4 && steps >= least * ranks && 2 * ranks * longest < 3 * room;
+        if (!fits && !pays) break;
+        ranks *= 2;
+    }
+    return ranks;
+}
+// About the most steps of 64 keys that a tile of queries has; the lengths of sequences are
+// not known here, and taken as up to twice their mean.
+inline int64_t steps_of(const Shape &s) {
+    const int64_t n = std::min(s.T, s.offsets ? 2 * s.T / s.sequences + 1 : s.T);
+    return (std::min<int64_t>(n, s.window ? int64_t{s.window} + s.sinks + 2 * kRows : n) + kRows - 1) / kRows;
+}
+
+// A thread's accumulator to rows of d in shared memory.
+__device__ __forceinline__ void plain_put(const float (&o)[4][2][4], float *to, int pitch, int d) {
+    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+            const int col = 4 * tx + 64 * a;
+            if (col < d)
+                *reinterpret_cast<float4 *>(to + (4 * ty + i) * pitch + col) =
+                    make_float4(o[i][a][0], o[i][a][1], o[i][a][2], o[i][a][3]);
+        }
+}
+// What each rank has at `p` in its shared memory.
+__device__ __forceinline__ void of_ranks(const float *p, int ranks, float4 (&x)[kMaxRanks]) {
+    const uint32_t at = ptx::smem_u32(p);
+#pragma unroll
+    for (int q = 0; q < kMaxRanks; ++q)
+        x[q] = q < ranks ? ptx::ld_cluster4(ptx::mapa_shared(at, q)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+}
+
 __device__ __forceinline__ float max16(float x) {
 #pragma unroll
     for (int d = 8; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));

@@ -109,10 +109,34 @@ __device__ __forceinline__ void plain_store(const Shape &s, const float (&o)[4][
     }
 }
 
+// The same of all ranks' sums, which they have in shared memory at `sums`.
+template <typename T>
+__device__ __forceinline__ void plain_store_shared(const Shape &s, const float *sums, int pitch, float f, T *to, int r0,
+                                                   int n, Share by) {
+    const int rows = kRows / by.ranks, vectors = s.d / 4;
+    for (int i = threadIdx.x; i < rows * vectors; i += kPlainThreads) {
+        const int row = by.rank * rows + i / vectors, col = i % vectors * 4;
+        if (r0 + row >= n) break;
+        float4 x[kMaxRanks];
+        of_ranks(sums + row * pitch + col, by.ranks, x);
+        float y[4] = {x[0].x, x[0].y, x[0].z, x[0].w};
+#pragma unroll
+        for (int q = 1; q < kMaxRanks; ++q) {
+            y[0] += x[q].x;
+            y[1] += x[q].y;
+            y[2] += x[q].z;
+            y[3] += x[q].w;
+        }
+#pragma unroll
+        for (int b = 0; b < 4; ++b) y[b] *= f;
+        store4(to + (r0 + row) * s.ld + col, y);
+    }
+}
+
 // dQ of queries q0 .. q0 + 63 of one head.
 template <typename T>
 __device__ __forceinline__ void plain_dq_tile(const Shape &s, const T *QKV, const T *dO, const float2 *stats,
-                                           int64_t row0, int n, int q0, int h, T *dQKV, float *smem) {
+                                           int64_t row0, int n, int q0, int h, T *dQKV, float *smem, Share by) {
     const PlainSmem lay(s.d);
     float *Q = smem, *K = Q + lay.rows(), *V = K + lay.rows(), *G = V + lay.rows(), *dS = G + lay.rows();
     const int d = s.d, kv = h / s.group;
@@ -127,17 +151,18 @@ __device__ __forceinline__ void plain_dq_tile(const Shape &s, const T *QKV, cons
     two.fetch(dO + row0 * ldo + static_cast<int64_t>(h) * d, ldo, q0, n, d);
     one.put(Q, lay.pitch, d);
     two.put(G, lay.pitch, d);
-    one.fetch(base + kc, s.ld, tiles.at(0) * kRows, n, d);
-    two.fetch(base + vc, s.ld, tiles.at(0) * kRows, n, d);
-    for (int u = 0; u < tiles.count(); ++u) {
+    auto fetch = [&](int u) {
+        if (u >= tiles.count()) return;
+        one.fetch(base + kc, s.ld, tiles.at(u) * kRows, n, d);
+        two.fetch(base + vc, s.ld, tiles.at(u) * kRows, n, d);
+    };
+    fetch(by.rank);
+    for (int u = by.rank; u < tiles.count(); u += by.ranks) {
         const int k0 = tiles.at(u) * kRows;
         plain_sync();
         one.put(K, lay.pitch, d);
         two.put(V, lay.pitch, d);
-        if (u + 1 < tiles.count()) {
-            one.fetch(base + kc, s.ld, tiles.at(u + 1) * kRows, n, d);
-            two.fetch(base + vc, s.ld, tiles.at(u + 1) * kRows, n, d);
-        }
+        fetch(u + by.ranks);
         plain_sync();
         const bool masked = !all_seen(s, q0, q0 + kRows, k0, k0 + kRows) || q0 + kRows > n;
         plain_scores(s, Q, K, G, V, lay.pitch, stats + h * s.T + row0, q0, k0, n, masked, nullptr, dS);
@@ -147,13 +172,21 @@ __device__ __forceinline__ void plain_dq_tile(const Shape &s, const T *QKV, cons
         else
             plain_add<false, false>(dS, K, lay.pitch, d, o);
     }
-    plain_store(s, o, s.scale, dQKV + row0 * s.ld + qc, q0, n);
+    if (by.ranks == 1) {
+        plain_store(s, o, s.scale, dQKV + row0 * s.ld + qc, q0, n);
+        return;
+    }
+    plain_sync();  // a rank may have had no step
+    plain_put(o, Q, lay.pitch, d);
+    ptx::cluster_sync();
+    plain_store_shared(s, Q, lay.pitch, s.scale, dQKV + row0 * s.ld + qc, q0, n, by);
+    ptx::cluster_sync();  // until all have read
 }
 
 // dK and dV of keys k0 .. k0 + 63 of one key/value head.
 template <typename T>
 __device__ __forceinline__ void plain_dkv_tile(const Shape &s, const T *QKV, const T *dO, const float2 *stats,
-                                            int64_t row0, int n, int k0, int kv, T *dQKV, float *smem) {
+                                            int64_t row0, int n, int k0, int kv, T *dQKV, float *smem, Share by) {
     const PlainSmem lay(s.d);
     float *Q = smem, *K = Q + lay.rows(), *V = K + lay.rows(), *G = V + lay.rows(), *P = G + lay.rows(),
           *dS = P + kRows * kPitchP;
@@ -169,68 +202,74 @@ __device__ __forceinline__ void plain_dkv_tile(const Shape &s, const T *QKV, con
     two.fetch(base + vc, s.ld, k0, n, d);
     one.put(K, lay.pitch, d);
     two.put(V, lay.pitch, d);
-    const int end = query_end(s, k0, min(n, k0 + kRows), n);
-    auto fetch = [&](int h, int q0) {
-        one.fetch(base + static_cast<int64_t>(s.q_head(h)) * d, s.ld, q0, n, d);
-        two.fetch(dO + row0 * ldo + static_cast<int64_t>(h) * d, ldo, q0, n, d);
+    // steps: the tiles of queries that see the keys, head by head
+    const int tiles = (query_end(s, k0, min(n, k0 + kRows), n) - k0 + kRows - 1) / kRows, steps = tiles * s.group;
+    auto fetch = [&](int u) {
+        if (u >= steps) return;
+        const int at = kv * s.group + u / tiles, r0 = k0 + u % tiles * kRows;
+        one.fetch(base + static_cast<int64_t>(s.q_head(at)) * d, s.ld, r0, n, d);
+        two.fetch(dO + row0 * ldo + static_cast<int64_t>(at) * d, ldo, r0, n, d);
     };
-    fetch(kv * s.group, k0);
-    for (int g = 0; g < s.group; ++g) {
-        const int h = kv * s.group + g;
-        for (int q0 = k0; q0 < end; q0 += kRows) {
-            plain_sync();
-            one.put(Q, lay.pitch, d);
-            two.put(G, lay.pitch, d);
-            if (q0 + kRows < end)
-                fetch(h, q0 + kRows);
-            else if (g + 1 < s.group)
-                fetch(h + 1, k0);
-            plain_sync();
-            const bool masked = !all_seen(s, q0, q0 + kRows, k0, k0 + kRows) || q0 + kRows > n;
-            plain_scores(s, Q, K, G, V, lay.pitch, stats + h * s.T + row0, q0, k0, n, masked, P, dS);
-            plain_sync();
-            if (masked) {
-                plain_add<true, true>(P, G, lay.pitch, d, ov);
-                plain_add<true, true>(dS, Q, lay.pitch, d, ok);
-            } else {
-                plain_add<false, true>(P, G, lay.pitch, d, ov);
-                plain_add<false, true>(dS, Q, lay.pitch, d, ok);
-            }
+    fetch(by.rank);
+    for (int u = by.rank; u < steps; u += by.ranks) {
+        const int h = kv * s.group + u / tiles, q0 = k0 + u % tiles * kRows;
+        plain_sync();
+        one.put(Q, lay.pitch, d);
+        two.put(G, lay.pitch, d);
+        fetch(u + by.ranks);
+        plain_sync();
+        const bool masked = !all_seen(s, q0, q0 + kRows, k0, k0 + kRows) || q0 + kRows > n;
+        plain_scores(s, Q, K, G, V, lay.pitch, stats + h * s.T + row0, q0, k0, n, masked, P, dS);
+        plain_sync();
+        if (masked) {
+            plain_add<true, true>(P, G, lay.pitch, d, ov);
+            plain_add<true, true>(dS, Q, lay.pitch, d, ok);
+        } else {
+            plain_add<false, true>(P, G, lay.pitch, d, ov);
+            plain_add<false, true>(dS, Q, lay.pitch, d, ok);
         }
     }
-    plain_store(s, ok, s.scale, dQKV + row0 * s.ld + kc, k0, n);
-    plain_store(s, ov, 1.0f, dQKV + row0 * s.ld + vc, k0, n);
+    if (by.ranks == 1) {
+        plain_store(s, ok, s.scale, dQKV + row0 * s.ld + kc, k0, n);
+        plain_store(s, ov, 1.0f, dQKV + row0 * s.ld + vc, k0, n);
+        return;
+    }
+    plain_sync();  // a rank may have had no step
+    plain_put(ok, K, lay.pitch, d);
+    plain_put(ov, V, lay.pitch, d);
+    ptx::cluster_sync();
+    plain_store_shared(s, K, lay.pitch, s.scale, dQKV + row0 * s.ld + kc, k0, n, by);
+    plain_store_shared(s, V, lay.pitch, 1.0f, dQKV + row0 * s.ld + vc, k0, n, by);
+    ptx::cluster_sync();  // until all have read
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kPlainThreads)
-    plain_dq_kernel(const Shape s, const T *QKV, const T *dO, const float2 *stats, int tiles, T *dQKV) {
+    plain_backward_kernel(const Shape s, const T *QKV, const T *dO, const float2 *stats, int tiles, int ranks, T *dQKV) {
     extern __shared__ float4 smem4[];
+    float *const smem = reinterpret_cast<float *>(smem4);
     grid_begin();
-    const int h = blockIdx.x % s.n_q;
-    const Tile t = find_tile(s, blockIdx.x / s.n_q, kRows, tiles);
-    if (t.n == 0) {
-        zero_rest(s, t, dQKV, s.ld, static_cast<int64_t>(s.q_head(h)) * s.d);
-        return;
+    const Share by = this_share(ranks);
+    const int unit = static_cast<int>(blockIdx.x / static_cast<unsigned>(ranks)), of_keys = tiles * s.n_kv;
+    // dK and dV have the most steps and come first: those of the first keys, seen by the most queries; then dQ,
+    // that of the last queries, which see the most keys
+    if (unit < of_keys) {
+        const int kv = unit % s.n_kv;
+        const Tile t = find_tile(s, unit / s.n_kv, kRows, tiles);
+        if (t.n) {
+            plain_dkv_tile(s, QKV, dO, stats, t.row0, t.n, t.tile * kRows, kv, dQKV, smem, by);
+        } else if (by.rank == 0) {
+            zero_rest(s, t, dQKV, s.ld, static_cast<int64_t>(s.k_head(kv)) * s.d);
+            zero_rest(s, t, dQKV, s.ld, static_cast<int64_t>(s.v_head(kv)) * s.d);
+        }
+    } else {
+        const int h = (unit - of_keys) % s.n_q;
+        const Tile t = find_tile(s, (unit - of_keys) / s.n_q, kRows, tiles);
+        if (t.n)
+            plain_dq_tile(s, QKV, dO, stats, t.row0, t.n, (t.tiles - 1 - t.tile) * kRows, h, dQKV, smem, by);
+        else if (by.rank == 0)
+            zero_rest(s, t, dQKV, s.ld, static_cast<int64_t>(s.q_head(h)) * s.d);
     }
-    plain_dq_tile(s, QKV, dO, stats, t.row0, t.n, (t.tiles - 1 - t.tile) * kRows, h, dQKV,
-                  reinterpret_cast<float *>(smem4));
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kPlainThreads)
-    plain_dkv_kernel(const Shape s, const T *QKV, const T *dO, const float2 *stats, int tiles, T *dQKV) {
-    extern __shared__ float4 smem4[];
-    grid_begin();
-    const int kv = blockIdx.x % s.n_kv;
-    const Tile t = find_tile(s, blockIdx.x / s.n_kv, kRows, tiles);
-    if (t.n == 0) {
-        zero_rest(s, t, dQKV, s.ld, static_cast<int64_t>(s.k_head(kv)) * s.d);
-        zero_rest(s, t, dQKV, s.ld, static_cast<int64_t>(s.v_head(kv)) * s.d);
-        return;
-    }
-    // the first keys are seen by the most queries: they come first
-    plain_dkv_tile(s, QKV, dO, stats, t.row0, t.n, t.tile * kRows, kv, dQKV, reinterpret_cast<float *>(smem4));
 }
 
 // ------------------------------------------------------------------ tiles on the tensor cores
@@ -781,9 +820,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         for (int at = w.first; at < min(w.t.n, w.first + kTile); at += kRows) {
             plain_sync();
             if (w.kind == kKeys)
-                plain_dkv_tile(s, QKV, dO, stats, w.t.row0, w.t.n, at, w.head, dQKV, reinterpret_cast<float *>(smem_raw));
+                plain_dkv_tile(s, QKV, dO, stats, w.t.row0, w.t.n, at, w.head, dQKV, reinterpret_cast<float *>(smem_raw),
+                               Share{0, 1});
             else
-                plain_dq_tile(s, QKV, dO, stats, w.t.row0, w.t.n, at, w.head, dQKV, reinterpret_cast<float *>(smem_raw));
+                plain_dq_tile(s, QKV, dO, stats, w.t.row0, w.t.n, at, w.head, dQKV, reinterpret_cast<float *>(smem_raw),
+                               Share{0, 1});
         }
     }
 }
@@ -820,20 +861,18 @@ tpce_status tc_backward(const Shape &s, const void *QKV, const void *dO, const f
 template <typename T>
 tpce_status plain_backward(const Shape &s, const void *QKV, const void *dO, const float2 *stats, void *dQKV,
                            cudaStream_t stream) {
+    const char *name = "attn_backward";
     const int tiles = static_cast<int>(grid_tiles(s, kRows));
     const size_t smem = PlainSmem(s.d).backward();
-    auto go = [&](auto kernel, const char *name, int heads) {
-        KernelTimer timer(name, stream);
-        const cudaError_t e = step::launch(kernel, static_cast<unsigned>(tiles) * heads, kPlainThreads, smem, stream, s,
-                                           static_cast<const T *>(QKV), static_cast<const T *>(dO), stats, tiles,
-                                           static_cast<T *>(dQKV));
-        return e == cudaSuccess ? check_launch(name, stream) : fail_cuda(e, name);
-    };
-    cudaError_t e = allow_smem<plain_dq_kernel<T>>();
-    if (e == cudaSuccess) e = allow_smem<plain_dkv_kernel<T>>();
-    if (e != cudaSuccess) return fail_cuda(e, "attn_backward");
-    const tpce_status st = go(plain_dkv_kernel<T>, "attn_dkv", s.n_kv);
-    return st != TPCE_OK ? st : go(plain_dq_kernel<T>, "attn_dq", s.n_q);
+    const int64_t units = static_cast<int64_t>(tiles) * (s.n_q + s.n_kv);
+    const int ranks = ranks_of(s, units, static_cast<int64_t>(tiles) * s.n_kv, steps_of(s) * s.group, 8);
+    cudaError_t e = allow_smem<plain_backward_kernel<T>>();
+    if (e != cudaSuccess) return fail_cuda(e, name);
+    KernelTimer timer(name, stream);
+    e = step::launch_clusters(ranks, plain_backward_kernel<T>, static_cast<unsigned>(units) * ranks, kPlainThreads, smem,
+                              stream, s, static_cast<const T *>(QKV), static_cast<const T *>(dO), stats, tiles, ranks,
+                              static_cast<T *>(dQKV));
+    return e == cudaSuccess ? check_launch(name, stream) : fail_cuda(e, name);
 }
 
 template <typename T>

@@ -14,7 +14,7 @@ using namespace attn;
 // m and sum l of each row: when m grows, what has been added so far is scaled down.
 template <typename T>
 __device__ __forceinline__ void plain_forward_tile(const Shape &s, const T *QKV, int64_t row0, int n, int q0, int h,
-                                                T *O, float *lse, float *smem) {
+                                                T *O, float *lse, float *smem, Share by) {
     const PlainSmem lay(s.d);
     float *Q = smem, *K = Q + lay.rows(), *V = K + lay.rows(), *P = V + lay.rows();
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
@@ -36,19 +36,20 @@ __device__ __forceinline__ void plain_forward_tile(const Shape &s, const T *QKV,
     }
     const float c = s.scale * kLog2e;
     PlainRows<T> rows_q, rows_k, rows_v;
+    auto fetch = [&](int u) {
+        if (u >= tiles.count()) return;
+        rows_k.fetch(k, s.ld, tiles.at(u) * kRows, n, d);
+        rows_v.fetch(v, s.ld, tiles.at(u) * kRows, n, d);
+    };
     rows_q.fetch(q, s.ld, q0, n, d);
-    rows_k.fetch(k, s.ld, tiles.at(0) * kRows, n, d);
-    rows_v.fetch(v, s.ld, tiles.at(0) * kRows, n, d);
+    fetch(by.rank);
     rows_q.put(Q, lay.pitch, d);
-    for (int u = 0; u < tiles.count(); ++u) {
+    for (int u = by.rank; u < tiles.count(); u += by.ranks) {
         const int k0 = tiles.at(u) * kRows;
         plain_sync();
         rows_k.put(K, lay.pitch, d);
         rows_v.put(V, lay.pitch, d);
-        if (u + 1 < tiles.count()) {
-            rows_k.fetch(k, s.ld, tiles.at(u + 1) * kRows, n, d);
-            rows_v.fetch(v, s.ld, tiles.at(u + 1) * kRows, n, d);
-        }
+        fetch(u + by.ranks);
         plain_sync();
         float x[4][4];
         plain_dots(Q, K, lay.pitch, d, x);
@@ -86,6 +87,46 @@ __device__ __forceinline__ void plain_forward_tile(const Shape &s, const T *QKV,
         else
             plain_add<false, false>(P, V, lay.pitch, d, o);
     }
+    if (by.ranks > 1) {
+        // each rank's maximum, sum and outputs so far, scaled to the largest maximum
+        plain_sync();  // a rank may have had no step
+        plain_put(o, Q, lay.pitch, d);
+        if (tx == 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<float4 *>(K + (4 * ty + i) * lay.pitch) = make_float4(m[i], l[i], 0.0f, 0.0f);
+        }
+        ptx::cluster_sync();
+        const int rows = kRows / by.ranks, vectors = d / 4;
+        for (int i = threadIdx.x; i < rows * vectors; i += kPlainThreads) {
+            const int r = by.rank * rows + i / vectors, row = q0 + r, col = i % vectors * 4;
+            if (row >= n) break;
+            float4 x[kMaxRanks], y[kMaxRanks];
+            of_ranks(K + r * lay.pitch, by.ranks, x);
+            of_ranks(Q + r * lay.pitch + col, by.ranks, y);
+            float top = -INFINITY, sum = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int w = 0; w < kMaxRanks; ++w)
+                if (w < by.ranks) top = fmaxf(top, x[w].x);
+            const float at = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+            for (int w = 0; w < kMaxRanks; ++w) {
+                const float f = w < by.ranks ? exp2f(x[w].x - at) : 0.0f;
+                sum = fmaf(x[w].y, f, sum);
+                v[0] = fmaf(y[w].x, f, v[0]);
+                v[1] = fmaf(y[w].y, f, v[1]);
+                v[2] = fmaf(y[w].z, f, v[2]);
+                v[3] = fmaf(y[w].w, f, v[3]);
+            }
+            const float inv = 1.0f / sum;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) v[b] *= inv;
+            store4(O + (row0 + row) * s.n_q * d + static_cast<int64_t>(h) * d + col, v);
+            if (col == 0) lse[h * s.T + row0 + row] = (top + log2f(sum)) * kLn2;
+        }
+        ptx::cluster_sync();  // until all have read
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int row = q0 + 4 * ty + i;
@@ -116,18 +157,19 @@ __device__ __forceinline__ void forward_rest(const Shape &s, const Tile &t, int 
 
 template <typename T>
 __global__ void __launch_bounds__(kPlainThreads)
-    plain_forward_kernel(const Shape s, const T *QKV, int tiles, T *O, float *lse) {
+    plain_forward_kernel(const Shape s, const T *QKV, int tiles, int ranks, T *O, float *lse) {
     extern __shared__ float4 smem4[];
     grid_begin();
-    const int h = blockIdx.x % s.n_q;
-    const Tile t = find_tile(s, blockIdx.x / s.n_q, kRows, tiles);
+    const Share by = this_share(ranks);
+    const int unit = static_cast<int>(blockIdx.x / static_cast<unsigned>(ranks)), h = unit % s.n_q;
+    const Tile t = find_tile(s, unit / s.n_q, kRows, tiles);
     if (t.n == 0) {
-        forward_rest(s, t, h, O, lse);
+        if (by.rank == 0) forward_rest(s, t, h, O, lse);
         return;
     }
     // the last queries see the most keys: they come first
     plain_forward_tile(s, QKV, t.row0, t.n, (t.tiles - 1 - t.tile) * kRows, h, O, lse,
-                       reinterpret_cast<float *>(smem4));
+                       reinterpret_cast<float *>(smem4), by);
 }
 
 template <typename T>
@@ -135,10 +177,12 @@ tpce_status plain_forward(const Shape &s, const void *QKV, void *O, float *lse, 
     KernelTimer timer("attn_forward", stream);
     const int tiles = static_cast<int>(grid_tiles(s, kRows));
     const size_t smem = PlainSmem(s.d).forward();
+    const int64_t units = static_cast<int64_t>(tiles) * s.n_q;
+    const int ranks = ranks_of(s, units, units, steps_of(s), 4);
     cudaError_t e = allow_smem<plain_forward_kernel<T>>();
     if (e == cudaSuccess)
-        e = step::launch(plain_forward_kernel<T>, static_cast<unsigned>(tiles) * s.n_q, kPlainThreads, smem, stream, s,
-                         static_cast<const T *>(QKV), tiles, static_cast<T *>(O), lse);
+        e = step::launch_clusters(ranks, plain_forward_kernel<T>, static_cast<unsigned>(units) * ranks, kPlainThreads, smem,
+                                  stream, s, static_cast<const T *>(QKV), tiles, ranks, static_cast<T *>(O), lse);
     return e == cudaSuccess ? check_launch("attn_forward", stream) : fail_cuda(e, "attn_forward");
 }
 
@@ -585,7 +629,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             for (int q = begin; q < min(w.t.n, begin + kTile); q += kRows) {
                 plain_sync();
                 plain_forward_tile(s, QKV, w.t.row0, w.t.n, q, i ? pr.head[1] : pr.head[0], O, lse,
-                                   reinterpret_cast<float *>(smem_raw));
+                                   reinterpret_cast<float *>(smem_raw), Share{0, 1});
             }
         }
     }
