@@ -51,7 +51,8 @@ def reference(model, ids, edges, targets, weight, eps=1e-6):
         GU = norm(S, p[f"w2.{i}"]) @ p[f"W1.{i}"]
         f = GU.shape[1] // 2
         S = S + (torch.nn.functional.silu(GU[:, :f]) * GU[:, f:]) @ p[f"W2.{i}"]
-    loss = torch.nn.functional.cross_entropy(norm(S, p["wf"]) @ p["E"][:model.vocab].T, targets.long(), reduction="none")
+    logits = norm(S, p["wf"]) @ p["E"][:model.vocab].T
+    loss = torch.nn.functional.cross_entropy(logits, targets.long(), reduction="none")
     (loss.sum() * weight).backward()
     return loss.detach(), {n: v.grad for n, v in p.items()}
 

@@ -27,7 +27,8 @@ __global__ void __launch_bounds__(256) delta_kernel(const Shape s, const T *dO, 
     const int64_t first = static_cast<int64_t>(blockIdx.x) * 16 * kDeltaRows + threadIdx.x / 16, rows = s.T * s.n_q;
     const int lane = threadIdx.x & 15;
     // lane k keeps row k's statistics: its lse is under way with everything else
-    const int64_t mine = first + 16 * (lane < kDeltaRows ? lane : 0), t = mine / s.n_q, at = (mine - t * s.n_q) * s.T + t;
+    const int64_t mine = first + 16 * (lane < kDeltaRows ? lane : 0), t = mine / s.n_q;
+    const int64_t at = (mine - t * s.n_q) * s.T + t;
     const bool keeps = lane < kDeltaRows && mine < rows;
     const float own_lse = keeps ? lse[at] : 0.0f;
     float own = 0.0f;
@@ -245,7 +246,8 @@ __device__ __forceinline__ void plain_dkv_tile(const Shape &s, const T *QKV, con
 
 template <typename T>
 __global__ void __launch_bounds__(kPlainThreads)
-    plain_backward_kernel(const Shape s, const T *QKV, const T *dO, const float2 *stats, int tiles, int ranks, T *dQKV) {
+    plain_backward_kernel(const Shape s, const T *QKV, const T *dO, const float2 *stats, int tiles, int ranks,
+                          T *dQKV) {
     extern __shared__ float4 smem4[];
     float *const smem = reinterpret_cast<float *>(smem4);
     grid_begin();
@@ -622,7 +624,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 if (leader) {
                     ptx::mbar_arrive_expect_tx(&m.stay_full, 2 * bytes);
                     load_tile(m.stay[0], &map, &m.stay_full, keys ? s.k_head(kv) : s.q_head(u.head), row, blocks);
-                    load_tile(m.stay[1], keys ? &map : &map_do, &m.stay_full, keys ? s.v_head(kv) : u.head, row, blocks);
+                    load_tile(m.stay[1], keys ? &map : &map_do, &m.stay_full, keys ? s.v_head(kv) : u.head, row,
+                              blocks);
                 }
                 const KeyTiles kt = key_tiles(s, u.first, min(u.t.n, u.first + kTile), kTile);
                 const int of_head = u.steps / s.group;
@@ -820,11 +823,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         for (int at = w.first; at < min(w.t.n, w.first + kTile); at += kRows) {
             plain_sync();
             if (w.kind == kKeys)
-                plain_dkv_tile(s, QKV, dO, stats, w.t.row0, w.t.n, at, w.head, dQKV, reinterpret_cast<float *>(smem_raw),
-                               Share{0, 1});
+                plain_dkv_tile(s, QKV, dO, stats, w.t.row0, w.t.n, at, w.head, dQKV,
+                               reinterpret_cast<float *>(smem_raw), Share{0, 1});
             else
-                plain_dq_tile(s, QKV, dO, stats, w.t.row0, w.t.n, at, w.head, dQKV, reinterpret_cast<float *>(smem_raw),
-                               Share{0, 1});
+                plain_dq_tile(s, QKV, dO, stats, w.t.row0, w.t.n, at, w.head, dQKV,
+                              reinterpret_cast<float *>(smem_raw), Share{0, 1});
         }
     }
 }
@@ -869,9 +872,9 @@ tpce_status plain_backward(const Shape &s, const void *QKV, const void *dO, cons
     cudaError_t e = allow_smem<plain_backward_kernel<T>>();
     if (e != cudaSuccess) return fail_cuda(e, name);
     KernelTimer timer(name, stream);
-    e = step::launch_clusters(ranks, plain_backward_kernel<T>, static_cast<unsigned>(units) * ranks, kPlainThreads, smem,
-                              stream, s, static_cast<const T *>(QKV), static_cast<const T *>(dO), stats, tiles, ranks,
-                              static_cast<T *>(dQKV));
+    e = step::launch_clusters(ranks, plain_backward_kernel<T>, static_cast<unsigned>(units * ranks), kPlainThreads,
+                              smem, stream, s, static_cast<const T *>(QKV), static_cast<const T *>(dO), stats, tiles,
+                              ranks, static_cast<T *>(dQKV));
     return e == cudaSuccess ? check_launch(name, stream) : fail_cuda(e, name);
 }
 
@@ -879,8 +882,9 @@ template <typename T>
 tpce_status delta(const Shape &s, const void *dO, const void *O, const float *lse, float2 *stats,
                   cudaStream_t stream) {
     KernelTimer timer("attn_delta", stream);
+    const int64_t blocks = (s.T * s.n_q + 16 * kDeltaRows - 1) / (16 * kDeltaRows);
     const cudaError_t e =
-        step::launch(delta_kernel<T>, static_cast<unsigned>((s.T * s.n_q + 16 * kDeltaRows - 1) / (16 * kDeltaRows)), 256, 0, stream, s,
+        step::launch(delta_kernel<T>, static_cast<unsigned>(blocks), 256, 0, stream, s,
                      static_cast<const T *>(dO), static_cast<const T *>(O), lse, stats,
                      reinterpret_cast<int *>(reinterpret_cast<char *>(stats) + stats_bytes(s.T, s.n_q)));
     return e == cudaSuccess ? check_launch("attn_delta", stream) : fail_cuda(e, "attn_delta");

@@ -181,8 +181,8 @@ tpce_status plain_forward(const Shape &s, const void *QKV, void *O, float *lse, 
     const int ranks = ranks_of(s, units, units, steps_of(s), 4);
     cudaError_t e = allow_smem<plain_forward_kernel<T>>();
     if (e == cudaSuccess)
-        e = step::launch_clusters(ranks, plain_forward_kernel<T>, static_cast<unsigned>(units) * ranks, kPlainThreads, smem,
-                                  stream, s, static_cast<const T *>(QKV), tiles, ranks, static_cast<T *>(O), lse);
+        e = step::launch_clusters(ranks, plain_forward_kernel<T>, static_cast<unsigned>(units * ranks), kPlainThreads,
+                                  smem, stream, s, static_cast<const T *>(QKV), tiles, ranks, static_cast<T *>(O), lse);
     return e == cudaSuccess ? check_launch("attn_forward", stream) : fail_cuda(e, "attn_forward");
 }
 

@@ -23,7 +23,8 @@ inline tpce_status make_shape(const char *name, const int32_t *offsets, int sequ
     if (T < 0 || sequences < (offsets ? 1 : 0))
         return fail(TPCE_ERR_SHAPE, "%s: T = %lld, %d sequences", name, static_cast<long long>(T), sequences);
     // blocks of the largest grid, and rows as 32-bit numbers
-    if (T > (int64_t{1} << 30) || T * n_heads > (int64_t{1} << 33) || (T / 32 + 2 * int64_t{sequences} + 2) * n_heads > INT_MAX)
+    if (T > (int64_t{1} << 30) || T * n_heads > (int64_t{1} << 33) ||
+        (T / 32 + 2 * int64_t{sequences} + 2) * n_heads > INT_MAX)
         return fail(TPCE_ERR_SHAPE, "%s: T = %lld, %lld heads, %d sequences: too many tiles", name,
                     static_cast<long long>(T), static_cast<long long>(n_heads), sequences);
     s.T = T;

@@ -55,17 +55,18 @@ __device__ __forceinline__ void mma_scores(bool leader, uint32_t d_tmem, uint32_
     }
 }
 
-// Steps FIRST .. LAST - 1 of sixteen rows of D (+)= A X: A (bf16 in tensor memory, from a_tmem on, its second 64 columns of K
-// second_half further) times a tile's 128 rows of d columns.
-template <int FIRST = 0, int LAST = kTile / 16>
-__device__ __forceinline__ void mma_weighted(bool leader, uint32_t d_tmem, uint32_t a_tmem, uint32_t second_half, uint32_t x_tile,
-                                             uint32_t idesc, bool accumulate) {
+// D (+)= A X: A (bf16 in tensor memory from a_tmem on, its second 64 columns second_half
+// further) times a tile's 128 rows of d columns. (With fewer columns or rows where a tile
+// has fewer keys that anything sees, the instructions that this takes in front of every
+// product cost 3 to 4% of everything, and a window with four sinks gained nothing.)
+__device__ __forceinline__ void mma_weighted(bool leader, uint32_t d_tmem, uint32_t a_tmem, uint32_t second_half,
+                                             uint32_t x_tile, uint32_t idesc, bool accumulate) {
     const uint64_t x = desc_cols(x_tile);
     if (leader) {
 #pragma unroll
-        for (int k = FIRST; k < LAST; ++k)
+        for (int k = 0; k < kTile / 16; ++k)
             ptx::mma_bf16_ts(d_tmem, a_tmem + (k & 3) * 8 + (k >> 2) * second_half, step_cols(x, k), idesc,
-                             (accumulate || k > FIRST) ? 1u : 0u);
+                             (accumulate || k > 0) ? 1u : 0u);
     }
 }
 // the width of such a product: d, rounded up to what the instruction takes
@@ -105,7 +106,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// 64 columns of this thread's row.
+// 64 columns of this thread's row, waited for.
 __device__ __forceinline__ void read_half(uint32_t taddr, float (&x)[2][32]) {
     ptx::tmem_ld32_async(taddr, x[0]);
     ptx::tmem_ld32_async(taddr + 32, x[1]);
@@ -130,8 +131,8 @@ __device__ __forceinline__ void pack32(const float (&x)[32], uint32_t *p) {
 // eight columns, so that they write 128 adjacent bytes of one row after the other: with
 // each lane writing its own row the stores of a tile took 4000 cycles. Returns whether
 // everything of this lane's row is finite.
-__device__ __forceinline__ bool write_rows(const float (&o)[2][32], float f, int c0, int d, __nv_bfloat16 *to, int64_t ld,
-                                           int rows) {
+__device__ __forceinline__ bool write_rows(const float (&o)[2][32], float f, int c0, int d, __nv_bfloat16 *to,
+                                           int64_t ld, int rows) {
     const int lane = threadIdx.x & 31, j = lane & 7;
     uint4 v[8];
     float check = 0.0f;
@@ -254,8 +255,9 @@ __device__ __forceinline__ void load_tile(uint8_t *to, const CUtensorMap *m, uin
 // The same by the warp that loads, counted on `full`; of a tile that a sequence ends in,
 // `rows` of it (0: all 128), the others are zeros: what is there belongs to the next
 // sequence or to none, its factors in a sum over rows are zeros, and it may be infinite or
-// NaN. Such a tile lands on `aux` first. withhold: the failure path's test, nothing is loaded. (Zeroed by the warps that issue products it cost
-// the forward 4 to 7%, for the instructions between a wait and its products.)
+// NaN. Such a tile lands on `aux` first. (Zeroed by the warps that issue products it cost
+// the forward 4 to 7%, for the instructions between a wait and its products.) withhold:
+// nothing is loaded, for the test of the waits' ends.
 __device__ __forceinline__ bool load_rows(bool leader, uint8_t *to, const CUtensorMap *m, uint64_t *full, uint64_t *aux,
                                           uint32_t &aux_phase, int head, int64_t row, int blocks, int rows,
                                           volatile int *abort_flag, uint32_t *err, bool withhold = false) {

@@ -465,7 +465,8 @@ struct Heads {
             need(offsets, "offsets", at::kInt, offsets.sizes());
             sequences = static_cast<int>(offsets.size(0) - 1);
         }
-        scale = none(a[5]) ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(d))) : static_cast<float>(number(a[5]));
+        scale = none(a[5]) ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(d)))
+                           : static_cast<float>(number(a[5]));
     }
 };
 
