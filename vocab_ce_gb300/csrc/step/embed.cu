@@ -363,32 +363,36 @@ __device__ __forceinline__ bool among(const int32_t *key, int64_t n, int32_t v) 
     return lo < n && key[lo] == v;
 }
 
-constexpr int kFillRows = 32;
+// Rows of a block that fills: 128 KB of them, each looked up by one thread (8192 tokens,
+// 262,144 rows of 1024 bf16: 104 us; 32 rows a block, one after the other, 138; 64 KB, 118;
+// a million rows of 64: 41, 126 and 43).
+inline int fill_rows(size_t row) {
+    return static_cast<int>(std::clamp<size_t>((size_t{128} << 10) / row, 32, kThreads));
+}
 
 // The first `fill` blocks write zeros to the rows from `zeroed` on that no token names,
-// kFillRows of them each; the others add up chunks. Loads are issued four tokens at a time, with
+// fill_rows of them each; the others add up chunks. Loads are issued four tokens at a time, with
 // the old row where a run ends. Bound by HBM: 16,384 tokens of 8192 bf16 into a tied table of
 // 129,024 rows (494 MB) in 92 us of the call's 123, 70% of DRAM's peak by its counters.
 template <typename T>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
     embed_sum_kernel(const T *dX, const int32_t *key, const int32_t *token, int64_t n, int64_t v_pad, int vectors,
-                     SumSplit sp, unsigned fill, int64_t zeroed, bool add, float scale, float *__restrict__ partial,
-                     T *dE) {
+                     SumSplit sp, unsigned fill, int fill_rows, int64_t zeroed, bool add, float scale,
+                     float *__restrict__ partial, T *dE) {
     grid_begin();
     if (blockIdx.x < fill) {
-        __shared__ bool named[kFillRows];
-        const int64_t v0 = zeroed + static_cast<int64_t>(blockIdx.x) * kFillRows;
-        if (threadIdx.x < kFillRows) {
+        __shared__ bool named[kThreads];
+        const int64_t v0 = zeroed + static_cast<int64_t>(blockIdx.x) * fill_rows;
+        if (static_cast<int>(threadIdx.x) < fill_rows) {
             const int64_t v = v0 + threadIdx.x;
             named[threadIdx.x] = v >= v_pad || among(key, n, static_cast<int32_t>(v));
         }
         __syncthreads();
         Raw8<T> zero;
         zero8(zero);
-        for (int r = 0; r < kFillRows; ++r) {
-            if (named[r]) continue;
-            for (int c = threadIdx.x; c < vectors; c += kThreads)
-                store8(dE + ((v0 + r) * vectors + c) * 8, zero);
+        for (int64_t i = threadIdx.x; i < static_cast<int64_t>(fill_rows) * vectors; i += kThreads) {
+            const int r = static_cast<int>(i / vectors);
+            if (!named[r]) store8(dE + (v0 * vectors + i) * 8, zero);
         }
         return;
     }
@@ -618,12 +622,13 @@ tpce_status embed_sums(const void *dX, int64_t tokens, int64_t h, int64_t v_pad,
     const int vectors = static_cast<int>(h / 8);
     const int64_t of_block = kThreads / sp.lanes;
     const int64_t blocks = (static_cast<int64_t>(sp.chunks) * sp.parts + of_block - 1) / of_block;
-    const unsigned fill = add ? 0u : static_cast<unsigned>((v_pad - zeroed + kFillRows - 1) / kFillRows);
+    const int rows = fill_rows(static_cast<size_t>(h) * sizeof(T));
+    const unsigned fill = add ? 0u : static_cast<unsigned>((v_pad - zeroed + rows - 1) / rows);
     {
         KernelTimer timer("embed_sum", s);
         const cudaError_t e =
             launch(embed_sum_kernel<T>, fill + static_cast<unsigned>(blocks), kThreads, 0, s,
-                   static_cast<const T *>(dX), key, token, tokens, v_pad, vectors, sp, fill, zeroed, add, scale,
+                   static_cast<const T *>(dX), key, token, tokens, v_pad, vectors, sp, fill, rows, zeroed, add, scale,
                    partial, static_cast<T *>(dE));
         if (e != cudaSuccess) return fail_cuda(e, "embed_sum");
         const tpce_status st = check_launch("embed_sum", s);
@@ -632,8 +637,8 @@ tpce_status embed_sums(const void *dX, int64_t tokens, int64_t h, int64_t v_pad,
     KernelTimer timer("embed_join", s);
     const unsigned groups = static_cast<unsigned>((sp.chunks + kJoinChunks - 1) / kJoinChunks);
     const unsigned columns = static_cast<unsigned>((vectors + kThreads - 1) / kThreads);
-    const cudaError_t e = launch(embed_join_kernel<T>, groups * columns, kThreads, 0, s, key, tokens, v_pad, vectors, sp,
-                                 groups, add, scale, partial, static_cast<T *>(dE));
+    const cudaError_t e = launch(embed_join_kernel<T>, groups * columns, kThreads, 0, s, key, tokens, v_pad, vectors,
+                                 sp, groups, add, scale, partial, static_cast<T *>(dE));
     return e == cudaSuccess ? check_launch("embed_join", s) : fail_cuda(e, "embed_join");
 }
 
