@@ -336,3 +336,28 @@ def test_tiles_that_blocks_share(lengths, n_kv, G, d, window, sinks, dtype):
     gpu_or_skip()
     QKV, dO, edges, offsets = make(lengths, 0, 2, n_kv, G, d, dtype, 11)
     check(QKV, dO, edges, offsets, n_kv * G, n_kv, window, sinks, dtype, 0.2 if dtype == F32 else -0.2)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n_kv,G,d,window,sinks", [(1, 2, 64, 0, 0), (2, 1, 8, 3, 1)])
+def test_many_sequences(n_kv, G, d, window, sinks, dtype):
+    # more than a lane, and than a warp, looks at in a step; blocks that take many tiles; rows before and behind
+    gpu_or_skip()
+    lengths = tuple((7 * i * i + 3 * i) % 23 if i % 5 else 0 for i in range(601)) + (200,) + (1,) * 300
+    QKV, dO, edges, offsets = make(lengths, 3, 4, n_kv, G, d, dtype, 12)
+    check(QKV, dO, edges, offsets, n_kv * G, n_kv, window, sinks, dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_offsets_that_fall_among_many(dtype):
+    gpu_or_skip()
+    lengths = (5, 0, 3) * 100
+    QKV, dO, edges, offsets = make(lengths, 0, 0, 1, 1, 16, dtype, 13)
+    good = tp.tp_attn_core_forward(QKV, 1, 1, offsets=offsets)
+    bad = offsets.clone()
+    at = 140  # an empty sequence's end: read as the one before, the same sequences
+    assert edges[at - 1] == edges[at]
+    bad[at] = -5
+    got = tp.tp_attn_core_forward(QKV, 1, 1, offsets=bad)
+    assert tp.device_status() != 0 and tp.device_status() == 0
+    assert torch.equal(got["O"], good["O"]) and torch.equal(got["lse"], good["lse"])

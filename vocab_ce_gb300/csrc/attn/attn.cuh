@@ -70,10 +70,79 @@ struct Tile {
     int part, parts;              // of the blocks without a tile
 };
 
-// Every lane of a warp calls it. `x` counts tiles of `rows` rows over all sequences;
-// the grid has grid_tiles of them for each head, more than there are tiles. Offsets
-// that fall, or lie outside, are read as the nearest that do not.
-__device__ __forceinline__ Tile find_tile(const Shape &s, int x, int rows, int grid_tiles) {
+// How far a search has come: sequences passed, their last row, their tiles. The next search
+// goes on there if it looks for no earlier tile, so that a block which takes tiles in order
+// reads the offsets once (4096 sequences of 16 tokens, 32 heads on 8 of 128: from the start
+// for each tile 15.3 ms and backward 29; so 1.7 and 7.0).
+struct Scan {
+    int first = -1, passed, end, before;
+};
+
+// Eight sequences a lane from scan.passed on, their loads under way together; true: the tile
+// is among them, else they are passed.
+__device__ __forceinline__ bool scan_step(const Shape &s, int x, int shift, Scan &scan, Tile &t) {
+    constexpr int K = 8;
+    const int lane = threadIdx.x & 31, T = static_cast<int>(s.T), b0 = scan.passed + lane * K;
+    int given[K], most = scan.end;
+#pragma unroll
+    for (int k = 0; k < K; ++k) given[k] = b0 + k < s.sequences ? s.offsets[b0 + k + 1] : INT_MIN;
+#pragma unroll
+    for (int k = 0; k < K; ++k) most = max(most, min(given[k], T));
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, most, d);
+        if (lane >= d) most = max(most, o);
+    }
+    const int up = __shfl_up_sync(0xffffffffu, most, 1), begin = lane == 0 ? scan.end : up;
+    int sum = 0, e = begin;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int from = e;
+        e = max(e, min(given[k], T));
+        if (b0 + k < s.sequences && given[k] != e) ptx::record_error(s.err, kErrInvalid | (6u << 8));
+        sum += (e - from + (1 << shift) - 1) >> shift;
+    }
+    int up_to = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, up_to, d);
+        if (lane >= d) up_to += o;
+    }
+    int at = x - scan.before - (up_to - sum);
+    const uint32_t found = __ballot_sync(0xffffffffu, at >= 0 && at < sum);
+    if (!found) {
+        scan.passed += 32 * K;
+        scan.end = __shfl_sync(0xffffffffu, most, 31);
+        scan.before += __shfl_sync(0xffffffffu, up_to, 31);
+        return false;
+    }
+    // of the lane that has it
+    int row0 = begin, n = 0, tiles = 0;
+    e = begin;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int from = e;
+        e = max(e, min(given[k], T));
+        const int here = (e - from + (1 << shift) - 1) >> shift;
+        if (tiles <= at) {  // not reached yet
+            at -= tiles;
+            row0 = from;
+            n = e - from;
+            tiles = here;
+        }
+    }
+    const int who = __ffs(found) - 1;
+    t.row0 = __shfl_sync(0xffffffffu, row0, who);
+    t.n = __shfl_sync(0xffffffffu, n, who);
+    t.tile = __shfl_sync(0xffffffffu, at, who);
+    t.tiles = __shfl_sync(0xffffffffu, tiles, who);
+    return true;
+}
+
+// Every lane of a warp calls it. `x` counts tiles of `rows` (a power of two) rows over all
+// sequences; the grid has grid_tiles of them for each head, more than there are tiles.
+// Offsets that fall, or lie outside, are read as the nearest that do not.
+__device__ __forceinline__ Tile find_tile(const Shape &s, int x, int rows, int grid_tiles, Scan &scan) {
     Tile t{};
     if (!s.offsets) {
         const int tiles = static_cast<int>((s.T + rows - 1) / rows);
@@ -88,49 +157,23 @@ __device__ __forceinline__ Tile find_tile(const Shape &s, int x, int rows, int g
         t.parts = grid_tiles - tiles;
         return t;
     }
-    const int lane = threadIdx.x & 31;
-    const int T = static_cast<int>(s.T);
-    int first = s.offsets[0], given = lane < s.sequences ? s.offsets[lane + 1] : 0;
-    if (first < 0 || first > T) {
-        if (lane == 0) ptx::record_error(s.err, kErrInvalid | (6u << 8));
-        first = first < 0 ? 0 : T;
+    if (scan.first < 0 || x < scan.before) {
+        const int T = static_cast<int>(s.T);
+        int first = s.offsets[0];
+        if (first < 0 || first > T) {
+            if ((threadIdx.x & 31) == 0) ptx::record_error(s.err, kErrInvalid | (6u << 8));
+            first = first < 0 ? 0 : T;
+        }
+        scan.first = scan.end = first;
+        scan.passed = scan.before = 0;
     }
-    int end = first, before = 0;  // of the sequences so far: the last row, the tiles
-    for (int b0 = 0; b0 < s.sequences; b0 += 32) {
-        if (b0) given = b0 + lane < s.sequences ? s.offsets[b0 + lane + 1] : 0;
-        int e = b0 + lane < s.sequences ? max(end, min(given, T)) : end;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, e, d);
-            if (lane >= d) e = max(e, o);
-        }
-        const int up = __shfl_up_sync(0xffffffffu, e, 1);
-        const int begin = lane == 0 ? end : up;
-        if (b0 + lane < s.sequences && given != e) ptx::record_error(s.err, kErrInvalid | (6u << 8));
-        const int tiles = (e - begin + rows - 1) / rows;
-        int sum = tiles;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, sum, d);
-            if (lane >= d) sum += o;
-        }
-        const int at = x - before - (sum - tiles);
-        const uint32_t found = __ballot_sync(0xffffffffu, at >= 0 && at < tiles);
-        if (found) {
-            const int who = __ffs(found) - 1;
-            t.row0 = __shfl_sync(0xffffffffu, begin, who);
-            t.n = __shfl_sync(0xffffffffu, e - begin, who);
-            t.tile = __shfl_sync(0xffffffffu, at, who);
-            t.tiles = __shfl_sync(0xffffffffu, tiles, who);
-            return t;
-        }
-        end = __shfl_sync(0xffffffffu, e, 31);
-        before += __shfl_sync(0xffffffffu, sum, 31);
-    }
-    t.head_rows = first;
-    t.tail_row = end;
-    t.part = x - before;
-    t.parts = grid_tiles - before;
+    const int shift = __ffs(rows) - 1;
+    while (scan.passed < s.sequences)
+        if (scan_step(s, x, shift, scan, t)) return t;
+    t.head_rows = scan.first;
+    t.tail_row = scan.end;
+    t.part = x - scan.before;
+    t.parts = grid_tiles - scan.before;
     return t;
 }
 
@@ -274,7 +317,8 @@ __device__ __forceinline__ void plain_add(const float *P, const float *X, int pi
         float4 p[4];  // four rows (or columns) of P, four k each
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            p[i] = *reinterpret_cast<const float4 *>(P + (ROWS ? (k + i) * kPitchP + 4 * ty : (4 * ty + i) * kPitchP + k));
+            p[i] = *reinterpret_cast<const float4 *>(
+                P + (ROWS ? (k + i) * kPitchP + 4 * ty : (4 * ty + i) * kPitchP + k));
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
             const int c = 4 * tx + 64 * m;
@@ -316,6 +360,10 @@ constexpr int kMaxRanks = 8;
 __device__ __forceinline__ Share this_share(int ranks) {
     return Share{static_cast<int>(blockIdx.x % static_cast<unsigned>(ranks)), ranks};
 }
+// One block (or cluster) for each tile, so that the SMs take them as they become free; of
+// many sequences fewer blocks, which take several tiles each, in order (see Scan).
+inline bool many_sequences(const Shape &s) { return s.offsets && s.sequences > 256; }
+inline int64_t many_blocks(int64_t units) { return std::min<int64_t>(units, 8 * num_sms()); }
 // For `units` tiles, `longest` of which have about `steps` steps each; an SM has the
 // registers for one block. As long as all blocks run at once more ranks cost nothing (a
 // sequence of 200 tokens, one head: forward 39 -> 14 us, backward 69 -> 24). Beyond that,
@@ -326,6 +374,7 @@ __device__ __forceinline__ Share this_share(int ranks) {
 // for as many SMs of one group), nor do any where a window makes all tiles alike (window
 // 128: 28 -> 44 and 92 -> 103 us).
 inline int ranks_of(const Shape &s, int64_t units, int64_t longest, int64_t steps, int64_t least) {
+    if (many_sequences(s)) return 1;
     const int64_t room = num_sms();
     const bool uneven = s.window == 0 || 2 * int64_t{s.window} >= s.T;
     int ranks = 1;

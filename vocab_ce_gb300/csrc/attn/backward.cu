@@ -244,7 +244,7 @@ __device__ __forceinline__ void plain_dkv_tile(const Shape &s, const T *QKV, con
     ptx::cluster_sync();  // until all have read
 }
 
-template <typename T>
+template <typename T, bool MANY>
 __global__ void __launch_bounds__(kPlainThreads)
     plain_backward_kernel(const Shape s, const T *QKV, const T *dO, const float2 *stats, int tiles, int ranks,
                           T *dQKV) {
@@ -252,26 +252,30 @@ __global__ void __launch_bounds__(kPlainThreads)
     float *const smem = reinterpret_cast<float *>(smem4);
     grid_begin();
     const Share by = this_share(ranks);
-    const int unit = static_cast<int>(blockIdx.x / static_cast<unsigned>(ranks)), of_keys = tiles * s.n_kv;
-    // dK and dV have the most steps and come first: those of the first keys, seen by the most queries; then dQ,
-    // that of the last queries, which see the most keys
-    if (unit < of_keys) {
-        const int kv = unit % s.n_kv;
-        const Tile t = find_tile(s, unit / s.n_kv, kRows, tiles);
-        if (t.n) {
-            plain_dkv_tile(s, QKV, dO, stats, t.row0, t.n, t.tile * kRows, kv, dQKV, smem, by);
-        } else if (by.rank == 0) {
-            zero_rest(s, t, dQKV, s.ld, static_cast<int64_t>(s.k_head(kv)) * s.d);
-            zero_rest(s, t, dQKV, s.ld, static_cast<int64_t>(s.v_head(kv)) * s.d);
+    const int64_t of_keys = static_cast<int64_t>(tiles) * s.n_kv;
+    Scan scan;
+    int64_t unit = blockIdx.x / static_cast<unsigned>(ranks);
+#pragma unroll 1
+    do {
+        // dK and dV have the most steps and come first: those of the first keys, seen by the most queries; then dQ,
+        // that of the last queries, which see the most keys
+        const bool keys = unit < of_keys;
+        const int heads = keys ? s.n_kv : s.n_q, at = static_cast<int>(keys ? unit : unit - of_keys), h = at % heads;
+        const Tile t = find_tile(s, at / heads, kRows, tiles, scan);
+        if (t.n == 0) {
+            if (by.rank == 0) {
+                zero_rest(s, t, dQKV, s.ld, static_cast<int64_t>(keys ? s.k_head(h) : s.q_head(h)) * s.d);
+                if (keys) zero_rest(s, t, dQKV, s.ld, static_cast<int64_t>(s.v_head(h)) * s.d);
+            }
+        } else {
+            if (MANY) plain_sync();  // the tile before
+            if (keys)
+                plain_dkv_tile(s, QKV, dO, stats, t.row0, t.n, t.tile * kRows, h, dQKV, smem, by);
+            else
+                plain_dq_tile(s, QKV, dO, stats, t.row0, t.n, (t.tiles - 1 - t.tile) * kRows, h, dQKV, smem, by);
         }
-    } else {
-        const int h = (unit - of_keys) % s.n_q;
-        const Tile t = find_tile(s, (unit - of_keys) / s.n_q, kRows, tiles);
-        if (t.n)
-            plain_dq_tile(s, QKV, dO, stats, t.row0, t.n, (t.tiles - 1 - t.tile) * kRows, h, dQKV, smem, by);
-        else if (by.rank == 0)
-            zero_rest(s, t, dQKV, s.ld, static_cast<int64_t>(s.q_head(h)) * s.d);
-    }
+        unit += gridDim.x;
+    } while (MANY && unit < of_keys + static_cast<int64_t>(tiles) * s.n_q);
 }
 
 // ------------------------------------------------------------------ tiles on the tensor cores
@@ -328,7 +332,8 @@ struct Shared {
 
 // Tiles of all sequences, and the rows of none.
 __device__ __forceinline__ Tile count_tiles(const Shape &s, int &tiles) {
-    Tile t = find_tile(s, INT_MAX, kTile, 0);
+    Scan scan;
+    Tile t = find_tile(s, INT_MAX, kTile, 0, scan);
     tiles = INT_MAX - t.part;
     t.part = blockIdx.x;
     t.parts = gridDim.x;
@@ -336,7 +341,7 @@ __device__ __forceinline__ Tile count_tiles(const Shape &s, int &tiles) {
 }
 
 // Unit `id` of so many tiles; every lane of a warp calls it.
-__device__ __forceinline__ Unit find_unit(const Shape &s, int id, int tiles) {
+__device__ __forceinline__ Unit find_unit(const Shape &s, int id, int tiles, Scan &scan) {
     Unit u{};
     u.id = id;
     u.kind = kEnd;
@@ -345,7 +350,7 @@ __device__ __forceinline__ Unit find_unit(const Shape &s, int id, int tiles) {
     u.kind = id < of_keys ? kKeys : kQueries;
     const int heads = u.kind == kKeys ? s.n_kv : s.n_q, at = u.kind == kKeys ? id : static_cast<int>(id - of_keys);
     u.head = at % heads;
-    u.t = find_tile(s, at / heads, kTile, 0);
+    u.t = find_tile(s, at / heads, kTile, 0, scan);
     if (u.kind == kKeys) {
         // the first keys are seen by the most queries, the last queries see the most keys
         u.first = u.t.tile * kTile;
@@ -781,6 +786,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             // ------------------------------------------------ what comes next
             int tiles;
             const Tile rest = count_tiles(s, tiles);
+            Scan scan;
             bool zero = rest.head_rows + (s.T - rest.tail_row) != 0;
             for (int r = 0;; ++r) {
                 Unit next{};
@@ -791,7 +797,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 } else {
                     int id = lane == 0 ? atomicAdd(shared.counter, 1) : 0;
                     id = __shfl_sync(0xffffffffu, id, 0);
-                    next = find_unit(s, id, tiles);
+                    next = find_unit(s, id, tiles, scan);
                 }
                 if (!wait(&m.unit_empty[r & 1], ((r >> 1) & 1) ^ 1, 28)) break;
                 if (lane == 0) {
@@ -818,7 +824,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     count_tiles(s, tiles);
     plain_sync();  // all have read m.odd
     for (; odd >= 0; odd = shared.next[odd]) {
-        const Unit w = find_unit(s, odd, tiles);
+        Scan scan;
+        const Unit w = find_unit(s, odd, tiles, scan);
 #pragma unroll 1
         for (int at = w.first; at < min(w.t.n, w.first + kTile); at += kRows) {
             plain_sync();
@@ -869,12 +876,17 @@ tpce_status plain_backward(const Shape &s, const void *QKV, const void *dO, cons
     const size_t smem = PlainSmem(s.d).backward();
     const int64_t units = static_cast<int64_t>(tiles) * (s.n_q + s.n_kv);
     const int ranks = ranks_of(s, units, static_cast<int64_t>(tiles) * s.n_kv, steps_of(s) * s.group, 8);
-    cudaError_t e = allow_smem<plain_backward_kernel<T>>();
-    if (e != cudaSuccess) return fail_cuda(e, name);
     KernelTimer timer(name, stream);
-    e = step::launch_clusters(ranks, plain_backward_kernel<T>, static_cast<unsigned>(units * ranks), kPlainThreads,
-                              smem, stream, s, static_cast<const T *>(QKV), static_cast<const T *>(dO), stats, tiles,
-                              ranks, static_cast<T *>(dQKV));
+    auto go = [&](auto kernel, cudaError_t e, int64_t blocks) {
+        if (e != cudaSuccess) return e;
+        return step::launch_clusters(ranks, kernel, static_cast<unsigned>(blocks), kPlainThreads, smem, stream, s,
+                                     static_cast<const T *>(QKV), static_cast<const T *>(dO), stats, tiles, ranks,
+                                     static_cast<T *>(dQKV));
+    };
+    const cudaError_t e =
+        many_sequences(s)
+            ? go(plain_backward_kernel<T, true>, allow_smem<plain_backward_kernel<T, true>>(), many_blocks(units))
+            : go(plain_backward_kernel<T, false>, allow_smem<plain_backward_kernel<T, false>>(), units * ranks);
     return e == cudaSuccess ? check_launch(name, stream) : fail_cuda(e, name);
 }
 

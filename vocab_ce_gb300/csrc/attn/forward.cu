@@ -155,21 +155,28 @@ __device__ __forceinline__ void forward_rest(const Shape &s, const Tile &t, int 
         lse[h * s.T + (r < t.head_rows ? r : t.tail_row + r - t.head_rows)] = 0.0f;
 }
 
-template <typename T>
+template <typename T, bool MANY>
 __global__ void __launch_bounds__(kPlainThreads)
     plain_forward_kernel(const Shape s, const T *QKV, int tiles, int ranks, T *O, float *lse) {
     extern __shared__ float4 smem4[];
     grid_begin();
     const Share by = this_share(ranks);
-    const int unit = static_cast<int>(blockIdx.x / static_cast<unsigned>(ranks)), h = unit % s.n_q;
-    const Tile t = find_tile(s, unit / s.n_q, kRows, tiles);
-    if (t.n == 0) {
-        if (by.rank == 0) forward_rest(s, t, h, O, lse);
-        return;
-    }
-    // the last queries see the most keys: they come first
-    plain_forward_tile(s, QKV, t.row0, t.n, (t.tiles - 1 - t.tile) * kRows, h, O, lse,
-                       reinterpret_cast<float *>(smem4), by);
+    Scan scan;
+    int64_t unit = blockIdx.x / static_cast<unsigned>(ranks);
+#pragma unroll 1
+    do {
+        const int h = static_cast<int>(unit % s.n_q);
+        const Tile t = find_tile(s, static_cast<int>(unit / s.n_q), kRows, tiles, scan);
+        if (t.n == 0) {
+            if (by.rank == 0) forward_rest(s, t, h, O, lse);
+        } else {
+            if (MANY) plain_sync();  // the tile before
+            // the last queries see the most keys: they come first
+            plain_forward_tile(s, QKV, t.row0, t.n, (t.tiles - 1 - t.tile) * kRows, h, O, lse,
+                               reinterpret_cast<float *>(smem4), by);
+        }
+        unit += gridDim.x;
+    } while (MANY && unit < static_cast<int64_t>(tiles) * s.n_q);
 }
 
 template <typename T>
@@ -179,10 +186,15 @@ tpce_status plain_forward(const Shape &s, const void *QKV, void *O, float *lse, 
     const size_t smem = PlainSmem(s.d).forward();
     const int64_t units = static_cast<int64_t>(tiles) * s.n_q;
     const int ranks = ranks_of(s, units, units, steps_of(s), 4);
-    cudaError_t e = allow_smem<plain_forward_kernel<T>>();
-    if (e == cudaSuccess)
-        e = step::launch_clusters(ranks, plain_forward_kernel<T>, static_cast<unsigned>(units * ranks), kPlainThreads,
-                                  smem, stream, s, static_cast<const T *>(QKV), tiles, ranks, static_cast<T *>(O), lse);
+    auto go = [&](auto kernel, cudaError_t e, int64_t blocks) {
+        if (e != cudaSuccess) return e;
+        return step::launch_clusters(ranks, kernel, static_cast<unsigned>(blocks), kPlainThreads, smem, stream, s,
+                                     static_cast<const T *>(QKV), tiles, ranks, static_cast<T *>(O), lse);
+    };
+    const cudaError_t e =
+        many_sequences(s)
+            ? go(plain_forward_kernel<T, true>, allow_smem<plain_forward_kernel<T, true>>(), many_blocks(units))
+            : go(plain_forward_kernel<T, false>, allow_smem<plain_forward_kernel<T, false>>(), units * ranks);
     return e == cudaSuccess ? check_launch("attn_forward", stream) : fail_cuda(e, "attn_forward");
 }
 
@@ -266,13 +278,13 @@ struct Pair {
 
 // The block's r-th pair: neighbouring blocks take neighbouring pairs, in turn from both
 // ends, and the pairs with the most keys come first.
-__device__ __forceinline__ Work find_work(const Shape &s, int r, int units, int tiles, bool by_heads) {
+__device__ __forceinline__ Work find_work(const Shape &s, int r, int units, int tiles, bool by_heads, Scan &scan) {
     Work w{};
     w.unit = -1;
     const int64_t item = static_cast<int64_t>(r) * gridDim.x + (r & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
     if (item >= static_cast<int64_t>(units) * tiles) return w;
     const int rows = by_heads ? kTile : 2 * kTile;
-    w.t = find_tile(s, static_cast<int>(item / units), rows, tiles);
+    w.t = find_tile(s, static_cast<int>(item / units), rows, tiles, scan);
     if (w.t.n == 0 && w.t.head_rows + (s.T - w.t.tail_row) == 0) return w;  // no rows left to be zeroed
     w.unit = static_cast<int>(item % units);
     w.first = (w.t.tiles - 1 - w.t.tile) * rows;
@@ -589,8 +601,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             __syncwarp();
         } else {
             // ------------------------------------------------ what comes next
+            Scan scan;
             for (int r = 0;; ++r) {
-                const Work w = find_work(s, r, units, tiles, by_heads);
+                const Work w = find_work(s, r, units, tiles, by_heads, scan);
                 if (!wait_all(&m.work_empty[r & 1], ((r >> 1) & 1) ^ 1, abort_flag, s.err, 29)) break;
                 if (lane == 0) {
                     m.work[r & 1] = w;
@@ -615,9 +628,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     if (any == 0 || *abort_flag || threadIdx.x >= kPlainThreads) return;
     // the bits lie where the tiles below do not reach
     static_assert(offsetof(FwdSmem, odd) >= 4 * (3 * kRows * (kMaxDim + 4) + kRows * kPitchP), "room for plain tiles");
+    Scan scan;
 #pragma unroll 1
     for (int r = 0;; ++r) {
-        const Work w = find_work(s, r, units, tiles, by_heads);
+        const Work w = find_work(s, r, units, tiles, by_heads, scan);
         if (w.unit < 0 || w.t.n == 0) break;
 #pragma unroll 1
         for (int i = 0; i < 2; ++i) {
