@@ -1,7 +1,8 @@
 """The operators of a training step around the GEMMs: RMS norm with the
-residual's addition, tokens sorted by expert and back, and the AdamW step.
+residual's addition, tokens sorted by expert and back, the embedding, the
+attention core, and the AdamW step.
 
-The arithmetic is in ``csrc/step/*.cu``; the checks of tensors, the outputs and
+The arithmetic is in ``csrc/step/*.cu`` and ``csrc/attn/*.cu``; the checks of tensors, the outputs and
 the calls of the C ABI are compiled too (``csrc/step/binding.cpp``), because in
 Python they would take several times as long as the smallest kernels. With
 ``stream`` given, new outputs and workspaces are taken from that stream's

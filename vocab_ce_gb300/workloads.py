@@ -160,8 +160,8 @@ def swiglu_inputs(w: Workload, seed: int = 0, device="cpu") -> Dict[str, torch.T
 
 def attn_inputs(w: Workload, seed: int = 0, device="cpu") -> Dict[str, torch.Tensor]:
     """Inputs of the attention projections: X [T,h], Wqkv [h,(n_q+2 n_kv) d],
-    O [T, n_q d] (the attention core's output, which this library does not
-    compute, drawn N(0,1)), Wo [n_q d, h] (scaled like B: it feeds the
+    O [T, n_q d] (the attention core's output, which the projections' workloads
+    do not run: drawn N(0,1)), Wo [n_q d, h] (scaled like B: it feeds the
     residual), upstream gradients dQKV [T,(n_q+2 n_kv) d] and dZ [T,h], and
     zero fp32 biases bqkv, bo."""
     dt = w.torch_dtype
