@@ -77,3 +77,17 @@ def test_cpu_tensors_are_refused(L):
         tp.tp_attn_core_forward(x, 2, 1)
     with pytest.raises(ValueError):
         tp.tp_attn_core_backward(torch.zeros(4, 128), x, torch.zeros(4, 128), torch.zeros(2, 4), 2, 1)
+
+
+@pytest.mark.parametrize("call", [forward, backward])
+def test_how_long_a_unit_of_work_may_take(L, call):
+    for bad in ({"T": (1 << 26) + 1, "n": 1, "kv": 1}, {"T": (1 << 20) + 1, "n": 64, "kv": 1},
+                {"T": 1 << 21, "n": 64, "kv": 1, "window": 1 << 20, "sinks": 1},
+                {"T": 1 << 21, "n": 64, "kv": 1, "window": 1 << 20}):
+        assert call(L, **bad) == SHAPE and b"2^26" in L.tpce_last_error(), bad
+    # not refused for that: a misaligned pointer is what these are turned down for
+    room = {"size": 1 << 40} if call is backward else {}
+    for fine in ({"T": 1 << 20, "n": 64, "kv": 1}, {"T": 1 << 21, "n": 64, "kv": 1, "window": 4096},
+                 {"T": 1 << 27, "n": 1, "kv": 1, "dtype": 1}):
+        assert call(L, O=3 * MB + 8, **room, **fine) == ALIGN, fine
+    assert call(L, scale=3e38) == INVALID

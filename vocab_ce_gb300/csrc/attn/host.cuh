@@ -8,11 +8,14 @@
 namespace tpce {
 namespace attn {
 
+constexpr int64_t kMaxReach = int64_t{1} << 26;
+
 inline tpce_status make_shape(const char *name, const int32_t *offsets, int sequences, int64_t T, int64_t n_heads,
                               int64_t n_kv_heads, int64_t head_dim, int64_t window, int64_t sinks, float scale,
                               int dtype, Shape &s) {
     if (dtype != TPCE_BF16 && dtype != TPCE_F32) return fail(TPCE_ERR_INVALID, "%s: dtype %d", name, dtype);
-    if (!std::isfinite(scale)) return fail(TPCE_ERR_INVALID, "%s: scale is not finite", name);
+    if (!std::isfinite(scale * kLog2e))
+        return fail(TPCE_ERR_INVALID, "%s: scale is not finite, or not times log2(e)", name);
     if (n_kv_heads < 1 || n_heads < 1 || n_heads > 4096 || n_heads % n_kv_heads != 0)
         return fail(TPCE_ERR_SHAPE, "%s: %lld query heads (up to 4096) over %lld key/value heads", name,
                     static_cast<long long>(n_heads), static_cast<long long>(n_kv_heads));
@@ -38,6 +41,12 @@ inline tpce_status make_shape(const char *name, const int32_t *offsets, int sequ
     // a window of T keys hides nothing, and then sinks show nothing more
     s.window = window >= T ? 0 : static_cast<int>(window);
     s.sinks = s.window ? static_cast<int>(std::min(sinks, T)) : 0;
+    // a unit of work on the tensor cores, 1.3 us for each 128 queries of a head that see its keys, stays well below
+    // the limit of the waits for it
+    const int64_t reach = s.window && !s.sinks ? std::min(T, window + 256) : T;
+    if (dtype == TPCE_BF16 && reach * s.group > kMaxReach)
+        return fail(TPCE_ERR_SHAPE, "%s: %lld tokens that see a key, with %d query heads that share it: more than 2^26",
+                    name, static_cast<long long>(reach), s.group);
     s.scale = scale;
     s.err = device_error_word();
     return TPCE_OK;
