@@ -259,3 +259,25 @@ def test_tensors_that_are_refused():
         tp.tp_embedding_backward(big[:10], ids, 9, out=big[9:])
     with pytest.raises(tp.TpceError, match="overlap"):
         tp.tp_embedding_forward(ids, big[:8], out=big[7:17])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,h,v_pad", [
+    (70_000, 8, 90_001), (70_000, 64, 5000), (66_000, 1000, 3001),  # more tokens than a cluster sorts
+    (66_000, 5000, 401),
+    (5, 1024, 60_000), (200, 16, 4_000_000),                        # larger tables than it zeroes
+    (900, 1000, 30_001),
+])
+def test_every_row_of_a_new_table_is_written(T, h, v_pad, dtype):
+    gpu_or_skip()
+    ids, dX = ids_of(T, v_pad, "zipf", 21), rows(T, h, dtype, 22)
+    dE = torch.full((v_pad, h), math.nan, device="cuda", dtype=dtype)
+    tp.tp_embedding_backward(dX, ids, v_pad, out=dE)
+    runs = torch.bincount(ids[ids >= 0].long(), minlength=v_pad)
+    assert not dE[runs == 0].view(torch.uint8).any()
+    named = (runs > 0).nonzero()[:, 0]
+    at = torch.full((v_pad,), -1, dtype=torch.int32, device="cuda")
+    at[named] = torch.arange(len(named), dtype=torch.int32, device="cuda")
+    few = torch.where(ids >= 0, at[ids.clamp_min(0).long()], -1)
+    check_backward(dE[named], dX, few, len(named), 1.0, dtype)
+    assert tp.device_status() == 0

@@ -654,7 +654,7 @@ extern "C" tpce_status tp_embedding_forward(const int32_t *ids, const void *E, i
     if (st != TPCE_OK || T == 0) return st;
     if ((st = check_pointers("tp_embedding_forward", {ids, E, X})) != TPCE_OK) return st;
     const size_t rows = bytes_of(T, h, dtype);
-    if (overlap(X, rows, E, bytes_of(v_valid, h, dtype)) || overlap(X, rows, ids, static_cast<size_t>(T) * 4))
+    if (overlap(X, rows, E, bytes_of(v_pad, h, dtype)) || overlap(X, rows, ids, static_cast<size_t>(T) * 4))
         return fail(TPCE_ERR_INVALID, "tp_embedding_forward: X overlaps E or ids");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return dtype == TPCE_BF16 ? embed_forward<__nv_bfloat16>(ids, E, T, h, v_valid, scale, X, s)
