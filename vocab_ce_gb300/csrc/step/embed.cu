@@ -76,14 +76,19 @@ __global__ void __launch_bounds__(kThreads)
 // sorted by the blocks of one cluster in one launch, which read each other's counts of
 // digits (16,384 tokens over 129,024 ids: two launches a pass took 22 us, this one
 // takes 18); for more the blocks' counts are one launch and their places the next.
+// Up to kRankTokens tokens are not sorted by digits: a token's place is the number of those
+// before it in the order, which all SMs count at once (embed_rank_kernel).
 constexpr int kClusterThreads = 1024;
-constexpr int64_t kZeroed = 96 << 20;
+constexpr int64_t kZeroed = 96 << 20, kRankZeroed = 48 << 20;
+constexpr int64_t kRankTokens = 2048;
 constexpr int kMaxBins = 1024, kCluster = 8;
+constexpr int kRankChunk = 32;
 constexpr int64_t kSortChunk = 1024, kSortBlocks = 256, kClusterTokens = 65536;
 
 struct SortSplit {
     int64_t chunk;
     int blocks, passes, bits;  // bits of a pass
+    bool rank;                 // `blocks` blocks that count
     bool cluster;              // one of `blocks` blocks
 };
 inline SortSplit sort_split(int64_t tokens, int64_t v_pad) {
@@ -92,9 +97,14 @@ inline SortSplit sort_split(int64_t tokens, int64_t v_pad) {
     while ((int64_t{1} << all) <= v_pad) ++all;
     sp.passes = (all + 9) / 10;
     sp.bits = (all + sp.passes - 1) / sp.passes;
-    sp.cluster = tokens <= kClusterTokens;
+    sp.rank = tokens <= kRankTokens;
+    sp.cluster = !sp.rank && tokens <= kClusterTokens;
     sp.chunk = std::max<int64_t>(kSortChunk, (tokens + kSortBlocks - 1) / kSortBlocks);
-    if (sp.cluster) {
+    if (sp.rank) {
+        sp.chunk = kRankChunk;
+        sp.blocks = static_cast<int>((tokens + kRankChunk - 1) / kRankChunk);
+        sp.passes = 0;  // the result lies in key[0], token[0]
+    } else if (sp.cluster) {
         sp.blocks = 1;
         while (sp.blocks < kCluster && sp.blocks * kSortChunk < tokens) sp.blocks *= 2;
         sp.chunk = (tokens + sp.blocks - 1) / sp.blocks;
@@ -286,6 +296,54 @@ __global__ void __launch_bounds__(kThreads)
                                   key_out, token_out, smem, scan, err);
 }
 
+// Place of each of a block's kRankChunk tokens: how many keys are smaller, or equal and of an
+// earlier token. Eight threads a token compare it with all keys, which lie in shared memory
+// (a call of 999 tokens of 1000 added to a table: 12 us, 18 with one block's two passes; of
+// 4096 of 1024 24 and 25, of 8192 36 and 26, since all pairs are compared). The blocks after the first `blocks` write zeros as in
+// embed_sort_kernel.
+__global__ void __launch_bounds__(kThreads)
+    embed_rank_kernel(const int32_t *ids, int n, int blocks, int32_t v_valid, int32_t v_pad, int32_t *key,
+                      int32_t *token, uint4 *table, int64_t vectors, uint32_t *err) {
+    extern __shared__ int4 keys4[];  // of n tokens, rounded up to chunks
+    grid_begin();
+    if (static_cast<int>(blockIdx.x) >= blocks) {
+        const int64_t stride = static_cast<int64_t>(gridDim.x - blocks) * kThreads;
+        for (int64_t i = static_cast<int64_t>(blockIdx.x - blocks) * kThreads + threadIdx.x; i < vectors; i += stride)
+            table[i] = make_uint4(0u, 0u, 0u, 0u);
+        return;
+    }
+    int32_t *keys = reinterpret_cast<int32_t *>(keys4);
+    const int first = blockIdx.x * kRankChunk;
+#pragma unroll 8
+    for (int i = threadIdx.x; i < blocks * kRankChunk; i += kThreads)
+        // those past the end are greater than any and come after all
+        keys[i] = i < n ? key_of(ids[i], v_valid, v_pad, i / kRankChunk == static_cast<int>(blockIdx.x) ? err : nullptr)
+                        : INT_MAX;
+    __syncthreads();
+    constexpr int kEach = kThreads / kRankChunk;  // threads a token
+    const int t = first + threadIdx.x / kEach, part = threadIdx.x % kEach;
+    const int32_t mine = keys[t];
+    int place = 0;
+#pragma unroll 4
+    for (int j = part; j < first / 4; j += kEach) {
+        const int4 k = keys4[j];
+        place += (k.x <= mine) + (k.y <= mine) + (k.z <= mine) + (k.w <= mine);
+    }
+#pragma unroll 4
+    for (int j = (first + kRankChunk) / 4 + part; j < blocks * kRankChunk / 4; j += kEach) {
+        const int4 k = keys4[j];
+        place += (k.x < mine) + (k.y < mine) + (k.z < mine) + (k.w < mine);
+    }
+    for (int j = first + part; j < first + kRankChunk; j += kEach)
+        place += keys[j] < mine || (keys[j] == mine && j < t);
+#pragma unroll
+    for (int d = kEach / 2; d > 0; d >>= 1) place += __shfl_xor_sync(0xffffffffu, place, d);
+    if (part == 0 && t < n) {
+        key[place] = mine;
+        token[place] = t;
+    }
+}
+
 // All passes of a cluster's tokens; the last one ends in key[1], token[1] (odd passes) or key[0], token[0].
 // The blocks after the first `blocks`, if there are any, write zeros to the table's first rows meanwhile, as many
 // as the sort leaves time for (kZeroed bytes), whether tokens name them or not: that is not known yet.
@@ -329,7 +387,9 @@ struct SumSplit {
 };
 inline SumSplit sum_split(int64_t tokens, int64_t h) {
     SumSplit sp{};
-    sp.chunk = std::max<int64_t>(16, (tokens + 1023) / 1024);
+    // shorter chains where there are few (999 tokens: 10.3 us a call, with sixteen 12.1; one id
+    // for all 18.3 and 14.2, its run crosses more cuts)
+    sp.chunk = std::max<int64_t>(tokens <= kRankTokens ? 8 : 16, (tokens + 1023) / 1024);
     sp.chunks = static_cast<int>((tokens + sp.chunk - 1) / sp.chunk);
     const int64_t vectors = h / 8;
     sp.lanes = 8;
@@ -545,7 +605,7 @@ inline Layout layout_of(int64_t T, int64_t h, int64_t v_pad) {
     l.each = round_up(static_cast<size_t>(T) * sizeof(int32_t), 256);
     l.counts = 4 * l.each;
     l.partial = l.counts +
-                round_up(!so.cluster ? static_cast<size_t>(so.blocks) * (size_t{4} << so.bits) : 0, 256);
+                round_up(!so.cluster && !so.rank ? static_cast<size_t>(so.blocks) * (size_t{4} << so.bits) : 0, 256);
     l.total = l.partial + (su.chunks > 1 ? 2 * static_cast<size_t>(su.chunks) * static_cast<size_t>(h) * 4 : 0);
     return l;
 }
@@ -575,6 +635,16 @@ tpce_status embed_sort(const int32_t *ids, int64_t T, int64_t v_pad, int64_t v_v
                        const SortBuffers &buf, uint32_t *counts, void *table, size_t table_bytes, cudaStream_t s) {
     const int32_t valid = static_cast<int32_t>(v_valid), pad = static_cast<int32_t>(v_pad);
     KernelTimer timer("embed_sort", s);
+    if (sp.rank) {
+        const int64_t vectors = static_cast<int64_t>(table_bytes / 16);
+        const int64_t fill = std::min<int64_t>((vectors + 4 * kThreads - 1) / (4 * kThreads), int64_t{8} * num_sms());
+        const cudaError_t e =
+            launch(embed_rank_kernel, static_cast<unsigned>(sp.blocks + fill), kThreads,
+                   static_cast<size_t>(sp.blocks) * kRankChunk * sizeof(int32_t), s, ids, static_cast<int>(T),
+                   sp.blocks, valid, pad, buf.key[0], buf.token[0], static_cast<uint4 *>(table), vectors,
+                   device_error_word());
+        return e == cudaSuccess ? check_launch("embed_sort", s) : fail_cuda(e, "embed_sort");
+    }
     if (sp.cluster) {
         static std::atomic<uint64_t> allowed{0};  // devices on which the kernel may have more than 48 KB
         const size_t smem = sort_smem<kClusterThreads, uint16_t>(sp.bits);
@@ -703,7 +773,8 @@ extern "C" tpce_status tp_embedding_backward(const void *dX, const int32_t *ids,
     float *partial = reinterpret_cast<float *>(base + l.partial);
     const SortSplit sp = sort_split(T, v_pad);
     const size_t row = table / static_cast<size_t>(v_pad);
-    const int64_t zeroed = sp.cluster && !accumulate ? std::min(v_pad, static_cast<int64_t>(kZeroed / row)) : 0;
+    const int64_t meanwhile = sp.rank ? kRankZeroed : sp.cluster ? kZeroed : 0;  // bytes zeroed during the sort
+    const int64_t zeroed = accumulate ? 0 : std::min(v_pad, meanwhile / static_cast<int64_t>(row));
     if ((st = embed_sort(ids, T, v_pad, v_valid, sp, buf, counts, dE, static_cast<size_t>(zeroed) * row, s)) != TPCE_OK)
         return st;
     const int last = sp.passes & 1;
