@@ -299,8 +299,8 @@ __global__ void __launch_bounds__(kThreads)
 // Place of each of a block's kRankChunk tokens: how many keys are smaller, or equal and of an
 // earlier token. Eight threads a token compare it with all keys, which lie in shared memory
 // (a call of 999 tokens of 1000 added to a table: 12 us, 18 with one block's two passes; of
-// 4096 of 1024 24 and 25, of 8192 36 and 26, since all pairs are compared). The blocks after the first `blocks` write zeros as in
-// embed_sort_kernel.
+// 4096 of 1024 24 and 25, of 8192 36 and 26, since all pairs are compared). The blocks after
+// the first `blocks` write zeros as in embed_sort_kernel.
 __global__ void __launch_bounds__(kThreads)
     embed_rank_kernel(const int32_t *ids, int n, int blocks, int32_t v_valid, int32_t v_pad, int32_t *key,
                       int32_t *token, uint4 *table, int64_t vectors, uint32_t *err) {
@@ -432,8 +432,9 @@ inline int fill_rows(size_t row) {
 
 // The first `fill` blocks write zeros to the rows from `zeroed` on that no token names,
 // fill_rows of them each; the others add up chunks. Loads are issued four tokens at a time, with
-// the old row where a run ends. Bound by HBM: 16,384 tokens of 8192 bf16 into a tied table of
-// 129,024 rows (494 MB) in 92 us of the call's 123, 70% of DRAM's peak by its counters.
+// the old row where a run ends, and the next four's ids with them (2 to 4% less). Bound by HBM:
+// 16,384 tokens of 8192 bf16 into a tied table of 129,024 rows (494 MB) in 90 us of the call's
+// 120, 70% of DRAM's peak by its counters; with two blocks an SM instead of three 104.
 template <typename T>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
     embed_sum_kernel(const T *dX, const int32_t *key, const int32_t *token, int64_t n, int64_t v_pad, int vectors,
@@ -465,21 +466,30 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
     bool open = p0 > 0 && key[p0 - 1] == now;  // the run at hand began in a chunk before
     float sum[8] = {};
     constexpr int kBatch = 4;
+    int32_t next_k[kBatch + 1], next_t[kBatch];
+    auto fetch = [&](int64_t p) {
+#pragma unroll
+        for (int u = 0; u <= kBatch; ++u) next_k[u] = p + u < n ? key[p + u] : -1;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) next_t[u] = p + u < p1 ? token[p + u] : -1;
+    };
+    fetch(p0);
     for (int64_t p = p0; p < p1 && static_cast<uint32_t>(now) < v_pad; p += kBatch) {
         int32_t k[kBatch + 1];
         Raw8<T> x[kBatch], old[kBatch];
         bool there[kBatch];
 #pragma unroll
-        for (int u = 0; u <= kBatch; ++u) k[u] = p + u < n ? key[p + u] : -1;
+        for (int u = 0; u <= kBatch; ++u) k[u] = next_k[u];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             // places that the sort has not written (ids that changed under it) lead nowhere
-            const int32_t t = p + u < p1 ? token[p + u] : -1;
+            const int32_t t = next_t[u];
             there[u] = static_cast<uint32_t>(k[u]) < v_pad && static_cast<uint32_t>(t) < n;
             if (there[u]) x[u] = load8(dX + (static_cast<int64_t>(t) * vectors + at) * 8);
             if (add && there[u] && k[u + 1] != k[u])
                 old[u] = load8(dE + (static_cast<int64_t>(k[u]) * vectors + at) * 8);
         }
+        fetch(p + kBatch);  // during this batch's rows
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             if (!there[u]) {
