@@ -281,3 +281,22 @@ def test_every_row_of_a_new_table_is_written(T, h, v_pad, dtype):
     few = torch.where(ids >= 0, at[ids.clamp_min(0).long()], -1)
     check_backward(dE[named], dX, few, len(named), 1.0, dtype)
     assert tp.device_status() == 0
+
+
+@pytest.mark.parametrize("T", [1, 31, 32, 33, 1000, 2047, 2048, 2049, 4064, 4095, 4096, 4097])
+@pytest.mark.parametrize("v_pad", [7, 50_000, (1 << 24) - 1, 1 << 24])
+def test_lengths_around_the_kinds_of_sorts(T, v_pad):
+    # whole numbers: sums are exact in any split, and a token in another's place would be seen
+    gpu_or_skip()
+    for kind in ("random", "zipf", "same", "sorted"):
+        ids = ids_of(T, v_pad, kind, T)
+        dX = torch.arange(T, device="cuda", dtype=torch.float32)[:, None].expand(T, 8).contiguous() % 1024
+        # places that no token was sorted to would name row 0
+        ws = torch.zeros(tp.embedding_workspace_bytes(T, 8, v_pad), dtype=torch.uint8, device="cuda")
+        dE = tp.tp_embedding_backward(dX, ids, v_pad, ws=ws)
+        want = torch.zeros(v_pad, 8, device="cuda").index_add_(0, ids.clamp_min(0).long(),
+                                                              torch.where(ids[:, None] >= 0, dX, 0.0))
+        assert torch.equal(dE, want), kind
+        dX = rows(T, 8, torch.float32, 5)
+        assert torch.equal(tp.tp_embedding_backward(dX, ids, v_pad), tp.tp_embedding_backward(dX, ids, v_pad)), kind
+    assert tp.device_status() == 0

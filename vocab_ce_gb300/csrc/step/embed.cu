@@ -7,8 +7,8 @@
 // tokens name are touched. The product and the sums are taken in 32 bits and
 // rounded once.
 //
-// The backward sorts the tokens by id, stably (a radix sort: whole numbers, no
-// order of atomics in it), and adds up runs of equal ids in the order of the
+// The backward sorts the tokens by id, stably (by counting or by digits: whole
+// numbers, no order of atomics in it), and adds up runs of equal ids in the order of the
 // tokens, so the result is the same every time. A frequent id's run is long: the
 // sorted tokens are cut into chunks of equal length, and a run that crosses a
 // cut leaves fp32 sums in the workspace that a last kernel adds in order.
@@ -80,9 +80,9 @@ __global__ void __launch_bounds__(kThreads)
 // before it in the order, which all SMs count at once (embed_rank_kernel).
 constexpr int kClusterThreads = 1024;
 constexpr int64_t kZeroed = 96 << 20, kRankZeroed = 48 << 20;
-constexpr int64_t kRankTokens = 2048;
+constexpr int64_t kRankTokens = 4096;
 constexpr int kMaxBins = 1024, kCluster = 8;
-constexpr int kRankChunk = 32;
+constexpr int kRankEach = 4, kRankChunk = kRankEach * kThreads / 32;  // tokens of a warp, of a block
 constexpr int64_t kSortChunk = 1024, kSortBlocks = 256, kClusterTokens = 65536;
 
 struct SortSplit {
@@ -97,7 +97,7 @@ inline SortSplit sort_split(int64_t tokens, int64_t v_pad) {
     while ((int64_t{1} << all) <= v_pad) ++all;
     sp.passes = (all + 9) / 10;
     sp.bits = (all + sp.passes - 1) / sp.passes;
-    sp.rank = tokens <= kRankTokens;
+    sp.rank = tokens <= kRankTokens && v_pad < (1 << 24);  // keys up to v_pad, and one more, as fp32
     sp.cluster = !sp.rank && tokens <= kClusterTokens;
     sp.chunk = std::max<int64_t>(kSortChunk, (tokens + kSortBlocks - 1) / kSortBlocks);
     if (sp.rank) {
@@ -296,15 +296,16 @@ __global__ void __launch_bounds__(kThreads)
                                   key_out, token_out, smem, scan, err);
 }
 
-// Place of each of a block's kRankChunk tokens: how many keys are smaller, or equal and of an
-// earlier token. Eight threads a token compare it with all keys, which lie in shared memory
-// (a call of 999 tokens of 1000 added to a table: 12 us, 18 with one block's two passes; of
-// 4096 of 1024 24 and 25, of 8192 36 and 26, since all pairs are compared). The blocks after
-// the first `blocks` write zeros as in embed_sort_kernel.
+// Place of each of a block's tokens, kRankEach a warp: how many keys are smaller, or equal and of
+// an earlier token. The keys lie in shared memory as fp32, so that a comparison and its sum
+// are a subtraction that saturates at 0 and 1 and an addition; a key that is read is compared
+// with all of the warp's (calls added to a table: 999 tokens of 1000 18.3 us with digits, 9.0
+// so; 4096 of 1024 25.5 and 20.8; 8192 27 and 31, since all pairs are compared). The blocks
+// after the first `blocks` write zeros as in embed_sort_kernel.
 __global__ void __launch_bounds__(kThreads)
     embed_rank_kernel(const int32_t *ids, int n, int blocks, int32_t v_valid, int32_t v_pad, int32_t *key,
                       int32_t *token, uint4 *table, int64_t vectors, uint32_t *err) {
-    extern __shared__ int4 keys4[];  // of n tokens, rounded up to chunks
+    extern __shared__ float4 keys4[];  // of n tokens, rounded up to whole blocks
     grid_begin();
     if (static_cast<int>(blockIdx.x) >= blocks) {
         const int64_t stride = static_cast<int64_t>(gridDim.x - blocks) * kThreads;
@@ -312,35 +313,61 @@ __global__ void __launch_bounds__(kThreads)
             table[i] = make_uint4(0u, 0u, 0u, 0u);
         return;
     }
-    int32_t *keys = reinterpret_cast<int32_t *>(keys4);
-    const int first = blockIdx.x * kRankChunk;
-#pragma unroll 8
-    for (int i = threadIdx.x; i < blocks * kRankChunk; i += kThreads)
-        // those past the end are greater than any and come after all
-        keys[i] = i < n ? key_of(ids[i], v_valid, v_pad, i / kRankChunk == static_cast<int>(blockIdx.x) ? err : nullptr)
-                        : INT_MAX;
-    __syncthreads();
-    constexpr int kEach = kThreads / kRankChunk;  // threads a token
-    const int t = first + threadIdx.x / kEach, part = threadIdx.x % kEach;
-    const int32_t mine = keys[t];
-    int place = 0;
-#pragma unroll 4
-    for (int j = part; j < first / 4; j += kEach) {
-        const int4 k = keys4[j];
-        place += (k.x <= mine) + (k.y <= mine) + (k.z <= mine) + (k.w <= mine);
-    }
-#pragma unroll 4
-    for (int j = (first + kRankChunk) / 4 + part; j < blocks * kRankChunk / 4; j += kEach) {
-        const int4 k = keys4[j];
-        place += (k.x < mine) + (k.y < mine) + (k.z < mine) + (k.w < mine);
-    }
-    for (int j = first + part; j < first + kRankChunk; j += kEach)
-        place += keys[j] < mine || (keys[j] == mine && j < t);
+    float *keys = reinterpret_cast<float *>(keys4);
+    const int all = blocks * kRankChunk, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kBatch = 16;  // loads under way together
+    for (int i0 = threadIdx.x; i0 < all; i0 += kBatch * kThreads) {
+        int32_t id[kBatch];
 #pragma unroll
-    for (int d = kEach / 2; d > 0; d >>= 1) place += __shfl_xor_sync(0xffffffffu, place, d);
-    if (part == 0 && t < n) {
-        key[place] = mine;
-        token[place] = t;
+        for (int u = 0; u < kBatch; ++u) id[u] = i0 + u * kThreads < n ? ids[i0 + u * kThreads] : 0;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int i = i0 + u * kThreads;
+            if (i >= all) break;
+            // those past the end are greater than any and come after all
+            uint32_t *const report = i / kRankChunk == static_cast<int>(blockIdx.x) ? err : nullptr;
+            keys[i] = i < n ? static_cast<float>(key_of(id[u], v_valid, v_pad, report)) : INFINITY;
+        }
+    }
+    __syncthreads();
+    const int t0 = blockIdx.x * kRankChunk + warp * kRankEach;  // the warp's first token
+    float mine[kRankEach], before[kRankEach];
+#pragma unroll
+    for (int u = 0; u < kRankEach; ++u) {
+        mine[u] = keys[t0 + u];
+        before[u] = 0.0f;
+    }
+    // all tokens before the warp's count if not greater, all behind them if smaller
+#pragma unroll 2
+    for (int j = lane; j < t0 / 4; j += 32) {
+        const float4 k = keys4[j];
+#pragma unroll
+        for (int u = 0; u < kRankEach; ++u) {
+            const float least = mine[u] + 1.0f;
+            before[u] += (__saturatef(least - k.x) + __saturatef(least - k.y)) +
+                         (__saturatef(least - k.z) + __saturatef(least - k.w));
+        }
+    }
+#pragma unroll 2
+    for (int j = (t0 + kRankEach) / 4 + lane; j < all / 4; j += 32) {
+        const float4 k = keys4[j];
+#pragma unroll
+        for (int u = 0; u < kRankEach; ++u)
+            before[u] += (__saturatef(mine[u] - k.x) + __saturatef(mine[u] - k.y)) +
+                         (__saturatef(mine[u] - k.z) + __saturatef(mine[u] - k.w));
+    }
+#pragma unroll
+    for (int u = 0; u < kRankEach; ++u) {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) before[u] += __shfl_xor_sync(0xffffffffu, before[u], d);
+#pragma unroll
+        for (int w = 0; w < kRankEach; ++w)
+            if (w != u) before[u] += mine[w] < mine[u] || (mine[w] == mine[u] && w < u) ? 1.0f : 0.0f;
+        if (lane == u && t0 + u < n) {
+            const int place = static_cast<int>(before[u]);
+            key[place] = static_cast<int32_t>(mine[u]);
+            token[place] = t0 + u;
+        }
     }
 }
 
@@ -389,7 +416,7 @@ inline SumSplit sum_split(int64_t tokens, int64_t h) {
     SumSplit sp{};
     // shorter chains where there are few (999 tokens: 10.3 us a call, with sixteen 12.1; one id
     // for all 18.3 and 14.2, its run crosses more cuts)
-    sp.chunk = std::max<int64_t>(tokens <= kRankTokens ? 8 : 16, (tokens + 1023) / 1024);
+    sp.chunk = std::max<int64_t>(tokens <= 2048 ? 8 : 16, (tokens + 1023) / 1024);
     sp.chunks = static_cast<int>((tokens + sp.chunk - 1) / sp.chunk);
     const int64_t vectors = h / 8;
     sp.lanes = 8;
@@ -650,9 +677,8 @@ tpce_status embed_sort(const int32_t *ids, int64_t T, int64_t v_pad, int64_t v_v
         const int64_t fill = std::min<int64_t>((vectors + 4 * kThreads - 1) / (4 * kThreads), int64_t{8} * num_sms());
         const cudaError_t e =
             launch(embed_rank_kernel, static_cast<unsigned>(sp.blocks + fill), kThreads,
-                   static_cast<size_t>(sp.blocks) * kRankChunk * sizeof(int32_t), s, ids, static_cast<int>(T),
-                   sp.blocks, valid, pad, buf.key[0], buf.token[0], static_cast<uint4 *>(table), vectors,
-                   device_error_word());
+                   static_cast<size_t>(sp.blocks) * kRankChunk * sizeof(float), s, ids, static_cast<int>(T), sp.blocks,
+                   valid, pad, buf.key[0], buf.token[0], static_cast<uint4 *>(table), vectors, device_error_word());
         return e == cudaSuccess ? check_launch("embed_sort", s) : fail_cuda(e, "embed_sort");
     }
     if (sp.cluster) {
