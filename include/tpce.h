@@ -714,8 +714,10 @@ tpce_status tpce_device_status(void *stream, int clear, uint32_t *detail);
  * blocks have a place, and every backward wider than 8192) takes it the same
  * way: block 0 counts bytes on its first row that nothing copies. So does a bf16 attention
  * core (tp_attn_core_*, scale above 0): block 0 loads none of its first tile of keys (or, in the
- * backward, of its first step's tiles). The arming is used up
- * by that one launch; tpce_debug_withhold_next_load(0) disarms it unused.
+ * backward, of its first step's tiles). With a number of nanoseconds, 2 to 2^20, instead of 1 the
+ * bf16 attention forward loads everything, and every block gives up so long after its first pair of
+ * tiles was found: some of its warps get what they wait for, and some do not. (Elsewhere as 1.)
+ * The arming is used up by that one launch; tpce_debug_withhold_next_load(0) disarms it unused.
  * Process-wide; returns TPCE_OK.
  * ------------------------------------------------------------------------- */
 tpce_status tpce_debug_withhold_next_load(int on);

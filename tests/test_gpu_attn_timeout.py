@@ -47,3 +47,29 @@ def test_a_tile_that_never_comes(direction, T, G, window):
     assert tp.device_status() == TIMEOUT and tp.device_status() == 0
     again = call()
     assert torch.equal(good, again) and tp.device_status() == 0
+
+
+@pytest.mark.parametrize("T,n_kv,G,window", [(3000, 4, 8, 0), (3000, 16, 1, 500), (90, 1, 2, 0)])
+def test_blocks_that_give_up_while_others_get_on(T, n_kv, G, window):
+    # two warps share queries: neither may wait for the other when that has left
+    gpu_or_skip()
+    g = torch.Generator(device="cuda").manual_seed(T)
+    QKV = torch.randn(T, (G + 2) * n_kv * 128, generator=g, device="cuda").bfloat16()
+
+    def call():
+        f = tp.tp_attn_core_forward(QKV, n_kv * G, n_kv, window=window)
+        return f["O"], f["lse"]
+
+    good = call()
+    torch.cuda.synchronize()
+    assert tp.device_status() == 0
+    for k in range(100):
+        assert lib().tpce_debug_withhold_next_load(2 + 311 * k) == 0       # up to 31 us
+        t0 = time.monotonic()
+        call()
+        torch.cuda.synchronize()
+        took = time.monotonic() - t0
+        assert tp.device_status_detail() == (TIMEOUT, TIMEOUT | 29 << 8), k
+        assert took < 1.0, (k, took)   # what is given up is not waited for
+    again = call()
+    assert all(torch.equal(x, y) for x, y in zip(good, again)) and tp.device_status() == 0

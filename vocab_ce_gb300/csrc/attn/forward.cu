@@ -331,18 +331,19 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     ptx::tc_fence_after();
     grid_begin();
     constexpr uint32_t tmem = 0;  // all columns there are: they begin at 0
-    // the next work of the warp that calls it, read by all its lanes; false at the end
+    // the next work of the warp that calls it, read by all its lanes; false at the end, or where all(it is there) is
     int round = 0;
-    auto next_work = [&](Work &w) {
+    auto next_work = [&](Work &w, auto all) {
         const int at = round & 1;
         const uint32_t parity = (round >> 1) & 1;
         ++round;
-        if (!wait_all(&m.work_full[at], parity, abort_flag, s.err, 28)) return false;
+        if (!all(wait_all(&m.work_full[at], parity, abort_flag, s.err, 28))) return false;
         w = m.work[at];
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&m.work_empty[at]);
         return w.unit >= 0;
     };
+    const auto alone = [](bool ok) { return ok; };
 
     if (warp < kSoftWarps) {
         // ------------------------------------------------ softmax
@@ -351,11 +352,26 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t s_tmem = tmem + i * 128 + lanes, o_tmem = tmem + 256 + i * 128 + half * 64 + lanes;
         const float c = s.scale * kLog2e;
-        // the two warps that share queries meet
-        auto meet = [&] { asm volatile("bar.sync %0, 64;" ::"r"(2 + i * 4 + (warp & 3)) : "memory"); };
+        // The two warps that share queries meet. Each waits for itself, and may be the only one whose wait runs out:
+        // so neither leaves within a pair, where the other counts on it. They go through all of it with whatever is
+        // there, and on to the next pair only if both have seen that it is there. (The two cases of attn_forward
+        // that are bound by the tensor cores take 1% longer for it; asking at each meeting took 3%.)
+        const int shared_by = 2 + i * 4 + (warp & 3);
+        auto meet = [&] { asm volatile("bar.sync %0, 64;" ::"r"(shared_by) : "memory"); };
+        auto both = [&](bool yes) {
+            uint32_t all;
+            __syncwarp();
+            asm volatile(
+                "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\t"
+                "bar.red.and.pred q, %1, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                : "=r"(all)
+                : "r"(shared_by), "r"(static_cast<uint32_t>(yes))
+                : "memory");
+            return all != 0;
+        };
         uint32_t phase = 0, o_phase = 0;
         Work w;
-        while (next_work(w)) {
+        while (next_work(w, both)) {
             if (w.t.n == 0) {
                 const int head0 = by_heads ? 2 * w.unit : w.unit;
                 forward_rest(s, w.t, head0, O, lse);
@@ -368,12 +384,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             const int my_q0 = i ? pr.q0[1] : pr.q0[0], my_head = i ? pr.head[1] : pr.head[0];
             const int row = my_q0 + r;
             float top = -INFINITY, l = 0.0f;  // the maximum that P is relative to, times c; the sum of P
-            bool alive = true;
             const int count = my.count();
             for (int u = 0; u < count; ++u) {
                 const int k0 = my.at(u) * kTile;
-                alive = wait_all(&m.s_full[i], phase, abort_flag, s.err, 24);
-                if (!alive) break;
+                wait_all(&m.s_full[i], phase, abort_flag, s.err, 24);
                 phase ^= 1;
                 ptx::tc_fence_after();
                 float x[2][32];
@@ -430,14 +444,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 if (lane == 0) ptx::mbar_arrive(&m.p_full[i]);
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             }
-            if (alive) {
-                // of both halves (the next pair's sums come after its maxima, when these have been read)
-                m.row_sum[warp][lane] = l;
-                meet();
-                l = m.row_sum[warp & ~4][lane] + m.row_sum[warp | 4][lane];
-            }
-            if (!alive || !wait_all(&m.o_full[i], o_phase, abort_flag, s.err, 25)) break;
+            // of both halves (the next pair's sums come after its maxima, when these have been read)
+            m.row_sum[warp][lane] = l;
+            meet();
+            l = m.row_sum[warp & ~4][lane] + m.row_sum[warp | 4][lane];
+            const bool there = wait_all(&m.o_full[i], o_phase, abort_flag, s.err, 25);
             o_phase ^= 1;
+            if (!there) continue;
             ptx::tc_fence_after();
             const float inv = 1.0f / l;
             const bool mine = row < w.t.n;
@@ -499,7 +512,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 ok = ok && wait_all(&m.empty[stage], phase ^ 1, abort_flag, s.err, 20);
                 if (!ok) return;
                 ok = load_rows(leader, m.ring[stage], &map, &m.full[stage], &m.aux, aux_phase, at_head, row, blocks,
-                               rows, abort_flag, s.err, debug_withhold != 0 && blockIdx.x == 0 && issued == 0);
+                               rows, abort_flag, s.err, debug_withhold == 1 && blockIdx.x == 0 && issued == 0);
                 issued |= 1u << stage;
                 parity = (parity & ~(1u << stage)) | (phase << stage);
                 if (++stage == kFwdStages) {
@@ -508,7 +521,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 }
             };
             Work w;
-            while (ok && next_work(w)) {
+            while (ok && next_work(w, alone)) {
                 if (w.t.n == 0) continue;
                 const Pair pr(s, w, by_heads);
                 const int kv = pr.head[0] / s.group;
@@ -561,7 +574,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 return Phase{before >= 0 ? &m.turn[i] : nullptr, before & 1u};
             };
             Work w;
-            while (ok && next_work(w)) {
+            while (ok && next_work(w, alone)) {
                 if (w.t.n == 0) continue;
                 const Pair pr(s, w, by_heads);
                 const KeyTiles my = i ? pr.one[1] : pr.one[0];
@@ -603,6 +616,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             // ------------------------------------------------ what comes next
             Scan scan;
             for (int r = 0;; ++r) {
+                if (r == 1 && debug_withhold > 1) {  // gives up after so many ns
+                    const uint64_t from = ptx::globaltimer(), ns = min(debug_withhold, 1 << 20);
+                    while (ptx::globaltimer() - from < ns) {}
+                    ptx::record_error(s.err, kErrTimeout | (29u << 8));
+                    *abort_flag = 1;
+                }
                 const Work w = find_work(s, r, units, tiles, by_heads, scan);
                 if (!wait_all(&m.work_empty[r & 1], ((r >> 1) & 1) ^ 1, abort_flag, s.err, 29)) break;
                 if (lane == 0) {

@@ -17,7 +17,7 @@ namespace tpce {
 uint32_t *device_error_word();
 // number of SMs of the current device (0 on failure)
 int num_sms();
-// 1 once after tpce_debug_withhold_next_load(1) armed it (the arming is used
+// What tpce_debug_withhold_next_load() was given, once (the arming is used
 // up by the launch that reads it: a CTA-pair GEMM, an RMS norm whose rows
 // come through a ring, or a bf16 attention core), else 0.
 int take_debug_withhold();

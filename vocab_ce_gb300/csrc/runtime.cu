@@ -503,7 +503,7 @@ extern "C" tpce_status tpce_device_status(void *stream, int clear, uint32_t *det
 }
 
 extern "C" tpce_status tpce_debug_withhold_next_load(int on) {
-    g_debug_withhold.store(on ? 1 : 0);
+    g_debug_withhold.store(on);
     return TPCE_OK;
 }
 
