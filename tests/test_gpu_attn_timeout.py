@@ -73,3 +73,23 @@ def test_blocks_that_give_up_while_others_get_on(T, n_kv, G, window):
         assert took < 1.0, (k, took)   # what is given up is not waited for
     again = call()
     assert all(torch.equal(x, y) for x, y in zip(good, again)) and tp.device_status() == 0
+
+
+def test_a_copy_that_is_given_up_is_waited_for_once_more():
+    # its tile ends a sequence, and lands on a barrier of its own: with nothing loaded the wait for what may still be
+    # under way takes its whole limit, 50 ms, after the 2 s
+    gpu_or_skip()
+    g = torch.Generator(device="cuda").manual_seed(1)
+    QKV = torch.randn(50, 6 * 64, generator=g, device="cuda").bfloat16()
+    dO = torch.randn(50, 4 * 64, generator=g, device="cuda").bfloat16()
+    f = tp.tp_attn_core_forward(QKV, 4, 1)
+    good = tp.tp_attn_core_backward(dO, QKV, f["O"], f["lse"], 4, 1)
+    torch.cuda.synchronize()
+    assert lib().tpce_debug_withhold_next_load(1) == 0
+    t0 = time.monotonic()
+    tp.tp_attn_core_backward(dO, QKV, f["O"], f["lse"], 4, 1)
+    torch.cuda.synchronize()
+    took = time.monotonic() - t0
+    assert WAIT_S + 0.045 <= took < WAIT_S + 1.0, took
+    assert tp.device_status() == TIMEOUT
+    assert torch.equal(good, tp.tp_attn_core_backward(dO, QKV, f["O"], f["lse"], 4, 1)) and tp.device_status() == 0

@@ -657,7 +657,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     shorts = ok ? n + 1 : shorts;
                 }
             }
-            if (*abort_flag && leader) {
+            // copies land before the block ends, also where others give up only after this warp is done
+            if (leader) {
                 if (units) ptx::mbar_wait_drain(&m.stay_full, (units - 1) & 1);
                 for (int i = max(0, longs - 3); i < longs; ++i)
                     ptx::mbar_wait_drain(&m.full[place_of(kLong, i)], round_of(kLong, i));

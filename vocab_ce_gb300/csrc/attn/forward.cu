@@ -544,7 +544,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     if (u < pr.count) load(s.k_head(kv), w.t.row0 + static_cast<int64_t>(pr.both.at(u)) * kTile, 0);
                 }
             }
-            if (*abort_flag && lane == 0) {
+            // copies land before the block ends, also where others give up only after this warp is done
+            if (lane == 0) {
                 if (any) ptx::mbar_wait_drain(&m.q_full, q_phase ^ 1);
                 for (int i = 0; i < kFwdStages; ++i)
                     if (issued & (1u << i)) ptx::mbar_wait_drain(&m.full[i], (parity >> i) & 1u);

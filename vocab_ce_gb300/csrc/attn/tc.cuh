@@ -269,8 +269,11 @@ __device__ __forceinline__ bool load_rows(bool leader, uint8_t *to, const CUtens
     __syncwarp();
     if (!rows) return true;
     const bool ok = wait_all<true>(aux, aux_phase, abort_flag, err, 49);
+    if (ok)
+        zero_tail(to, rows, blocks);
+    else if (leader)
+        ptx::mbar_wait_drain(aux, aux_phase);  // the copy may still be under way
     aux_phase ^= 1;
-    if (ok) zero_tail(to, rows, blocks);
     if (leader) ptx::mbar_arrive(full);
     return ok;
 }
