@@ -405,7 +405,7 @@ tpce_status tp_attn_out_backward(const void *dZ, const void *O, const void *Wo,
  * Shapes: n_heads a multiple of n_kv_heads, up to 4096; d a multiple of 8 up to
  * 128; T up to 2^30, T n_heads up to 2^33, (T / 32 + 2 sequences + 2) n_heads
  * below 2^31; in bf16 T n_heads / n_kv_heads up to 2^26 (with a window and no
- * sinks: the smaller of T and window + 256 in place of T); scale finite, times
+ * sinks: the smaller of T and window + 256 in place of T), and up to 2^26 sequences; scale finite, times
  * log2(e) too; window and sinks not negative. What is written overlaps nothing
  * else (TPCE_ERR_INVALID). T == 0 is a no-op.
  * Workspace: tpce_attn_core_workspace_bytes for the backward.

@@ -91,3 +91,13 @@ def test_how_long_a_unit_of_work_may_take(L, call):
                  {"T": 1 << 27, "n": 1, "kv": 1, "dtype": 1}):
         assert call(L, O=3 * MB + 8, **room, **fine) == ALIGN, fine
     assert call(L, scale=3e38) == INVALID
+
+
+@pytest.mark.parametrize("call", [forward, backward])
+def test_how_long_the_search_for_a_unit_may_take(L, call):
+    one = {"n": 1, "kv": 1}
+    for bad in ({"b": (1 << 26) + 1, **one}, {"b": 1 << 29, **one}, {"b": (1 << 26) + 1, "scale": -1.0, **one}):
+        assert call(L, **bad) == SHAPE and b"2^26" in L.tpce_last_error(), bad
+    # not refused for that: a misaligned pointer is what these are turned down for
+    for fine in ({"b": 1 << 26, **one}, {"b": 1 << 29, "dtype": 1, **one}, {"b": 1 << 29, "offsets": 0, **one}):
+        assert call(L, O=3 * MB + 8, **fine) == ALIGN, fine

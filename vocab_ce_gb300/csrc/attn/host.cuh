@@ -9,6 +9,7 @@ namespace tpce {
 namespace attn {
 
 constexpr int64_t kMaxReach = int64_t{1} << 26;
+constexpr int kMaxSequences = 1 << 26;
 
 inline tpce_status make_shape(const char *name, const int32_t *offsets, int sequences, int64_t T, int64_t n_heads,
                               int64_t n_kv_heads, int64_t head_dim, int64_t window, int64_t sinks, float scale,
@@ -47,6 +48,10 @@ inline tpce_status make_shape(const char *name, const int32_t *offsets, int sequ
     if (dtype == TPCE_BF16 && reach * s.group > kMaxReach)
         return fail(TPCE_ERR_SHAPE, "%s: %lld tokens that see a key, with %d query heads that share it: more than 2^26",
                     name, static_cast<long long>(reach), s.group);
+    // and so does the search for one, which may pass all sequences (2^26 of them take 0.23 s, and are passed
+    // twice before the backward's first unit)
+    if (dtype == TPCE_BF16 && offsets && sequences > kMaxSequences)
+        return fail(TPCE_ERR_SHAPE, "%s: %d sequences: more than 2^26", name, sequences);
     s.scale = scale;
     s.err = device_error_word();
     return TPCE_OK;
