@@ -375,3 +375,15 @@ def test_the_most_sequences():
     assert torch.equal(got["O"], want["O"]) and torch.equal(got["lse"], want["lse"])
     a, b = (tp.tp_attn_core_backward(dO, QKV, want["O"], want["lse"], 1, 1, offsets=x) for x in (offsets, few))
     assert torch.equal(a, b) and tp.device_status() == 0
+
+
+def test_offsets_that_are_part_of_a_vector():
+    gpu_or_skip()
+    QKV, dO, edges, _ = make((90, 30, 50), 0, 0, 1, 2, 64, BF, 15)
+    longer = torch.tensor([7] + edges + [9], dtype=torch.int32, device="cuda")
+    part, whole = longer[1:-1], torch.tensor(edges, dtype=torch.int32, device="cuda")
+    assert part.data_ptr() % 16
+    f, w = (tp.tp_attn_core_forward(QKV, 2, 1, offsets=x) for x in (part, whole))
+    assert torch.equal(f["O"], w["O"]) and torch.equal(f["lse"], w["lse"])
+    a, b = (tp.tp_attn_core_backward(dO, QKV, w["O"], w["lse"], 2, 1, offsets=x) for x in (part, whole))
+    assert torch.equal(a, b) and tp.device_status() == 0

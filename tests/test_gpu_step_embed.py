@@ -300,3 +300,34 @@ def test_lengths_around_the_kinds_of_sorts(T, v_pad):
         dX = rows(T, 8, torch.float32, 5)
         assert torch.equal(tp.tp_embedding_backward(dX, ids, v_pad), tp.tp_embedding_backward(dX, ids, v_pad)), kind
     assert tp.device_status() == 0
+
+
+def test_ids_that_are_part_of_a_batch():
+    # inputs and targets of next-token prediction are the same rows, one token apart: not 16-byte aligned
+    gpu_or_skip()
+    v, h, T = 500, 64, 99
+    tokens = ids_of(3 * (T + 1), v, "zipf", 31).reshape(3, T + 1)
+    E, dX = rows(v, h, torch.bfloat16, 32), rows(T, h, torch.bfloat16, 33)
+    for b in range(3):
+        for ids in (tokens[b, :-1], tokens[b, 1:], tokens[b, 3:]):
+            n = len(ids)
+            X, dE = tp.tp_embedding_forward(ids.clone(), E), tp.tp_embedding_backward(dX[:n], ids.clone(), v)
+            assert torch.equal(tp.tp_embedding_forward(ids, E), X)
+            assert torch.equal(tp.tp_embedding_backward(dX[:n], ids, v), dE)
+            s = torch.cuda.Stream()
+            s.wait_stream(torch.cuda.current_stream())
+            other = tp.tp_embedding_forward(ids, E, stream=s), tp.tp_embedding_backward(dX[:n], ids, v, stream=s)
+            s.synchronize()
+            assert torch.equal(other[0], X) and torch.equal(other[1], dE)
+    # captured: what the tokens are at the replay counts
+    ids, X, dE = tokens[1, 1:], torch.empty_like(dX), torch.empty_like(E)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        tp.tp_embedding_forward(ids, E, out=X)
+        tp.tp_embedding_backward(dX, ids, v, out=dE)
+    for seed in (34, 35):
+        tokens.copy_(ids_of(3 * (T + 1), v, "zipf", seed).reshape(3, T + 1))
+        g.replay()
+        assert torch.equal(X, tp.tp_embedding_forward(ids.clone(), E))
+        assert torch.equal(dE, tp.tp_embedding_backward(dX, ids.clone(), v))
+    assert tp.device_status() == 0

@@ -399,17 +399,22 @@ PyObject *expert_combine_backward(PyObject *const *a) {
     return res.take();
 }
 
+// The library's pointers are 16-byte aligned, which a part of a longer vector of tokens or offsets (a row of a
+// batch, without its last token) need not be: such a one is copied, on the stream of the call.
+at::Tensor aligned(const at::Tensor &x) { return reinterpret_cast<uintptr_t>(x.data_ptr()) % 16 ? x.clone() : x; }
+
 // ------------------------------------------------------------------ embedding
-void need_ids(const at::Tensor &ids) {
+at::Tensor need_ids(const at::Tensor &ids) {
     if (ids.dim() != 1) throw Refused{"ids must be a vector of tokens, got shape " + shape_text(ids.sizes())};
     need(ids, "ids", at::kInt, ids.sizes());
+    return aligned(ids);
 }
 
 // ids, E, v_valid (or None), scale, out
 PyObject *embedding_forward(PyObject *const *a) {
-    const at::Tensor &ids = tensor(a[0], "ids"), &E = tensor(a[1], "E");
+    const at::Tensor &E = tensor(a[1], "E");
     const int dt = matrix(E, "E");
-    need_ids(ids);
+    const at::Tensor ids = need_ids(tensor(a[0], "ids"));
     const int64_t T = ids.size(0), h = E.size(1), v_pad = E.size(0), v_valid = none(a[2]) ? v_pad : integer(a[2]);
     const double scale = number(a[3]);
     const Output X = output(a[4], "X", {T, h}, E.scalar_type(), E);
@@ -422,9 +427,9 @@ PyObject *embedding_forward(PyObject *const *a) {
 
 // dX, ids, v_pad, v_valid (or None), scale, out, accumulate, ws
 PyObject *embedding_backward(PyObject *const *a) {
-    const at::Tensor &dX = tensor(a[0], "dX"), &ids = tensor(a[1], "ids");
+    const at::Tensor &dX = tensor(a[0], "dX");
     const int dt = matrix(dX, "dX");
-    need_ids(ids);
+    const at::Tensor ids = need_ids(tensor(a[1], "ids"));
     const int64_t T = ids.size(0), h = dX.size(1), v_pad = integer(a[2]), v_valid = none(a[3]) ? v_pad : integer(a[3]);
     need(dX, "dX", dX.scalar_type(), {T, h});
     const double scale = number(a[4]);
@@ -463,6 +468,7 @@ struct Heads {
             if (offsets.dim() != 1 || offsets.size(0) < 2 || offsets.size(0) > (1 << 30))
                 throw Refused{"offsets must hold sequences + 1 values"};
             need(offsets, "offsets", at::kInt, offsets.sizes());
+            offsets = aligned(offsets);
             sequences = static_cast<int>(offsets.size(0) - 1);
         }
         scale = none(a[5]) ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(d)))

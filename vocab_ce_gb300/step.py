@@ -9,7 +9,9 @@ Python they would take several times as long as the smallest kernels. With
 memory, and the tensors passed in are recorded on it, so that memory freed
 while the stream still works is not handed out again. Ordering the stream
 against the ones that made the inputs, or use the outputs, is the caller's, as
-with any kernel.
+with any kernel. The library's pointers are 16-byte aligned; the embedding's ids
+and the attention core's offsets, which may be part of a longer vector, are
+copied first where they are not.
 """
 
 from __future__ import annotations
