@@ -74,3 +74,19 @@ def test_without_a_built_binding_or_gpu_nothing_runs_on_the_cpu(L):
         tp.tp_embedding_forward(ids, E)
     with pytest.raises(ValueError, match="CUDA"):
         tp.tp_embedding_backward(torch.zeros(4, 64), ids, 8)
+
+
+def test_workspace_holds_every_part(L):
+    import vocab_ce_gb300 as tp
+    for T in (1, 8, 9, 16, 17, 999, 2047, 2048, 2049, 4096, 4097, 16_384, 16_385, 65_536, 65_537, 1 << 20):
+        for h, v in ((8, 5), (64, 100), (1000, 30_001), (8192, 129_024), (64, 1 << 24)):
+            chunk = max(8 if T <= 2048 else 16, -(-T // 1024))
+            chunks = -(-T // chunk)
+            sums = 2 * chunks * h * 4 if chunks > 1 else 0
+            sorted_ids = 4 * (-(-4 * T // 256) * 256)
+            # more tokens than one launch sorts: counts of up to 1024 digits by up to 256 blocks
+            counts = 256 * 4096 if T > 65_536 else 0
+            need = tp.embedding_workspace_bytes(T, h, v)
+            assert sorted_ids + sums <= need <= sorted_ids + sums + counts, (T, h, v)
+            if counts:
+                assert need > sorted_ids + sums

@@ -331,3 +331,22 @@ def test_ids_that_are_part_of_a_batch():
         assert torch.equal(X, tp.tp_embedding_forward(ids.clone(), E))
         assert torch.equal(dE, tp.tp_embedding_backward(dX, ids.clone(), v))
     assert tp.device_status() == 0
+
+
+@pytest.mark.parametrize("T", [4097, 5000, 65_536, 65_537, 70_000, 300_000])
+@pytest.mark.parametrize("v_pad", [1 << 20, (1 << 20) + 7, (1 << 21) + 3])
+def test_three_passes_of_a_sort(T, v_pad):
+    # 2^20 keys and the one for padding no longer fit two passes of ten bits; each token's row is its number's
+    # digits, whose sums are exact in any split, and which tell one token from another
+    gpu_or_skip()
+    t = torch.arange(T, device="cuda")
+    dX = torch.stack([t >> 4 * c & 15 for c in range(8)], 1).float()
+    for kind in ("random", "zipf", "same", "sorted"):
+        ids = ids_of(T, v_pad, kind, T)
+        ids[::7] = v_pad - 1                    # the largest key
+        want = torch.zeros(v_pad, 8, device="cuda").index_add_(0, ids.clamp_min(0).long(),
+                                                              torch.where(ids[:, None] >= 0, dX, 0.0))
+        assert float(want.max()) < 2 ** 24
+        ws = torch.zeros(tp.embedding_workspace_bytes(T, 8, v_pad), dtype=torch.uint8, device="cuda")
+        assert torch.equal(tp.tp_embedding_backward(dX, ids, v_pad, ws=ws), want), kind
+    assert tp.device_status() == 0
