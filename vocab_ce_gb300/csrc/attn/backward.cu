@@ -1,10 +1,11 @@
 // backward.cu -- the attention core, backward (attn.cuh has the formulas).
 //
-// Three kernels: delta of every query and head; dQ by tiles of queries; dK and dV
-// by tiles of keys, over all queries of all heads that share them. S and dP are
-// computed in both of the last two, which is seven products for the five that the
-// formulas name, and in return every gradient is summed in one place, in registers
-// or tensor memory: nothing is added by atomics and results are the same every time.
+// Two kernels: delta of every query and head; and the gradients, dK and dV by tiles
+// of keys, over all queries of all heads that share them, and dQ by tiles of queries.
+// S and dP are computed for both kinds of tiles, which is seven products for the five
+// that the formulas name, and in return every gradient is summed in one place, in
+// registers or tensor memory: nothing is added by atomics and results are the same
+// every time.
 #include "attn/attn.cuh"
 #include "attn/host.cuh"
 #include "attn/tc.cuh"

@@ -35,8 +35,9 @@ constexpr int kThreads = 256;
 
 // ------------------------------------------------------------------ forward
 // `lanes` threads of a block share a piece of lanes * U vectors of a token's row, whose
-// loads are under way together (16,384 rows of 8192 bf16: 61 us with four vectors a thread,
-// 6.3 TB/s of rows read and written, 94% of a copy's rate; one vector a thread is 6% slower).
+// loads are under way together (16,384 rows of 8192 bf16: 61 us with four vectors a thread where
+// ids are as frequent as words, 6.3 TB/s of rows read and written, 94% of a copy's rate; one
+// vector a thread is 6% slower).
 template <typename T, int U>
 __global__ void __launch_bounds__(kThreads)
     embed_forward_kernel(const T *E, const int32_t *ids, int64_t tokens, int64_t v_valid, int vectors, int lanes,
@@ -79,6 +80,10 @@ __global__ void __launch_bounds__(kThreads)
 // Up to kRankTokens tokens are not sorted by digits: a token's place is the number of those
 // before it in the order, which all SMs count at once (embed_rank_kernel).
 constexpr int kClusterThreads = 1024;
+// What the SMs that do not sort zero meanwhile, of a table that is written whole: about what the sort's
+// time is enough for. A cluster's sort: 8192 tokens of 4096 and 51,200 rows 92 us a call, with 48 MB 96, with
+// 192 MB 98. By counting, which is shorter: 999 tokens of 1000 fp32 and 30,001 rows 25.5 us, with none 31.9, with
+// 24 MB 28.7, with 96 MB 25.5; 4096 of 2048 and 131,072 rows 95, 102, 99 and 91.
 constexpr int64_t kZeroed = 96 << 20, kRankZeroed = 48 << 20;
 constexpr int64_t kRankTokens = 4096;
 constexpr int kMaxBins = 1024, kCluster = 8;
@@ -299,7 +304,7 @@ __global__ void __launch_bounds__(kThreads)
 // Place of each of a block's tokens, kRankEach a warp: how many keys are smaller, or equal and of
 // an earlier token. The keys lie in shared memory as fp32, so that a comparison and its sum
 // are a subtraction that saturates at 0 and 1 and an addition; a key that is read is compared
-// with all of the warp's (calls added to a table: 999 tokens of 1000 18.3 us with digits, 9.0
+// with all of the warp's (calls added to a table: 999 tokens of 1000 18.3 us with digits, 9.4
 // so; 4096 of 1024 25.5 and 20.8; 8192 27 and 31, since all pairs are compared). The blocks
 // after the first `blocks` write zeros as in embed_sort_kernel.
 __global__ void __launch_bounds__(kThreads)
@@ -414,8 +419,8 @@ struct SumSplit {
 };
 inline SumSplit sum_split(int64_t tokens, int64_t h) {
     SumSplit sp{};
-    // shorter chains where there are few (999 tokens: 10.3 us a call, with sixteen 12.1; one id
-    // for all 18.3 and 14.2, its run crosses more cuts)
+    // shorter chains where there are few (999 tokens of 1000 bf16: 9.4 us a call, with sixteen 10.4;
+    // one id for all 18.6 and 14.8, its run crosses more cuts)
     sp.chunk = std::max<int64_t>(tokens <= 2048 ? 8 : 16, (tokens + 1023) / 1024);
     sp.chunks = static_cast<int>((tokens + sp.chunk - 1) / sp.chunk);
     const int64_t vectors = h / 8;
@@ -653,7 +658,8 @@ tpce_status embed_forward(const int32_t *ids, const void *E, int64_t tokens, int
     const int vectors = static_cast<int>(h / 8);
     int lanes = 8;
     while (lanes < kThreads && lanes * 2 < vectors) lanes *= 2;
-    // four vectors a thread (16,384 rows of 8192 bf16: 66 us, with two 70), one where that would leave SMs idle
+    // four vectors a thread (16,384 rows of 8192 bf16, all ids equally frequent: 79 us, with two 81), one where
+    // that would leave SMs idle
     const bool few = tokens * vectors < int64_t{4} * kThreads * 2 * num_sms();
     const int each = lanes * (few ? 1 : 4);
     const int parts = (vectors + each - 1) / each;
@@ -667,7 +673,7 @@ tpce_status embed_forward(const int32_t *ids, const void *E, int64_t tokens, int
     return e == cudaSuccess ? check_launch("embed_forward", s) : fail_cuda(e, "embed_forward");
 }
 
-// table_bytes of the table are zeroed meanwhile (by a cluster's sort only)
+// table_bytes of the table are zeroed meanwhile, by the two sorts of one launch; 0 for the third
 tpce_status embed_sort(const int32_t *ids, int64_t T, int64_t v_pad, int64_t v_valid, const SortSplit &sp,
                        const SortBuffers &buf, uint32_t *counts, void *table, size_t table_bytes, cudaStream_t s) {
     const int32_t valid = static_cast<int32_t>(v_valid), pad = static_cast<int32_t>(v_pad);
