@@ -117,3 +117,51 @@ def test_windows_past_32_bits(window, sinks, dtype):
     check(QKV, dO, edges, offsets, 2, 1, window, sinks, dtype)
     got = tp.tp_attn_core_forward(QKV, 2, 1, offsets=offsets, window=window, sinks=sinks)
     assert torch.equal(got["O"], tp.tp_attn_core_forward(QKV, 2, 1, offsets=offsets)["O"])
+
+
+def test_the_longest_sequence():
+    # 2^30 tokens, a pattern of 4096 over and over: with a window all periods but the first and the last are alike
+    gpu_or_skip()
+    T, P, d, w = 1 << 30, 4096, 8, 33
+    QKV, dO, _, _ = make((P,), 0, 0, 1, 1, d, BF, 45)
+    kw = dict(n_heads=1, n_kv_heads=1, window=w)
+    few = [x.repeat(4, 1) for x in (QKV, dO)]
+    f = tp.tp_attn_core_forward(few[0], **kw)
+    g = tp.tp_attn_core_backward(few[1], few[0], f["O"], f["lse"], **kw)
+    torch.cuda.empty_cache()
+    many = [x.repeat(T // P, 1) for x in (QKV, dO)]
+    got = tp.tp_attn_core_forward(many[0], **kw)
+    grad = tp.tp_attn_core_backward(many[1], many[0], got["O"], got["lse"], **kw)
+    for x, want in ((got["O"], f["O"]), (got["lse"].T, f["lse"].T), (grad, g)):
+        x, want = x.reshape(T // P, P, -1), want.reshape(4, P, -1)
+        assert torch.equal(x[:2], want[:2]) and torch.equal(x[-1], want[-1])
+        assert all(bool((part == want[1]).all()) for part in x[1:-1].split(1 << 14))
+    assert tp.device_status() == 0
+    del many, got, grad, x
+    torch.cuda.empty_cache()
+
+
+def test_calls_on_two_streams_at_once():
+    gpu_or_skip()
+    QKV, dO, _, offsets = make((700, 1300), 0, 0, 2, 4, 128, BF, 46)
+    small, dsmall, _, _ = make((300,), 0, 0, 1, 2, 64, F32, 47)
+    g = torch.Generator(device="cuda").manual_seed(48)
+    ids = torch.randint(0, 900, (5000,), generator=g, device="cuda").int()
+    dX = torch.randn(5000, 512, generator=g, device="cuda").to(BF)
+
+    def calls(stream):
+        f = tp.tp_attn_core_forward(QKV, 8, 2, offsets=offsets, window=300, sinks=4, stream=stream)
+        out = [f["O"], f["lse"], tp.tp_attn_core_backward(dO, QKV, f["O"], f["lse"], 8, 2, offsets=offsets, window=300,
+                                                          sinks=4, stream=stream)]
+        f = tp.tp_attn_core_forward(small, 2, 1, stream=stream)
+        out += [f["O"], tp.tp_attn_core_backward(dsmall, small, f["O"], f["lse"], 2, 1, stream=stream)]
+        return out + [tp.tp_embedding_backward(dX, ids, 1000, stream=stream)]
+
+    want = calls(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for _ in range(10):
+        for got in [calls(s) for s in streams]:
+            torch.cuda.synchronize()
+            assert all(torch.equal(x, y) for x, y in zip(got, want))
+    assert tp.device_status() == 0

@@ -350,3 +350,23 @@ def test_three_passes_of_a_sort(T, v_pad):
         ws = torch.zeros(tp.embedding_workspace_bytes(T, 8, v_pad), dtype=torch.uint8, device="cuda")
         assert torch.equal(tp.tp_embedding_backward(dX, ids, v_pad, ws=ws), want), kind
     assert tp.device_status() == 0
+
+
+@pytest.mark.parametrize("T", [3000, 5000, 70_000])
+def test_the_largest_table(T):
+    # 2^30 rows: ids of 31 bits, in four passes
+    gpu_or_skip()
+    v, h = 1 << 30, 8
+    ids = ids_of(T, v, "random", T)
+    ids[::5], ids[1::5], ids[2::11] = v - 1, 7, -1
+    dX = (torch.arange(T * h, device="cuda").reshape(T, h) % 4).to(torch.bfloat16)
+    kept = ids >= 0
+    named, at = ids[kept].long().unique(return_inverse=True)
+    want = torch.zeros(len(named), h, device="cuda").index_add_(0, at, dX[kept].float()).to(torch.bfloat16)
+    dE = tp.tp_embedding_backward(dX, ids, v)
+    assert torch.equal(dE[named], want)
+    X = torch.where(kept[:, None], dE[ids.clamp_min(0).long()], 0.0)
+    assert torch.equal(tp.tp_embedding_forward(ids, dE), X)
+    dE[named] = 0
+    assert not any(bool(part.view(torch.int16).any()) for part in dE.split(1 << 27))
+    assert tp.device_status() == 0
