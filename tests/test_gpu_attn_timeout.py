@@ -4,7 +4,8 @@ tpce_debug_withhold_next_load(1) makes block 0 of the next bf16 attention launch
 load nothing of its first tile of keys (of its first step's tiles in the
 backward): the waits for it cannot complete. No fault is involved. The call
 returns after the waits' bound (2 s) and a drain's, the status word names a
-timeout, and the same call again gives the bits from before.
+timeout, and the same call again gives the bits from before. With a number of nanoseconds
+the next forward's blocks give up after that time instead, in the middle of their work.
 """
 
 import time

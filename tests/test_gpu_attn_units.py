@@ -2,6 +2,7 @@
 work: more of them than there are SMs, against the 64-bit forms and their bounds
 (_attn_ref); and where several of a block's have results that are not finite, which
 it computes again: what is masked must not reach there either.
+Windows past 32 bits, the longest sequence, and calls on several streams at once.
 """
 
 import math
